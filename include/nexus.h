@@ -65,7 +65,12 @@ enum {
   NX_DEV_BAD_LEN = 2,       /* lens[slice] < 0 or > capacity: slice left untouched */
   NX_DEV_BAD_BUDGET = 4,    /* the slice's budget < n_sink + n_recent or > budget_max:
                                slice left untouched */
-  NX_DEV_BAD_PAGE = 8       /* a block_table entry is outside [0, num_pages): untouched */
+  NX_DEV_BAD_PAGE = 8,      /* a block_table entry is outside [0, num_pages): untouched */
+  NX_DEV_BAD_TOKENS = 16,   /* cu_tokens of a sequence decreases, leaves [0, tokens] or spans
+                               more than max_tokens: the sequence's tokens are not processed */
+  NX_DEV_FULL = 32,         /* a slice has no room for its new rows: slice left untouched */
+  NX_DEV_BAD_IMAGE = 64     /* an image holds a row count that is negative, not whole blocks
+                               or beyond the slice's rows: slice left untouched */
 };
 
 enum { NX_DTYPE_F32 = 0, NX_DTYPE_BF16 = 1 };
@@ -244,6 +249,131 @@ nx_status kv_compact_noalloc(nx_cache* cache, const int32_t* keep_idx, const nx_
 nx_status nexus_evict_step(nx_cache* cache, const void* q, const nx_params* params,
                            int32_t* keep_idx_out, void* ws, size_t ws_bytes,
                            int32_t* dev_status, nx_stream_t stream);
+
+/* ------------------------------------------------------------------------------------
+ * Filling and reading the cache between two evictions: the three calls with which a
+ * decoder layer uses a cache that nexus_evict_step bounds. A slice's rows are in arrival
+ * order, but after an eviction a row's slot says nothing about its position: positions
+ * come from the caller (new tokens) and stay in `pos`.
+ * ------------------------------------------------------------------------------------ */
+
+/*
+ * New tokens of one layer. Sequence s owns rows [cu_tokens[s], cu_tokens[s + 1]) of every
+ * per-token array, oldest first; sequences may own none. cu_tokens NULL: every sequence
+ * owns max_tokens rows and tokens must be seqs * max_tokens.
+ */
+typedef struct nx_tokens {
+  int32_t layer;               /* layer of the cache, 0..layers - 1 */
+  int32_t tokens;              /* rows of the per-token arrays, >= 0 */
+  int32_t max_tokens;          /* host bound: no sequence owns more (>= 1) */
+  int32_t reserved;            /* 0 */
+  const int32_t* cu_tokens;    /* nullable device int32 [seqs + 1] */
+} nx_tokens;
+
+/*
+ * What nexus_append reads and writes next to the cache. q, k, v: rows of cache->dtype, the
+ * heads of one token behind one another (head_dim elements each), `*_stride` elements
+ * between tokens, so that all three may lie in one packed projection. Base addresses are
+ * 16-byte aligned, strides multiples of 16 bytes.
+ */
+typedef struct nx_append {
+  const void* q;               /* [tokens][kv_heads * group][head_dim]; nullable */
+  const void* k;               /* [tokens][kv_heads][head_dim] */
+  const void* v;               /* [tokens][kv_heads][head_dim] */
+  int64_t q_stride, k_stride, v_stride;
+  void* q_out;                 /* [tokens][kv_heads * group][head_dim], packed; may be q
+                                  itself when q is packed; NULL with q */
+  const int32_t* pos;          /* [tokens] absolute position of each token */
+  const int32_t* lens_in;      /* nullable [seqs][kv_heads]: rows each slice of the layer
+                                  holds before the call; NULL: the layer's part of lens */
+  const uint64_t* rotary;      /* [rotary_dim / 2] turns per position in units of 2^-64
+                                  turn (modulo one turn); NULL with rotary_dim 0 */
+  int32_t rotary_dim;          /* rotated features of every q and k head: a multiple of 8,
+                                  0..head_dim; the others pass through */
+  int32_t interleaved;         /* pairs are (2i, 2i + 1) if nonzero, (i, i + rotary_dim / 2)
+                                  otherwise */
+  const void* q_norm;          /* nullable [head_dim], cache->dtype: RMS-norm weight */
+  const void* k_norm;          /* nullable [head_dim], cache->dtype */
+  float eps;                   /* of the norms, >= 0 */
+  int32_t reserved;            /* 0 */
+} nx_append;
+
+/*
+ * Appends the new tokens of one layer. For every q and k head row x of a token at position
+ * p, in binary32 and rounded once to cache->dtype at the end:
+ *   x <- x / sqrt(mean(x^2) + eps) * weight                     (with a norm weight)
+ *   (x_a, x_b) <- (x_a cos - x_b sin, x_b cos + x_a sin),  angle = 2 pi p turns_i 2^-64,
+ *                                                               (for every rotated pair)
+ * q goes to q_out; k, v and p become row lens_in + i of the slice (l, s, h) for the i-th
+ * token of sequence s; then lens = lens_in + the sequence's tokens. The angle is reduced in
+ * integers modulo one turn, so it is as exact at the last position as at the first.
+ * lens_in lets a caller take tokens back: rows behind it (rejected drafts) are overwritten.
+ * A slice without room (NX_DEV_FULL) or with a bad length (NX_DEV_BAD_LEN) is left
+ * untouched; a row whose page is out of range (NX_DEV_BAD_PAGE) is not written.
+ * lens_in may be the layer's part of cache->lens, but not overlap it otherwise.
+ * NX_ERR_UNSUPPORTED for more than 8192 KV heads or 2^20 query heads.
+ */
+nx_status nexus_append(nx_cache* cache, const nx_tokens* tokens, const nx_append* args,
+                       int32_t* dev_status, nx_stream_t stream);
+
+/*
+ * An 8-bit image of a bf16 cache: k and v in e4m3 (4 exponent bits, 3 mantissa bits,
+ * largest value 448) in the layout of the cache's k and v, and one scale per block of
+ * consecutive slots of a slice -- b = 32 rows, or page_size where pages are smaller:
+ *   contiguous: k_scale, v_scale [layers][seqs][kv_heads][ceil(capacity / b)];
+ *   paged:                       [layers][num_pages][kv_heads][page_size / b].
+ * rows [layers][seqs][kv_heads]: the image holds slots 0 .. rows - 1 of a slice, whole
+ * blocks; the cache keeps every row, so that evictions go on from the exact keys. An
+ * eviction moves rows: the caller sets rows to 0 behind it (or passes rows_in below).
+ */
+typedef struct nx_image {
+  void* k;                     /* 16-byte aligned */
+  void* v;                     /* 16-byte aligned */
+  float* k_scale;
+  float* v_scale;
+  int32_t* rows;
+} nx_image;
+
+/*
+ * Brings the image up to date in every slice: blocks rows_in / b .. lens / b - 1 are taken
+ * from the cache, then rows = floor(lens / b) b. rows_in (nullable, laid out like rows, NULL:
+ * rows itself, no other overlap): slots that the image holds already. A block's scale is
+ * the least power of two s with max |x| <= 448 s over the block's finite values (1 if they
+ * are all 0; exponents are kept in -100..120), its codes are x / s rounded to nearest even:
+ * s is a power of two, so that this is the only rounding and code times scale is exact in
+ * bf16. Infinities become the largest code, NaN stays NaN. A block on a page out of range
+ * (NX_DEV_BAD_PAGE) is left out. bf16 caches only (NX_ERR_UNSUPPORTED otherwise).
+ */
+nx_status nexus_quantize(const nx_cache* cache, const nx_image* image, const int32_t* rows_in,
+                         int32_t* dev_status, nx_stream_t stream);
+
+typedef struct nx_attend {
+  const void* q;               /* [tokens][kv_heads * group][head_dim], cache->dtype */
+  void* out;                   /* [tokens][kv_heads * group][head_dim], cache->dtype */
+  float* lse;                  /* nullable [tokens][kv_heads * group] */
+  int64_t q_stride;            /* elements between tokens of q (multiple of 16 bytes) */
+  int64_t out_stride;          /* elements between tokens of out (multiple of 16 bytes) */
+  float scale;                 /* of the logits; finite */
+  int32_t causal;              /* nonzero: see below */
+} nx_attend;
+
+/* Bytes of workspace nexus_attend needs for these arguments (0 on invalid arguments). */
+size_t nexus_attend_workspace_bytes(const nx_cache* cache, const nx_tokens* tokens);
+
+/*
+ * Attention of the new tokens of one layer over its slices: for token i (of n) of sequence
+ * s and query head h * group + g, over the slots j < M of slice (l, s, h),
+ *   x_j = scale <q, k_j>;  out = sum_j exp(x_j) v_j / sum_j exp(x_j);  lse = ln sum_j exp(x_j)
+ * with M = lens - (n - 1 - i) if causal (the n tokens are the slice's newest rows, as
+ * nexus_append leaves them), M = lens otherwise. M <= 0 gives out = 0 and lse = -inf.
+ * image (nullable): slots below image->rows are read from it (code times scale) instead of
+ * the cache. Slices flagged NX_DEV_BAD_LEN or NX_DEV_BAD_IMAGE count as empty; a row on a
+ * page out of range (NX_DEV_BAD_PAGE) is left out of the sums. Rows at or beyond lens are
+ * never read into a result, whatever they hold.
+ */
+nx_status nexus_attend(const nx_cache* cache, const nx_tokens* tokens, const nx_image* image,
+                       const nx_attend* args, void* ws, size_t ws_bytes, int32_t* dev_status,
+                       nx_stream_t stream);
 
 /*
  * Testing hook for failure detection (not part of the method): kv_compact, except that

@@ -8,18 +8,6 @@
 #include "nx_internal.cuh"
 
 namespace nx {
-namespace {
-
-thread_local int32_t g_last_launches = 0;
-thread_local int32_t g_last_scorer = NX_SCORER_NONE;
-std::atomic<bool> g_force_simt{false};   // set by nexus_debug_force_simt (tests, comparisons)
-constexpr int kMaxLaunchNames = 16;
-thread_local const char* g_launch_names[kMaxLaunchNames];
-thread_local void* const* g_prof_events = nullptr;   // armed by nexus_profile_next_call
-thread_local int32_t g_prof_n = 0;
-thread_local bool g_prof_active = false;
-
-constexpr size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 bool valid_cache(const nx_cache* c) {
   if (!c) return false;
@@ -39,6 +27,19 @@ bool valid_cache(const nx_cache* c) {
   }
   return true;
 }
+
+namespace {
+
+thread_local int32_t g_last_launches = 0;
+thread_local int32_t g_last_scorer = NX_SCORER_NONE;
+std::atomic<bool> g_force_simt{false};   // set by nexus_debug_force_simt (tests, comparisons)
+constexpr int kMaxLaunchNames = 16;
+thread_local const char* g_launch_names[kMaxLaunchNames];
+thread_local void* const* g_prof_events = nullptr;   // armed by nexus_profile_next_call
+thread_local int32_t g_prof_n = 0;
+thread_local bool g_prof_active = false;
+
+constexpr size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 nx_status check_params(const nx_cache* c, const nx_params* p) {
   if (!p) return NX_ERR_INVALID_ARG;

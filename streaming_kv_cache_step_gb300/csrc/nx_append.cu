@@ -1,0 +1,279 @@
+// nx_append.cu -- nexus_append: RMS norm and position rotation of new queries and keys, and
+// the rows of k, v and pos behind what every slice of one layer holds.
+//
+// One thread block takes kTokens tokens of one sequence. Its threads first compute the
+// cosines and sines of those tokens (one pair each, shared by all heads of a token: 128
+// features x 40 heads need 64 angles, not 2560), then groups of head_dim / 8 threads take
+// one head row each, 8 features per thread. A thread's 8 features are two runs of 4 that
+// hold 4 whole pairs (runs 4i and rotary_dim / 2 + 4i, or 8i and 8i + 4 when interleaved),
+// so that a rotation needs no exchange between threads; only the norm's sum does.
+#include "nx_internal.cuh"
+
+namespace nx {
+namespace {
+
+constexpr int kTokens = 4;            // tokens of a thread block
+constexpr int kAppendThreads = 256;   // its threads, unless one block covers a sequence
+
+struct AppendArgs {
+  nx_cache c;
+  nx_tokens t;
+  nx_append a;
+  int32_t* dev_status;
+  int32_t* lens;        // the layer's part of c.lens
+  int tiles;            // thread blocks per sequence
+  bool set_lens;        // the kernel sets the new lengths itself
+};
+
+// cos and sin of 2 pi p f 2^-64. p f modulo 2^64 is the angle's fraction of a turn, exact
+// up to f's own rounding; its nearest quarter turn comes off in integers, and what is left
+// (at most 1/8 turn, in 30 bits) is what the float functions see.
+__device__ __forceinline__ float2 rotation_of(int32_t p, uint64_t f) {
+  const uint64_t turn = (uint64_t)(int64_t)p * f;
+  const uint32_t hi = (uint32_t)(turn >> 32) + (uint32_t)((turn >> 31) & 1u);
+  const uint32_t quarter = (hi + 0x20000000u) >> 30;
+  const int32_t rest = (int32_t)(hi - (quarter << 30));
+  float s, c;
+  sincospif((float)rest * 4.656612873077393e-10f, &s, &c);   // 2^-31: units of half turns
+  if (quarter & 1u) {
+    const float x = c;
+    c = -s;
+    s = x;
+  }
+  return quarter & 2u ? make_float2(-c, -s) : make_float2(c, s);
+}
+
+template <typename T>
+__device__ __forceinline__ void load4(const T* p, float* x) {
+  if constexpr (sizeof(T) == 2) {
+    const uint2 r = *reinterpret_cast<const uint2*>(p);
+    x[0] = __uint_as_float(r.x << 16);
+    x[1] = __uint_as_float(r.x & 0xFFFF0000u);
+    x[2] = __uint_as_float(r.y << 16);
+    x[3] = __uint_as_float(r.y & 0xFFFF0000u);
+  } else {
+    const float4 r = *reinterpret_cast<const float4*>(p);
+    x[0] = r.x; x[1] = r.y; x[2] = r.z; x[3] = r.w;
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void store4(T* p, const float* x) {
+  if constexpr (sizeof(T) == 2) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]);
+    const __nv_bfloat162 b = __floats2bfloat162_rn(x[2], x[3]);
+    *reinterpret_cast<uint2*>(p) = make_uint2(reinterpret_cast<const uint32_t&>(a),
+                                              reinterpret_cast<const uint32_t&>(b));
+  } else {
+    *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+  }
+}
+
+template <typename T, int D>
+__global__ void append_kernel(AppendArgs g) {
+  constexpr int kLanes = D / 8;                      // threads of one head row
+  __shared__ float2 s_rot[kTokens][D / 2];
+  extern __shared__ int s_len[];                     // [kv_heads], -1: leave alone
+  grid_dep_wait();
+
+  const nx_cache& c = g.c;
+  const nx_append& a = g.a;
+  const int s = blockIdx.x / g.tiles, tile = blockIdx.x % g.tiles;
+  const int tid = threadIdx.x;
+  int first;
+  const int n = tokens_of(g.t, s, first);
+  if (n < 0) {
+    if (tile == 0 && tid == 0) atomicOr(g.dev_status, NX_DEV_BAD_TOKENS);
+    return;
+  }
+  const int t0 = tile * kTokens;
+  const int nt = min(kTokens, n - t0);
+  if (nt <= 0 && tile > 0) return;
+
+  const int H = c.kv_heads, HQ = a.q ? H * c.group : 0;
+  const int32_t* lens_in = (a.lens_in ? a.lens_in : g.lens) + (long long)s * H;
+  for (int h = tid; h < H; h += blockDim.x) {
+    int len = lens_in[h];
+    int flag = 0;
+    if (len < 0 || len > c.capacity) flag = NX_DEV_BAD_LEN;
+    else if (n > c.capacity - len) flag = NX_DEV_FULL;
+    if (flag) {
+      len = -1;
+      if (tile == 0) atomicOr(g.dev_status, flag);
+    }
+    s_len[h] = len;
+  }
+  const int half = a.rotary_dim / 2;
+  for (int i = tid; i < nt * half; i += blockDim.x)
+    s_rot[i / half][i % half] = rotation_of(a.pos[first + t0 + i / half], a.rotary[i % half]);
+  __syncthreads();
+
+  // this thread's two runs of four features, and its pairs' first index
+  const int lane = tid % kLanes;
+  const bool turns = lane < a.rotary_dim / 8;
+  const bool split = turns && !a.interleaved;
+  const int o0 = split ? 4 * lane : 8 * lane;
+  const int o1 = split ? half + 4 * lane : 8 * lane + 4;
+  const int rows = HQ + 2 * H;                       // head rows per token: q, k, v
+  const int groups = blockDim.x / kLanes;
+  const int total = nt * rows;
+  int item = tid / kLanes;
+  for (int base = (tid & ~31) / kLanes; base < total; base += groups, item += groups) {
+    const bool live = item < total;
+    const int tok = live ? item / rows : 0;
+    const int r = live ? item - tok * rows : 0;
+    const long long token = first + t0 + tok;
+    const bool is_q = r < HQ, is_v = r >= HQ + H;
+    const int h = is_q ? r : is_v ? r - HQ - H : r - HQ;
+    const T* src = is_q ? static_cast<const T*>(a.q) + token * a.q_stride
+                 : is_v ? static_cast<const T*>(a.v) + token * a.v_stride
+                        : static_cast<const T*>(a.k) + token * a.k_stride;
+    src += (long long)h * D;
+    float x[8] = {};
+    if (live) {
+      load4(src + o0, x);
+      load4(src + o1, x + 4);
+    }
+    const void* weight = is_q ? a.q_norm : is_v ? nullptr : a.k_norm;
+    if (a.q_norm || a.k_norm) {                      // the shuffles take the whole warp
+      float ss = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+#pragma unroll
+      for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      if (weight) {
+        const float f = 1.0f / sqrtf(ss * (1.0f / D) + a.eps);
+        float w[8];
+        load4(static_cast<const T*>(weight) + o0, w);
+        load4(static_cast<const T*>(weight) + o1, w + 4);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = x[i] * f * w[i];
+      }
+    }
+    if (!live) continue;
+    if (turns && !is_v) {
+      const float2* cs = s_rot[tok] + 4 * lane;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float& u = a.interleaved ? x[2 * i] : x[i];
+        float& v = a.interleaved ? x[2 * i + 1] : x[i + 4];
+        const float u0 = u, v0 = v;
+        u = u0 * cs[i].x - v0 * cs[i].y;
+        v = v0 * cs[i].x + u0 * cs[i].y;
+      }
+    }
+    T* dst;
+    if (is_q) {
+      dst = static_cast<T*>(a.q_out) + (token * HQ + h) * D;
+    } else {
+      if (s_len[h] < 0) continue;
+      const long long row = row_of(c, g.t.layer, s, h, s_len[h] + t0 + tok);
+      if (row < 0) {
+        atomicOr(g.dev_status, NX_DEV_BAD_PAGE);
+        continue;
+      }
+      dst = static_cast<T*>(is_v ? c.v : c.k) + row * D;
+      if (!is_v && lane == 0) c.pos[row] = a.pos[token];
+    }
+    store4(dst + o0, x);
+    store4(dst + o1, x + 4);
+  }
+  // s_len was read before the barrier above: with one block per sequence, or lengths that
+  // come from elsewhere, nobody still reads what is set here
+  if (g.set_lens && tile == 0)
+    for (int h = tid; h < H; h += blockDim.x)
+      if (s_len[h] >= 0) g.lens[(long long)s * H + h] = s_len[h] + n;
+}
+
+// lens += tokens, for sequences of several thread blocks that read lens themselves.
+__global__ void append_lens_kernel(AppendArgs g) {
+  grid_dep_wait();
+  const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+  if (i >= (long long)g.c.seqs * g.c.kv_heads) return;
+  int first;
+  const int n = tokens_of(g.t, (int)(i / g.c.kv_heads), first);
+  const int len = g.lens[i];
+  if (n < 0 || len < 0 || len > g.c.capacity || n > g.c.capacity - len) return;
+  g.lens[i] = len + n;
+}
+
+bool aligned(const void* p, long long stride, int size) {
+  return ((uintptr_t)p & 15u) == 0 && stride >= 0 && (stride * size) % 16 == 0;
+}
+
+template <typename T, int D>
+cudaError_t launch_append(AppendArgs& g, cudaStream_t st, int* launches) {
+  const int rows = (g.a.q ? g.c.kv_heads * g.c.group : 0) + 2 * g.c.kv_heads;
+  g.tiles = (int)(((long long)g.t.max_tokens + kTokens - 1) / kTokens);
+  const bool in_place = !g.a.lens_in || g.a.lens_in == g.lens;
+  g.set_lens = !in_place || g.tiles == 1;
+  int threads = kAppendThreads;
+  if (g.tiles == 1) {                 // a thread group per head row, as far as they go
+    const long long want = (long long)rows * g.t.max_tokens * (D / 8);
+    threads = want > 1024 ? 1024 : (int)((want + 31) / 32 * 32);
+  }
+  const long long blocks = (long long)g.c.seqs * g.tiles;
+  if (blocks > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
+  cudaError_t e = launch_after(append_kernel<T, D>, dim3((unsigned)blocks), dim3(threads),
+                               (size_t)g.c.kv_heads * 4, st, g);
+  if (e != cudaSuccess) return e;
+  note_launch(st, launches, "append");
+  if (g.set_lens) return cudaSuccess;
+  const long long slices = (long long)g.c.seqs * g.c.kv_heads;
+  e = launch_after(append_lens_kernel, dim3((unsigned)((slices + 255) / 256)), dim3(256), 0, st,
+                   g);
+  if (e == cudaSuccess) note_launch(st, launches, "append_lens");
+  return e;
+}
+
+}  // namespace
+}  // namespace nx
+
+extern "C" nx_status nexus_append(nx_cache* cache, const nx_tokens* tokens, const nx_append* args,
+                                  int32_t* dev_status, nx_stream_t stream) {
+  using namespace nx;
+  int launches = 0;
+  begin_call();
+  if (!valid_cache(cache) || !valid_tokens(*cache, tokens) || !args || !dev_status)
+    return NX_ERR_INVALID_ARG;
+  const nx_cache& c = *cache;
+  const nx_append& a = *args;
+  const int size = c.dtype == NX_DTYPE_BF16 ? 2 : 4;
+  const int D = c.head_dim;
+  if (a.reserved != 0 || !(a.eps >= 0.f) || !(a.eps < 3.0e38f)) return NX_ERR_INVALID_ARG;
+  if (a.rotary_dim < 0 || a.rotary_dim > D || a.rotary_dim % 8) return NX_ERR_INVALID_ARG;
+  if ((a.rotary_dim > 0) != (a.rotary != nullptr) || ((uintptr_t)a.rotary & 7u))
+    return NX_ERR_INVALID_ARG;
+  if (c.kv_heads > kMaxAppendHeads || (long long)c.kv_heads * c.group > (1 << 20))
+    return NX_ERR_UNSUPPORTED;
+  if ((a.q == nullptr) != (a.q_out == nullptr) && tokens->tokens > 0) return NX_ERR_INVALID_ARG;
+  if (tokens->tokens > 0) {
+    if (!a.k || !a.v || !a.pos) return NX_ERR_INVALID_ARG;
+    if (!aligned(a.k, a.k_stride, size) || !aligned(a.v, a.v_stride, size) ||
+        !aligned(a.q, a.q_stride, size) || !aligned(a.q_out, 0, size))
+      return NX_ERR_INVALID_ARG;
+    const long long hq = (long long)c.kv_heads * c.group * D;
+    if (a.q && a.q == a.q_out && a.q_stride != hq) return NX_ERR_INVALID_ARG;
+  }
+  if (((uintptr_t)a.q_norm & 15u) || ((uintptr_t)a.k_norm & 15u)) return NX_ERR_INVALID_ARG;
+
+  AppendArgs g{};
+  g.c = c;
+  g.t = *tokens;
+  g.a = a;
+  g.dev_status = dev_status;
+  const long long per_layer = (long long)c.seqs * c.kv_heads;
+  g.lens = c.lens + tokens->layer * per_layer;
+  if (a.lens_in && a.lens_in != g.lens && a.lens_in < g.lens + per_layer &&
+      g.lens < a.lens_in + per_layer)
+    return NX_ERR_INVALID_ARG;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (size == 2)
+    e = D == 128 ? launch_append<__nv_bfloat16, 128>(g, st, &launches)
+                 : launch_append<__nv_bfloat16, 64>(g, st, &launches);
+  else
+    e = D == 128 ? launch_append<float, 128>(g, st, &launches)
+                 : launch_append<float, 64>(g, st, &launches);
+  return finish(e, launches);
+}

@@ -25,6 +25,7 @@ constexpr long long kSpinLimit = 1LL << 22;   // bounded waits: ~0.3-1 s at most
 // the multi-block selection serves up to kMultiSlices slices, kMultiStride ints of scratch each
 constexpr int kMultiSlices = 256;
 constexpr int kMultiStride = 512;
+constexpr int kMaxAppendHeads = 8192; // KV heads of nexus_append (their lengths sit in shared memory)
 constexpr uint32_t kForcedKey = 0xFFFFFFFFu;  // order key of a forced (always kept) slot
 
 // ---------------------------------------------------------------------------
@@ -81,6 +82,41 @@ __device__ __forceinline__ long long row_of(const nx_cache& c, int l, int s, int
   if (page < 0 || page >= c.num_pages) return -1;
   return (((long long)l * c.num_pages + page) * c.kv_heads + h) * (long long)c.page_size +
          (j % c.page_size);
+}
+
+// Whether a description of new tokens fits the cache.
+inline bool valid_tokens(const nx_cache& c, const nx_tokens* t) {
+  if (!t || t->layer < 0 || t->layer >= c.layers || t->reserved != 0) return false;
+  if (t->tokens < 0 || t->max_tokens < 1) return false;
+  return t->cu_tokens || (long long)c.seqs * t->max_tokens == t->tokens;
+}
+
+// The rows [first, first + return value) that sequence s owns of the per-token arrays; -1
+// for a bad cu_tokens.
+__device__ __forceinline__ int tokens_of(const nx_tokens& t, int s, int& first) {
+  if (!t.cu_tokens) {
+    first = s * t.max_tokens;
+    return t.max_tokens;
+  }
+  first = t.cu_tokens[s];
+  const int end = t.cu_tokens[s + 1];
+  if (first < 0 || end < first || end > t.tokens || end - first > t.max_tokens) return -1;
+  return end - first;
+}
+
+// Rows of one block of an 8-bit image.
+__host__ __device__ __forceinline__ int image_block(const nx_cache& c) {
+  return c.page_size && c.page_size < kBlockRows ? c.page_size : kBlockRows;
+}
+
+// Index of the scale of the block that starts at slot j of slice (l, s, h) (b = image_block);
+// -1 if the page table entry is out of range.
+__device__ __forceinline__ long long image_scale_at(const nx_cache& c, int l, int s, int h,
+                                                    int j, int b) {
+  if (c.page_size == 0)
+    return (((long long)l * c.seqs + s) * c.kv_heads + h) * ((c.capacity + b - 1) / b) + j / b;
+  const long long row = row_of(c, l, s, h, j);
+  return row < 0 ? -1 : row / b;
 }
 
 __device__ __forceinline__ void slice_coords(const nx_cache& c, int slice, int& l, int& s,
@@ -302,6 +338,11 @@ __device__ __forceinline__ bool wait_at_least(const int* addr, int target, int32
   atomicOr(dev_status, NX_DEV_TIMEOUT);
   return false;
 }
+
+// nx_api.cu: whether a cache's sizes, pointers and alignments are usable.
+bool valid_cache(const nx_cache* c);
+// nx_image.cu: whether an 8-bit image has its pointers.
+bool valid_image(const nx_image* im);
 
 // Bookkeeping after every kernel launch of an entry point: counts it, remembers its
 // name and, when a benchmark armed nexus_profile_next_call, records its event.
