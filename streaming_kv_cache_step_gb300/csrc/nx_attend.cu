@@ -1,111 +1,812 @@
 // nx_attend.cu -- nexus_attend: softmax attention of new tokens over one layer's slices, from
 // the cache or from its 8-bit image.
 //
-// One thread block per token and query head; its warps take every fourth row each, a lane
-// holding head_dim / 32 features, with the running maximum and sum of the softmax in
-// binary32, and are joined in shared memory at the end.
+// With x_j = c1 <q, k_j> (c1 = scale log2 e), one pass over a slice keeps a running reference
+// m, the sum l = sum 2^(x_j - m) and o = sum 2^(x_j - m) v_j; raising m to m' multiplies l and
+// o by 2^(m - m'). Pieces of a slice join by the same rule. All three are binary32.
+//
+// A slice with one new token has group = 4..8 query rows per 512 B of K and V (256 B from the
+// image): some 4 flop a byte, far below what the tensor cores need to matter, so the kernel
+// is a stream of K and V from HBM. What it does per byte is kept small instead:
+//   - every warp works alone on 16 slots at a time: its lanes load K and V straight into the
+//     registers of mma fragments (16-byte loads, whole 64- or 128-byte lines). The order of
+//     features inside a dot product is free, so that a lane's 16 bytes of a K row are its
+//     operands of two (bf16) or four (e4m3) k-steps, with the query rows loaded in the same
+//     order; V's operands pair two slots of one feature, which takes one byte permute each.
+//     No shared memory, no barrier, nothing between a load and the mma that waits for it;
+//   - the next 16 slots' K is in flight during softmax and PV, their V during QK;
+//   - an mma has 16 rows, a decode step 8 or fewer: the spare eight carry the probabilities'
+//     rounding errors (p = hi + lo), so that bf16 probabilities cost no accuracy.
+// The slots of all slices, 64 to a tile, are dealt out evenly to as many thread blocks as fit
+// the GPU at once, whatever the slices' lengths; a slice that a boundary cuts is joined by
+// attend_join_kernel.
 #include <cuda_fp8.h>
-#include <math.h>
 
-#include "nx_internal.cuh"
+#include "nx_attend.cuh"
 
 namespace nx {
 namespace {
 
-struct AttendArgs {
-  nx_cache c;
-  nx_tokens t;
-  nx_image im;          // im.k null: no image
-  nx_attend a;
-  int32_t* dev_status;
-  int b;                // rows per image block
+constexpr int kWarps = 4;
+constexpr int kTileSlots = 64;         // slots of one tile of a thread block
+// kTail: bf16 rows behind an image, with their output features in the image's order
+enum Kind { kBf16 = 0, kImage = 1, kF32 = 2, kTail = 3 };
+template <int KIND>
+constexpr bool kIsBf16 = KIND == kBf16 || KIND == kTail;
+
+// Probabilities are kept at 2^kUp times their size, and m is only raised when a logit is more
+// than 2^kSlack above it, so they are at most 2^(kUp + kSlack) = 32768: below fp16's largest
+// value, with 2^-36 of the largest one still representable.
+constexpr float kUp = 11.f, kSlack = 4.f;
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+template <int KIND>
+__device__ __forceinline__ void mma16(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  if constexpr (kIsBf16<KIND>)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else if constexpr (KIND == kImage)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t e4m3_pair(uint32_t two) {
+  const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
+  return (uint32_t)r.x | (uint32_t)r.y << 16;
+}
+
+template <int KIND>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  if constexpr (kIsBf16<KIND>) {
+    const __nv_bfloat162 r = __floats2bfloat162_rn(a, b);
+    return reinterpret_cast<const uint32_t&>(r);
+  } else {
+    const __half2 r = __floats2half2_rn(a, b);
+    return reinterpret_cast<const uint32_t&>(r);
+  }
+}
+
+// What rounding to 16 bits took off a pair.
+template <int KIND>
+__device__ __forceinline__ uint32_t rest2(float a, float b, uint32_t hi) {
+  if constexpr (kIsBf16<KIND>)
+    return pack2<KIND>(a - __uint_as_float(hi << 16), b - __uint_as_float(hi & 0xFFFF0000u));
+  const __half2 h = reinterpret_cast<const __half2&>(hi);
+  return pack2<KIND>(a - __low2float(h), b - __high2float(h));
+}
+
+// The part of a binary32 value that a tf32 operand holds exactly; the rest is the other term.
+__device__ __forceinline__ uint32_t tf32_hi(uint32_t x) { return x & 0xFFFFE000u; }
+__device__ __forceinline__ uint32_t tf32_lo(uint32_t x) {
+  return __float_as_uint(__uint_as_float(x) - __uint_as_float(tf32_hi(x)));
+}
+
+// How K and V of KIND reach the fragments. g = lane / 4 and c = lane % 4 as in an mma.
+template <int KIND, int D>
+struct Shape {
+  static constexpr int kSlots = KIND == kF32 ? 8 : 16;           // slots of a warp's step
+  static constexpr int NT = kSlots / 8;                          // mma column tiles of them
+  static constexpr int kBytes = KIND == kF32 ? 4 : kIsBf16<KIND> ? 2 : 1;
+  static constexpr int KV = D * kBytes / 64;                     // 16-byte loads of a K row
+  static constexpr int VV = D * kBytes >= 128 ? D * kBytes / 128 : 1;   // loads of a V row
+  static constexpr int kPer = D / 8 / VV;                        // features of one V load
+  // V load w of lane g covers features w kWide + g kStep .. + kPer - 1: whole lines for a
+  // load, but behind an image what the image's lane g has (D / 8 features in a row)
+  static constexpr int kStep = KIND == kTail ? D / 8 : kPer;
+  static constexpr int kWide = KIND == kTail ? kPer : 8 * kPer;
+  // the feature that column n of output tile t stands for
+  static __device__ __forceinline__ int feature(int t, int n) {
+    return t / kPer * kWide + n * kStep + t % kPer;
+  }
 };
 
-constexpr int kAttendWarps = 4;
+template <int KIND, int D>
+struct Rows {
+  using S = Shape<KIND, D>;
+  uint4 k[S::NT][S::KV];
+  uint4 v[S::NT][2][S::VV];            // image with D = 64: .x and .y only
+};
 
-__device__ __forceinline__ float e4m3_value(uint8_t x) {
-  const __half_raw r = __nv_cvt_fp8_to_halfraw(x, __NV_E4M3);
-  return __half2float(__half(r));
+// One warp's running state: o[t] holds rows g (c0, c1) and g + 8 (c2, c3) of output tile t.
+template <int D, int ROWS>
+struct State {
+  float o[D / 8][4];
+  float m[ROWS / 8], l[ROWS / 8];
+};
+
+// Where a unit's rows lie. One page table entry per 8 slots is enough: pages and image blocks
+// are multiples of 8 rows, and so is every t below. Entries are fetched two steps ahead of the
+// rows they lead to, so that their latency is not added to the rows'.
+struct Where {
+  const int32_t* table;  // the sequence's pages; null: contiguous
+  long long first;       // contiguous: the slice's first row; paged: (layer, head)'s offset
+  long long per_page;    // rows from one page to the next
+  int shift, pages;
+
+  __device__ __forceinline__ Where(const AttendArgs& g, const AttendUnit& u) {
+    const nx_cache& c = g.c;
+    shift = 0;
+    pages = c.num_pages;
+    per_page = 0;
+    if (c.page_size) {
+      table = c.block_table + (long long)u.s * c.max_pages_per_seq;
+      shift = __ffs(c.page_size) - 1;
+      per_page = (long long)c.kv_heads << shift;
+      first = (long long)g.t.layer * c.num_pages * per_page + ((long long)u.h << shift);
+    } else {
+      table = nullptr;
+      first = (((long long)g.t.layer * c.seqs + u.s) * c.kv_heads + u.h) * c.capacity;
+    }
+  }
+  template <int NT>
+  __device__ __forceinline__ void pages_of(int t, int end, int* page) const {
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+      page[j] = table && t + 8 * j < end ? table[(t + 8 * j) >> shift] : 0;
+  }
+  // row indexes of slots t, t + 8; -1: a bad page, -2: nothing there
+  template <int NT>
+  __device__ __forceinline__ void rows_of(int t, int end, const int* page, long long* row) const {
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const int slot = t + 8 * j;
+      row[j] = slot >= end                             ? -2
+               : !table                                ? first + slot
+               : page[j] < 0 || page[j] >= pages       ? -1
+                   : first + page[j] * per_page + (slot & ((1 << shift) - 1));
+    }
+  }
+};
+
+template <int KIND, int D>
+__device__ __forceinline__ void load_k(const AttendArgs& g, const long long* row, int left,
+                                       int lane, Rows<KIND, D>& x) {
+  using S = Shape<KIND, D>;
+  const char* base = static_cast<const char*>(KIND == kImage ? g.im.k : g.c.k);
+#pragma unroll
+  for (int j = 0; j < S::NT; ++j) {
+    const bool ok = row[j] >= 0 && 8 * j + lane / 4 < left;
+    const char* p = base + (row[j] + lane / 4) * (D * S::kBytes) + (lane % 4) * 16;
+#pragma unroll
+    for (int u = 0; u < S::KV; ++u)
+      x.k[j][u] = ok ? __ldcs(reinterpret_cast<const uint4*>(p + u * 64))
+                     : make_uint4(0, 0, 0, 0);
+  }
+}
+
+template <int KIND, int D>
+__device__ __forceinline__ void load_v(const AttendArgs& g, const long long* row, int left,
+                                       int lane, Rows<KIND, D>& x) {
+  using S = Shape<KIND, D>;
+  const char* base = static_cast<const char*>(KIND == kImage ? g.im.v : g.c.v);
+#pragma unroll
+  for (int j = 0; j < S::NT; ++j)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int slot = 2 * (lane % 4) + e;
+      const bool ok = row[j] >= 0 && 8 * j + slot < left;
+      const char* p = base + (row[j] + slot) * (D * S::kBytes);
+      if constexpr (D * S::kBytes < 128) {
+        const uint2 r = ok ? __ldcs(reinterpret_cast<const uint2*>(p + lane / 4 * 8))
+                           : make_uint2(0, 0);
+        x.v[j][e][0].x = r.x;
+        x.v[j][e][0].y = r.y;
+      } else {
+#pragma unroll
+        for (int w = 0; w < S::VV; ++w)
+          x.v[j][e][w] = ok ? __ldcs(reinterpret_cast<const uint4*>(
+                                  p + (w * S::kWide + lane / 4 * S::kStep) * S::kBytes))
+                            : make_uint4(0, 0, 0, 0);
+      }
+    }
+}
+
+__device__ __forceinline__ uint32_t word(const uint4& x, int i) {
+  return i == 0 ? x.x : i == 1 ? x.y : i == 2 ? x.z : x.w;
+}
+
+// The query rows of a unit as mma operands, in the feature order of load_k.
+template <int KIND, int D, int ROWS>
+struct Query {
+  using S = Shape<KIND, D>;
+  static constexpr int kSteps = KIND == kF32 ? D / 8 : D / 16;
+  static constexpr int kRegs = KIND == kF32 ? 2 : 2 * (ROWS / 8);   // per k-step
+  uint32_t a[kSteps][kRegs];
+  float c1[ROWS / 8];            // c1, times what the queries were divided by
+
+  __device__ __forceinline__ void load(const AttendArgs& g, const AttendUnit& u, int lane) {
+#pragma unroll
+    for (int e = 0; e < ROWS / 8; ++e) {
+      const int r = lane / 4 + 8 * e;
+      const bool ok = r < u.rows;
+      const int row = u.r0 + r;
+      const long long at = ok ? (u.first + row / g.c.group) * g.a.q_stride +
+                                    ((long long)u.h * g.c.group + row % g.c.group) * D
+                              : 0;
+      c1[e] = g.c1;
+      if constexpr (kIsBf16<KIND>) {
+        const char* p = static_cast<const char*>(g.a.q) + at * 2 + lane % 4 * 16;
+#pragma unroll
+        for (int i = 0; i < S::KV; ++i) {
+          const uint4 x = ok ? *reinterpret_cast<const uint4*>(p + i * 64) : make_uint4(0, 0, 0, 0);
+          a[2 * i][2 * e] = x.x;
+          a[2 * i][2 * e + 1] = x.y;
+          a[2 * i + 1][2 * e] = x.z;
+          a[2 * i + 1][2 * e + 1] = x.w;
+        }
+      } else if constexpr (KIND == kF32) {
+        const char* p = static_cast<const char*>(g.a.q) + at * 4 + lane % 4 * 16;
+#pragma unroll
+        for (int i = 0; i < S::KV; ++i) {
+          const uint4 x = ok ? *reinterpret_cast<const uint4*>(p + i * 64) : make_uint4(0, 0, 0, 0);
+          a[2 * i][0] = x.x;
+          a[2 * i][1] = x.y;
+          a[2 * i + 1][0] = x.z;
+          a[2 * i + 1][1] = x.w;
+        }
+      } else {
+        // e4m3 codes become fp16, and so does the query row, divided by the power of two that
+        // brings its largest value to [2^13, 2^14): bf16's eight bits are kept down to 2^-28
+        // of that value, and what is lost below is at most 2^-38 of it
+        const char* p = static_cast<const char*>(g.a.q) + at * 2 + lane % 4 * 32;
+        uint4 x[S::KV][2];
+        float most = 0.f;
+#pragma unroll
+        for (int i = 0; i < S::KV; ++i)
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            x[i][y] = ok ? *reinterpret_cast<const uint4*>(p + i * 128 + y * 16)
+                         : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              most = fmaxf(most, fabsf(__uint_as_float(word(x[i][y], w) << 16)));
+              most = fmaxf(most, fabsf(__uint_as_float(word(x[i][y], w) & 0xFFFF0000u)));
+            }
+          }
+        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+        int up = 0;
+        if (most > 0.f && most < INFINITY) {
+          frexpf(most, &up);
+          up = 14 - up;
+        }
+        c1[e] = ldexpf(g.c1, -up);
+        const float f0 = ldexpf(1.f, up / 2), f1 = ldexpf(1.f, up - up / 2);
+#pragma unroll
+        for (int i = 0; i < S::KV; ++i)
+#pragma unroll
+          for (int y = 0; y < 2; ++y)
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              const uint32_t two = word(x[i][y], w);
+              a[4 * i + 2 * y + w / 2][2 * e + w % 2] =
+                  pack2<kImage>(__uint_as_float(two << 16) * f0 * f1,
+                                __uint_as_float(two & 0xFFFF0000u) * f0 * f1);
+            }
+      }
+    }
+  }
+};
+
+// The products of the query rows with 8 or 16 rows of K.
+template <int KIND, int D, int ROWS>
+__device__ __forceinline__ void qk(const Query<KIND, D, ROWS>& q, const Rows<KIND, D>& x,
+                                   float s[][4]) {
+  using S = Shape<KIND, D>;
+#pragma unroll
+  for (int j = 0; j < S::NT; ++j) {
+    s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
+#pragma unroll
+    for (int u = 0; u < S::KV; ++u) {
+      if constexpr (kIsBf16<KIND>) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t* a = q.a[2 * u + i];
+          const uint32_t f[4] = {a[0], ROWS == 16 ? a[2 % (2 * (ROWS / 8))] : 0u, a[1],
+                                 ROWS == 16 ? a[3 % (2 * (ROWS / 8))] : 0u};
+          mma16<KIND>(s[j], f, word(x.k[j][u], 2 * i), word(x.k[j][u], 2 * i + 1));
+        }
+      } else if constexpr (KIND == kImage) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t* a = q.a[4 * u + i];
+          const uint32_t f[4] = {a[0], ROWS == 16 ? a[2 % (2 * (ROWS / 8))] : 0u, a[1],
+                                 ROWS == 16 ? a[3 % (2 * (ROWS / 8))] : 0u};
+          const uint32_t w = word(x.k[j][u], i);
+          mma16<KIND>(s[j], f, e4m3_pair(w & 0xFFFFu), e4m3_pair(w >> 16));
+        }
+      } else {
+        // rows g hold q's high part, rows g + 8 its low part: two products give all four terms
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t* a = q.a[2 * u + i];
+          const uint32_t f[4] = {tf32_hi(a[0]), tf32_lo(a[0]), tf32_hi(a[1]), tf32_lo(a[1])};
+          const uint32_t b0 = word(x.k[j][u], 2 * i), b1 = word(x.k[j][u], 2 * i + 1);
+          mma16<KIND>(s[j], f, tf32_hi(b0), tf32_hi(b1));
+          mma16<KIND>(s[j], f, tf32_lo(b0), tf32_lo(b1));
+        }
+      }
+    }
+    if constexpr (KIND == kF32) {
+      s[j][0] += s[j][2];
+      s[j][1] += s[j][3];
+    }
+  }
+}
+
+// o += p V.
+template <int KIND, int D, int ROWS>
+__device__ __forceinline__ void pv(const Rows<KIND, D>& x, const float p[][4], State<D, ROWS>& st) {
+  using S = Shape<KIND, D>;
+  if constexpr (KIND == kF32) {
+    const uint32_t p0 = __float_as_uint(p[0][0]), p1 = __float_as_uint(p[0][1]);
+    const uint32_t f[4] = {tf32_hi(p0), tf32_lo(p0), tf32_hi(p1), tf32_lo(p1)};
+#pragma unroll
+    for (int w = 0; w < S::VV; ++w)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t b0 = word(x.v[0][0][w], e), b1 = word(x.v[0][1][w], e);
+        mma16<KIND>(st.o[4 * w + e], f, tf32_hi(b0), tf32_hi(b1));
+        mma16<KIND>(st.o[4 * w + e], f, tf32_lo(b0), tf32_lo(b1));
+      }
+  } else {
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      hi[2 * j] = pack2<KIND>(p[j][0], p[j][1]);
+      lo[2 * j] = rest2<KIND>(p[j][0], p[j][1], hi[2 * j]);
+      if constexpr (ROWS == 8) {
+        hi[2 * j + 1] = lo[2 * j];
+      } else {
+        hi[2 * j + 1] = pack2<KIND>(p[j][2], p[j][3]);
+        lo[2 * j + 1] = rest2<KIND>(p[j][2], p[j][3], hi[2 * j + 1]);
+      }
+    }
+#pragma unroll
+    for (int w = 0; w < S::VV; ++w)
+#pragma unroll
+      for (int i = 0; i < (KIND == kImage && D == 64 ? 2 : 4); ++i) {
+        uint32_t b[2][kIsBf16<KIND> ? 2 : 4];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const uint32_t y0 = word(x.v[j][0][w], i), y1 = word(x.v[j][1][w], i);
+          if constexpr (kIsBf16<KIND>) {
+            b[j][0] = __byte_perm(y0, y1, 0x5410);
+            b[j][1] = __byte_perm(y0, y1, 0x7632);
+          } else {
+            const uint32_t z0 = __byte_perm(y0, y1, 0x5140), z1 = __byte_perm(y0, y1, 0x7362);
+            b[j][0] = e4m3_pair(z0 & 0xFFFFu);
+            b[j][1] = e4m3_pair(z0 >> 16);
+            b[j][2] = e4m3_pair(z1 & 0xFFFFu);
+            b[j][3] = e4m3_pair(z1 >> 16);
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < (kIsBf16<KIND> ? 2 : 4); ++e) {
+          float* o = st.o[S::kPer * w + (kIsBf16<KIND> ? 2 : 4) * i + e];
+          mma16<KIND>(o, hi, b[0][e], b[1][e]);
+          // sixteen rows leave no spare ones; fp16 probabilities (2^-11) do without
+          if constexpr (ROWS == 16 && kIsBf16<KIND>) mma16<KIND>(o, lo, b[0][e], b[1][e]);
+        }
+      }
+  }
+}
+
+// Slots [base + kSlots * i, ...) for i = from, from + kWarps, ... < to, up to slot `end`.
+template <int KIND, int D, int ROWS>
+__device__ __forceinline__ void attend_part(const AttendArgs& g, const AttendUnit& u, int base,
+                                            int end, int from, int to, State<D, ROWS>& st) {
+  using S = Shape<KIND, D>;
+  if (from >= to) return;
+  const int lane = threadIdx.x % 32;
+  Query<KIND, D, ROWS> q;
+  q.load(g, u, lane);
+  int lim[ROWS / 8];
+#pragma unroll
+  for (int e = 0; e < ROWS / 8; ++e) {
+    const int r = lane / 4 + 8 * e;
+    lim[e] = r < u.rows ? min(end, row_limit(g, u, u.r0 + r)) : 0;
+  }
+  const int low = min(end, u.low);
+  float vref = 1.1754944e-38f;          // image: the largest value scale so far; o is in it
+  Rows<KIND, D> x;
+  const Where at(g, u);
+  const long long blocks0 =
+      KIND == kImage && !g.c.page_size ? image_scale_at(g.c, g.t.layer, u.s, u.h, 0, g.b) : 0;
+  long long row[S::NT], next[S::NT];
+  int page[S::NT];
+  float ks[S::NT], vs[S::NT], ks_next[S::NT], vs_next[S::NT];
+  constexpr int kNext = S::kSlots * kWarps;
+  const auto scales = [&](int t, const long long* r, float* k, float* v) {
+#pragma unroll
+    for (int j = 0; j < S::NT; ++j) {
+      const long long i = g.c.page_size ? r[j] / g.b : blocks0 + (t + 8 * j) / g.b;
+      k[j] = r[j] < 0 ? 0.f : g.im.k_scale[i];
+      v[j] = r[j] < 0 ? 0.f : g.im.v_scale[i];
+    }
+  };
+  {
+    const int t = base + S::kSlots * from;
+    at.pages_of<S::NT>(t, end, page);
+    at.rows_of<S::NT>(t, end, page, row);
+    load_k(g, row, end - t, lane, x);
+    if constexpr (KIND == kImage) scales(t, row, ks, vs);
+    load_v(g, row, end - t, lane, x);
+    at.pages_of<S::NT>(t + kNext, end, page);
+  }
+  for (int i = from; i < to; i += kWarps) {
+    const int t = base + S::kSlots * i, tn = t + kNext;
+    const int endn = i + kWarps < to ? end : 0;
+    at.rows_of<S::NT>(tn, endn, page, next);
+    at.pages_of<S::NT>(tn + kNext, end, page);
+    if constexpr (KIND == kImage) scales(tn, next, ks_next, vs_next);
+    float s[S::NT][4];
+    qk<KIND, D, ROWS>(q, x, s);
+    load_k(g, next, end - tn, lane, x);
+
+    // logits in log2 units; beyond a row's limit or on a bad page: -inf
+    float top[ROWS / 8];
+#pragma unroll
+    for (int e = 0; e < ROWS / 8; ++e) top[e] = -INFINITY;
+    bool bad = false;
+#pragma unroll
+    for (int j = 0; j < S::NT; ++j) bad |= row[j] < 0;
+    const bool mask = bad || t + S::kSlots > low;
+#pragma unroll
+    for (int j = 0; j < S::NT; ++j)
+#pragma unroll
+      for (int e = 0; e < ROWS / 8; ++e)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          float& z = s[j][2 * e + y];
+          z *= KIND == kImage ? q.c1[e] * ks[j] : q.c1[e];
+          if (mask && (row[j] < 0 || t + 8 * j + 2 * (lane % 4) + y >= lim[e])) z = -INFINITY;
+          top[e] = fmaxf(top[e], z);
+        }
+    if (bad) {
+#pragma unroll
+      for (int j = 0; j < S::NT; ++j)
+        if (row[j] == -1 && lane == 0) atomicOr(g.dev_status, NX_DEV_BAD_PAGE);
+    }
+    bool up = false;
+#pragma unroll
+    for (int e = 0; e < ROWS / 8; ++e) {
+      top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 1));
+      top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 2));
+      up |= top[e] > st.m[e] + kSlack;
+    }
+    float vnew = vref;
+    if constexpr (KIND == kImage) {
+#pragma unroll
+      for (int j = 0; j < S::NT; ++j) vnew = fmaxf(vnew, vs[j]);
+      up |= vnew > vref;
+    }
+    if (__any_sync(0xffffffffu, up)) {
+      const float vf = KIND == kImage ? vref / vnew : 1.f;
+      vref = vnew;
+      float f[ROWS / 8];
+#pragma unroll
+      for (int e = 0; e < ROWS / 8; ++e) {
+        const float m = top[e] > st.m[e] + kSlack ? top[e] : st.m[e];
+        f[e] = m > st.m[e] ? ex2(st.m[e] - m) : 1.f;
+        st.m[e] = m;
+        st.l[e] *= f[e];
+        f[e] *= vf;
+      }
+#pragma unroll
+      for (int n = 0; n < D / 8; ++n) {
+        st.o[n][0] *= f[0];
+        st.o[n][1] *= f[0];
+        st.o[n][2] *= f[ROWS / 8 - 1];
+        st.o[n][3] *= f[ROWS / 8 - 1];
+      }
+    }
+    float vr[S::NT];
+    if constexpr (KIND == kImage) {
+#pragma unroll
+      for (int j = 0; j < S::NT; ++j) vr[j] = vs[j] / vref;
+    }
+#pragma unroll
+    for (int e = 0; e < ROWS / 8; ++e) {
+      const float sub = (st.m[e] == -INFINITY ? 0.f : st.m[e]) - kUp;
+#pragma unroll
+      for (int j = 0; j < S::NT; ++j)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          float& z = s[j][2 * e + y];
+          z = ex2(z - sub);
+          st.l[e] += z;
+          if constexpr (KIND == kImage) z *= vr[j];
+        }
+    }
+    pv<KIND, D, ROWS>(x, s, st);
+    load_v(g, next, end - tn, lane, x);
+#pragma unroll
+    for (int j = 0; j < S::NT; ++j) {
+      row[j] = next[j];
+      if constexpr (KIND == kImage) {
+        ks[j] = ks_next[j];
+        vs[j] = vs_next[j];
+      }
+    }
+  }
+  if constexpr (KIND == kImage) {
+#pragma unroll
+    for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) st.o[n][e] *= vref;
+  }
+}
+
+__device__ __forceinline__ int unit_tiles(const AttendUnit& u) {
+  if (!u.rows) return 0;
+  const int ea = min(u.held, u.end);
+  const int n = (ea + kTileSlots - 1) / kTileSlots + (u.end - ea + kTileSlots - 1) / kTileSlots;
+  return n < 1 ? 1 : n;                 // an empty row still has an output
+}
+
+template <typename T>
+__device__ __forceinline__ void store_out(const AttendArgs& g, const AttendUnit& u, int r, int D,
+                                          int f, float x) {
+  const int row = u.r0 + r;
+  static_cast<T*>(g.a.out)[(long long)(u.first + row / g.c.group) * g.a.out_stride +
+                           ((long long)u.h * g.c.group + row % g.c.group) * D + f] = (T)x;
+}
+
+// o / l, and ln l with the reference put back.
+__device__ __forceinline__ void finish_row(const AttendArgs& g, const AttendUnit& u, int r, int D,
+                                           int f, float m, float l, float o) {
+  const float y = l == 0.f ? 0.f : o / l;
+  if (g.c.dtype == NX_DTYPE_BF16) store_out<__nv_bfloat16>(g, u, r, D, f, y);
+  else store_out<float>(g, u, r, D, f, y);
+  if (f == 0 && g.a.lse) {
+    const int row = u.r0 + r;
+    g.a.lse[(long long)(u.first + row / g.c.group) * (g.c.kv_heads * g.c.group) +
+            u.h * g.c.group + row % g.c.group] =
+        l == 0.f ? -INFINITY : (m - kUp + log2f(l)) * 0.69314718055994531f;
+  }
+}
+
+template <int KIND, int D, int ROWS>
+__global__ void __launch_bounds__(kWarps * 32, 2) attend_kernel(AttendArgs g) {
+  __shared__ float s_o[kWarps][ROWS][D];
+  __shared__ float s_m[kWarps][ROWS], s_l[kWarps][ROWS];
+  __shared__ int s_sum[kWarps], s_at[3];
+  grid_dep_wait();
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  const int b = blockIdx.x;
+
+  // where this block's share of all tiles starts: every thread adds up a run of units
+  const int run = (g.units + kWarps * 32 - 1) / (kWarps * 32);
+  const int u0 = min(g.units, tid * run), u1 = min(g.units, u0 + run);
+  int sum = 0;
+  for (int i = u0; i < u1; ++i) sum += unit_tiles(attend_unit<ROWS>(g, i));
+  int incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o *= 2) {
+    const int y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) s_sum[warp] = incl;
+  __syncthreads();
+  int before = incl - sum, total = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) before += s_sum[w];
+    total += s_sum[w];
+  }
+  const int per = max(g.min_tiles, (total + (int)gridDim.x - 1) / (int)gridDim.x);
+  const long long start = (long long)b * per;
+  if (start >= before && start < before + sum) {
+    int at = before;
+    for (int i = u0; i < u1; ++i) {
+      const int n = unit_tiles(attend_unit<ROWS>(g, i));
+      if (start < at + n) {
+        s_at[0] = i;
+        s_at[1] = at;
+        break;
+      }
+      at += n;
+    }
+  }
+  __syncthreads();
+  grid_dep_trigger();
+  if (start >= total) {
+    if (tid == 0) g.ws.desc[b] = make_int2(-1, 0);
+    return;
+  }
+  const int stop = (int)min((long long)total, start + per);
+  int unit = s_at[0], at = s_at[1], pos = (int)start;   // `at`: the unit's first tile
+  int2 desc = make_int2(-1, 0);
+  while (pos < stop) {
+    const AttendUnit u = attend_unit<ROWS>(g, unit);
+    const int tiles = unit_tiles(u);
+    const int a0 = pos - at, a1 = min(tiles, stop - at);
+    if (tiles > 0) {
+      State<D, ROWS> st;
+#pragma unroll
+      for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) st.o[n][e] = 0.f;
+#pragma unroll
+      for (int e = 0; e < ROWS / 8; ++e) {
+        st.m[e] = -INFINITY;
+        st.l[e] = 0.f;
+      }
+      const int ea = min(u.held, u.end), ta = (ea + kTileSlots - 1) / kTileSlots;
+      if constexpr (KIND == kImage) {
+        constexpr int k = kTileSlots / Shape<kImage, D>::kSlots;
+        attend_part<kImage, D, ROWS>(g, u, 0, ea, a0 * k + warp,
+                                     min(min(a1, ta) * k, (ea + 15) / 16), st);
+        attend_part<kTail, D, ROWS>(g, u, ea, u.end, max(a0 - ta, 0) * k + warp,
+                                    min((a1 - ta) * k, (u.end - ea + 15) / 16), st);
+      } else {
+        constexpr int k = kTileSlots / Shape<KIND, D>::kSlots, w = Shape<KIND, D>::kSlots;
+        attend_part<KIND, D, ROWS>(g, u, 0, u.end, a0 * k + warp, min(a1 * k, (u.end + w - 1) / w),
+                                   st);
+      }
+      // the warps' states meet in shared memory; rows g and g + 8 of an 8-row tile are the
+      // two terms of the same row
+#pragma unroll
+      for (int e = 0; e < ROWS / 8; ++e) {
+        float l = st.l[e];
+        l += __shfl_xor_sync(0xffffffffu, l, 1);
+        l += __shfl_xor_sync(0xffffffffu, l, 2);
+        if (lane % 4 == 0) {
+          s_m[warp][lane / 4 + 8 * e] = st.m[e];
+          s_l[warp][lane / 4 + 8 * e] = l;
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const int f = Shape<KIND, D>::feature(n, 2 * (lane % 4) + y);
+          if constexpr (ROWS == 8) {
+            s_o[warp][lane / 4][f] = st.o[n][y] + st.o[n][2 + y];
+          } else {
+            s_o[warp][lane / 4][f] = st.o[n][y];
+            s_o[warp][lane / 4 + 8][f] = st.o[n][2 + y];
+          }
+        }
+      __syncthreads();
+      const bool whole = a0 == 0 && a1 == tiles;
+      const int slot = 2 * b + (a0 == 0 ? 1 : 0);
+      for (int i = tid; i < u.rows * D; i += kWarps * 32) {
+        const int r = i / D, f = i % D;
+        float m = -INFINITY, l = 0.f, o = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) m = fmaxf(m, s_m[w][r]);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float k = s_m[w][r] == -INFINITY ? (s_l[w][r] != s_l[w][r] ? 1.f : 0.f)
+                                                 : ex2(s_m[w][r] - m);
+          l += k * s_l[w][r];
+          o += k * s_o[w][r][f];
+        }
+        if (whole) {
+          finish_row(g, u, r, D, f, m, l, o);
+        } else {
+          if (f == 0) g.ws.stat[slot * kPieceRows + r] = make_float2(m, l);
+          g.ws.out[((long long)slot * kPieceRows + r) * D + f] = o;
+        }
+      }
+      __syncthreads();
+      if (a0 == 0 && a1 < tiles) desc = make_int2(unit, (at + tiles - 1) / per);
+    }
+    pos = at + a1;
+    at += tiles;
+    ++unit;
+  }
+  if (tid == 0) g.ws.desc[b] = desc;
+}
+
+// Joins the pieces of the unit that starts in block b and ends in a later one: its first piece
+// lies at 2 b + 1, the others at 2 b' of the blocks that go on with it.
+constexpr int kJoinWarps = 16;
+template <int D, int ROWS>
+__global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(AttendArgs g) {
+  constexpr int E = D / 32, GR = kJoinWarps / ROWS > 0 ? kJoinWarps / ROWS : 1;
+  __shared__ float s_o[kJoinWarps][D], s_m[kJoinWarps], s_l[kJoinWarps];
+  grid_dep_wait();
+  const int b = blockIdx.x;
+  const int2 desc = g.ws.desc[b];
+  if (desc.x < 0) return;
+  const AttendUnit u = attend_unit<ROWS>(g, desc.x);
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int r = warp / GR, part = warp % GR;
+  float m = -INFINITY, l = 0.f, o[E] = {};
+  if (r < u.rows) {
+#pragma unroll 4
+    for (int i = b + part; i <= desc.y; i += GR) {
+      const int slot = i == b ? 2 * b + 1 : 2 * i;
+      const float2 x = g.ws.stat[slot * kPieceRows + r];
+      const float* p = g.ws.out + ((long long)slot * kPieceRows + r) * D + lane;
+      float y[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) y[e] = p[32 * e];
+      const float top = fmaxf(m, x.x), ref = top == -INFINITY ? 0.f : top;
+      const float f0 = ex2(m - ref), f1 = x.x == -INFINITY && x.y != x.y ? 1.f : ex2(x.x - ref);
+      l = l * f0 + x.y * f1;
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = o[e] * f0 + y[e] * f1;
+      m = top;
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < E; ++e) s_o[warp][lane + 32 * e] = o[e];
+  if (lane == 0) {
+    s_m[warp] = m;
+    s_l[warp] = l;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < u.rows * D; i += kJoinWarps * 32) {
+    const int rr = i / D, f = i % D;
+    float top = -INFINITY, sum = 0.f, x = 0.f;
+    for (int w = rr * GR; w < (rr + 1) * GR; ++w) top = fmaxf(top, s_m[w]);
+    for (int w = rr * GR; w < (rr + 1) * GR; ++w) {
+      const float k = s_m[w] == -INFINITY ? (s_l[w] != s_l[w] ? 1.f : 0.f) : ex2(s_m[w] - top);
+      sum += k * s_l[w];
+      x += k * s_o[w][f];
+    }
+    finish_row(g, u, rr, D, f, top, sum, x);
+  }
+}
+
+size_t round256(size_t x) { return (x + 255) / 256 * 256; }
+
+size_t attend_layout(int D, char* base, AttendWs* ws) {
+  size_t at = 0;
+  ws->desc = reinterpret_cast<int2*>(base + at);
+  at += round256(kAttendGrid * sizeof(int2));
+  ws->stat = reinterpret_cast<float2*>(base + at);
+  at += round256((size_t)2 * kAttendGrid * kPieceRows * sizeof(float2));
+  ws->out = reinterpret_cast<float*>(base + at);
+  return at + (size_t)2 * kAttendGrid * kPieceRows * D * sizeof(float);
+}
+
+template <int KIND, int D, int ROWS>
+cudaError_t launch_attend(AttendArgs& g, cudaStream_t st, int* launches) {
+  g.mtiles = (int)(((long long)g.t.max_tokens * g.c.group + ROWS - 1) / ROWS);
+  const long long units = (long long)g.c.seqs * g.c.kv_heads * g.mtiles;
+  const long long most = units * ((g.c.capacity + kTileSlots - 1) / kTileSlots + 1);
+  if (most > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
+  g.units = (int)units;
+  g.min_tiles = 1;
+  const long long fit = 152 * 2;
+  const int grid = (int)(most < fit ? most : fit);
+  cudaError_t e = launch_after(attend_kernel<KIND, D, ROWS>, dim3(grid), dim3(kWarps * 32), 0, st,
+                               g);
+  if (e != cudaSuccess) return e;
+  note_launch(st, launches, "attend");
+  e = launch_after(attend_join_kernel<D, ROWS>, dim3(grid), dim3(kJoinWarps * 32), 0, st, g);
+  if (e == cudaSuccess) note_launch(st, launches, "attend_join");
+  return e;
 }
 
 template <int D>
-__global__ void __launch_bounds__(kAttendWarps * 32) attend_kernel(AttendArgs g) {
-  constexpr int E = D / 32;
-  __shared__ float s_m[kAttendWarps], s_z[kAttendWarps], s_o[kAttendWarps][D];
-  grid_dep_wait();
-  const nx_cache& c = g.c;
-  const int HQ = c.kv_heads * c.group;
-  const long long id = blockIdx.x;
-  const int hq = (int)(id % HQ), i = (int)(id / HQ % g.t.max_tokens);
-  const int s = (int)(id / HQ / g.t.max_tokens);
-  const int h = hq / c.group, l = g.t.layer;
-  int first;
-  const int n = tokens_of(g.t, s, first);
-  if (n < 0 && i == 0 && threadIdx.x == 0) atomicOr(g.dev_status, NX_DEV_BAD_TOKENS);
-  if (i >= n) return;
-  const int slice = (l * c.seqs + s) * c.kv_heads + h;
-  int T = c.lens[slice], held = g.im.k ? g.im.rows[slice] : 0, flag = 0;
-  if (T < 0 || T > c.capacity) flag = NX_DEV_BAD_LEN;
-  else if (held < 0 || held > T || held % g.b) flag = NX_DEV_BAD_IMAGE;
-  if (flag) {
-    if (threadIdx.x == 0) atomicOr(g.dev_status, flag);
-    T = 0;
-  }
-  const int M = g.a.causal ? T - (n - 1 - i) : T;
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  float q[E], o[E] = {}, m = -INFINITY, z = 0.f;
-  for (int e = 0; e < E; ++e)
-    q[e] = ld_elem(g.a.q, c.dtype, (first + i) * g.a.q_stride + hq * D + lane * E + e);
-  for (int j = warp; j < M; j += kAttendWarps) {
-    const long long row = row_of(c, l, s, h, j);
-    if (row < 0) {
-      if (lane == 0) atomicOr(g.dev_status, NX_DEV_BAD_PAGE);
-      continue;
-    }
-    float k[E], v[E], x = 0.f;
-    if (j < held) {
-      const long long at = image_scale_at(c, l, s, h, j, g.b);
-      for (int e = 0; e < E; ++e) {
-        const long long w = row * D + lane * E + e;
-        k[e] = e4m3_value(static_cast<const uint8_t*>(g.im.k)[w]) * g.im.k_scale[at];
-        v[e] = e4m3_value(static_cast<const uint8_t*>(g.im.v)[w]) * g.im.v_scale[at];
-      }
-    } else {
-      for (int e = 0; e < E; ++e) {
-        k[e] = ld_elem(c.k, c.dtype, row * D + lane * E + e);
-        v[e] = ld_elem(c.v, c.dtype, row * D + lane * E + e);
-      }
-    }
-    for (int e = 0; e < E; ++e) x = fmaf(q[e], k[e], x);
-    for (int w = 16; w > 0; w >>= 1) x += __shfl_xor_sync(0xffffffffu, x, w);
-    x *= g.a.scale;
-    const float top = fmaxf(m, x), ref = top == -INFINITY ? 0.f : top;
-    const float old = expf(m - ref), p = expf(x - ref);
-    for (int e = 0; e < E; ++e) o[e] = o[e] * old + p * v[e];
-    z = z * old + p;
-    m = top;
-  }
-  for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = o[e];
-  if (lane == 0) {
-    s_m[warp] = m;
-    s_z[warp] = z;
-  }
-  __syncthreads();
-  float top = -INFINITY, sum = 0.f, r = 0.f;
-  for (int w = 0; w < kAttendWarps; ++w) top = fmaxf(top, s_m[w]);
-  const int f = threadIdx.x;
-  for (int w = 0; w < kAttendWarps; ++w) {
-    const float k = s_m[w] == -INFINITY ? 0.f : expf(s_m[w] - top);
-    sum += k * s_z[w];
-    if (f < D) r += k * s_o[w][f];
-  }
-  if (f < D) {
-    r = sum > 0.f ? r / sum : sum == 0.f ? 0.f : NAN;
-    const long long at = (first + i) * g.a.out_stride + hq * D + f;
-    if (c.dtype == NX_DTYPE_BF16) static_cast<__nv_bfloat16*>(g.a.out)[at] = __float2bfloat16(r);
-    else static_cast<float*>(g.a.out)[at] = r;
-  }
-  if (f == 0 && g.a.lse) g.a.lse[(long long)(first + i) * HQ + hq] = top + logf(sum);
+cudaError_t launch_attend(AttendArgs& g, cudaStream_t st, int* launches) {
+  if (g.c.dtype == NX_DTYPE_F32) return launch_attend<kF32, D, 8>(g, st, launches);
+  const bool few = (long long)g.t.max_tokens * g.c.group <= 8;
+  if (g.im.k)
+    return few ? launch_attend<kImage, D, 8>(g, st, launches)
+               : launch_attend<kImage, D, 16>(g, st, launches);
+  return few ? launch_attend<kBf16, D, 8>(g, st, launches)
+             : launch_attend<kBf16, D, 16>(g, st, launches);
 }
 
 }  // namespace
@@ -114,7 +815,8 @@ __global__ void __launch_bounds__(kAttendWarps * 32) attend_kernel(AttendArgs g)
 extern "C" size_t nexus_attend_workspace_bytes(const nx_cache* cache, const nx_tokens* tokens) {
   using namespace nx;
   if (!valid_cache(cache) || !valid_tokens(*cache, tokens)) return 0;
-  return 256;
+  AttendWs ws;
+  return attend_layout(cache->head_dim, nullptr, &ws);
 }
 
 extern "C" nx_status nexus_attend(const nx_cache* cache, const nx_tokens* tokens,
@@ -146,15 +848,11 @@ extern "C" nx_status nexus_attend(const nx_cache* cache, const nx_tokens* tokens
   if (image) g.im = *image;
   g.a = a;
   g.dev_status = dev_status;
+  attend_layout(c.head_dim, static_cast<char*>(ws), &g.ws);
   g.b = image_block(c);
+  g.c1 = a.scale * 1.4426950408889634f;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const long long blocks = (long long)c.seqs * tokens->max_tokens * c.kv_heads * c.group;
-  if (blocks > 0x7FFFFFFFLL) return NX_ERR_UNSUPPORTED;
-  cudaError_t e = c.head_dim == 128
-                      ? launch_after(attend_kernel<128>, dim3((unsigned)blocks),
-                                     dim3(kAttendWarps * 32), 0, st, g)
-                      : launch_after(attend_kernel<64>, dim3((unsigned)blocks),
-                                     dim3(kAttendWarps * 32), 0, st, g);
-  if (e == cudaSuccess) note_launch(st, &launches, "attend");
-  return finish(e, launches);
+  return finish(c.head_dim == 128 ? launch_attend<128>(g, st, &launches)
+                                  : launch_attend<64>(g, st, &launches),
+                launches);
 }
