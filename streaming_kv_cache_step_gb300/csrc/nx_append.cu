@@ -3,17 +3,21 @@
 //
 // One thread block takes kTokens tokens of one sequence. Its threads first compute the
 // cosines and sines of those tokens (one pair each, shared by all heads of a token: 128
-// features x 40 heads need 64 angles, not 2560), then groups of head_dim / 8 threads take
-// one head row each, 8 features per thread. A thread's 8 features are two runs of 4 that
-// hold 4 whole pairs (runs 4i and rotary_dim / 2 + 4i, or 8i and 8i + 4 when interleaved),
-// so that a rotation needs no exchange between threads; only the norm's sum does.
+// features x 40 heads need 64 angles, not 2560), then a group of head_dim / 8 threads takes
+// one head row of every token in turn, 8 features per thread: what is the same for a head
+// (where it reads and writes, norm weights, the slice's length) is found once. A thread's 8
+// features are two runs of 4 that hold 4 whole pairs (runs 4i and rotary_dim / 2 + 4i, or 8i
+// and 8i + 4 when interleaved), so that a rotation needs no exchange between threads; only
+// the norm's sum does. Rows of kAhead tokens are in flight per thread.
+#include <type_traits>
+
 #include "nx_internal.cuh"
 
 namespace nx {
 namespace {
 
-constexpr int kTokens = 4;            // tokens of a thread block
-constexpr int kAppendThreads = 256;   // its threads, unless one block covers a sequence
+constexpr int kTokens = 16;           // tokens of a thread block
+constexpr int kAppendThreads = 256;   // threads of a block, unless one block covers a sequence
 
 struct AppendArgs {
   nx_cache c;
@@ -21,7 +25,7 @@ struct AppendArgs {
   nx_append a;
   int32_t* dev_status;
   int32_t* lens;        // the layer's part of c.lens
-  int tiles;            // thread blocks per sequence
+  int tiles, parts;     // thread blocks per sequence: token tiles x parts of the head rows
   bool set_lens;        // the kernel sets the new lengths itself
 };
 
@@ -44,18 +48,21 @@ __device__ __forceinline__ float2 rotation_of(int32_t p, uint64_t f) {
 }
 
 template <typename T>
-__device__ __forceinline__ void load4(const T* p, float* x) {
-  if constexpr (sizeof(T) == 2) {
-    const uint2 r = *reinterpret_cast<const uint2*>(p);
-    x[0] = __uint_as_float(r.x << 16);
-    x[1] = __uint_as_float(r.x & 0xFFFF0000u);
-    x[2] = __uint_as_float(r.y << 16);
-    x[3] = __uint_as_float(r.y & 0xFFFF0000u);
-  } else {
-    const float4 r = *reinterpret_cast<const float4*>(p);
-    x[0] = r.x; x[1] = r.y; x[2] = r.z; x[3] = r.w;
+struct Run4 {                         // four features of a row as they lie in memory
+  using Raw = typename std::conditional<sizeof(T) == 2, uint2, float4>::type;
+  Raw r;
+  __device__ __forceinline__ void load(const T* p) { r = *reinterpret_cast<const Raw*>(p); }
+  __device__ __forceinline__ void get(float* x) const {
+    if constexpr (sizeof(T) == 2) {
+      x[0] = __uint_as_float(r.x << 16);
+      x[1] = __uint_as_float(r.x & 0xFFFF0000u);
+      x[2] = __uint_as_float(r.y << 16);
+      x[3] = __uint_as_float(r.y & 0xFFFF0000u);
+    } else {
+      x[0] = r.x; x[1] = r.y; x[2] = r.z; x[3] = r.w;
+    }
   }
-}
+};
 
 template <typename T>
 __device__ __forceinline__ void store4(T* p, const float* x) {
@@ -70,20 +77,24 @@ __device__ __forceinline__ void store4(T* p, const float* x) {
 }
 
 template <typename T, int D>
-__global__ void append_kernel(AppendArgs g) {
+__global__ void __launch_bounds__(1024) append_kernel(AppendArgs g) {
   constexpr int kLanes = D / 8;                      // threads of one head row
+  constexpr int kAhead = sizeof(T) == 2 ? 4 : 2;     // tokens loaded before one is used
   __shared__ float2 s_rot[kTokens][D / 2];
+  __shared__ int s_pos[kTokens];
   extern __shared__ int s_len[];                     // [kv_heads], -1: leave alone
   grid_dep_wait();
 
   const nx_cache& c = g.c;
   const nx_append& a = g.a;
-  const int s = blockIdx.x / g.tiles, tile = blockIdx.x % g.tiles;
+  const int part = blockIdx.x % g.parts, tile = blockIdx.x / g.parts % g.tiles;
+  const int s = blockIdx.x / g.parts / g.tiles;
   const int tid = threadIdx.x;
+  const bool lead = tile == 0 && part == 0;
   int first;
   const int n = tokens_of(g.t, s, first);
   if (n < 0) {
-    if (tile == 0 && tid == 0) atomicOr(g.dev_status, NX_DEV_BAD_TOKENS);
+    if (lead && tid == 0) atomicOr(g.dev_status, NX_DEV_BAD_TOKENS);
     return;
   }
   const int t0 = tile * kTokens;
@@ -99,16 +110,17 @@ __global__ void append_kernel(AppendArgs g) {
     else if (n > c.capacity - len) flag = NX_DEV_FULL;
     if (flag) {
       len = -1;
-      if (tile == 0) atomicOr(g.dev_status, flag);
+      if (lead) atomicOr(g.dev_status, flag);
     }
     s_len[h] = len;
   }
   const int half = a.rotary_dim / 2;
   for (int i = tid; i < nt * half; i += blockDim.x)
     s_rot[i / half][i % half] = rotation_of(a.pos[first + t0 + i / half], a.rotary[i % half]);
+  if (tid < nt) s_pos[tid] = a.pos[first + t0 + tid];
   __syncthreads();
 
-  // this thread's two runs of four features, and its pairs' first index
+  // this thread's two runs of four features, and whether they turn
   const int lane = tid % kLanes;
   const bool turns = lane < a.rotary_dim / 8;
   const bool split = turns && !a.interleaved;
@@ -116,71 +128,100 @@ __global__ void append_kernel(AppendArgs g) {
   const int o1 = split ? half + 4 * lane : 8 * lane + 4;
   const int rows = HQ + 2 * H;                       // head rows per token: q, k, v
   const int groups = blockDim.x / kLanes;
-  const int total = nt * rows;
-  int item = tid / kLanes;
-  for (int base = (tid & ~31) / kLanes; base < total; base += groups, item += groups) {
-    const bool live = item < total;
-    const int tok = live ? item / rows : 0;
-    const int r = live ? item - tok * rows : 0;
-    const long long token = first + t0 + tok;
-    const bool is_q = r < HQ, is_v = r >= HQ + H;
+  // a warp's groups take neighbouring head rows; a row that does not exist takes part in the
+  // warp's shuffles, with zeros
+  for (int base = part * groups + (tid & ~31) / kLanes; base < rows; base += g.parts * groups) {
+    const int r = base + tid % 32 / kLanes;
+    const bool live = r < rows, is_q = r < HQ, is_v = r >= HQ + H;
     const int h = is_q ? r : is_v ? r - HQ - H : r - HQ;
-    const T* src = is_q ? static_cast<const T*>(a.q) + token * a.q_stride
-                 : is_v ? static_cast<const T*>(a.v) + token * a.v_stride
-                        : static_cast<const T*>(a.k) + token * a.k_stride;
-    src += (long long)h * D;
-    float x[8] = {};
-    if (live) {
-      load4(src + o0, x);
-      load4(src + o1, x + 4);
+    const long long token = first + t0;
+    const long long stride = is_q ? a.q_stride : is_v ? a.v_stride : a.k_stride;
+    const T* src = static_cast<const T*>(is_q ? a.q : is_v ? a.v : a.k) + token * stride +
+                   (long long)h * D;
+    const T* weight = static_cast<const T*>(is_q ? a.q_norm : is_v ? nullptr : a.k_norm);
+    float w[8];
+    if (weight && live) {
+      Run4<T> x;
+      x.load(weight + o0);
+      x.get(w);
+      x.load(weight + o1);
+      x.get(w + 4);
     }
-    const void* weight = is_q ? a.q_norm : is_v ? nullptr : a.k_norm;
-    if (a.q_norm || a.k_norm) {                      // the shuffles take the whole warp
-      float ss = 0.f;
+    const int len = live && !is_q ? s_len[h] : 0;
+    // q: rows of tokens are rows * D apart; k, v: one row after the other within a page
+    T* dst = is_q ? static_cast<T*>(a.q_out) + (token * HQ + h) * D
+                  : static_cast<T*>(is_v ? c.v : c.k);
+    for (int t = 0; t < nt; t += kAhead) {
+      Run4<T> x0[kAhead], x1[kAhead];
+      if (live) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+        for (int i = 0; i < kAhead; ++i)
+          if (t + i < nt) {
+            x0[i].load(src + (t + i) * stride + o0);
+            x1[i].load(src + (t + i) * stride + o1);
+          }
+      }
 #pragma unroll
-      for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      if (weight) {
-        const float f = 1.0f / sqrtf(ss * (1.0f / D) + a.eps);
-        float w[8];
-        load4(static_cast<const T*>(weight) + o0, w);
-        load4(static_cast<const T*>(weight) + o1, w + 4);
+      for (int i = 0; i < kAhead; ++i) {
+        if (t + i >= nt) break;
+        float x[8];
+        x0[i].get(x);
+        x1[i].get(x + 4);
+        if (a.q_norm || a.k_norm) {                  // the shuffles take the whole warp
+          float ss = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = x[i] * f * w[i];
+          for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
+#pragma unroll
+          for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+          if (weight) {
+            const float f = 1.0f / sqrtf(ss * (1.0f / D) + a.eps);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = x[j] * f * w[j];
+          }
+        }
+        if (!live) continue;
+        if (turns && !is_v) {
+          const float4* cs = reinterpret_cast<const float4*>(s_rot[t + i] + 4 * lane);
+          const float4 r0 = cs[0], r1 = cs[1];
+          const float co[4] = {r0.x, r0.z, r1.x, r1.z}, si[4] = {r0.y, r0.w, r1.y, r1.w};
+          float y[8];
+          if (a.interleaved) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              y[2 * j] = x[2 * j] * co[j] - x[2 * j + 1] * si[j];
+              y[2 * j + 1] = x[2 * j + 1] * co[j] + x[2 * j] * si[j];
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              y[j] = x[j] * co[j] - x[j + 4] * si[j];
+              y[j + 4] = x[j + 4] * co[j] + x[j] * si[j];
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j) x[j] = y[j];
+        }
+        T* to = dst;
+        if (is_q) {
+          to += (long long)(t + i) * HQ * D;
+        } else {
+          if (len < 0) continue;
+          const long long row = row_of(c, g.t.layer, s, h, len + t0 + t + i);
+          if (row < 0) {
+            atomicOr(g.dev_status, NX_DEV_BAD_PAGE);
+            continue;
+          }
+          to += row * D;
+          if (!is_v && lane == 0) c.pos[row] = s_pos[t + i];
+        }
+        store4(to + o0, x);
+        store4(to + o1, x + 4);
       }
     }
-    if (!live) continue;
-    if (turns && !is_v) {
-      const float2* cs = s_rot[tok] + 4 * lane;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float& u = a.interleaved ? x[2 * i] : x[i];
-        float& v = a.interleaved ? x[2 * i + 1] : x[i + 4];
-        const float u0 = u, v0 = v;
-        u = u0 * cs[i].x - v0 * cs[i].y;
-        v = v0 * cs[i].x + u0 * cs[i].y;
-      }
-    }
-    T* dst;
-    if (is_q) {
-      dst = static_cast<T*>(a.q_out) + (token * HQ + h) * D;
-    } else {
-      if (s_len[h] < 0) continue;
-      const long long row = row_of(c, g.t.layer, s, h, s_len[h] + t0 + tok);
-      if (row < 0) {
-        atomicOr(g.dev_status, NX_DEV_BAD_PAGE);
-        continue;
-      }
-      dst = static_cast<T*>(is_v ? c.v : c.k) + row * D;
-      if (!is_v && lane == 0) c.pos[row] = a.pos[token];
-    }
-    store4(dst + o0, x);
-    store4(dst + o1, x + 4);
   }
   // s_len was read before the barrier above: with one block per sequence, or lengths that
   // come from elsewhere, nobody still reads what is set here
-  if (g.set_lens && tile == 0)
+  if (g.set_lens && lead)
     for (int h = tid; h < H; h += blockDim.x)
       if (s_len[h] >= 0) g.lens[(long long)s * H + h] = s_len[h] + n;
 }
@@ -204,15 +245,21 @@ bool aligned(const void* p, long long stride, int size) {
 template <typename T, int D>
 cudaError_t launch_append(AppendArgs& g, cudaStream_t st, int* launches) {
   const int rows = (g.a.q ? g.c.kv_heads * g.c.group : 0) + 2 * g.c.kv_heads;
+  constexpr int kLanes = D / 8;
   g.tiles = (int)(((long long)g.t.max_tokens + kTokens - 1) / kTokens);
   const bool in_place = !g.a.lens_in || g.a.lens_in == g.lens;
-  g.set_lens = !in_place || g.tiles == 1;
   int threads = kAppendThreads;
-  if (g.tiles == 1) {                 // a thread group per head row, as far as they go
-    const long long want = (long long)rows * g.t.max_tokens * (D / 8);
+  if (g.tiles == 1) {
+    // few tokens: one block per sequence, with a thread group per head row as far as they go,
+    // reads the lengths before it sets them, so that one launch does
+    g.parts = 1;
+    const long long want = (long long)rows * kLanes;
     threads = want > 1024 ? 1024 : (int)((want + 31) / 32 * 32);
+  } else {
+    g.parts = (rows * kLanes + threads - 1) / threads;
   }
-  const long long blocks = (long long)g.c.seqs * g.tiles;
+  g.set_lens = !in_place || g.tiles == 1;
+  const long long blocks = (long long)g.c.seqs * g.tiles * g.parts;
   if (blocks > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
   cudaError_t e = launch_after(append_kernel<T, D>, dim3((unsigned)blocks), dim3(threads),
                                (size_t)g.c.kv_heads * 4, st, g);

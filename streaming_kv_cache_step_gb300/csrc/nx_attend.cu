@@ -8,13 +8,12 @@
 // A slice with one new token has group = 4..8 query rows per 512 B of K and V (256 B from the
 // image): some 4 flop a byte, far below what the tensor cores need to matter, so the kernel
 // is a stream of K and V from HBM. What it does per byte is kept small instead:
-//   - every warp works alone on 16 slots at a time: its lanes load K and V straight into the
-//     registers of mma fragments (16-byte loads, whole 64- or 128-byte lines). The order of
-//     features inside a dot product is free, so that a lane's 16 bytes of a K row are its
-//     operands of two (bf16) or four (e4m3) k-steps, with the query rows loaded in the same
-//     order; V's operands pair two slots of one feature, which takes one byte permute each.
-//     No shared memory, no barrier, nothing between a load and the mma that waits for it;
-//   - the next 16 slots' K is in flight during softmax and PV, their V during QK;
+//   - every warp works alone on 16 slots at a time: K and V reach a ring of its own in shared
+//     memory by asynchronous 16-byte copies, some steps ahead, and go from there into mma
+//     fragments by 16-byte loads. The order of features inside a dot product is free, so that
+//     16 bytes of a K row are a lane's operands of two (bf16) or four (e4m3) k-steps, with the
+//     query rows loaded in the same order; V's operands pair two slots of one feature, which
+//     takes one byte permute each. No barrier but the warp's own;
 //   - an mma has 16 rows, a decode step 8 or fewer: the spare eight carry the probabilities'
 //     rounding errors (p = hi + lo), so that bf16 probabilities cost no accuracy.
 // The slots of all slices, 64 to a tile, are dealt out evenly to as many thread blocks as fit
@@ -22,12 +21,20 @@
 // attend_join_kernel.
 #include <cuda_fp8.h>
 
+#include <atomic>
+
 #include "nx_attend.cuh"
 
 namespace nx {
 namespace {
 
 constexpr int kWarps = 4;
+// A warp's ring, for rows of so many bytes (of KIND; an image's tail takes the image's ring):
+// stages of one step each. Two thread blocks, eight warps, share an SM's 227 KB.
+template <int ROW>
+constexpr int kStageBytes = ROW == 512 ? 8192 : ROW * 32;
+template <int ROW>
+constexpr int kStages = ROW >= 256 ? 3 : ROW == 128 ? 5 : 8;
 constexpr int kTileSlots = 64;         // slots of one tile of a thread block
 // kTail: bf16 rows behind an image, with their output features in the image's order
 enum Kind { kBf16 = 0, kImage = 1, kF32 = 2, kTail = 3 };
@@ -98,27 +105,33 @@ __device__ __forceinline__ uint32_t tf32_lo(uint32_t x) {
 // How K and V of KIND reach the fragments. g = lane / 4 and c = lane % 4 as in an mma.
 template <int KIND, int D>
 struct Shape {
-  static constexpr int kSlots = KIND == kF32 ? 8 : 16;           // slots of a warp's step
+  static constexpr int kSlots = KIND == kF32 || KIND == kTail ? 8 : 16;  // slots of a step
   static constexpr int NT = kSlots / 8;                          // mma column tiles of them
   static constexpr int kBytes = KIND == kF32 ? 4 : kIsBf16<KIND> ? 2 : 1;
-  static constexpr int KV = D * kBytes / 64;                     // 16-byte loads of a K row
-  static constexpr int VV = D * kBytes >= 128 ? D * kBytes / 128 : 1;   // loads of a V row
+  static constexpr int kRow = D * kBytes;                        // bytes of a row
+  static constexpr int kChunks = kRow / 16;                      // 16-byte chunks of a row
+  static constexpr int kStage = 2 * kSlots * kRow;               // one step's K and V
+  static constexpr int KV = kRow / 64;                           // 16-byte loads of a K row
+  static constexpr int VV = kRow >= 128 ? kRow / 128 : 1;        // loads of a V row
   static constexpr int kPer = D / 8 / VV;                        // features of one V load
-  // V load w of lane g covers features w kWide + g kStep .. + kPer - 1: whole lines for a
-  // load, but behind an image what the image's lane g has (D / 8 features in a row)
+  // V load w of lane g covers features w kWide + g kStep .. + kPer - 1: neighbouring lanes
+  // neighbouring chunks, but behind an image what the image's lane g has (D / 8 in a row)
   static constexpr int kStep = KIND == kTail ? D / 8 : kPer;
   static constexpr int kWide = KIND == kTail ? kPer : 8 * kPer;
   // the feature that column n of output tile t stands for
   static __device__ __forceinline__ int feature(int t, int n) {
     return t / kPer * kWide + n * kStep + t % kPer;
   }
-};
-
-template <int KIND, int D>
-struct Rows {
-  using S = Shape<KIND, D>;
-  uint4 k[S::NT][S::KV];
-  uint4 v[S::NT][2][S::VV];            // image with D = 64: .x and .y only
+  // Where chunk i of row r lies in a stage: rows are multiples of 128 bytes (64 for an image
+  // with D = 64), so that the rows one load instruction touches would share their banks. K is
+  // read as chunks c .. of rows g (two rows to a 128-byte wavefront), V as chunks g of rows
+  // 2c (four rows to one).
+  static __device__ __forceinline__ int k_at(int r, int i) {
+    return r * kRow + 16 * (kChunks >= 8 ? i ^ 4 * (r & 1) : i);
+  }
+  static __device__ __forceinline__ int v_at(int r, int i) {
+    return r * kRow + 16 * (kChunks >= 8 ? i ^ 2 * (r >> 1 & 3) : i ^ (r >> 1 & 3));
+  }
 };
 
 // One warp's running state: o[t] holds rows g (c0, c1) and g + 8 (c2, c3) of output tile t.
@@ -172,47 +185,70 @@ struct Where {
   }
 };
 
-template <int KIND, int D>
-__device__ __forceinline__ void load_k(const AttendArgs& g, const long long* row, int left,
-                                       int lane, Rows<KIND, D>& x) {
-  using S = Shape<KIND, D>;
-  const char* base = static_cast<const char*>(KIND == kImage ? g.im.k : g.c.k);
-#pragma unroll
-  for (int j = 0; j < S::NT; ++j) {
-    const bool ok = row[j] >= 0 && 8 * j + lane / 4 < left;
-    const char* p = base + (row[j] + lane / 4) * (D * S::kBytes) + (lane % 4) * 16;
-#pragma unroll
-    for (int u = 0; u < S::KV; ++u)
-      x.k[j][u] = ok ? __ldcs(reinterpret_cast<const uint4*>(p + u * 64))
-                     : make_uint4(0, 0, 0, 0);
-  }
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool ok) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(ok ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool ok) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src),
+               "r"(ok ? 4 : 0)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t smem_at(const void* p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+__device__ __forceinline__ uint4 lds16(uint32_t at) {
+  uint4 x;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+               : "r"(at)
+               : "memory");
+  return x;
 }
 
+// What a step needs to know besides its rows.
+struct Meta {
+  float ks[2], vs[2];   // image: the scales of its 8-slot halves
+  int bad[2];           // 1: a bad page
+};
+
+// Starts the copies of a step's rows (those that exist; zeros take the place of others).
 template <int KIND, int D>
-__device__ __forceinline__ void load_v(const AttendArgs& g, const long long* row, int left,
-                                       int lane, Rows<KIND, D>& x) {
+__device__ __forceinline__ void copy_rows(const AttendArgs& g, const long long* row, int left,
+                                          int lane, uint32_t stage) {
   using S = Shape<KIND, D>;
-  const char* base = static_cast<const char*>(KIND == kImage ? g.im.v : g.c.v);
+  constexpr int kLine = 32 / S::kChunks > 0 ? 32 / S::kChunks : 1;   // rows per instruction
+  static_assert(S::kChunks <= 32 && 8 % kLine == 0, "");
+  const char* kb = static_cast<const char*>(KIND == kImage ? g.im.k : g.c.k);
+  const char* vb = static_cast<const char*>(KIND == kImage ? g.im.v : g.c.v);
+  const int sub = lane / S::kChunks, chunk = lane % S::kChunks;
+  bool full = left >= S::kSlots;
 #pragma unroll
-  for (int j = 0; j < S::NT; ++j)
+  for (int j = 0; j < S::NT; ++j) full = full && row[j] >= 0;
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int slot = 2 * (lane % 4) + e;
-      const bool ok = row[j] >= 0 && 8 * j + slot < left;
-      const char* p = base + (row[j] + slot) * (D * S::kBytes);
-      if constexpr (D * S::kBytes < 128) {
-        const uint2 r = ok ? __ldcs(reinterpret_cast<const uint2*>(p + lane / 4 * 8))
-                           : make_uint2(0, 0);
-        x.v[j][e][0].x = r.x;
-        x.v[j][e][0].y = r.y;
-      } else {
+  for (int j = 0; j < S::NT; ++j) {
+    const long long at = (row[j] < 0 ? 0 : row[j]) * S::kRow + lane * 16;
+    const char *k = kb + at, *v = vb + at;
+    if (full) {
 #pragma unroll
-        for (int w = 0; w < S::VV; ++w)
-          x.v[j][e][w] = ok ? __ldcs(reinterpret_cast<const uint4*>(
-                                  p + (w * S::kWide + lane / 4 * S::kStep) * S::kBytes))
-                            : make_uint4(0, 0, 0, 0);
+      for (int i = 0; i < 8; i += kLine) {
+        copy16(stage + S::k_at(8 * j + i + sub, chunk), k + i * S::kRow);
+        copy16(stage + S::kStage / 2 + S::v_at(8 * j + i + sub, chunk), v + i * S::kRow);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; i += kLine) {
+        const bool ok = row[j] >= 0 && 8 * j + i + sub < left;
+        copy16(stage + S::k_at(8 * j + i + sub, chunk), ok ? k + i * S::kRow : kb, ok);
+        copy16(stage + S::kStage / 2 + S::v_at(8 * j + i + sub, chunk),
+               ok ? v + i * S::kRow : vb, ok);
       }
     }
+  }
 }
 
 __device__ __forceinline__ uint32_t word(const uint4& x, int i) {
@@ -304,7 +340,7 @@ struct Query {
 
 // The products of the query rows with 8 or 16 rows of K.
 template <int KIND, int D, int ROWS>
-__device__ __forceinline__ void qk(const Query<KIND, D, ROWS>& q, const Rows<KIND, D>& x,
+__device__ __forceinline__ void qk(const Query<KIND, D, ROWS>& q, uint32_t stage, int lane,
                                    float s[][4]) {
   using S = Shape<KIND, D>;
 #pragma unroll
@@ -312,13 +348,14 @@ __device__ __forceinline__ void qk(const Query<KIND, D, ROWS>& q, const Rows<KIN
     s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
 #pragma unroll
     for (int u = 0; u < S::KV; ++u) {
+      const uint4 k = lds16(stage + S::k_at(8 * j + lane / 4, 4 * u + lane % 4));
       if constexpr (kIsBf16<KIND>) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const uint32_t* a = q.a[2 * u + i];
           const uint32_t f[4] = {a[0], ROWS == 16 ? a[2 % (2 * (ROWS / 8))] : 0u, a[1],
                                  ROWS == 16 ? a[3 % (2 * (ROWS / 8))] : 0u};
-          mma16<KIND>(s[j], f, word(x.k[j][u], 2 * i), word(x.k[j][u], 2 * i + 1));
+          mma16<KIND>(s[j], f, word(k, 2 * i), word(k, 2 * i + 1));
         }
       } else if constexpr (KIND == kImage) {
 #pragma unroll
@@ -326,7 +363,7 @@ __device__ __forceinline__ void qk(const Query<KIND, D, ROWS>& q, const Rows<KIN
           const uint32_t* a = q.a[4 * u + i];
           const uint32_t f[4] = {a[0], ROWS == 16 ? a[2 % (2 * (ROWS / 8))] : 0u, a[1],
                                  ROWS == 16 ? a[3 % (2 * (ROWS / 8))] : 0u};
-          const uint32_t w = word(x.k[j][u], i);
+          const uint32_t w = word(k, i);
           mma16<KIND>(s[j], f, e4m3_pair(w & 0xFFFFu), e4m3_pair(w >> 16));
         }
       } else {
@@ -335,7 +372,7 @@ __device__ __forceinline__ void qk(const Query<KIND, D, ROWS>& q, const Rows<KIN
         for (int i = 0; i < 2; ++i) {
           const uint32_t* a = q.a[2 * u + i];
           const uint32_t f[4] = {tf32_hi(a[0]), tf32_lo(a[0]), tf32_hi(a[1]), tf32_lo(a[1])};
-          const uint32_t b0 = word(x.k[j][u], 2 * i), b1 = word(x.k[j][u], 2 * i + 1);
+          const uint32_t b0 = word(k, 2 * i), b1 = word(k, 2 * i + 1);
           mma16<KIND>(s[j], f, tf32_hi(b0), tf32_hi(b1));
           mma16<KIND>(s[j], f, tf32_lo(b0), tf32_lo(b1));
         }
@@ -350,23 +387,36 @@ __device__ __forceinline__ void qk(const Query<KIND, D, ROWS>& q, const Rows<KIN
 
 // o += p V.
 template <int KIND, int D, int ROWS>
-__device__ __forceinline__ void pv(const Rows<KIND, D>& x, const float p[][4], State<D, ROWS>& st) {
+__device__ __forceinline__ void pv(uint32_t stage, int lane, const float p[][4],
+                                   State<D, ROWS>& st) {
   using S = Shape<KIND, D>;
+  // V load w of slot 8 j + 2 c + e
+  const auto load = [&](int j, int e, int w) {
+    const int f = (w * S::kWide + lane / 4 * S::kStep) * S::kBytes;    // byte in the row
+    const uint32_t at = stage + S::kStage / 2 + S::v_at(8 * j + 2 * (lane % 4) + e, f / 16);
+    if constexpr (S::kRow >= 128) return lds16(at);
+    uint4 x = make_uint4(0, 0, 0, 0);
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(x.x), "=r"(x.y) : "r"(at + f % 16)
+                 : "memory");
+    return x;
+  };
   if constexpr (KIND == kF32) {
     const uint32_t p0 = __float_as_uint(p[0][0]), p1 = __float_as_uint(p[0][1]);
     const uint32_t f[4] = {tf32_hi(p0), tf32_lo(p0), tf32_hi(p1), tf32_lo(p1)};
 #pragma unroll
-    for (int w = 0; w < S::VV; ++w)
+    for (int w = 0; w < S::VV; ++w) {
+      const uint4 v0 = load(0, 0, w), v1 = load(0, 1, w);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const uint32_t b0 = word(x.v[0][0][w], e), b1 = word(x.v[0][1][w], e);
+        const uint32_t b0 = word(v0, e), b1 = word(v1, e);
         mma16<KIND>(st.o[4 * w + e], f, tf32_hi(b0), tf32_hi(b1));
         mma16<KIND>(st.o[4 * w + e], f, tf32_lo(b0), tf32_lo(b1));
       }
+    }
   } else {
-    uint32_t hi[4], lo[4];
+    uint32_t hi[4] = {0, 0, 0, 0}, lo[4] = {0, 0, 0, 0};
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
+    for (int j = 0; j < S::NT; ++j) {
       hi[2 * j] = pack2<KIND>(p[j][0], p[j][1]);
       lo[2 * j] = rest2<KIND>(p[j][0], p[j][1], hi[2 * j]);
       if constexpr (ROWS == 8) {
@@ -377,13 +427,19 @@ __device__ __forceinline__ void pv(const Rows<KIND, D>& x, const float p[][4], S
       }
     }
 #pragma unroll
-    for (int w = 0; w < S::VV; ++w)
+    for (int w = 0; w < S::VV; ++w) {
+      uint4 v[S::NT][2];
+#pragma unroll
+      for (int j = 0; j < S::NT; ++j) {
+        v[j][0] = load(j, 0, w);
+        v[j][1] = load(j, 1, w);
+      }
 #pragma unroll
       for (int i = 0; i < (KIND == kImage && D == 64 ? 2 : 4); ++i) {
-        uint32_t b[2][kIsBf16<KIND> ? 2 : 4];
+        uint32_t b[2][kIsBf16<KIND> ? 2 : 4] = {};
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const uint32_t y0 = word(x.v[j][0][w], i), y1 = word(x.v[j][1][w], i);
+        for (int j = 0; j < S::NT; ++j) {
+          const uint32_t y0 = word(v[j][0], i), y1 = word(v[j][1], i);
           if constexpr (kIsBf16<KIND>) {
             b[j][0] = __byte_perm(y0, y1, 0x5410);
             b[j][1] = __byte_perm(y0, y1, 0x7632);
@@ -403,13 +459,15 @@ __device__ __forceinline__ void pv(const Rows<KIND, D>& x, const float p[][4], S
           if constexpr (ROWS == 16 && kIsBf16<KIND>) mma16<KIND>(o, lo, b[0][e], b[1][e]);
         }
       }
+    }
   }
 }
 
 // Slots [base + kSlots * i, ...) for i = from, from + kWarps, ... < to, up to slot `end`.
 template <int KIND, int D, int ROWS>
 __device__ __forceinline__ void attend_part(const AttendArgs& g, const AttendUnit& u, int base,
-                                            int end, int from, int to, State<D, ROWS>& st) {
+                                            int end, int from, int to, uint32_t ring, Meta* meta,
+                                            State<D, ROWS>& st) {
   using S = Shape<KIND, D>;
   if (from >= to) return;
   const int lane = threadIdx.x % 32;
@@ -423,40 +481,59 @@ __device__ __forceinline__ void attend_part(const AttendArgs& g, const AttendUni
   }
   const int low = min(end, u.low);
   float vref = 1.1754944e-38f;          // image: the largest value scale so far; o is in it
-  Rows<KIND, D> x;
   const Where at(g, u);
   const long long blocks0 =
       KIND == kImage && !g.c.page_size ? image_scale_at(g.c, g.t.layer, u.s, u.h, 0, g.b) : 0;
-  long long row[S::NT], next[S::NT];
-  int page[S::NT];
-  float ks[S::NT], vs[S::NT], ks_next[S::NT], vs_next[S::NT];
   constexpr int kNext = S::kSlots * kWarps;
-  const auto scales = [&](int t, const long long* r, float* k, float* v) {
+  constexpr int kDeep = kStages<D * (KIND == kF32 ? 4 : KIND == kBf16 ? 2 : 1)>;
+  static_assert(S::kStage <= kStageBytes<D * (KIND == kF32 ? 4 : KIND == kBf16 ? 2 : 1)>, "");
+  int page[S::NT];
+  // starts step i's copies into stage i / kWarps % kDeep; `page` holds its table entries and
+  // then the next step's
+  const auto start = [&](int i, int n) {
+    const int t = base + S::kSlots * i;
+    if (i < to) {
+      long long row[S::NT];
+      at.rows_of<S::NT>(t, end, page, row);
+      at.pages_of<S::NT>(t + kNext, end, page);
+      copy_rows<KIND, D>(g, row, end - t, lane, ring + n * S::kStage);
+#pragma unroll
+      for (int j = 0; j < S::NT; ++j) {
+        if (lane == 0) meta[n].bad[j] = row[j] == -1;
+        if constexpr (KIND == kImage) {
+          const long long x = g.c.page_size ? row[j] / g.b : blocks0 + (t + 8 * j) / g.b;
+          const bool ok = row[j] >= 0;
+          if (lane == 0) copy4(smem_at(&meta[n].ks[j]), g.im.k_scale + (ok ? x : 0), ok);
+          if (lane == 1) copy4(smem_at(&meta[n].vs[j]), g.im.v_scale + (ok ? x : 0), ok);
+        }
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  at.pages_of<S::NT>(base + S::kSlots * from, end, page);
+  __syncwarp();                         // the warp is done with what the ring held before
+#pragma unroll
+  for (int n = 0; n < kDeep - 1; ++n) start(from + n * kWarps, n);
+  int n = 0;
+  for (int i = from; i < to; i += kWarps) {
+    const int t = base + S::kSlots * i;
+    asm volatile("cp.async.wait_group %0;" ::"n"(kDeep - 2) : "memory");
+    __syncwarp();                       // everyone's copies are in, and step i - 1 is read
+    start(i + (kDeep - 1) * kWarps, n == 0 ? kDeep - 1 : n - 1);
+    const uint32_t stage = ring + n * S::kStage;
+    float ks[S::NT], vs[S::NT];
+    bool bad_half[S::NT];
 #pragma unroll
     for (int j = 0; j < S::NT; ++j) {
-      const long long i = g.c.page_size ? r[j] / g.b : blocks0 + (t + 8 * j) / g.b;
-      k[j] = r[j] < 0 ? 0.f : g.im.k_scale[i];
-      v[j] = r[j] < 0 ? 0.f : g.im.v_scale[i];
+      bad_half[j] = meta[n].bad[j] != 0;
+      if constexpr (KIND == kImage) {
+        ks[j] = meta[n].ks[j];
+        vs[j] = meta[n].vs[j];
+      }
     }
-  };
-  {
-    const int t = base + S::kSlots * from;
-    at.pages_of<S::NT>(t, end, page);
-    at.rows_of<S::NT>(t, end, page, row);
-    load_k(g, row, end - t, lane, x);
-    if constexpr (KIND == kImage) scales(t, row, ks, vs);
-    load_v(g, row, end - t, lane, x);
-    at.pages_of<S::NT>(t + kNext, end, page);
-  }
-  for (int i = from; i < to; i += kWarps) {
-    const int t = base + S::kSlots * i, tn = t + kNext;
-    const int endn = i + kWarps < to ? end : 0;
-    at.rows_of<S::NT>(tn, endn, page, next);
-    at.pages_of<S::NT>(tn + kNext, end, page);
-    if constexpr (KIND == kImage) scales(tn, next, ks_next, vs_next);
+    n = n == kDeep - 1 ? 0 : n + 1;
     float s[S::NT][4];
-    qk<KIND, D, ROWS>(q, x, s);
-    load_k(g, next, end - tn, lane, x);
+    qk<KIND, D, ROWS>(q, stage, lane, s);
 
     // logits in log2 units; beyond a row's limit or on a bad page: -inf
     float top[ROWS / 8];
@@ -464,7 +541,7 @@ __device__ __forceinline__ void attend_part(const AttendArgs& g, const AttendUni
     for (int e = 0; e < ROWS / 8; ++e) top[e] = -INFINITY;
     bool bad = false;
 #pragma unroll
-    for (int j = 0; j < S::NT; ++j) bad |= row[j] < 0;
+    for (int j = 0; j < S::NT; ++j) bad |= bad_half[j];
     const bool mask = bad || t + S::kSlots > low;
 #pragma unroll
     for (int j = 0; j < S::NT; ++j)
@@ -474,14 +551,10 @@ __device__ __forceinline__ void attend_part(const AttendArgs& g, const AttendUni
         for (int y = 0; y < 2; ++y) {
           float& z = s[j][2 * e + y];
           z *= KIND == kImage ? q.c1[e] * ks[j] : q.c1[e];
-          if (mask && (row[j] < 0 || t + 8 * j + 2 * (lane % 4) + y >= lim[e])) z = -INFINITY;
+          if (mask && (bad_half[j] || t + 8 * j + 2 * (lane % 4) + y >= lim[e])) z = -INFINITY;
           top[e] = fmaxf(top[e], z);
         }
-    if (bad) {
-#pragma unroll
-      for (int j = 0; j < S::NT; ++j)
-        if (row[j] == -1 && lane == 0) atomicOr(g.dev_status, NX_DEV_BAD_PAGE);
-    }
+    if (bad && lane == 0) atomicOr(g.dev_status, NX_DEV_BAD_PAGE);
     bool up = false;
 #pragma unroll
     for (int e = 0; e < ROWS / 8; ++e) {
@@ -533,16 +606,7 @@ __device__ __forceinline__ void attend_part(const AttendArgs& g, const AttendUni
           if constexpr (KIND == kImage) z *= vr[j];
         }
     }
-    pv<KIND, D, ROWS>(x, s, st);
-    load_v(g, next, end - tn, lane, x);
-#pragma unroll
-    for (int j = 0; j < S::NT; ++j) {
-      row[j] = next[j];
-      if constexpr (KIND == kImage) {
-        ks[j] = ks_next[j];
-        vs[j] = vs_next[j];
-      }
-    }
+    pv<KIND, D, ROWS>(stage, lane, s, st);
   }
   if constexpr (KIND == kImage) {
 #pragma unroll
@@ -583,12 +647,18 @@ __device__ __forceinline__ void finish_row(const AttendArgs& g, const AttendUnit
 
 template <int KIND, int D, int ROWS>
 __global__ void __launch_bounds__(kWarps * 32, 2) attend_kernel(AttendArgs g) {
-  __shared__ float s_o[kWarps][ROWS][D];
+  constexpr int kRowBytes = Shape<KIND, D>::kRow, kRing = kStages<kRowBytes> * kStageBytes<kRowBytes>;
+  // the rings, and over them, once a piece's steps are done, its warps' outputs
+  extern __shared__ __align__(128) char s_ring[];
+  float (*s_o)[ROWS][D] = reinterpret_cast<float (*)[ROWS][D]>(s_ring);
+  static_assert(kRing >= ROWS * D * 4, "");
+  __shared__ Meta s_meta[kWarps][kStages<kRowBytes>];
   __shared__ float s_m[kWarps][ROWS], s_l[kWarps][ROWS];
   __shared__ int s_sum[kWarps], s_at[3];
   grid_dep_wait();
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const int b = blockIdx.x;
+  const uint32_t ring = smem_at(s_ring) + warp * kRing;
 
   // where this block's share of all tiles starts: every thread adds up a run of units
   const int run = (g.units + kWarps * 32 - 1) / (kWarps * 32);
@@ -651,14 +721,18 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attend_kernel(AttendArgs g) {
       if constexpr (KIND == kImage) {
         constexpr int k = kTileSlots / Shape<kImage, D>::kSlots;
         attend_part<kImage, D, ROWS>(g, u, 0, ea, a0 * k + warp,
-                                     min(min(a1, ta) * k, (ea + 15) / 16), st);
-        attend_part<kTail, D, ROWS>(g, u, ea, u.end, max(a0 - ta, 0) * k + warp,
-                                    min((a1 - ta) * k, (u.end - ea + 15) / 16), st);
+                                     min(min(a1, ta) * k, (ea + 15) / 16), ring, s_meta[warp], st);
+        constexpr int kt = kTileSlots / Shape<kTail, D>::kSlots;
+        attend_part<kTail, D, ROWS>(g, u, ea, u.end, max(a0 - ta, 0) * kt + warp,
+                                    min((a1 - ta) * kt, (u.end - ea + 7) / 8), ring, s_meta[warp],
+                                    st);
       } else {
         constexpr int k = kTileSlots / Shape<KIND, D>::kSlots, w = Shape<KIND, D>::kSlots;
         attend_part<KIND, D, ROWS>(g, u, 0, u.end, a0 * k + warp, min(a1 * k, (u.end + w - 1) / w),
-                                   st);
+                                   ring, s_meta[warp], st);
       }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      __syncthreads();
       // the warps' states meet in shared memory; rows g and g + 8 of an 8-row tile are the
       // two terms of the same row
 #pragma unroll
@@ -779,6 +853,19 @@ size_t attend_layout(int D, char* base, AttendWs* ws) {
   return at + (size_t)2 * kAttendGrid * kPieceRows * D * sizeof(float);
 }
 
+// Lets a kernel use so much dynamic shared memory, once per device (twice does no harm).
+template <void (*kernel)(AttendArgs)>
+cudaError_t allow_smem(int bytes) {
+  static std::atomic<bool> done[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 0 && dev < 64 && done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev].store(true, std::memory_order_release);
+  return e;
+}
+
 template <int KIND, int D, int ROWS>
 cudaError_t launch_attend(AttendArgs& g, cudaStream_t st, int* launches) {
   g.mtiles = (int)(((long long)g.t.max_tokens * g.c.group + ROWS - 1) / ROWS);
@@ -789,8 +876,11 @@ cudaError_t launch_attend(AttendArgs& g, cudaStream_t st, int* launches) {
   g.min_tiles = 1;
   const long long fit = 152 * 2;
   const int grid = (int)(most < fit ? most : fit);
-  cudaError_t e = launch_after(attend_kernel<KIND, D, ROWS>, dim3(grid), dim3(kWarps * 32), 0, st,
-                               g);
+  constexpr int kRow = Shape<KIND, D>::kRow;
+  constexpr int smem = kWarps * kStages<kRow> * kStageBytes<kRow>;
+  cudaError_t e = allow_smem<attend_kernel<KIND, D, ROWS>>(smem);
+  if (e != cudaSuccess) return e;
+  e = launch_after(attend_kernel<KIND, D, ROWS>, dim3(grid), dim3(kWarps * 32), smem, st, g);
   if (e != cudaSuccess) return e;
   note_launch(st, launches, "attend");
   e = launch_after(attend_join_kernel<D, ROWS>, dim3(grid), dim3(kJoinWarps * 32), 0, st, g);
