@@ -29,13 +29,6 @@ namespace nx {
 namespace {
 
 constexpr int kWarps = 4;
-// A warp's ring, for rows of so many bytes (of KIND; an image's tail takes the image's ring):
-// stages of one step each. Two thread blocks, eight warps, share an SM's 227 KB.
-template <int ROW>
-constexpr int kStageBytes = ROW == 512 ? 8192 : ROW * 32;
-template <int ROW>
-constexpr int kStages = ROW >= 256 ? 3 : ROW == 128 ? 5 : 8;
-constexpr int kTileSlots = 64;         // slots of one tile of a thread block
 // kTail: bf16 rows behind an image, with their output features in the image's order
 enum Kind { kBf16 = 0, kImage = 1, kF32 = 2, kTail = 3 };
 template <int KIND>
@@ -71,9 +64,12 @@ __device__ __forceinline__ void mma16(float* d, const uint32_t* a, uint32_t b0, 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ uint32_t e4m3_pair(uint32_t two) {
-  const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
-  return (uint32_t)r.x | (uint32_t)r.y << 16;
+// Four e4m3 codes as two pairs of fp16.
+__device__ __forceinline__ void e4m3_pairs(uint32_t four, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(four));
 }
 
 template <int KIND>
@@ -105,7 +101,8 @@ __device__ __forceinline__ uint32_t tf32_lo(uint32_t x) {
 // How K and V of KIND reach the fragments. g = lane / 4 and c = lane % 4 as in an mma.
 template <int KIND, int D>
 struct Shape {
-  static constexpr int kSlots = KIND == kF32 || KIND == kTail ? 8 : 16;  // slots of a step
+  static constexpr int kSlots = KIND == kImage ? 32 : KIND == kBf16 ? 16 : 8;  // of a step
+  static constexpr int kTile = KIND == kImage ? 128 : 64;        // slots of a block's tile
   static constexpr int NT = kSlots / 8;                          // mma column tiles of them
   static constexpr int kBytes = KIND == kF32 ? 4 : kIsBf16<KIND> ? 2 : 1;
   static constexpr int kRow = D * kBytes;                        // bytes of a row
@@ -132,6 +129,16 @@ struct Shape {
   static __device__ __forceinline__ int v_at(int r, int i) {
     return r * kRow + 16 * (kChunks >= 8 ? i ^ 2 * (r >> 1 & 3) : i ^ (r >> 1 & 3));
   }
+};
+
+// A warp's ring: stages of one step each. kPerSm thread blocks of four warps share an SM's
+// 227 KB; an image's tail takes the image's ring.
+template <int KIND, int D, int ROWS>
+struct Ring {
+  static constexpr int kPerSm = KIND == kImage && ROWS == 8 ? 3 : 2;
+  static constexpr int kBytes = Shape<KIND, D>::kStage;
+  static constexpr int kFit = 196608 / (kPerSm * kWarps * kBytes);
+  static constexpr int kDeep = kFit > 8 ? 8 : kFit;
 };
 
 // One warp's running state: o[t] holds rows g (c0, c1) and g + 8 (c2, c3) of output tile t.
@@ -212,8 +219,8 @@ __device__ __forceinline__ uint4 lds16(uint32_t at) {
 
 // What a step needs to know besides its rows.
 struct Meta {
-  float ks[2], vs[2];   // image: the scales of its 8-slot halves
-  int bad[2];           // 1: a bad page
+  float ks[4], vs[4];   // image: the scales of its runs of 8 slots
+  int bad[4];           // 1: a bad page
 };
 
 // Starts the copies of a step's rows (those that exist; zeros take the place of others).
@@ -363,8 +370,9 @@ __device__ __forceinline__ void qk(const Query<KIND, D, ROWS>& q, uint32_t stage
           const uint32_t* a = q.a[4 * u + i];
           const uint32_t f[4] = {a[0], ROWS == 16 ? a[2 % (2 * (ROWS / 8))] : 0u, a[1],
                                  ROWS == 16 ? a[3 % (2 * (ROWS / 8))] : 0u};
-          const uint32_t w = word(k, i);
-          mma16<KIND>(s[j], f, e4m3_pair(w & 0xFFFFu), e4m3_pair(w >> 16));
+          uint32_t b0, b1;
+          e4m3_pairs(word(k, i), b0, b1);
+          mma16<KIND>(s[j], f, b0, b1);
         }
       } else {
         // rows g hold q's high part, rows g + 8 its low part: two products give all four terms
@@ -414,49 +422,52 @@ __device__ __forceinline__ void pv(uint32_t stage, int lane, const float p[][4],
       }
     }
   } else {
-    uint32_t hi[4] = {0, 0, 0, 0}, lo[4] = {0, 0, 0, 0};
 #pragma unroll
-    for (int j = 0; j < S::NT; ++j) {
-      hi[2 * j] = pack2<KIND>(p[j][0], p[j][1]);
-      lo[2 * j] = rest2<KIND>(p[j][0], p[j][1], hi[2 * j]);
-      if constexpr (ROWS == 8) {
-        hi[2 * j + 1] = lo[2 * j];
-      } else {
-        hi[2 * j + 1] = pack2<KIND>(p[j][2], p[j][3]);
-        lo[2 * j + 1] = rest2<KIND>(p[j][2], p[j][3], hi[2 * j + 1]);
-      }
-    }
+    for (int h = 0; h < (S::NT + 1) / 2; ++h) {      // 16 slots (or the only 8) at a time
+      constexpr int N = S::NT < 2 ? 1 : 2;
+      uint32_t hi[4] = {0, 0, 0, 0}, lo[4] = {0, 0, 0, 0};
 #pragma unroll
-    for (int w = 0; w < S::VV; ++w) {
-      uint4 v[S::NT][2];
-#pragma unroll
-      for (int j = 0; j < S::NT; ++j) {
-        v[j][0] = load(j, 0, w);
-        v[j][1] = load(j, 1, w);
+      for (int j = 0; j < N; ++j) {
+        const float* y = p[2 * h + j];
+        hi[2 * j] = pack2<KIND>(y[0], y[1]);
+        lo[2 * j] = rest2<KIND>(y[0], y[1], hi[2 * j]);
+        if constexpr (ROWS == 8) {
+          hi[2 * j + 1] = lo[2 * j];
+        } else {
+          hi[2 * j + 1] = pack2<KIND>(y[2], y[3]);
+          lo[2 * j + 1] = rest2<KIND>(y[2], y[3], hi[2 * j + 1]);
+        }
       }
 #pragma unroll
-      for (int i = 0; i < (KIND == kImage && D == 64 ? 2 : 4); ++i) {
-        uint32_t b[2][kIsBf16<KIND> ? 2 : 4] = {};
+      for (int w = 0; w < S::VV; ++w) {
+        uint4 v[N][2];
 #pragma unroll
-        for (int j = 0; j < S::NT; ++j) {
-          const uint32_t y0 = word(v[j][0], i), y1 = word(v[j][1], i);
-          if constexpr (kIsBf16<KIND>) {
-            b[j][0] = __byte_perm(y0, y1, 0x5410);
-            b[j][1] = __byte_perm(y0, y1, 0x7632);
-          } else {
-            const uint32_t z0 = __byte_perm(y0, y1, 0x5140), z1 = __byte_perm(y0, y1, 0x7362);
-            b[j][0] = e4m3_pair(z0 & 0xFFFFu);
-            b[j][1] = e4m3_pair(z0 >> 16);
-            b[j][2] = e4m3_pair(z1 & 0xFFFFu);
-            b[j][3] = e4m3_pair(z1 >> 16);
-          }
+        for (int j = 0; j < N; ++j) {
+          v[j][0] = load(2 * h + j, 0, w);
+          v[j][1] = load(2 * h + j, 1, w);
         }
 #pragma unroll
-        for (int e = 0; e < (kIsBf16<KIND> ? 2 : 4); ++e) {
-          float* o = st.o[S::kPer * w + (kIsBf16<KIND> ? 2 : 4) * i + e];
-          mma16<KIND>(o, hi, b[0][e], b[1][e]);
-          // sixteen rows leave no spare ones; fp16 probabilities (2^-11) do without
-          if constexpr (ROWS == 16 && kIsBf16<KIND>) mma16<KIND>(o, lo, b[0][e], b[1][e]);
+        for (int i = 0; i < (KIND == kImage && D == 64 ? 2 : 4); ++i) {
+          uint32_t b[2][kIsBf16<KIND> ? 2 : 4] = {};
+#pragma unroll
+          for (int j = 0; j < N; ++j) {
+            const uint32_t y0 = word(v[j][0], i), y1 = word(v[j][1], i);
+            if constexpr (kIsBf16<KIND>) {
+              b[j][0] = __byte_perm(y0, y1, 0x5410);
+              b[j][1] = __byte_perm(y0, y1, 0x7632);
+            } else {
+              const uint32_t z0 = __byte_perm(y0, y1, 0x5140), z1 = __byte_perm(y0, y1, 0x7362);
+              e4m3_pairs(z0, b[j][0], b[j][1]);
+              e4m3_pairs(z1, b[j][2], b[j][3]);
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < (kIsBf16<KIND> ? 2 : 4); ++e) {
+            float* o = st.o[S::kPer * w + (kIsBf16<KIND> ? 2 : 4) * i + e];
+            mma16<KIND>(o, hi, b[0][e], b[1][e]);
+            // sixteen rows leave no spare ones; fp16 probabilities (2^-11) do without
+            if constexpr (ROWS == 16 && kIsBf16<KIND>) mma16<KIND>(o, lo, b[0][e], b[1][e]);
+          }
         }
       }
     }
@@ -464,7 +475,7 @@ __device__ __forceinline__ void pv(uint32_t stage, int lane, const float p[][4],
 }
 
 // Slots [base + kSlots * i, ...) for i = from, from + kWarps, ... < to, up to slot `end`.
-template <int KIND, int D, int ROWS>
+template <int KIND, int D, int ROWS, int kDeep, int kStageBytes>
 __device__ __forceinline__ void attend_part(const AttendArgs& g, const AttendUnit& u, int base,
                                             int end, int from, int to, uint32_t ring, Meta* meta,
                                             State<D, ROWS>& st) {
@@ -485,8 +496,7 @@ __device__ __forceinline__ void attend_part(const AttendArgs& g, const AttendUni
   const long long blocks0 =
       KIND == kImage && !g.c.page_size ? image_scale_at(g.c, g.t.layer, u.s, u.h, 0, g.b) : 0;
   constexpr int kNext = S::kSlots * kWarps;
-  constexpr int kDeep = kStages<D * (KIND == kF32 ? 4 : KIND == kBf16 ? 2 : 1)>;
-  static_assert(S::kStage <= kStageBytes<D * (KIND == kF32 ? 4 : KIND == kBf16 ? 2 : 1)>, "");
+  static_assert(S::kStage <= kStageBytes, "");
   int page[S::NT];
   // starts step i's copies into stage i / kWarps % kDeep; `page` holds its table entries and
   // then the next step's
@@ -496,7 +506,7 @@ __device__ __forceinline__ void attend_part(const AttendArgs& g, const AttendUni
       long long row[S::NT];
       at.rows_of<S::NT>(t, end, page, row);
       at.pages_of<S::NT>(t + kNext, end, page);
-      copy_rows<KIND, D>(g, row, end - t, lane, ring + n * S::kStage);
+      copy_rows<KIND, D>(g, row, end - t, lane, ring + n * kStageBytes);
 #pragma unroll
       for (int j = 0; j < S::NT; ++j) {
         if (lane == 0) meta[n].bad[j] = row[j] == -1;
@@ -520,7 +530,7 @@ __device__ __forceinline__ void attend_part(const AttendArgs& g, const AttendUni
     asm volatile("cp.async.wait_group %0;" ::"n"(kDeep - 2) : "memory");
     __syncwarp();                       // everyone's copies are in, and step i - 1 is read
     start(i + (kDeep - 1) * kWarps, n == 0 ? kDeep - 1 : n - 1);
-    const uint32_t stage = ring + n * S::kStage;
+    const uint32_t stage = ring + n * kStageBytes;
     float ks[S::NT], vs[S::NT];
     bool bad_half[S::NT];
 #pragma unroll
@@ -616,7 +626,9 @@ __device__ __forceinline__ void attend_part(const AttendArgs& g, const AttendUni
   }
 }
 
+template <int KIND>
 __device__ __forceinline__ int unit_tiles(const AttendUnit& u) {
+  constexpr int kTileSlots = Shape<KIND, 64>::kTile;
   if (!u.rows) return 0;
   const int ea = min(u.held, u.end);
   const int n = (ea + kTileSlots - 1) / kTileSlots + (u.end - ea + kTileSlots - 1) / kTileSlots;
@@ -646,13 +658,16 @@ __device__ __forceinline__ void finish_row(const AttendArgs& g, const AttendUnit
 }
 
 template <int KIND, int D, int ROWS>
-__global__ void __launch_bounds__(kWarps * 32, 2) attend_kernel(AttendArgs g) {
-  constexpr int kRowBytes = Shape<KIND, D>::kRow, kRing = kStages<kRowBytes> * kStageBytes<kRowBytes>;
+__global__ void __launch_bounds__(kWarps * 32, Ring<KIND, D, ROWS>::kPerSm)
+    attend_kernel(AttendArgs g) {
+  constexpr int kTileSlots = Shape<KIND, D>::kTile;
+  using R = Ring<KIND, D, ROWS>;
+  constexpr int kRing = R::kDeep * R::kBytes;
   // the rings, and over them, once a piece's steps are done, its warps' outputs
   extern __shared__ __align__(128) char s_ring[];
   float (*s_o)[ROWS][D] = reinterpret_cast<float (*)[ROWS][D]>(s_ring);
   static_assert(kRing >= ROWS * D * 4, "");
-  __shared__ Meta s_meta[kWarps][kStages<kRowBytes>];
+  __shared__ Meta s_meta[kWarps][R::kDeep];
   __shared__ float s_m[kWarps][ROWS], s_l[kWarps][ROWS];
   __shared__ int s_sum[kWarps], s_at[3];
   grid_dep_wait();
@@ -664,7 +679,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attend_kernel(AttendArgs g) {
   const int run = (g.units + kWarps * 32 - 1) / (kWarps * 32);
   const int u0 = min(g.units, tid * run), u1 = min(g.units, u0 + run);
   int sum = 0;
-  for (int i = u0; i < u1; ++i) sum += unit_tiles(attend_unit<ROWS>(g, i));
+  for (int i = u0; i < u1; ++i) sum += unit_tiles<KIND>(attend_unit<ROWS>(g, i));
   int incl = sum;
 #pragma unroll
   for (int o = 1; o < 32; o *= 2) {
@@ -684,7 +699,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attend_kernel(AttendArgs g) {
   if (start >= before && start < before + sum) {
     int at = before;
     for (int i = u0; i < u1; ++i) {
-      const int n = unit_tiles(attend_unit<ROWS>(g, i));
+      const int n = unit_tiles<KIND>(attend_unit<ROWS>(g, i));
       if (start < at + n) {
         s_at[0] = i;
         s_at[1] = at;
@@ -704,7 +719,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attend_kernel(AttendArgs g) {
   int2 desc = make_int2(-1, 0);
   while (pos < stop) {
     const AttendUnit u = attend_unit<ROWS>(g, unit);
-    const int tiles = unit_tiles(u);
+    const int tiles = unit_tiles<KIND>(u);
     const int a0 = pos - at, a1 = min(tiles, stop - at);
     if (tiles > 0) {
       State<D, ROWS> st;
@@ -720,15 +735,15 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attend_kernel(AttendArgs g) {
       const int ea = min(u.held, u.end), ta = (ea + kTileSlots - 1) / kTileSlots;
       if constexpr (KIND == kImage) {
         constexpr int k = kTileSlots / Shape<kImage, D>::kSlots;
-        attend_part<kImage, D, ROWS>(g, u, 0, ea, a0 * k + warp,
-                                     min(min(a1, ta) * k, (ea + 15) / 16), ring, s_meta[warp], st);
+        attend_part<kImage, D, ROWS, R::kDeep, R::kBytes>(g, u, 0, ea, a0 * k + warp,
+                                     min(min(a1, ta) * k, (ea + 31) / 32), ring, s_meta[warp], st);
         constexpr int kt = kTileSlots / Shape<kTail, D>::kSlots;
-        attend_part<kTail, D, ROWS>(g, u, ea, u.end, max(a0 - ta, 0) * kt + warp,
+        attend_part<kTail, D, ROWS, R::kDeep, R::kBytes>(g, u, ea, u.end, max(a0 - ta, 0) * kt + warp,
                                     min((a1 - ta) * kt, (u.end - ea + 7) / 8), ring, s_meta[warp],
                                     st);
       } else {
         constexpr int k = kTileSlots / Shape<KIND, D>::kSlots, w = Shape<KIND, D>::kSlots;
-        attend_part<KIND, D, ROWS>(g, u, 0, u.end, a0 * k + warp, min(a1 * k, (u.end + w - 1) / w),
+        attend_part<KIND, D, ROWS, R::kDeep, R::kBytes>(g, u, 0, u.end, a0 * k + warp, min(a1 * k, (u.end + w - 1) / w),
                                    ring, s_meta[warp], st);
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
@@ -868,16 +883,17 @@ cudaError_t allow_smem(int bytes) {
 
 template <int KIND, int D, int ROWS>
 cudaError_t launch_attend(AttendArgs& g, cudaStream_t st, int* launches) {
+  using R = Ring<KIND, D, ROWS>;
   g.mtiles = (int)(((long long)g.t.max_tokens * g.c.group + ROWS - 1) / ROWS);
   const long long units = (long long)g.c.seqs * g.c.kv_heads * g.mtiles;
+  constexpr int kTileSlots = Shape<KIND, D>::kTile;
   const long long most = units * ((g.c.capacity + kTileSlots - 1) / kTileSlots + 1);
   if (most > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
   g.units = (int)units;
   g.min_tiles = 1;
-  const long long fit = 152 * 2;
+  const long long fit = 152 * R::kPerSm;
   const int grid = (int)(most < fit ? most : fit);
-  constexpr int kRow = Shape<KIND, D>::kRow;
-  constexpr int smem = kWarps * kStages<kRow> * kStageBytes<kRow>;
+  constexpr int smem = kWarps * R::kDeep * R::kBytes;
   cudaError_t e = allow_smem<attend_kernel<KIND, D, ROWS>>(smem);
   if (e != cudaSuccess) return e;
   e = launch_after(attend_kernel<KIND, D, ROWS>, dim3(grid), dim3(kWarps * 32), smem, st, g);
