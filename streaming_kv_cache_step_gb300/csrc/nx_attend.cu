@@ -29,6 +29,8 @@ namespace nx {
 namespace {
 
 constexpr int kWarps = 4;
+constexpr int kAttendGrid = kSms * 4;  // thread blocks of one launch, at most
+constexpr int kPieceRows = 16;         // query rows of a piece, at most
 // kTail: bf16 rows behind an image, with their output features in the image's order
 enum Kind { kBf16 = 0, kImage = 1, kF32 = 2, kTail = 3 };
 template <int KIND>
@@ -669,53 +671,20 @@ __global__ void __launch_bounds__(kWarps * 32, Ring<KIND, D, ROWS>::kPerSm)
   static_assert(kRing >= ROWS * D * 4, "");
   __shared__ Meta s_meta[kWarps][R::kDeep];
   __shared__ float s_m[kWarps][ROWS], s_l[kWarps][ROWS];
-  __shared__ int s_sum[kWarps], s_at[3];
   grid_dep_wait();
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const int b = blockIdx.x;
   const uint32_t ring = smem_at(s_ring) + warp * kRing;
 
-  // where this block's share of all tiles starts: every thread adds up a run of units
-  const int run = (g.units + kWarps * 32 - 1) / (kWarps * 32);
-  const int u0 = min(g.units, tid * run), u1 = min(g.units, u0 + run);
-  int sum = 0;
-  for (int i = u0; i < u1; ++i) sum += unit_tiles<KIND>(attend_unit<ROWS>(g, i));
-  int incl = sum;
-#pragma unroll
-  for (int o = 1; o < 32; o *= 2) {
-    const int y = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += y;
-  }
-  if (lane == 31) s_sum[warp] = incl;
-  __syncthreads();
-  int before = incl - sum, total = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) before += s_sum[w];
-    total += s_sum[w];
-  }
-  const int per = max(g.min_tiles, (total + (int)gridDim.x - 1) / (int)gridDim.x);
-  const long long start = (long long)b * per;
-  if (start >= before && start < before + sum) {
-    int at = before;
-    for (int i = u0; i < u1; ++i) {
-      const int n = unit_tiles<KIND>(attend_unit<ROWS>(g, i));
-      if (start < at + n) {
-        s_at[0] = i;
-        s_at[1] = at;
-        break;
-      }
-      at += n;
-    }
-  }
-  __syncthreads();
+  const AttendShare sh = attend_share<kWarps * 32>(
+      g, [&](int i) { return unit_tiles<KIND>(attend_unit<ROWS>(g, i)); });
   grid_dep_trigger();
-  if (start >= total) {
+  if (sh.start >= sh.total) {
     if (tid == 0) g.ws.desc[b] = make_int2(-1, 0);
     return;
   }
-  const int stop = (int)min((long long)total, start + per);
-  int unit = s_at[0], at = s_at[1], pos = (int)start;   // `at`: the unit's first tile
+  const int per = sh.per, stop = min(sh.total, sh.start + per);
+  int unit = sh.unit, at = sh.at, pos = sh.start;       // `at`: the unit's first tile
   int2 desc = make_int2(-1, 0);
   while (pos < stop) {
     const AttendUnit u = attend_unit<ROWS>(g, unit);
@@ -804,8 +773,7 @@ __global__ void __launch_bounds__(kWarps * 32, Ring<KIND, D, ROWS>::kPerSm)
   if (tid == 0) g.ws.desc[b] = desc;
 }
 
-// Joins the pieces of the unit that starts in block b and ends in a later one: its first piece
-// lies at 2 b + 1, the others at 2 b' of the blocks that go on with it.
+// Joins the pieces of the unit that starts in block b and ends in a later one.
 constexpr int kJoinWarps = 16;
 template <int D, int ROWS>
 __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(AttendArgs g) {
@@ -890,8 +858,7 @@ cudaError_t launch_attend(AttendArgs& g, cudaStream_t st, int* launches) {
   const long long most = units * ((g.c.capacity + kTileSlots - 1) / kTileSlots + 1);
   if (most > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
   g.units = (int)units;
-  g.min_tiles = 1;
-  const long long fit = 152 * R::kPerSm;
+  const long long fit = kSms * R::kPerSm;
   const int grid = (int)(most < fit ? most : fit);
   constexpr int smem = kWarps * R::kDeep * R::kBytes;
   cudaError_t e = allow_smem<attend_kernel<KIND, D, ROWS>>(smem);
@@ -907,6 +874,7 @@ cudaError_t launch_attend(AttendArgs& g, cudaStream_t st, int* launches) {
 template <int D>
 cudaError_t launch_attend(AttendArgs& g, cudaStream_t st, int* launches) {
   if (g.c.dtype == NX_DTYPE_F32) return launch_attend<kF32, D, 8>(g, st, launches);
+  if (attend_tc_takes(g.c, g.t)) return launch_attend_tc(g, st, launches);
   const bool few = (long long)g.t.max_tokens * g.c.group <= 8;
   if (g.im.k)
     return few ? launch_attend<kImage, D, 8>(g, st, launches)
@@ -922,7 +890,8 @@ extern "C" size_t nexus_attend_workspace_bytes(const nx_cache* cache, const nx_t
   using namespace nx;
   if (!valid_cache(cache) || !valid_tokens(*cache, tokens)) return 0;
   AttendWs ws;
-  return attend_layout(cache->head_dim, nullptr, &ws);
+  return attend_tc_takes(*cache, *tokens) ? attend_tc_layout(cache->head_dim, nullptr, &ws)
+                                          : attend_layout(cache->head_dim, nullptr, &ws);
 }
 
 extern "C" nx_status nexus_attend(const nx_cache* cache, const nx_tokens* tokens,
@@ -954,7 +923,8 @@ extern "C" nx_status nexus_attend(const nx_cache* cache, const nx_tokens* tokens
   if (image) g.im = *image;
   g.a = a;
   g.dev_status = dev_status;
-  attend_layout(c.head_dim, static_cast<char*>(ws), &g.ws);
+  if (attend_tc_takes(c, *tokens)) attend_tc_layout(c.head_dim, static_cast<char*>(ws), &g.ws);
+  else attend_layout(c.head_dim, static_cast<char*>(ws), &g.ws);
   g.b = image_block(c);
   g.c1 = a.scale * 1.4426950408889634f;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);

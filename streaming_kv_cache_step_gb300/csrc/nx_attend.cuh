@@ -8,16 +8,17 @@
 
 namespace nx {
 
-// The workspace of nexus_attend, of a size that depends on head_dim alone: a split unit is
-// one that the boundary between two thread blocks cuts, so there are at most two pieces per
-// thread block, however many units there are.
-constexpr int kAttendGrid = 152 * 4;          // thread blocks of one launch, at most
-constexpr int kPieceRows = 16;                // query rows of a piece, at most
+// Where the pieces of split units wait to be joined. A unit is split where the boundary between
+// two thread blocks cuts it, so there are at most two pieces per thread block, however many
+// units there are: a unit's first piece, if it goes on in the next block, is at slot 2 b + 1 of
+// the block b that it starts in, its other pieces are at 2 b' of the blocks b' that go on with
+// it. The layout within a slot is its kernel's own.
+constexpr int kSms = 152;
 struct AttendWs {
-  int2* desc;          // [kAttendGrid] (unit, last block) of the unit that starts in block b
-                       // and goes on in the next ones; unit < 0: none
-  float2* stat;        // [2 * kAttendGrid][kPieceRows] running maximum (log2 units) and sum
-  float* out;          // [2 * kAttendGrid][kPieceRows][head_dim] unnormalised output
+  int2* desc;          // [blocks] (unit, last block) of the unit that starts in block b and goes
+                       // on in the next ones; unit < 0: none
+  float2* stat;        // [2 * blocks][rows] running maximum (log2 units) and sum
+  float* out;          // [2 * blocks][rows x head_dim] unnormalised output
 };
 
 struct AttendArgs {
@@ -30,7 +31,6 @@ struct AttendArgs {
   int b;                // rows per image block
   int mtiles;           // row tiles per slice
   int units;            // seqs * kv_heads * mtiles
-  int min_tiles;        // tiles of a thread block, at least
   float c1;             // scale * log2(e)
 };
 
@@ -76,5 +76,64 @@ __device__ __forceinline__ AttendUnit attend_unit(const AttendArgs& g, int id) {
   u.low = u.rows ? row_limit(g, u, u.r0) : 0;
   return u;
 }
+
+// A thread block's share of all tiles: `per` of `total` from `start` on, which lies in unit
+// `unit`, whose first tile has number `at`.
+struct AttendShare {
+  int per, total, start, unit, at;
+};
+
+// Every one of THREADS threads adds up a run of units; tiles(i): tiles of unit i. unit and at
+// are undefined if start >= total.
+template <int THREADS, typename Tiles>
+__device__ __forceinline__ AttendShare attend_share(const AttendArgs& g, const Tiles& tiles) {
+  __shared__ int s_sum[THREADS / 32], s_at[2];
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  const int run = (g.units + THREADS - 1) / THREADS;
+  const int u0 = (int)min((long long)g.units, (long long)tid * run), u1 = min(g.units, u0 + run);
+  int sum = 0;
+  for (int i = u0; i < u1; ++i) sum += tiles(i);
+  int incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o *= 2) {
+    const int y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) s_sum[warp] = incl;
+  __syncthreads();
+  int before = incl - sum, total = 0;
+#pragma unroll
+  for (int w = 0; w < THREADS / 32; ++w) {
+    if (w < warp) before += s_sum[w];
+    total += s_sum[w];
+  }
+  AttendShare x;
+  x.total = total;
+  x.per = max(1, (total + (int)gridDim.x - 1) / (int)gridDim.x);
+  const long long start = (long long)blockIdx.x * x.per;
+  if (start >= before && start < (long long)before + sum) {
+    int at = before;
+    for (int i = u0; i < u1; ++i) {
+      const int n = tiles(i);
+      if (start < at + n) {
+        s_at[0] = i;
+        s_at[1] = at;
+        break;
+      }
+      at += n;
+    }
+  }
+  __syncthreads();
+  x.start = (int)min(start, (long long)total);
+  x.unit = s_at[0];
+  x.at = s_at[1];
+  return x;
+}
+
+// nx_attend_tc.cu: the tensor-core kernel for many query rows per slice (bf16 caches), its
+// workspace (base may be null; returns the bytes), and whether it takes a call.
+bool attend_tc_takes(const nx_cache& c, const nx_tokens& t);
+size_t attend_tc_layout(int D, char* base, AttendWs* ws);
+cudaError_t launch_attend_tc(AttendArgs& g, cudaStream_t st, int* launches);
 
 }  // namespace nx

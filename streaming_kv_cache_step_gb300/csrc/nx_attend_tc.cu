@@ -1,0 +1,685 @@
+// nx_attend_tc.cu -- nexus_attend for many query rows per slice (prompt chunks, drafts of
+// several tokens): the same softmax as nx_attend.cu on the 5th-generation tensor cores.
+//
+// A thread block holds two streams of 128 query rows (thread = row): two row tiles that share
+// each tile of 128 slots of K and V, or, for slices with up to 128 rows, one row tile whose
+// even and odd slot tiles are the two streams. Per slot tile and stream:
+//   S = Q K^T      tcgen05.mma, 128 x 128 x head_dim, Q and K in shared memory, S in TMEM
+//   p = 2^(c1 S - m), bf16, over S's own columns of TMEM; l += sum p
+//   O += p V       tcgen05.mma, p from TMEM, V in shared memory (features contiguous), O in TMEM
+// While one stream's warps take their exponentials the other's matrices multiply. m is raised,
+// and O in TMEM multiplied, only when a logit exceeds it by more than 2^8: rarely after the
+// first tiles. The roles:
+//   warps 0-3, 4-7  softmax of the two streams, and the results
+//   warps 8-11      K and V into a ring of shared-memory slots (asynchronous 16-byte copies into
+//                   the 128-byte swizzle that the matrix descriptors name; rows that do not
+//                   exist become zeros), or 8-bit rows through registers: a code times its
+//                   power-of-two scale is a bf16 value exactly
+//   warp 12         issues the matrix instructions
+// Every wait is bounded; when one gives up, the block flags NX_DEV_TIMEOUT, waits for nothing
+// more, issues nothing more and ends, its TMEM freed.
+#include <cuda_fp8.h>
+
+#include <atomic>
+
+#include "nx_attend.cuh"
+
+namespace nx {
+namespace {
+
+constexpr int kTile = 128;                 // slots of a tile, rows of a stream
+constexpr int kThreads = 13 * 32;
+constexpr int kLoaders = 128;              // threads of the loading warps
+constexpr int kTcRows = 256;               // rows of a piece, at most
+constexpr int kTcGrid = kSms;
+constexpr int kPolls = 1 << 20;               // mbarrier polls before giving up
+constexpr float kRaise = 8.f;              // log2 units
+
+__device__ __forceinline__ uint32_t smem_at(const void* p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+__device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count));
+}
+__device__ __forceinline__ void bar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool bar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// Waits for a phase, unless the block has given up already.
+__device__ __forceinline__ void bar_wait(uint32_t bar, uint32_t parity, volatile int* gave_up,
+                                         int32_t* dev_status) {
+  if (bar_test(bar, parity)) return;
+  for (int i = 0; i < kPolls; ++i) {
+    if (*gave_up) return;
+    if (bar_test(bar, parity)) return;
+  }
+  *gave_up = 1;
+  atomicOr(dev_status, NX_DEV_TIMEOUT);
+}
+__device__ __forceinline__ void tc_before() {
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tc_after() {
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void commit(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+      : "memory");
+}
+
+// Matrix descriptors, 128-byte swizzle. K-major (Q, K: features contiguous, rows of 128 bytes,
+// 8-row groups 1024 bytes apart). MN-major (V: the output's features contiguous): 64-feature
+// blocks `block` bytes apart, groups of 8 slots 1024 bytes apart.
+__device__ __forceinline__ uint64_t desc_k(uint32_t at) {
+  return (uint64_t)((at & 0x3FFFFu) >> 4) | (uint64_t)1 << 16 | (uint64_t)(1024 >> 4) << 32 |
+         (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+__device__ __forceinline__ uint64_t desc_mn(uint32_t at, uint32_t block) {
+  return (uint64_t)((at & 0x3FFFFu) >> 4) | (uint64_t)(block >> 4) << 16 |
+         (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+// kind::f16, fp32 accumulator, bf16 operands, M = 128; `mn`: B is MN-major.
+__host__ __device__ constexpr uint32_t idesc(int n, bool mn) {
+  return 1u << 4 | 1u << 7 | 1u << 10 | (mn ? 1u << 16 : 0u) | (uint32_t)(n >> 3) << 17 |
+         (uint32_t)(128 >> 4) << 24;
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id,
+                                       uint32_t add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"(add)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id,
+                                       uint32_t add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(id), "r"(add)
+      : "memory");
+}
+
+// 32 columns of this thread's TMEM lane.
+__device__ __forceinline__ void tmem_ld32(uint32_t at, float* x) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(x);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(at));
+}
+__device__ __forceinline__ void tmem_ld_wait() {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
+      "%13,%14,%15,%16};" ::"r"(at),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+      "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
+  const __nv_bfloat162 r = __floats2bfloat162_rn(a, b);
+  return reinterpret_cast<const uint32_t&>(r);
+}
+
+template <int D, int NQ>
+struct Plan {
+  static constexpr int kBlocks = D / 64;                      // 128-byte columns of a row
+  static constexpr int kBlockBytes = kTile * 128;             // of 128 rows
+  static constexpr int kSlotBytes = kBlocks * kBlockBytes;    // one K or V tile, one Q tile
+  static constexpr int kSlots = NQ == 2 ? 5 : 6;
+  static constexpr int kBars = 2 * kSlots + 1 + 3 * 2;
+  static constexpr int kSmem = 1024 + (NQ + kSlots) * kSlotBytes;
+};
+
+// Units of this kernel: 128 NQ rows, tiles of 128 slots.
+template <int NQ>
+__device__ __forceinline__ int tc_tiles(const AttendUnit& u) {
+  return !u.rows ? 0 : u.end ? (u.end + kTile - 1) / kTile : 1;
+}
+
+// Rows of 8-slot groups of a unit, as in a page table.
+struct TcRows {
+  const int32_t* table;
+  long long first, per_page;
+  int shift, pages;
+  __device__ __forceinline__ TcRows(const AttendArgs& g, const AttendUnit& u) {
+    const nx_cache& c = g.c;
+    shift = 0;
+    pages = c.num_pages;
+    per_page = 0;
+    if (c.page_size) {
+      table = c.block_table + (long long)u.s * c.max_pages_per_seq;
+      shift = __ffs(c.page_size) - 1;
+      per_page = (long long)c.kv_heads << shift;
+      first = (long long)g.t.layer * c.num_pages * per_page + ((long long)u.h << shift);
+    } else {
+      table = nullptr;
+      first = (((long long)g.t.layer * c.seqs + u.s) * c.kv_heads + u.h) * c.capacity;
+    }
+  }
+  __device__ __forceinline__ int page(int slot, int end) const {
+    return table && slot < end ? table[slot >> shift] : 0;
+  }
+  // row of a slot; -1: a bad page, -2: nothing there
+  __device__ __forceinline__ long long row(int slot, int end, int page) const {
+    return slot >= end              ? -2
+           : !table                 ? first + slot
+           : page < 0 || page >= pages ? -1
+                                    : first + page * per_page + (slot & ((1 << shift) - 1));
+  }
+};
+
+// One tile of K or V of a unit into a ring slot. The 128 loading threads take 8 rows (16 with
+// 64 features) at a time, 16 neighbouring threads a row's 256 bytes. Marks bad pages (a bit
+// per 8 slots) in *bad.
+template <int D, bool IMAGE>
+__device__ __forceinline__ void load_tile(const AttendArgs& g, const AttendUnit& u,
+                                          const TcRows& rows, bool is_v, int t0, uint32_t slot,
+                                          int tid, int* bad) {
+  constexpr int kChunks = D / 8;                    // 16-byte chunks of a bf16 row
+  constexpr int kLine = kLoaders / kChunks;         // rows per step
+  const char* src = static_cast<const char*>(is_v ? g.c.v : g.c.k);
+  const int chunk = tid % kChunks, sub = tid / kChunks;
+  int page[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) page[i] = rows.page(t0 + 8 * i, u.end);
+  if (!is_v && tid < 32) {
+    const int t = t0 + 8 * (tid & 15);
+    const unsigned marks =
+        __ballot_sync(0xffffffffu, rows.row(t, u.end, rows.page(t, u.end)) == -1) & 0xFFFFu;
+    if (tid == 0) {
+      *bad = (int)marks;
+      if (marks) atomicOr(g.dev_status, NX_DEV_BAD_PAGE);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kTile / kLine; ++i) {
+    const int r = i * kLine + sub, t = t0 + r;
+    const int pg = kLine == 8 ? page[i] : sub < 8 ? page[2 * i] : page[2 * i + 1 < 16 ? 2 * i + 1 : 15];
+    const long long row = rows.row(t, u.end, pg);
+    const uint32_t dst = slot + chunk / 8 * (kTile * 128) + r * 128 + ((chunk ^ r) & 7) * 16;
+    bool done = false;
+    if constexpr (IMAGE) {
+      if (row >= 0 && t < u.held) {
+        const uint2 x = *reinterpret_cast<const uint2*>(
+            static_cast<const char*>(is_v ? g.im.v : g.im.k) + row * D + chunk * 8);
+        const float sc = (is_v ? g.im.v_scale : g.im.k_scale)[
+            g.c.page_size ? row / g.b : image_scale_at(g.c, g.t.layer, u.s, u.h, t, g.b)];
+        uint32_t y[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t two = (j < 2 ? x.x : x.y) >> (j % 2 * 16) & 0xFFFFu;
+          const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
+          const float2 f = __half22float2(__half2(h));
+          y[j] = bf16_pair(f.x * sc, f.y * sc);
+        }
+        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst), "r"(y[0]), "r"(y[1]),
+                     "r"(y[2]), "r"(y[3])
+                     : "memory");
+        done = true;
+      }
+    }
+    if (!done)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst),
+                   "l"(src + (row < 0 ? 0 : row * (D * 2) + chunk * 16)), "r"(row < 0 ? 0 : 16)
+                   : "memory");
+  }
+}
+
+// Where row r of a unit's output and its statistics go.
+__device__ __forceinline__ void store_row(const AttendArgs& g, const AttendUnit& u, int r, int D,
+                                          int d0, const float* x, int n, float f) {
+  const int row = u.r0 + r;
+  __nv_bfloat16* p = static_cast<__nv_bfloat16*>(g.a.out) +
+                     (long long)(u.first + row / g.c.group) * g.a.out_stride +
+                     ((long long)u.h * g.c.group + row % g.c.group) * D + d0;
+  for (int i = 0; i < n; i += 8)
+    *reinterpret_cast<uint4*>(p + i) =
+        make_uint4(bf16_pair(x[i] * f, x[i + 1] * f), bf16_pair(x[i + 2] * f, x[i + 3] * f),
+                   bf16_pair(x[i + 4] * f, x[i + 5] * f), bf16_pair(x[i + 6] * f, x[i + 7] * f));
+}
+__device__ __forceinline__ void store_lse(const AttendArgs& g, const AttendUnit& u, int r, float m,
+                                          float l) {
+  if (!g.a.lse) return;
+  const int row = u.r0 + r;
+  g.a.lse[(long long)(u.first + row / g.c.group) * (g.c.kv_heads * g.c.group) +
+          u.h * g.c.group + row % g.c.group] =
+      l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+}
+
+template <int D, int NQ, bool IMAGE>
+__global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(AttendArgs g) {
+  using P = Plan<D, NQ>;
+  extern __shared__ char s_raw[];
+  __shared__ __align__(8) uint64_t s_bar[P::kBars];
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_up, s_bad[16];                   // bad-page marks of tile % 16
+  __shared__ float s_m[kTile], s_l[kTile];
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, b = blockIdx.x;
+  char* base = s_raw + (1024 - (smem_at(s_raw) & 1023)) % 1024;
+  const uint32_t s_q = smem_at(base), s_ring = s_q + NQ * P::kSlotBytes;
+  const uint32_t bars = smem_at(s_bar);
+  const uint32_t full = bars, empty = bars + 8 * P::kSlots, qfull = empty + 8 * P::kSlots;
+  const uint32_t sfull = qfull + 8, pfull = sfull + 16, odone = pfull + 16;
+  if (warp == 12) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_at(&s_tmem)),
+                 "r"(512u));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  if (tid == 0) {
+    for (int i = 0; i < P::kSlots; ++i) {
+      bar_init(full + 8 * i, kLoaders);
+      bar_init(empty + 8 * i, 1);
+    }
+    bar_init(qfull, kLoaders);
+    for (int i = 0; i < 2; ++i) {
+      bar_init(sfull + 8 * i, 1);
+      bar_init(pfull + 8 * i, kTile);
+      bar_init(odone + 8 * i, 1);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    s_up = 0;
+  }
+  grid_dep_wait();
+  tc_before();
+  const AttendShare sh = attend_share<kThreads>(
+      g, [&](int i) { return tc_tiles<NQ>(attend_unit<kTile * NQ>(g, i)); });
+  tc_after();
+  grid_dep_trigger();
+  const uint32_t tmem = s_tmem;
+  int unit = sh.unit, at = sh.at, pos = sh.start;
+  const int stop = min(sh.total, sh.start + sh.per);
+  int2 desc = make_int2(-1, 0);
+  int slot_no = 0;                     // ring slots filled or used so far (loader, issuer)
+  int segment = 0;                     // pieces done
+  int used[2] = {0, 0};                // slot tiles done by each stream
+  volatile int* up = &s_up;
+
+  while (pos < stop) {
+    const AttendUnit u = attend_unit<kTile * NQ>(g, unit);
+    const int tiles = tc_tiles<NQ>(u);
+    const int a0 = pos - at, a1 = min(tiles, stop - at), n = a1 - a0;
+    if (tiles > 0) {
+      // tiles of each stream: all of them, or the even and the odd ones
+      const int count[2] = {NQ == 2 ? n : (n + 1) / 2, NQ == 2 ? n : n / 2};
+      if (warp >= 8 && warp < 12) {
+        // ---- loader ----
+        const int lt = tid - 256;
+        const TcRows rows(g, u);
+        // the query rows, 128 bytes to a row of a 64-feature block
+        constexpr int kChunks = D / 8;
+        for (int i = lt; i < NQ * kTile * kChunks; i += kLoaders) {
+          const int r = i / kChunks, chunk = i % kChunks, row = u.r0 + r;
+          uint4 x = make_uint4(0, 0, 0, 0);
+          if (r < u.rows)
+            x = *reinterpret_cast<const uint4*>(
+                static_cast<const __nv_bfloat16*>(g.a.q) +
+                (u.first + row / g.c.group) * g.a.q_stride +
+                ((long long)u.h * g.c.group + row % g.c.group) * D + chunk * 8);
+          if (g.c1 < 0.f) {            // the kernel scales by |c1|
+            x.x ^= 0x80008000u; x.y ^= 0x80008000u; x.z ^= 0x80008000u; x.w ^= 0x80008000u;
+          }
+          const int rr = r % kTile;
+          const uint32_t dst = s_q + r / kTile * P::kSlotBytes + chunk / 8 * P::kBlockBytes +
+                               rr * 128 + ((chunk ^ rr) & 7) * 16;
+          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst), "r"(x.x), "r"(x.y),
+                       "r"(x.z), "r"(x.w)
+                       : "memory");
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        bar_arrive(qfull);
+        // K and V tiles in turn; a slot is announced two slots later, when its copies are in
+        const auto announce = [&](int k) {
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          bar_arrive(full + 8 * (k % P::kSlots));
+        };
+        for (int i = 0; i < 2 * n; ++i) {
+          const int k = slot_no + i, sl = k % P::kSlots;
+          bar_wait(empty + 8 * sl, (k / P::kSlots & 1) ^ 1, up, g.dev_status);
+          load_tile<D, IMAGE>(g, u, rows, i & 1, (a0 + i / 2) * kTile,
+                              s_ring + sl * P::kSlotBytes, lt, &s_bad[i / 2 & 15]);
+          asm volatile("cp.async.commit_group;" ::: "memory");
+          if (i >= 2) {
+            asm volatile("cp.async.wait_group 2;" ::: "memory");
+            announce(k - 2);
+          }
+        }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        if (n > 0) {
+          announce(slot_no + 2 * n - 2);
+          announce(slot_no + 2 * n - 1);
+        }
+      } else if (warp == 12 && lane == 0) {
+        // ---- matrix instructions ----
+        const auto qk = [&](int x, int i) {          // tile i of the piece, for stream x
+          const int k = slot_no + 2 * i, sl = k % P::kSlots;
+          bar_wait(full + 8 * sl, k / P::kSlots & 1, up, g.dev_status);
+          tc_after();
+          if (*up) return;
+          const uint32_t q = s_q + (NQ == 2 ? x : 0) * P::kSlotBytes;
+          const uint32_t kk = s_ring + sl * P::kSlotBytes;
+#pragma unroll
+          for (int s = 0; s < D / 16; ++s) {
+            const uint32_t o = s / 4 * P::kBlockBytes + s % 4 * 32;
+            mma_ss(tmem + x * 256, desc_k(q + o), desc_k(kk + o), idesc(kTile, false), s > 0);
+          }
+          commit(sfull + 8 * x);
+          if (NQ == 1 || x == 1) commit(empty + 8 * sl);
+        };
+        const auto pv = [&](int x, int i, int turn, bool first) {
+          const int k = slot_no + 2 * i + 1, sl = k % P::kSlots;
+          bar_wait(full + 8 * sl, k / P::kSlots & 1, up, g.dev_status);
+          bar_wait(pfull + 8 * x, turn & 1, up, g.dev_status);
+          tc_after();
+          if (*up) return;
+          const uint32_t vv = s_ring + sl * P::kSlotBytes;
+#pragma unroll
+          for (int s = 0; s < kTile / 16; ++s)
+            mma_ts(tmem + x * 256 + 128, tmem + x * 256 + 8 * s,
+                   desc_mn(vv + s * 2048, P::kBlockBytes), idesc(D, true), !first || s > 0);
+          commit(odone + 8 * x);
+          if (NQ == 1 || x == 1) commit(empty + 8 * sl);
+        };
+        bar_wait(qfull, segment & 1, up, g.dev_status);
+        const auto tile = [&](int x, int j) { return NQ == 2 ? j : 2 * j + x; };
+        for (int x = 0; x < 2; ++x)
+          if (count[x] > 0) qk(x, tile(x, 0));
+        for (int j = 0; j < count[0]; ++j)
+          for (int x = 0; x < 2; ++x) {
+            if (j >= count[x]) continue;
+            pv(x, tile(x, j), used[x] + j, j == 0);
+            if (j + 1 < count[x]) qk(x, tile(x, j + 1));
+          }
+      } else if (warp < 8) {
+        // ---- softmax ----
+        const int x = warp / 4, r = tid % kTile, rr = (NQ == 2 ? x * kTile : 0) + r;
+        const uint32_t lanes = (uint32_t)(warp % 4 * 32) << 16;
+        const uint32_t ts = tmem + lanes + x * 256, to = ts + 128;
+        const float c1 = fabsf(g.c1);
+        const int lim = rr < u.rows ? min(u.end, row_limit(g, u, u.r0 + rr)) : 0;
+        const int low = min(u.end, u.low);
+        float m = -INFINITY, l = 0.f;
+        for (int j = 0; j < count[x]; ++j) {
+          const int i = NQ == 2 ? j : 2 * j + x, t0 = (a0 + i) * kTile;
+          bar_wait(sfull + 8 * x, (used[x] + j) & 1, up, g.dev_status);
+          // complete already (the issuer's commits are in order): keeps the phases in step
+          if (j > 0) bar_wait(odone + 8 * x, (used[x] + j - 1) & 1, up, g.dev_status);
+          __syncwarp();
+          tc_after();
+          const int bad = s_bad[i & 15];
+          const bool mask = t0 + kTile > low || bad;
+          float s[32], top = -INFINITY;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            tmem_ld32(ts + 32 * q, s);
+            tmem_ld_wait();
+            if (mask) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (t0 + 32 * q + e >= lim || (bad >> (4 * q + e / 8) & 1)) s[e] = -INFINITY;
+            }
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) top = fmaxf(fmaxf(s[e], s[e + 1]), top);
+          }
+          // a scale of 0 leaves every visible logit 0
+          top = top == -INFINITY ? top : top * c1;
+          const bool raise = top > m + kRaise;
+          if (__any_sync(0xffffffffu, raise)) {
+            const float nm = raise ? top : m, f = raise ? ex2(m - nm) : 1.f;
+            m = nm;
+            l *= f;
+            if (j > 0) {               // S is complete, so the products before it are too
+#pragma unroll
+              for (int q = 0; q < D / 32; ++q) {
+                tmem_ld32(to + 32 * q, s);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) s[e] *= f;
+                tmem_st16(to + 32 * q, reinterpret_cast<const uint32_t*>(s));
+                tmem_st16(to + 32 * q + 16, reinterpret_cast<const uint32_t*>(s) + 16);
+              }
+            }
+          }
+          const float ref = m == -INFINITY ? 0.f : m;
+          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            tmem_ld32(ts + 32 * q, s);
+            tmem_ld_wait();
+            if (mask) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (t0 + 32 * q + e >= lim || (bad >> (4 * q + e / 8) & 1)) s[e] = -INFINITY;
+            }
+            uint32_t p[16];
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              // -inf stays -inf (a masked slot) even where c1 is 0
+              const float y0 = ex2(mask && s[e] == -INFINITY ? s[e] : fmaf(s[e], c1, -ref));
+              const float y1 = ex2(mask && s[e + 1] == -INFINITY ? s[e + 1]
+                                                                  : fmaf(s[e + 1], c1, -ref));
+              sum[e / 2 % 4] += y0;
+              sum[e / 2 % 4] += y1;
+              p[e / 2] = bf16_pair(y0, y1);
+            }
+            tmem_st16(ts + 16 * q, p);   // over columns of S that have been read
+          }
+          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          tmem_st_wait();
+          tc_before();
+          bar_arrive(pfull + 8 * x);
+        }
+        if (count[x] > 0) {
+          bar_wait(odone + 8 * x, (used[x] + count[x] - 1) & 1, up, g.dev_status);
+          __syncwarp();
+          tc_after();
+        }
+        // ---- results ----
+        float* s_o = reinterpret_cast<float*>(base + NQ * P::kSlotBytes);   // the ring is idle
+        const auto between = [] { asm volatile("bar.sync 1, 256;" ::: "memory"); };
+        if (NQ == 1) {
+          between();                   // both streams' products are done with the ring
+          if (x == 1) {
+            s_m[r] = m;
+            s_l[r] = l;
+            if (count[1] > 0)
+#pragma unroll
+              for (int q = 0; q < D / 32; ++q) {
+                float o[32];
+                tmem_ld32(to + 32 * q, o);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) s_o[(32 * q + e) * kTile + r] = o[e];
+              }
+          }
+          between();
+        }
+        if (NQ == 2 || x == 0) {
+          const bool whole = a0 == 0 && a1 == tiles;
+          const int piece = 2 * b + (a0 == 0 ? 1 : 0);
+          float f0 = 1.f, f1 = 0.f;
+          if (NQ == 1) {
+            const float m1 = s_m[r], nm = fmaxf(m, m1), ref = nm == -INFINITY ? 0.f : nm;
+            f0 = m == -INFINITY && l != l ? 1.f : ex2(m - ref);
+            f1 = count[1] == 0 ? 0.f : m1 == -INFINITY && s_l[r] != s_l[r] ? 1.f : ex2(m1 - ref);
+            l = l * f0 + (count[1] ? s_l[r] * f1 : 0.f);
+            m = nm;
+          }
+          const float f = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+#pragma unroll
+          for (int q = 0; q < D / 32; ++q) {
+            float o[32];
+            tmem_ld32(to + 32 * q, o);
+            tmem_ld_wait();
+            if (NQ == 1)
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                o[e] = o[e] * f0 + (count[1] ? s_o[(32 * q + e) * kTile + r] * f1 : 0.f);
+            if (rr < u.rows) {
+              if (whole) {
+                if (l == 0.f)
+#pragma unroll
+                  for (int e = 0; e < 32; ++e) o[e] = 0.f;
+                store_row(g, u, rr, D, 32 * q, o, 32, f);
+              } else {
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                  g.ws.out[((long long)piece * D + 32 * q + e) * kTcRows + rr] = o[e];
+              }
+            }
+          }
+          if (rr < u.rows) {
+            if (whole) store_lse(g, u, rr, m, l);
+            else g.ws.stat[piece * kTcRows + rr] = make_float2(m, l);
+          }
+        }
+        tc_before();
+      }
+      slot_no += 2 * n;
+      used[0] += count[0];
+      used[1] += count[1];
+      ++segment;
+      if (a0 == 0 && a1 < tiles) desc = make_int2(unit, (at + tiles - 1) / sh.per);
+      // the next piece's loads and products come after this one's results
+      __syncwarp();
+      __syncthreads();
+      tc_after();
+    }
+    pos = at + a1;
+    at += tiles;
+    ++unit;
+  }
+  if (tid == 0) g.ws.desc[b] = desc;
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  tc_before();
+  __syncthreads();
+  if (warp == 12) {
+    tc_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
+  }
+}
+
+// Joins the pieces of the unit that starts in block blockIdx.x and ends in a later one:
+// 32 features of it, a thread per row.
+template <int D, int NQ>
+__global__ void __launch_bounds__(kTcRows) attend_tc_join_kernel(AttendArgs g) {
+  grid_dep_wait();
+  const int b = blockIdx.x, d0 = blockIdx.y * 32, r = threadIdx.x;
+  const int2 desc = g.ws.desc[b];
+  if (desc.x < 0) return;
+  const AttendUnit u = attend_unit<kTile * NQ>(g, desc.x);
+  if (r >= u.rows) return;
+  float m = -INFINITY, l = 0.f, o[32];
+#pragma unroll
+  for (int e = 0; e < 32; ++e) o[e] = 0.f;
+  for (int i = b; i <= desc.y; ++i) {
+    const int piece = i == b ? 2 * b + 1 : 2 * i;
+    const float2 x = g.ws.stat[piece * kTcRows + r];
+    const float nm = fmaxf(m, x.x), ref = nm == -INFINITY ? 0.f : nm;
+    const float f0 = ex2(m - ref), f1 = x.x == -INFINITY && x.y != x.y ? 1.f : ex2(x.x - ref);
+    l = l * f0 + x.y * f1;
+    m = nm;
+    const float* p = g.ws.out + ((long long)piece * D + d0) * kTcRows + r;
+#pragma unroll
+    for (int e = 0; e < 32; ++e) o[e] = o[e] * f0 + p[e * kTcRows] * f1;
+  }
+  if (l == 0.f)
+#pragma unroll
+    for (int e = 0; e < 32; ++e) o[e] = 0.f;
+  store_row(g, u, r, D, d0, o, 32, l == 0.f ? 0.f : 1.f / l);
+  if (d0 == 0) store_lse(g, u, r, m, l);
+}
+
+// Lets a kernel use so much dynamic shared memory, once per device (twice does no harm).
+template <void (*kernel)(AttendArgs)>
+cudaError_t allow_smem(int bytes) {
+  static std::atomic<bool> done[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 0 && dev < 64 && done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev].store(true, std::memory_order_release);
+  return e;
+}
+
+template <int D, int NQ, bool IMAGE>
+cudaError_t launch_t(AttendArgs& g, cudaStream_t st, int* launches) {
+  constexpr int smem = Plan<D, NQ>::kSmem;
+  const long long all = (long long)g.t.max_tokens * g.c.group;
+  g.mtiles = (int)((all + kTile * NQ - 1) / (kTile * NQ));
+  const long long units = (long long)g.c.seqs * g.c.kv_heads * g.mtiles;
+  const long long most = units * ((g.c.capacity + kTile - 1) / kTile);
+  if (most > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
+  g.units = (int)units;
+  cudaError_t e = allow_smem<attend_tc_kernel<D, NQ, IMAGE>>(smem);
+  if (e != cudaSuccess) return e;
+  const int grid = (int)(most < kTcGrid ? most : kTcGrid);
+  e = launch_after(attend_tc_kernel<D, NQ, IMAGE>, dim3(grid), dim3(kThreads), smem, st, g);
+  if (e != cudaSuccess) return e;
+  note_launch(st, launches, "attend_tc");
+  e = launch_after(attend_tc_join_kernel<D, NQ>, dim3(grid, D / 32), dim3(kTcRows), 0, st, g);
+  if (e == cudaSuccess) note_launch(st, launches, "attend_tc_join");
+  return e;
+}
+
+template <int D, int NQ>
+cudaError_t launch_t(AttendArgs& g, cudaStream_t st, int* launches) {
+  return g.im.k ? launch_t<D, NQ, true>(g, st, launches) : launch_t<D, NQ, false>(g, st, launches);
+}
+
+size_t round256(size_t x) { return (x + 255) / 256 * 256; }
+
+}  // namespace
+
+bool attend_tc_takes(const nx_cache& c, const nx_tokens& t) {
+  return c.dtype == NX_DTYPE_BF16 && (long long)t.max_tokens * c.group > 16;
+}
+
+size_t attend_tc_layout(int D, char* base, AttendWs* ws) {
+  size_t at = 0;
+  ws->desc = reinterpret_cast<int2*>(base + at);
+  at += round256(kTcGrid * sizeof(int2));
+  ws->stat = reinterpret_cast<float2*>(base + at);
+  at += round256((size_t)2 * kTcGrid * kTcRows * sizeof(float2));
+  ws->out = reinterpret_cast<float*>(base + at);
+  return at + (size_t)2 * kTcGrid * kTcRows * D * sizeof(float);
+}
+
+cudaError_t launch_attend_tc(AttendArgs& g, cudaStream_t st, int* launches) {
+  const bool two = (long long)g.t.max_tokens * g.c.group > kTile;
+  if (g.c.head_dim == 128)
+    return two ? launch_t<128, 2>(g, st, launches) : launch_t<128, 1>(g, st, launches);
+  return two ? launch_t<64, 2>(g, st, launches) : launch_t<64, 1>(g, st, launches);
+}
+
+}  // namespace nx
