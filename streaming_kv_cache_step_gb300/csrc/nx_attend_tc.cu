@@ -11,11 +11,15 @@
 // and O in TMEM multiplied, only when a logit exceeds it by more than 2^8: rarely after the
 // first tiles. The roles:
 //   warps 0-3, 4-7  softmax of the two streams, and the results
-//   warps 8-11      K and V into a ring of shared-memory slots (asynchronous 16-byte copies into
+//   warps 8-10      K and V into a ring of shared-memory slots: asynchronous 16-byte copies into
 //                   the 128-byte swizzle that the matrix descriptors name; rows that do not
-//                   exist become zeros), or 8-bit rows through registers: a code times its
-//                   power-of-two scale is a bf16 value exactly
-//   warp 12         issues the matrix instructions
+//                   exist become zeros. 8-bit rows are copied some tiles ahead to a ring of
+//                   their own and go from there to the slots as bf16, which holds a code times
+//                   its power-of-two scale exactly
+//   warp 11         issues the matrix instructions
+// Where the tensor cores have time to spare (one row tile: K and V from HBM bound the kernel)
+// and for 8-bit rows, whose values need no rounding, p is kept as two bf16 terms, p = hi + lo,
+// with one product each; else as one (half a step of bf16, 2^-8, in each p).
 // Every wait is bounded; when one gives up, the block flags NX_DEV_TIMEOUT, waits for nothing
 // more, issues nothing more and ends, its TMEM freed.
 #include <cuda_fp8.h>
@@ -28,8 +32,10 @@ namespace nx {
 namespace {
 
 constexpr int kTile = 128;                 // slots of a tile, rows of a stream
-constexpr int kThreads = 13 * 32;
-constexpr int kLoaders = 128;              // threads of the loading warps
+constexpr int kThreads = 12 * 32;         // three warps per scheduler: 168 registers a thread
+constexpr int kLoadWarp = 8, kIssueWarp = 11;
+constexpr int kLoadWarps = 3, kLoaders = 32 * kLoadWarps;
+constexpr int kGroups = kTile / 8;         // runs of 8 slots of a tile
 constexpr int kTcRows = 256;               // rows of a piece, at most
 constexpr int kTcGrid = kSms;
 constexpr int kPolls = 1 << 20;               // mbarrier polls before giving up
@@ -149,14 +155,17 @@ __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
   return reinterpret_cast<const uint32_t&>(r);
 }
 
-template <int D, int NQ>
+template <int D, int NQ, bool IMAGE>
 struct Plan {
+  static constexpr bool kLo = IMAGE || NQ == 1;               // p as two terms
   static constexpr int kBlocks = D / 64;                      // 128-byte columns of a row
   static constexpr int kBlockBytes = kTile * 128;             // of 128 rows
   static constexpr int kSlotBytes = kBlocks * kBlockBytes;    // one K or V tile, one Q tile
-  static constexpr int kSlots = NQ == 2 ? 5 : 6;
+  static constexpr int kRawBytes = kTile * D;                 // its codes
+  static constexpr int kSlots = IMAGE ? 4 : NQ == 2 ? 5 : 6;
+  static constexpr int kRaw = IMAGE ? (NQ == 2 ? 2 : 4) : 0;
   static constexpr int kBars = 2 * kSlots + 1 + 3 * 2;
-  static constexpr int kSmem = 1024 + (NQ + kSlots) * kSlotBytes;
+  static constexpr int kSmem = 1024 + (NQ + kSlots) * kSlotBytes + kRaw * kRawBytes;
 };
 
 // Units of this kernel: 128 NQ rows, tiles of 128 slots.
@@ -197,60 +206,53 @@ struct TcRows {
   }
 };
 
-// One tile of K or V of a unit into a ring slot. The 128 loading threads take 8 rows (16 with
-// 64 features) at a time, 16 neighbouring threads a row's 256 bytes. Marks bad pages (a bit
-// per 8 slots) in *bad.
-template <int D, bool IMAGE>
-__device__ __forceinline__ void load_tile(const AttendArgs& g, const AttendUnit& u,
-                                          const TcRows& rows, bool is_v, int t0, uint32_t slot,
-                                          int tid, int* bad) {
-  constexpr int kChunks = D / 8;                    // 16-byte chunks of a bf16 row
-  constexpr int kLine = kLoaders / kChunks;         // rows per step
-  const char* src = static_cast<const char*>(is_v ? g.c.v : g.c.k);
-  const int chunk = tid % kChunks, sub = tid / kChunks;
-  int page[16];
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool ok) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(ok ? 16 : 0)
+               : "memory");
+}
+
+// The copies of 8 bf16 rows of K or V (slots t .. t + 7, one warp) to rows r .. r + 7 of a ring
+// slot. row: the first one's; < 0: none of them exist.
+template <int D>
+__device__ __forceinline__ void copy_group(const char* src, long long row, int t, int end,
+                                           uint32_t slot, int r, int lane) {
+  constexpr int kChunks = D / 8, kLine = 32 / kChunks;     // 16-byte chunks; rows per step
+  const int chunk = lane % kChunks, sub = lane / kChunks;
+  const char* p = src + (row < 0 ? 0 : row * (D * 2)) + lane * 16;
+  const uint32_t dst = slot + chunk / 8 * (kTile * 128) + (r + sub) * 128;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) page[i] = rows.page(t0 + 8 * i, u.end);
-  if (!is_v && tid < 32) {
-    const int t = t0 + 8 * (tid & 15);
-    const unsigned marks =
-        __ballot_sync(0xffffffffu, rows.row(t, u.end, rows.page(t, u.end)) == -1) & 0xFFFFu;
-    if (tid == 0) {
-      *bad = (int)marks;
-      if (marks) atomicOr(g.dev_status, NX_DEV_BAD_PAGE);
-    }
+  for (int i = 0; i < 8; i += kLine) {
+    const bool ok = row >= 0 && t + i + sub < end;
+    copy16(dst + i * 128 + ((chunk ^ (i + sub)) & 7) * 16, ok ? p + i * (D * 2) : src, ok);
   }
+}
+
+// 8 rows of codes in shared memory, times their scale, to rows r .. r + 7 of a ring slot.
+template <int D>
+__device__ __forceinline__ void expand_group(uint32_t raw, float scale, uint32_t slot, int r,
+                                             int lane) {
+  constexpr int kChunks = D / 8, kLine = 32 / kChunks;
+  const int chunk = lane % kChunks, sub = lane / kChunks;
+  const uint32_t dst = slot + chunk / 8 * (kTile * 128) + (r + sub) * 128;
 #pragma unroll
-  for (int i = 0; i < kTile / kLine; ++i) {
-    const int r = i * kLine + sub, t = t0 + r;
-    const int pg = kLine == 8 ? page[i] : sub < 8 ? page[2 * i] : page[2 * i + 1 < 16 ? 2 * i + 1 : 15];
-    const long long row = rows.row(t, u.end, pg);
-    const uint32_t dst = slot + chunk / 8 * (kTile * 128) + r * 128 + ((chunk ^ r) & 7) * 16;
-    bool done = false;
-    if constexpr (IMAGE) {
-      if (row >= 0 && t < u.held) {
-        const uint2 x = *reinterpret_cast<const uint2*>(
-            static_cast<const char*>(is_v ? g.im.v : g.im.k) + row * D + chunk * 8);
-        const float sc = (is_v ? g.im.v_scale : g.im.k_scale)[
-            g.c.page_size ? row / g.b : image_scale_at(g.c, g.t.layer, u.s, u.h, t, g.b)];
-        uint32_t y[4];
+  for (int i = 0; i < 8; i += kLine) {
+    uint32_t x[2], y[4];
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];"
+                 : "=r"(x[0]), "=r"(x[1])
+                 : "r"(raw + i * D + lane * 8)
+                 : "memory");
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t two = (j < 2 ? x.x : x.y) >> (j % 2 * 16) & 0xFFFFu;
-          const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
-          const float2 f = __half22float2(__half2(h));
-          y[j] = bf16_pair(f.x * sc, f.y * sc);
-        }
-        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst), "r"(y[0]), "r"(y[1]),
-                     "r"(y[2]), "r"(y[3])
-                     : "memory");
-        done = true;
-      }
+    for (int j = 0; j < 4; ++j) {
+      const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
+          (__nv_fp8x2_storage_t)(x[j / 2] >> (j % 2 * 16) & 0xFFFFu), __NV_E4M3);
+      const float2 f = __half22float2(__half2(h));
+      y[j] = bf16_pair(f.x * scale, f.y * scale);
     }
-    if (!done)
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst),
-                   "l"(src + (row < 0 ? 0 : row * (D * 2) + chunk * 16)), "r"(row < 0 ? 0 : 16)
-                   : "memory");
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(
+                     dst + i * 128 + ((chunk ^ (i + sub)) & 7) * 16),
+                 "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3])
+                 : "memory");
   }
 }
 
@@ -277,19 +279,21 @@ __device__ __forceinline__ void store_lse(const AttendArgs& g, const AttendUnit&
 
 template <int D, int NQ, bool IMAGE>
 __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(AttendArgs g) {
-  using P = Plan<D, NQ>;
+  using P = Plan<D, NQ, IMAGE>;
   extern __shared__ char s_raw[];
   __shared__ __align__(8) uint64_t s_bar[P::kBars];
   __shared__ uint32_t s_tmem;
   __shared__ int s_up, s_bad[16];                   // bad-page marks of tile % 16
   __shared__ float s_m[kTile], s_l[kTile];
+  __shared__ float s_scale[IMAGE ? P::kRaw : 1][kGroups];
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, b = blockIdx.x;
   char* base = s_raw + (1024 - (smem_at(s_raw) & 1023)) % 1024;
   const uint32_t s_q = smem_at(base), s_ring = s_q + NQ * P::kSlotBytes;
+  const uint32_t s_codes = s_ring + P::kSlots * P::kSlotBytes;
   const uint32_t bars = smem_at(s_bar);
   const uint32_t full = bars, empty = bars + 8 * P::kSlots, qfull = empty + 8 * P::kSlots;
   const uint32_t sfull = qfull + 8, pfull = sfull + 16, odone = pfull + 16;
-  if (warp == 12) {
+  if (warp == kIssueWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_at(&s_tmem)),
                  "r"(512u));
@@ -331,9 +335,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(AttendArgs g) {
     if (tiles > 0) {
       // tiles of each stream: all of them, or the even and the odd ones
       const int count[2] = {NQ == 2 ? n : (n + 1) / 2, NQ == 2 ? n : n / 2};
-      if (warp >= 8 && warp < 12) {
+      if (warp >= kLoadWarp && warp < kIssueWarp) {
         // ---- loader ----
-        const int lt = tid - 256;
+        const int lt = tid - 32 * kLoadWarp, lw = warp - kLoadWarp;
         const TcRows rows(g, u);
         // the query rows, 128 bytes to a row of a 64-feature block
         constexpr int kChunks = D / 8;
@@ -357,28 +361,118 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(AttendArgs g) {
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         bar_arrive(qfull);
-        // K and V tiles in turn; a slot is announced two slots later, when its copies are in
+        // K and V tiles in turn, every warp its runs of 8 slots
         const auto announce = [&](int k) {
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           bar_arrive(full + 8 * (k % P::kSlots));
         };
-        for (int i = 0; i < 2 * n; ++i) {
-          const int k = slot_no + i, sl = k % P::kSlots;
-          bar_wait(empty + 8 * sl, (k / P::kSlots & 1) ^ 1, up, g.dev_status);
-          load_tile<D, IMAGE>(g, u, rows, i & 1, (a0 + i / 2) * kTile,
-                              s_ring + sl * P::kSlotBytes, lt, &s_bad[i / 2 & 15]);
-          asm volatile("cp.async.commit_group;" ::: "memory");
-          if (i >= 2) {
-            asm volatile("cp.async.wait_group 2;" ::: "memory");
-            announce(k - 2);
+        const auto commit_copies = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
+        const auto bad_pages = [&](int i) {       // of tile i of the piece
+          if (lw > 0) return;
+          const int t = (a0 + i) * kTile + 8 * (lane & 15);
+          const unsigned marks =
+              __ballot_sync(0xffffffffu, rows.row(t, u.end, rows.page(t, u.end)) == -1) & 0xFFFFu;
+          if (lane == 0) {
+            s_bad[i & 15] = (int)marks;
+            if (marks) atomicOr(g.dev_status, NX_DEV_BAD_PAGE);
           }
-        }
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
-        if (n > 0) {
+        };
+        if constexpr (!IMAGE) {
+          // a slot is announced two slots later, when its copies are in
+          for (int i = 0; i < 2 * n; ++i) {
+            const int k = slot_no + i, sl = k % P::kSlots, t0 = (a0 + i / 2) * kTile;
+            const char* src = static_cast<const char*>(i & 1 ? g.c.v : g.c.k);
+            int page[(kGroups + kLoadWarps - 1) / kLoadWarps];
+#pragma unroll
+            for (int q = 0; q < (kGroups + kLoadWarps - 1) / kLoadWarps; ++q)
+              page[q] = rows.page(t0 + 8 * (q * kLoadWarps + lw), u.end);
+            if (!(i & 1)) bad_pages(i / 2);
+            bar_wait(empty + 8 * sl, (k / P::kSlots & 1) ^ 1, up, g.dev_status);
+            __syncwarp();
+#pragma unroll
+            for (int q = 0; q < (kGroups + kLoadWarps - 1) / kLoadWarps; ++q) {
+              const int r = 8 * (q * kLoadWarps + lw);
+              if (r < kTile)
+                copy_group<D>(src, rows.row(t0 + r, u.end, page[q]), t0 + r, u.end,
+                              s_ring + sl * P::kSlotBytes, r, lane);
+            }
+            commit_copies();
+            if (i >= 2) {
+              asm volatile("cp.async.wait_group 2;" ::: "memory");
+              announce(k - 2);
+            }
+          }
+          asm volatile("cp.async.wait_group 0;" ::: "memory");
           announce(slot_no + 2 * n - 2);
           announce(slot_no + 2 * n - 1);
+        } else {
+          // codes and scales of tile i / 2 of the piece to raw stage i % kRaw
+          const auto copy_codes = [&](int i) {
+            if (i < 2 * n) {
+              const int t0 = (a0 + i / 2) * kTile, held = min(u.held, u.end);
+              const char* src = static_cast<const char*>(i & 1 ? g.im.v : g.im.k);
+              const float* scales = i & 1 ? g.im.v_scale : g.im.k_scale;
+              int page[(kGroups + kLoadWarps - 1) / kLoadWarps];
+#pragma unroll
+              for (int q = 0; q < (kGroups + kLoadWarps - 1) / kLoadWarps; ++q)
+                page[q] = rows.page(t0 + 8 * (q * kLoadWarps + lw), held);
+#pragma unroll
+              for (int q = 0; q < (kGroups + kLoadWarps - 1) / kLoadWarps; ++q) {
+                const int r = 8 * (q * kLoadWarps + lw), t = t0 + r;
+                if (r >= kTile || t >= held) continue;
+                const long long row = rows.row(t, held, page[q]);
+                const uint32_t dst = s_codes + i % P::kRaw * P::kRawBytes + r * D + lane * 16;
+#pragma unroll
+                for (int y = 0; y < 8 * D; y += 512) {
+                  // a run that the image's last rows cut has zeros behind them
+                  const int rest = (min(held, t + 8) - t) * D - y - lane * 16;
+                  const bool ok = row >= 0 && rest > 0;
+                  copy16(dst + y, ok ? src + row * D + y + lane * 16 : src, ok);
+                }
+                if (lane == 0) {
+                  const long long at = g.c.page_size
+                                           ? row / g.b
+                                           : image_scale_at(g.c, g.t.layer, u.s, u.h, t, g.b);
+                  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(
+                                   smem_at(&s_scale[i % P::kRaw][r / 8])),
+                               "l"(scales + (row < 0 ? 0 : at)), "r"(row < 0 ? 0 : 4)
+                               : "memory");
+                }
+              }
+            }
+            commit_copies();
+          };
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < P::kRaw - 1; ++i) copy_codes(i);
+          for (int i = 0; i < 2 * n; ++i) {
+            const int k = slot_no + i, sl = k % P::kSlots, t0 = (a0 + i / 2) * kTile;
+            if (!(i & 1)) bad_pages(i / 2);
+            asm volatile("cp.async.wait_group %0;" ::"n"(P::kRaw - 2) : "memory");
+            __syncwarp();              // this warp's codes are in, and stage i - 1 is read
+            copy_codes(i + P::kRaw - 1);
+            bar_wait(empty + 8 * sl, (k / P::kSlots & 1) ^ 1, up, g.dev_status);
+            __syncwarp();
+            const uint32_t slot = s_ring + sl * P::kSlotBytes;
+            bool rest = false;
+            for (int q = lw; q < kGroups; q += kLoadWarps) {
+              const int r = 8 * q, t = t0 + r;
+              if (t < u.held && t < u.end) {
+                // behind u.end, within the run: zeros (codes), as for rows that do not exist
+                expand_group<D>(s_codes + i % P::kRaw * P::kRawBytes + r * D,
+                                s_scale[i % P::kRaw][q], slot, r, lane);
+              } else {
+                const char* src = static_cast<const char*>(i & 1 ? g.c.v : g.c.k);
+                copy_group<D>(src, rows.row(t, u.end, rows.page(t, u.end)), t, u.end, slot, r,
+                              lane);
+                rest = true;
+              }
+            }
+            if (rest) asm volatile("cp.async.wait_all;" ::: "memory");
+            announce(k);
+          }
         }
-      } else if (warp == 12 && lane == 0) {
+      } else if (warp == kIssueWarp && lane == 0) {
         // ---- matrix instructions ----
         const auto qk = [&](int x, int i) {          // tile i of the piece, for stream x
           const int k = slot_no + 2 * i, sl = k % P::kSlots;
@@ -406,6 +500,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(AttendArgs g) {
           for (int s = 0; s < kTile / 16; ++s)
             mma_ts(tmem + x * 256 + 128, tmem + x * 256 + 8 * s,
                    desc_mn(vv + s * 2048, P::kBlockBytes), idesc(D, true), !first || s > 0);
+          if constexpr (P::kLo)
+#pragma unroll
+            for (int s = 0; s < kTile / 16; ++s)
+              mma_ts(tmem + x * 256 + 128, tmem + x * 256 + 64 + 8 * s,
+                     desc_mn(vv + s * 2048, P::kBlockBytes), idesc(D, true), 1);
           commit(odone + 8 * x);
           if (NQ == 1 || x == 1) commit(empty + 8 * sl);
         };
@@ -471,8 +570,14 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(AttendArgs g) {
           }
           const float ref = m == -INFINITY ? 0.f : m;
           float sum[4] = {0.f, 0.f, 0.f, 0.f};
+          // p's columns lie over S's: a run of 32 logits is read before anything is stored over
+          // it. hi of run q goes to columns 16 q .., lo to 64 + 16 q ..; with lo, the upper runs
+          // come first, and hi waits in registers until its columns have been read
+          uint32_t hi[P::kLo ? 4 : 1][16];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
+          for (int step = 0; step < 4; ++step) {
+            const int q = P::kLo ? 3 - step : step;
+            uint32_t (&p)[16] = hi[P::kLo ? q : 0];
             tmem_ld32(ts + 32 * q, s);
             tmem_ld_wait();
             if (mask) {
@@ -480,7 +585,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(AttendArgs g) {
               for (int e = 0; e < 32; ++e)
                 if (t0 + 32 * q + e >= lim || (bad >> (4 * q + e / 8) & 1)) s[e] = -INFINITY;
             }
-            uint32_t p[16];
+            uint32_t lo[16];
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
               // -inf stays -inf (a masked slot) even where c1 is 0
@@ -490,8 +595,22 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(AttendArgs g) {
               sum[e / 2 % 4] += y0;
               sum[e / 2 % 4] += y1;
               p[e / 2] = bf16_pair(y0, y1);
+              if constexpr (P::kLo)
+                lo[e / 2] = bf16_pair(y0 - __uint_as_float(p[e / 2] << 16),
+                                      y1 - __uint_as_float(p[e / 2] & 0xFFFF0000u));
             }
-            tmem_st16(ts + 16 * q, p);   // over columns of S that have been read
+            if constexpr (!P::kLo) {
+              tmem_st16(ts + 16 * q, p);
+            } else {
+              tmem_st16(ts + 64 + 16 * q, lo);       // over a run at or above q
+              if (q == 1) {
+                tmem_st16(ts + 48, hi[3]);
+                tmem_st16(ts + 32, hi[2]);
+              } else if (q == 0) {
+                tmem_st16(ts + 16, hi[1]);
+                tmem_st16(ts, hi[0]);
+              }
+            }
           }
           l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
           tmem_st_wait();
@@ -582,7 +701,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(AttendArgs g) {
   asm volatile("cp.async.wait_all;" ::: "memory");
   tc_before();
   __syncthreads();
-  if (warp == 12) {
+  if (warp == kIssueWarp) {
     tc_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
   }
@@ -634,7 +753,7 @@ cudaError_t allow_smem(int bytes) {
 
 template <int D, int NQ, bool IMAGE>
 cudaError_t launch_t(AttendArgs& g, cudaStream_t st, int* launches) {
-  constexpr int smem = Plan<D, NQ>::kSmem;
+  constexpr int smem = Plan<D, NQ, IMAGE>::kSmem;
   const long long all = (long long)g.t.max_tokens * g.c.group;
   g.mtiles = (int)((all + kTile * NQ - 1) / (kTile * NQ));
   const long long units = (long long)g.c.seqs * g.c.kv_heads * g.mtiles;
