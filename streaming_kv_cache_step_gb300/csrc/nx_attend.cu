@@ -513,7 +513,8 @@ __device__ __forceinline__ void attend_part(const AttendArgs& g, const AttendUni
       for (int j = 0; j < S::NT; ++j) {
         if (lane == 0) meta[n].bad[j] = row[j] == -1;
         if constexpr (KIND == kImage) {
-          const long long x = g.c.page_size ? row[j] / g.b : blocks0 + (t + 8 * j) / g.b;
+          const long long x =
+              g.c.page_size ? row[j] >> g.b_shift : blocks0 + (t + 8 * j >> g.b_shift);
           const bool ok = row[j] >= 0;
           if (lane == 0) copy4(smem_at(&meta[n].ks[j]), g.im.k_scale + (ok ? x : 0), ok);
           if (lane == 1) copy4(smem_at(&meta[n].vs[j]), g.im.v_scale + (ok ? x : 0), ok);
@@ -926,6 +927,7 @@ extern "C" nx_status nexus_attend(const nx_cache* cache, const nx_tokens* tokens
   if (attend_tc_takes(c, *tokens)) attend_tc_layout(c.head_dim, static_cast<char*>(ws), &g.ws);
   else attend_layout(c.head_dim, static_cast<char*>(ws), &g.ws);
   g.b = image_block(c);
+  while (1 << g.b_shift < g.b) ++g.b_shift;
   g.c1 = a.scale * 1.4426950408889634f;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   return finish(c.head_dim == 128 ? launch_attend<128>(g, st, &launches)

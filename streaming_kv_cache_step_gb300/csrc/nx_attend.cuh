@@ -28,7 +28,7 @@ struct AttendArgs {
   nx_attend a;
   int32_t* dev_status;
   AttendWs ws;
-  int b;                // rows per image block
+  int b, b_shift;       // rows per image block, a power of two
   int mtiles;           // row tiles per slice
   int units;            // seqs * kv_heads * mtiles
   float c1;             // scale * log2(e)

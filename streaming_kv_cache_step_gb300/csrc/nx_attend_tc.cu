@@ -95,7 +95,8 @@ __device__ __forceinline__ uint64_t desc_mn(uint32_t at, uint32_t block) {
   return (uint64_t)((at & 0x3FFFFu) >> 4) | (uint64_t)(block >> 4) << 16 |
          (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
-// kind::f16, fp32 accumulator, bf16 operands, M = 128; `mn`: B is MN-major.
+// kind::f16, fp32 accumulator, bf16 operands, M = 128; `mn`: B is MN-major. kNegate: -A B.
+constexpr uint32_t kNegate = 1u << 13;
 __host__ __device__ constexpr uint32_t idesc(int n, bool mn) {
   return 1u << 4 | 1u << 7 | 1u << 10 | (mn ? 1u << 16 : 0u) | (uint32_t)(n >> 3) << 17 |
          (uint32_t)(128 >> 4) << 24;
@@ -128,6 +129,15 @@ __device__ __forceinline__ void tmem_ld32(uint32_t at, float* x) {
         "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
         "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
         "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(at));
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t at, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
       : "r"(at));
 }
 __device__ __forceinline__ void tmem_ld_wait() {
@@ -235,22 +245,28 @@ __device__ __forceinline__ void expand_group(uint32_t raw, float scale, uint32_t
   constexpr int kChunks = D / 8, kLine = 32 / kChunks;
   const int chunk = lane % kChunks, sub = lane / kChunks;
   const uint32_t dst = slot + chunk / 8 * (kTile * 128) + (r + sub) * 128;
+  uint32_t x[8 / kLine][2];
 #pragma unroll
-  for (int i = 0; i < 8; i += kLine) {
-    uint32_t x[2], y[4];
+  for (int i = 0; i < 8 / kLine; ++i)
     asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];"
-                 : "=r"(x[0]), "=r"(x[1])
-                 : "r"(raw + i * D + lane * 8)
+                 : "=r"(x[i][0]), "=r"(x[i][1])
+                 : "r"(raw + i * kLine * D + lane * 8)
                  : "memory");
 #pragma unroll
+  for (int i = 0; i < 8 / kLine; ++i) {
+    uint32_t y[4];
+#pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
-          (__nv_fp8x2_storage_t)(x[j / 2] >> (j % 2 * 16) & 0xFFFFu), __NV_E4M3);
-      const float2 f = __half22float2(__half2(h));
+      uint32_t h;
+      asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\t"
+          "cvt.rn.f16x2.e4m3x2 %0, a;\n\t}"
+          : "=r"(h)
+          : "r"(j % 2 ? x[i][j / 2] >> 16 : x[i][j / 2]));
+      const float2 f = __half22float2(reinterpret_cast<const __half2&>(h));
       y[j] = bf16_pair(f.x * scale, f.y * scale);
     }
     asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(
-                     dst + i * 128 + ((chunk ^ (i + sub)) & 7) * 16),
+                     dst + i * kLine * 128 + ((chunk ^ (i * kLine + sub)) & 7) * 16),
                  "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3])
                  : "memory");
   }
@@ -312,6 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(AttendArgs g) {
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     s_up = 0;
+    for (int i = 0; i < 16; ++i) s_bad[i] = 0;       // the loader's, where there are pages
   }
   grid_dep_wait();
   tc_before();
@@ -341,24 +358,21 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(AttendArgs g) {
         const TcRows rows(g, u);
         // the query rows, 128 bytes to a row of a 64-feature block
         constexpr int kChunks = D / 8;
+#pragma unroll 4
         for (int i = lt; i < NQ * kTile * kChunks; i += kLoaders) {
-          const int r = i / kChunks, chunk = i % kChunks, row = u.r0 + r;
-          uint4 x = make_uint4(0, 0, 0, 0);
-          if (r < u.rows)
-            x = *reinterpret_cast<const uint4*>(
-                static_cast<const __nv_bfloat16*>(g.a.q) +
-                (u.first + row / g.c.group) * g.a.q_stride +
-                ((long long)u.h * g.c.group + row % g.c.group) * D + chunk * 8);
-          if (g.c1 < 0.f) {            // the kernel scales by |c1|
-            x.x ^= 0x80008000u; x.y ^= 0x80008000u; x.z ^= 0x80008000u; x.w ^= 0x80008000u;
-          }
-          const int rr = r % kTile;
-          const uint32_t dst = s_q + r / kTile * P::kSlotBytes + chunk / 8 * P::kBlockBytes +
-                               rr * 128 + ((chunk ^ rr) & 7) * 16;
-          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst), "r"(x.x), "r"(x.y),
-                       "r"(x.z), "r"(x.w)
-                       : "memory");
+          const int r = i / kChunks, chunk = i % kChunks, row = u.r0 + r, rr = r % kTile;
+          const bool ok = r < u.rows;
+          const int token = row / g.c.group;
+          copy16(s_q + r / kTile * P::kSlotBytes + chunk / 8 * P::kBlockBytes + rr * 128 +
+                     ((chunk ^ rr) & 7) * 16,
+                 static_cast<const __nv_bfloat16*>(g.a.q) +
+                     (ok ? (u.first + token) * g.a.q_stride +
+                               ((long long)u.h * g.c.group + row - token * g.c.group) * D +
+                               chunk * 8
+                         : 0),
+                 ok);
         }
+        asm volatile("cp.async.wait_all;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         bar_arrive(qfull);
         // K and V tiles in turn, every warp its runs of 8 slots
@@ -368,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(AttendArgs g) {
         };
         const auto commit_copies = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
         const auto bad_pages = [&](int i) {       // of tile i of the piece
-          if (lw > 0) return;
+          if (lw > 0 || !rows.table) return;
           const int t = (a0 + i) * kTile + 8 * (lane & 15);
           const unsigned marks =
               __ballot_sync(0xffffffffu, rows.row(t, u.end, rows.page(t, u.end)) == -1) & 0xFFFFu;
@@ -406,6 +420,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(AttendArgs g) {
           announce(slot_no + 2 * n - 2);
           announce(slot_no + 2 * n - 1);
         } else {
+          const long long blocks0 =
+              g.c.page_size ? 0 : image_scale_at(g.c, g.t.layer, u.s, u.h, 0, g.b);
           // codes and scales of tile i / 2 of the piece to raw stage i % kRaw
           const auto copy_codes = [&](int i) {
             if (i < 2 * n) {
@@ -430,9 +446,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(AttendArgs g) {
                   copy16(dst + y, ok ? src + row * D + y + lane * 16 : src, ok);
                 }
                 if (lane == 0) {
-                  const long long at = g.c.page_size
-                                           ? row / g.b
-                                           : image_scale_at(g.c, g.t.layer, u.s, u.h, t, g.b);
+                  const long long at =
+                      g.c.page_size ? row >> g.b_shift : blocks0 + (t >> g.b_shift);
                   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(
                                    smem_at(&s_scale[i % P::kRaw][r / 8])),
                                "l"(scales + (row < 0 ? 0 : at)), "r"(row < 0 ? 0 : 4)
@@ -474,6 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(AttendArgs g) {
         }
       } else if (warp == kIssueWarp && lane == 0) {
         // ---- matrix instructions ----
+        const uint32_t negate = g.c1 < 0.f ? kNegate : 0u;   // the softmax scales by |c1|
         const auto qk = [&](int x, int i) {          // tile i of the piece, for stream x
           const int k = slot_no + 2 * i, sl = k % P::kSlots;
           bar_wait(full + 8 * sl, k / P::kSlots & 1, up, g.dev_status);
@@ -484,7 +500,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(AttendArgs g) {
 #pragma unroll
           for (int s = 0; s < D / 16; ++s) {
             const uint32_t o = s / 4 * P::kBlockBytes + s % 4 * 32;
-            mma_ss(tmem + x * 256, desc_k(q + o), desc_k(kk + o), idesc(kTile, false), s > 0);
+            mma_ss(tmem + x * 256, desc_k(q + o), desc_k(kk + o),
+                   idesc(kTile, false) | negate, s > 0);
           }
           commit(sfull + 8 * x);
           if (NQ == 1 || x == 1) commit(empty + 8 * sl);
@@ -536,21 +553,18 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(AttendArgs g) {
           tc_after();
           const int bad = s_bad[i & 15];
           const bool mask = t0 + kTile > low || bad;
-          float s[32], top = -INFINITY;
+          float s[kTile], top = -INFINITY;
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            tmem_ld32(ts + 32 * q, s);
-            tmem_ld_wait();
-            if (mask) {
+          for (int q = 0; q < 4; ++q) tmem_ld32(ts + 32 * q, s + 32 * q);
+          tmem_ld_wait();
+          if (mask) {
 #pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (t0 + 32 * q + e >= lim || (bad >> (4 * q + e / 8) & 1)) s[e] = -INFINITY;
-            }
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) top = fmaxf(fmaxf(s[e], s[e + 1]), top);
+            for (int e = 0; e < kTile; ++e)
+              if (t0 + e >= lim || (bad >> (e / 8) & 1)) s[e] = -INFINITY;
           }
-          // a scale of 0 leaves every visible logit 0
-          top = top == -INFINITY ? top : top * c1;
+#pragma unroll
+          for (int e = 0; e < kTile; e += 2) top = fmaxf(fmaxf(s[e], s[e + 1]), top);
+          top = top == -INFINITY ? top : top * c1;     // also where c1 is 0
           const bool raise = top > m + kRaise;
           if (__any_sync(0xffffffffu, raise)) {
             const float nm = raise ? top : m, f = raise ? ex2(m - nm) : 1.f;
@@ -558,59 +572,43 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(AttendArgs g) {
             l *= f;
             if (j > 0) {               // S is complete, so the products before it are too
 #pragma unroll
-              for (int q = 0; q < D / 32; ++q) {
-                tmem_ld32(to + 32 * q, s);
+              for (int q = 0; q < D / 16; ++q) {
+                uint32_t o[16];
+                tmem_ld16(to + 16 * q, o);
                 tmem_ld_wait();
 #pragma unroll
-                for (int e = 0; e < 32; ++e) s[e] *= f;
-                tmem_st16(to + 32 * q, reinterpret_cast<const uint32_t*>(s));
-                tmem_st16(to + 32 * q + 16, reinterpret_cast<const uint32_t*>(s) + 16);
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                tmem_st16(to + 16 * q, o);
               }
             }
           }
           const float ref = m == -INFINITY ? 0.f : m;
           float sum[4] = {0.f, 0.f, 0.f, 0.f};
-          // p's columns lie over S's: a run of 32 logits is read before anything is stored over
-          // it. hi of run q goes to columns 16 q .., lo to 64 + 16 q ..; with lo, the upper runs
-          // come first, and hi waits in registers until its columns have been read
-          uint32_t hi[P::kLo ? 4 : 1][16];
+          if (mask) {
+            // -inf stays -inf where c1 is 0 or the reference was raised to an infinity
 #pragma unroll
-          for (int step = 0; step < 4; ++step) {
-            const int q = P::kLo ? 3 - step : step;
-            uint32_t (&p)[16] = hi[P::kLo ? q : 0];
-            tmem_ld32(ts + 32 * q, s);
-            tmem_ld_wait();
-            if (mask) {
+            for (int e = 0; e < kTile; ++e)
+              s[e] = s[e] == -INFINITY ? s[e] : fmaf(s[e], c1, -ref);
+          } else {
 #pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (t0 + 32 * q + e >= lim || (bad >> (4 * q + e / 8) & 1)) s[e] = -INFINITY;
-            }
-            uint32_t lo[16];
+            for (int e = 0; e < kTile; ++e) s[e] = fmaf(s[e], c1, -ref);
+          }
+          // p's columns lie over S's: hi in 0 .. 63, lo in 64 .. 127
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              // -inf stays -inf (a masked slot) even where c1 is 0
-              const float y0 = ex2(mask && s[e] == -INFINITY ? s[e] : fmaf(s[e], c1, -ref));
-              const float y1 = ex2(mask && s[e + 1] == -INFINITY ? s[e + 1]
-                                                                  : fmaf(s[e + 1], c1, -ref));
-              sum[e / 2 % 4] += y0;
-              sum[e / 2 % 4] += y1;
-              p[e / 2] = bf16_pair(y0, y1);
+          for (int q = 0; q < 4; ++q) {
+            uint32_t hi[16], lo[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float y0 = ex2(s[32 * q + 2 * e]), y1 = ex2(s[32 * q + 2 * e + 1]);
+              sum[e % 4] += y0;
+              sum[e % 4] += y1;
+              hi[e] = bf16_pair(y0, y1);
               if constexpr (P::kLo)
-                lo[e / 2] = bf16_pair(y0 - __uint_as_float(p[e / 2] << 16),
-                                      y1 - __uint_as_float(p[e / 2] & 0xFFFF0000u));
+                lo[e] = bf16_pair(y0 - __uint_as_float(hi[e] << 16),
+                                  y1 - __uint_as_float(hi[e] & 0xFFFF0000u));
             }
-            if constexpr (!P::kLo) {
-              tmem_st16(ts + 16 * q, p);
-            } else {
-              tmem_st16(ts + 64 + 16 * q, lo);       // over a run at or above q
-              if (q == 1) {
-                tmem_st16(ts + 48, hi[3]);
-                tmem_st16(ts + 32, hi[2]);
-              } else if (q == 0) {
-                tmem_st16(ts + 16, hi[1]);
-                tmem_st16(ts, hi[0]);
-              }
-            }
+            tmem_st16(ts + 16 * q, hi);
+            if constexpr (P::kLo) tmem_st16(ts + 64 + 16 * q, lo);
           }
           l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
           tmem_st_wait();
