@@ -36,6 +36,7 @@ constexpr int kThreads = 12 * 32;         // three warps per scheduler: 168 regi
 constexpr int kLoadWarp = 8, kIssueWarp = 11;
 constexpr int kLoadWarps = 3, kLoaders = 32 * kLoadWarps;
 constexpr int kGroups = kTile / 8;         // runs of 8 slots of a tile
+constexpr int kRuns = (kGroups + kLoadWarps - 1) / kLoadWarps;   // of one loading warp
 constexpr int kTcRows = 256;               // rows of a piece, at most
 constexpr int kTcGrid = kSms;
 constexpr int kPolls = 1 << 20;               // mbarrier polls before giving up
@@ -84,16 +85,29 @@ __device__ __forceinline__ void commit(uint32_t bar) {
       : "memory");
 }
 
-// Matrix descriptors, 128-byte swizzle. K-major (Q, K: features contiguous, rows of 128 bytes,
-// 8-row groups 1024 bytes apart). MN-major (V: the output's features contiguous): 64-feature
-// blocks `block` bytes apart, groups of 8 slots 1024 bytes apart.
+// Matrix descriptors, 128-byte swizzle: the address (in 16-byte units) in the low 18 bits, the
+// rest as follows. K-major (Q, K: features contiguous, rows of 128 bytes): 8-row groups 1024
+// bytes apart. MN-major (V: the output's features contiguous): 64-feature blocks `block` bytes
+// apart, groups of 8 slots 1024 bytes apart.
+constexpr uint32_t kDescHigh = (1024 >> 4) | 1u << 14 | 2u << 29;
 __device__ __forceinline__ uint64_t desc_k(uint32_t at) {
-  return (uint64_t)((at & 0x3FFFFu) >> 4) | (uint64_t)1 << 16 | (uint64_t)(1024 >> 4) << 32 |
-         (uint64_t)1 << 46 | (uint64_t)2 << 61;
+  return (uint64_t)kDescHigh << 32 | (at >> 4 | 1u << 16);
 }
 __device__ __forceinline__ uint64_t desc_mn(uint32_t at, uint32_t block) {
-  return (uint64_t)((at & 0x3FFFFu) >> 4) | (uint64_t)(block >> 4) << 16 |
-         (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
+  return (uint64_t)kDescHigh << 32 | (at >> 4 | block >> 4 << 16);
+}
+// The same value in all lanes, and known to be: what the matrix instructions take lies in
+// registers of the warp, and is moved there from a lane's, 80 clocks an instruction, unless the
+// compiler sees that it is the warp's already.
+__device__ __forceinline__ uint32_t warp_value(uint32_t x) {
+  return __shfl_sync(0xffffffffu, x, 0);
+}
+__device__ __forceinline__ bool elected() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
 }
 // kind::f16, fp32 accumulator, bf16 operands, M = 128; `mn`: B is MN-major. kNegate: -A B.
 constexpr uint32_t kNegate = 1u << 13;
@@ -396,19 +410,19 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(AttendArgs g) {
           for (int i = 0; i < 2 * n; ++i) {
             const int k = slot_no + i, sl = k % P::kSlots, t0 = (a0 + i / 2) * kTile;
             const char* src = static_cast<const char*>(i & 1 ? g.c.v : g.c.k);
-            int page[(kGroups + kLoadWarps - 1) / kLoadWarps];
+            int page[kRuns];
 #pragma unroll
-            for (int q = 0; q < (kGroups + kLoadWarps - 1) / kLoadWarps; ++q)
+            for (int q = 0; q < kRuns; ++q)
               page[q] = rows.page(t0 + 8 * (q * kLoadWarps + lw), u.end);
             if (!(i & 1)) bad_pages(i / 2);
             bar_wait(empty + 8 * sl, (k / P::kSlots & 1) ^ 1, up, g.dev_status);
             __syncwarp();
+#pragma unroll 1
+            for (int r = 8 * lw; r < kTile; r += 8 * kLoadWarps) {
+              copy_group<D>(src, rows.row(t0 + r, u.end, page[0]), t0 + r, u.end,
+                            s_ring + sl * P::kSlotBytes, r, lane);
 #pragma unroll
-            for (int q = 0; q < (kGroups + kLoadWarps - 1) / kLoadWarps; ++q) {
-              const int r = 8 * (q * kLoadWarps + lw);
-              if (r < kTile)
-                copy_group<D>(src, rows.row(t0 + r, u.end, page[q]), t0 + r, u.end,
-                              s_ring + sl * P::kSlotBytes, r, lane);
+              for (int q = 0; q + 1 < kRuns; ++q) page[q] = page[q + 1];
             }
             commit_copies();
             if (i >= 2) {
@@ -428,15 +442,16 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(AttendArgs g) {
               const int t0 = (a0 + i / 2) * kTile, held = min(u.held, u.end);
               const char* src = static_cast<const char*>(i & 1 ? g.im.v : g.im.k);
               const float* scales = i & 1 ? g.im.v_scale : g.im.k_scale;
-              int page[(kGroups + kLoadWarps - 1) / kLoadWarps];
+              int page[kRuns];
 #pragma unroll
-              for (int q = 0; q < (kGroups + kLoadWarps - 1) / kLoadWarps; ++q)
+              for (int q = 0; q < kRuns; ++q)
                 page[q] = rows.page(t0 + 8 * (q * kLoadWarps + lw), held);
+#pragma unroll 1
+              for (int r = 8 * lw; r < kTile && t0 + r < held; r += 8 * kLoadWarps) {
+                const int t = t0 + r;
+                const long long row = rows.row(t, held, page[0]);
 #pragma unroll
-              for (int q = 0; q < (kGroups + kLoadWarps - 1) / kLoadWarps; ++q) {
-                const int r = 8 * (q * kLoadWarps + lw), t = t0 + r;
-                if (r >= kTile || t >= held) continue;
-                const long long row = rows.row(t, held, page[q]);
+                for (int q = 0; q + 1 < kRuns; ++q) page[q] = page[q + 1];
                 const uint32_t dst = s_codes + i % P::kRaw * P::kRawBytes + r * D + lane * 16;
 #pragma unroll
                 for (int y = 0; y < 8 * D; y += 512) {
@@ -470,6 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(AttendArgs g) {
             __syncwarp();
             const uint32_t slot = s_ring + sl * P::kSlotBytes;
             bool rest = false;
+#pragma unroll 1
             for (int q = lw; q < kGroups; q += kLoadWarps) {
               const int r = 8 * q, t = t0 + r;
               if (t < u.held && t < u.end) {
@@ -487,49 +503,65 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(AttendArgs g) {
             announce(k);
           }
         }
-      } else if (warp == kIssueWarp && lane == 0) {
-        // ---- matrix instructions ----
+      } else if (warp == kIssueWarp) {
+        // ---- matrix instructions: the whole warp goes along, one lane issues ----
         const uint32_t negate = g.c1 < 0.f ? kNegate : 0u;   // the softmax scales by |c1|
+        const uint32_t tm = warp_value(tmem);
+        int k_no = (int)warp_value(slot_no);
         const auto qk = [&](int x, int i) {          // tile i of the piece, for stream x
-          const int k = slot_no + 2 * i, sl = k % P::kSlots;
+          const int k = k_no + 2 * i, sl = k % P::kSlots;
           bar_wait(full + 8 * sl, k / P::kSlots & 1, up, g.dev_status);
+          __syncwarp();
+          if (warp_value(*up)) return;
           tc_after();
-          if (*up) return;
-          const uint32_t q = s_q + (NQ == 2 ? x : 0) * P::kSlotBytes;
-          const uint32_t kk = s_ring + sl * P::kSlotBytes;
+          const uint32_t q = warp_value(s_q + (NQ == 2 ? x : 0) * P::kSlotBytes);
+          const uint32_t kk = warp_value(s_ring + sl * P::kSlotBytes);
+          const uint32_t d = warp_value(tm + x * 256);
+          const uint32_t id = warp_value(idesc(kTile, false) | negate);
+          if (elected()) {
 #pragma unroll
-          for (int s = 0; s < D / 16; ++s) {
-            const uint32_t o = s / 4 * P::kBlockBytes + s % 4 * 32;
-            mma_ss(tmem + x * 256, desc_k(q + o), desc_k(kk + o),
-                   idesc(kTile, false) | negate, s > 0);
+            for (int s = 0; s < D / 16; ++s) {
+              const uint32_t o = s / 4 * P::kBlockBytes + s % 4 * 32;
+              mma_ss(d, desc_k(q + o), desc_k(kk + o), id, s > 0);
+            }
+            commit(sfull + 8 * x);
+            if (NQ == 1 || x == 1) commit(empty + 8 * sl);
           }
-          commit(sfull + 8 * x);
-          if (NQ == 1 || x == 1) commit(empty + 8 * sl);
+          __syncwarp();
         };
         const auto pv = [&](int x, int i, int turn, bool first) {
-          const int k = slot_no + 2 * i + 1, sl = k % P::kSlots;
+          const int k = k_no + 2 * i + 1, sl = k % P::kSlots;
           bar_wait(full + 8 * sl, k / P::kSlots & 1, up, g.dev_status);
           bar_wait(pfull + 8 * x, turn & 1, up, g.dev_status);
+          __syncwarp();
+          if (warp_value(*up)) return;
           tc_after();
-          if (*up) return;
-          const uint32_t vv = s_ring + sl * P::kSlotBytes;
-#pragma unroll
-          for (int s = 0; s < kTile / 16; ++s)
-            mma_ts(tmem + x * 256 + 128, tmem + x * 256 + 8 * s,
-                   desc_mn(vv + s * 2048, P::kBlockBytes), idesc(D, true), !first || s > 0);
-          if constexpr (P::kLo)
+          const uint32_t vv = warp_value(s_ring + sl * P::kSlotBytes);
+          const uint32_t d = warp_value(tm + x * 256);
+          const uint32_t add = warp_value(first ? 0u : 1u);
+          if (elected()) {
 #pragma unroll
             for (int s = 0; s < kTile / 16; ++s)
-              mma_ts(tmem + x * 256 + 128, tmem + x * 256 + 64 + 8 * s,
-                     desc_mn(vv + s * 2048, P::kBlockBytes), idesc(D, true), 1);
-          commit(odone + 8 * x);
-          if (NQ == 1 || x == 1) commit(empty + 8 * sl);
+              mma_ts(d + 128, d + s / 4 * 64 + s % 4 * 8, desc_mn(vv + s * 2048, P::kBlockBytes), idesc(D, true),
+                     s > 0 ? 1u : add);
+            if constexpr (P::kLo)
+#pragma unroll
+              for (int s = 0; s < kTile / 16; ++s)
+                mma_ts(d + 128, d + s / 4 * 64 + 32 + s % 4 * 8, desc_mn(vv + s * 2048, P::kBlockBytes),
+                       idesc(D, true), 1u);
+            commit(odone + 8 * x);
+            if (NQ == 1 || x == 1) commit(empty + 8 * sl);
+          }
+          __syncwarp();
         };
         bar_wait(qfull, segment & 1, up, g.dev_status);
+        __syncwarp();
         const auto tile = [&](int x, int j) { return NQ == 2 ? j : 2 * j + x; };
+#pragma unroll 1
         for (int x = 0; x < 2; ++x)
           if (count[x] > 0) qk(x, tile(x, 0));
         for (int j = 0; j < count[0]; ++j)
+#pragma unroll 1
           for (int x = 0; x < 2; ++x) {
             if (j >= count[x]) continue;
             pv(x, tile(x, j), used[x] + j, j == 0);
@@ -540,7 +572,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(AttendArgs g) {
         const int x = warp / 4, r = tid % kTile, rr = (NQ == 2 ? x * kTile : 0) + r;
         const uint32_t lanes = (uint32_t)(warp % 4 * 32) << 16;
         const uint32_t ts = tmem + lanes + x * 256, to = ts + 128;
-        const float c1 = fabsf(g.c1);
+        const float c1 = fmaxf(fabsf(g.c1), 1.1754944e-38f);   // not 0: -inf c1 is -inf
         const int lim = rr < u.rows ? min(u.end, row_limit(g, u, u.r0 + rr)) : 0;
         const int low = min(u.end, u.low);
         float m = -INFINITY, l = 0.f;
@@ -553,25 +585,38 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(AttendArgs g) {
           tc_after();
           const int bad = s_bad[i & 15];
           const bool mask = t0 + kTile > low || bad;
-          float s[kTile], top = -INFINITY;
+          // Loops over 64 columns, not unrolled: warps that run through thousands of different
+          // instructions wait for those (a third of all stalls when these were unrolled).
+          // a masked logit is -inf
+          const auto logits = [&](int h, float* s) {
+            tmem_ld32(ts + 64 * h, s);
+            tmem_ld32(ts + 64 * h + 32, s + 32);
+            tmem_ld_wait();
+            if (mask) {
+              const int left = lim - t0 - 64 * h;
 #pragma unroll
-          for (int q = 0; q < 4; ++q) tmem_ld32(ts + 32 * q, s + 32 * q);
-          tmem_ld_wait();
-          if (mask) {
+              for (int e = 0; e < 64; ++e)
+                if (e >= left || (bad >> (8 * h + e / 8) & 1)) s[e] = -INFINITY;
+            }
+          };
+          float top = -INFINITY;
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {
+            float s[64];
+            logits(h, s);
+            float t[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-            for (int e = 0; e < kTile; ++e)
-              if (t0 + e >= lim || (bad >> (e / 8) & 1)) s[e] = -INFINITY;
+            for (int e = 4; e < 64; ++e) t[e % 4] = fmaxf(t[e % 4], s[e]);
+            top = fmaxf(top, fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])));
           }
-#pragma unroll
-          for (int e = 0; e < kTile; e += 2) top = fmaxf(fmaxf(s[e], s[e + 1]), top);
-          top = top == -INFINITY ? top : top * c1;     // also where c1 is 0
+          top *= c1;
           const bool raise = top > m + kRaise;
           if (__any_sync(0xffffffffu, raise)) {
             const float nm = raise ? top : m, f = raise ? ex2(m - nm) : 1.f;
             m = nm;
             l *= f;
             if (j > 0) {               // S is complete, so the products before it are too
-#pragma unroll
+#pragma unroll 1
               for (int q = 0; q < D / 16; ++q) {
                 uint32_t o[16];
                 tmem_ld16(to + 16 * q, o);
@@ -584,31 +629,28 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(AttendArgs g) {
           }
           const float ref = m == -INFINITY ? 0.f : m;
           float sum[4] = {0.f, 0.f, 0.f, 0.f};
-          if (mask) {
-            // -inf stays -inf where c1 is 0 or the reference was raised to an infinity
+          // p lies over S, each half's hi and lo over its own columns
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {
+            float s[64];
+            logits(h, s);
 #pragma unroll
-            for (int e = 0; e < kTile; ++e)
-              s[e] = s[e] == -INFINITY ? s[e] : fmaf(s[e], c1, -ref);
-          } else {
+            for (int q = 0; q < 2; ++q) {
+              uint32_t hi[16], lo[16];
 #pragma unroll
-            for (int e = 0; e < kTile; ++e) s[e] = fmaf(s[e], c1, -ref);
-          }
-          // p's columns lie over S's: hi in 0 .. 63, lo in 64 .. 127
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            uint32_t hi[16], lo[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float y0 = ex2(s[32 * q + 2 * e]), y1 = ex2(s[32 * q + 2 * e + 1]);
-              sum[e % 4] += y0;
-              sum[e % 4] += y1;
-              hi[e] = bf16_pair(y0, y1);
-              if constexpr (P::kLo)
-                lo[e] = bf16_pair(y0 - __uint_as_float(hi[e] << 16),
-                                  y1 - __uint_as_float(hi[e] & 0xFFFF0000u));
+              for (int e = 0; e < 16; ++e) {
+                const float y0 = ex2(fmaf(s[32 * q + 2 * e], c1, -ref));
+                const float y1 = ex2(fmaf(s[32 * q + 2 * e + 1], c1, -ref));
+                sum[e % 4] += y0;
+                sum[e % 4] += y1;
+                hi[e] = bf16_pair(y0, y1);
+                if constexpr (P::kLo)
+                  lo[e] = bf16_pair(y0 - __uint_as_float(hi[e] << 16),
+                                    y1 - __uint_as_float(hi[e] & 0xFFFF0000u));
+              }
+              tmem_st16(ts + 64 * h + 16 * q, hi);
+              if constexpr (P::kLo) tmem_st16(ts + 64 * h + 32 + 16 * q, lo);
             }
-            tmem_st16(ts + 16 * q, hi);
-            if constexpr (P::kLo) tmem_st16(ts + 64 + 16 * q, lo);
           }
           l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
           tmem_st_wait();
@@ -629,7 +671,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(AttendArgs g) {
             s_m[r] = m;
             s_l[r] = l;
             if (count[1] > 0)
-#pragma unroll
+#pragma unroll 1
               for (int q = 0; q < D / 32; ++q) {
                 float o[32];
                 tmem_ld32(to + 32 * q, o);
@@ -652,7 +694,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(AttendArgs g) {
             m = nm;
           }
           const float f = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
-#pragma unroll
+#pragma unroll 1
           for (int q = 0; q < D / 32; ++q) {
             float o[32];
             tmem_ld32(to + 32 * q, o);
