@@ -11,12 +11,12 @@
 // and O in TMEM multiplied, only when a logit exceeds it by more than 2^8: rarely after the
 // first tiles. The roles:
 //   warps 0-3, 4-7  softmax of the two streams, and the results
-//   warps 8-10      K and V into a ring of shared-memory slots: asynchronous 16-byte copies into
+//   warps 8-10      (8-14 for 8-bit rows) K and V into a ring of shared-memory slots: asynchronous 16-byte copies into
 //                   the 128-byte swizzle that the matrix descriptors name; rows that do not
 //                   exist become zeros. 8-bit rows are copied some tiles ahead to a ring of
 //                   their own and go from there to the slots as bf16, which holds a code times
 //                   its power-of-two scale exactly
-//   warp 11         issues the matrix instructions
+//   the last warp   issues the matrix instructions
 // Where the tensor cores have time to spare (one row tile: K and V from HBM bound the kernel)
 // and for 8-bit rows, whose values need no rounding, p is kept as two bf16 terms, p = hi + lo,
 // with one product each; else as one (half a step of bf16, 2^-8, in each p).
@@ -32,11 +32,8 @@ namespace nx {
 namespace {
 
 constexpr int kTile = 128;                 // slots of a tile, rows of a stream
-constexpr int kThreads = 12 * 32;         // three warps per scheduler: 168 registers a thread
-constexpr int kLoadWarp = 8, kIssueWarp = 11;
-constexpr int kLoadWarps = 3, kLoaders = 32 * kLoadWarps;
+constexpr int kLoadWarp = 8;
 constexpr int kGroups = kTile / 8;         // runs of 8 slots of a tile
-constexpr int kRuns = (kGroups + kLoadWarps - 1) / kLoadWarps;   // of one loading warp
 constexpr int kTcRows = 256;               // rows of a piece, at most
 constexpr int kTcGrid = kSms;
 constexpr int kPolls = 1 << 20;               // mbarrier polls before giving up
@@ -181,6 +178,11 @@ __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
 
 template <int D, int NQ, bool IMAGE>
 struct Plan {
+  // three warps per scheduler leave 168 registers a thread, four 128: 8-bit rows need the
+  // warps to expand them
+  static constexpr int kLoadWarps = IMAGE ? 7 : 3, kLoaders = 32 * kLoadWarps;
+  static constexpr int kIssueWarp = kLoadWarp + kLoadWarps, kThreads = 32 * (kIssueWarp + 1);
+  static constexpr int kRuns = (kGroups + kLoadWarps - 1) / kLoadWarps;   // of one loading warp
   static constexpr bool kLo = IMAGE || NQ == 1;               // p as two terms
   static constexpr int kBlocks = D / 64;                      // 128-byte columns of a row
   static constexpr int kBlockBytes = kTile * 128;             // of 128 rows
@@ -308,8 +310,11 @@ __device__ __forceinline__ void store_lse(const AttendArgs& g, const AttendUnit&
 }
 
 template <int D, int NQ, bool IMAGE>
-__global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(AttendArgs g) {
+__global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
+    attend_tc_kernel(AttendArgs g) {
   using P = Plan<D, NQ, IMAGE>;
+  constexpr int kLoadWarps = P::kLoadWarps, kLoaders = P::kLoaders, kRuns = P::kRuns;
+  constexpr int kIssueWarp = P::kIssueWarp, kThreads = P::kThreads;
   extern __shared__ char s_raw[];
   __shared__ __align__(8) uint64_t s_bar[P::kBars];
   __shared__ uint32_t s_tmem;
@@ -334,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(AttendArgs g) {
       bar_init(full + 8 * i, kLoaders);
       bar_init(empty + 8 * i, 1);
     }
-    bar_init(qfull, kLoaders);
+    bar_init(qfull, NQ * kTile);
     for (int i = 0; i < 2; ++i) {
       bar_init(sfull + 8 * i, 1);
       bar_init(pfull + 8 * i, kTile);
@@ -370,40 +375,29 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(AttendArgs g) {
         // ---- loader ----
         const int lt = tid - 32 * kLoadWarp, lw = warp - kLoadWarp;
         const TcRows rows(g, u);
-        // the query rows, 128 bytes to a row of a 64-feature block
-        constexpr int kChunks = D / 8;
-#pragma unroll 4
-        for (int i = lt; i < NQ * kTile * kChunks; i += kLoaders) {
-          const int r = i / kChunks, chunk = i % kChunks, row = u.r0 + r, rr = r % kTile;
-          const bool ok = r < u.rows;
-          const int token = row / g.c.group;
-          copy16(s_q + r / kTile * P::kSlotBytes + chunk / 8 * P::kBlockBytes + rr * 128 +
-                     ((chunk ^ rr) & 7) * 16,
-                 static_cast<const __nv_bfloat16*>(g.a.q) +
-                     (ok ? (u.first + token) * g.a.q_stride +
-                               ((long long)u.h * g.c.group + row - token * g.c.group) * D +
-                               chunk * 8
-                         : 0),
-                 ok);
-        }
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        bar_arrive(qfull);
         // K and V tiles in turn, every warp its runs of 8 slots
         const auto announce = [&](int k) {
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           bar_arrive(full + 8 * (k % P::kSlots));
         };
         const auto commit_copies = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
+        // whether any page of the piece is bad; then every K tile gets its marks
+        bool any_bad = false;
+        if (rows.table) {
+          const int t1 = min(u.end, a1 * kTile);
+#pragma unroll 4
+          for (int t = a0 * kTile + 8 * lane; t < t1; t += 256)
+            any_bad |= rows.row(t, u.end, rows.page(t, u.end)) == -1;
+          any_bad = __any_sync(0xffffffffu, any_bad);
+          if (any_bad && lt == 0) atomicOr(g.dev_status, NX_DEV_BAD_PAGE);
+        }
         const auto bad_pages = [&](int i) {       // of tile i of the piece
-          if (lw > 0 || !rows.table) return;
+          if (lw > 0 || !rows.table || !(any_bad || i < 16)) return;
           const int t = (a0 + i) * kTile + 8 * (lane & 15);
           const unsigned marks =
-              __ballot_sync(0xffffffffu, rows.row(t, u.end, rows.page(t, u.end)) == -1) & 0xFFFFu;
-          if (lane == 0) {
-            s_bad[i & 15] = (int)marks;
-            if (marks) atomicOr(g.dev_status, NX_DEV_BAD_PAGE);
-          }
+              any_bad ? __ballot_sync(0xffffffffu, rows.row(t, u.end, rows.page(t, u.end)) == -1)
+                      : 0u;
+          if (lane == 0) s_bad[i & 15] = (int)(marks & 0xFFFFu);
         };
         if constexpr (!IMAGE) {
           // a slot is announced two slots later, when its copies are in
@@ -437,15 +431,18 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(AttendArgs g) {
           const long long blocks0 =
               g.c.page_size ? 0 : image_scale_at(g.c, g.t.layer, u.s, u.h, 0, g.b);
           // codes and scales of tile i / 2 of the piece to raw stage i % kRaw
+          int page[kRuns];             // table entries for the next copy_codes()
+          const auto fetch_pages = [&](int i) {
+            const int t0 = (a0 + i / 2) * kTile, held = i < 2 * n ? min(u.held, u.end) : 0;
+#pragma unroll
+            for (int q = 0; q < kRuns; ++q)
+              page[q] = rows.page(t0 + 8 * (q * kLoadWarps + lw), held);
+          };
           const auto copy_codes = [&](int i) {
             if (i < 2 * n) {
               const int t0 = (a0 + i / 2) * kTile, held = min(u.held, u.end);
               const char* src = static_cast<const char*>(i & 1 ? g.im.v : g.im.k);
               const float* scales = i & 1 ? g.im.v_scale : g.im.k_scale;
-              int page[kRuns];
-#pragma unroll
-              for (int q = 0; q < kRuns; ++q)
-                page[q] = rows.page(t0 + 8 * (q * kLoadWarps + lw), held);
 #pragma unroll 1
               for (int r = 8 * lw; r < kTile && t0 + r < held; r += 8 * kLoadWarps) {
                 const int t = t0 + r;
@@ -471,7 +468,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(AttendArgs g) {
               }
             }
             commit_copies();
+            fetch_pages(i + 1);
           };
+          fetch_pages(0);
           __syncwarp();
 #pragma unroll
           for (int i = 0; i < P::kRaw - 1; ++i) copy_codes(i);
@@ -575,6 +574,26 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(AttendArgs g) {
         const float c1 = fmaxf(fabsf(g.c1), 1.1754944e-38f);   // not 0: -inf c1 is -inf
         const int lim = rr < u.rows ? min(u.end, row_limit(g, u, u.r0 + rr)) : 0;
         const int low = min(u.end, u.low);
+        if (NQ == 2 || x == 0) {       // this thread's query row, 128 bytes of it to a block
+          const int row = u.r0 + rr, token = row / g.c.group;
+          const bool ok = rr < u.rows;
+          const __nv_bfloat16* src =
+              static_cast<const __nv_bfloat16*>(g.a.q) +
+              (ok ? (u.first + token) * g.a.q_stride +
+                        ((long long)u.h * g.c.group + row - token * g.c.group) * D
+                  : 0);
+#pragma unroll 4
+          for (int i = 0; i < D / 8; ++i)
+            copy16(s_q + (NQ == 2 ? x : 0) * P::kSlotBytes + i / 8 * P::kBlockBytes + r * 128 +
+                       ((i ^ r) & 7) * 16,
+                   ok ? src + 8 * i : src, ok);
+          asm volatile("cp.async.wait_all;" ::: "memory");
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          bar_arrive(qfull);
+        }
+        // a warp without rows only keeps the count: what the products make of its rows is
+        // never read
+        const bool idle = (rr & ~31) >= u.rows;
         float m = -INFINITY, l = 0.f;
         for (int j = 0; j < count[x]; ++j) {
           const int i = NQ == 2 ? j : 2 * j + x, t0 = (a0 + i) * kTile;
@@ -582,6 +601,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(AttendArgs g) {
           // complete already (the issuer's commits are in order): keeps the phases in step
           if (j > 0) bar_wait(odone + 8 * x, (used[x] + j - 1) & 1, up, g.dev_status);
           __syncwarp();
+          if (idle) {
+            bar_arrive(pfull + 8 * x);
+            continue;
+          }
           tc_after();
           const int bad = s_bad[i & 15];
           const bool mask = t0 + kTile > low || bad;
@@ -803,7 +826,7 @@ cudaError_t launch_t(AttendArgs& g, cudaStream_t st, int* launches) {
   cudaError_t e = allow_smem<attend_tc_kernel<D, NQ, IMAGE>>(smem);
   if (e != cudaSuccess) return e;
   const int grid = (int)(most < kTcGrid ? most : kTcGrid);
-  e = launch_after(attend_tc_kernel<D, NQ, IMAGE>, dim3(grid), dim3(kThreads), smem, st, g);
+  e = launch_after(attend_tc_kernel<D, NQ, IMAGE>, dim3(grid), dim3(Plan<D, NQ, IMAGE>::kThreads), smem, st, g);
   if (e != cudaSuccess) return e;
   note_launch(st, launches, "attend_tc");
   e = launch_after(attend_tc_join_kernel<D, NQ>, dim3(grid, D / 32), dim3(kTcRows), 0, st, g);
