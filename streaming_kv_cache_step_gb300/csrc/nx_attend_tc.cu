@@ -11,17 +11,20 @@
 // and O in TMEM multiplied, only when a logit exceeds it by more than 2^8: rarely after the
 // first tiles. The roles:
 //   warps 0-3, 4-7  softmax of the two streams, and the results
-//   warps 8-10      (8-14 for 8-bit rows) K and V into a ring of shared-memory slots: asynchronous 16-byte copies into
-//                   the 128-byte swizzle that the matrix descriptors name; rows that do not
-//                   exist become zeros. 8-bit rows are copied some tiles ahead to a ring of
-//                   their own and go from there to the slots as bf16, which holds a code times
-//                   its power-of-two scale exactly
-//   the last warp   issues the matrix instructions
+//   warps 8-9       (8-13 for 8-bit rows) K and V into a ring of shared-memory slots, in the
+//                   128-byte swizzle that the matrix descriptors name: whole tiles by TMA
+//                   boxes (one per page and 64 features), a slice's last tile by asynchronous
+//                   16-byte copies, with zeros for rows that do not exist. 8-bit rows come some
+//                   tiles ahead, by bulk copies, to a ring of their own and go from there to
+//                   the slots as bf16, which holds a code times its power-of-two scale exactly
+//   the last two    issue the matrix instructions, one warp for each stream
 // Where the tensor cores have time to spare (one row tile: K and V from HBM bound the kernel)
 // and for 8-bit rows, whose values need no rounding, p is kept as two bf16 terms, p = hi + lo,
 // with one product each; else as one (half a step of bf16, 2^-8, in each p).
 // Every wait is bounded; when one gives up, the block flags NX_DEV_TIMEOUT, waits for nothing
 // more, issues nothing more and ends, its TMEM freed.
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_fp8.h>
 
 #include <atomic>
@@ -58,6 +61,26 @@ __device__ __forceinline__ bool bar_test(uint32_t bar, uint32_t parity) {
       : "r"(bar), "r"(parity)
       : "memory");
   return ok != 0;
+}
+__device__ __forceinline__ void bar_arrive_tx(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int x, int y,
+                                        uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes,
+                                          uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+          "r"(dst),
+      "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
+      : "memory");
 }
 // Waits for a phase, unless the block has given up already.
 __device__ __forceinline__ void bar_wait(uint32_t bar, uint32_t parity, volatile int* gave_up,
@@ -180,8 +203,8 @@ template <int D, int NQ, bool IMAGE>
 struct Plan {
   // three warps per scheduler leave 168 registers a thread, four 128: 8-bit rows need the
   // warps to expand them
-  static constexpr int kLoadWarps = IMAGE ? 7 : 3, kLoaders = 32 * kLoadWarps;
-  static constexpr int kIssueWarp = kLoadWarp + kLoadWarps, kThreads = 32 * (kIssueWarp + 1);
+  static constexpr int kLoadWarps = IMAGE ? 6 : 2, kLoaders = 32 * kLoadWarps;
+  static constexpr int kIssueWarp = kLoadWarp + kLoadWarps, kThreads = 32 * (kIssueWarp + 2);
   static constexpr int kRuns = (kGroups + kLoadWarps - 1) / kLoadWarps;   // of one loading warp
   static constexpr bool kLo = IMAGE || NQ == 1;               // p as two terms
   static constexpr int kBlocks = D / 64;                      // 128-byte columns of a row
@@ -190,7 +213,7 @@ struct Plan {
   static constexpr int kRawBytes = kTile * D;                 // its codes
   static constexpr int kSlots = IMAGE ? 4 : NQ == 2 ? 5 : 6;
   static constexpr int kRaw = IMAGE ? (NQ == 2 ? 2 : 4) : 0;
-  static constexpr int kBars = 2 * kSlots + 1 + 3 * 2;
+  static constexpr int kBars = 2 * kSlots + 1 + 3 * 2 + 2 * kRaw;
   static constexpr int kSmem = 1024 + (NQ + kSlots) * kSlotBytes + kRaw * kRawBytes;
 };
 
@@ -254,10 +277,11 @@ __device__ __forceinline__ void copy_group(const char* src, long long row, int t
   }
 }
 
-// 8 rows of codes in shared memory, times their scale, to rows r .. r + 7 of a ring slot.
+// `some` (at most 8) rows of codes in shared memory, times their scale, and zeros behind them
+// to rows r .. r + 7 of a ring slot.
 template <int D>
-__device__ __forceinline__ void expand_group(uint32_t raw, float scale, uint32_t slot, int r,
-                                             int lane) {
+__device__ __forceinline__ void expand_group(uint32_t raw, float scale, int some, uint32_t slot,
+                                             int r, int lane) {
   constexpr int kChunks = D / 8, kLine = 32 / kChunks;
   const int chunk = lane % kChunks, sub = lane / kChunks;
   const uint32_t dst = slot + chunk / 8 * (kTile * 128) + (r + sub) * 128;
@@ -268,6 +292,11 @@ __device__ __forceinline__ void expand_group(uint32_t raw, float scale, uint32_t
                  : "=r"(x[i][0]), "=r"(x[i][1])
                  : "r"(raw + i * kLine * D + lane * 8)
                  : "memory");
+  if (some < 8) {
+#pragma unroll
+    for (int i = 0; i < 8 / kLine; ++i)
+      if (i * kLine + sub >= some) x[i][0] = x[i][1] = 0;
+  }
 #pragma unroll
   for (int i = 0; i < 8 / kLine; ++i) {
     uint32_t y[4];
@@ -311,7 +340,8 @@ __device__ __forceinline__ void store_lse(const AttendArgs& g, const AttendUnit&
 
 template <int D, int NQ, bool IMAGE>
 __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
-    attend_tc_kernel(AttendArgs g) {
+    attend_tc_kernel(const __grid_constant__ CUtensorMap map_k,
+                     const __grid_constant__ CUtensorMap map_v, bool use_maps, AttendArgs g) {
   using P = Plan<D, NQ, IMAGE>;
   constexpr int kLoadWarps = P::kLoadWarps, kLoaders = P::kLoaders, kRuns = P::kRuns;
   constexpr int kIssueWarp = P::kIssueWarp, kThreads = P::kThreads;
@@ -320,7 +350,6 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
   __shared__ uint32_t s_tmem;
   __shared__ int s_up, s_bad[16];                   // bad-page marks of tile % 16
   __shared__ float s_m[kTile], s_l[kTile];
-  __shared__ float s_scale[IMAGE ? P::kRaw : 1][kGroups];
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, b = blockIdx.x;
   char* base = s_raw + (1024 - (smem_at(s_raw) & 1023)) % 1024;
   const uint32_t s_q = smem_at(base), s_ring = s_q + NQ * P::kSlotBytes;
@@ -328,6 +357,7 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
   const uint32_t bars = smem_at(s_bar);
   const uint32_t full = bars, empty = bars + 8 * P::kSlots, qfull = empty + 8 * P::kSlots;
   const uint32_t sfull = qfull + 8, pfull = sfull + 16, odone = pfull + 16;
+  const uint32_t rfull = odone + 16, rempty = rfull + 8 * P::kRaw;    // of the raw ring
   if (warp == kIssueWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_at(&s_tmem)),
@@ -337,7 +367,11 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < P::kSlots; ++i) {
       bar_init(full + 8 * i, kLoaders);
-      bar_init(empty + 8 * i, 1);
+      bar_init(empty + 8 * i, NQ);                 // its users are done
+    }
+    for (int i = 0; i < P::kRaw; ++i) {
+      bar_init(rfull + 8 * i, 1);
+      bar_init(rempty + 8 * i, kLoadWarps);
     }
     bar_init(qfull, NQ * kTile);
     for (int i = 0; i < 2; ++i) {
@@ -347,7 +381,6 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     s_up = 0;
-    for (int i = 0; i < 16; ++i) s_bad[i] = 0;       // the loader's, where there are pages
   }
   grid_dep_wait();
   tc_before();
@@ -360,6 +393,7 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
   const int stop = min(sh.total, sh.start + sh.per);
   int2 desc = make_int2(-1, 0);
   int slot_no = 0;                     // ring slots filled or used so far (loader, issuer)
+  int raw_no = 0;                      // raw stages filled so far
   int segment = 0;                     // pieces done
   int used[2] = {0, 0};                // slot tiles done by each stream
   volatile int* up = &s_up;
@@ -380,7 +414,6 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           bar_arrive(full + 8 * (k % P::kSlots));
         };
-        const auto commit_copies = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
         // whether any page of the piece is bad; then every K tile gets its marks
         bool any_bad = false;
         if (rows.table) {
@@ -391,95 +424,146 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
           any_bad = __any_sync(0xffffffffu, any_bad);
           if (any_bad && lt == 0) atomicOr(g.dev_status, NX_DEV_BAD_PAGE);
         }
+        if (lw == 0 && lane < 16) s_bad[lane] = 0;
         const auto bad_pages = [&](int i) {       // of tile i of the piece
-          if (lw > 0 || !rows.table || !(any_bad || i < 16)) return;
+          if (lw > 0 || !any_bad) return;
           const int t = (a0 + i) * kTile + 8 * (lane & 15);
           const unsigned marks =
-              any_bad ? __ballot_sync(0xffffffffu, rows.row(t, u.end, rows.page(t, u.end)) == -1)
-                      : 0u;
+              __ballot_sync(0xffffffffu, rows.row(t, u.end, rows.page(t, u.end)) == -1);
           if (lane == 0) s_bad[i & 15] = (int)(marks & 0xFFFFu);
         };
-        if constexpr (!IMAGE) {
-          // a slot is announced two slots later, when its copies are in
-          for (int i = 0; i < 2 * n; ++i) {
-            const int k = slot_no + i, sl = k % P::kSlots, t0 = (a0 + i / 2) * kTile;
-            const char* src = static_cast<const char*>(i & 1 ? g.c.v : g.c.k);
-            int page[kRuns];
+        // bf16 rows of slot i into ring slot sl, by 16-byte copies
+        const auto copy_tile = [&](int i, int sl) {
+          const int t0 = (a0 + i / 2) * kTile;
+          const char* src = static_cast<const char*>(i & 1 ? g.c.v : g.c.k);
+          int page[kRuns];
 #pragma unroll
-            for (int q = 0; q < kRuns; ++q)
-              page[q] = rows.page(t0 + 8 * (q * kLoadWarps + lw), u.end);
+          for (int q = 0; q < kRuns; ++q)
+            page[q] = rows.page(t0 + 8 * (q * kLoadWarps + lw), u.end);
+#pragma unroll 1
+          for (int r = 8 * lw; r < kTile; r += 8 * kLoadWarps) {
+            copy_group<D>(src, rows.row(t0 + r, u.end, page[0]), t0 + r, u.end,
+                          s_ring + sl * P::kSlotBytes, r, lane);
+#pragma unroll
+            for (int q = 0; q + 1 < kRuns; ++q) page[q] = page[q + 1];
+          }
+          asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        // slots of a TMA box or bulk copy
+        const int box = g.c.page_size ? min(kTile, 1 << rows.shift) : kTile;
+        if constexpr (!IMAGE) {
+          // whole tiles: one warp issues their boxes
+          const int whole = use_maps && !any_bad ? max(0, min(n, u.end / kTile - a0)) : 0;
+          const int boxes = kTile / box * P::kBlocks;
+          int y = 0;
+          for (int i = 0; i < 2 * whole; ++i) {
+            const int k = slot_no + i, sl = k % P::kSlots, t0 = (a0 + i / 2) * kTile;
+            const int t = t0 + lane / P::kBlocks * box;
+            if (lw == 0 && !(i & 1) && lane < boxes)
+              y = (int)rows.row(t, u.end, rows.page(t, u.end));
+            bar_wait(empty + 8 * sl, (k / P::kSlots & 1) ^ 1, up, g.dev_status);
+            __syncwarp();
+            if (lw == 0 && *up == 0) {
+              if (lane == 0) bar_arrive_tx(full + 8 * sl, P::kSlotBytes);
+              __syncwarp();
+              if (lane < boxes) {
+                const int blk = lane % P::kBlocks;
+                tma_box(s_ring + sl * P::kSlotBytes + blk * P::kBlockBytes + (t - t0) * 128,
+                        i & 1 ? &map_v : &map_k, 64 * blk, y, full + 8 * sl);
+              }
+              if (lane > 0) bar_arrive(full + 8 * sl);
+            } else {
+              bar_arrive(full + 8 * sl);
+            }
+          }
+          // the others: a slot is announced two slots later, when its copies are in
+          for (int i = 2 * whole; i < 2 * n; ++i) {
+            const int k = slot_no + i, sl = k % P::kSlots;
             if (!(i & 1)) bad_pages(i / 2);
             bar_wait(empty + 8 * sl, (k / P::kSlots & 1) ^ 1, up, g.dev_status);
             __syncwarp();
-#pragma unroll 1
-            for (int r = 8 * lw; r < kTile; r += 8 * kLoadWarps) {
-              copy_group<D>(src, rows.row(t0 + r, u.end, page[0]), t0 + r, u.end,
-                            s_ring + sl * P::kSlotBytes, r, lane);
-#pragma unroll
-              for (int q = 0; q + 1 < kRuns; ++q) page[q] = page[q + 1];
-            }
-            commit_copies();
-            if (i >= 2) {
+            copy_tile(i, sl);
+            if (i >= 2 * whole + 2) {
               asm volatile("cp.async.wait_group 2;" ::: "memory");
               announce(k - 2);
             }
           }
           asm volatile("cp.async.wait_group 0;" ::: "memory");
-          announce(slot_no + 2 * n - 2);
-          announce(slot_no + 2 * n - 1);
+          if (n > whole) {
+            announce(slot_no + 2 * n - 2);
+            announce(slot_no + 2 * n - 1);
+          }
         } else {
+          const int held = min(u.held, u.end);
           const long long blocks0 =
               g.c.page_size ? 0 : image_scale_at(g.c, g.t.layer, u.s, u.h, 0, g.b);
-          // codes and scales of tile i / 2 of the piece to raw stage i % kRaw
-          int page[kRuns];             // table entries for the next copy_codes()
-          const auto fetch_pages = [&](int i) {
-            const int t0 = (a0 + i / 2) * kTile, held = i < 2 * n ? min(u.held, u.end) : 0;
-#pragma unroll
-            for (int q = 0; q < kRuns; ++q)
-              page[q] = rows.page(t0 + 8 * (q * kLoadWarps + lw), held);
+          // lane q of every warp looks after run q of a tile: its page (fetched a tile ahead),
+          // row and scale (a slot ahead)
+          const auto page_of = [&](int i) {
+            return lane < kGroups ? rows.page((a0 + i / 2) * kTile + 8 * lane,
+                                              i < 2 * n ? held : 0)
+                                  : 0;
           };
-          const auto copy_codes = [&](int i) {
-            if (i < 2 * n) {
-              const int t0 = (a0 + i / 2) * kTile, held = min(u.held, u.end);
-              const char* src = static_cast<const char*>(i & 1 ? g.im.v : g.im.k);
-              const float* scales = i & 1 ? g.im.v_scale : g.im.k_scale;
+          const auto row_of_run = [&](int i, int page) {
+            return lane < kGroups && i < 2 * n
+                       ? rows.row((a0 + i / 2) * kTile + 8 * lane, held, page)
+                       : -2;
+          };
+          const auto scale_of = [&](int i, long long row) {
+            if (row < 0) return 0.f;
+            const int t = (a0 + i / 2) * kTile + 8 * lane;
+            return (i & 1 ? g.im.v_scale : g.im.k_scale)[
+                g.c.page_size ? row >> g.b_shift : blocks0 + (t >> g.b_shift)];
+          };
+          // codes of slot i to raw stage (raw_no + i) % kRaw: the first warp's lanes with the
+          // first run of a page (or the tile) copy all of its rows
+          const auto copy_codes = [&](int i, long long row) {
+            if (lw > 0 || i >= 2 * n || *up) return;
+            const int no = raw_no + i, st = no % P::kRaw, t0 = (a0 + i / 2) * kTile;
+            bar_wait(rempty + 8 * st, (no / P::kRaw & 1) ^ 1, up, g.dev_status);
+            __syncwarp();
+            const int t = t0 + 8 * lane;
+            const bool lead = row >= 0 && (t - t0) % box == 0;
+            const int bytes = lead ? (min(held, t + box) - t) * D : 0;
+            const unsigned total = __reduce_add_sync(0xffffffffu, (unsigned)bytes);
+            if (lane == 0) bar_arrive_tx(rfull + 8 * st, total);
+            __syncwarp();
+            if (lead)
+              bulk_copy(s_codes + st * P::kRawBytes + (t - t0) * D,
+                        static_cast<const char*>(i & 1 ? g.im.v : g.im.k) + row * D, bytes,
+                        rfull + 8 * st);
+          };
+          int page = page_of(0);
+          long long row = row_of_run(0, page);                  // of tile i / 2
+          int page1 = page_of(2);                               // of the next tile
+          long long row_ahead = row;                            // of the slot copied next
+          int page_ahead = page1;
 #pragma unroll 1
-              for (int r = 8 * lw; r < kTile && t0 + r < held; r += 8 * kLoadWarps) {
-                const int t = t0 + r;
-                const long long row = rows.row(t, held, page[0]);
-#pragma unroll
-                for (int q = 0; q + 1 < kRuns; ++q) page[q] = page[q + 1];
-                const uint32_t dst = s_codes + i % P::kRaw * P::kRawBytes + r * D + lane * 16;
-#pragma unroll
-                for (int y = 0; y < 8 * D; y += 512) {
-                  // a run that the image's last rows cut has zeros behind them
-                  const int rest = (min(held, t + 8) - t) * D - y - lane * 16;
-                  const bool ok = row >= 0 && rest > 0;
-                  copy16(dst + y, ok ? src + row * D + y + lane * 16 : src, ok);
-                }
-                if (lane == 0) {
-                  const long long at =
-                      g.c.page_size ? row >> g.b_shift : blocks0 + (t >> g.b_shift);
-                  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(
-                                   smem_at(&s_scale[i % P::kRaw][r / 8])),
-                               "l"(scales + (row < 0 ? 0 : at)), "r"(row < 0 ? 0 : 4)
-                               : "memory");
-                }
-              }
+          for (int i = 0; i < P::kRaw - 1; ++i) {
+            if (i > 0 && !(i & 1)) {
+              row_ahead = row_of_run(i, page_ahead);
+              page_ahead = page_of(i + 2);
             }
-            commit_copies();
-            fetch_pages(i + 1);
-          };
-          fetch_pages(0);
-          __syncwarp();
-#pragma unroll
-          for (int i = 0; i < P::kRaw - 1; ++i) copy_codes(i);
+            copy_codes(i, row_ahead);
+          }
+          float scale = scale_of(0, row);
+#pragma unroll 1
           for (int i = 0; i < 2 * n; ++i) {
             const int k = slot_no + i, sl = k % P::kSlots, t0 = (a0 + i / 2) * kTile;
+            const int no = raw_no + i, st = no % P::kRaw, ahead = i + P::kRaw - 1;
             if (!(i & 1)) bad_pages(i / 2);
-            asm volatile("cp.async.wait_group %0;" ::"n"(P::kRaw - 2) : "memory");
-            __syncwarp();              // this warp's codes are in, and stage i - 1 is read
-            copy_codes(i + P::kRaw - 1);
+            if (!(ahead & 1)) {
+              row_ahead = row_of_run(ahead, page_ahead);
+              page_ahead = page_of(ahead + 2);
+            }
+            copy_codes(ahead, row_ahead);
+            long long row1 = row;                               // of slot i + 1
+            if (i & 1) {
+              row1 = row_of_run(i + 1, page1);
+              page1 = page_of(i + 3);
+            }
+            const float scale1 = scale_of(i + 1, row1);
+            bar_wait(rfull + 8 * st, no / P::kRaw & 1, up, g.dev_status);
             bar_wait(empty + 8 * sl, (k / P::kSlots & 1) ^ 1, up, g.dev_status);
             __syncwarp();
             const uint32_t slot = s_ring + sl * P::kSlotBytes;
@@ -487,27 +571,32 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
 #pragma unroll 1
             for (int q = lw; q < kGroups; q += kLoadWarps) {
               const int r = 8 * q, t = t0 + r;
-              if (t < u.held && t < u.end) {
-                // behind u.end, within the run: zeros (codes), as for rows that do not exist
-                expand_group<D>(s_codes + i % P::kRaw * P::kRawBytes + r * D,
-                                s_scale[i % P::kRaw][q], slot, r, lane);
+              const float sc = __shfl_sync(0xffffffffu, scale, q);
+              if (t < held) {
+                const bool good = __shfl_sync(0xffffffffu, row >= 0 ? 1 : 0, q) != 0;
+                expand_group<D>(s_codes + st * P::kRawBytes + r * D, sc, good ? held - t : 0, slot,
+                                r, lane);
               } else {
-                const char* src = static_cast<const char*>(i & 1 ? g.c.v : g.c.k);
-                copy_group<D>(src, rows.row(t, u.end, rows.page(t, u.end)), t, u.end, slot, r,
-                              lane);
+                copy_group<D>(static_cast<const char*>(i & 1 ? g.c.v : g.c.k),
+                              rows.row(t, u.end, rows.page(t, u.end)), t, u.end, slot, r, lane);
                 rest = true;
               }
             }
             if (rest) asm volatile("cp.async.wait_all;" ::: "memory");
             announce(k);
+            __syncwarp();
+            if (lane == 0) bar_arrive(rempty + 8 * st);
+            row = row1;
+            scale = scale1;
           }
         }
-      } else if (warp == kIssueWarp) {
+      } else if (warp >= kIssueWarp) {
         // ---- matrix instructions: the whole warp goes along, one lane issues ----
+        const int x = (int)warp_value(warp - kIssueWarp);   // the stream
         const uint32_t negate = g.c1 < 0.f ? kNegate : 0u;   // the softmax scales by |c1|
         const uint32_t tm = warp_value(tmem);
         int k_no = (int)warp_value(slot_no);
-        const auto qk = [&](int x, int i) {          // tile i of the piece, for stream x
+        const auto qk = [&](int i) {                 // tile i of the piece
           const int k = k_no + 2 * i, sl = k % P::kSlots;
           bar_wait(full + 8 * sl, k / P::kSlots & 1, up, g.dev_status);
           __syncwarp();
@@ -524,11 +613,11 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
               mma_ss(d, desc_k(q + o), desc_k(kk + o), id, s > 0);
             }
             commit(sfull + 8 * x);
-            if (NQ == 1 || x == 1) commit(empty + 8 * sl);
+            commit(empty + 8 * sl);
           }
           __syncwarp();
         };
-        const auto pv = [&](int x, int i, int turn, bool first) {
+        const auto pv = [&](int i, int turn, bool first) {
           const int k = k_no + 2 * i + 1, sl = k % P::kSlots;
           bar_wait(full + 8 * sl, k / P::kSlots & 1, up, g.dev_status);
           bar_wait(pfull + 8 * x, turn & 1, up, g.dev_status);
@@ -549,23 +638,20 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
                 mma_ts(d + 128, d + s / 4 * 64 + 32 + s % 4 * 8, desc_mn(vv + s * 2048, P::kBlockBytes),
                        idesc(D, true), 1u);
             commit(odone + 8 * x);
-            if (NQ == 1 || x == 1) commit(empty + 8 * sl);
+            commit(empty + 8 * sl);
           }
           __syncwarp();
         };
         bar_wait(qfull, segment & 1, up, g.dev_status);
         __syncwarp();
-        const auto tile = [&](int x, int j) { return NQ == 2 ? j : 2 * j + x; };
+        const auto tile = [&](int j) { return NQ == 2 ? j : 2 * j + x; };
+        const int mine = count[x];
+        if (mine > 0) qk(tile(0));
 #pragma unroll 1
-        for (int x = 0; x < 2; ++x)
-          if (count[x] > 0) qk(x, tile(x, 0));
-        for (int j = 0; j < count[0]; ++j)
-#pragma unroll 1
-          for (int x = 0; x < 2; ++x) {
-            if (j >= count[x]) continue;
-            pv(x, tile(x, j), used[x] + j, j == 0);
-            if (j + 1 < count[x]) qk(x, tile(x, j + 1));
-          }
+        for (int j = 0; j < mine; ++j) {
+          pv(tile(j), used[x] + j, j == 0);
+          if (j + 1 < mine) qk(tile(j + 1));
+        }
       } else if (warp < 8) {
         // ---- softmax ----
         const int x = warp / 4, r = tid % kTile, rr = (NQ == 2 ? x * kTile : 0) + r;
@@ -747,6 +833,7 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
         tc_before();
       }
       slot_no += 2 * n;
+      raw_no += 2 * n;
       used[0] += count[0];
       used[1] += count[1];
       ++segment;
@@ -762,6 +849,9 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
   }
   if (tid == 0) g.ws.desc[b] = desc;
   asm volatile("cp.async.wait_all;" ::: "memory");
+  // after giving up, bulk copies may be under way that nobody waited for: a millisecond's grace
+  if (*up)
+    for (int i = 0; i < 1000; ++i) __nanosleep(1000);
   tc_before();
   __syncthreads();
   if (warp == kIssueWarp) {
@@ -802,7 +892,7 @@ __global__ void __launch_bounds__(kTcRows) attend_tc_join_kernel(AttendArgs g) {
 }
 
 // Lets a kernel use so much dynamic shared memory, once per device (twice does no harm).
-template <void (*kernel)(AttendArgs)>
+template <void (*kernel)(CUtensorMap, CUtensorMap, bool, AttendArgs)>
 cudaError_t allow_smem(int bytes) {
   static std::atomic<bool> done[64];
   int dev = 0;
@@ -812,6 +902,31 @@ cudaError_t allow_smem(int bytes) {
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev].store(true, std::memory_order_release);
   return e;
+}
+
+// Rows of head_dim bf16 values in boxes of 64 features x a page (or a tile); false if the
+// driver does not take it or the rows do not fit its 32-bit coordinates.
+bool encode_rows(const nx_cache& c, void* base, CUtensorMap* map) {
+  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    return cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                            &q) == cudaSuccess &&
+                   q == cudaDriverEntryPointSuccess
+               ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p)
+               : nullptr;
+  }();
+  const long long rows = (long long)c.layers * c.kv_heads *
+                         (c.page_size ? (long long)c.num_pages * c.page_size
+                                      : (long long)c.seqs * c.capacity);
+  if (!fn || rows >= (1LL << 31)) return false;
+  const cuuint64_t dim[2] = {(cuuint64_t)c.head_dim, (cuuint64_t)rows};
+  const cuuint64_t stride[1] = {(cuuint64_t)c.head_dim * 2};
+  const cuuint32_t box[2] = {64, (cuuint32_t)(c.page_size ? c.page_size : kTile)};
+  const cuuint32_t one[2] = {1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dim, stride, box, one,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int D, int NQ, bool IMAGE>
@@ -826,7 +941,10 @@ cudaError_t launch_t(AttendArgs& g, cudaStream_t st, int* launches) {
   cudaError_t e = allow_smem<attend_tc_kernel<D, NQ, IMAGE>>(smem);
   if (e != cudaSuccess) return e;
   const int grid = (int)(most < kTcGrid ? most : kTcGrid);
-  e = launch_after(attend_tc_kernel<D, NQ, IMAGE>, dim3(grid), dim3(Plan<D, NQ, IMAGE>::kThreads), smem, st, g);
+  CUtensorMap map_k{}, map_v{};
+  const bool maps = !IMAGE && encode_rows(g.c, g.c.k, &map_k) && encode_rows(g.c, g.c.v, &map_v);
+  e = launch_after(attend_tc_kernel<D, NQ, IMAGE>, dim3(grid),
+                   dim3(Plan<D, NQ, IMAGE>::kThreads), smem, st, map_k, map_v, maps, g);
   if (e != cudaSuccess) return e;
   note_launch(st, launches, "attend_tc");
   e = launch_after(attend_tc_join_kernel<D, NQ>, dim3(grid, D / 32), dim3(kTcRows), 0, st, g);
