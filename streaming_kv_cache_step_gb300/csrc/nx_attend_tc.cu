@@ -2,12 +2,13 @@
 // several tokens): the same softmax as nx_attend.cu on the 5th-generation tensor cores.
 //
 // A thread block holds two streams of 128 query rows (thread = row): two row tiles that share
-// each tile of 128 slots of K and V, or, for slices with up to 128 rows, one row tile whose
+// each tile of 64 slots of K and V, or, for slices with up to 128 rows, one row tile whose
 // even and odd slot tiles are the two streams. Per slot tile and stream:
-//   S = Q K^T      tcgen05.mma, 128 x 128 x head_dim, Q and K in shared memory, S in TMEM
+//   S = Q K^T      tcgen05.mma, 128 x 64 x head_dim, Q and K in shared memory, S in TMEM
 //   p = 2^(c1 S - m), bf16, over S's own columns of TMEM; l += sum p
 //   O += p V       tcgen05.mma, p from TMEM, V in shared memory (features contiguous), O in TMEM
-// While one stream's warps take their exponentials the other's matrices multiply. m is raised,
+// A stream has two S buffers: its next logits are on their way while its warps take the
+// exponentials of these, and the other stream's products run meanwhile. m is raised,
 // and O in TMEM multiplied, only when a logit exceeds it by more than 2^8: rarely after the
 // first tiles. The roles:
 //   warps 0-3, 4-7  softmax of the two streams, and the results
@@ -34,9 +35,10 @@
 namespace nx {
 namespace {
 
-constexpr int kTile = 128;                 // slots of a tile, rows of a stream
+constexpr int kRows = 128;                 // query rows of a stream
+constexpr int kCols = 64;                  // slots of a tile
 constexpr int kLoadWarp = 8;
-constexpr int kGroups = kTile / 8;         // runs of 8 slots of a tile
+constexpr int kGroups = kCols / 8;         // runs of 8 slots of a tile
 constexpr int kTcRows = 256;               // rows of a piece, at most
 constexpr int kTcGrid = kSms;
 constexpr int kPolls = 1 << 20;               // mbarrier polls before giving up
@@ -208,19 +210,19 @@ struct Plan {
   static constexpr int kRuns = (kGroups + kLoadWarps - 1) / kLoadWarps;   // of one loading warp
   static constexpr bool kLo = IMAGE || NQ == 1;               // p as two terms
   static constexpr int kBlocks = D / 64;                      // 128-byte columns of a row
-  static constexpr int kBlockBytes = kTile * 128;             // of 128 rows
-  static constexpr int kSlotBytes = kBlocks * kBlockBytes;    // one K or V tile, one Q tile
-  static constexpr int kRawBytes = kTile * D;                 // its codes
-  static constexpr int kSlots = IMAGE ? 4 : NQ == 2 ? 5 : 6;
-  static constexpr int kRaw = IMAGE ? (NQ == 2 ? 2 : 4) : 0;
-  static constexpr int kBars = 2 * kSlots + 1 + 3 * 2 + 2 * kRaw;
-  static constexpr int kSmem = 1024 + (NQ + kSlots) * kSlotBytes + kRaw * kRawBytes;
+  static constexpr int kRowBlock = kRows * 128, kColBlock = kCols * 128;   // of a Q, K or V tile
+  static constexpr int kQBytes = kBlocks * kRowBlock, kSlotBytes = kBlocks * kColBlock;
+  static constexpr int kRawBytes = kCols * D;                 // codes of a K or V tile
+  static constexpr int kSlots = IMAGE ? 8 : NQ == 2 ? 10 : 12;
+  static constexpr int kRaw = IMAGE ? (NQ == 2 ? 4 : 8) : 0;
+  static constexpr int kBars = 2 * kSlots + 1 + 3 * 4 + 2 * kRaw;
+  static constexpr int kSmem = 1024 + NQ * kQBytes + kSlots * kSlotBytes + kRaw * kRawBytes;
 };
 
-// Units of this kernel: 128 NQ rows, tiles of 128 slots.
+// Units of this kernel: 128 NQ rows, tiles of 64 slots.
 template <int NQ>
 __device__ __forceinline__ int tc_tiles(const AttendUnit& u) {
-  return !u.rows ? 0 : u.end ? (u.end + kTile - 1) / kTile : 1;
+  return !u.rows ? 0 : u.end ? (u.end + kCols - 1) / kCols : 1;
 }
 
 // Rows of 8-slot groups of a unit, as in a page table.
@@ -269,7 +271,7 @@ __device__ __forceinline__ void copy_group(const char* src, long long row, int t
   constexpr int kChunks = D / 8, kLine = 32 / kChunks;     // 16-byte chunks; rows per step
   const int chunk = lane % kChunks, sub = lane / kChunks;
   const char* p = src + (row < 0 ? 0 : row * (D * 2)) + lane * 16;
-  const uint32_t dst = slot + chunk / 8 * (kTile * 128) + (r + sub) * 128;
+  const uint32_t dst = slot + chunk / 8 * (kCols * 128) + (r + sub) * 128;
 #pragma unroll
   for (int i = 0; i < 8; i += kLine) {
     const bool ok = row >= 0 && t + i + sub < end;
@@ -284,7 +286,7 @@ __device__ __forceinline__ void expand_group(uint32_t raw, float scale, int some
                                              int r, int lane) {
   constexpr int kChunks = D / 8, kLine = 32 / kChunks;
   const int chunk = lane % kChunks, sub = lane / kChunks;
-  const uint32_t dst = slot + chunk / 8 * (kTile * 128) + (r + sub) * 128;
+  const uint32_t dst = slot + chunk / 8 * (kCols * 128) + (r + sub) * 128;
   uint32_t x[8 / kLine][2];
 #pragma unroll
   for (int i = 0; i < 8 / kLine; ++i)
@@ -349,15 +351,16 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
   __shared__ __align__(8) uint64_t s_bar[P::kBars];
   __shared__ uint32_t s_tmem;
   __shared__ int s_up, s_bad[16];                   // bad-page marks of tile % 16
-  __shared__ float s_m[kTile], s_l[kTile];
+  __shared__ float s_m[kRows], s_l[kRows];
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, b = blockIdx.x;
   char* base = s_raw + (1024 - (smem_at(s_raw) & 1023)) % 1024;
-  const uint32_t s_q = smem_at(base), s_ring = s_q + NQ * P::kSlotBytes;
+  const uint32_t s_q = smem_at(base), s_ring = s_q + NQ * P::kQBytes;
   const uint32_t s_codes = s_ring + P::kSlots * P::kSlotBytes;
   const uint32_t bars = smem_at(s_bar);
   const uint32_t full = bars, empty = bars + 8 * P::kSlots, qfull = empty + 8 * P::kSlots;
-  const uint32_t sfull = qfull + 8, pfull = sfull + 16, odone = pfull + 16;
-  const uint32_t rfull = odone + 16, rempty = rfull + 8 * P::kRaw;    // of the raw ring
+  // per stream and TMEM buffer: logits there, probabilities there, their product done
+  const uint32_t sfull = qfull + 8, pfull = sfull + 32, odone = pfull + 32;
+  const uint32_t rfull = odone + 32, rempty = rfull + 8 * P::kRaw;    // of the raw ring
   if (warp == kIssueWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_at(&s_tmem)),
@@ -373,10 +376,10 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
       bar_init(rfull + 8 * i, 1);
       bar_init(rempty + 8 * i, kLoadWarps);
     }
-    bar_init(qfull, NQ * kTile);
-    for (int i = 0; i < 2; ++i) {
+    bar_init(qfull, NQ * kRows);
+    for (int i = 0; i < 4; ++i) {
       bar_init(sfull + 8 * i, 1);
-      bar_init(pfull + 8 * i, kTile);
+      bar_init(pfull + 8 * i, kRows);
       bar_init(odone + 8 * i, 1);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -385,7 +388,7 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
   grid_dep_wait();
   tc_before();
   const AttendShare sh = attend_share<kThreads>(
-      g, [&](int i) { return tc_tiles<NQ>(attend_unit<kTile * NQ>(g, i)); });
+      g, [&](int i) { return tc_tiles<NQ>(attend_unit<kRows * NQ>(g, i)); });
   tc_after();
   grid_dep_trigger();
   const uint32_t tmem = s_tmem;
@@ -399,7 +402,7 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
   volatile int* up = &s_up;
 
   while (pos < stop) {
-    const AttendUnit u = attend_unit<kTile * NQ>(g, unit);
+    const AttendUnit u = attend_unit<kRows * NQ>(g, unit);
     const int tiles = tc_tiles<NQ>(u);
     const int a0 = pos - at, a1 = min(tiles, stop - at), n = a1 - a0;
     if (tiles > 0) {
@@ -417,9 +420,9 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
         // whether any page of the piece is bad; then every K tile gets its marks
         bool any_bad = false;
         if (rows.table) {
-          const int t1 = min(u.end, a1 * kTile);
+          const int t1 = min(u.end, a1 * kCols);
 #pragma unroll 4
-          for (int t = a0 * kTile + 8 * lane; t < t1; t += 256)
+          for (int t = a0 * kCols + 8 * lane; t < t1; t += 256)
             any_bad |= rows.row(t, u.end, rows.page(t, u.end)) == -1;
           any_bad = __any_sync(0xffffffffu, any_bad);
           if (any_bad && lt == 0) atomicOr(g.dev_status, NX_DEV_BAD_PAGE);
@@ -427,21 +430,21 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
         if (lw == 0 && lane < 16) s_bad[lane] = 0;
         const auto bad_pages = [&](int i) {       // of tile i of the piece
           if (lw > 0 || !any_bad) return;
-          const int t = (a0 + i) * kTile + 8 * (lane & 15);
+          const int t = (a0 + i) * kCols + 8 * (lane & 7);
           const unsigned marks =
               __ballot_sync(0xffffffffu, rows.row(t, u.end, rows.page(t, u.end)) == -1);
-          if (lane == 0) s_bad[i & 15] = (int)(marks & 0xFFFFu);
+          if (lane == 0) s_bad[i & 15] = (int)(marks & 0xFFu);
         };
         // bf16 rows of slot i into ring slot sl, by 16-byte copies
         const auto copy_tile = [&](int i, int sl) {
-          const int t0 = (a0 + i / 2) * kTile;
+          const int t0 = (a0 + i / 2) * kCols;
           const char* src = static_cast<const char*>(i & 1 ? g.c.v : g.c.k);
           int page[kRuns];
 #pragma unroll
           for (int q = 0; q < kRuns; ++q)
             page[q] = rows.page(t0 + 8 * (q * kLoadWarps + lw), u.end);
 #pragma unroll 1
-          for (int r = 8 * lw; r < kTile; r += 8 * kLoadWarps) {
+          for (int r = 8 * lw; r < kCols; r += 8 * kLoadWarps) {
             copy_group<D>(src, rows.row(t0 + r, u.end, page[0]), t0 + r, u.end,
                           s_ring + sl * P::kSlotBytes, r, lane);
 #pragma unroll
@@ -450,14 +453,14 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
           asm volatile("cp.async.commit_group;" ::: "memory");
         };
         // slots of a TMA box or bulk copy
-        const int box = g.c.page_size ? min(kTile, 1 << rows.shift) : kTile;
+        const int box = g.c.page_size ? min(kCols, 1 << rows.shift) : kCols;
         if constexpr (!IMAGE) {
           // whole tiles: one warp issues their boxes
-          const int whole = use_maps && !any_bad ? max(0, min(n, u.end / kTile - a0)) : 0;
-          const int boxes = kTile / box * P::kBlocks;
+          const int whole = use_maps && !any_bad ? max(0, min(n, u.end / kCols - a0)) : 0;
+          const int boxes = kCols / box * P::kBlocks;
           int y = 0;
           for (int i = 0; i < 2 * whole; ++i) {
-            const int k = slot_no + i, sl = k % P::kSlots, t0 = (a0 + i / 2) * kTile;
+            const int k = slot_no + i, sl = k % P::kSlots, t0 = (a0 + i / 2) * kCols;
             const int t = t0 + lane / P::kBlocks * box;
             if (lw == 0 && !(i & 1) && lane < boxes)
               y = (int)rows.row(t, u.end, rows.page(t, u.end));
@@ -468,7 +471,7 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
               __syncwarp();
               if (lane < boxes) {
                 const int blk = lane % P::kBlocks;
-                tma_box(s_ring + sl * P::kSlotBytes + blk * P::kBlockBytes + (t - t0) * 128,
+                tma_box(s_ring + sl * P::kSlotBytes + blk * P::kColBlock + (t - t0) * 128,
                         i & 1 ? &map_v : &map_k, 64 * blk, y, full + 8 * sl);
               }
               if (lane > 0) bar_arrive(full + 8 * sl);
@@ -476,23 +479,21 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
               bar_arrive(full + 8 * sl);
             }
           }
-          // the others: a slot is announced two slots later, when its copies are in
+          // the others: a slot is announced kLag slots later, when its copies are in
+          constexpr int kLag = 4;
           for (int i = 2 * whole; i < 2 * n; ++i) {
             const int k = slot_no + i, sl = k % P::kSlots;
             if (!(i & 1)) bad_pages(i / 2);
             bar_wait(empty + 8 * sl, (k / P::kSlots & 1) ^ 1, up, g.dev_status);
             __syncwarp();
             copy_tile(i, sl);
-            if (i >= 2 * whole + 2) {
-              asm volatile("cp.async.wait_group 2;" ::: "memory");
-              announce(k - 2);
+            if (i >= 2 * whole + kLag) {
+              asm volatile("cp.async.wait_group %0;" ::"n"(kLag) : "memory");
+              announce(k - kLag);
             }
           }
           asm volatile("cp.async.wait_group 0;" ::: "memory");
-          if (n > whole) {
-            announce(slot_no + 2 * n - 2);
-            announce(slot_no + 2 * n - 1);
-          }
+          for (int i = max(2 * whole, 2 * n - kLag); i < 2 * n; ++i) announce(slot_no + i);
         } else {
           const int held = min(u.held, u.end);
           const long long blocks0 =
@@ -500,18 +501,18 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
           // lane q of every warp looks after run q of a tile: its page (fetched a tile ahead),
           // row and scale (a slot ahead)
           const auto page_of = [&](int i) {
-            return lane < kGroups ? rows.page((a0 + i / 2) * kTile + 8 * lane,
+            return lane < kGroups ? rows.page((a0 + i / 2) * kCols + 8 * lane,
                                               i < 2 * n ? held : 0)
                                   : 0;
           };
           const auto row_of_run = [&](int i, int page) {
             return lane < kGroups && i < 2 * n
-                       ? rows.row((a0 + i / 2) * kTile + 8 * lane, held, page)
+                       ? rows.row((a0 + i / 2) * kCols + 8 * lane, held, page)
                        : -2;
           };
           const auto scale_of = [&](int i, long long row) {
             if (row < 0) return 0.f;
-            const int t = (a0 + i / 2) * kTile + 8 * lane;
+            const int t = (a0 + i / 2) * kCols + 8 * lane;
             return (i & 1 ? g.im.v_scale : g.im.k_scale)[
                 g.c.page_size ? row >> g.b_shift : blocks0 + (t >> g.b_shift)];
           };
@@ -519,7 +520,7 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
           // first run of a page (or the tile) copy all of its rows
           const auto copy_codes = [&](int i, long long row) {
             if (lw > 0 || i >= 2 * n || *up) return;
-            const int no = raw_no + i, st = no % P::kRaw, t0 = (a0 + i / 2) * kTile;
+            const int no = raw_no + i, st = no % P::kRaw, t0 = (a0 + i / 2) * kCols;
             bar_wait(rempty + 8 * st, (no / P::kRaw & 1) ^ 1, up, g.dev_status);
             __syncwarp();
             const int t = t0 + 8 * lane;
@@ -549,7 +550,7 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
           float scale = scale_of(0, row);
 #pragma unroll 1
           for (int i = 0; i < 2 * n; ++i) {
-            const int k = slot_no + i, sl = k % P::kSlots, t0 = (a0 + i / 2) * kTile;
+            const int k = slot_no + i, sl = k % P::kSlots, t0 = (a0 + i / 2) * kCols;
             const int no = raw_no + i, st = no % P::kRaw, ahead = i + P::kRaw - 1;
             if (!(i & 1)) bad_pages(i / 2);
             if (!(ahead & 1)) {
@@ -596,67 +597,71 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
         const uint32_t negate = g.c1 < 0.f ? kNegate : 0u;   // the softmax scales by |c1|
         const uint32_t tm = warp_value(tmem);
         int k_no = (int)warp_value(slot_no);
-        const auto qk = [&](int i) {                 // tile i of the piece
-          const int k = k_no + 2 * i, sl = k % P::kSlots;
+        const int mine = count[x], turn0 = used[x];
+        const auto tile = [&](int j) { return NQ == 2 ? j : 2 * j + x; };   // of the piece
+        // The stream's tile j goes through TMEM buffer (turn0 + j) % 2. Products of one thread
+        // run in the order they are issued in, so tile j + 2 may be issued behind the last
+        // reader of its buffer.
+        const auto qk = [&](int j) {
+          const int k = k_no + 2 * tile(j), sl = k % P::kSlots, c = turn0 + j;
           bar_wait(full + 8 * sl, k / P::kSlots & 1, up, g.dev_status);
           __syncwarp();
           if (warp_value(*up)) return;
           tc_after();
-          const uint32_t q = warp_value(s_q + (NQ == 2 ? x : 0) * P::kSlotBytes);
+          const uint32_t q = warp_value(s_q + (NQ == 2 ? x : 0) * P::kQBytes);
           const uint32_t kk = warp_value(s_ring + sl * P::kSlotBytes);
-          const uint32_t d = warp_value(tm + x * 256);
-          const uint32_t id = warp_value(idesc(kTile, false) | negate);
+          const uint32_t d = warp_value(tm + x * 256 + (c & 1) * 64);
+          const uint32_t id = warp_value(idesc(kCols, false) | negate);
           if (elected()) {
 #pragma unroll
-            for (int s = 0; s < D / 16; ++s) {
-              const uint32_t o = s / 4 * P::kBlockBytes + s % 4 * 32;
-              mma_ss(d, desc_k(q + o), desc_k(kk + o), id, s > 0);
-            }
-            commit(sfull + 8 * x);
+            for (int s = 0; s < D / 16; ++s)
+              mma_ss(d, desc_k(q + s / 4 * P::kRowBlock + s % 4 * 32),
+                     desc_k(kk + s / 4 * P::kColBlock + s % 4 * 32), id, s > 0);
+            commit(sfull + 16 * x + 8 * (c & 1));
             commit(empty + 8 * sl);
           }
           __syncwarp();
         };
-        const auto pv = [&](int i, int turn, bool first) {
-          const int k = k_no + 2 * i + 1, sl = k % P::kSlots;
+        const auto pv = [&](int j) {
+          const int k = k_no + 2 * tile(j) + 1, sl = k % P::kSlots, c = turn0 + j;
           bar_wait(full + 8 * sl, k / P::kSlots & 1, up, g.dev_status);
-          bar_wait(pfull + 8 * x, turn & 1, up, g.dev_status);
+          bar_wait(pfull + 16 * x + 8 * (c & 1), c >> 1 & 1, up, g.dev_status);
           __syncwarp();
           if (warp_value(*up)) return;
           tc_after();
           const uint32_t vv = warp_value(s_ring + sl * P::kSlotBytes);
-          const uint32_t d = warp_value(tm + x * 256);
-          const uint32_t add = warp_value(first ? 0u : 1u);
+          const uint32_t o = warp_value(tm + x * 256 + 128);
+          const uint32_t p = warp_value(tm + x * 256 + (c & 1) * 64);
+          const uint32_t add = warp_value(j > 0 ? 1u : 0u);
           if (elected()) {
 #pragma unroll
-            for (int s = 0; s < kTile / 16; ++s)
-              mma_ts(d + 128, d + s / 4 * 64 + s % 4 * 8, desc_mn(vv + s * 2048, P::kBlockBytes), idesc(D, true),
+            for (int s = 0; s < kCols / 16; ++s)
+              mma_ts(o, p + 8 * s, desc_mn(vv + s * 2048, P::kColBlock), idesc(D, true),
                      s > 0 ? 1u : add);
             if constexpr (P::kLo)
 #pragma unroll
-              for (int s = 0; s < kTile / 16; ++s)
-                mma_ts(d + 128, d + s / 4 * 64 + 32 + s % 4 * 8, desc_mn(vv + s * 2048, P::kBlockBytes),
-                       idesc(D, true), 1u);
-            commit(odone + 8 * x);
+              for (int s = 0; s < kCols / 16; ++s)
+                mma_ts(o, p + 32 + 8 * s, desc_mn(vv + s * 2048, P::kColBlock), idesc(D, true),
+                       1u);
+            commit(odone + 16 * x + 8 * (c & 1));
             commit(empty + 8 * sl);
           }
           __syncwarp();
         };
         bar_wait(qfull, segment & 1, up, g.dev_status);
         __syncwarp();
-        const auto tile = [&](int j) { return NQ == 2 ? j : 2 * j + x; };
-        const int mine = count[x];
-        if (mine > 0) qk(tile(0));
+        if (mine > 0) qk(0);
+        if (mine > 1) qk(1);
 #pragma unroll 1
         for (int j = 0; j < mine; ++j) {
-          pv(tile(j), used[x] + j, j == 0);
-          if (j + 1 < mine) qk(tile(j + 1));
+          pv(j);
+          if (j + 2 < mine) qk(j + 2);
         }
       } else if (warp < 8) {
         // ---- softmax ----
-        const int x = warp / 4, r = tid % kTile, rr = (NQ == 2 ? x * kTile : 0) + r;
+        const int x = warp / 4, r = tid % kRows, rr = (NQ == 2 ? x * kRows : 0) + r;
         const uint32_t lanes = (uint32_t)(warp % 4 * 32) << 16;
-        const uint32_t ts = tmem + lanes + x * 256, to = ts + 128;
+        const uint32_t to = tmem + lanes + x * 256 + 128;
         const float c1 = fmaxf(fabsf(g.c1), 1.1754944e-38f);   // not 0: -inf c1 is -inf
         const int lim = rr < u.rows ? min(u.end, row_limit(g, u, u.r0 + rr)) : 0;
         const int low = min(u.end, u.low);
@@ -670,7 +675,7 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
                   : 0);
 #pragma unroll 4
           for (int i = 0; i < D / 8; ++i)
-            copy16(s_q + (NQ == 2 ? x : 0) * P::kSlotBytes + i / 8 * P::kBlockBytes + r * 128 +
+            copy16(s_q + (NQ == 2 ? x : 0) * P::kQBytes + i / 8 * P::kRowBlock + r * 128 +
                        ((i ^ r) & 7) * 16,
                    ok ? src + 8 * i : src, ok);
           asm volatile("cp.async.wait_all;" ::: "memory");
@@ -682,41 +687,36 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
         const bool idle = (rr & ~31) >= u.rows;
         float m = -INFINITY, l = 0.f;
         for (int j = 0; j < count[x]; ++j) {
-          const int i = NQ == 2 ? j : 2 * j + x, t0 = (a0 + i) * kTile;
-          bar_wait(sfull + 8 * x, (used[x] + j) & 1, up, g.dev_status);
-          // complete already (the issuer's commits are in order): keeps the phases in step
-          if (j > 0) bar_wait(odone + 8 * x, (used[x] + j - 1) & 1, up, g.dev_status);
+          const int i = NQ == 2 ? j : 2 * j + x, t0 = (a0 + i) * kCols;
+          const int c = used[x] + j, buf = 16 * x + 8 * (c & 1);
+          const uint32_t ts = tmem + lanes + x * 256 + (c & 1) * 64;
+          bar_wait(sfull + buf, c >> 1 & 1, up, g.dev_status);
+          // the buffer's product before is done (its logits were issued behind it)
+          if (j > 1) bar_wait(odone + buf, (c >> 1 & 1) ^ 1, up, g.dev_status);
           __syncwarp();
           if (idle) {
-            bar_arrive(pfull + 8 * x);
+            bar_arrive(pfull + buf);
             continue;
           }
           tc_after();
           const int bad = s_bad[i & 15];
-          const bool mask = t0 + kTile > low || bad;
-          // Loops over 64 columns, not unrolled: warps that run through thousands of different
-          // instructions wait for those (a third of all stalls when these were unrolled).
-          // a masked logit is -inf
-          const auto logits = [&](int h, float* s) {
-            tmem_ld32(ts + 64 * h, s);
-            tmem_ld32(ts + 64 * h + 32, s + 32);
-            tmem_ld_wait();
-            if (mask) {
-              const int left = lim - t0 - 64 * h;
+          const bool mask = t0 + kCols > low || bad;
+          float s[kCols];
+          tmem_ld32(ts, s);
+          tmem_ld32(ts + 32, s + 32);
+          tmem_ld_wait();
+          if (mask) {                  // a masked logit is -inf
+            const int left = lim - t0;
 #pragma unroll
-              for (int e = 0; e < 64; ++e)
-                if (e >= left || (bad >> (8 * h + e / 8) & 1)) s[e] = -INFINITY;
-            }
-          };
-          float top = -INFINITY;
-#pragma unroll 1
-          for (int h = 0; h < 2; ++h) {
-            float s[64];
-            logits(h, s);
+            for (int e = 0; e < kCols; ++e)
+              if (e >= left || (bad >> (e / 8) & 1)) s[e] = -INFINITY;
+          }
+          float top;
+          {
             float t[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-            for (int e = 4; e < 64; ++e) t[e % 4] = fmaxf(t[e % 4], s[e]);
-            top = fmaxf(top, fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])));
+            for (int e = 4; e < kCols; ++e) t[e % 4] = fmaxf(t[e % 4], s[e]);
+            top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
           }
           top *= c1;
           const bool raise = top > m + kRaise;
@@ -724,7 +724,10 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
             const float nm = raise ? top : m, f = raise ? ex2(m - nm) : 1.f;
             m = nm;
             l *= f;
-            if (j > 0) {               // S is complete, so the products before it are too
+            if (j > 0) {               // once the product before this one is done
+              bar_wait(odone + (buf ^ 8), (c - 1) >> 1 & 1, up, g.dev_status);
+              __syncwarp();
+              tc_after();
 #pragma unroll 1
               for (int q = 0; q < D / 16; ++q) {
                 uint32_t o[16];
@@ -738,41 +741,37 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
           }
           const float ref = m == -INFINITY ? 0.f : m;
           float sum[4] = {0.f, 0.f, 0.f, 0.f};
-          // p lies over S, each half's hi and lo over its own columns
-#pragma unroll 1
-          for (int h = 0; h < 2; ++h) {
-            float s[64];
-            logits(h, s);
+          // p lies over S: hi in columns 0 .. 31, lo in 32 .. 63
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              uint32_t hi[16], lo[16];
+          for (int q = 0; q < 2; ++q) {
+            uint32_t hi[16], lo[16];
 #pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                const float y0 = ex2(fmaf(s[32 * q + 2 * e], c1, -ref));
-                const float y1 = ex2(fmaf(s[32 * q + 2 * e + 1], c1, -ref));
-                sum[e % 4] += y0;
-                sum[e % 4] += y1;
-                hi[e] = bf16_pair(y0, y1);
-                if constexpr (P::kLo)
-                  lo[e] = bf16_pair(y0 - __uint_as_float(hi[e] << 16),
-                                    y1 - __uint_as_float(hi[e] & 0xFFFF0000u));
-              }
-              tmem_st16(ts + 64 * h + 16 * q, hi);
-              if constexpr (P::kLo) tmem_st16(ts + 64 * h + 32 + 16 * q, lo);
+            for (int e = 0; e < 16; ++e) {
+              const float y0 = ex2(fmaf(s[32 * q + 2 * e], c1, -ref));
+              const float y1 = ex2(fmaf(s[32 * q + 2 * e + 1], c1, -ref));
+              sum[e % 4] += y0;
+              sum[e % 4] += y1;
+              hi[e] = bf16_pair(y0, y1);
+              if constexpr (P::kLo)
+                lo[e] = bf16_pair(y0 - __uint_as_float(hi[e] << 16),
+                                  y1 - __uint_as_float(hi[e] & 0xFFFF0000u));
             }
+            tmem_st16(ts + 16 * q, hi);
+            if constexpr (P::kLo) tmem_st16(ts + 32 + 16 * q, lo);
           }
           l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
           tmem_st_wait();
           tc_before();
-          bar_arrive(pfull + 8 * x);
+          bar_arrive(pfull + buf);
         }
-        if (count[x] > 0) {
-          bar_wait(odone + 8 * x, (used[x] + count[x] - 1) & 1, up, g.dev_status);
-          __syncwarp();
-          tc_after();
+        for (int j = max(0, count[x] - 2); j < count[x]; ++j) {
+          const int c = used[x] + j;
+          bar_wait(odone + 16 * x + 8 * (c & 1), c >> 1 & 1, up, g.dev_status);
         }
+        __syncwarp();
+        tc_after();
         // ---- results ----
-        float* s_o = reinterpret_cast<float*>(base + NQ * P::kSlotBytes);   // the ring is idle
+        float* s_o = reinterpret_cast<float*>(base + NQ * P::kQBytes);   // the ring is idle
         const auto between = [] { asm volatile("bar.sync 1, 256;" ::: "memory"); };
         if (NQ == 1) {
           between();                   // both streams' products are done with the ring
@@ -786,7 +785,7 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
                 tmem_ld32(to + 32 * q, o);
                 tmem_ld_wait();
 #pragma unroll
-                for (int e = 0; e < 32; ++e) s_o[(32 * q + e) * kTile + r] = o[e];
+                for (int e = 0; e < 32; ++e) s_o[(32 * q + e) * kRows + r] = o[e];
               }
           }
           between();
@@ -811,7 +810,7 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
             if (NQ == 1)
 #pragma unroll
               for (int e = 0; e < 32; ++e)
-                o[e] = o[e] * f0 + (count[1] ? s_o[(32 * q + e) * kTile + r] * f1 : 0.f);
+                o[e] = o[e] * f0 + (count[1] ? s_o[(32 * q + e) * kRows + r] * f1 : 0.f);
             if (rr < u.rows) {
               if (whole) {
                 if (l == 0.f)
@@ -868,7 +867,7 @@ __global__ void __launch_bounds__(kTcRows) attend_tc_join_kernel(AttendArgs g) {
   const int b = blockIdx.x, d0 = blockIdx.y * 32, r = threadIdx.x;
   const int2 desc = g.ws.desc[b];
   if (desc.x < 0) return;
-  const AttendUnit u = attend_unit<kTile * NQ>(g, desc.x);
+  const AttendUnit u = attend_unit<kRows * NQ>(g, desc.x);
   if (r >= u.rows) return;
   float m = -INFINITY, l = 0.f, o[32];
 #pragma unroll
@@ -922,7 +921,7 @@ bool encode_rows(const nx_cache& c, void* base, CUtensorMap* map) {
   if (!fn || rows >= (1LL << 31)) return false;
   const cuuint64_t dim[2] = {(cuuint64_t)c.head_dim, (cuuint64_t)rows};
   const cuuint64_t stride[1] = {(cuuint64_t)c.head_dim * 2};
-  const cuuint32_t box[2] = {64, (cuuint32_t)(c.page_size ? c.page_size : kTile)};
+  const cuuint32_t box[2] = {64, (cuuint32_t)(c.page_size && c.page_size < kCols ? c.page_size : kCols)};
   const cuuint32_t one[2] = {1, 1};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dim, stride, box, one,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -933,9 +932,9 @@ template <int D, int NQ, bool IMAGE>
 cudaError_t launch_t(AttendArgs& g, cudaStream_t st, int* launches) {
   constexpr int smem = Plan<D, NQ, IMAGE>::kSmem;
   const long long all = (long long)g.t.max_tokens * g.c.group;
-  g.mtiles = (int)((all + kTile * NQ - 1) / (kTile * NQ));
+  g.mtiles = (int)((all + kRows * NQ - 1) / (kRows * NQ));
   const long long units = (long long)g.c.seqs * g.c.kv_heads * g.mtiles;
-  const long long most = units * ((g.c.capacity + kTile - 1) / kTile);
+  const long long most = units * ((g.c.capacity + kCols - 1) / kCols);
   if (most > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
   g.units = (int)units;
   cudaError_t e = allow_smem<attend_tc_kernel<D, NQ, IMAGE>>(smem);
@@ -976,7 +975,7 @@ size_t attend_tc_layout(int D, char* base, AttendWs* ws) {
 }
 
 cudaError_t launch_attend_tc(AttendArgs& g, cudaStream_t st, int* launches) {
-  const bool two = (long long)g.t.max_tokens * g.c.group > kTile;
+  const bool two = (long long)g.t.max_tokens * g.c.group > kRows;
   if (g.c.head_dim == 128)
     return two ? launch_t<128, 2>(g, st, launches) : launch_t<128, 1>(g, st, launches);
   return two ? launch_t<64, 2>(g, st, launches) : launch_t<64, 1>(g, st, launches);
