@@ -84,16 +84,17 @@ __device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_
       "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
       : "memory");
 }
-// Waits for a phase, unless the block has given up already.
-__device__ __forceinline__ void bar_wait(uint32_t bar, uint32_t parity, volatile int* gave_up,
+// Waits for a phase, unless the block gives up or has given up: false then.
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int* gave_up,
                                          int32_t* dev_status) {
-  if (bar_test(bar, parity)) return;
+  if (bar_test(bar, parity)) return true;
   for (int i = 0; i < kPolls; ++i) {
-    if (*gave_up) return;
-    if (bar_test(bar, parity)) return;
+    if (*gave_up) return false;
+    if (bar_test(bar, parity)) return true;
   }
   *gave_up = 1;
   atomicOr(dev_status, NX_DEV_TIMEOUT);
+  return false;
 }
 __device__ __forceinline__ void tc_before() {
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -595,67 +596,66 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
         // ---- matrix instructions: the whole warp goes along, one lane issues ----
         const int x = (int)warp_value(warp - kIssueWarp);   // the stream
         const uint32_t negate = g.c1 < 0.f ? kNegate : 0u;   // the softmax scales by |c1|
-        const uint32_t tm = warp_value(tmem);
-        int k_no = (int)warp_value(slot_no);
-        const int mine = count[x], turn0 = used[x];
-        const auto tile = [&](int j) { return NQ == 2 ? j : 2 * j + x; };   // of the piece
-        // The stream's tile j goes through TMEM buffer (turn0 + j) % 2. Products of one thread
-        // run in the order they are issued in, so tile j + 2 may be issued behind the last
-        // reader of its buffer.
-        const auto qk = [&](int j) {
-          const int k = k_no + 2 * tile(j), sl = k % P::kSlots, c = turn0 + j;
-          bar_wait(full + 8 * sl, k / P::kSlots & 1, up, g.dev_status);
-          __syncwarp();
-          if (warp_value(*up)) return;
-          tc_after();
-          const uint32_t q = warp_value(s_q + (NQ == 2 ? x : 0) * P::kQBytes);
-          const uint32_t kk = warp_value(s_ring + sl * P::kSlotBytes);
-          const uint32_t d = warp_value(tm + x * 256 + (c & 1) * 64);
-          const uint32_t id = warp_value(idesc(kCols, false) | negate);
-          if (elected()) {
+        const uint32_t tm = warp_value(tmem) + x * 256, o = tm + 128;
+        const uint32_t q = warp_value(s_q) + (NQ == 2 ? x : 0) * P::kQBytes;
+        const uint32_t ring = warp_value(s_ring), id = idesc(kCols, false) | negate;
+        const int k_no = (int)warp_value(slot_no), turn0 = (int)warp_value(used[x]);
+        const int mine = (int)warp_value(count[x]);
+        const auto k_of = [&](int j) { return k_no + 2 * (NQ == 2 ? j : 2 * j + x); };
+        const auto qk = [&](int j) {   // the stream's tile j, to TMEM buffer (turn0 + j) % 2
+          const int sl = k_of(j) % P::kSlots, c = turn0 + j;
+          const uint32_t kk = ring + sl * P::kSlotBytes, d = tm + (c & 1) * 64;
 #pragma unroll
-            for (int s = 0; s < D / 16; ++s)
-              mma_ss(d, desc_k(q + s / 4 * P::kRowBlock + s % 4 * 32),
-                     desc_k(kk + s / 4 * P::kColBlock + s % 4 * 32), id, s > 0);
-            commit(sfull + 16 * x + 8 * (c & 1));
-            commit(empty + 8 * sl);
-          }
-          __syncwarp();
+          for (int s = 0; s < D / 16; ++s)
+            mma_ss(d, desc_k(q + s / 4 * P::kRowBlock + s % 4 * 32),
+                   desc_k(kk + s / 4 * P::kColBlock + s % 4 * 32), id, s > 0);
+          commit(sfull + 16 * x + 8 * (c & 1));
+          commit(empty + 8 * sl);
         };
         const auto pv = [&](int j) {
-          const int k = k_no + 2 * tile(j) + 1, sl = k % P::kSlots, c = turn0 + j;
-          bar_wait(full + 8 * sl, k / P::kSlots & 1, up, g.dev_status);
-          bar_wait(pfull + 16 * x + 8 * (c & 1), c >> 1 & 1, up, g.dev_status);
-          __syncwarp();
-          if (warp_value(*up)) return;
-          tc_after();
-          const uint32_t vv = warp_value(s_ring + sl * P::kSlotBytes);
-          const uint32_t o = warp_value(tm + x * 256 + 128);
-          const uint32_t p = warp_value(tm + x * 256 + (c & 1) * 64);
-          const uint32_t add = warp_value(j > 0 ? 1u : 0u);
-          if (elected()) {
+          const int sl = (k_of(j) + 1) % P::kSlots, c = turn0 + j;
+          const uint32_t vv = ring + sl * P::kSlotBytes, p = tm + (c & 1) * 64;
+#pragma unroll
+          for (int s = 0; s < kCols / 16; ++s)
+            mma_ts(o, p + 8 * s, desc_mn(vv + s * 2048, P::kColBlock), idesc(D, true),
+                   s > 0 || j > 0);
+          if constexpr (P::kLo)
 #pragma unroll
             for (int s = 0; s < kCols / 16; ++s)
-              mma_ts(o, p + 8 * s, desc_mn(vv + s * 2048, P::kColBlock), idesc(D, true),
-                     s > 0 ? 1u : add);
-            if constexpr (P::kLo)
-#pragma unroll
-              for (int s = 0; s < kCols / 16; ++s)
-                mma_ts(o, p + 32 + 8 * s, desc_mn(vv + s * 2048, P::kColBlock), idesc(D, true),
-                       1u);
-            commit(odone + 16 * x + 8 * (c & 1));
-            commit(empty + 8 * sl);
+              mma_ts(o, p + 32 + 8 * s, desc_mn(vv + s * 2048, P::kColBlock), idesc(D, true), 1u);
+          commit(odone + 16 * x + 8 * (c & 1));
+          commit(empty + 8 * sl);
+        };
+        // Steps -2 and -1 issue the first logits; step j the product of tile j and, behind it
+        // (products of one thread run in the order they are issued in), the logits of tile
+        // j + 2, into the buffer that the product read. What a step waits for is watched by a
+        // lane each: the query rows or the probabilities, V, the next K. (That K is two tiles
+        // ahead of V: the ring holds them all, and kLag slots more.)
+        bool fine = true;
+#pragma unroll 1
+        for (int j = -2; j < mine && fine; ++j) {
+          const int c = turn0 + j, kv = k_of(j) + 1, kk = k_of(j + 2);
+          const bool product = j >= 0, logits = j + 2 < mine;
+          uint32_t bar = 0, parity = 0;
+          if (lane == 0) {
+            bar = product ? pfull + 16 * x + 8 * (c & 1) : j == -2 ? qfull : 0;
+            parity = product ? c >> 1 & 1 : segment & 1;
+          } else if (lane == 1 && product) {
+            bar = full + 8 * (kv % P::kSlots);
+            parity = kv / P::kSlots & 1;
+          } else if (lane == 2 && logits) {
+            bar = full + 8 * (kk % P::kSlots);
+            parity = kk / P::kSlots & 1;
+          }
+          const bool ok = bar == 0 || bar_wait(bar, parity, up, g.dev_status);
+          fine = __all_sync(0xffffffffu, ok);
+          if (!fine) break;
+          tc_after();
+          if (elected()) {
+            if (product) pv(j);
+            if (logits) qk(j + 2);
           }
           __syncwarp();
-        };
-        bar_wait(qfull, segment & 1, up, g.dev_status);
-        __syncwarp();
-        if (mine > 0) qk(0);
-        if (mine > 1) qk(1);
-#pragma unroll 1
-        for (int j = 0; j < mine; ++j) {
-          pv(j);
-          if (j + 2 < mine) qk(j + 2);
         }
       } else if (warp < 8) {
         // ---- softmax ----
