@@ -132,7 +132,7 @@ __device__ __forceinline__ AttendShare attend_share(const AttendArgs& g, const T
 
 // nx_attend_tc.cu: the tensor-core kernel for many query rows per slice (bf16 caches), its
 // workspace (base may be null; returns the bytes), and whether it takes a call.
-bool attend_tc_takes(const nx_cache& c, const nx_tokens& t);
+bool attend_tc_takes(const nx_cache& c, const nx_tokens& t, bool image);
 size_t attend_tc_layout(int D, char* base, AttendWs* ws);
 cudaError_t launch_attend_tc(AttendArgs& g, cudaStream_t st, int* launches);
 

@@ -960,8 +960,8 @@ size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 
 }  // namespace
 
-bool attend_tc_takes(const nx_cache& c, const nx_tokens& t) {
-  return c.dtype == NX_DTYPE_BF16 && (long long)t.max_tokens * c.group > 16;
+bool attend_tc_takes(const nx_cache& c, const nx_tokens& t, bool image) {
+  return c.dtype == NX_DTYPE_BF16 && (long long)t.max_tokens * c.group > (image ? 96 : 16);
 }
 
 size_t attend_tc_layout(int D, char* base, AttendWs* ws) {
