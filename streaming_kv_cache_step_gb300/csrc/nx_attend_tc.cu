@@ -280,43 +280,49 @@ __device__ __forceinline__ void copy_group(const char* src, long long row, int t
   }
 }
 
-// `some` (at most 8) rows of codes in shared memory, times their scale, and zeros behind them
-// to rows r .. r + 7 of a ring slot.
-template <int D>
-__device__ __forceinline__ void expand_group(uint32_t raw, float scale, int some, uint32_t slot,
-                                             int r, int lane) {
-  constexpr int kChunks = D / 8, kLine = 32 / kChunks;
-  const int chunk = lane % kChunks, sub = lane / kChunks;
-  const uint32_t dst = slot + chunk / 8 * (kCols * 128) + (r + sub) * 128;
-  uint32_t x[8 / kLine][2];
+// The codes of a tile's rows below `some`, times the scales of their runs of 8, as bf16 in a ring
+// slot, with zeros behind them up to the next run. Thread `tid` of N takes every N-th 8 codes.
+template <int D, int N>
+__device__ __forceinline__ void expand_tile(uint32_t raw, const float* scale, int some,
+                                            uint32_t slot, int tid) {
+  constexpr int kChunks = D / 8, kAll = kCols * kChunks, kEach = (kAll + N - 1) / N;
+  const int rows = min(kCols, (some + 7) / 8 * 8);
+  uint32_t x[kEach][2];
+  float f[kEach];
 #pragma unroll
-  for (int i = 0; i < 8 / kLine; ++i)
-    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];"
-                 : "=r"(x[i][0]), "=r"(x[i][1])
-                 : "r"(raw + i * kLine * D + lane * 8)
-                 : "memory");
-  if (some < 8) {
-#pragma unroll
-    for (int i = 0; i < 8 / kLine; ++i)
-      if (i * kLine + sub >= some) x[i][0] = x[i][1] = 0;
+  for (int i = 0; i < kEach; ++i) {
+    const int c = tid + i * N, r = c / kChunks;
+    x[i][0] = x[i][1] = 0;
+    f[i] = 0.f;
+    if (r < some && (kAll % N == 0 || c < kAll)) {
+      asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];"
+                   : "=r"(x[i][0]), "=r"(x[i][1])
+                   : "r"(raw + c * 8)
+                   : "memory");
+      f[i] = scale[r / 8];
+    }
   }
 #pragma unroll
-  for (int i = 0; i < 8 / kLine; ++i) {
+  for (int i = 0; i < kEach; ++i) {
+    const int c = tid + i * N, r = c / kChunks, chunk = c % kChunks;
     uint32_t y[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      uint32_t h;
-      asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\t"
-          "cvt.rn.f16x2.e4m3x2 %0, a;\n\t}"
-          : "=r"(h)
-          : "r"(j % 2 ? x[i][j / 2] >> 16 : x[i][j / 2]));
-      const float2 f = __half22float2(reinterpret_cast<const __half2&>(h));
-      y[j] = bf16_pair(f.x * scale, f.y * scale);
+    for (int j = 0; j < 2; ++j) {
+      uint32_t h0, h1;
+      asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+          "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+          : "=r"(h0), "=r"(h1)
+          : "r"(x[i][j]));
+      const float2 v0 = __half22float2(reinterpret_cast<const __half2&>(h0));
+      const float2 v1 = __half22float2(reinterpret_cast<const __half2&>(h1));
+      y[2 * j] = bf16_pair(v0.x * f[i], v0.y * f[i]);
+      y[2 * j + 1] = bf16_pair(v1.x * f[i], v1.y * f[i]);
     }
-    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(
-                     dst + i * kLine * 128 + ((chunk ^ (i * kLine + sub)) & 7) * 16),
-                 "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3])
-                 : "memory");
+    if (r < rows && (kAll % N == 0 || c < kAll))
+      asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(
+                       slot + chunk / 8 * (kCols * 128) + r * 128 + ((chunk ^ r) & 7) * 16),
+                   "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3])
+                   : "memory");
   }
 }
 
@@ -353,6 +359,7 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
   __shared__ uint32_t s_tmem;
   __shared__ int s_up, s_bad[16];                   // bad-page marks of tile % 16
   __shared__ float s_m[kRows], s_l[kRows];
+  __shared__ float s_scale[IMAGE ? P::kRaw : 1][kGroups];     // of the runs in a raw stage
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, b = blockIdx.x;
   char* base = s_raw + (1024 - (smem_at(s_raw) & 1023)) % 1024;
   const uint32_t s_q = smem_at(base), s_ring = s_q + NQ * P::kQBytes;
@@ -370,12 +377,12 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
   }
   if (tid == 0) {
     for (int i = 0; i < P::kSlots; ++i) {
-      bar_init(full + 8 * i, kLoaders);
+      bar_init(full + 8 * i, IMAGE ? kLoaders - 32 : kLoaders);
       bar_init(empty + 8 * i, NQ);                 // its users are done
     }
     for (int i = 0; i < P::kRaw; ++i) {
-      bar_init(rfull + 8 * i, 1);
-      bar_init(rempty + 8 * i, kLoadWarps);
+      bar_init(rfull + 8 * i, 32);
+      bar_init(rempty + 8 * i, kLoadWarps - 1);
     }
     bar_init(qfull, NQ * kRows);
     for (int i = 0; i < 4; ++i) {
@@ -497,99 +504,78 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
           for (int i = max(2 * whole, 2 * n - kLag); i < 2 * n; ++i) announce(slot_no + i);
         } else {
           const int held = min(u.held, u.end);
-          const long long blocks0 =
-              g.c.page_size ? 0 : image_scale_at(g.c, g.t.layer, u.s, u.h, 0, g.b);
-          // lane q of every warp looks after run q of a tile: its page (fetched a tile ahead),
-          // row and scale (a slot ahead)
-          const auto page_of = [&](int i) {
-            return lane < kGroups ? rows.page((a0 + i / 2) * kCols + 8 * lane,
-                                              i < 2 * n ? held : 0)
-                                  : 0;
-          };
-          const auto row_of_run = [&](int i, int page) {
-            return lane < kGroups && i < 2 * n
-                       ? rows.row((a0 + i / 2) * kCols + 8 * lane, held, page)
-                       : -2;
-          };
-          const auto scale_of = [&](int i, long long row) {
-            if (row < 0) return 0.f;
-            const int t = (a0 + i / 2) * kCols + 8 * lane;
-            return (i & 1 ? g.im.v_scale : g.im.k_scale)[
-                g.c.page_size ? row >> g.b_shift : blocks0 + (t >> g.b_shift)];
-          };
-          // codes of slot i to raw stage (raw_no + i) % kRaw: the first warp's lanes with the
-          // first run of a page (or the tile) copy all of its rows
-          const auto copy_codes = [&](int i, long long row) {
-            if (lw > 0 || i >= 2 * n || *up) return;
-            const int no = raw_no + i, st = no % P::kRaw, t0 = (a0 + i / 2) * kCols;
-            bar_wait(rempty + 8 * st, (no / P::kRaw & 1) ^ 1, up, g.dev_status);
-            __syncwarp();
-            const int t = t0 + 8 * lane;
-            const bool lead = row >= 0 && (t - t0) % box == 0;
-            const int bytes = lead ? (min(held, t + box) - t) * D : 0;
-            const unsigned total = __reduce_add_sync(0xffffffffu, (unsigned)bytes);
-            if (lane == 0) bar_arrive_tx(rfull + 8 * st, total);
-            __syncwarp();
-            if (lead)
-              bulk_copy(s_codes + st * P::kRawBytes + (t - t0) * D,
-                        static_cast<const char*>(i & 1 ? g.im.v : g.im.k) + row * D, bytes,
-                        rfull + 8 * st);
-          };
-          int page = page_of(0);
-          long long row = row_of_run(0, page);                  // of tile i / 2
-          int page1 = page_of(2);                               // of the next tile
-          long long row_ahead = row;                            // of the slot copied next
-          int page_ahead = page1;
+          if (lw == 0) {
+            // the first warp copies codes ahead: lane q < 8 looks after run q of a tile, its page
+            // (fetched a tile ahead), its row, its scale (fetched a slot ahead); a page's (or the
+            // tile's) first run copies all of its rows
+            const long long blocks0 =
+                g.c.page_size ? 0 : image_scale_at(g.c, g.t.layer, u.s, u.h, 0, g.b);
+            const auto slot_of = [&](int i) { return (a0 + i / 2) * kCols + 8 * lane; };
+            const auto page_of = [&](int i) {
+              return lane < kGroups ? rows.page(slot_of(i), i < 2 * n ? held : 0) : 0;
+            };
+            const auto row_of_run = [&](int i, int page) {
+              return lane < kGroups && i < 2 * n ? rows.row(slot_of(i), held, page) : -2;
+            };
+            const auto scale_of = [&](int i, long long row) {
+              if (row < 0) return 0.f;
+              return (i & 1 ? g.im.v_scale : g.im.k_scale)[
+                  g.c.page_size ? row >> g.b_shift : blocks0 + (slot_of(i) >> g.b_shift)];
+            };
+            long long row = row_of_run(0, page_of(0));
+            int page1 = page_of(2);
+            float scale = scale_of(0, row);
 #pragma unroll 1
-          for (int i = 0; i < P::kRaw - 1; ++i) {
-            if (i > 0 && !(i & 1)) {
-              row_ahead = row_of_run(i, page_ahead);
-              page_ahead = page_of(i + 2);
-            }
-            copy_codes(i, row_ahead);
-          }
-          float scale = scale_of(0, row);
-#pragma unroll 1
-          for (int i = 0; i < 2 * n; ++i) {
-            const int k = slot_no + i, sl = k % P::kSlots, t0 = (a0 + i / 2) * kCols;
-            const int no = raw_no + i, st = no % P::kRaw, ahead = i + P::kRaw - 1;
-            if (!(i & 1)) bad_pages(i / 2);
-            if (!(ahead & 1)) {
-              row_ahead = row_of_run(ahead, page_ahead);
-              page_ahead = page_of(ahead + 2);
-            }
-            copy_codes(ahead, row_ahead);
-            long long row1 = row;                               // of slot i + 1
-            if (i & 1) {
-              row1 = row_of_run(i + 1, page1);
-              page1 = page_of(i + 3);
-            }
-            const float scale1 = scale_of(i + 1, row1);
-            bar_wait(rfull + 8 * st, no / P::kRaw & 1, up, g.dev_status);
-            bar_wait(empty + 8 * sl, (k / P::kSlots & 1) ^ 1, up, g.dev_status);
-            __syncwarp();
-            const uint32_t slot = s_ring + sl * P::kSlotBytes;
-            bool rest = false;
-#pragma unroll 1
-            for (int q = lw; q < kGroups; q += kLoadWarps) {
-              const int r = 8 * q, t = t0 + r;
-              const float sc = __shfl_sync(0xffffffffu, scale, q);
-              if (t < held) {
-                const bool good = __shfl_sync(0xffffffffu, row >= 0 ? 1 : 0, q) != 0;
-                expand_group<D>(s_codes + st * P::kRawBytes + r * D, sc, good ? held - t : 0, slot,
-                                r, lane);
-              } else {
-                copy_group<D>(static_cast<const char*>(i & 1 ? g.c.v : g.c.k),
-                              rows.row(t, u.end, rows.page(t, u.end)), t, u.end, slot, r, lane);
-                rest = true;
+            for (int i = 0; i < 2 * n; ++i) {
+              const int no = raw_no + i, st = no % P::kRaw, t = slot_of(i);
+              if (!(i & 1)) bad_pages(i / 2);
+              long long row1 = row;                             // of slot i + 1
+              if (i & 1) {
+                row1 = row_of_run(i + 1, page1);
+                page1 = page_of(i + 3);
               }
+              const float scale1 = scale_of(i + 1, row1);
+              const bool go =
+                  bar_wait(rempty + 8 * st, (no / P::kRaw & 1) ^ 1, up, g.dev_status);
+              if (lane < kGroups) s_scale[st][lane] = scale;
+              const bool lead = go && row >= 0 && 8 * lane % box == 0;
+              const int bytes = lead ? (min(held, t + box) - t) * D : 0;
+              const unsigned total = __reduce_add_sync(0xffffffffu, (unsigned)bytes);
+              if (lane == 0) bar_arrive_tx(rfull + 8 * st, total);
+              else bar_arrive(rfull + 8 * st);
+              __syncwarp();
+              if (lead)
+                bulk_copy(s_codes + st * P::kRawBytes + 8 * lane * D,
+                          static_cast<const char*>(i & 1 ? g.im.v : g.im.k) + row * D, bytes,
+                          rfull + 8 * st);
+              row = row1;
+              scale = scale1;
             }
-            if (rest) asm volatile("cp.async.wait_all;" ::: "memory");
-            announce(k);
-            __syncwarp();
-            if (lane == 0) bar_arrive(rempty + 8 * st);
-            row = row1;
-            scale = scale1;
+          } else {
+            // the others expand them
+#pragma unroll 1
+            for (int i = 0; i < 2 * n; ++i) {
+              const int k = slot_no + i, sl = k % P::kSlots, t0 = (a0 + i / 2) * kCols;
+              const int no = raw_no + i, st = no % P::kRaw;
+              bar_wait(rfull + 8 * st, no / P::kRaw & 1, up, g.dev_status);
+              bar_wait(empty + 8 * sl, (k / P::kSlots & 1) ^ 1, up, g.dev_status);
+              const uint32_t slot = s_ring + sl * P::kSlotBytes;
+              if (held > t0)
+                expand_tile<D, kLoaders - 32>(s_codes + st * P::kRawBytes, s_scale[st], held - t0,
+                                              slot, lt - 32);
+              if (t0 + kCols > held) {                          // bf16 rows, or none, behind it
+                __syncwarp();
+                const int q0 = held > t0 ? (held - t0 + 7) / 8 : 0;
+                for (int r = 8 * (q0 + lw - 1); r < kCols; r += 8 * (kLoadWarps - 1))
+                  copy_group<D>(static_cast<const char*>(i & 1 ? g.c.v : g.c.k),
+                                rows.row(t0 + r, u.end, rows.page(t0 + r, u.end)), t0 + r, u.end,
+                                slot, r, lane);
+                asm volatile("cp.async.wait_all;" ::: "memory");
+              }
+              announce(k);
+              __syncwarp();
+              if (lane == 0) bar_arrive(rempty + 8 * st);
+            }
           }
         }
       } else if (warp >= kIssueWarp) {
