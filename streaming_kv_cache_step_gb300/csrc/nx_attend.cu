@@ -29,18 +29,12 @@ namespace nx {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kAttendGrid = kSms * 3;  // thread blocks of one launch, at most
-constexpr int kPieceRows = 32;         // query rows of a piece, at most
+constexpr int kAttendGrid = kSms * 4;  // thread blocks of one launch, at most
+constexpr int kPieceRows = 16;         // query rows of a piece, at most
 // kTail: bf16 rows behind an image, with their output features in the image's order
-// kImage16: an image in steps of 16 slots, for 32 rows, which leave no registers for 32
-enum Kind { kBf16 = 0, kImage = 1, kF32 = 2, kTail = 3, kImage16 = 4 };
+enum Kind { kBf16 = 0, kImage = 1, kF32 = 2, kTail = 3 };
 template <int KIND>
 constexpr bool kIsBf16 = KIND == kBf16 || KIND == kTail;
-template <int KIND>
-constexpr bool kIsImage = KIND == kImage || KIND == kImage16;
-// mma row tiles of a unit's rows, and values of them per thread and column tile
-template <int ROWS>
-constexpr int kValues = ROWS == 32 ? 8 : 4;
 
 // Probabilities are kept at 2^kUp times their size, and m is only raised when a logit is more
 // than 2^kSlack above it, so they are at most 2^(kUp + kSlack) = 32768: below fp16's largest
@@ -60,7 +54,7 @@ __device__ __forceinline__ void mma16(float* d, const uint32_t* a, uint32_t b0, 
         "{%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-  else if constexpr (kIsImage<KIND>)
+  else if constexpr (KIND == kImage)
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
         "{%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -109,8 +103,8 @@ __device__ __forceinline__ uint32_t tf32_lo(uint32_t x) {
 // How K and V of KIND reach the fragments. g = lane / 4 and c = lane % 4 as in an mma.
 template <int KIND, int D>
 struct Shape {
-  static constexpr int kSlots = KIND == kImage ? 32 : KIND == kBf16 || KIND == kImage16 ? 16 : 8;  // of a step
-  static constexpr int kTile = kIsImage<KIND> ? 128 : 64;        // slots of a block's tile
+  static constexpr int kSlots = KIND == kImage ? 32 : KIND == kBf16 ? 16 : 8;  // of a step
+  static constexpr int kTile = KIND == kImage ? 128 : 64;        // slots of a block's tile
   static constexpr int NT = kSlots / 8;                          // mma column tiles of them
   static constexpr int kBytes = KIND == kF32 ? 4 : kIsBf16<KIND> ? 2 : 1;
   static constexpr int kRow = D * kBytes;                        // bytes of a row
@@ -149,11 +143,10 @@ struct Ring {
   static constexpr int kDeep = kFit > 8 ? 8 : kFit;
 };
 
-// One warp's running state: o[t] holds rows g (c0, c1), g + 8 (c2, c3) and so on of output tile
-// t.
+// One warp's running state: o[t] holds rows g (c0, c1) and g + 8 (c2, c3) of output tile t.
 template <int D, int ROWS>
 struct State {
-  float o[D / 8][kValues<ROWS>];
+  float o[D / 8][4];
   float m[ROWS / 8], l[ROWS / 8];
 };
 
@@ -239,8 +232,8 @@ __device__ __forceinline__ void copy_rows(const AttendArgs& g, const long long* 
   using S = Shape<KIND, D>;
   constexpr int kLine = 32 / S::kChunks > 0 ? 32 / S::kChunks : 1;   // rows per instruction
   static_assert(S::kChunks <= 32 && 8 % kLine == 0, "");
-  const char* kb = static_cast<const char*>(kIsImage<KIND> ? g.im.k : g.c.k);
-  const char* vb = static_cast<const char*>(kIsImage<KIND> ? g.im.v : g.c.v);
+  const char* kb = static_cast<const char*>(KIND == kImage ? g.im.k : g.c.k);
+  const char* vb = static_cast<const char*>(KIND == kImage ? g.im.v : g.c.v);
   const int sub = lane / S::kChunks, chunk = lane % S::kChunks;
   bool full = left >= S::kSlots;
 #pragma unroll
@@ -357,48 +350,31 @@ struct Query {
 // The products of the query rows with 8 or 16 rows of K.
 template <int KIND, int D, int ROWS>
 __device__ __forceinline__ void qk(const Query<KIND, D, ROWS>& q, uint32_t stage, int lane,
-                                   float (*s)[kValues<ROWS>]) {
+                                   float s[][4]) {
   using S = Shape<KIND, D>;
-  // the operand rows of k-step k, row tile m
-  const auto rows = [&](int k, int m, uint32_t* f) {
-    const uint32_t* a = q.a[k] + 4 * m;
-    f[0] = a[0];
-    f[2] = a[1];
-    if constexpr (ROWS >= 16) {
-      f[1] = a[2];
-      f[3] = a[3];
-    } else {
-      f[1] = f[3] = 0;
-    }
-  };
 #pragma unroll
   for (int j = 0; j < S::NT; ++j) {
-#pragma unroll
-    for (int e = 0; e < kValues<ROWS>; ++e) s[j][e] = 0.f;
+    s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
 #pragma unroll
     for (int u = 0; u < S::KV; ++u) {
       const uint4 k = lds16(stage + S::k_at(8 * j + lane / 4, 4 * u + lane % 4));
       if constexpr (kIsBf16<KIND>) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-#pragma unroll
-          for (int m = 0; m < kValues<ROWS> / 4; ++m) {
-            uint32_t f[4];
-            rows(2 * u + i, m, f);
-            mma16<KIND>(s[j] + 4 * m, f, word(k, 2 * i), word(k, 2 * i + 1));
-          }
+          const uint32_t* a = q.a[2 * u + i];
+          const uint32_t f[4] = {a[0], ROWS == 16 ? a[2 % (2 * (ROWS / 8))] : 0u, a[1],
+                                 ROWS == 16 ? a[3 % (2 * (ROWS / 8))] : 0u};
+          mma16<KIND>(s[j], f, word(k, 2 * i), word(k, 2 * i + 1));
         }
-      } else if constexpr (kIsImage<KIND>) {
+      } else if constexpr (KIND == kImage) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
+          const uint32_t* a = q.a[4 * u + i];
+          const uint32_t f[4] = {a[0], ROWS == 16 ? a[2 % (2 * (ROWS / 8))] : 0u, a[1],
+                                 ROWS == 16 ? a[3 % (2 * (ROWS / 8))] : 0u};
           uint32_t b0, b1;
           e4m3_pairs(word(k, i), b0, b1);
-#pragma unroll
-          for (int m = 0; m < kValues<ROWS> / 4; ++m) {
-            uint32_t f[4];
-            rows(4 * u + i, m, f);
-            mma16<kImage>(s[j] + 4 * m, f, b0, b1);
-          }
+          mma16<KIND>(s[j], f, b0, b1);
         }
       } else {
         // rows g hold q's high part, rows g + 8 its low part: two products give all four terms
@@ -421,7 +397,7 @@ __device__ __forceinline__ void qk(const Query<KIND, D, ROWS>& q, uint32_t stage
 
 // o += p V.
 template <int KIND, int D, int ROWS>
-__device__ __forceinline__ void pv(uint32_t stage, int lane, const float (*p)[kValues<ROWS>],
+__device__ __forceinline__ void pv(uint32_t stage, int lane, const float p[][4],
                                    State<D, ROWS>& st) {
   using S = Shape<KIND, D>;
   // V load w of slot 8 j + 2 c + e
@@ -451,22 +427,19 @@ __device__ __forceinline__ void pv(uint32_t stage, int lane, const float (*p)[kV
 #pragma unroll
     for (int h = 0; h < (S::NT + 1) / 2; ++h) {      // 16 slots (or the only 8) at a time
       constexpr int N = S::NT < 2 ? 1 : 2;
-      constexpr int MT = kValues<ROWS> / 4;
-      uint32_t hi[MT][4] = {}, lo[MT][4] = {};
+      uint32_t hi[4] = {0, 0, 0, 0}, lo[4] = {0, 0, 0, 0};
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int j = 0; j < N; ++j) {
-          const float* y = p[2 * h + j] + 4 * m;
-          hi[m][2 * j] = pack2<KIND>(y[0], y[1]);
-          lo[m][2 * j] = rest2<KIND>(y[0], y[1], hi[m][2 * j]);
-          if constexpr (ROWS == 8) {
-            hi[m][2 * j + 1] = lo[m][2 * j];
-          } else {
-            hi[m][2 * j + 1] = pack2<KIND>(y[2], y[3]);
-            lo[m][2 * j + 1] = rest2<KIND>(y[2], y[3], hi[m][2 * j + 1]);
-          }
+      for (int j = 0; j < N; ++j) {
+        const float* y = p[2 * h + j];
+        hi[2 * j] = pack2<KIND>(y[0], y[1]);
+        lo[2 * j] = rest2<KIND>(y[0], y[1], hi[2 * j]);
+        if constexpr (ROWS == 8) {
+          hi[2 * j + 1] = lo[2 * j];
+        } else {
+          hi[2 * j + 1] = pack2<KIND>(y[2], y[3]);
+          lo[2 * j + 1] = rest2<KIND>(y[2], y[3], hi[2 * j + 1]);
         }
+      }
 #pragma unroll
       for (int w = 0; w < S::VV; ++w) {
         uint4 v[N][2];
@@ -476,7 +449,7 @@ __device__ __forceinline__ void pv(uint32_t stage, int lane, const float (*p)[kV
           v[j][1] = load(2 * h + j, 1, w);
         }
 #pragma unroll
-        for (int i = 0; i < (kIsImage<KIND> && D == 64 ? 2 : 4); ++i) {
+        for (int i = 0; i < (KIND == kImage && D == 64 ? 2 : 4); ++i) {
           uint32_t b[2][kIsBf16<KIND> ? 2 : 4] = {};
 #pragma unroll
           for (int j = 0; j < N; ++j) {
@@ -492,13 +465,10 @@ __device__ __forceinline__ void pv(uint32_t stage, int lane, const float (*p)[kV
           }
 #pragma unroll
           for (int e = 0; e < (kIsBf16<KIND> ? 2 : 4); ++e) {
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-              float* o = st.o[S::kPer * w + (kIsBf16<KIND> ? 2 : 4) * i + e] + 4 * m;
-              mma16<KIND>(o, hi[m], b[0][e], b[1][e]);
-              // sixteen rows leave no spare ones; fp16 probabilities (2^-11) do without
-              if constexpr (ROWS > 8 && kIsBf16<KIND>) mma16<KIND>(o, lo[m], b[0][e], b[1][e]);
-            }
+            float* o = st.o[S::kPer * w + (kIsBf16<KIND> ? 2 : 4) * i + e];
+            mma16<KIND>(o, hi, b[0][e], b[1][e]);
+            // sixteen rows leave no spare ones; fp16 probabilities (2^-11) do without
+            if constexpr (ROWS == 16 && kIsBf16<KIND>) mma16<KIND>(o, lo, b[0][e], b[1][e]);
           }
         }
       }
@@ -526,7 +496,7 @@ __device__ __forceinline__ void attend_part(const AttendArgs& g, const AttendUni
   float vref = 1.1754944e-38f;          // image: the largest value scale so far; o is in it
   const Where at(g, u);
   const long long blocks0 =
-      kIsImage<KIND> && !g.c.page_size ? image_scale_at(g.c, g.t.layer, u.s, u.h, 0, g.b) : 0;
+      KIND == kImage && !g.c.page_size ? image_scale_at(g.c, g.t.layer, u.s, u.h, 0, g.b) : 0;
   constexpr int kNext = S::kSlots * kWarps;
   static_assert(S::kStage <= kStageBytes, "");
   int page[S::NT];
@@ -542,7 +512,7 @@ __device__ __forceinline__ void attend_part(const AttendArgs& g, const AttendUni
 #pragma unroll
       for (int j = 0; j < S::NT; ++j) {
         if (lane == 0) meta[n].bad[j] = row[j] == -1;
-        if constexpr (kIsImage<KIND>) {
+        if constexpr (KIND == kImage) {
           const long long x =
               g.c.page_size ? row[j] >> g.b_shift : blocks0 + (t + 8 * j >> g.b_shift);
           const bool ok = row[j] >= 0;
@@ -569,13 +539,13 @@ __device__ __forceinline__ void attend_part(const AttendArgs& g, const AttendUni
 #pragma unroll
     for (int j = 0; j < S::NT; ++j) {
       bad_half[j] = meta[n].bad[j] != 0;
-      if constexpr (kIsImage<KIND>) {
+      if constexpr (KIND == kImage) {
         ks[j] = meta[n].ks[j];
         vs[j] = meta[n].vs[j];
       }
     }
     n = n == kDeep - 1 ? 0 : n + 1;
-    float s[S::NT][kValues<ROWS>];
+    float s[S::NT][4];
     qk<KIND, D, ROWS>(q, stage, lane, s);
 
     // logits in log2 units; beyond a row's limit or on a bad page: -inf
@@ -593,7 +563,7 @@ __device__ __forceinline__ void attend_part(const AttendArgs& g, const AttendUni
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
           float& z = s[j][2 * e + y];
-          z *= kIsImage<KIND> ? q.c1[e] * ks[j] : q.c1[e];
+          z *= KIND == kImage ? q.c1[e] * ks[j] : q.c1[e];
           if (mask && (bad_half[j] || t + 8 * j + 2 * (lane % 4) + y >= lim[e])) z = -INFINITY;
           top[e] = fmaxf(top[e], z);
         }
@@ -606,13 +576,13 @@ __device__ __forceinline__ void attend_part(const AttendArgs& g, const AttendUni
       up |= top[e] > st.m[e] + kSlack;
     }
     float vnew = vref;
-    if constexpr (kIsImage<KIND>) {
+    if constexpr (KIND == kImage) {
 #pragma unroll
       for (int j = 0; j < S::NT; ++j) vnew = fmaxf(vnew, vs[j]);
       up |= vnew > vref;
     }
     if (__any_sync(0xffffffffu, up)) {
-      const float vf = kIsImage<KIND> ? vref / vnew : 1.f;
+      const float vf = KIND == kImage ? vref / vnew : 1.f;
       vref = vnew;
       float f[ROWS / 8];
 #pragma unroll
@@ -624,12 +594,15 @@ __device__ __forceinline__ void attend_part(const AttendArgs& g, const AttendUni
         f[e] *= vf;
       }
 #pragma unroll
-      for (int n = 0; n < D / 8; ++n)
-#pragma unroll
-        for (int e = 0; e < kValues<ROWS>; ++e) st.o[n][e] *= f[ROWS == 8 ? 0 : e / 2];
+      for (int n = 0; n < D / 8; ++n) {
+        st.o[n][0] *= f[0];
+        st.o[n][1] *= f[0];
+        st.o[n][2] *= f[ROWS / 8 - 1];
+        st.o[n][3] *= f[ROWS / 8 - 1];
+      }
     }
     float vr[S::NT];
-    if constexpr (kIsImage<KIND>) {
+    if constexpr (KIND == kImage) {
 #pragma unroll
       for (int j = 0; j < S::NT; ++j) vr[j] = vs[j] / vref;
     }
@@ -643,16 +616,16 @@ __device__ __forceinline__ void attend_part(const AttendArgs& g, const AttendUni
           float& z = s[j][2 * e + y];
           z = ex2(z - sub);
           st.l[e] += z;
-          if constexpr (kIsImage<KIND>) z *= vr[j];
+          if constexpr (KIND == kImage) z *= vr[j];
         }
     }
     pv<KIND, D, ROWS>(stage, lane, s, st);
   }
-  if constexpr (kIsImage<KIND>) {
+  if constexpr (KIND == kImage) {
 #pragma unroll
     for (int n = 0; n < D / 8; ++n)
 #pragma unroll
-      for (int e = 0; e < kValues<ROWS>; ++e) st.o[n][e] *= vref;
+      for (int e = 0; e < 4; ++e) st.o[n][e] *= vref;
   }
 }
 
@@ -723,27 +696,25 @@ __global__ void __launch_bounds__(kWarps * 32, Ring<KIND, D, ROWS>::kPerSm)
 #pragma unroll
       for (int n = 0; n < D / 8; ++n)
 #pragma unroll
-        for (int e = 0; e < kValues<ROWS>; ++e) st.o[n][e] = 0.f;
+        for (int e = 0; e < 4; ++e) st.o[n][e] = 0.f;
 #pragma unroll
       for (int e = 0; e < ROWS / 8; ++e) {
         st.m[e] = -INFINITY;
         st.l[e] = 0.f;
       }
       const int ea = min(u.held, u.end), ta = (ea + kTileSlots - 1) / kTileSlots;
-      if constexpr (kIsImage<KIND>) {
-        constexpr int w = Shape<KIND, D>::kSlots, k = kTileSlots / w;
-        constexpr int wt = Shape<kTail, D>::kSlots, kt = kTileSlots / wt;
-        attend_part<KIND, D, ROWS, R::kDeep, R::kBytes>(
-            g, u, 0, ea, a0 * k + warp, min(min(a1, ta) * k, (ea + w - 1) / w), ring, s_meta[warp],
-            st);
-        attend_part<kTail, D, ROWS, R::kDeep, R::kBytes>(
-            g, u, ea, u.end, max(a0 - ta, 0) * kt + warp,
-            min((a1 - ta) * kt, (u.end - ea + wt - 1) / wt), ring, s_meta[warp], st);
+      if constexpr (KIND == kImage) {
+        constexpr int k = kTileSlots / Shape<kImage, D>::kSlots;
+        attend_part<kImage, D, ROWS, R::kDeep, R::kBytes>(g, u, 0, ea, a0 * k + warp,
+                                     min(min(a1, ta) * k, (ea + 31) / 32), ring, s_meta[warp], st);
+        constexpr int kt = kTileSlots / Shape<kTail, D>::kSlots;
+        attend_part<kTail, D, ROWS, R::kDeep, R::kBytes>(g, u, ea, u.end, max(a0 - ta, 0) * kt + warp,
+                                    min((a1 - ta) * kt, (u.end - ea + 7) / 8), ring, s_meta[warp],
+                                    st);
       } else {
-        constexpr int w = Shape<KIND, D>::kSlots, k = kTileSlots / w;
-        attend_part<KIND, D, ROWS, R::kDeep, R::kBytes>(
-            g, u, 0, u.end, a0 * k + warp, min(a1 * k, (u.end + w - 1) / w), ring, s_meta[warp],
-            st);
+        constexpr int k = kTileSlots / Shape<KIND, D>::kSlots, w = Shape<KIND, D>::kSlots;
+        attend_part<KIND, D, ROWS, R::kDeep, R::kBytes>(g, u, 0, u.end, a0 * k + warp, min(a1 * k, (u.end + w - 1) / w),
+                                   ring, s_meta[warp], st);
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
       __syncthreads();
@@ -767,8 +738,8 @@ __global__ void __launch_bounds__(kWarps * 32, Ring<KIND, D, ROWS>::kPerSm)
           if constexpr (ROWS == 8) {
             s_o[warp][lane / 4][f] = st.o[n][y] + st.o[n][2 + y];
           } else {
-#pragma unroll
-            for (int e = 0; e < ROWS / 8; ++e) s_o[warp][lane / 4 + 8 * e][f] = st.o[n][2 * e + y];
+            s_o[warp][lane / 4][f] = st.o[n][y];
+            s_o[warp][lane / 4 + 8][f] = st.o[n][2 + y];
           }
         }
       __syncthreads();
@@ -804,12 +775,11 @@ __global__ void __launch_bounds__(kWarps * 32, Ring<KIND, D, ROWS>::kPerSm)
 }
 
 // Joins the pieces of the unit that starts in block b and ends in a later one.
-template <int ROWS>
-constexpr int kJoinWarps = ROWS == 32 ? 32 : 16;
+constexpr int kJoinWarps = 16;
 template <int D, int ROWS>
-__global__ void __launch_bounds__(kJoinWarps<ROWS> * 32) attend_join_kernel(AttendArgs g) {
-  constexpr int E = D / 32, W = kJoinWarps<ROWS>, GR = W / ROWS;
-  __shared__ float s_o[W][D], s_m[W], s_l[W];
+__global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(AttendArgs g) {
+  constexpr int E = D / 32, GR = kJoinWarps / ROWS > 0 ? kJoinWarps / ROWS : 1;
+  __shared__ float s_o[kJoinWarps][D], s_m[kJoinWarps], s_l[kJoinWarps];
   grid_dep_wait();
   const int b = blockIdx.x;
   const int2 desc = g.ws.desc[b];
@@ -842,7 +812,7 @@ __global__ void __launch_bounds__(kJoinWarps<ROWS> * 32) attend_join_kernel(Atte
     s_l[warp] = l;
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < u.rows * D; i += W * 32) {
+  for (int i = threadIdx.x; i < u.rows * D; i += kJoinWarps * 32) {
     const int rr = i / D, f = i % D;
     float top = -INFINITY, sum = 0.f, x = 0.f;
     for (int w = rr * GR; w < (rr + 1) * GR; ++w) top = fmaxf(top, s_m[w]);
@@ -897,7 +867,7 @@ cudaError_t launch_attend(AttendArgs& g, cudaStream_t st, int* launches) {
   e = launch_after(attend_kernel<KIND, D, ROWS>, dim3(grid), dim3(kWarps * 32), smem, st, g);
   if (e != cudaSuccess) return e;
   note_launch(st, launches, "attend");
-  e = launch_after(attend_join_kernel<D, ROWS>, dim3(grid), dim3(kJoinWarps<ROWS> * 32), 0, st, g);
+  e = launch_after(attend_join_kernel<D, ROWS>, dim3(grid), dim3(kJoinWarps * 32), 0, st, g);
   if (e == cudaSuccess) note_launch(st, launches, "attend_join");
   return e;
 }
@@ -906,12 +876,10 @@ template <int D>
 cudaError_t launch_attend(AttendArgs& g, cudaStream_t st, int* launches) {
   if (g.c.dtype == NX_DTYPE_F32) return launch_attend<kF32, D, 8>(g, st, launches);
   if (attend_tc_takes(g.c, g.t, g.im.k != nullptr)) return launch_attend_tc(g, st, launches);
-  const long long rows = (long long)g.t.max_tokens * g.c.group;
-  const bool few = rows <= 8;
+  const bool few = (long long)g.t.max_tokens * g.c.group <= 8;
   if (g.im.k)
-    return few          ? launch_attend<kImage, D, 8>(g, st, launches)
-           : rows <= 16 ? launch_attend<kImage, D, 16>(g, st, launches)
-                        : launch_attend<kImage16, D, 32>(g, st, launches);
+    return few ? launch_attend<kImage, D, 8>(g, st, launches)
+               : launch_attend<kImage, D, 16>(g, st, launches);
   return few ? launch_attend<kBf16, D, 8>(g, st, launches)
              : launch_attend<kBf16, D, 16>(g, st, launches);
 }

@@ -946,8 +946,10 @@ size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 
 }  // namespace
 
+// The row kernel reads K and V once for 16 rows, this one once for 256 but at a higher cost, from
+// 8-bit rows more so.
 bool attend_tc_takes(const nx_cache& c, const nx_tokens& t, bool image) {
-  return c.dtype == NX_DTYPE_BF16 && (long long)t.max_tokens * c.group > (image ? 96 : 16);
+  return c.dtype == NX_DTYPE_BF16 && (long long)t.max_tokens * c.group > (image ? 32 : 16);
 }
 
 size_t attend_tc_layout(int D, char* base, AttendWs* ws) {
