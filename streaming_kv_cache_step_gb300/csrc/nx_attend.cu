@@ -484,8 +484,6 @@ __device__ __forceinline__ void attend_part(const AttendArgs& g, const AttendUni
   using S = Shape<KIND, D>;
   if (from >= to) return;
   const int lane = threadIdx.x % 32;
-  Query<KIND, D, ROWS> q;
-  q.load(g, u, lane);
   int lim[ROWS / 8];
 #pragma unroll
   for (int e = 0; e < ROWS / 8; ++e) {
@@ -527,6 +525,8 @@ __device__ __forceinline__ void attend_part(const AttendArgs& g, const AttendUni
   __syncwarp();                         // the warp is done with what the ring held before
 #pragma unroll
   for (int n = 0; n < kDeep - 1; ++n) start(from + n * kWarps, n);
+  Query<KIND, D, ROWS> q;               // while the first rows are on their way
+  q.load(g, u, lane);
   int n = 0;
   for (int i = from; i < to; i += kWarps) {
     const int t = base + S::kSlots * i;
@@ -786,11 +786,12 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(AttendArgs
   if (desc.x < 0) return;
   const AttendUnit u = attend_unit<ROWS>(g, desc.x);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int r = warp / GR, part = warp % GR;
+  const int groups = max(GR, u.rows <= ROWS / 4 ? 4 * GR : u.rows <= ROWS / 2 ? 2 * GR : GR);
+  const int r = warp / groups, part = warp % groups;    // as many warps per row as there are
   float m = -INFINITY, l = 0.f, o[E] = {};
   if (r < u.rows) {
 #pragma unroll 4
-    for (int i = b + part; i <= desc.y; i += GR) {
+    for (int i = b + part; i <= desc.y; i += groups) {
       const int slot = i == b ? 2 * b + 1 : 2 * i;
       const float2 x = g.ws.stat[slot * kPieceRows + r];
       const float* p = g.ws.out + ((long long)slot * kPieceRows + r) * D + lane;
@@ -815,8 +816,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(AttendArgs
   for (int i = threadIdx.x; i < u.rows * D; i += kJoinWarps * 32) {
     const int rr = i / D, f = i % D;
     float top = -INFINITY, sum = 0.f, x = 0.f;
-    for (int w = rr * GR; w < (rr + 1) * GR; ++w) top = fmaxf(top, s_m[w]);
-    for (int w = rr * GR; w < (rr + 1) * GR; ++w) {
+    for (int w = rr * groups; w < (rr + 1) * groups; ++w) top = fmaxf(top, s_m[w]);
+    for (int w = rr * groups; w < (rr + 1) * groups; ++w) {
       const float k = s_m[w] == -INFINITY ? (s_l[w] != s_l[w] ? 1.f : 0.f) : ex2(s_m[w] - top);
       sum += k * s_l[w];
       x += k * s_o[w][f];
@@ -859,6 +860,7 @@ cudaError_t launch_attend(AttendArgs& g, cudaStream_t st, int* launches) {
   const long long most = units * ((g.c.capacity + kTileSlots - 1) / kTileSlots + 1);
   if (most > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
   g.units = (int)units;
+  g.min_tiles = 2;
   const long long fit = kSms * R::kPerSm;
   const int grid = (int)(most < fit ? most : fit);
   constexpr int smem = kWarps * R::kDeep * R::kBytes;

@@ -923,6 +923,7 @@ cudaError_t launch_t(AttendArgs& g, cudaStream_t st, int* launches) {
   const long long most = units * ((g.c.capacity + kCols - 1) / kCols);
   if (most > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
   g.units = (int)units;
+  g.min_tiles = 1;
   cudaError_t e = allow_smem<attend_tc_kernel<D, NQ, IMAGE>>(smem);
   if (e != cudaSuccess) return e;
   const int grid = (int)(most < kTcGrid ? most : kTcGrid);
