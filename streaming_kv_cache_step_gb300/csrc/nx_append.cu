@@ -148,9 +148,22 @@ __global__ void __launch_bounds__(1024) append_kernel(AppendArgs g) {
       x.get(w + 4);
     }
     const int len = live && !is_q ? s_len[h] : 0;
-    // q: rows of tokens are rows * D apart; k, v: one row after the other within a page
-    T* dst = is_q ? static_cast<T*>(a.q_out) + (token * HQ + h) * D
-                  : static_cast<T*>(is_v ? c.v : c.k);
+    const bool writes = live && len >= 0;
+    // where the first token's row goes: the next ones follow `step` elements apart, but with
+    // pages every row of k and v is looked up
+    const bool lookup = !is_q && c.page_size;
+    T* dst = static_cast<T*>(is_q ? a.q_out : is_v ? c.v : c.k);
+    const int step = is_q ? HQ * D : D;
+    int32_t* pos_out = c.pos;
+    if (is_q) {
+      dst += (token * HQ + h) * D;
+    } else if (!lookup && writes) {
+      const long long row = row_of(c, g.t.layer, s, h, len + t0);
+      dst += row * D;
+      pos_out += row;
+    }
+    const bool keeps_pos = !is_q && !is_v && lane == 0;
+    const bool norms = __any_sync(0xffffffffu, weight != nullptr);   // the shuffles take the warp
     for (int t = 0; t < nt; t += kAhead) {
       Run4<T> x0[kAhead], x1[kAhead];
       if (live) {
@@ -167,19 +180,19 @@ __global__ void __launch_bounds__(1024) append_kernel(AppendArgs g) {
         float x[8];
         x0[i].get(x);
         x1[i].get(x + 4);
-        if (a.q_norm || a.k_norm) {                  // the shuffles take the whole warp
+        if (norms) {
           float ss = 0.f;
 #pragma unroll
           for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
 #pragma unroll
           for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
           if (weight) {
-            const float f = 1.0f / sqrtf(ss * (1.0f / D) + a.eps);
+            const float f = rsqrtf(ss * (1.0f / D) + a.eps);      // 2^-22, as exact as the rest
 #pragma unroll
             for (int j = 0; j < 8; ++j) x[j] = x[j] * f * w[j];
           }
         }
-        if (!live) continue;
+        if (!writes) continue;
         if (turns && !is_v) {
           const float4* cs = reinterpret_cast<const float4*>(s_rot[t + i] + 4 * lane);
           const float4 r0 = cs[0], r1 = cs[1];
@@ -201,19 +214,18 @@ __global__ void __launch_bounds__(1024) append_kernel(AppendArgs g) {
 #pragma unroll
           for (int j = 0; j < 8; ++j) x[j] = y[j];
         }
-        T* to = dst;
-        if (is_q) {
-          to += (long long)(t + i) * HQ * D;
-        } else {
-          if (len < 0) continue;
+        T* to = dst + (t + i) * step;
+        int32_t* p = pos_out + (t + i);
+        if (lookup) {
           const long long row = row_of(c, g.t.layer, s, h, len + t0 + t + i);
           if (row < 0) {
             atomicOr(g.dev_status, NX_DEV_BAD_PAGE);
             continue;
           }
-          to += row * D;
-          if (!is_v && lane == 0) c.pos[row] = s_pos[t + i];
+          to = dst + row * D;
+          p = c.pos + row;
         }
+        if (keeps_pos) *p = s_pos[t + i];
         store4(to + o0, x);
         store4(to + o1, x + 4);
       }
