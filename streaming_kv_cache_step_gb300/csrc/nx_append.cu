@@ -3,12 +3,12 @@
 //
 // One thread block takes kTokens tokens of one sequence. Its threads first compute the
 // cosines and sines of those tokens (one pair each, shared by all heads of a token: 128
-// features x 40 heads need 64 angles, not 2560), then a group of head_dim / 8 threads takes
-// one head row of every token in turn, 8 features per thread: what is the same for a head
-// (where it reads and writes, norm weights, the slice's length) is found once. A thread's 8
-// features are two runs of 4 that hold 4 whole pairs (runs 4i and rotary_dim / 2 + 4i, or 8i
-// and 8i + 4 when interleaved), so that a rotation needs no exchange between threads; only
-// the norm's sum does. Rows of kAhead tokens are in flight per thread.
+// features x 40 heads need 64 angles, not 2560), then a group of threads takes one head row of
+// every token in turn, 16 features per thread (8 of fp32): what is the same for a head (where
+// it reads and writes, norm weights, the slice's length) is found once. A thread's features are
+// two runs that hold whole pairs (with runs of R: R i and rotary_dim / 2 + R i, or 2 R i and
+// 2 R i + R when interleaved), so that a rotation needs no exchange between threads; only the
+// norm's sum does. Rows of kAhead tokens are in flight per thread.
 #include <type_traits>
 
 #include "nx_internal.cuh"
@@ -17,6 +17,7 @@ namespace nx {
 namespace {
 
 constexpr int kTokens = 16;           // tokens of a thread block
+constexpr int kMaxThreads = 768;
 constexpr int kAppendThreads = 256;   // threads of a block, unless one block covers a sequence
 
 struct AppendArgs {
@@ -47,40 +48,47 @@ __device__ __forceinline__ float2 rotation_of(int32_t p, uint64_t f) {
   return quarter & 2u ? make_float2(-c, -s) : make_float2(c, s);
 }
 
-template <typename T>
-struct Run4 {                         // four features of a row as they lie in memory
-  using Raw = typename std::conditional<sizeof(T) == 2, uint2, float4>::type;
+template <typename T, int RUN>
+struct Run {                          // RUN features of a row as they lie in memory
+  using Raw = typename std::conditional<sizeof(T) * RUN == 8, uint2, uint4>::type;
+  static_assert(sizeof(T) * RUN == sizeof(Raw), "");
   Raw r;
   __device__ __forceinline__ void load(const T* p) { r = *reinterpret_cast<const Raw*>(p); }
+  __device__ __forceinline__ void store(T* p) const { *reinterpret_cast<Raw*>(p) = r; }
   __device__ __forceinline__ void get(float* x) const {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(&r);
     if constexpr (sizeof(T) == 2) {
-      x[0] = __uint_as_float(r.x << 16);
-      x[1] = __uint_as_float(r.x & 0xFFFF0000u);
-      x[2] = __uint_as_float(r.y << 16);
-      x[3] = __uint_as_float(r.y & 0xFFFF0000u);
+#pragma unroll
+      for (int i = 0; i < RUN / 2; ++i) {
+        x[2 * i] = __uint_as_float(w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+      }
     } else {
-      x[0] = r.x; x[1] = r.y; x[2] = r.z; x[3] = r.w;
+#pragma unroll
+      for (int i = 0; i < RUN; ++i) x[i] = __uint_as_float(w[i]);
+    }
+  }
+  __device__ __forceinline__ void set(const float* x) {
+    uint32_t* w = reinterpret_cast<uint32_t*>(&r);
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+      for (int i = 0; i < RUN / 2; ++i) {
+        const __nv_bfloat162 a = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+        w[i] = reinterpret_cast<const uint32_t&>(a);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < RUN; ++i) w[i] = __float_as_uint(x[i]);
     }
   }
 };
 
-template <typename T>
-__device__ __forceinline__ void store4(T* p, const float* x) {
-  if constexpr (sizeof(T) == 2) {
-    const __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]);
-    const __nv_bfloat162 b = __floats2bfloat162_rn(x[2], x[3]);
-    *reinterpret_cast<uint2*>(p) = make_uint2(reinterpret_cast<const uint32_t&>(a),
-                                              reinterpret_cast<const uint32_t&>(b));
-  } else {
-    *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
-  }
-}
-
-template <typename T, int D>
-__global__ void __launch_bounds__(1024) append_kernel(AppendArgs g) {
-  constexpr int kLanes = D / 8;                      // threads of one head row
-  constexpr int kAhead = sizeof(T) == 2 ? 4 : 2;     // tokens loaded before one is used
-  __shared__ float2 s_rot[kTokens][D / 2];
+template <typename T, int D, int RUN>
+__global__ void __launch_bounds__(kMaxThreads) append_kernel(AppendArgs g) {
+  constexpr int N = 2 * RUN, kLanes = D / N;         // threads of one head row
+  constexpr int kAhead = 2;                          // tokens loaded before one is used
+  // by token, then pair e of thread l at [e / 2][l][e % 2]: neighbours read neighbouring words
+  __shared__ __align__(16) float2 s_rot[kTokens][D / 2];
   __shared__ int s_pos[kTokens];
   extern __shared__ int s_len[];                     // [kv_heads], -1: leave alone
   grid_dep_wait();
@@ -115,17 +123,19 @@ __global__ void __launch_bounds__(1024) append_kernel(AppendArgs g) {
     s_len[h] = len;
   }
   const int half = a.rotary_dim / 2;
-  for (int i = tid; i < nt * half; i += blockDim.x)
-    s_rot[i / half][i % half] = rotation_of(a.pos[first + t0 + i / half], a.rotary[i % half]);
+  for (int t = tid / 32; t < nt; t += blockDim.x / 32)
+    for (int i = tid % 32; i < half; i += 32)
+      s_rot[t][(i % RUN / 2 * kLanes + i / RUN) * 2 + i % 2] =
+          rotation_of(a.pos[first + t0 + t], a.rotary[i]);
   if (tid < nt) s_pos[tid] = a.pos[first + t0 + tid];
   __syncthreads();
 
-  // this thread's two runs of four features, and whether they turn
+  // this thread's two runs of features, and whether they turn
   const int lane = tid % kLanes;
-  const bool turns = lane < a.rotary_dim / 8;
+  const bool turns = lane < a.rotary_dim / N;
   const bool split = turns && !a.interleaved;
-  const int o0 = split ? 4 * lane : 8 * lane;
-  const int o1 = split ? half + 4 * lane : 8 * lane + 4;
+  const int o0 = split ? RUN * lane : N * lane;
+  const int o1 = split ? half + RUN * lane : N * lane + RUN;
   const int rows = HQ + 2 * H;                       // head rows per token: q, k, v
   const int groups = blockDim.x / kLanes;
   // a warp's groups take neighbouring head rows; a row that does not exist takes part in the
@@ -139,13 +149,13 @@ __global__ void __launch_bounds__(1024) append_kernel(AppendArgs g) {
     const T* src = static_cast<const T*>(is_q ? a.q : is_v ? a.v : a.k) + token * stride +
                    (long long)h * D;
     const T* weight = static_cast<const T*>(is_q ? a.q_norm : is_v ? nullptr : a.k_norm);
-    float w[8];
+    float w[N];
     if (weight && live) {
-      Run4<T> x;
+      Run<T, RUN> x;
       x.load(weight + o0);
       x.get(w);
       x.load(weight + o1);
-      x.get(w + 4);
+      x.get(w + RUN);
     }
     const int len = live && !is_q ? s_len[h] : 0;
     const bool writes = live && len >= 0;
@@ -165,7 +175,7 @@ __global__ void __launch_bounds__(1024) append_kernel(AppendArgs g) {
     const bool keeps_pos = !is_q && !is_v && lane == 0;
     const bool norms = __any_sync(0xffffffffu, weight != nullptr);   // the shuffles take the warp
     for (int t = 0; t < nt; t += kAhead) {
-      Run4<T> x0[kAhead], x1[kAhead];
+      Run<T, RUN> x0[kAhead], x1[kAhead];
       if (live) {
 #pragma unroll
         for (int i = 0; i < kAhead; ++i)
@@ -177,42 +187,41 @@ __global__ void __launch_bounds__(1024) append_kernel(AppendArgs g) {
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
         if (t + i >= nt) break;
-        float x[8];
+        float x[N];
         x0[i].get(x);
-        x1[i].get(x + 4);
+        x1[i].get(x + RUN);
         if (norms) {
           float ss = 0.f;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
+          for (int j = 0; j < N; ++j) ss = fmaf(x[j], x[j], ss);
 #pragma unroll
           for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
           if (weight) {
             const float f = rsqrtf(ss * (1.0f / D) + a.eps);      // 2^-22, as exact as the rest
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = x[j] * f * w[j];
+            for (int j = 0; j < N; ++j) x[j] = x[j] * f * w[j];
           }
         }
         if (!writes) continue;
         if (turns && !is_v) {
-          const float4* cs = reinterpret_cast<const float4*>(s_rot[t + i] + 4 * lane);
-          const float4 r0 = cs[0], r1 = cs[1];
-          const float co[4] = {r0.x, r0.z, r1.x, r1.z}, si[4] = {r0.y, r0.w, r1.y, r1.w};
-          float y[8];
-          if (a.interleaved) {
+          const float4* cs = reinterpret_cast<const float4*>(s_rot[t + i]) + lane;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              y[2 * j] = x[2 * j] * co[j] - x[2 * j + 1] * si[j];
-              y[2 * j + 1] = x[2 * j + 1] * co[j] + x[2 * j] * si[j];
-            }
-          } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              y[j] = x[j] * co[j] - x[j + 4] * si[j];
-              y[j + 4] = x[j + 4] * co[j] + x[j] * si[j];
+          for (int j = 0; j < RUN; j += 2) {
+            const float4 r = cs[j / 2 * kLanes];     // cos, sin of pairs j and j + 1
+            if (a.interleaved) {
+              const float p0 = x[2 * j], q0 = x[2 * j + 1], p1 = x[2 * j + 2], q1 = x[2 * j + 3];
+              x[2 * j] = p0 * r.x - q0 * r.y;
+              x[2 * j + 1] = q0 * r.x + p0 * r.y;
+              x[2 * j + 2] = p1 * r.z - q1 * r.w;
+              x[2 * j + 3] = q1 * r.z + p1 * r.w;
+            } else {
+              const float p0 = x[j], q0 = x[j + RUN], p1 = x[j + 1], q1 = x[j + 1 + RUN];
+              x[j] = p0 * r.x - q0 * r.y;
+              x[j + RUN] = q0 * r.x + p0 * r.y;
+              x[j + 1] = p1 * r.z - q1 * r.w;
+              x[j + 1 + RUN] = q1 * r.z + p1 * r.w;
             }
           }
-#pragma unroll
-          for (int j = 0; j < 8; ++j) x[j] = y[j];
         }
         T* to = dst + (t + i) * step;
         int32_t* p = pos_out + (t + i);
@@ -226,8 +235,10 @@ __global__ void __launch_bounds__(1024) append_kernel(AppendArgs g) {
           p = c.pos + row;
         }
         if (keeps_pos) *p = s_pos[t + i];
-        store4(to + o0, x);
-        store4(to + o1, x + 4);
+        x0[i].set(x);
+        x1[i].set(x + RUN);
+        x0[i].store(to + o0);
+        x1[i].store(to + o1);
       }
     }
   }
@@ -254,10 +265,10 @@ bool aligned(const void* p, long long stride, int size) {
   return ((uintptr_t)p & 15u) == 0 && stride >= 0 && (stride * size) % 16 == 0;
 }
 
-template <typename T, int D>
+template <typename T, int D, int RUN>
 cudaError_t launch_append(AppendArgs& g, cudaStream_t st, int* launches) {
   const int rows = (g.a.q ? g.c.kv_heads * g.c.group : 0) + 2 * g.c.kv_heads;
-  constexpr int kLanes = D / 8;
+  constexpr int kLanes = D / (2 * RUN);
   g.tiles = (int)(((long long)g.t.max_tokens + kTokens - 1) / kTokens);
   const bool in_place = !g.a.lens_in || g.a.lens_in == g.lens;
   int threads = kAppendThreads;
@@ -266,14 +277,14 @@ cudaError_t launch_append(AppendArgs& g, cudaStream_t st, int* launches) {
     // reads the lengths before it sets them, so that one launch does
     g.parts = 1;
     const long long want = (long long)rows * kLanes;
-    threads = want > 1024 ? 1024 : (int)((want + 31) / 32 * 32);
+    threads = want > kMaxThreads ? kMaxThreads : (int)((want + 31) / 32 * 32);
   } else {
     g.parts = (rows * kLanes + threads - 1) / threads;
   }
   g.set_lens = !in_place || g.tiles == 1;
   const long long blocks = (long long)g.c.seqs * g.tiles * g.parts;
   if (blocks > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
-  cudaError_t e = launch_after(append_kernel<T, D>, dim3((unsigned)blocks), dim3(threads),
+  cudaError_t e = launch_after(append_kernel<T, D, RUN>, dim3((unsigned)blocks), dim3(threads),
                                (size_t)g.c.kv_heads * 4, st, g);
   if (e != cudaSuccess) return e;
   note_launch(st, launches, "append");
@@ -328,11 +339,14 @@ extern "C" nx_status nexus_append(nx_cache* cache, const nx_tokens* tokens, cons
     return NX_ERR_INVALID_ARG;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;
-  if (size == 2)
-    e = D == 128 ? launch_append<__nv_bfloat16, 128>(g, st, &launches)
-                 : launch_append<__nv_bfloat16, 64>(g, st, &launches);
+  if (size == 4)
+    e = D == 128 ? launch_append<float, 128, 4>(g, st, &launches)
+                 : launch_append<float, 64, 4>(g, st, &launches);
+  else if (a.rotary_dim % 16 == 0)       // runs of 8 hold whole pairs: 16-byte loads
+    e = D == 128 ? launch_append<__nv_bfloat16, 128, 8>(g, st, &launches)
+                 : launch_append<__nv_bfloat16, 64, 8>(g, st, &launches);
   else
-    e = D == 128 ? launch_append<float, 128>(g, st, &launches)
-                 : launch_append<float, 64>(g, st, &launches);
+    e = D == 128 ? launch_append<__nv_bfloat16, 128, 4>(g, st, &launches)
+                 : launch_append<__nv_bfloat16, 64, 4>(g, st, &launches);
   return finish(e, launches);
 }
