@@ -17,6 +17,7 @@ namespace nx {
 namespace {
 
 constexpr int kTokens = 16;           // tokens of a thread block
+constexpr int kSoloTokens = 16;       // up to so many tokens one block takes a sequence
 constexpr int kMaxThreads = 768;
 constexpr int kAppendThreads = 256;   // threads of a block, unless one block covers a sequence
 
@@ -272,16 +273,17 @@ cudaError_t launch_append(AppendArgs& g, cudaStream_t st, int* launches) {
   g.tiles = (int)(((long long)g.t.max_tokens + kTokens - 1) / kTokens);
   const bool in_place = !g.a.lens_in || g.a.lens_in == g.lens;
   int threads = kAppendThreads;
-  if (g.tiles == 1) {
+  if (g.t.max_tokens <= kSoloTokens) {
     // few tokens: one block per sequence, with a thread group per head row as far as they go,
     // reads the lengths before it sets them, so that one launch does
     g.parts = 1;
     const long long want = (long long)rows * kLanes;
     threads = want > kMaxThreads ? kMaxThreads : (int)((want + 31) / 32 * 32);
   } else {
-    g.parts = (rows * kLanes + threads - 1) / threads;
+    g.parts = (rows * kLanes + threads - 1) / threads;       // even parts of the head rows
+    threads = ((rows + g.parts - 1) / g.parts * kLanes + 31) / 32 * 32;
   }
-  g.set_lens = !in_place || g.tiles == 1;
+  g.set_lens = !in_place || g.tiles * g.parts == 1;
   const long long blocks = (long long)g.c.seqs * g.tiles * g.parts;
   if (blocks > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
   cudaError_t e = launch_after(append_kernel<T, D, RUN>, dim3((unsigned)blocks), dim3(threads),
