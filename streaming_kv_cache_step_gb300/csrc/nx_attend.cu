@@ -54,13 +54,8 @@ __device__ __forceinline__ void mma16(float* d, const uint32_t* a, uint32_t b0, 
         "{%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-  else if constexpr (KIND == kImage)
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-        "{%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
   else
-    asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
         "{%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -94,10 +89,35 @@ __device__ __forceinline__ uint32_t rest2(float a, float b, uint32_t hi) {
   return pack2<KIND>(a - __low2float(h), b - __high2float(h));
 }
 
-// The part of a binary32 value that a tf32 operand holds exactly; the rest is the other term.
-__device__ __forceinline__ uint32_t tf32_hi(uint32_t x) { return x & 0xFFFFE000u; }
-__device__ __forceinline__ uint32_t tf32_lo(uint32_t x) {
-  return __float_as_uint(__uint_as_float(x) - __uint_as_float(tf32_hi(x)));
+// A binary32 value as the sum of two tf32 operands (11 bits each), to 2^-24 of it: the nearest
+// tf32, and the nearest to what that leaves.
+__device__ __forceinline__ uint32_t tf32_near(float x) {
+  uint32_t y;
+  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void tf32_terms(uint32_t x, uint32_t& hi, uint32_t& lo) {
+  hi = tf32_near(__uint_as_float(x));
+  lo = tf32_near(__uint_as_float(x) - __uint_as_float(hi));
+}
+// All four products of the terms of a (rows 0-7: high, 8-15: low) and b over 8 features or
+// slots, as two mma with a fresh accumulator: the tensor cores cut off what they add up
+// (their sums err to one side), so long sums are left to rounded additions.
+__device__ __forceinline__ void mma_f32(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  uint32_t h0, l0, h1, l1;
+  tf32_terms(b0, h0, l0);
+  tf32_terms(b1, h1, l1);
+  float t[4];
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(t[0]), "=f"(t[1]), "=f"(t[2]), "=f"(t[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(l0), "r"(l1), "f"(0.f));
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(t[0]), "+f"(t[1]), "+f"(t[2]), "+f"(t[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(h0), "r"(h1));
+  d[0] += t[0] + t[2];
+  d[1] += t[1] + t[3];
 }
 
 // How K and V of KIND reach the fragments. g = lane / 4 and c = lane % 4 as in an mma.
@@ -377,20 +397,15 @@ __device__ __forceinline__ void qk(const Query<KIND, D, ROWS>& q, uint32_t stage
           mma16<KIND>(s[j], f, b0, b1);
         }
       } else {
-        // rows g hold q's high part, rows g + 8 its low part: two products give all four terms
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const uint32_t* a = q.a[2 * u + i];
-          const uint32_t f[4] = {tf32_hi(a[0]), tf32_lo(a[0]), tf32_hi(a[1]), tf32_lo(a[1])};
-          const uint32_t b0 = word(k, 2 * i), b1 = word(k, 2 * i + 1);
-          mma16<KIND>(s[j], f, tf32_hi(b0), tf32_hi(b1));
-          mma16<KIND>(s[j], f, tf32_lo(b0), tf32_lo(b1));
+          uint32_t f[4];
+          tf32_terms(a[0], f[0], f[1]);
+          tf32_terms(a[1], f[2], f[3]);
+          mma_f32(s[j], f, word(k, 2 * i), word(k, 2 * i + 1));
         }
       }
-    }
-    if constexpr (KIND == kF32) {
-      s[j][0] += s[j][2];
-      s[j][1] += s[j][3];
     }
   }
 }
@@ -411,17 +426,14 @@ __device__ __forceinline__ void pv(uint32_t stage, int lane, const float p[][4],
     return x;
   };
   if constexpr (KIND == kF32) {
-    const uint32_t p0 = __float_as_uint(p[0][0]), p1 = __float_as_uint(p[0][1]);
-    const uint32_t f[4] = {tf32_hi(p0), tf32_lo(p0), tf32_hi(p1), tf32_lo(p1)};
+    uint32_t f[4];
+    tf32_terms(__float_as_uint(p[0][0]), f[0], f[1]);
+    tf32_terms(__float_as_uint(p[0][1]), f[2], f[3]);
 #pragma unroll
     for (int w = 0; w < S::VV; ++w) {
       const uint4 v0 = load(0, 0, w), v1 = load(0, 1, w);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint32_t b0 = word(v0, e), b1 = word(v1, e);
-        mma16<KIND>(st.o[4 * w + e], f, tf32_hi(b0), tf32_hi(b1));
-        mma16<KIND>(st.o[4 * w + e], f, tf32_lo(b0), tf32_lo(b1));
-      }
+      for (int e = 0; e < 4; ++e) mma_f32(st.o[4 * w + e], f, word(v0, e), word(v1, e));
     }
   } else {
 #pragma unroll
