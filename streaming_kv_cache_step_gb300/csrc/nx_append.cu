@@ -270,10 +270,11 @@ template <typename T, int D, int RUN>
 cudaError_t launch_append(AppendArgs& g, cudaStream_t st, int* launches) {
   const int rows = (g.a.q ? g.c.kv_heads * g.c.group : 0) + 2 * g.c.kv_heads;
   constexpr int kLanes = D / (2 * RUN);
-  g.tiles = (int)(((long long)g.t.max_tokens + kTokens - 1) / kTokens);
+  const int most = g.t.max_tokens < g.t.tokens ? g.t.max_tokens : g.t.tokens;
+  g.tiles = most > kTokens ? (int)(((long long)most + kTokens - 1) / kTokens) : 1;
   const bool in_place = !g.a.lens_in || g.a.lens_in == g.lens;
   int threads = kAppendThreads;
-  if (g.t.max_tokens <= kSoloTokens) {
+  if (most <= kSoloTokens) {
     // few tokens: one block per sequence, with a thread group per head row as far as they go,
     // reads the lengths before it sets them, so that one launch does
     g.parts = 1;
@@ -285,7 +286,6 @@ cudaError_t launch_append(AppendArgs& g, cudaStream_t st, int* launches) {
   }
   g.set_lens = !in_place || g.tiles * g.parts == 1;
   const long long blocks = (long long)g.c.seqs * g.tiles * g.parts;
-  if (blocks > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
   cudaError_t e = launch_after(append_kernel<T, D, RUN>, dim3((unsigned)blocks), dim3(threads),
                                (size_t)g.c.kv_heads * 4, st, g);
   if (e != cudaSuccess) return e;
@@ -316,7 +316,11 @@ extern "C" nx_status nexus_append(nx_cache* cache, const nx_tokens* tokens, cons
   if (a.rotary_dim < 0 || a.rotary_dim > D || a.rotary_dim % 8) return NX_ERR_INVALID_ARG;
   if ((a.rotary_dim > 0) != (a.rotary != nullptr) || ((uintptr_t)a.rotary & 7u))
     return NX_ERR_INVALID_ARG;
-  if (c.kv_heads > kMaxAppendHeads || (long long)c.kv_heads * c.group > (1 << 20))
+  // thread blocks: tiles of 16 tokens x parts of at least 16 head rows
+  const int most = tokens->max_tokens < tokens->tokens ? tokens->max_tokens : tokens->tokens;
+  const long long blocks = (long long)c.seqs * (most / kTokens + 1) *
+                           ((long long)c.kv_heads * (c.group + 2) / 16 + 1);
+  if (c.kv_heads > kMaxAppendHeads || blocks > 0x7FFFFFFFLL || (long long)c.kv_heads * c.group > (1 << 20))
     return NX_ERR_UNSUPPORTED;
   if ((a.q == nullptr) != (a.q_out == nullptr) && tokens->tokens > 0) return NX_ERR_INVALID_ARG;
   if (tokens->tokens > 0) {

@@ -19,17 +19,13 @@
 // The slots of all slices, 64 to a tile, are dealt out evenly to as many thread blocks as fit
 // the GPU at once, whatever the slices' lengths; a slice that a boundary cuts is joined by
 // attend_join_kernel.
-#include <cuda_fp8.h>
-
-#include <atomic>
-
 #include "nx_attend.cuh"
 
 namespace nx {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kAttendGrid = kSms * 4;  // thread blocks of one launch, at most
+constexpr int kAttendGrid = kSms * 3;  // thread blocks of one launch, at most
 constexpr int kPieceRows = 16;         // query rows of a piece, at most
 // kTail: bf16 rows behind an image, with their output features in the image's order
 enum Kind { kBf16 = 0, kImage = 1, kF32 = 2, kTail = 3 };
@@ -40,12 +36,6 @@ constexpr bool kIsBf16 = KIND == kBf16 || KIND == kTail;
 // than 2^kSlack above it, so they are at most 2^(kUp + kSlack) = 32768: below fp16's largest
 // value, with 2^-36 of the largest one still representable.
 constexpr float kUp = 11.f, kSlack = 4.f;
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 
 template <int KIND>
 __device__ __forceinline__ void mma16(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
@@ -61,19 +51,10 @@ __device__ __forceinline__ void mma16(float* d, const uint32_t* a, uint32_t b0, 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Four e4m3 codes as two pairs of fp16.
-__device__ __forceinline__ void e4m3_pairs(uint32_t four, uint32_t& lo, uint32_t& hi) {
-  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
-      "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
-      : "=r"(lo), "=r"(hi)
-      : "r"(four));
-}
-
 template <int KIND>
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
   if constexpr (kIsBf16<KIND>) {
-    const __nv_bfloat162 r = __floats2bfloat162_rn(a, b);
-    return reinterpret_cast<const uint32_t&>(r);
+    return bf16_pair(a, b);
   } else {
     const __half2 r = __floats2half2_rn(a, b);
     return reinterpret_cast<const uint32_t&>(r);
@@ -120,11 +101,14 @@ __device__ __forceinline__ void mma_f32(float* d, const uint32_t* a, uint32_t b0
   d[1] += t[1] + t[3];
 }
 
+// Slots of a thread block's tile: a step, or more, of each warp.
+template <int KIND>
+constexpr int kTileOf = KIND == kImage ? 128 : 64;
+
 // How K and V of KIND reach the fragments. g = lane / 4 and c = lane % 4 as in an mma.
 template <int KIND, int D>
 struct Shape {
   static constexpr int kSlots = KIND == kImage ? 32 : KIND == kBf16 ? 16 : 8;  // of a step
-  static constexpr int kTile = KIND == kImage ? 128 : 64;        // slots of a block's tile
   static constexpr int NT = kSlots / 8;                          // mma column tiles of them
   static constexpr int kBytes = KIND == kF32 ? 4 : kIsBf16<KIND> ? 2 : 1;
   static constexpr int kRow = D * kBytes;                        // bytes of a row
@@ -170,65 +154,24 @@ struct State {
   float m[ROWS / 8], l[ROWS / 8];
 };
 
-// Where a unit's rows lie. One page table entry per 8 slots is enough: pages and image blocks
-// are multiples of 8 rows, and so is every t below. Entries are fetched two steps ahead of the
-// rows they lead to, so that their latency is not added to the rows'.
-struct Where {
-  const int32_t* table;  // the sequence's pages; null: contiguous
-  long long first;       // contiguous: the slice's first row; paged: (layer, head)'s offset
-  long long per_page;    // rows from one page to the next
-  int shift, pages;
-
-  __device__ __forceinline__ Where(const AttendArgs& g, const AttendUnit& u) {
-    const nx_cache& c = g.c;
-    shift = 0;
-    pages = c.num_pages;
-    per_page = 0;
-    if (c.page_size) {
-      table = c.block_table + (long long)u.s * c.max_pages_per_seq;
-      shift = __ffs(c.page_size) - 1;
-      per_page = (long long)c.kv_heads << shift;
-      first = (long long)g.t.layer * c.num_pages * per_page + ((long long)u.h << shift);
-    } else {
-      table = nullptr;
-      first = (((long long)g.t.layer * c.seqs + u.s) * c.kv_heads + u.h) * c.capacity;
-    }
-  }
-  template <int NT>
-  __device__ __forceinline__ void pages_of(int t, int end, int* page) const {
+// The table entries and rows of the runs of a step from slot t on. Entries are fetched a step
+// before the rows they lead to, so that their latency is not added to the rows'.
+template <int NT>
+__device__ __forceinline__ void pages_of(const SlotRows& at, int t, int end, int* page) {
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
-      page[j] = table && t + 8 * j < end ? table[(t + 8 * j) >> shift] : 0;
-  }
-  // row indexes of slots t, t + 8; -1: a bad page, -2: nothing there
-  template <int NT>
-  __device__ __forceinline__ void rows_of(int t, int end, const int* page, long long* row) const {
+  for (int j = 0; j < NT; ++j) page[j] = at.page(t + 8 * j, end);
+}
+template <int NT>
+__device__ __forceinline__ void rows_of(const SlotRows& at, int t, int end, const int* page,
+                                        long long* row) {
 #pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      const int slot = t + 8 * j;
-      row[j] = slot >= end                             ? -2
-               : !table                                ? first + slot
-               : page[j] < 0 || page[j] >= pages       ? -1
-                   : first + page[j] * per_page + (slot & ((1 << shift) - 1));
-    }
-  }
-};
+  for (int j = 0; j < NT; ++j) row[j] = at.row(t + 8 * j, end, page[j]);
+}
 
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool ok) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "r"(ok ? 16 : 0)
-               : "memory");
-}
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
 __device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool ok) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src),
                "r"(ok ? 4 : 0)
                : "memory");
-}
-__device__ __forceinline__ uint32_t smem_at(const void* p) {
-  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
 __device__ __forceinline__ uint4 lds16(uint32_t at) {
   uint4 x;
@@ -504,7 +447,7 @@ __device__ __forceinline__ void attend_part(const AttendArgs& g, const AttendUni
   }
   const int low = min(end, u.low);
   float vref = 1.1754944e-38f;          // image: the largest value scale so far; o is in it
-  const Where at(g, u);
+  const SlotRows at(g, u);
   const long long blocks0 =
       KIND == kImage && !g.c.page_size ? image_scale_at(g.c, g.t.layer, u.s, u.h, 0, g.b) : 0;
   constexpr int kNext = S::kSlots * kWarps;
@@ -516,8 +459,8 @@ __device__ __forceinline__ void attend_part(const AttendArgs& g, const AttendUni
     const int t = base + S::kSlots * i;
     if (i < to) {
       long long row[S::NT];
-      at.rows_of<S::NT>(t, end, page, row);
-      at.pages_of<S::NT>(t + kNext, end, page);
+      rows_of<S::NT>(at, t, end, page, row);
+      pages_of<S::NT>(at, t + kNext, end, page);
       copy_rows<KIND, D>(g, row, end - t, lane, ring + n * kStageBytes);
 #pragma unroll
       for (int j = 0; j < S::NT; ++j) {
@@ -533,7 +476,7 @@ __device__ __forceinline__ void attend_part(const AttendArgs& g, const AttendUni
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  at.pages_of<S::NT>(base + S::kSlots * from, end, page);
+  pages_of<S::NT>(at, base + S::kSlots * from, end, page);
   __syncwarp();                         // the warp is done with what the ring held before
 #pragma unroll
   for (int n = 0; n < kDeep - 1; ++n) start(from + n * kWarps, n);
@@ -643,7 +586,7 @@ __device__ __forceinline__ void attend_part(const AttendArgs& g, const AttendUni
 
 template <int KIND>
 __device__ __forceinline__ int unit_tiles(const AttendUnit& u) {
-  constexpr int kTileSlots = Shape<KIND, 64>::kTile;
+  constexpr int kTileSlots = kTileOf<KIND>;
   if (!u.rows) return 0;
   const int ea = min(u.held, u.end);
   const int n = (ea + kTileSlots - 1) / kTileSlots + (u.end - ea + kTileSlots - 1) / kTileSlots;
@@ -675,7 +618,7 @@ __device__ __forceinline__ void finish_row(const AttendArgs& g, const AttendUnit
 template <int KIND, int D, int ROWS>
 __global__ void __launch_bounds__(kWarps * 32, Ring<KIND, D, ROWS>::kPerSm)
     attend_kernel(AttendArgs g) {
-  constexpr int kTileSlots = Shape<KIND, D>::kTile;
+  constexpr int kTileSlots = kTileOf<KIND>;
   using R = Ring<KIND, D, ROWS>;
   constexpr int kRing = R::kDeep * R::kBytes;
   // the rings, and over them, once a piece's steps are done, its warps' outputs
@@ -838,8 +781,6 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(AttendArgs
   }
 }
 
-size_t round256(size_t x) { return (x + 255) / 256 * 256; }
-
 size_t attend_layout(int D, char* base, AttendWs* ws) {
   size_t at = 0;
   ws->desc = reinterpret_cast<int2*>(base + at);
@@ -850,27 +791,14 @@ size_t attend_layout(int D, char* base, AttendWs* ws) {
   return at + (size_t)2 * kAttendGrid * kPieceRows * D * sizeof(float);
 }
 
-// Lets a kernel use so much dynamic shared memory, once per device (twice does no harm).
-template <void (*kernel)(AttendArgs)>
-cudaError_t allow_smem(int bytes) {
-  static std::atomic<bool> done[64];
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev >= 0 && dev < 64 && done[dev].load(std::memory_order_acquire)) return cudaSuccess;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev].store(true, std::memory_order_release);
-  return e;
-}
-
 template <int KIND, int D, int ROWS>
 cudaError_t launch_attend(AttendArgs& g, cudaStream_t st, int* launches) {
   using R = Ring<KIND, D, ROWS>;
-  g.mtiles = (int)(((long long)g.t.max_tokens * g.c.group + ROWS - 1) / ROWS);
-  const long long units = (long long)g.c.seqs * g.c.kv_heads * g.mtiles;
-  constexpr int kTileSlots = Shape<KIND, D>::kTile;
+  const long long mtiles = (most_tokens(g.t) * g.c.group + ROWS - 1) / ROWS;
+  const long long units = (long long)g.c.seqs * g.c.kv_heads * mtiles;
+  constexpr int kTileSlots = kTileOf<KIND>;
   const long long most = units * ((g.c.capacity + kTileSlots - 1) / kTileSlots + 1);
-  if (most > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
+  g.mtiles = (int)mtiles;
   g.units = (int)units;
   g.min_tiles = 2;
   const long long fit = kSms * R::kPerSm;
@@ -890,7 +818,7 @@ template <int D>
 cudaError_t launch_attend(AttendArgs& g, cudaStream_t st, int* launches) {
   if (g.c.dtype == NX_DTYPE_F32) return launch_attend<kF32, D, 8>(g, st, launches);
   if (attend_tc_takes(g.c, g.t, g.im.k != nullptr)) return launch_attend_tc(g, st, launches);
-  const bool few = (long long)g.t.max_tokens * g.c.group <= 8;
+  const bool few = most_tokens(g.t) * g.c.group <= 8;
   if (g.im.k)
     return few ? launch_attend<kImage, D, 8>(g, st, launches)
                : launch_attend<kImage, D, 16>(g, st, launches);
@@ -924,13 +852,19 @@ extern "C" nx_status nexus_attend(const nx_cache* cache, const nx_tokens* tokens
   const nx_attend& a = *args;
   if (image && !valid_image(image)) return NX_ERR_INVALID_ARG;
   if (image && c.dtype != NX_DTYPE_BF16) return NX_ERR_UNSUPPORTED;
+  // tiles (of at least 64 slots, and a partial one) of all units (of at least 8 rows)
+  const long long heads = (long long)c.kv_heads * c.group;
+  if (heads > (1 << 20) || (long long)c.seqs * c.kv_heads > (1 << 24) ||
+      (long long)c.seqs * c.kv_heads * (most_tokens(*tokens) * c.group / 8 + 1) >
+          0x7FFFFFFFLL / (c.capacity / 64 + 2))
+    return NX_ERR_UNSUPPORTED;
   const int size = c.dtype == NX_DTYPE_BF16 ? 2 : 4;
   if (!isfinite(a.scale)) return NX_ERR_INVALID_ARG;
   if (a.q_stride < 0 || a.out_stride < 0 || a.q_stride * size % 16 || a.out_stride * size % 16 ||
       ((uintptr_t)a.q & 15u) || ((uintptr_t)a.out & 15u))
     return NX_ERR_INVALID_ARG;
   if (tokens->tokens > 0 && (!a.q || !a.out)) return NX_ERR_INVALID_ARG;
-  if (tokens->tokens > 1 && a.out_stride < (long long)c.kv_heads * c.group * c.head_dim)
+  if (tokens->tokens > 1 && a.out_stride < heads * c.head_dim)
     return NX_ERR_INVALID_ARG;           // rows of out would overlap
   if (!ws || ((uintptr_t)ws & 255u) || ws_bytes < nexus_attend_workspace_bytes(cache, tokens))
     return NX_ERR_WORKSPACE;

@@ -2,7 +2,10 @@
 // and where the pieces of a split unit meet. Not part of the public ABI.
 #pragma once
 
+#include <cuda_fp8.h>
 #include <math.h>
+
+#include <atomic>
 
 #include "nx_internal.cuh"
 
@@ -129,6 +132,91 @@ __device__ __forceinline__ AttendShare attend_share(const AttendArgs& g, const T
   x.unit = s_at[0];
   x.at = s_at[1];
   return x;
+}
+
+// Where a unit's rows lie. A run of 8 slots that starts at a multiple of 8 needs one page table
+// entry: pages and image blocks are multiples of 8 rows.
+struct SlotRows {
+  const int32_t* table;  // the sequence's pages; null: contiguous
+  long long first;       // contiguous: the slice's first row; paged: (layer, head)'s offset
+  long long per_page;    // rows from one page to the next
+  int shift, pages;
+
+  __device__ __forceinline__ SlotRows(const AttendArgs& g, const AttendUnit& u) {
+    const nx_cache& c = g.c;
+    shift = 0;
+    pages = c.num_pages;
+    per_page = 0;
+    if (c.page_size) {
+      table = c.block_table + (long long)u.s * c.max_pages_per_seq;
+      shift = __ffs(c.page_size) - 1;
+      per_page = (long long)c.kv_heads << shift;
+      first = (long long)g.t.layer * c.num_pages * per_page + ((long long)u.h << shift);
+    } else {
+      table = nullptr;
+      first = (((long long)g.t.layer * c.seqs + u.s) * c.kv_heads + u.h) * c.capacity;
+    }
+  }
+  __device__ __forceinline__ int page(int slot, int end) const {
+    return table && slot < end ? table[slot >> shift] : 0;
+  }
+  // row of a slot below `end`, given its page() ; -1: a bad page, -2: at or beyond `end`
+  __device__ __forceinline__ long long row(int slot, int end, int page) const {
+    return slot >= end                 ? -2
+           : !table                    ? first + slot
+           : page < 0 || page >= pages ? -1
+                                       : first + page * per_page + (slot & ((1 << shift) - 1));
+  }
+};
+
+__device__ __forceinline__ uint32_t smem_at(const void* p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+// Asynchronous copy of 16 bytes to shared memory, or of as many zeros.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool ok) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(ok ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// 2^x to about 2^-22.
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
+  const __nv_bfloat162 r = __floats2bfloat162_rn(a, b);
+  return reinterpret_cast<const uint32_t&>(r);
+}
+// Four e4m3 codes as two pairs of fp16.
+__device__ __forceinline__ void e4m3_pairs(uint32_t four, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(four));
+}
+
+// Lets a kernel use so much dynamic shared memory, once per device (twice does no harm).
+template <auto kernel>
+cudaError_t allow_smem(int bytes) {
+  static std::atomic<bool> done[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 0 && dev < 64 && done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev].store(true, std::memory_order_release);
+  return e;
+}
+
+inline size_t round256(size_t x) { return (x + 255) / 256 * 256; }
+
+// The most tokens that one sequence can own.
+inline long long most_tokens(const nx_tokens& t) {
+  return t.max_tokens < t.tokens ? t.max_tokens : t.tokens;
 }
 
 // nx_attend_tc.cu: the tensor-core kernel for many query rows per slice (bf16 caches), its

@@ -26,9 +26,6 @@
 // more, issues nothing more and ends, its TMEM freed.
 #include <cuda.h>
 #include <cudaTypedefs.h>
-#include <cuda_fp8.h>
-
-#include <atomic>
 
 #include "nx_attend.cuh"
 
@@ -44,9 +41,6 @@ constexpr int kTcGrid = kSms;
 constexpr int kPolls = 1 << 20;               // mbarrier polls before giving up
 constexpr float kRaise = 8.f;              // log2 units
 
-__device__ __forceinline__ uint32_t smem_at(const void* p) {
-  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
 __device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count));
 }
@@ -192,16 +186,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t* r) {
 __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
-  const __nv_bfloat162 r = __floats2bfloat162_rn(a, b);
-  return reinterpret_cast<const uint32_t&>(r);
-}
-
 template <int D, int NQ, bool IMAGE>
 struct Plan {
   // three warps per scheduler leave 168 registers a thread, four 128: 8-bit rows need the
@@ -224,44 +208,6 @@ struct Plan {
 template <int NQ>
 __device__ __forceinline__ int tc_tiles(const AttendUnit& u) {
   return !u.rows ? 0 : u.end ? (u.end + kCols - 1) / kCols : 1;
-}
-
-// Rows of 8-slot groups of a unit, as in a page table.
-struct TcRows {
-  const int32_t* table;
-  long long first, per_page;
-  int shift, pages;
-  __device__ __forceinline__ TcRows(const AttendArgs& g, const AttendUnit& u) {
-    const nx_cache& c = g.c;
-    shift = 0;
-    pages = c.num_pages;
-    per_page = 0;
-    if (c.page_size) {
-      table = c.block_table + (long long)u.s * c.max_pages_per_seq;
-      shift = __ffs(c.page_size) - 1;
-      per_page = (long long)c.kv_heads << shift;
-      first = (long long)g.t.layer * c.num_pages * per_page + ((long long)u.h << shift);
-    } else {
-      table = nullptr;
-      first = (((long long)g.t.layer * c.seqs + u.s) * c.kv_heads + u.h) * c.capacity;
-    }
-  }
-  __device__ __forceinline__ int page(int slot, int end) const {
-    return table && slot < end ? table[slot >> shift] : 0;
-  }
-  // row of a slot; -1: a bad page, -2: nothing there
-  __device__ __forceinline__ long long row(int slot, int end, int page) const {
-    return slot >= end              ? -2
-           : !table                 ? first + slot
-           : page < 0 || page >= pages ? -1
-                                    : first + page * per_page + (slot & ((1 << shift) - 1));
-  }
-};
-
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool ok) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "r"(ok ? 16 : 0)
-               : "memory");
 }
 
 // The copies of 8 bf16 rows of K or V (slots t .. t + 7, one warp) to rows r .. r + 7 of a ring
@@ -300,6 +246,7 @@ __device__ __forceinline__ void expand_tile(uint32_t raw, const float* scale, in
                    : "r"(raw + c * 8)
                    : "memory");
       f[i] = scale[r / 8];
+      if (f[i] == 0.f) x[i][0] = x[i][1] = 0;      // a bad page: its codes were not copied
     }
   }
 #pragma unroll
@@ -309,10 +256,7 @@ __device__ __forceinline__ void expand_tile(uint32_t raw, const float* scale, in
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       uint32_t h0, h1;
-      asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
-          "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
-          : "=r"(h0), "=r"(h1)
-          : "r"(x[i][j]));
+      e4m3_pairs(x[i][j], h0, h1);
       const float2 v0 = __half22float2(reinterpret_cast<const __half2&>(h0));
       const float2 v1 = __half22float2(reinterpret_cast<const __half2&>(h1));
       y[2 * j] = bf16_pair(v0.x * f[i], v0.y * f[i]);
@@ -419,7 +363,7 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
       if (warp >= kLoadWarp && warp < kIssueWarp) {
         // ---- loader ----
         const int lt = tid - 32 * kLoadWarp, lw = warp - kLoadWarp;
-        const TcRows rows(g, u);
+        const SlotRows rows(g, u);
         // K and V tiles in turn, every warp its runs of 8 slots
         const auto announce = [&](int k) {
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -876,19 +820,6 @@ __global__ void __launch_bounds__(kTcRows) attend_tc_join_kernel(AttendArgs g) {
   if (d0 == 0) store_lse(g, u, r, m, l);
 }
 
-// Lets a kernel use so much dynamic shared memory, once per device (twice does no harm).
-template <void (*kernel)(CUtensorMap, CUtensorMap, bool, AttendArgs)>
-cudaError_t allow_smem(int bytes) {
-  static std::atomic<bool> done[64];
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev >= 0 && dev < 64 && done[dev].load(std::memory_order_acquire)) return cudaSuccess;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev].store(true, std::memory_order_release);
-  return e;
-}
-
 // Rows of head_dim bf16 values in boxes of 64 features x a page (or a tile); false if the
 // driver does not take it or the rows do not fit its 32-bit coordinates.
 bool encode_rows(const nx_cache& c, void* base, CUtensorMap* map) {
@@ -917,11 +848,10 @@ bool encode_rows(const nx_cache& c, void* base, CUtensorMap* map) {
 template <int D, int NQ, bool IMAGE>
 cudaError_t launch_t(AttendArgs& g, cudaStream_t st, int* launches) {
   constexpr int smem = Plan<D, NQ, IMAGE>::kSmem;
-  const long long all = (long long)g.t.max_tokens * g.c.group;
+  const long long all = most_tokens(g.t) * g.c.group;
   g.mtiles = (int)((all + kRows * NQ - 1) / (kRows * NQ));
   const long long units = (long long)g.c.seqs * g.c.kv_heads * g.mtiles;
   const long long most = units * ((g.c.capacity + kCols - 1) / kCols);
-  if (most > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
   g.units = (int)units;
   g.min_tiles = 1;
   cudaError_t e = allow_smem<attend_tc_kernel<D, NQ, IMAGE>>(smem);
@@ -943,14 +873,12 @@ cudaError_t launch_t(AttendArgs& g, cudaStream_t st, int* launches) {
   return g.im.k ? launch_t<D, NQ, true>(g, st, launches) : launch_t<D, NQ, false>(g, st, launches);
 }
 
-size_t round256(size_t x) { return (x + 255) / 256 * 256; }
-
 }  // namespace
 
 // The row kernel reads K and V once for 16 rows, this one once for 256 but at a higher cost, from
 // 8-bit rows more so.
 bool attend_tc_takes(const nx_cache& c, const nx_tokens& t, bool image) {
-  return c.dtype == NX_DTYPE_BF16 && (long long)t.max_tokens * c.group > (image ? 32 : 16);
+  return c.dtype == NX_DTYPE_BF16 && most_tokens(t) * c.group > (image ? 32 : 16);
 }
 
 size_t attend_tc_layout(int D, char* base, AttendWs* ws) {
@@ -964,7 +892,7 @@ size_t attend_tc_layout(int D, char* base, AttendWs* ws) {
 }
 
 cudaError_t launch_attend_tc(AttendArgs& g, cudaStream_t st, int* launches) {
-  const bool two = (long long)g.t.max_tokens * g.c.group > kRows;
+  const bool two = most_tokens(g.t) * g.c.group > kRows;
   if (g.c.head_dim == 128)
     return two ? launch_t<128, 2>(g, st, launches) : launch_t<128, 1>(g, st, launches);
   return two ? launch_t<64, 2>(g, st, launches) : launch_t<64, 1>(g, st, launches);

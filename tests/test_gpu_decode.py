@@ -573,3 +573,87 @@ def test_decode_calls_replay_from_a_graph():
     torch.cuda.synchronize()
     assert int(st.item()) == 0
     assert torch.equal(out, ref) and torch.equal(cache.lens, ref_lens)
+
+
+# ---------------------------------------------------------------------------
+# many query rows: pages, bounds, wide loops
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("kind", ["bf16", "image"])
+@pytest.mark.parametrize("page", [8, 16, 64, 128])
+def test_attend_bad_page_under_many_rows(kind, page):
+    # a page out of range is left out of every row's sums, whatever kernel takes the call
+    c = Case(seqs=2, kv_heads=2, group=4, page=page, capacity=640, lens=[[640, 600], [300, 511]], seed=page)
+    cache, st = c.device_cache(), _status()
+    im = None
+    if kind == "image":
+        im = _image(c, cache)
+        nexus.quantize(cache, im, st)
+    which = 256 // page
+    cache.block_table[0, which] = c.pages + 5
+    n = 24                                                           # 96 rows per slice
+    q = torch.randn(2 * n, 8, 128, generator=c.g).to(BF)
+    out = torch.full((2 * n, 8, 128), math.nan, dtype=BF, device=DEV)
+    ws = nexus.alloc_attend_workspace(cache, tokens=2 * n, max_tokens=n)
+    nexus.attend(cache, 0, q.to(DEV), out, ws, st, max_tokens=n, image=im)
+    torch.cuda.synchronize()
+    assert int(st.item()) == nexus.NX_DEV_BAD_PAGE
+    assert torch.isfinite(out.float()).all()
+    for s in range(2):
+        for h in range(2):
+            T = int(c.lens[0, s, h])
+            at = c.at(0, s, h, T)
+            slots = torch.arange(T)
+            good = (slots // page != which) if s == 0 else slots >= 0
+            k, v = c.k[at][good].double(), c.v[at][good].double()
+            rows = q[s * n:(s + 1) * n, h * 4:(h + 1) * 4].reshape(-1, 128)
+            M = [int((slots[:T - (n - 1 - i)] >= 0)[good[:T - (n - 1 - i)]].sum())
+                 for i in range(n) for _ in range(4)]
+            ref, _, A, _ = attend64(rows, k, v, M, 128 ** -0.5)
+            got = out[s * n:(s + 1) * n, h * 4:(h + 1) * 4].reshape(-1, 128).cpu().double()
+            # the image's own rounding: half a step of e4m3, 2^-4, of keys and values
+            tol = (2.0 ** -6 if im is None else 0.5) * A + 2.0 ** -8
+            assert torch.all((got - ref).abs() <= tol), (s, h)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "image", "f32"])
+def test_attend_bound_far_above_the_tokens(kind):
+    # max_tokens is only a bound: 3 tokens under a bound of 2^30
+    c = Case(seqs=3, kv_heads=2, group=2, dtype=F32 if kind == "f32" else BF, capacity=64, lens=40, seed=3)
+    cache, st = c.device_cache(), _status()
+    im = None
+    if kind == "image":
+        im = _image(c, cache)
+        nexus.quantize(cache, im, st)
+    cu = c.cu([1, 0, 2]).to(DEV)
+    q = torch.randn(3, 4, 128, generator=c.g).to(DEV, c.dtype)
+    a, b = torch.empty_like(q), torch.empty_like(q)
+    ws = nexus.alloc_attend_workspace(cache, tokens=3, max_tokens=1 << 30)
+    nexus.attend(cache, 0, q, a, ws, st, max_tokens=1 << 30, cu_tokens=cu, image=im)
+    nexus.attend(cache, 0, q, b, ws, st, max_tokens=2, cu_tokens=cu, image=im)
+    kv = torch.zeros(3, 2, 128, dtype=c.dtype, device=DEV)
+    nexus.append(cache, 0, None, kv, kv, torch.zeros(3, dtype=torch.int32, device=DEV), None, st,
+                 max_tokens=1 << 30, cu_tokens=cu)
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0
+    assert torch.equal(a, b)
+    assert cache.lens[0].tolist() == [[41, 41], [40, 40], [42, 42]]
+
+
+@pytest.mark.parametrize("kind", ["bf16", "image"])
+@pytest.mark.parametrize("group,tokens", [(8, 17), (4, 64), (2, 129), (16, 40)])
+def test_attend_many_rows_split_over_blocks(kind, group, tokens):
+    # long slices of few sequences: every unit's pieces come from many thread blocks
+    c = Case(seqs=1, kv_heads=2, group=group, capacity=6000, lens=[[6000, 4321]], seed=tokens)
+    _check_attend(c, [tokens], image=kind == "image")
+    _check_attend(c, [tokens], image=kind == "image", causal=False, scale=-0.05)
+
+
+def test_attend_many_sequences_many_rows():
+    # more units than thread blocks, ragged, some empty
+    rng = np.random.default_rng(0)
+    lens = rng.integers(0, 200, (60, 3))
+    c = Case(seqs=60, kv_heads=3, group=2, d=64, page=16, capacity=208, lens=lens, seed=1)
+    n = rng.integers(0, 20, 60).tolist()
+    _check_attend(c, n)
+    _check_attend(c, n, image=True)
