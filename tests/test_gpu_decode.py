@@ -657,3 +657,53 @@ def test_attend_many_sequences_many_rows():
     n = rng.integers(0, 20, 60).tolist()
     _check_attend(c, n)
     _check_attend(c, n, image=True)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("group", [4, 16, 40, 200])
+@pytest.mark.parametrize("scale", [1.0, 2.0 ** -30, 2.0 ** 7, 2.0 ** 9, 2.0 ** 100, 0.7])
+def test_attend_reads_every_code(d, group, scale):
+    # equal keys and 32 equal value rows per block: the output is the value, code times scale,
+    # for every finite code, below the normal range too (0.7: any scale will do)
+    c = Case(seqs=4, kv_heads=1, group=group, d=d, capacity=64, lens=64, seed=1)
+    cache, st = c.device_cache(), _status()
+    cache.k.zero_()
+    im = _image(c, cache)
+    im.k.view(torch.uint8).zero_()
+    codes = torch.arange(256, dtype=torch.uint8)
+    codes[(codes & 0x7F) == 0x7F] = 0x35
+    if d == 64:
+        rows = codes.view(4, 64)
+    else:
+        rows = codes.view(2, 128).repeat(2, 1)
+    im.v.view(torch.uint8)[0, :, 0] = rows[:, None].to(DEV)
+    im.k_scale.fill_(1.0)
+    im.v_scale.fill_(scale)
+    im.rows.fill_(64)
+    q = torch.randn(4, group, d, generator=c.g).to(DEV, BF)
+    out = torch.full_like(q, math.nan)
+    ws = nexus.alloc_attend_workspace(cache, tokens=4, max_tokens=1)
+    nexus.attend(cache, 0, q, out, ws, st, max_tokens=1, image=im)
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0
+    want = rows.view(torch.float8_e4m3fn).double() * torch.tensor(scale, dtype=torch.float32).double()
+    # 64 equal probabilities: sums of equal terms; a scale that is no power of two is rounded
+    # with its values once more
+    err = (out.cpu().double() - want[:, None]).abs()
+    assert torch.all(err <= (2.0 ** -16 if scale != 0.7 else 2.0 ** -7) * want[:, None].abs())
+
+
+@pytest.mark.parametrize("group", [4, 16, 40])
+def test_attend_nan_codes_give_nan(group):
+    c = Case(seqs=2, kv_heads=1, group=group, capacity=64, lens=64, seed=1)
+    c.v[0, 1, 0, 7, 3] = math.nan
+    cache, st = c.device_cache(), _status()
+    im = _image(c, cache)
+    nexus.quantize(cache, im, st)
+    q = torch.randn(2, group, 128, generator=c.g).to(DEV, BF)
+    out = torch.zeros_like(q)
+    ws = nexus.alloc_attend_workspace(cache, tokens=2, max_tokens=1)
+    nexus.attend(cache, 0, q, out, ws, st, max_tokens=1, image=im)
+    torch.cuda.synchronize()
+    bad = torch.isnan(out.float())
+    assert not bad[0].any() and bad[1, :, 3].all() and not bad[1, :, :3].any() and not bad[1, :, 4:].any()
