@@ -8,7 +8,12 @@
 // it reads and writes, norm weights, the slice's length) is found once. A thread's features are
 // two runs that hold whole pairs (with runs of R: R i and rotary_dim / 2 + R i, or 2 R i and
 // 2 R i + R when interleaved), so that a rotation needs no exchange between threads; only the
-// norm's sum does. Rows of kAhead tokens are in flight per thread.
+// norm's sum does. The rows of the next kAhead tokens are loaded while these are worked on.
+//
+// What bounds it: reads and writes of head rows, 2 B a value each way, at 85 us for the prompts
+// below if they ran at the copy rate; measured 108 us (20500 tokens of 40 normed and rotated and
+// 8 plain head rows of 128, bf16: 4.7 TB/s). A single token of 48 head rows takes 3.1 us, all
+// latency.
 #include <type_traits>
 
 #include "nx_internal.cuh"
@@ -18,7 +23,9 @@ namespace {
 
 constexpr int kTokens = 16;           // tokens of a thread block
 constexpr int kSoloTokens = 16;       // up to so many tokens one block takes a sequence
-constexpr int kMaxThreads = 768;
+// The largest block, and with it the registers of a thread: 640 leave 96 (108 us for 8192-token
+// prompts); 768 leave 80 and spill (113 us), 512 leave 128 and fewer warps (137 us).
+constexpr int kMaxThreads = 640;
 constexpr int kAppendThreads = 256;   // threads of a block, unless one block covers a sequence
 
 struct AppendArgs {
@@ -175,16 +182,24 @@ __global__ void __launch_bounds__(kMaxThreads) append_kernel(AppendArgs g) {
     }
     const bool keeps_pos = !is_q && !is_v && lane == 0;
     const bool norms = __any_sync(0xffffffffu, weight != nullptr);   // the shuffles take the warp
+    Run<T, RUN> n0[kAhead], n1[kAhead];              // the rows that come next
+    const auto fetch = [&](int t) {
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i)
+        if (live && t + i < nt) {
+          n0[i].load(src + (t + i) * stride + o0);
+          n1[i].load(src + (t + i) * stride + o1);
+        }
+    };
+    fetch(0);
     for (int t = 0; t < nt; t += kAhead) {
       Run<T, RUN> x0[kAhead], x1[kAhead];
-      if (live) {
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i)
-          if (t + i < nt) {
-            x0[i].load(src + (t + i) * stride + o0);
-            x1[i].load(src + (t + i) * stride + o1);
-          }
+      for (int i = 0; i < kAhead; ++i) {
+        x0[i] = n0[i];
+        x1[i] = n1[i];
       }
+      fetch(t + kAhead);
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
         if (t + i >= nt) break;
