@@ -357,7 +357,8 @@ typedef struct nx_attend {
   int32_t causal;              /* nonzero: see below */
 } nx_attend;
 
-/* Bytes of workspace nexus_attend needs for these arguments (0 on invalid arguments). */
+/* Bytes of workspace nexus_attend needs for these arguments, with an image or without (0 on
+   invalid arguments); it goes by head_dim and by whether max_tokens * group is above 16. */
 size_t nexus_attend_workspace_bytes(const nx_cache* cache, const nx_tokens* tokens);
 
 /*
@@ -368,8 +369,15 @@ size_t nexus_attend_workspace_bytes(const nx_cache* cache, const nx_tokens* toke
  * nexus_append leaves them), M = lens otherwise. M <= 0 gives out = 0 and lse = -inf.
  * image (nullable): slots below image->rows are read from it (code times scale) instead of
  * the cache. Slices flagged NX_DEV_BAD_LEN or NX_DEV_BAD_IMAGE count as empty; a row on a
- * page out of range (NX_DEV_BAD_PAGE) is left out of the sums. Rows at or beyond lens are
- * never read into a result, whatever they hold.
+ * page out of range (NX_DEV_BAD_PAGE) is left out of the sums; tokens of a sequence flagged
+ * NX_DEV_BAD_TOKENS get no output. Rows at or beyond lens never show in a result, whatever they
+ * hold. A row below lens that is not finite shows in its own slice only; a value row there
+ * shows also in the outputs of tokens of this call that do not see it yet (their weight is 0,
+ * and 0 times an infinity or NaN is NaN). Up to 16 query rows per slice (max_tokens * group;
+ * 32 from an image) go to a kernel that streams rows through mma.sync, more to one on
+ * tcgen05; fp32 caches always to the first. Two launches; the same bits every time.
+ * NX_ERR_UNSUPPORTED for an image of an fp32 cache, for more than 2^20 query heads or 2^24
+ * (sequence, KV head) pairs, or more than 2^31 tiles of 8 query rows x 64 slots.
  */
 nx_status nexus_attend(const nx_cache* cache, const nx_tokens* tokens, const nx_image* image,
                        const nx_attend* args, void* ws, size_t ws_bytes, int32_t* dev_status,

@@ -24,6 +24,12 @@
 // with one product each; else as one (half a step of bf16, 2^-8, in each p).
 // Every wait is bounded; when one gives up, the block flags NX_DEV_TIMEOUT, waits for nothing
 // more, issues nothing more and ends, its TMEM freed.
+//
+// Measured: two chunks of 512 tokens, 8 x 4 heads, over 8704 rows: 134 us on the GPU, 1.09 PFLOP/s,
+// 59 % of a plain bf16 product's rate; a step of a stream (64 slots) takes about 2000 clocks, of
+// which its products need 640 and the other stream's as many: the rest is the latency of issuing
+// and committing them. 20 to 128 rows over 32 x 8 slices of 6960 rows: 181 to 186 us in bf16
+// (5.0 TB/s), 335 to 363 us from the image, where expanding the codes bounds it.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
