@@ -159,20 +159,6 @@ struct State {
   float m[ROWS / 8], l[ROWS / 8];
 };
 
-// The table entries and rows of the runs of a step from slot t on. Entries are fetched a step
-// before the rows they lead to, so that their latency is not added to the rows'.
-template <int NT>
-__device__ __forceinline__ void pages_of(const SlotRows& at, int t, int end, int* page) {
-#pragma unroll
-  for (int j = 0; j < NT; ++j) page[j] = at.page(t + 8 * j, end);
-}
-template <int NT>
-__device__ __forceinline__ void rows_of(const SlotRows& at, int t, int end, const int* page,
-                                        long long* row) {
-#pragma unroll
-  for (int j = 0; j < NT; ++j) row[j] = at.row(t + 8 * j, end, page[j]);
-}
-
 __device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool ok) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src),
                "r"(ok ? 4 : 0)
@@ -188,13 +174,14 @@ __device__ __forceinline__ uint4 lds16(uint32_t at) {
 }
 
 // What a step needs to know besides its rows.
-struct Meta {
-  float ks[4], vs[4];   // image: the scales of its runs of 8 slots
-  int bad[4];           // 1: a bad page
+struct __align__(16) Meta {
+  float scale[8];       // image: the scales of K's (0-3) and V's (4-7) runs of 8 slots
+  int bad[4];           // 1: a run on a bad page
 };
 
-// Starts the copies of a step's rows (those that exist; zeros take the place of others).
-template <int KIND, int D>
+// Starts the copies of a step's rows. WHOLE: all of them follow row[0]. Otherwise run j's are at
+// row[j], and zeros take the place of those that do not exist (`left` slots are left).
+template <int KIND, int D, bool WHOLE>
 __device__ __forceinline__ void copy_rows(const AttendArgs& g, const long long* row, int left,
                                           int lane, uint32_t stage) {
   using S = Shape<KIND, D>;
@@ -203,20 +190,19 @@ __device__ __forceinline__ void copy_rows(const AttendArgs& g, const long long* 
   const char* kb = static_cast<const char*>(KIND == kImage ? g.im.k : g.c.k);
   const char* vb = static_cast<const char*>(KIND == kImage ? g.im.v : g.c.v);
   const int sub = lane / S::kChunks, chunk = lane % S::kChunks;
-  bool full = left >= S::kSlots;
-#pragma unroll
-  for (int j = 0; j < S::NT; ++j) full = full && row[j] >= 0;
-#pragma unroll
-  for (int j = 0; j < S::NT; ++j) {
-    const long long at = (row[j] < 0 ? 0 : row[j]) * S::kRow + lane * 16;
+  if constexpr (WHOLE) {
+    const long long at = row[0] * S::kRow + lane * 16;
     const char *k = kb + at, *v = vb + at;
-    if (full) {
 #pragma unroll
-      for (int i = 0; i < 8; i += kLine) {
-        copy16(stage + S::k_at(8 * j + i + sub, chunk), k + i * S::kRow);
-        copy16(stage + S::kStage / 2 + S::v_at(8 * j + i + sub, chunk), v + i * S::kRow);
-      }
-    } else {
+    for (int i = 0; i < S::kSlots; i += kLine) {
+      copy16(stage + S::k_at(i + sub, chunk), k + i * S::kRow);
+      copy16(stage + S::kStage / 2 + S::v_at(i + sub, chunk), v + i * S::kRow);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < S::NT; ++j) {
+      const long long at = (row[j] < 0 ? 0 : row[j]) * S::kRow + lane * 16;
+      const char *k = kb + at, *v = vb + at;
 #pragma unroll
       for (int i = 0; i < 8; i += kLine) {
         const bool ok = row[j] >= 0 && 8 * j + i + sub < left;
@@ -451,37 +437,58 @@ __device__ __forceinline__ void attend_part(const AttendArgs& g, const AttendUni
     lim[e] = r < u.rows ? min(end, row_limit(g, u, u.r0 + r)) : 0;
   }
   const int low = min(end, u.low);
-  float vref = 1.1754944e-38f;          // image: the largest value scale so far; o is in it
+  float vref = 1.1754944e-38f, vinv = 0.f;   // image: the largest value scale so far; o is in it
   const SlotRows at(g, u);
   const long long blocks0 =
       KIND == kImage && !g.c.page_size ? image_scale_at(g.c, g.t.layer, u.s, u.h, 0, g.b) : 0;
   constexpr int kNext = S::kSlots * kWarps;
   static_assert(S::kStage <= kStageBytes, "");
+  // whether the rows of a whole step follow one another (base is a multiple of its slots, but
+  // behind an image, where a step is one run): one page table entry is enough then
+  const bool follow = S::NT == 1 || !at.table || (1 << at.shift) >= S::kSlots;
   int page[S::NT];
-  // starts step i's copies into stage i / kWarps % kDeep; `page` holds its table entries and
-  // then the next step's
+  const auto fetch_pages = [&](int t) {
+    page[0] = at.page(t, end);
+#pragma unroll
+    for (int j = 1; j < S::NT; ++j) page[j] = follow ? page[0] : at.page(t + 8 * j, end);
+  };
+  // starts step i's copies into stage n; `page` holds its table entries (fetched a step ahead,
+  // so that their latency is not added to the rows') and then the next step's
   const auto start = [&](int i, int n) {
     const int t = base + S::kSlots * i;
     if (i < to) {
       long long row[S::NT];
-      rows_of<S::NT>(at, t, end, page, row);
-      pages_of<S::NT>(at, t + kNext, end, page);
-      copy_rows<KIND, D>(g, row, end - t, lane, ring + n * kStageBytes);
+      row[0] = at.row(t, end, page[0]);
+      // lane j looks after run j: whether its page is good, and the scale of its keys; lane
+      // NT + j after that of its values
+      const int run = lane % S::NT;
+      long long mine;
+      if (follow && row[0] >= 0 && t + S::kSlots <= end) {
+        copy_rows<KIND, D, true>(g, row, S::kSlots, lane, ring + n * kStageBytes);
+        mine = row[0] + 8 * run;
+      } else {
+        mine = row[0];
 #pragma unroll
-      for (int j = 0; j < S::NT; ++j) {
-        if (lane == 0) meta[n].bad[j] = row[j] == -1;
-        if constexpr (KIND == kImage) {
-          const long long x =
-              g.c.page_size ? row[j] >> g.b_shift : blocks0 + (t + 8 * j >> g.b_shift);
-          const bool ok = row[j] >= 0;
-          if (lane == 0) copy4(smem_at(&meta[n].ks[j]), g.im.k_scale + (ok ? x : 0), ok);
-          if (lane == 1) copy4(smem_at(&meta[n].vs[j]), g.im.v_scale + (ok ? x : 0), ok);
+        for (int j = 1; j < S::NT; ++j) {
+          row[j] = at.row(t + 8 * j, end, page[j]);
+          if (run == j) mine = row[j];
         }
+        copy_rows<KIND, D, false>(g, row, end - t, lane, ring + n * kStageBytes);
       }
+      if (lane < S::NT) meta[n].bad[lane] = mine == -1;
+      if constexpr (KIND == kImage) {
+        const bool ok = mine >= 0;
+        const long long x =
+            g.c.page_size ? mine >> g.b_shift : blocks0 + (t + 8 * run >> g.b_shift);
+        if (lane < 2 * S::NT)
+          copy4(smem_at(&meta[n].scale[lane < S::NT ? lane : lane - S::NT + 4]),
+                (lane < S::NT ? g.im.k_scale : g.im.v_scale) + (ok ? x : 0), ok);
+      }
+      fetch_pages(t + kNext);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  pages_of<S::NT>(at, base + S::kSlots * from, end, page);
+  fetch_pages(base + S::kSlots * from);
   __syncwarp();                         // the warp is done with what the ring held before
 #pragma unroll
   for (int n = 0; n < kDeep - 1; ++n) start(from + n * kWarps, n);
@@ -500,8 +507,8 @@ __device__ __forceinline__ void attend_part(const AttendArgs& g, const AttendUni
     for (int j = 0; j < S::NT; ++j) {
       bad_half[j] = meta[n].bad[j] != 0;
       if constexpr (KIND == kImage) {
-        ks[j] = meta[n].ks[j];
-        vs[j] = meta[n].vs[j];
+        ks[j] = meta[n].scale[j];
+        vs[j] = meta[n].scale[4 + j];
       }
     }
     n = n == kDeep - 1 ? 0 : n + 1;
@@ -524,9 +531,22 @@ __device__ __forceinline__ void attend_part(const AttendArgs& g, const AttendUni
         for (int y = 0; y < 2; ++y) {
           float& z = s[j][2 * e + y];
           z *= KIND == kImage ? q.c1[e] * ks[j] : q.c1[e];
-          if (mask && (bad_half[j] || t + 8 * j + 2 * (lane % 4) + y >= lim[e])) z = -INFINITY;
-          top[e] = fmaxf(top[e], z);
         }
+    if (mask) {
+#pragma unroll
+      for (int j = 0; j < S::NT; ++j)
+#pragma unroll
+        for (int e = 0; e < ROWS / 8; ++e)
+#pragma unroll
+          for (int y = 0; y < 2; ++y)
+            if (bad_half[j] || t + 8 * j + 2 * (lane % 4) + y >= lim[e])
+              s[j][2 * e + y] = -INFINITY;
+    }
+#pragma unroll
+    for (int j = 0; j < S::NT; ++j)
+#pragma unroll
+      for (int e = 0; e < ROWS / 8; ++e)
+        top[e] = fmaxf(top[e], fmaxf(s[j][2 * e], s[j][2 * e + 1]));
     if (bad && lane == 0) atomicOr(g.dev_status, NX_DEV_BAD_PAGE);
     bool up = false;
 #pragma unroll
@@ -544,6 +564,7 @@ __device__ __forceinline__ void attend_part(const AttendArgs& g, const AttendUni
     if (__any_sync(0xffffffffu, up)) {
       const float vf = KIND == kImage ? vref / vnew : 1.f;
       vref = vnew;
+      if constexpr (KIND == kImage) vinv = 1.f / vnew;
       float f[ROWS / 8];
 #pragma unroll
       for (int e = 0; e < ROWS / 8; ++e) {
@@ -564,7 +585,7 @@ __device__ __forceinline__ void attend_part(const AttendArgs& g, const AttendUni
     float vr[S::NT];
     if constexpr (KIND == kImage) {
 #pragma unroll
-      for (int j = 0; j < S::NT; ++j) vr[j] = vs[j] / vref;
+      for (int j = 0; j < S::NT; ++j) vr[j] = vs[j] * vinv;
     }
 #pragma unroll
     for (int e = 0; e < ROWS / 8; ++e) {
