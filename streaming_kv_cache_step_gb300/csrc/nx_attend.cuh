@@ -34,6 +34,7 @@ struct AttendArgs {
   int b, b_shift;       // rows per image block, a power of two
   int mtiles;           // row tiles per slice
   int min_tiles;        // tiles of a thread block, at least: fewer pieces to join
+  bool whole;           // row kernel: a thread block per unit, nothing to join
   int units;            // seqs * kv_heads * mtiles
   float c1;             // scale * log2(e)
 };

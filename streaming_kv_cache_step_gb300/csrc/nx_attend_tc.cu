@@ -252,7 +252,6 @@ __device__ __forceinline__ void expand_tile(uint32_t raw, const float* scale, in
                    : "r"(raw + c * 8)
                    : "memory");
       f[i] = scale[r / 8];
-      if (f[i] == 0.f) x[i][0] = x[i][1] = 0;      // a bad page: its codes were not copied
     }
   }
 #pragma unroll
@@ -488,6 +487,17 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
               const bool go =
                   bar_wait(rempty + 8 * st, (no / P::kRaw & 1) ^ 1, up, g.dev_status);
               if (lane < kGroups) s_scale[st][lane] = scale;
+              // a run on a bad page: zeros for what the stage held before
+              if (any_bad)
+                for (int q = 0; q < kGroups; ++q) {
+                  const bool zero = __shfl_sync(0xffffffffu, row == -1 ? 1 : 0, q) != 0 && go;
+                  if (zero)
+                    for (int x = lane; x < 8 * D / 16; x += 32)
+                      asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(
+                                       s_codes + st * P::kRawBytes + q * 8 * D + x * 16),
+                                   "r"(0)
+                                   : "memory");
+                }
               const bool lead = go && row >= 0 && 8 * lane % box == 0;
               const int bytes = lead ? (min(held, t + box) - t) * D : 0;
               const unsigned total = __reduce_add_sync(0xffffffffu, (unsigned)bytes);
@@ -884,7 +894,7 @@ cudaError_t launch_t(AttendArgs& g, cudaStream_t st, int* launches) {
 // The row kernel reads K and V once for 16 rows, this one once for 256 but at a higher cost, from
 // 8-bit rows more so.
 bool attend_tc_takes(const nx_cache& c, const nx_tokens& t, bool image) {
-  return c.dtype == NX_DTYPE_BF16 && most_tokens(t) * c.group > (image ? 32 : 16);
+  return c.dtype == NX_DTYPE_BF16 && most_tokens(t) * c.group > (image ? 64 : 16);
 }
 
 size_t attend_tc_layout(int D, char* base, AttendWs* ws) {

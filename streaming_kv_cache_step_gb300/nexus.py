@@ -450,12 +450,15 @@ def _heads(t, tokens: int, heads: int, cache: Cache, name: str):
     """A per-token tensor [tokens, heads, head_dim] whose heads lie behind one another;
     returns the elements between two tokens."""
     d = cache.head_dim
-    if t.dim() != 3 or t.shape != (tokens, heads, d) or t.dtype != cache.k.dtype or \
-            not t.is_cuda:
+    if t.shape != (tokens, heads, d) or t.dtype != cache.k.dtype or not t.is_cuda:
         raise ValueError(f"{name} must be {(tokens, heads, d)} in the cache's type on the GPU")
-    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != d):
-        raise ValueError(f"{name}: the heads of a token must lie behind one another")
-    return t.stride(0) if tokens > 1 else heads * d
+    if not t.is_contiguous():
+        step, head, one = t.stride()
+        if one != 1 or (heads > 1 and head != d):
+            raise ValueError(f"{name}: the heads of a token must lie behind one another")
+        if tokens > 1:
+            return step
+    return heads * d
 
 
 def append(cache: Cache, layer: int, q, k, v, token_pos, q_out, dev_status, *, max_tokens: int,
