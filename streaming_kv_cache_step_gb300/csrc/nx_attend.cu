@@ -20,10 +20,10 @@
 // the GPU at once, whatever the slices' lengths; a slice that a boundary cuts is joined by
 // attend_join_kernel.
 //
-// Measured, one new token of 16 x 8 slices of 32768 rows, 4 query heads each: 312 us in bf16
-// (6.9 TB/s of K and V, what a plain copy reaches), 190 us from the image (5.6 TB/s; the rest
-// are issue slots of the conversions); 64 sequences of ragged lengths in 16-row pages 283 us
-// (6.45 TB/s); 8 slices of 1638 rows 9.7 us, the latencies of two launches.
+// Measured, one new token of 16 x 8 slices of 32768 rows, 4 query heads each: 308 us in bf16
+// (7.0 TB/s of K and V, what a plain copy reaches), 164 us from the image (6.55 TB/s); 64
+// sequences of ragged lengths in 16-row pages 271 us (6.7 TB/s); 8 slices of 1638 rows 9.9 us,
+// the latencies of two launches; 8 slices of 64 rows, in one, 5.7 us.
 #include "nx_attend.cuh"
 
 namespace nx {
