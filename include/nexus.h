@@ -358,7 +358,7 @@ typedef struct nx_attend {
 } nx_attend;
 
 /* Bytes of workspace nexus_attend needs for these arguments, with an image or without (0 on
-   invalid arguments); it goes by head_dim and by whether max_tokens * group is above 16. */
+   invalid arguments); it goes by head_dim and by max_tokens * group. */
 size_t nexus_attend_workspace_bytes(const nx_cache* cache, const nx_tokens* tokens);
 
 /*
@@ -374,7 +374,7 @@ size_t nexus_attend_workspace_bytes(const nx_cache* cache, const nx_tokens* toke
  * hold. A row below lens that is not finite shows in its own slice only; a value row there
  * shows also in the outputs of tokens of this call that do not see it yet (their weight is 0,
  * and 0 times an infinity or NaN is NaN). Up to 16 query rows per slice (max_tokens * group;
- * 64 from an image) go to a kernel that streams rows through mma.sync, more to one on
+ * 32 where the layer's slices take up to 128 MB, 64 from an image) go to a kernel that streams rows through mma.sync, more to one on
  * tcgen05; fp32 caches always to the first. One launch for short
  * caches (a few hundred rows) on the first, else two; the same bits every time.
  * NX_ERR_UNSUPPORTED for an image of an fp32 cache, for more than 2^20 query heads or 2^24

@@ -757,7 +757,9 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
 #pragma unroll
               for (int e = 0; e < 32; ++e)
                 o[e] = o[e] * f0 + (count[1] ? s_o[(32 * q + e) * kRows + r] * f1 : 0.f);
-            if (rr < u.rows) {
+            // of a piece all 32 rows of a warp: whole 128-byte lines (with parts of them the join
+            // of 19 pieces took 13 us longer)
+            if (whole ? rr < u.rows : !idle) {
               if (whole) {
                 if (l == 0.f)
 #pragma unroll
@@ -770,7 +772,7 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
               }
             }
           }
-          if (rr < u.rows) {
+          if (whole ? rr < u.rows : !idle) {
             if (whole) store_lse(g, u, rr, m, l);
             else g.ws.stat[piece * kTcRows + rr] = make_float2(m, l);
           }
@@ -891,10 +893,15 @@ cudaError_t launch_t(AttendArgs& g, cudaStream_t st, int* launches) {
 
 }  // namespace
 
-// The row kernel reads K and V once for 16 rows, this one once for 256 but at a higher cost, from
-// 8-bit rows more so.
+// The row kernel takes 16 rows a pass over K and V, this one 256 but at a higher cost, from 8-bit
+// rows more so. Measured (us, this kernel / the row kernel) on 32 x 8 slices of 6960 rows: bf16, 16
+// rows 181 / 151, 20 rows 181 / 282; 8 bits, 64 rows 371 / 293, 96 rows 374 / 413. A second pass
+// that finds K and V in L2 costs less: bf16, 32 rows, 4 x 8 slices 45 / 43, one sequence of 8
+// slices of 32768 rows 62 / 50.
 bool attend_tc_takes(const nx_cache& c, const nx_tokens& t, bool image) {
-  return c.dtype == NX_DTYPE_BF16 && most_tokens(t) * c.group > (image ? 64 : 16);
+  const long long bytes = (long long)c.seqs * c.kv_heads * c.capacity * c.head_dim * 4;
+  const int rows = image ? 64 : bytes <= (128LL << 20) ? 32 : 16;
+  return c.dtype == NX_DTYPE_BF16 && most_tokens(t) * c.group > rows;
 }
 
 size_t attend_tc_layout(int D, char* base, AttendWs* ws) {
