@@ -18,12 +18,14 @@
 //     rounding errors (p = hi + lo), so that bf16 probabilities cost no accuracy.
 // The slots of all slices, 64 to a tile, are dealt out evenly to as many thread blocks as fit
 // the GPU at once, whatever the slices' lengths; a slice that a boundary cuts is joined by
-// attend_join_kernel.
+// attend_join_kernel. Where a cache has few or short slices the latencies of two launches count
+// more than an even deal: a slice is then a block's own, or a cluster's, whose blocks join their
+// pieces from one another's shared memory.
 //
 // Measured, one new token of 16 x 8 slices of 32768 rows, 4 query heads each: 308 us in bf16
 // (7.0 TB/s of K and V, what a plain copy reaches), 164 us from the image (6.55 TB/s); 64
-// sequences of ragged lengths in 16-row pages 271 us (6.7 TB/s); 8 slices of 1638 rows 9.9 us,
-// the latencies of two launches; 8 slices of 64 rows, in one, 5.7 us.
+// sequences of ragged lengths in 16-row pages 271 us (6.7 TB/s); 8 slices of 1638 rows 9.3 us,
+// latencies; 8 slices of 64 rows 5.7 us.
 #include "nx_attend.cuh"
 
 namespace nx {
@@ -31,6 +33,7 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kAttendGrid = kSms * 3;  // thread blocks of one launch, at most
+constexpr int kRanks = 8;              // thread blocks of a cluster (the portable limit)
 constexpr int kPieceRows = 16;         // query rows of a piece, at most
 // kTail: bf16 rows behind an image, with their output features in the image's order
 enum Kind { kBf16 = 0, kImage = 1, kF32 = 2, kTail = 3 };
@@ -641,7 +644,25 @@ __device__ __forceinline__ void finish_row(const AttendArgs& g, const AttendUnit
   }
 }
 
-template <int KIND, int D, int ROWS>
+// Thread block clusters: everyone's arrival, and another block's shared memory.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float remote(const float* p, int rank) {
+  float x;
+  asm volatile(
+      "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\t"
+      "ld.shared::cluster.f32 %0, [a];\n\t}"
+      : "=f"(x)
+      : "r"(smem_at(p)), "r"(rank)
+      : "memory");
+  return x;
+}
+
+// EVEN: the blocks share all tiles evenly; else `g.ranks` blocks, one cluster, have a unit. Two
+// kernels: as one, 8 image rows of 128 features spill 132 bytes of registers instead of 24, and 16
+// sequences of 16384 rows take 167.4 us instead of 163.9.
+template <int KIND, int D, int ROWS, bool EVEN>
 __global__ void __launch_bounds__(kWarps * 32, Ring<KIND, D, ROWS>::kPerSm)
     attend_kernel(AttendArgs g) {
   constexpr int kTileSlots = kTileOf<KIND>;
@@ -653,14 +674,24 @@ __global__ void __launch_bounds__(kWarps * 32, Ring<KIND, D, ROWS>::kPerSm)
   static_assert(kRing >= ROWS * D * 4, "");
   __shared__ Meta s_meta[kWarps][R::kDeep];
   __shared__ float s_m[kWarps][ROWS], s_l[kWarps][ROWS];
+  __shared__ float s_pm[ROWS], s_pl[ROWS];              // of the block's piece
   grid_dep_wait();
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const int b = blockIdx.x;
   const uint32_t ring = smem_at(s_ring) + warp * kRing;
 
-  int per = 1, stop, unit = b, at = 0, pos = 0;         // `at`: the unit's first tile
-  if (g.whole) {
-    stop = unit_tiles<KIND>(attend_unit<ROWS>(g, unit));
+  int per = 1, stop, unit, at = 0, pos;                 // `at`: the unit's first tile
+  bool meets = false;                                   // the cluster's pieces do
+  if constexpr (!EVEN) {
+    unit = b / g.ranks;
+    const int tiles = unit_tiles<KIND>(attend_unit<ROWS>(g, unit)), rank = b % g.ranks;
+    pos = (int)((long long)tiles * rank / g.ranks);
+    stop = (int)((long long)tiles * (rank + 1) / g.ranks);
+    meets = g.ranks > 1 && tiles > 1;
+    if (meets && tid < ROWS) {
+      s_pm[tid] = -INFINITY;                            // in case this block has no tile
+      s_pl[tid] = 0.f;
+    }
   } else {
     const AttendShare sh = attend_share<kWarps * 32>(
         g, [&](int i) { return unit_tiles<KIND>(attend_unit<ROWS>(g, i)); });
@@ -697,13 +728,14 @@ __global__ void __launch_bounds__(kWarps * 32, Ring<KIND, D, ROWS>::kPerSm)
         attend_part<kImage, D, ROWS, R::kDeep, R::kBytes>(g, u, 0, ea, a0 * k + warp,
                                      min(min(a1, ta) * k, (ea + 31) / 32), ring, s_meta[warp], st);
         constexpr int kt = kTileSlots / Shape<kTail, D>::kSlots;
-        attend_part<kTail, D, ROWS, R::kDeep, R::kBytes>(g, u, ea, u.end, max(a0 - ta, 0) * kt + warp,
-                                    min((a1 - ta) * kt, (u.end - ea + 7) / 8), ring, s_meta[warp],
-                                    st);
+        attend_part<kTail, D, ROWS, R::kDeep, R::kBytes>(
+            g, u, ea, u.end, max(a0 - ta, 0) * kt + warp,
+            min((a1 - ta) * kt, (u.end - ea + 7) / 8), ring, s_meta[warp], st);
       } else {
         constexpr int k = kTileSlots / Shape<KIND, D>::kSlots, w = Shape<KIND, D>::kSlots;
-        attend_part<KIND, D, ROWS, R::kDeep, R::kBytes>(g, u, 0, u.end, a0 * k + warp, min(a1 * k, (u.end + w - 1) / w),
-                                   ring, s_meta[warp], st);
+        attend_part<KIND, D, ROWS, R::kDeep, R::kBytes>(
+            g, u, 0, u.end, a0 * k + warp, min(a1 * k, (u.end + w - 1) / w), ring, s_meta[warp],
+            st);
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
       __syncthreads();
@@ -748,6 +780,12 @@ __global__ void __launch_bounds__(kWarps * 32, Ring<KIND, D, ROWS>::kPerSm)
         }
         if (whole) {
           finish_row(g, u, r, D, f, m, l, o);
+        } else if (!EVEN && meets) {
+          s_o[0][r][f] = o;                             // read by this thread alone so far
+          if (f == 0) {
+            s_pm[r] = m;
+            s_pl[r] = l;
+          }
         } else {
           if (f == 0) g.ws.stat[slot * kPieceRows + r] = make_float2(m, l);
           g.ws.out[((long long)slot * kPieceRows + r) * D + f] = o;
@@ -760,7 +798,37 @@ __global__ void __launch_bounds__(kWarps * 32, Ring<KIND, D, ROWS>::kPerSm)
     at += tiles;
     ++unit;
   }
-  if (tid == 0 && !g.whole) g.ws.desc[b] = desc;
+  if constexpr (EVEN) {
+    if (tid == 0) g.ws.desc[b] = desc;
+  } else if (meets) {
+    // the cluster's pieces, in the order of their slots, from the blocks' shared memory
+    cluster_sync();
+    const AttendUnit u = attend_unit<ROWS>(g, b / g.ranks);
+    for (int i = b % g.ranks * (kWarps * 32) + tid; i < u.rows * D; i += g.ranks * kWarps * 32) {
+      const int r = i / D, f = i % D;
+      float m[kRanks], z[kRanks], x[kRanks], top = -INFINITY, l = 0.f, o = 0.f;
+#pragma unroll
+      for (int p = 0; p < kRanks; ++p) {                // all under way at once
+        m[p] = -INFINITY;
+        z[p] = x[p] = 0.f;
+        if (p >= g.ranks) continue;
+        m[p] = remote(&s_pm[r], p);
+        z[p] = remote(&s_pl[r], p);
+        x[p] = remote(&s_o[0][r][f], p);
+      }
+#pragma unroll
+      for (int p = 0; p < kRanks; ++p) top = fmaxf(top, m[p]);
+#pragma unroll
+      for (int p = 0; p < kRanks; ++p) {
+        if (m[p] == -INFINITY && z[p] == 0.f) continue; // nothing seen, or no tile at all
+        const float k = m[p] == -INFINITY ? 1.f : ex2(m[p] - top);
+        l += k * z[p];
+        o += k * x[p];
+      }
+      finish_row(g, u, r, D, f, top, l, o);
+    }
+    cluster_sync();                                     // nobody reads this block any more
+  }
 }
 
 // Joins the pieces of the unit that starts in block b and ends in a later one.
@@ -835,21 +903,41 @@ cudaError_t launch_attend(AttendArgs& g, cudaStream_t st, int* launches) {
   const long long fit = kSms * R::kPerSm;
   g.mtiles = (int)mtiles;
   g.units = (int)units;
-  g.min_tiles = 2;
-  // Short slices, of up to eight steps per warp and 512 slots (1024 if the units fill the GPU): a
-  // block per unit saves the join, its launch and the search for a share. bf16, 8 slices of 64
-  // rows 5.7 us against 10.7, of 512 rows 9.5 against 9.6, of 1024 rows 14.1 against 10.5; 512
-  // slices of 1024 rows 46.5 against 52.8.
-  const int eight = 8 * Shape<KIND, D>::kSlots * kWarps, few = eight < 512 ? eight : 512;
-  g.whole = g.c.capacity <= (units >= fit ? 2 * few : few);
-  const int grid = (int)(g.whole ? units : most < fit ? most : fit);
+  // A unit is one block's, or a cluster's of 2, 4 or 8 blocks, as many as fit the GPU at once;
+  // either way there is one launch and no workspace. That pays up to `few` slots (eight steps
+  // per warp, 512 at most) for one block and up to `most_of` for each block of a cluster; beyond
+  // that even shares keep more of the GPU busy. On the GPU, one token, 4 query rows, in us, even
+  // shares / one block / clusters:
+  //   bf16, 8 slices of 128 slots 9.1 / 6.2 / 8.4, of 256 9.3 / 7.5 / 7.7, of 512 9.6 / 9.5 / 7.9,
+  //   of 2048 12.7 / 22.9 / 9.5, of 4096 13.2 / 40.2 / 11.7, of 8192 14.9 / - / 16.2; 64 slices of
+  //   512 12.0 / 9.7 / 9.6, of 1024 13.6 / 14.2 / 10.9, of 4096 32.6 / 41.4 / 27.0; 80 slices of
+  //   512 15.9 / 9.8 / 11.4, of 1024 17.0 / 14.1 / 14.1; 512 slices of 1024 52.8 / 46.5 / -;
+  //   image, 8 slices of 512 11.4 / 10.3 / 9.5, 64 of 4096 25.2 / 36.8 / 20.5;
+  //   fp32, 8 slices of 512 11.7 / 22.2 / 9.7, of 2048 15.2 / 70.9 / 15.8, of 4096 18.8 / 136 /
+  //   24.1; 80 slices of 512 23.0 / 22.5 / 20.7, of 1024 28.7 / 39.3 / 33.4.
+  constexpr int eight = 8 * Shape<KIND, D>::kSlots * kWarps, few = eight < 512 ? eight : 512;
+  constexpr int most_of = KIND == kF32 ? few : 2 * few;
+  int ranks = kRanks;
+  while (ranks > 1 && units * ranks > fit) ranks /= 2;
+  if (g.c.capacity <= (units * kRanks <= 2 * kSms ? few / 2 : few)) ranks = 1;
+  const int limit = ranks > 1 ? ranks * most_of : units >= fit ? 2 * few : few;
+  g.ranks = g.c.capacity <= limit ? ranks : 0;
+  const int grid = (int)(g.ranks ? units * g.ranks : most < fit ? most : fit);
   constexpr int smem = kWarps * R::kDeep * R::kBytes;
-  cudaError_t e = allow_smem<attend_kernel<KIND, D, ROWS>>(smem);
+  cudaError_t e;
+  if (g.ranks) {
+    e = allow_smem<attend_kernel<KIND, D, ROWS, false>>(smem);
+    if (e != cudaSuccess) return e;
+    e = launch_after_clusters(attend_kernel<KIND, D, ROWS, false>, dim3(grid), dim3(kWarps * 32),
+                              smem, g.ranks, st, g);
+    if (e == cudaSuccess) note_launch(st, launches, "attend");
+    return e;
+  }
+  e = allow_smem<attend_kernel<KIND, D, ROWS, true>>(smem);
   if (e != cudaSuccess) return e;
-  e = launch_after(attend_kernel<KIND, D, ROWS>, dim3(grid), dim3(kWarps * 32), smem, st, g);
+  e = launch_after(attend_kernel<KIND, D, ROWS, true>, dim3(grid), dim3(kWarps * 32), smem, st, g);
   if (e != cudaSuccess) return e;
   note_launch(st, launches, "attend");
-  if (g.whole) return cudaSuccess;
   e = launch_after(attend_join_kernel<D, ROWS>, dim3(grid), dim3(kJoinWarps * 32), 0, st, g);
   if (e == cudaSuccess) note_launch(st, launches, "attend_join");
   return e;
@@ -916,7 +1004,8 @@ extern "C" nx_status nexus_attend(const nx_cache* cache, const nx_tokens* tokens
   if (image) g.im = *image;
   g.a = a;
   g.dev_status = dev_status;
-  if (attend_tc_takes(c, *tokens, image != nullptr)) attend_tc_layout(c.head_dim, static_cast<char*>(ws), &g.ws);
+  if (attend_tc_takes(c, *tokens, image != nullptr))
+    attend_tc_layout(c.head_dim, static_cast<char*>(ws), &g.ws);
   else attend_layout(c.head_dim, static_cast<char*>(ws), &g.ws);
   g.b = image_block(c);
   while (1 << g.b_shift < g.b) ++g.b_shift;

@@ -33,8 +33,7 @@ struct AttendArgs {
   AttendWs ws;
   int b, b_shift;       // rows per image block, a power of two
   int mtiles;           // row tiles per slice
-  int min_tiles;        // tiles of a thread block, at least: fewer pieces to join
-  bool whole;           // row kernel: a thread block per unit, nothing to join
+  int ranks;            // row kernel: thread blocks per unit, one cluster (0: even shares)
   int units;            // seqs * kv_heads * mtiles
   float c1;             // scale * log2(e)
 };
@@ -114,7 +113,7 @@ __device__ __forceinline__ AttendShare attend_share(const AttendArgs& g, const T
   }
   AttendShare x;
   x.total = total;
-  x.per = max(g.min_tiles, (total + (int)gridDim.x - 1) / (int)gridDim.x);
+  x.per = max(1, (total + (int)gridDim.x - 1) / (int)gridDim.x);
   const long long start = (long long)blockIdx.x * x.per;
   if (start >= before && start < (long long)before + sum) {
     int at = before;

@@ -856,7 +856,8 @@ bool encode_rows(const nx_cache& c, void* base, CUtensorMap* map) {
   if (!fn || rows >= (1LL << 31)) return false;
   const cuuint64_t dim[2] = {(cuuint64_t)c.head_dim, (cuuint64_t)rows};
   const cuuint64_t stride[1] = {(cuuint64_t)c.head_dim * 2};
-  const cuuint32_t box[2] = {64, (cuuint32_t)(c.page_size && c.page_size < kCols ? c.page_size : kCols)};
+  const cuuint32_t box[2] = {
+      64, (cuuint32_t)(c.page_size && c.page_size < kCols ? c.page_size : kCols)};
   const cuuint32_t one[2] = {1, 1};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dim, stride, box, one,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -871,7 +872,6 @@ cudaError_t launch_t(AttendArgs& g, cudaStream_t st, int* launches) {
   const long long units = (long long)g.c.seqs * g.c.kv_heads * g.mtiles;
   const long long most = units * ((g.c.capacity + kCols - 1) / kCols);
   g.units = (int)units;
-  g.min_tiles = 1;
   cudaError_t e = allow_smem<attend_tc_kernel<D, NQ, IMAGE>>(smem);
   if (e != cudaSuccess) return e;
   const int grid = (int)(most < kTcGrid ? most : kTcGrid);
