@@ -79,7 +79,7 @@ __device__ __forceinline__ uint32_t rest2(float a, float b, uint32_t hi) {
 }
 
 // A binary32 value as the sum of two tf32 operands (11 bits each), to 2^-24 of it: the nearest
-// tf32, and the nearest to what that leaves.
+// tf32, and the nearest to what that leaves (of an infinity: NaN, see plain_logits).
 __device__ __forceinline__ uint32_t tf32_near(float x) {
   uint32_t y;
   asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(y) : "f"(x));
@@ -347,6 +347,35 @@ __device__ __forceinline__ void qk(const Query<KIND, D, ROWS>& q, uint32_t stage
   }
 }
 
+// fp32: the logits that came out as NaN, over again without terms: those of an infinite key are
+// infinite, and one of -infinity drops out of the softmax. Few registers, and rarely run (with
+// terms that mind infinities in every product 64 slices of 6000 rows took 98 us, not 79).
+template <int D>
+__device__ __forceinline__ void plain_logits(const AttendArgs& g, const AttendUnit& u,
+                                             uint32_t stage, int lane, float* s) {
+  using S = Shape<kF32, D>;
+  const int r = lane / 4, row = u.r0 + r;
+  const float4* q = reinterpret_cast<const float4*>(
+      static_cast<const float*>(g.a.q) + (u.first + row / g.c.group) * g.a.q_stride +
+      ((long long)u.h * g.c.group + row % g.c.group) * D);
+#pragma unroll 1
+  for (int y = 0; y < 2 && r < u.rows; ++y) {
+    float sum = 0.f;
+#pragma unroll 1
+    for (int i = 0; i < S::kChunks; ++i) {
+      const uint4 k = lds16(stage + S::k_at(2 * (lane % 4) + y, i));
+      const float4 x = q[i];
+      sum += x.x * __uint_as_float(k.x) + x.y * __uint_as_float(k.y) +
+             x.z * __uint_as_float(k.z) + x.w * __uint_as_float(k.w);
+    }
+    if (y == 0) {
+      if (s[0] != s[0]) s[0] = sum;
+    } else if (s[1] != s[1]) {
+      s[1] = sum;
+    }
+  }
+}
+
 // o += p V.
 template <int KIND, int D, int ROWS>
 __device__ __forceinline__ void pv(uint32_t stage, int lane, const float p[][4],
@@ -517,6 +546,9 @@ __device__ __forceinline__ void attend_part(const AttendArgs& g, const AttendUni
     n = n == kDeep - 1 ? 0 : n + 1;
     float s[S::NT][4];
     qk<KIND, D, ROWS>(q, stage, lane, s);
+    if constexpr (KIND == kF32)
+      if (__any_sync(0xffffffffu, s[0][0] != s[0][0] || s[0][1] != s[0][1]))
+        plain_logits<D>(g, u, stage, lane, s[0]);
 
     // logits in log2 units; beyond a row's limit or on a bad page: -inf
     float top[ROWS / 8];

@@ -707,3 +707,56 @@ def test_attend_nan_codes_give_nan(group):
     torch.cuda.synchronize()
     bad = torch.isnan(out.float())
     assert not bad[0].any() and bad[1, :, 3].all() and not bad[1, :, :3].any() and not bad[1, :, 4:].any()
+
+
+CUTS = [0, 1, 8, 63, 64, 65, 128, 129, 191, 300, 447, 449, 511, 513, 800, 899, 900]
+
+
+@pytest.mark.parametrize("kind", ["bf16", "bf16_64", "image", "image_64", "f32", "f32_64"])
+@pytest.mark.parametrize("seqs,capacity,one", [
+    (2, 900, True), (5, 2000, False), (20, 900, False), (20, 2001, False), (40, 500, False),
+    (45, 900, False), (60, 450, True), (120, 512, True)])
+def test_attend_blocks_per_slice(kind, seqs, capacity, one):
+    # a block, a cluster of 8, 4 or 2 blocks, or an even share per slice, by the number of slices
+    # and their capacity; fewer tiles than blocks, none, and rows that see none of a block's
+    group = 4
+    c = Case(seqs=seqs, kv_heads=2, group=group, d=64 if kind.endswith("_64") else 128,
+             dtype=F32 if kind.startswith("f32") else BF, capacity=capacity,
+             lens=[[min(capacity, CUTS[i % 17]), min(capacity, CUTS[(7 * i + 3) % 17]) if i else capacity]
+                   for i in range(seqs)], seed=seqs)
+    _check_attend(c, [1] * seqs, image=kind.startswith("image"), uniform=True)
+    if one and not kind.startswith("f32"):
+        assert nexus.last_launch_names() == ["attend"]
+    n = [(3 * i + 1) % 5 for i in range(seqs)]
+    _check_attend(c, n, image=kind.startswith("image"))
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("tokens", [1, 5, 30])
+@pytest.mark.parametrize("at", [0, 63, 64, 700])
+def test_attend_nan_and_infinite_rows_among_the_blocks_of_a_slice(kind, tokens, at):
+    # a NaN key or value reaches every row of its slice and no other slice; an infinite key
+    # drops out; an infinite value makes infinities or NaN
+    dt = F32 if kind == "f32" else BF
+    c = Case(seqs=5, kv_heads=1, group=2, dtype=dt, capacity=701, lens=701, seed=at)
+    q = (torch.rand(5 * tokens, 2, 128, generator=c.g) + 0.5).to(dt)  # positive
+    c.k[0, 0, 0, at] = -math.inf
+    c.v[0, 1, 0, at] = math.nan
+    c.k[0, 2, 0, at] = math.nan
+    c.v[0, 4, 0, at] = math.inf
+    cache, st = c.device_cache(), _status()
+    out = torch.zeros(5 * tokens, 2, 128, dtype=dt, device=DEV)
+    ws = nexus.alloc_attend_workspace(cache, tokens=5 * tokens, max_tokens=tokens)
+    nexus.attend(cache, 0, q.to(DEV), out, ws, st, max_tokens=tokens, causal=False)
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0
+    if tokens == 1:
+        assert nexus.last_launch_names() == ["attend"]
+    out = out.reshape(5, tokens * 2, 128).cpu()
+    keep = torch.tensor([j for j in range(701) if j != at])
+    ref, _, A, _ = attend64(q[:tokens].reshape(-1, 128), c.k[0, 0, 0][keep], c.v[0, 0, 0][keep],
+                            [700] * (2 * tokens), 128 ** -0.5)
+    assert torch.all((out[0].double() - ref).abs() <= 2.0 ** -6 * A)
+    nan = torch.isnan(out)
+    assert not nan[0].any() and nan[1].all() and nan[2].all() and not nan[3].any()
+    assert not torch.isfinite(out[4]).any()
