@@ -25,7 +25,8 @@ constexpr int kTokens = 16;           // tokens of a thread block
 constexpr int kSoloTokens = 16;       // up to so many tokens one block takes a sequence
 // The largest block, and with it the registers of a thread: 640 leave 96 (108 us for 8192-token
 // prompts); 768 leave 80 and spill (113 us), 512 leave 128 and fewer warps (137 us).
-constexpr int kMaxThreads = 640;
+constexpr int kRing = 4;              // tokens whose rows are loaded at a time, less one
+constexpr int kMaxThreads = 768;
 constexpr int kAppendThreads = 256;   // threads of a block, unless one block covers a sequence
 
 struct AppendArgs {
@@ -35,6 +36,7 @@ struct AppendArgs {
   int32_t* dev_status;
   int32_t* lens;        // the layer's part of c.lens
   int tiles, parts;     // thread blocks per sequence: token tiles x parts of the head rows
+  int most;             // tokens of a block, at most
   bool set_lens;        // the kernel sets the new lengths itself
 };
 
@@ -61,6 +63,13 @@ struct Run {                          // RUN features of a row as they lie in me
   using Raw = typename std::conditional<sizeof(T) * RUN == 8, uint2, uint4>::type;
   static_assert(sizeof(T) * RUN == sizeof(Raw), "");
   Raw r;
+  // starts the copy of a run from memory to an address of shared memory
+  static __device__ __forceinline__ void start(uint32_t to, const T* from) {
+    if constexpr (sizeof(Raw) == 16)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+    else
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to), "l"(from) : "memory");
+  }
   __device__ __forceinline__ void load(const T* p) { r = *reinterpret_cast<const Raw*>(p); }
   __device__ __forceinline__ void store(T* p) const { *reinterpret_cast<Raw*>(p) = r; }
   __device__ __forceinline__ void get(float* x) const {
@@ -94,11 +103,14 @@ struct Run {                          // RUN features of a row as they lie in me
 template <typename T, int D, int RUN>
 __global__ void __launch_bounds__(kMaxThreads) append_kernel(AppendArgs g) {
   constexpr int N = 2 * RUN, kLanes = D / N;         // threads of one head row
-  constexpr int kAhead = 2;                          // tokens loaded before one is used
+  using R = Run<T, RUN>;
   // by token, then pair e of thread l at [e / 2][l][e % 2]: neighbours read neighbouring words
   __shared__ __align__(16) float2 s_rot[kTokens][D / 2];
   __shared__ int s_pos[kTokens];
-  extern __shared__ int s_len[];                     // [kv_heads], -1: leave alone
+  // the runs under way, [slot][run][thread], then [kv_heads] lengths, -1: leave alone
+  extern __shared__ __align__(16) char s_ring[];
+  const int slots = min(kRing, g.most), run_bytes = blockDim.x * (int)sizeof(R);
+  int* s_len = reinterpret_cast<int*>(s_ring + slots * 2 * run_bytes);
   grid_dep_wait();
 
   const nx_cache& c = g.c;
@@ -118,28 +130,8 @@ __global__ void __launch_bounds__(kMaxThreads) append_kernel(AppendArgs g) {
   if (nt <= 0 && tile > 0) return;
 
   const int H = c.kv_heads, HQ = a.q ? H * c.group : 0;
-  const int32_t* lens_in = (a.lens_in ? a.lens_in : g.lens) + (long long)s * H;
-  for (int h = tid; h < H; h += blockDim.x) {
-    int len = lens_in[h];
-    int flag = 0;
-    if (len < 0 || len > c.capacity) flag = NX_DEV_BAD_LEN;
-    else if (n > c.capacity - len) flag = NX_DEV_FULL;
-    if (flag) {
-      len = -1;
-      if (lead) atomicOr(g.dev_status, flag);
-    }
-    s_len[h] = len;
-  }
-  const int half = a.rotary_dim / 2;
-  for (int t = tid / 32; t < nt; t += blockDim.x / 32)
-    for (int i = tid % 32; i < half; i += 32)
-      s_rot[t][(i % RUN / 2 * kLanes + i / RUN) * 2 + i % 2] =
-          rotation_of(a.pos[first + t0 + t], a.rotary[i]);
-  if (tid < nt) s_pos[tid] = a.pos[first + t0 + tid];
-  __syncthreads();
-
   // this thread's two runs of features, and whether they turn
-  const int lane = tid % kLanes;
+  const int lane = tid % kLanes, half = a.rotary_dim / 2;
   const bool turns = lane < a.rotary_dim / N;
   const bool split = turns && !a.interleaved;
   const int o0 = split ? RUN * lane : N * lane;
@@ -148,7 +140,9 @@ __global__ void __launch_bounds__(kMaxThreads) append_kernel(AppendArgs g) {
   const int groups = blockDim.x / kLanes;
   // a warp's groups take neighbouring head rows; a row that does not exist takes part in the
   // warp's shuffles, with zeros
-  for (int base = part * groups + (tid & ~31) / kLanes; base < rows; base += g.parts * groups) {
+  bool primed = false;
+  for (int base = part * groups + (tid & ~31) / kLanes; !primed || base < rows;
+       base += g.parts * groups) {
     const int r = base + tid % 32 / kLanes;
     const bool live = r < rows, is_q = r < HQ, is_v = r >= HQ + H;
     const int h = is_q ? r : is_v ? r - HQ - H : r - HQ;
@@ -157,6 +151,16 @@ __global__ void __launch_bounds__(kMaxThreads) append_kernel(AppendArgs g) {
     const T* src = static_cast<const T*>(is_q ? a.q : is_v ? a.v : a.k) + token * stride +
                    (long long)h * D;
     const T* weight = static_cast<const T*>(is_q ? a.q_norm : is_v ? nullptr : a.k_norm);
+    const uint32_t ring = smem_at(s_ring) + tid * (int)sizeof(R);
+    const auto fetch = [&](int t, int slot) {
+      if (live && t < nt) {
+        R::start(ring + 2 * slot * run_bytes, src + t * stride + o0);
+        R::start(ring + (2 * slot + 1) * run_bytes, src + t * stride + o1);
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int t = 0; t < kRing - 1; ++t) fetch(t, t);
     float w[N];
     if (weight && live) {
       Run<T, RUN> x;
@@ -164,6 +168,27 @@ __global__ void __launch_bounds__(kMaxThreads) append_kernel(AppendArgs g) {
       x.get(w);
       x.load(weight + o1);
       x.get(w + RUN);
+    }
+    if (!primed) {                                  // while the first rows are on their way
+      const int32_t* lens_in = (a.lens_in ? a.lens_in : g.lens) + (long long)s * H;
+      for (int h = tid; h < H; h += blockDim.x) {
+        int len = lens_in[h];
+        int flag = 0;
+        if (len < 0 || len > c.capacity) flag = NX_DEV_BAD_LEN;
+        else if (n > c.capacity - len) flag = NX_DEV_FULL;
+        if (flag) {
+          len = -1;
+          if (lead) atomicOr(g.dev_status, flag);
+        }
+        s_len[h] = len;
+      }
+      for (int t = tid / 32; t < nt; t += blockDim.x / 32)
+        for (int i = tid % 32; i < half; i += 32)
+          s_rot[t][(i % RUN / 2 * kLanes + i / RUN) * 2 + i % 2] =
+              rotation_of(a.pos[first + t0 + t], a.rotary[i]);
+      if (tid < nt) s_pos[tid] = a.pos[first + t0 + tid];
+      __syncthreads();
+      primed = true;
     }
     const int len = live && !is_q ? s_len[h] : 0;
     const bool writes = live && len >= 0;
@@ -182,81 +207,68 @@ __global__ void __launch_bounds__(kMaxThreads) append_kernel(AppendArgs g) {
     }
     const bool keeps_pos = !is_q && !is_v && lane == 0;
     const bool norms = __any_sync(0xffffffffu, weight != nullptr);   // the shuffles take the warp
-    Run<T, RUN> n0[kAhead], n1[kAhead];              // the rows that come next
-    const auto fetch = [&](int t) {
+    int slot = 0;
+    for (int t = 0; t < nt; ++t) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 2) : "memory");
+      R x0, x1;                                    // a thread's runs are nobody else's
+      x0.load(reinterpret_cast<const T*>(s_ring + tid * sizeof(R) + 2 * slot * run_bytes));
+      x1.load(reinterpret_cast<const T*>(s_ring + tid * sizeof(R) + (2 * slot + 1) * run_bytes));
+      fetch(t + kRing - 1, slot == 0 ? kRing - 1 : slot - 1);     // read a token ago
+      slot = slot == kRing - 1 ? 0 : slot + 1;
+      float x[N];
+      x0.get(x);
+      x1.get(x + RUN);
+      if (norms) {
+        float ss = 0.f;
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i)
-        if (live && t + i < nt) {
-          n0[i].load(src + (t + i) * stride + o0);
-          n1[i].load(src + (t + i) * stride + o1);
+        for (int j = 0; j < N; ++j) ss = fmaf(x[j], x[j], ss);
+#pragma unroll
+        for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        if (weight) {
+          const float f = rsqrtf(ss * (1.0f / D) + a.eps);      // 2^-22, as exact as the rest
+#pragma unroll
+          for (int j = 0; j < N; ++j) x[j] = x[j] * f * w[j];
         }
-    };
-    fetch(0);
-    for (int t = 0; t < nt; t += kAhead) {
-      Run<T, RUN> x0[kAhead], x1[kAhead];
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        x0[i] = n0[i];
-        x1[i] = n1[i];
       }
-      fetch(t + kAhead);
+      if (!writes) continue;
+      if (turns && !is_v) {
+        const float4* cs = reinterpret_cast<const float4*>(s_rot[t]) + lane;
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        if (t + i >= nt) break;
-        float x[N];
-        x0[i].get(x);
-        x1[i].get(x + RUN);
-        if (norms) {
-          float ss = 0.f;
-#pragma unroll
-          for (int j = 0; j < N; ++j) ss = fmaf(x[j], x[j], ss);
-#pragma unroll
-          for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-          if (weight) {
-            const float f = rsqrtf(ss * (1.0f / D) + a.eps);      // 2^-22, as exact as the rest
-#pragma unroll
-            for (int j = 0; j < N; ++j) x[j] = x[j] * f * w[j];
+        for (int j = 0; j < RUN; j += 2) {
+          const float4 r = cs[j / 2 * kLanes];     // cos, sin of pairs j and j + 1
+          if (a.interleaved) {
+            const float p0 = x[2 * j], q0 = x[2 * j + 1], p1 = x[2 * j + 2], q1 = x[2 * j + 3];
+            x[2 * j] = p0 * r.x - q0 * r.y;
+            x[2 * j + 1] = q0 * r.x + p0 * r.y;
+            x[2 * j + 2] = p1 * r.z - q1 * r.w;
+            x[2 * j + 3] = q1 * r.z + p1 * r.w;
+          } else {
+            const float p0 = x[j], q0 = x[j + RUN], p1 = x[j + 1], q1 = x[j + 1 + RUN];
+            x[j] = p0 * r.x - q0 * r.y;
+            x[j + RUN] = q0 * r.x + p0 * r.y;
+            x[j + 1] = p1 * r.z - q1 * r.w;
+            x[j + 1 + RUN] = q1 * r.z + p1 * r.w;
           }
         }
-        if (!writes) continue;
-        if (turns && !is_v) {
-          const float4* cs = reinterpret_cast<const float4*>(s_rot[t + i]) + lane;
-#pragma unroll
-          for (int j = 0; j < RUN; j += 2) {
-            const float4 r = cs[j / 2 * kLanes];     // cos, sin of pairs j and j + 1
-            if (a.interleaved) {
-              const float p0 = x[2 * j], q0 = x[2 * j + 1], p1 = x[2 * j + 2], q1 = x[2 * j + 3];
-              x[2 * j] = p0 * r.x - q0 * r.y;
-              x[2 * j + 1] = q0 * r.x + p0 * r.y;
-              x[2 * j + 2] = p1 * r.z - q1 * r.w;
-              x[2 * j + 3] = q1 * r.z + p1 * r.w;
-            } else {
-              const float p0 = x[j], q0 = x[j + RUN], p1 = x[j + 1], q1 = x[j + 1 + RUN];
-              x[j] = p0 * r.x - q0 * r.y;
-              x[j + RUN] = q0 * r.x + p0 * r.y;
-              x[j + 1] = p1 * r.z - q1 * r.w;
-              x[j + 1 + RUN] = q1 * r.z + p1 * r.w;
-            }
-          }
-        }
-        T* to = dst + (t + i) * step;
-        int32_t* p = pos_out + (t + i);
-        if (lookup) {
-          const long long row = row_of(c, g.t.layer, s, h, len + t0 + t + i);
-          if (row < 0) {
-            atomicOr(g.dev_status, NX_DEV_BAD_PAGE);
-            continue;
-          }
-          to = dst + row * D;
-          p = c.pos + row;
-        }
-        if (keeps_pos) *p = s_pos[t + i];
-        x0[i].set(x);
-        x1[i].set(x + RUN);
-        x0[i].store(to + o0);
-        x1[i].store(to + o1);
       }
+      T* to = dst + t * step;
+      int32_t* p = pos_out + t;
+      if (lookup) {
+        const long long row = row_of(c, g.t.layer, s, h, len + t0 + t);
+        if (row < 0) {
+          atomicOr(g.dev_status, NX_DEV_BAD_PAGE);
+          continue;
+        }
+        to = dst + row * D;
+        p = c.pos + row;
+      }
+      if (keeps_pos) *p = s_pos[t];
+      x0.set(x);
+      x1.set(x + RUN);
+      x0.store(to + o0);
+      x1.store(to + o1);
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
   }
   // s_len was read before the barrier above: with one block per sequence, or lengths that
   // come from elsewhere, nobody still reads what is set here
@@ -301,8 +313,13 @@ cudaError_t launch_append(AppendArgs& g, cudaStream_t st, int* launches) {
   }
   g.set_lens = !in_place || g.tiles * g.parts == 1;
   const long long blocks = (long long)g.c.seqs * g.tiles * g.parts;
-  cudaError_t e = launch_after(append_kernel<T, D, RUN>, dim3((unsigned)blocks), dim3(threads),
-                               (size_t)g.c.kv_heads * 4, st, g);
+  g.most = most < 1 ? 1 : most < kTokens ? most : kTokens;
+  const int slots = g.most < kRing ? g.most : kRing;
+  const int smem = slots * 2 * threads * (int)sizeof(Run<T, RUN>) + g.c.kv_heads * 4;
+  cudaError_t e = allow_smem<append_kernel<T, D, RUN>>(
+      kRing * 2 * kMaxThreads * (int)sizeof(Run<T, RUN>) + kMaxAppendHeads * 4);
+  if (e != cudaSuccess) return e;
+  e = launch_after(append_kernel<T, D, RUN>, dim3((unsigned)blocks), dim3(threads), smem, st, g);
   if (e != cudaSuccess) return e;
   note_launch(st, launches, "append");
   if (g.set_lens) return cudaSuccess;

@@ -5,8 +5,6 @@
 #include <cuda_fp8.h>
 #include <math.h>
 
-#include <atomic>
-
 #include "nx_internal.cuh"
 
 namespace nx {
@@ -169,9 +167,6 @@ struct SlotRows {
   }
 };
 
-__device__ __forceinline__ uint32_t smem_at(const void* p) {
-  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
 // Asynchronous copy of 16 bytes to shared memory, or of as many zeros.
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool ok) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
@@ -197,19 +192,6 @@ __device__ __forceinline__ void e4m3_pairs(uint32_t four, uint32_t& lo, uint32_t
       "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
       : "=r"(lo), "=r"(hi)
       : "r"(four));
-}
-
-// Lets a kernel use so much dynamic shared memory, once per device (twice does no harm).
-template <auto kernel>
-cudaError_t allow_smem(int bytes) {
-  static std::atomic<bool> done[64];
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev >= 0 && dev < 64 && done[dev].load(std::memory_order_acquire)) return cudaSuccess;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev].store(true, std::memory_order_release);
-  return e;
 }
 
 inline size_t round256(size_t x) { return (x + 255) / 256 * 256; }

@@ -4,8 +4,10 @@
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
-#include <utility>
 #include <stdint.h>
+
+#include <atomic>
+#include <utility>
 
 #include "nexus.h"
 
@@ -67,6 +69,9 @@ __host__ __device__ inline void pair_of(int k, int& u, int& t) {
 // ---------------------------------------------------------------------------
 // Small device helpers
 // ---------------------------------------------------------------------------
+__device__ __forceinline__ uint32_t smem_at(const void* p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
 __device__ __forceinline__ float ld_elem(const void* base, int dtype, long long idx) {
   if (dtype == NX_DTYPE_BF16)
     return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(base)[idx]);
@@ -392,6 +397,19 @@ cudaError_t launch_after(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
+// Lets a kernel use so much dynamic shared memory, once per device (twice does no harm).
+template <auto kernel>
+cudaError_t allow_smem(int bytes) {
+  static std::atomic<bool> done[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 0 && dev < 64 && done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev].store(true, std::memory_order_release);
+  return e;
 }
 
 // launch_after() of thread block clusters.
