@@ -8,12 +8,13 @@
 // it reads and writes, norm weights, the slice's length) is found once. A thread's features are
 // two runs that hold whole pairs (with runs of R: R i and rotary_dim / 2 + R i, or 2 R i and
 // 2 R i + R when interleaved), so that a rotation needs no exchange between threads; only the
-// norm's sum does. The rows of the next kAhead tokens are loaded while these are worked on.
+// norm's sum does. A thread's runs of the next tokens come into a ring of its own in shared memory
+// by asynchronous copies, which hold no registers and start before the angles are computed.
 //
-// What bounds it: reads and writes of head rows, 2 B a value each way, at 85 us for the prompts
-// below if they ran at the copy rate; measured 108 us (20500 tokens of 40 normed and rotated and
-// 8 plain head rows of 128, bf16: 4.7 TB/s). A single token of 48 head rows takes 3.1 us, all
-// latency.
+// What bounds it: reads and writes of head rows, 2 B a value each way. 25144 tokens of prompts of
+// up to 8192, 40 normed and rotated and 8 plain head rows of 128 each, bf16: 618 MB in 97.3 us,
+// 6.35 TB/s, 93 % of a plain copy's rate (108 us with the next two tokens in registers). A
+// single token of 48 head rows takes 2.6 us, all latency.
 #include <type_traits>
 
 #include "nx_internal.cuh"
@@ -23,9 +24,10 @@ namespace {
 
 constexpr int kTokens = 16;           // tokens of a thread block
 constexpr int kSoloTokens = 16;       // up to so many tokens one block takes a sequence
-// The largest block, and with it the registers of a thread: 640 leave 96 (108 us for 8192-token
-// prompts); 768 leave 80 and spill (113 us), 512 leave 128 and fewer warps (137 us).
-constexpr int kRing = 4;              // tokens whose rows are loaded at a time, less one
+// Tokens whose rows are on their way, less one: 3 take 101.9 us for the prompts, 4 98.4, 6 97.9.
+constexpr int kRing = 4;
+// The largest block, and with it the registers of a thread: 768 leave 80 (98.4 us), 640 leave 96,
+// and fewer warps (102.8 us), 1024 leave 64 (98.5 us).
 constexpr int kMaxThreads = 768;
 constexpr int kAppendThreads = 256;   // threads of a block, unless one block covers a sequence
 
@@ -56,6 +58,28 @@ __device__ __forceinline__ float2 rotation_of(int32_t p, uint64_t f) {
     s = x;
   }
   return quarter & 2u ? make_float2(-c, -s) : make_float2(c, s);
+}
+
+// Two binary32 products, or products and sums, by one instruction (a seventh of all instructions
+// less: one token of 48 head rows 2.62 us, not 2.74).
+__device__ __forceinline__ float2 pair(const float* x, int j) {
+  return make_float2(x[j], x[j + 1]);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 y;
+  asm("{\n\t.reg .b64 a, b, y;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mul.rn.f32x2 y, a, b;\n\tmov.b64 {%0, %1}, y;\n\t}"
+      : "=f"(y.x), "=f"(y.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return y;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 y;
+  asm("{\n\t.reg .b64 a, b, c, y;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mov.b64 c, {%6, %7};\n\tfma.rn.f32x2 y, a, b, c;\n\tmov.b64 {%0, %1}, y;\n\t}"
+      : "=f"(y.x), "=f"(y.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return y;
 }
 
 template <typename T, int RUN>
@@ -104,8 +128,9 @@ template <typename T, int D, int RUN>
 __global__ void __launch_bounds__(kMaxThreads) append_kernel(AppendArgs g) {
   constexpr int N = 2 * RUN, kLanes = D / N;         // threads of one head row
   using R = Run<T, RUN>;
-  // by token, then pair e of thread l at [e / 2][l][e % 2]: neighbours read neighbouring words
-  __shared__ __align__(16) float2 s_rot[kTokens][D / 2];
+  // by token, cosines and sines of pairs e and e + 1 of thread l at [e / 2][l] (two and two):
+  // neighbours read neighbouring words
+  __shared__ float4 s_rot[kTokens][D / 4];
   __shared__ int s_pos[kTokens];
   // the runs under way, [slot][run][thread], then [kv_heads] lengths, -1: leave alone
   extern __shared__ __align__(16) char s_ring[];
@@ -183,9 +208,12 @@ __global__ void __launch_bounds__(kMaxThreads) append_kernel(AppendArgs g) {
         s_len[h] = len;
       }
       for (int t = tid / 32; t < nt; t += blockDim.x / 32)
-        for (int i = tid % 32; i < half; i += 32)
-          s_rot[t][(i % RUN / 2 * kLanes + i / RUN) * 2 + i % 2] =
-              rotation_of(a.pos[first + t0 + t], a.rotary[i]);
+        for (int i = tid % 32; i < half; i += 32) {
+          const float2 v = rotation_of(a.pos[first + t0 + t], a.rotary[i]);
+          float* to = reinterpret_cast<float*>(&s_rot[t][i % RUN / 2 * kLanes + i / RUN]) + i % 2;
+          to[0] = v.x;
+          to[2] = v.y;
+        }
       if (tid < nt) s_pos[tid] = a.pos[first + t0 + tid];
       __syncthreads();
       primed = true;
@@ -219,35 +247,42 @@ __global__ void __launch_bounds__(kMaxThreads) append_kernel(AppendArgs g) {
       x0.get(x);
       x1.get(x + RUN);
       if (norms) {
-        float ss = 0.f;
+        float2 two = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int j = 0; j < N; ++j) ss = fmaf(x[j], x[j], ss);
+        for (int j = 0; j < N; j += 2) two = fma2(pair(x, j), pair(x, j), two);
+        float ss = two.x + two.y;
 #pragma unroll
         for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
         if (weight) {
           const float f = rsqrtf(ss * (1.0f / D) + a.eps);      // 2^-22, as exact as the rest
 #pragma unroll
-          for (int j = 0; j < N; ++j) x[j] = x[j] * f * w[j];
+          for (int j = 0; j < N; j += 2) {
+            const float2 y = mul2(mul2(pair(x, j), make_float2(f, f)), pair(w, j));
+            x[j] = y.x;
+            x[j + 1] = y.y;
+          }
         }
       }
       if (!writes) continue;
       if (turns && !is_v) {
-        const float4* cs = reinterpret_cast<const float4*>(s_rot[t]) + lane;
+        const float4* cs = s_rot[t] + lane;
 #pragma unroll
         for (int j = 0; j < RUN; j += 2) {
-          const float4 r = cs[j / 2 * kLanes];     // cos, sin of pairs j and j + 1
+          const float4 r = cs[j / 2 * kLanes];     // cosines and sines of pairs j and j + 1
           if (a.interleaved) {
             const float p0 = x[2 * j], q0 = x[2 * j + 1], p1 = x[2 * j + 2], q1 = x[2 * j + 3];
-            x[2 * j] = p0 * r.x - q0 * r.y;
-            x[2 * j + 1] = q0 * r.x + p0 * r.y;
-            x[2 * j + 2] = p1 * r.z - q1 * r.w;
-            x[2 * j + 3] = q1 * r.z + p1 * r.w;
+            x[2 * j] = p0 * r.x - q0 * r.z;
+            x[2 * j + 1] = q0 * r.x + p0 * r.z;
+            x[2 * j + 2] = p1 * r.y - q1 * r.w;
+            x[2 * j + 3] = q1 * r.y + p1 * r.w;
           } else {
-            const float p0 = x[j], q0 = x[j + RUN], p1 = x[j + 1], q1 = x[j + 1 + RUN];
-            x[j] = p0 * r.x - q0 * r.y;
-            x[j + RUN] = q0 * r.x + p0 * r.y;
-            x[j + 1] = p1 * r.z - q1 * r.w;
-            x[j + 1 + RUN] = q1 * r.z + p1 * r.w;
+            const float2 p = pair(x, j), q = pair(x, j + RUN), cos = make_float2(r.x, r.y),
+                         sin = make_float2(r.z, r.w);
+            const float2 qs = mul2(q, sin), turned = fma2(q, cos, mul2(p, sin));
+            x[j] = fmaf(p.x, cos.x, -qs.x);
+            x[j + 1] = fmaf(p.y, cos.y, -qs.y);
+            x[j + RUN] = turned.x;
+            x[j + 1 + RUN] = turned.y;
           }
         }
       }
@@ -316,8 +351,10 @@ cudaError_t launch_append(AppendArgs& g, cudaStream_t st, int* launches) {
   g.most = most < 1 ? 1 : most < kTokens ? most : kTokens;
   const int slots = g.most < kRing ? g.most : kRing;
   const int smem = slots * 2 * threads * (int)sizeof(Run<T, RUN>) + g.c.kv_heads * 4;
-  cudaError_t e = allow_smem<append_kernel<T, D, RUN>>(
-      kRing * 2 * kMaxThreads * (int)sizeof(Run<T, RUN>) + kMaxAppendHeads * 4);
+  cudaError_t e = cudaSuccess;
+  if (smem > 32 * 1024)                              // with the angles: 48 KB need no leave
+    e = allow_smem<append_kernel<T, D, RUN>>(
+        kRing * 2 * kMaxThreads * (int)sizeof(Run<T, RUN>) + kMaxAppendHeads * 4);
   if (e != cudaSuccess) return e;
   e = launch_after(append_kernel<T, D, RUN>, dim3((unsigned)blocks), dim3(threads), smem, st, g);
   if (e != cudaSuccess) return e;
@@ -352,7 +389,8 @@ extern "C" nx_status nexus_append(nx_cache* cache, const nx_tokens* tokens, cons
   const int most = tokens->max_tokens < tokens->tokens ? tokens->max_tokens : tokens->tokens;
   const long long blocks = (long long)c.seqs * (most / kTokens + 1) *
                            ((long long)c.kv_heads * (c.group + 2) / 16 + 1);
-  if (c.kv_heads > kMaxAppendHeads || blocks > 0x7FFFFFFFLL || (long long)c.kv_heads * c.group > (1 << 20))
+  if (c.kv_heads > kMaxAppendHeads || blocks > 0x7FFFFFFFLL ||
+      (long long)c.kv_heads * c.group > (1 << 20))
     return NX_ERR_UNSUPPORTED;
   if ((a.q == nullptr) != (a.q_out == nullptr) && tokens->tokens > 0) return NX_ERR_INVALID_ARG;
   if (tokens->tokens > 0) {
