@@ -146,10 +146,13 @@ struct Shape {
 };
 
 // A warp's ring: stages of one step each. kPerSm thread blocks of four warps share an SM's
-// 227 KB; an image's tail takes the image's ring.
+// 227 KB; an image's tail takes the image's ring. From the image three blocks, for their
+// conversions' latencies (16 rows against two blocks: 4 x 32768 slots, 8 heads, 20 query rows 86.9
+// us, not 100.4, 16 rows 65.4, not 67.2; 32 x 6960, 20 rows 140.4, not 154.3, 16 rows 93.7, not
+// 90.5).
 template <int KIND, int D, int ROWS>
 struct Ring {
-  static constexpr int kPerSm = KIND == kImage && ROWS == 8 ? 3 : 2;
+  static constexpr int kPerSm = KIND == kImage ? 3 : 2;
   static constexpr int kBytes = Shape<KIND, D>::kStage;
   static constexpr int kFit = 196608 / (kPerSm * kWarps * kBytes);
   static constexpr int kDeep = kFit > 8 ? 8 : kFit;
@@ -728,17 +731,14 @@ __global__ void __launch_bounds__(kWarps * 32, Ring<KIND, D, ROWS>::kPerSm)
     const AttendShare sh = attend_share<kWarps * 32>(
         g, [&](int i) { return unit_tiles<KIND>(attend_unit<ROWS>(g, i)); });
     grid_dep_trigger();
-    if (sh.start >= sh.total) {
-      if (tid == 0) g.ws.desc[b] = make_int2(-1, 0);
-      return;
-    }
+    if (tid == 0 && !g.splits) g.ws.desc[b] = make_int2(-1, 0);
+    if (sh.start >= sh.total) return;
     per = sh.per;
     stop = min(sh.total, sh.start + per);
     unit = sh.unit;
     at = sh.at;
     pos = sh.start;
   }
-  int2 desc = make_int2(-1, 0);
   while (pos < stop) {
     const AttendUnit u = attend_unit<ROWS>(g, unit);
     const int tiles = unit_tiles<KIND>(u);
@@ -824,15 +824,16 @@ __global__ void __launch_bounds__(kWarps * 32, Ring<KIND, D, ROWS>::kPerSm)
         }
       }
       __syncthreads();
-      if (a0 == 0 && a1 < tiles) desc = make_int2(unit, (at + tiles - 1) / per);
+      // for the join: by unit where it has blocks for each, else by its first block
+      if (EVEN && a0 == 0 && tid == 0 && (g.splits || a1 < tiles))
+        g.ws.desc[g.splits ? unit : b] =
+            make_int2(!g.splits ? unit : a1 < tiles ? b : -1, (at + tiles - 1) / per);
     }
     pos = at + a1;
     at += tiles;
     ++unit;
   }
-  if constexpr (EVEN) {
-    if (tid == 0) g.ws.desc[b] = desc;
-  } else if (meets) {
+  if (!EVEN && meets) {
     // the cluster's pieces, in the order of their slots, from the blocks' shared memory
     cluster_sync();
     const AttendUnit u = attend_unit<ROWS>(g, b / g.ranks);
@@ -863,20 +864,34 @@ __global__ void __launch_bounds__(kWarps * 32, Ring<KIND, D, ROWS>::kPerSm)
   }
 }
 
-// Joins the pieces of the unit that starts in block b and ends in a later one.
+// Joins the pieces of a unit that starts in a block b and ends in a later one. Few units, each of
+// many pieces: `g.splits` blocks a unit, for its rows in turn (8 slices of 32768 rows, 16 query
+// rows: attention takes 38.2 us in bf16, 48.9 with a block for each b; 31.9 and 43.1 us from the
+// image); else a block for each b.
 constexpr int kJoinWarps = 16;
-template <int D, int ROWS>
+template <int KIND, int D, int ROWS>
 __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(AttendArgs g) {
-  constexpr int E = D / 32, GR = kJoinWarps / ROWS > 0 ? kJoinWarps / ROWS : 1;
+  constexpr int E = D / 32;
   __shared__ float s_o[kJoinWarps][D], s_m[kJoinWarps], s_l[kJoinWarps];
   grid_dep_wait();
-  const int b = blockIdx.x;
-  const int2 desc = g.ws.desc[b];
+  const int splits = max(g.splits, 1), split = blockIdx.x % splits;
+  int b = blockIdx.x / splits, unit = b;
+  int2 desc = make_int2(-1, 0);
+  if (!g.splits) {
+    desc = g.ws.desc[b];
+    unit = desc.x;
+  } else if (unit_tiles<KIND>(attend_unit<ROWS>(g, unit)) > 0) {   // else nobody described it
+    desc = g.ws.desc[unit];
+    b = desc.x;
+  }
   if (desc.x < 0) return;
-  const AttendUnit u = attend_unit<ROWS>(g, desc.x);
+  const AttendUnit u = attend_unit<ROWS>(g, unit);
+  const int mine = (u.rows - split + splits - 1) / splits;         // rows split, split + splits ..
+  if (mine <= 0) return;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int groups = max(GR, u.rows <= ROWS / 4 ? 4 * GR : u.rows <= ROWS / 2 ? 2 * GR : GR);
-  const int r = warp / groups, part = warp % groups;    // as many warps per row as there are
+  int groups = kJoinWarps;                               // warps of a row
+  while (groups > 1 && mine * groups > kJoinWarps) groups /= 2;
+  const int part = warp % groups, r = split + warp / groups * splits;
   float m = -INFINITY, l = 0.f, o[E] = {};
   if (r < u.rows) {
 #pragma unroll 4
@@ -902,7 +917,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(AttendArgs
     s_l[warp] = l;
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < u.rows * D; i += kJoinWarps * 32) {
+  for (int i = threadIdx.x; i < mine * D; i += kJoinWarps * 32) {
     const int rr = i / D, f = i % D;
     float top = -INFINITY, sum = 0.f, x = 0.f;
     for (int w = rr * groups; w < (rr + 1) * groups; ++w) top = fmaxf(top, s_m[w]);
@@ -911,7 +926,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(AttendArgs
       sum += k * s_l[w];
       x += k * s_o[w][f];
     }
-    finish_row(g, u, rr, D, f, top, sum, x);
+    finish_row(g, u, split + rr * splits, D, f, top, sum, x);
   }
 }
 
@@ -954,6 +969,9 @@ cudaError_t launch_attend(AttendArgs& g, cudaStream_t st, int* launches) {
   if (g.c.capacity <= (units * kRanks <= 2 * kSms ? few / 2 : few)) ranks = 1;
   const int limit = ranks > 1 ? ranks * most_of : units >= fit ? 2 * few : few;
   g.ranks = g.c.capacity <= limit ? ranks : 0;
+  g.splits = 0;
+  if (units * 2 <= kSms)
+    for (g.splits = ROWS; g.splits > 1 && units * g.splits > kSms;) g.splits /= 2;
   const int grid = (int)(g.ranks ? units * g.ranks : most < fit ? most : fit);
   constexpr int smem = kWarps * R::kDeep * R::kBytes;
   cudaError_t e;
@@ -970,7 +988,9 @@ cudaError_t launch_attend(AttendArgs& g, cudaStream_t st, int* launches) {
   e = launch_after(attend_kernel<KIND, D, ROWS, true>, dim3(grid), dim3(kWarps * 32), smem, st, g);
   if (e != cudaSuccess) return e;
   note_launch(st, launches, "attend");
-  e = launch_after(attend_join_kernel<D, ROWS>, dim3(grid), dim3(kJoinWarps * 32), 0, st, g);
+  e = launch_after(attend_join_kernel<KIND, D, ROWS>,
+                   dim3(g.splits ? (unsigned)(units * g.splits) : (unsigned)grid),
+                   dim3(kJoinWarps * 32), 0, st, g);
   if (e == cudaSuccess) note_launch(st, launches, "attend_join");
   return e;
 }

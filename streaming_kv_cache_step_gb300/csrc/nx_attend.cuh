@@ -32,6 +32,7 @@ struct AttendArgs {
   int b, b_shift;       // rows per image block, a power of two
   int mtiles;           // row tiles per slice
   int ranks;            // row kernel: thread blocks per unit, one cluster (0: even shares)
+  int splits;           // its join: blocks per unit (0: a block for each block's last unit)
   int units;            // seqs * kv_heads * mtiles
   float c1;             // scale * log2(e)
 };
