@@ -895,12 +895,12 @@ cudaError_t launch_t(AttendArgs& g, cudaStream_t st, int* launches) {
 
 // The row kernel takes 16 rows a pass over K and V, this one 256 but at a higher cost, from 8-bit
 // rows more so. Measured (us, this kernel / the row kernel) on 32 x 8 slices of 6960 rows: bf16, 16
-// rows 181 / 151, 20 rows 181 / 282; 8 bits, 64 rows 371 / 293, 96 rows 374 / 413. A second pass
+// rows 181 / 151, 20 rows 180 / 283; 8 bits, 80 rows 363 / 339, 96 rows 366 / 420. A second pass
 // that finds K and V in L2 costs less: bf16, 32 rows, 4 x 8 slices 45 / 43, one sequence of 8
-// slices of 32768 rows 62 / 50.
+// slices of 32768 rows 62 / 45; 36 rows 45 / 53 and 62 / 58.
 bool attend_tc_takes(const nx_cache& c, const nx_tokens& t, bool image) {
   const long long bytes = (long long)c.seqs * c.kv_heads * c.capacity * c.head_dim * 4;
-  const int rows = image ? 64 : bytes <= (128LL << 20) ? 32 : 16;
+  const int rows = image ? 80 : bytes <= (128LL << 20) ? 32 : 16;
   return c.dtype == NX_DTYPE_BF16 && most_tokens(t) * c.group > rows;
 }
 
