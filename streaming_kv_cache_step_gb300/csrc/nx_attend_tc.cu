@@ -96,6 +96,11 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile
   atomicOr(dev_status, NX_DEV_TIMEOUT);
   return false;
 }
+// Orders this thread's accesses to shared memory before those of TMA, bulk copies and tcgen05 that
+// a barrier lets go after it.
+__device__ __forceinline__ void fence_async() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
 __device__ __forceinline__ void tc_before() {
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
 }
@@ -371,7 +376,7 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
         const SlotRows rows(g, u);
         // K and V tiles in turn, every warp its runs of 8 slots
         const auto announce = [&](int k) {
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          fence_async();
           bar_arrive(full + 8 * (k % P::kSlots));
         };
         // whether any page of the piece is bad; then every K tile gets its marks
@@ -487,8 +492,9 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
               const bool go =
                   bar_wait(rempty + 8 * st, (no / P::kRaw & 1) ^ 1, up, g.dev_status);
               if (lane < kGroups) s_scale[st][lane] = scale;
-              // a run on a bad page: zeros for what the stage held before
-              if (any_bad)
+              // a run on a bad page: zeros for what the stage held before; the stage's next bulk
+              // copy, of the other proxy, comes behind them
+              if (any_bad) {
                 for (int q = 0; q < kGroups; ++q) {
                   const bool zero = __shfl_sync(0xffffffffu, row == -1 ? 1 : 0, q) != 0 && go;
                   if (zero)
@@ -498,6 +504,8 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
                                    "r"(0)
                                    : "memory");
                 }
+                fence_async();
+              }
               const bool lead = go && row >= 0 && 8 * lane % box == 0;
               const int bytes = lead ? (min(held, t + box) - t) * D : 0;
               const unsigned total = __reduce_add_sync(0xffffffffu, (unsigned)bytes);
@@ -625,7 +633,7 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
                        ((i ^ r) & 7) * 16,
                    ok ? src + 8 * i : src, ok);
           asm volatile("cp.async.wait_all;" ::: "memory");
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          fence_async();
           bar_arrive(qfull);
         }
         // a warp without rows only keeps the count: what the products make of its rows is
@@ -777,6 +785,8 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
             else g.ws.stat[piece * kTcRows + rr] = make_float2(m, l);
           }
         }
+        // s_o lies over the ring, which the next piece's boxes fill by the other proxy
+        if constexpr (NQ == 1 && !IMAGE) fence_async();
         tc_before();
       }
       slot_no += 2 * n;
