@@ -380,7 +380,9 @@ size_t nexus_attend_workspace_bytes(const nx_cache* cache, const nx_tokens* toke
  * few or short slices (capacity up to some hundred rows, some thousand for a few dozen slices) on
  * the first, else two; the same bits every time.
  * NX_ERR_UNSUPPORTED for an image of an fp32 cache, for more than 2^20 query heads or 2^24
- * (sequence, KV head) pairs, or more than 2^31 tiles of 8 query rows x 64 slots.
+ * (sequence, KV head) pairs, or more than 2^31 tiles of 8 query rows x 64 slots. The scales of an
+ * image are non-negative; a slice's blocks may differ in scale by any factor up to 2^120 (values
+ * below that part of the slice's largest may be lost).
  */
 nx_status nexus_attend(const nx_cache* cache, const nx_tokens* tokens, const nx_image* image,
                        const nx_attend* args, void* ws, size_t ws_bytes, int32_t* dev_status,

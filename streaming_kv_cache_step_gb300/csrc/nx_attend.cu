@@ -42,8 +42,13 @@ constexpr bool kIsBf16 = KIND == kBf16 || KIND == kTail;
 
 // Probabilities are kept at 2^kUp times their size, and m is only raised when a logit is more
 // than 2^kSlack above it, so they are at most 2^(kUp + kSlack) = 32768: below fp16's largest
-// value, with 2^-36 of the largest one still representable.
-constexpr float kUp = 11.f, kSlack = 4.f;
+// value, with 2^-36 of the largest one still representable. From the image a probability is
+// multiplied by its values' scale, in units of the largest scale so far, before it becomes fp16: that
+// leaves 2^-28 of the largest while scales stay within kApart of one another. From the first step
+// with a run below that on, a warp's steps go to pv_apart, whose operands never hold a scale (behind a
+// block of zeros, whose scale is 1, values of 2^-12 take 116 us over 32 x 8 x 6960 rows, one token, not
+// 83; the check itself 0.6 of 165 us over 16 x 8 x 32768).
+constexpr float kUp = 11.f, kSlack = 4.f, kApart = 0.00390625f;
 
 template <int KIND>
 __device__ __forceinline__ void mma16(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
@@ -379,21 +384,31 @@ __device__ __forceinline__ void plain_logits(const AttendArgs& g, const AttendUn
   }
 }
 
+// V load w of slot 8 j + 2 c + e.
+template <int KIND, int D>
+__device__ __forceinline__ uint4 load_v(uint32_t stage, int lane, int j, int e, int w) {
+  using S = Shape<KIND, D>;
+  const int f = (w * S::kWide + lane / 4 * S::kStep) * S::kBytes;    // byte in the row
+  const uint32_t at = stage + S::kStage / 2 + S::v_at(8 * j + 2 * (lane % 4) + e, f / 16);
+  if constexpr (S::kRow >= 128) return lds16(at);
+  uint4 x = make_uint4(0, 0, 0, 0);
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(x.x), "=r"(x.y) : "r"(at + f % 16)
+               : "memory");
+  return x;
+}
+// The codes of two slots' words as operands, feature by feature.
+__device__ __forceinline__ void code_pairs(uint32_t y0, uint32_t y1, uint32_t* b) {
+  const uint32_t z0 = __byte_perm(y0, y1, 0x5140), z1 = __byte_perm(y0, y1, 0x7362);
+  e4m3_pairs(z0, b[0], b[1]);
+  e4m3_pairs(z1, b[2], b[3]);
+}
+
 // o += p V.
 template <int KIND, int D, int ROWS>
 __device__ __forceinline__ void pv(uint32_t stage, int lane, const float p[][4],
                                    State<D, ROWS>& st) {
   using S = Shape<KIND, D>;
-  // V load w of slot 8 j + 2 c + e
-  const auto load = [&](int j, int e, int w) {
-    const int f = (w * S::kWide + lane / 4 * S::kStep) * S::kBytes;    // byte in the row
-    const uint32_t at = stage + S::kStage / 2 + S::v_at(8 * j + 2 * (lane % 4) + e, f / 16);
-    if constexpr (S::kRow >= 128) return lds16(at);
-    uint4 x = make_uint4(0, 0, 0, 0);
-    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(x.x), "=r"(x.y) : "r"(at + f % 16)
-                 : "memory");
-    return x;
-  };
+  const auto load = [&](int j, int e, int w) { return load_v<KIND, D>(stage, lane, j, e, w); };
   if constexpr (KIND == kF32) {
     uint32_t f[4];
     tf32_terms(__float_as_uint(p[0][0]), f[0], f[1]);
@@ -439,9 +454,7 @@ __device__ __forceinline__ void pv(uint32_t stage, int lane, const float p[][4],
               b[j][0] = __byte_perm(y0, y1, 0x5410);
               b[j][1] = __byte_perm(y0, y1, 0x7632);
             } else {
-              const uint32_t z0 = __byte_perm(y0, y1, 0x5140), z1 = __byte_perm(y0, y1, 0x7362);
-              e4m3_pairs(z0, b[j][0], b[j][1]);
-              e4m3_pairs(z1, b[j][2], b[j][3]);
+              code_pairs(y0, y1, b[j]);
             }
           }
 #pragma unroll
@@ -457,11 +470,75 @@ __device__ __forceinline__ void pv(uint32_t stage, int lane, const float p[][4],
   }
 }
 
-// Slots [base + kSlots * i, ...) for i = from, from + kWarps, ... < to, up to slot `end`.
-template <int KIND, int D, int ROWS, int kDeep, int kStageBytes>
+// l += sum p and o += p V of an image step whose runs' scales lie far apart, p = 2^(x - m): a run by
+// itself, its probabilities in units of the row's largest in the run, and what turns them into o's
+// units (scale and all) in binary32 behind the product. x waits where the step's keys were.
+template <int D, int ROWS>
+__device__ __forceinline__ void pv_apart(uint32_t stage, int lane, const float x[][4],
+                                         const float* scale, float vinv, State<D, ROWS>& st) {
+  using S = Shape<kImage, D>;
+  static_assert(S::NT * 512 <= S::kStage / 2, "");
+  __syncwarp();                         // everyone has read the keys
+#pragma unroll
+  for (int j = 0; j < S::NT; ++j)
+    asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(stage + (32 * j + lane) * 16),
+                 "f"(x[j][0]), "f"(x[j][1]), "f"(x[j][2]), "f"(x[j][3])
+                 : "memory");
+#pragma unroll 1
+  for (int j = 0; j < S::NT; ++j) {
+    const uint4 y = lds16(stage + (32 * j + lane) * 16);
+    float p[4] = {__uint_as_float(y.x), __uint_as_float(y.y), __uint_as_float(y.z),
+                  __uint_as_float(y.w)};
+    float f[ROWS / 8];
+#pragma unroll
+    for (int e = 0; e < ROWS / 8; ++e) {
+      float top = fmaxf(p[2 * e], p[2 * e + 1]);
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const float m = st.m[e] == -INFINITY ? 0.f : st.m[e];
+      f[e] = top == -INFINITY ? 0.f : ex2(top - m) * (scale[j] * vinv);
+      st.l[e] += ex2(p[2 * e] - m + kUp) + ex2(p[2 * e + 1] - m + kUp);
+      const float sub = (top == -INFINITY ? 0.f : top) - kUp;
+      p[2 * e] = ex2(p[2 * e] - sub);
+      p[2 * e + 1] = ex2(p[2 * e + 1] - sub);
+    }
+    uint32_t a[4] = {pack2<kImage>(p[0], p[1]), 0, 0, 0};
+    if constexpr (ROWS == 8) a[1] = rest2<kImage>(p[0], p[1], a[0]);
+    else a[1] = pack2<kImage>(p[2], p[3]);
+#pragma unroll
+    for (int w = 0; w < S::VV; ++w) {
+      const uint4 v0 = load_v<kImage, D>(stage, lane, j, 0, w);
+      const uint4 v1 = load_v<kImage, D>(stage, lane, j, 1, w);
+#pragma unroll
+      for (int i = 0; i < (D == 64 ? 2 : 4); ++i) {
+        uint32_t b[4];
+        code_pairs(word(v0, i), word(v1, i), b);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float t[4] = {0.f, 0.f, 0.f, 0.f};
+          mma16<kImage>(t, a, b[e], 0u);
+          float* o = st.o[S::kPer * w + 4 * i + e];
+          o[0] += t[0] * f[0];
+          o[1] += t[1] * f[0];
+          o[2] += t[2] * f[ROWS / 8 - 1];
+          o[3] += t[3] * f[ROWS / 8 - 1];
+        }
+      }
+    }
+  }
+}
+
+// Slots [base + kSlots * i, ...) for i = from, from + kWarps, ... < to, up to slot `end`. vref: the
+// image's largest value scale so far, which o is in units of. Where a run's scale is far below it,
+// the steps from there on are attend_apart's.
+template <int D, int ROWS, int kDeep, int kStageBytes>
+__device__ __noinline__ void attend_apart(const AttendArgs& g, const AttendUnit& u, int base, int end,
+                                          int from, int to, uint32_t ring, Meta* meta,
+                                          State<D, ROWS>& st, float vref);
+template <int KIND, int D, int ROWS, int kDeep, int kStageBytes, bool APART = false>
 __device__ __forceinline__ void attend_part(const AttendArgs& g, const AttendUnit& u, int base,
                                             int end, int from, int to, uint32_t ring, Meta* meta,
-                                            State<D, ROWS>& st) {
+                                            State<D, ROWS>& st, float vref = 1.1754944e-38f) {
   using S = Shape<KIND, D>;
   if (from >= to) return;
   const int lane = threadIdx.x % 32;
@@ -472,7 +549,7 @@ __device__ __forceinline__ void attend_part(const AttendArgs& g, const AttendUni
     lim[e] = r < u.rows ? min(end, row_limit(g, u, u.r0 + r)) : 0;
   }
   const int low = min(end, u.low);
-  float vref = 1.1754944e-38f, vinv = 0.f;   // image: the largest value scale so far; o is in it
+  float vinv = 1.f / vref;
   const SlotRows at(g, u);
   const long long blocks0 =
       KIND == kImage && !g.c.page_size ? image_scale_at(g.c, g.t.layer, u.s, u.h, 0, g.b) : 0;
@@ -529,8 +606,8 @@ __device__ __forceinline__ void attend_part(const AttendArgs& g, const AttendUni
   for (int n = 0; n < kDeep - 1; ++n) start(from + n * kWarps, n);
   Query<KIND, D, ROWS> q;               // while the first rows are on their way
   q.load(g, u, lane);
-  int n = 0;
-  for (int i = from; i < to; i += kWarps) {
+  int n = 0, i = from;
+  for (; i < to; i += kWarps) {
     const int t = base + S::kSlots * i;
     asm volatile("cp.async.wait_group %0;" ::"n"(kDeep - 2) : "memory");
     __syncwarp();                       // everyone's copies are in, and step i - 1 is read
@@ -546,6 +623,11 @@ __device__ __forceinline__ void attend_part(const AttendArgs& g, const AttendUni
         vs[j] = meta[n].scale[4 + j];
       }
     }
+    // whether run lane % NT's scale is far below (less one: that of no run is 0)
+    const auto far_below = [&](float v) {
+      return __float_as_uint(meta[n].scale[4 + lane % S::NT]) - 1u < __float_as_uint(v * kApart) - 1u;
+    };
+    const bool far = KIND == kImage && !APART && far_below(vref);
     n = n == kDeep - 1 ? 0 : n + 1;
     float s[S::NT][4];
     qk<KIND, D, ROWS>(q, stage, lane, s);
@@ -597,9 +679,15 @@ __device__ __forceinline__ void attend_part(const AttendArgs& g, const AttendUni
     if constexpr (KIND == kImage) {
 #pragma unroll
       for (int j = 0; j < S::NT; ++j) vnew = fmaxf(vnew, vs[j]);
-      up |= vnew > vref;
+      up |= vnew > vref || far;
     }
     if (__any_sync(0xffffffffu, up)) {
+      if constexpr (KIND == kImage && !APART) {
+        n = n == 0 ? kDeep - 1 : n - 1;
+        const bool leave = __any_sync(0xffffffffu, far_below(vnew));
+        n = n == kDeep - 1 ? 0 : n + 1;
+        if (leave) break;
+      }
       const float vf = KIND == kImage ? vref / vnew : 1.f;
       vref = vnew;
       if constexpr (KIND == kImage) vinv = 1.f / vnew;
@@ -619,6 +707,10 @@ __device__ __forceinline__ void attend_part(const AttendArgs& g, const AttendUni
         st.o[n][2] *= f[ROWS / 8 - 1];
         st.o[n][3] *= f[ROWS / 8 - 1];
       }
+    }
+    if constexpr (APART) {
+      pv_apart<D, ROWS>(stage, lane, s, meta[n == 0 ? kDeep - 1 : n - 1].scale + 4, vinv, st);
+      continue;
     }
     float vr[S::NT];
     if constexpr (KIND == kImage) {
@@ -641,11 +733,32 @@ __device__ __forceinline__ void attend_part(const AttendArgs& g, const AttendUni
     pv<KIND, D, ROWS>(stage, lane, s, st);
   }
   if constexpr (KIND == kImage) {
+    if constexpr (!APART)
+      if (i < to) {
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        State<D, ROWS> copy = st;       // in local memory: st and u stay in registers
+        const AttendUnit unit = u;
+        attend_apart<D, ROWS, kDeep, kStageBytes>(g, unit, base, end, i, to, ring, meta, copy, vref);
+        st = copy;
+        return;
+      }
 #pragma unroll
     for (int n = 0; n < D / 8; ++n)
 #pragma unroll
       for (int e = 0; e < 4; ++e) st.o[n][e] *= vref;
   }
+}
+
+// The steps of an image from `from` on by pv_apart: a function of its own, so that the others' loop
+// keeps its registers.
+template <int D, int ROWS, int kDeep, int kStageBytes>
+__device__ __noinline__ void attend_apart(const AttendArgs& g, const AttendUnit& u, int base, int end,
+                                          int from, int to, uint32_t ring, Meta* meta,
+                                          State<D, ROWS>& st, float vref) {
+  State<D, ROWS> mine = st;
+  attend_part<kImage, D, ROWS, kDeep, kStageBytes, true>(g, u, base, end, from, to, ring, meta, mine,
+                                                         vref);
+  st = mine;
 }
 
 template <int KIND>
@@ -699,7 +812,7 @@ __device__ __forceinline__ float remote(const float* p, int rank) {
 // sequences of 16384 rows take 167.4 us instead of 163.9.
 template <int KIND, int D, int ROWS, bool EVEN>
 __global__ void __launch_bounds__(kWarps * 32, Ring<KIND, D, ROWS>::kPerSm)
-    attend_kernel(AttendArgs g) {
+    attend_kernel(const __grid_constant__ AttendArgs g) {
   constexpr int kTileSlots = kTileOf<KIND>;
   using R = Ring<KIND, D, ROWS>;
   constexpr int kRing = R::kDeep * R::kBytes;

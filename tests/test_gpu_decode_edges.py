@@ -24,3 +24,77 @@ def test_attend_pieces_of_one_block_follow_one_another(d, page, tokens):
     c = Case(seqs=60, kv_heads=4, group=4, d=d, page=page, capacity=384,
              lens=rng.choice([64, 128, 192, 256, 320, 384], (60, 4)), seed=page)
     _check_attend(c, [tokens] * 60, uniform=True)
+
+
+# ---------------------------------------------------------------------------
+# attend from an image whose blocks differ in scale
+# ---------------------------------------------------------------------------
+
+def _by_block(c, powers, name="v"):
+    """Multiplies a slice's blocks by powers of two (None: zeros), in turn, in every slice."""
+    t = getattr(c, name)
+    for s in range(c.S):
+        for h in range(c.H):
+            T = int(c.lens[0, s, h])
+            for i, j in enumerate(range(0, T, c.b)):
+                p = powers[(i + s + h) % len(powers)]
+                at = c.at(0, s, h, min(T, j + c.b), j)
+                t[at] = t[at] * 2.0 ** p if p is not None else 0.0
+
+
+@pytest.mark.parametrize("page", [0, 8, 16, 64])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("group,tokens", [(4, 1), (16, 1), (5, 9)])
+@pytest.mark.parametrize("powers", [[None, -24, -24, -24], [None, -30, 20], [-70, 40, -9, -10, 0],
+                                    [None, -50, -50, -50, -50, -50, -50], [0, 7, 0, 9, -8]],
+                         ids=["zeros", "mixed", "far", "tiny", "near"])
+def test_attend_image_scales_differ_within_a_slice(powers, group, tokens, d, page):
+    # a block's scale is its own: next to zeros (their scale is 1) or to values 2^50 times its own,
+    # its codes come out as exactly as alone, wherever the weights lie
+    c = Case(seqs=2, kv_heads=2, group=group, d=d, page=page, capacity=704,
+             lens=[[704, 640], [96, 352]], seed=len(powers))
+    _by_block(c, powers)
+    _check_attend(c, [tokens] * 2, image=True, uniform=True)
+
+
+@pytest.mark.parametrize("page", [0, 8])
+@pytest.mark.parametrize("group", [4, 16])
+@pytest.mark.parametrize("less", [24.0, 30.0, 40.0, 100.0])
+def test_attend_image_large_values_with_small_weights(less, group, page):
+    # values 2^40 times the others', at logits that leave them a small part (e^-24 2^40 = 41), an
+    # even part or nothing of the sum, block by block: both sides of it show in the output
+    c = Case(seqs=1, kv_heads=2, group=group, page=page, capacity=512, lens=512, seed=7)
+    for h in range(2):
+        for j in range(0, 512, 2 * c.b):
+            at = c.at(0, 0, h, j + c.b, j)
+            c.v[at] = c.v[at] * 2.0 ** 40
+            c.k[at][..., 0] = 0.0
+            k = c.k[at]
+            k[:, 0] = -less
+            c.k[at] = k
+        for j in range(c.b, 512, 2 * c.b):
+            at = c.at(0, 0, h, j + c.b, j)
+            k = c.k[at]
+            k[:, 0] = 0.0
+            c.k[at] = k
+
+    def mutate(c, q):
+        q[..., 0] = 128 ** 0.5                                       # times the scale: 1
+
+    _check_attend(c, [1], image=True, mutate=mutate)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("group,tokens", [(1, 8), (2, 8), (4, 10), (8, 10)])
+def test_attend_image_large_values_that_are_not_seen_yet(group, tokens, d):
+    # the newest rows, 2^40 and 2^100 times the others, stand in the image but most tokens do not
+    # see them
+    for up in (40, 100):
+        c = Case(seqs=2, kv_heads=2, group=group, d=d, page=8, capacity=256, lens=[[256, 128], [64, 8]],
+                 seed=up)
+        for s in range(2):
+            for h in range(2):
+                T = int(c.lens[0, s, h])
+                at = c.at(0, s, h, T, T - 8)
+                c.v[at] = c.v[at] * 2.0 ** up
+        _check_attend(c, [tokens] * 2, image=True, uniform=True)
