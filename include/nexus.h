@@ -307,7 +307,8 @@ typedef struct nx_append {
  * q goes to q_out; k, v and p become row lens_in + i of the slice (l, s, h) for the i-th
  * token of sequence s; then lens = lens_in + the sequence's tokens. The angle is reduced in
  * integers modulo one turn, so it is as exact at the last position as at the first.
- * lens_in lets a caller take tokens back: rows behind it (rejected drafts) are overwritten.
+ * lens_in lets a caller take tokens back: rows behind it (rejected drafts) are overwritten (in
+ * the cache: for an image of it see nexus_append_image).
  * A slice without room (NX_DEV_FULL) or with a bad length (NX_DEV_BAD_LEN) is left
  * untouched; a row whose page is out of range (NX_DEV_BAD_PAGE) is not written.
  * lens_in may be the layer's part of cache->lens, but not overlap it otherwise.
@@ -323,8 +324,11 @@ nx_status nexus_append(nx_cache* cache, const nx_tokens* tokens, const nx_append
  *   contiguous: k_scale, v_scale [layers][seqs][kv_heads][ceil(capacity / b)];
  *   paged:                       [layers][num_pages][kv_heads][page_size / b].
  * rows [layers][seqs][kv_heads]: the image holds slots 0 .. rows - 1 of a slice, whole
- * blocks; the cache keeps every row, so that evictions go on from the exact keys. An
- * eviction moves rows: the caller sets rows to 0 behind it (or passes rows_in below).
+ * blocks; the cache keeps every row, so that evictions go on from the exact keys. The image
+ * does not follow the cache by itself. An eviction moves rows: the caller sets rows to 0 behind
+ * it (or passes rows_in below). Rows that are taken back (lens_in of nexus_append) may stand in
+ * it: nexus_append_image lowers rows to the blocks that stay; a caller of nexus_append does so
+ * itself, to floor(lens_in / b) b at most, or attention reads the codes of rows that are gone.
  */
 typedef struct nx_image {
   void* k;                     /* 16-byte aligned */
@@ -333,6 +337,14 @@ typedef struct nx_image {
   float* v_scale;
   int32_t* rows;
 } nx_image;
+
+/*
+ * nexus_append, and the image (nullable) forgets what the new rows replace: rows of every slice of
+ * the layer that takes its tokens drops to floor(lens_in / b) b where it is more.
+ * NX_ERR_UNSUPPORTED for an image of an fp32 cache.
+ */
+nx_status nexus_append_image(nx_cache* cache, const nx_tokens* tokens, const nx_append* args,
+                             const nx_image* image, int32_t* dev_status, nx_stream_t stream);
 
 /*
  * Brings the image up to date in every slice: blocks rows_in / b .. lens / b - 1 are taken

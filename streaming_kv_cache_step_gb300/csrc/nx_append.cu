@@ -37,6 +37,7 @@ struct AppendArgs {
   nx_append a;
   int32_t* dev_status;
   int32_t* lens;        // the layer's part of c.lens
+  int32_t* held;        // the layer's part of an image's rows, or null
   int tiles, parts;     // thread blocks per sequence: token tiles x parts of the head rows
   int most;             // tokens of a block, at most
   bool set_lens;        // the kernel sets the new lengths itself
@@ -205,6 +206,12 @@ __global__ void __launch_bounds__(kMaxThreads) append_kernel(AppendArgs g) {
           len = -1;
           if (lead) atomicOr(g.dev_status, flag);
         }
+        // rows that an image holds of what the new ones take the place of
+        if (lead && g.held && len >= 0) {
+          int32_t* held = g.held + (long long)s * H + h;
+          const int whole = len - len % image_block(c);
+          if (*held > whole) *held = whole;
+        }
         s_len[h] = len;
       }
       for (int t = tid / 32; t < nt; t += blockDim.x / 32)
@@ -372,11 +379,19 @@ cudaError_t launch_append(AppendArgs& g, cudaStream_t st, int* launches) {
 
 extern "C" nx_status nexus_append(nx_cache* cache, const nx_tokens* tokens, const nx_append* args,
                                   int32_t* dev_status, nx_stream_t stream) {
+  return nexus_append_image(cache, tokens, args, nullptr, dev_status, stream);
+}
+
+extern "C" nx_status nexus_append_image(nx_cache* cache, const nx_tokens* tokens,
+                                        const nx_append* args, const nx_image* image,
+                                        int32_t* dev_status, nx_stream_t stream) {
   using namespace nx;
   int launches = 0;
   begin_call();
   if (!valid_cache(cache) || !valid_tokens(*cache, tokens) || !args || !dev_status)
     return NX_ERR_INVALID_ARG;
+  if (image && !valid_image(image)) return NX_ERR_INVALID_ARG;
+  if (image && cache->dtype != NX_DTYPE_BF16) return NX_ERR_UNSUPPORTED;
   const nx_cache& c = *cache;
   const nx_append& a = *args;
   const int size = c.dtype == NX_DTYPE_BF16 ? 2 : 4;
@@ -410,6 +425,7 @@ extern "C" nx_status nexus_append(nx_cache* cache, const nx_tokens* tokens, cons
   g.dev_status = dev_status;
   const long long per_layer = (long long)c.seqs * c.kv_heads;
   g.lens = c.lens + tokens->layer * per_layer;
+  if (image) g.held = image->rows + tokens->layer * per_layer;
   if (a.lens_in && a.lens_in != g.lens && a.lens_in < g.lens + per_layer &&
       g.lens < a.lens_in + per_layer)
     return NX_ERR_INVALID_ARG;

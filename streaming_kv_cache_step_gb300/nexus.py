@@ -33,7 +33,7 @@ SYMBOLS = ("nexus_workspace_bytes", "nexus_direct_scores", "nexus_walk",
            "nexus_profile_next_call", "nexus_debug_force_simt", "nexus_debug_set_trace",
            "nexus_debug_scorer_config", "nexus_debug_scorer_layout", "kv_compact_noalloc",
            "nexus_last_scorer", "nexus_debug_compact_kernel", "nexus_append",
-           "nexus_quantize", "nexus_attend_workspace_bytes", "nexus_attend")
+           "nexus_append_image", "nexus_quantize", "nexus_attend_workspace_bytes", "nexus_attend")
 SCORER_NONE, SCORER_TENSOR_CORE, SCORER_CUDA_CORE, SCORER_TENSOR_CORE_TWO_PASS = 0, 1, 2, 3
 
 
@@ -134,9 +134,11 @@ def load(path: str = LIB_PATH):
             lib.nexus_debug_scorer_config.argtypes = [ctypes.c_void_p]
             lib.nexus_debug_scorer_config.restype = None
             lib.nexus_append.argtypes = [P, P, P, P, P]
+            lib.nexus_append_image.argtypes = [P, P, P, P, P, P]
             lib.nexus_quantize.argtypes = [P, P, P, P, P]
             lib.nexus_attend.argtypes = [P, P, P, P, P, ctypes.c_size_t, P, P]
-            for name in ("nexus_append", "nexus_quantize", "nexus_attend"):
+            for name in ("nexus_append", "nexus_append_image", "nexus_quantize",
+                         "nexus_attend"):
                 getattr(lib, name).restype = ctypes.c_int
             lib.nexus_attend_workspace_bytes.argtypes = [P, P]
             lib.nexus_attend_workspace_bytes.restype = ctypes.c_size_t
@@ -463,12 +465,14 @@ def _heads(t, tokens: int, heads: int, cache: Cache, name: str):
 
 def append(cache: Cache, layer: int, q, k, v, token_pos, q_out, dev_status, *, max_tokens: int,
            cu_tokens=None, lens_in=None, rotary: Rotary | None = None, q_norm=None, k_norm=None,
-           eps: float = 1e-6, stream=None):
+           eps: float = 1e-6, image: Image | None = None, stream=None):
     """nexus_append: norms and rotates q and k, appends k, v and token_pos to the slices of
     `layer`, writes the queries to q_out. q [tokens, kv_heads * group, d] (or None, with
     q_out), k, v [tokens, kv_heads, d]: views of one packed projection will do. max_tokens:
     no sequence owns more tokens; cu_tokens int32 [seqs + 1], or None where each owns
-    max_tokens. lens_in int32 [seqs, kv_heads]: rows to append behind, if not cache.lens."""
+    max_tokens. lens_in int32 [seqs, kv_heads]: rows to append behind, if not cache.lens (tokens
+    behind it are taken back). image: an image of the cache forgets the blocks that held such
+    tokens; without it the caller lowers image.rows, or attend reads their codes."""
     n, H = token_pos.numel(), cache.kv_heads
     HQ = H * cache.group
     _int32(token_pos, n, "token_pos")
@@ -493,9 +497,10 @@ def append(cache: Cache, layer: int, q, k, v, token_pos, q_out, dev_status, *, m
                     w.numel() != cache.head_dim:
                 raise ValueError(f"{name} must be head_dim values in the cache's type")
             setattr(a, name, w.data_ptr())
-    _check(load().nexus_append(ctypes.byref(cache.c_struct()),
-                               ctypes.byref(_tokens(cache, layer, n, max_tokens, cu_tokens)),
-                               ctypes.byref(a), _ptr(dev_status), _stream(stream)),
+    im = None if image is None else ctypes.byref(image.c_struct(cache))
+    _check(load().nexus_append_image(ctypes.byref(cache.c_struct()),
+                                     ctypes.byref(_tokens(cache, layer, n, max_tokens, cu_tokens)),
+                                     ctypes.byref(a), im, _ptr(dev_status), _stream(stream)),
            "nexus_append")
 
 

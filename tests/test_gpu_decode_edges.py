@@ -98,3 +98,77 @@ def test_attend_image_large_values_that_are_not_seen_yet(group, tokens, d):
                 at = c.at(0, s, h, T, T - 8)
                 c.v[at] = c.v[at] * 2.0 ** up
         _check_attend(c, [tokens] * 2, image=True, uniform=True)
+
+
+# ---------------------------------------------------------------------------
+# an image of rows that are taken back
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("page", [0, 8, 64])
+@pytest.mark.parametrize("in_place", [False, True], ids=["lens_in", "lens"])
+@pytest.mark.parametrize("tokens", [6, 40])
+def test_append_takes_drafts_back_from_an_image(page, in_place, tokens):
+    # drafts that stood in full blocks of the image are replaced: their codes are read no more, the
+    # blocks before them are, and other layers keep theirs
+    c = Case(seqs=3, kv_heads=2, group=2, layers=2, page=page, capacity=192,
+             lens=[[27, 60], [32, 31], [64, 5]], seed=tokens)
+    cache, st = c.device_cache(), _status()
+    im = nexus.new_image(cache)
+    new = lambda: [torch.randn(3 * tokens, h, 128, generator=c.g).to(DEV, BF) for h in (4, 2, 2)]  # noqa: E731
+    pos = torch.arange(3 * tokens, dtype=torch.int32, device=DEV)
+    base = cache.lens[1].clone()
+    base[0, 0] += 2                                                  # two drafts are good
+    q, k, v = new()
+    out = torch.empty_like(q)
+    nexus.append(cache, 1, q, k, v, pos, out, st, max_tokens=tokens)
+    nexus.quantize(cache, im, st)
+    held = im.rows.clone()
+    if in_place:
+        cache.lens[1] = base
+    q, k, v = new()
+    nexus.append(cache, 1, q, k, v, pos, q, st, max_tokens=tokens, image=im,
+                 lens_in=None if in_place else base)
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0 and torch.equal(cache.lens[1], base + tokens)
+    want = held.clone()
+    want[1] = torch.minimum(held[1], base // c.b * c.b)
+    assert torch.equal(im.rows, want) and not torch.equal(want, held)
+    # a new image that holds the same rows gives the same bits
+    fresh = nexus.new_image(cache)
+    nexus.quantize(cache, fresh, st)
+    fresh.rows.copy_(im.rows)
+    outs = []
+    ws = nexus.alloc_attend_workspace(cache, tokens=3 * tokens, max_tokens=tokens)
+    for x in (im, fresh):
+        outs.append(torch.full_like(q, math.nan))
+        nexus.attend(cache, 1, q, outs[-1], ws, st, max_tokens=tokens, image=x)
+    # and brought up to date it is the one that was made from nothing
+    nexus.quantize(cache, im, st)
+    nexus.quantize(cache, fresh, st)
+    for x in (im, fresh):
+        outs.append(torch.full_like(q, math.nan))
+        nexus.attend(cache, 1, q, outs[-1], ws, st, max_tokens=tokens, image=x)
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0 and torch.equal(im.rows, cache.lens // c.b * c.b)
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[2], outs[3])
+
+
+def test_append_leaves_the_image_of_a_slice_that_takes_nothing():
+    # no room, a bad length, bad token ranges: the slice stays, and so does what the image holds
+    c = Case(seqs=2, kv_heads=2, group=1, page=8, capacity=64, lens=[[40, 64], [40, 40]], seed=1)
+    cache, st = c.device_cache(), _status()
+    im = nexus.new_image(cache)
+    nexus.quantize(cache, im, st)
+    x = torch.ones(6, 2, 128, dtype=BF, device=DEV)
+    pos = torch.zeros(6, dtype=torch.int32, device=DEV)
+    before = torch.tensor([[[20, 62], [-1, 20]]], dtype=torch.int32, device=DEV)
+    nexus.append(cache, 0, None, x, x, pos, None, st, max_tokens=3, lens_in=before[0], image=im)
+    torch.cuda.synchronize()
+    assert int(st.item()) == nexus.NX_DEV_FULL | nexus.NX_DEV_BAD_LEN
+    assert im.rows[0].tolist() == [[16, 64], [40, 16]]
+    st.zero_()
+    nexus.append(cache, 0, None, x, x, pos, None, st, max_tokens=3, lens_in=before[0] * 0, image=im,
+                 cu_tokens=torch.tensor([0, 6, 6], dtype=torch.int32, device=DEV))
+    torch.cuda.synchronize()
+    assert int(st.item()) == nexus.NX_DEV_BAD_TOKENS
+    assert im.rows[0].tolist() == [[16, 64], [0, 0]]
