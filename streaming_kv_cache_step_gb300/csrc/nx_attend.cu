@@ -40,9 +40,9 @@ enum Kind { kBf16 = 0, kImage = 1, kF32 = 2, kTail = 3 };
 template <int KIND>
 constexpr bool kIsBf16 = KIND == kBf16 || KIND == kTail;
 
-// Probabilities are kept at 2^kUp times their size, and m is only raised when a logit is more
-// than 2^kSlack above it, so they are at most 2^(kUp + kSlack) = 32768: below fp16's largest
-// value, with 2^-36 of the largest one still representable. From the image a probability is
+// m is only raised when a logit is more than 2^kSlack above it, so probabilities are at most 16. From
+// the image they are kept at 2^kUp times their size while its rows last, at most 32768: below fp16's
+// largest value, with 2^-36 of the largest one still representable. A probability is then
 // multiplied by its values' scale, in units of the largest scale so far, before it becomes fp16: that
 // leaves 2^-28 of the largest while scales stay within kApart of one another. From the first step
 // with a run below that on, a warp's steps go to pv_apart, whose operands never hold a scale (behind a
@@ -719,7 +719,7 @@ __device__ __forceinline__ void attend_part(const AttendArgs& g, const AttendUni
     }
 #pragma unroll
     for (int e = 0; e < ROWS / 8; ++e) {
-      const float sub = (st.m[e] == -INFINITY ? 0.f : st.m[e]) - kUp;
+      const float sub = (st.m[e] == -INFINITY ? 0.f : st.m[e]) - (KIND == kImage ? kUp : 0.f);
 #pragma unroll
       for (int j = 0; j < S::NT; ++j)
 #pragma unroll
@@ -742,10 +742,13 @@ __device__ __forceinline__ void attend_part(const AttendArgs& g, const AttendUni
         st = copy;
         return;
       }
+    constexpr float down = 1.f / (1 << (int)kUp);
+#pragma unroll
+    for (int e = 0; e < ROWS / 8; ++e) st.l[e] *= down;
 #pragma unroll
     for (int n = 0; n < D / 8; ++n)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) st.o[n][e] *= vref;
+      for (int e = 0; e < 4; ++e) st.o[n][e] *= vref * down;
   }
 }
 
@@ -788,7 +791,7 @@ __device__ __forceinline__ void finish_row(const AttendArgs& g, const AttendUnit
     const int row = u.r0 + r;
     g.a.lse[(long long)(u.first + row / g.c.group) * (g.c.kv_heads * g.c.group) +
             u.h * g.c.group + row % g.c.group] =
-        l == 0.f ? -INFINITY : (m - kUp + log2f(l)) * 0.69314718055994531f;
+        l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
   }
 }
 

@@ -172,3 +172,14 @@ def test_append_leaves_the_image_of_a_slice_that_takes_nothing():
     torch.cuda.synchronize()
     assert int(st.item()) == nexus.NX_DEV_BAD_TOKENS
     assert im.rows[0].tolist() == [[16, 64], [0, 0]]
+
+
+@pytest.mark.parametrize("kind", ["bf16", "bf16_64", "image", "image_64", "f32", "f32_64"])
+@pytest.mark.parametrize("tokens", [1, 5, 12])
+@pytest.mark.parametrize("size", [1e36, 1e-30])
+def test_attend_values_near_the_end_of_the_range(kind, tokens, size):
+    # finite values whose weighted sums are finite come out finite: 100 rows of 10^36
+    c = Case(seqs=2, kv_heads=2, group=4, d=64 if kind.endswith("_64") else 128,
+             dtype=F32 if kind.startswith("f32") else BF, capacity=104, lens=[[104, 96], [33, 70]], seed=3)
+    c.v *= size
+    _check_attend(c, [tokens] * 2, image=kind.startswith("image"), uniform=True)
