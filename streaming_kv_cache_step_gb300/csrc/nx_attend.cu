@@ -850,7 +850,7 @@ __global__ void __launch_bounds__(kWarps * 32, Ring<KIND, D, ROWS>::kPerSm)
     if (tid == 0 && !g.splits) g.ws.desc[b] = make_int2(-1, 0);
     if (sh.start >= sh.total) return;
     per = sh.per;
-    stop = min(sh.total, sh.start + per);
+    stop = sh.stop;
     unit = sh.unit;
     at = sh.at;
     pos = sh.start;

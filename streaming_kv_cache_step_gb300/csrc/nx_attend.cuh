@@ -80,11 +80,18 @@ __device__ __forceinline__ AttendUnit attend_unit(const AttendArgs& g, int id) {
   return u;
 }
 
-// A thread block's share of all tiles: `per` of `total` from `start` on, which lies in unit
-// `unit`, whose first tile has number `at`.
+// A thread block's share of all tiles (up to 2^31 - 1): `per` of `total` from `start` to `stop`,
+// the first of them in unit `unit`, whose first tile has number `at`.
 struct AttendShare {
-  int per, total, start, unit, at;
+  int per, total, start, stop, unit, at;
 };
+__host__ __device__ constexpr int share_per(int total, int blocks) {
+  return total < 1 ? 1 : (int)((total + (long long)blocks - 1) / blocks);
+}
+// Where block b's share begins; it ends where the next one's does.
+__host__ __device__ constexpr int share_start(int total, int per, int b) {
+  return (long long)per * b < total ? per * b : total;
+}
 
 // Every one of THREADS threads adds up a run of units; tiles(i): tiles of unit i. unit and at
 // are undefined if start >= total.
@@ -112,13 +119,13 @@ __device__ __forceinline__ AttendShare attend_share(const AttendArgs& g, const T
   }
   AttendShare x;
   x.total = total;
-  x.per = max(1, (total + (int)gridDim.x - 1) / (int)gridDim.x);
-  const long long start = (long long)blockIdx.x * x.per;
-  if (start >= before && start < (long long)before + sum) {
+  x.per = share_per(total, gridDim.x);
+  const int start = share_start(total, x.per, blockIdx.x);
+  if (start >= before && start - before < sum) {
     int at = before;
     for (int i = u0; i < u1; ++i) {
       const int n = tiles(i);
-      if (start < at + n) {
+      if (start - at < n) {
         s_at[0] = i;
         s_at[1] = at;
         break;
@@ -127,7 +134,8 @@ __device__ __forceinline__ AttendShare attend_share(const AttendArgs& g, const T
     }
   }
   __syncthreads();
-  x.start = (int)min(start, (long long)total);
+  x.start = start;
+  x.stop = share_start(total, x.per, blockIdx.x + 1);
   x.unit = s_at[0];
   x.at = s_at[1];
   return x;

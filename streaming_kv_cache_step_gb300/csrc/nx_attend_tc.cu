@@ -355,7 +355,7 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
   grid_dep_trigger();
   const uint32_t tmem = s_tmem;
   int unit = sh.unit, at = sh.at, pos = sh.start;
-  const int stop = min(sh.total, sh.start + sh.per);
+  const int stop = sh.stop;
   int2 desc = make_int2(-1, 0);
   int slot_no = 0;                     // ring slots filled or used so far (loader, issuer)
   int raw_no = 0;                      // raw stages filled so far

@@ -1,7 +1,10 @@
 """Host-side tests (no GPU) of what nexus_append, nexus_quantize and nexus_attend refuse and ask
 for, beside those of test_decode_host.py."""
 import ctypes
+import os
+import subprocess
 
+from streaming_kv_cache_step_gb300 import build
 from test_abi_host import _structs
 from test_decode_host import STATUS, _image, _tok, lib  # noqa: F401
 
@@ -25,3 +28,19 @@ def test_append_image_refuses(lib):  # noqa: F811
         assert call(**bad) == nexus.NX_ERR_INVALID_ARG, bad
     f32 = dict(dtype=nexus.DTYPE_F32)
     assert call(cache=f32, image=_image()) == nexus.NX_ERR_UNSUPPORTED
+
+
+def test_shares_of_many_tiles(tmp_path):
+    # the blocks' shares follow one another without a gap up to the largest total that attend takes
+    csrc = os.path.join(os.path.dirname(build.__file__), "csrc")
+    src = tmp_path / "shares.cu"
+    src.write_text('#include "nx_attend.cuh"\n' + "".join(
+        f"""static_assert(nx::share_start({total}, nx::share_per({total}, {blocks}), 0) == 0, "");
+static_assert(nx::share_start({total}, nx::share_per({total}, {blocks}), {blocks}) == {total}, "");
+static_assert(nx::share_start({total}, nx::share_per({total}, {blocks}), {blocks} - 1) <= {total}, "");
+static_assert(nx::share_per({total}, {blocks}) >= 1 &&
+              nx::share_per({total}, {blocks}) <= {total // blocks + 1}LL, "");
+""" for total in (0, 1, 455, 456, 457, 65536, 2 ** 31 - 400, 2 ** 31 - 1) for blocks in (1, 152, 304, 456)))
+    p = subprocess.run([build._nvcc(), *build.ARCH, *build.FLAGS, "-I", csrc, "-c", str(src), "-o",
+                        str(tmp_path / "shares.o")], capture_output=True, text=True)
+    assert p.returncode == 0, p.stderr
