@@ -370,7 +370,8 @@ typedef struct nx_attend {
 } nx_attend;
 
 /* Bytes of workspace nexus_attend needs for these arguments, with an image or without (0 on
-   invalid arguments); it goes by head_dim and by max_tokens * group. */
+   invalid arguments). They go by dtype, head_dim and min(max_tokens, tokens) * group alone, so that
+   one buffer serves caches of any number of slices and any capacity. */
 size_t nexus_attend_workspace_bytes(const nx_cache* cache, const nx_tokens* tokens);
 
 /*

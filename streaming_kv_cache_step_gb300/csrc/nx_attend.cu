@@ -1129,9 +1129,9 @@ cudaError_t launch_attend(AttendArgs& g, cudaStream_t st, int* launches) {
 extern "C" size_t nexus_attend_workspace_bytes(const nx_cache* cache, const nx_tokens* tokens) {
   using namespace nx;
   if (!valid_cache(cache) || !valid_tokens(*cache, tokens)) return 0;
-  AttendWs ws;                            // with an image or without
+  AttendWs ws;                            // of any cache of this type, with an image or without
   const size_t rows = attend_layout(cache->head_dim, nullptr, &ws);
-  const size_t tc = attend_tc_takes(*cache, *tokens, false)
+  const size_t tc = attend_tc_may_take(*cache, *tokens)
                         ? attend_tc_layout(cache->head_dim, nullptr, &ws)
                         : 0;
   return rows > tc ? rows : tc;

@@ -211,8 +211,10 @@ inline long long most_tokens(const nx_tokens& t) {
 }
 
 // nx_attend_tc.cu: the tensor-core kernel for many query rows per slice (bf16 caches), its
-// workspace (base may be null; returns the bytes), and whether it takes a call.
+// workspace (base may be null; returns the bytes), and whether it takes a call, or may take one of
+// another capacity or from an image.
 bool attend_tc_takes(const nx_cache& c, const nx_tokens& t, bool image);
+bool attend_tc_may_take(const nx_cache& c, const nx_tokens& t);
 size_t attend_tc_layout(int D, char* base, AttendWs* ws);
 cudaError_t launch_attend_tc(AttendArgs& g, cudaStream_t st, int* launches);
 

@@ -46,6 +46,7 @@ constexpr int kTcRows = 256;               // rows of a piece, at most
 constexpr int kTcGrid = kSms;
 constexpr int kPolls = 1 << 20;               // mbarrier polls before giving up
 constexpr float kRaise = 8.f;              // log2 units
+constexpr int kFewRows = 16;               // query rows that never come here
 
 __device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count));
@@ -910,8 +911,12 @@ cudaError_t launch_t(AttendArgs& g, cudaStream_t st, int* launches) {
 // slices of 32768 rows 62 / 45; 36 rows 45 / 53 and 62 / 58.
 bool attend_tc_takes(const nx_cache& c, const nx_tokens& t, bool image) {
   const long long bytes = (long long)c.seqs * c.kv_heads * c.capacity * c.head_dim * 4;
-  const int rows = image ? 80 : bytes <= (128LL << 20) ? 32 : 16;
+  const int rows = image ? 80 : bytes <= (128LL << 20) ? 32 : kFewRows;
   return c.dtype == NX_DTYPE_BF16 && most_tokens(t) * c.group > rows;
+}
+
+bool attend_tc_may_take(const nx_cache& c, const nx_tokens& t) {
+  return c.dtype == NX_DTYPE_BF16 && most_tokens(t) * c.group > kFewRows;
 }
 
 size_t attend_tc_layout(int D, char* base, AttendWs* ws) {

@@ -4,6 +4,8 @@ import ctypes
 import os
 import subprocess
 
+import pytest
+
 from streaming_kv_cache_step_gb300 import build
 from test_abi_host import _structs
 from test_decode_host import STATUS, _image, _tok, lib  # noqa: F401
@@ -44,3 +46,18 @@ static_assert(nx::share_per({total}, {blocks}) >= 1 &&
     p = subprocess.run([build._nvcc(), *build.ARCH, *build.FLAGS, "-I", csrc, "-c", str(src), "-o",
                         str(tmp_path / "shares.o")], capture_output=True, text=True)
     assert p.returncode == 0, p.stderr
+
+
+@pytest.mark.parametrize("head_dim", [64, 128])
+@pytest.mark.parametrize("rows", [1, 16, 17, 32, 33, 80, 81, 4096])
+def test_attend_workspace_goes_by_the_rows_alone(lib, rows, head_dim):  # noqa: F811
+    def size(tokens, max_tokens, **cache):
+        c, _ = _structs(group=1, head_dim=head_dim, **cache)
+        t = _tok(tokens=tokens, max_tokens=max_tokens, cu_tokens=0x8000)
+        return lib.nexus_attend_workspace_bytes(ctypes.byref(c), ctypes.byref(t))
+
+    one = size(rows, rows, seqs=1, kv_heads=1, capacity=64)
+    for cache in (dict(seqs=1, kv_heads=1, capacity=1 << 22), dict(seqs=256, kv_heads=8, capacity=512),
+                  dict(seqs=64, kv_heads=8, capacity=1 << 17)):
+        assert size(rows, rows, **cache) == one and size(rows, 1 << 30, **cache) == one
+        assert size(1 << 20, rows, **cache) == one
