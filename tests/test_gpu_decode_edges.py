@@ -183,3 +183,79 @@ def test_attend_values_near_the_end_of_the_range(kind, tokens, size):
              dtype=F32 if kind.startswith("f32") else BF, capacity=104, lens=[[104, 96], [33, 70]], seed=3)
     c.v *= size
     _check_attend(c, [tokens] * 2, image=kind.startswith("image"), uniform=True)
+
+
+# ---------------------------------------------------------------------------
+# pages out of range, held to the tolerances of whole slices
+# ---------------------------------------------------------------------------
+
+def _check_bad_pages(c, n, bad, image, held=None, causal=True):
+    """Pages bad[s] (indexes into the sequence's table) of sequence s are out of range: their slots
+    count for nothing, in the output and in lse."""
+    HG, N = c.H * c.G, int(sum(n))
+    q = torch.randn(N, HG, c.d, generator=c.g).to(c.dtype)
+    cache, st = c.device_cache(), _status()
+    im = None
+    if image:
+        im = _image(c, cache)
+        nexus.quantize(cache, im, st)
+        if held is not None:
+            im.rows.copy_(torch.as_tensor(held))
+    for s, pages in enumerate(bad):
+        for i, p in enumerate(pages):
+            cache.block_table[s, p] = (-1, c.pages, 1 << 30)[i % 3]
+    out = torch.full((N, HG, c.d), math.nan, dtype=c.dtype, device=DEV)
+    lse = torch.full((N, HG), math.nan, device=DEV)
+    ws = nexus.alloc_attend_workspace(cache, tokens=N, max_tokens=max(n))
+    ws.fill_(0xFF)
+    nexus.attend(cache, 0, q.to(DEV), out, ws, st, max_tokens=max(n), cu_tokens=c.cu(n).to(DEV),
+                 causal=causal, lse=lse, image=im)
+    torch.cuda.synchronize()
+    assert int(st.item()) == nexus.NX_DEV_BAD_PAGE
+    sc, a = c.d ** -0.5, 0
+    deq = None if im is None else [x.cpu().float() for x in (im.k, im.v, im.k_scale, im.v_scale)]
+    for s, m in enumerate(n):
+        for h in range(c.H):
+            T = int(c.lens[0, s, h])
+            at = c.at(0, s, h, T)
+            k, v = c.k[at].double(), c.v[at].double()
+            if image:
+                r = int(im.rows[0, s, h])
+                for t, codes, scales in ((k, deq[0], deq[2]), (v, deq[1], deq[3])):
+                    per = [float(scales[_scale_at(c, 0, s, h, j)]) for j in range(0, r, c.b)]
+                    t[:r] = codes[c.at(0, s, h, r)].double() * \
+                        torch.tensor(per, dtype=torch.float64).repeat_interleave(c.b)[:, None]
+            good = ~torch.isin(torch.arange(T) // c.page, torch.tensor(bad[s], dtype=torch.long))
+            M = [int(good[:max(0, T - (m - 1 - i if causal else 0))].sum())
+                 for i in range(m) for _ in range(c.G)]
+            rows = q[a:a + m, h * c.G:(h + 1) * c.G].reshape(m * c.G, c.d)
+            ro, rl, A, big = attend64(rows, k[good], v[good], M, sc)
+            got = out[a:a + m, h * c.G:(h + 1) * c.G].reshape(m * c.G, c.d).cpu().double()
+            gl = lse[a:a + m, h * c.G:(h + 1) * c.G].reshape(-1).cpu().double()
+            dx = sc * big * (2.0 ** -24 * (c.d + 8) if c.dtype == BF else 2.0 ** -20)
+            p = 2.0 ** -8 if c.dtype == BF else 2.0 ** -19
+            if image and int(im.rows[0, s, h]) == T:
+                p = 2.0 ** -11 + 2.0 ** -19
+            half = 2.0 ** -8 if c.dtype == BF else 2.0 ** -24
+            tol = half * ro.abs() + (p + 2 * dx)[:, None] * A + 1e-30
+            assert torch.all((got - ro).abs() <= tol), (s, h)
+            some = torch.tensor([x > 0 for x in M], dtype=torch.bool)
+            assert torch.all(gl[~some] == -math.inf) and torch.all(got[~some] == 0)
+            assert torch.all((gl - rl).abs()[some] <= (dx + 2.0 ** -19 * (1 + rl.abs()))[some]), (s, h)
+        a += m
+
+
+@pytest.mark.parametrize("kind", ["bf16", "image", "f32"])
+@pytest.mark.parametrize("page", [8, 16, 32, 128])
+@pytest.mark.parametrize("group,tokens", [(4, 1), (4, 4), (4, 10), (8, 12), (4, 60)])
+def test_attend_leaves_bad_pages_out(kind, page, group, tokens):
+    # 4 to 240 query rows per slice; a bad page in the middle, two in a row at an odd place, the first
+    # and the last ones, and every page of a sequence
+    per = 512 // page
+    c = Case(seqs=5, kv_heads=2, group=group, dtype=F32 if kind == "f32" else BF, page=page, capacity=512,
+             lens=[[512, 480], [300, 511], [256, 129], [512, 77], [130, 64]], seed=page + tokens)
+    bad = [[per // 2], [1, 2], [0, 256 // page - 1], [per - 1], list(range(per))]
+    _check_bad_pages(c, [tokens, 1, tokens, tokens, tokens], bad, kind == "image")
+    if kind == "image":            # some of them among the rows behind the image
+        held = [[[256, 480 // c.b * c.b], [32, 0], [128, 128], [480, 64], [0, 64]]]
+        _check_bad_pages(c, [tokens, 1, tokens, tokens, tokens], bad, True, held=held, causal=False)
