@@ -22,8 +22,8 @@
 // Where the tensor cores have time to spare (one row tile: K and V from HBM bound the kernel)
 // and for 8-bit rows, whose values need no rounding, p is kept as two bf16 terms, p = hi + lo,
 // with one product each; else as one (half a step of bf16, 2^-8, in each p).
-// Every wait is bounded; when one gives up, the block flags NX_DEV_TIMEOUT, waits for nothing
-// more, issues nothing more and ends, its TMEM freed.
+// Every wait is bounded; when one gives up, the block flags NX_DEV_TIMEOUT, starts no more copies,
+// waits (bounded too) for the copies and products that are under way and ends, its TMEM freed.
 //
 // Measured: two chunks of 512 tokens, 8 x 4 heads, over 8704 rows: 134 us on the GPU, 1.09 PFLOP/s,
 // 59 % of a plain bf16 product's rate; a step of a stream (64 slots) takes about 2000 clocks, of
@@ -96,6 +96,10 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile
   *gave_up = 1;
   atomicOr(dev_status, NX_DEV_TIMEOUT);
   return false;
+}
+// The same for what is under way when the block has given up: some milliseconds at most.
+__device__ __forceinline__ void bar_drain(uint32_t bar, uint32_t parity) {
+  for (int i = 0; i < kPolls / 16 && !bar_test(bar, parity); ++i) {}
 }
 // Orders this thread's accesses to shared memory before those of TMA, bulk copies and tcgen05 that
 // a barrier lets go after it.
@@ -212,7 +216,7 @@ struct Plan {
   static constexpr int kRawBytes = kCols * D;                 // codes of a K or V tile
   static constexpr int kSlots = IMAGE ? 8 : NQ == 2 ? 10 : 12;
   static constexpr int kRaw = IMAGE ? (NQ == 2 ? 4 : 8) : 0;
-  static constexpr int kBars = 2 * kSlots + 1 + 3 * 4 + 2 * kRaw;
+  static constexpr int kBars = 2 * kSlots + 1 + 3 * 4 + 2 * kRaw + 1;
   static constexpr int kSmem = 1024 + NQ * kQBytes + kSlots * kSlotBytes + kRaw * kRawBytes;
 };
 
@@ -239,12 +243,13 @@ __device__ __forceinline__ void copy_group(const char* src, long long row, int t
 }
 
 // The codes of a tile's rows below `some`, times the scales of their runs of 8, as bf16 in a ring
-// slot, with zeros behind them up to the next run. Thread `tid` of N takes every N-th 8 codes.
-template <int D, int N>
+// slot, with zeros behind them up to the next run. Thread `tid` of N takes every N-th 8 codes. WHOLE:
+// all rows, so that every load is on its way before the first one is used.
+template <int D, int N, bool WHOLE>
 __device__ __forceinline__ void expand_tile(uint32_t raw, const float* scale, int some,
                                             uint32_t slot, int tid) {
   constexpr int kChunks = D / 8, kAll = kCols * kChunks, kEach = (kAll + N - 1) / N;
-  const int rows = min(kCols, (some + 7) / 8 * 8);
+  const int rows = WHOLE ? kCols : min(kCols, (some + 7) / 8 * 8);
   uint32_t x[kEach][2];
   float f[kEach];
 #pragma unroll
@@ -252,7 +257,7 @@ __device__ __forceinline__ void expand_tile(uint32_t raw, const float* scale, in
     const int c = tid + i * N, r = c / kChunks;
     x[i][0] = x[i][1] = 0;
     f[i] = 0.f;
-    if (r < some && (kAll % N == 0 || c < kAll)) {
+    if ((WHOLE || r < some) && ((i + 1) * N <= kAll || c < kAll)) {
       asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];"
                    : "=r"(x[i][0]), "=r"(x[i][1])
                    : "r"(raw + c * 8)
@@ -273,7 +278,7 @@ __device__ __forceinline__ void expand_tile(uint32_t raw, const float* scale, in
       y[2 * j] = bf16_pair(v0.x * f[i], v0.y * f[i]);
       y[2 * j + 1] = bf16_pair(v1.x * f[i], v1.y * f[i]);
     }
-    if (r < rows && (kAll % N == 0 || c < kAll))
+    if ((WHOLE || r < rows) && ((i + 1) * N <= kAll || c < kAll))
       asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(
                        slot + chunk / 8 * (kCols * 128) + r * 128 + ((chunk ^ r) & 7) * 16),
                    "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3])
@@ -324,6 +329,7 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
   // per stream and TMEM buffer: logits there, probabilities there, their product done
   const uint32_t sfull = qfull + 8, pfull = sfull + 32, odone = pfull + 32;
   const uint32_t rfull = odone + 32, rempty = rfull + 8 * P::kRaw;    // of the raw ring
+  const uint32_t drained = rempty + 8 * P::kRaw;    // products done, after giving up
   if (warp == kIssueWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_at(&s_tmem)),
@@ -345,6 +351,7 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
       bar_init(pfull + 8 * i, kRows);
       bar_init(odone + 8 * i, 1);
     }
+    bar_init(drained, 2);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     s_up = 0;
   }
@@ -360,6 +367,7 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
   int2 desc = make_int2(-1, 0);
   int slot_no = 0;                     // ring slots filled or used so far (loader, issuer)
   int raw_no = 0;                      // raw stages filled so far
+  int sent = 0;                        // behind the last ring slot or raw stage with copies under way
   int segment = 0;                     // pieces done
   int used[2] = {0, 0};                // slot tiles done by each stream
   volatile int* up = &s_up;
@@ -378,7 +386,7 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
         // K and V tiles in turn, every warp its runs of 8 slots
         const auto announce = [&](int k) {
           fence_async();
-          bar_arrive(full + 8 * (k % P::kSlots));
+          if (IMAGE || *up == 0) bar_arrive(full + 8 * (k % P::kSlots));
         };
         // whether any page of the piece is bad; then every K tile gets its marks
         bool any_bad = false;
@@ -438,7 +446,8 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
                         i & 1 ? &map_v : &map_k, 64 * blk, y, full + 8 * sl);
               }
               if (lane > 0) bar_arrive(full + 8 * sl);
-            } else {
+              sent = k + 1;
+            } else if (*up == 0) {
               bar_arrive(full + 8 * sl);
             }
           }
@@ -490,8 +499,8 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
                 page1 = page_of(i + 3);
               }
               const float scale1 = scale_of(i + 1, row1);
-              const bool go =
-                  bar_wait(rempty + 8 * st, (no / P::kRaw & 1) ^ 1, up, g.dev_status);
+              bar_wait(rempty + 8 * st, (no / P::kRaw & 1) ^ 1, up, g.dev_status);
+              const bool go = *up == 0;
               if (lane < kGroups) s_scale[st][lane] = scale;
               // a run on a bad page: zeros for what the stage held before; the stage's next bulk
               // copy, of the other proxy, comes behind them
@@ -510,8 +519,11 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
               const bool lead = go && row >= 0 && 8 * lane % box == 0;
               const int bytes = lead ? (min(held, t + box) - t) * D : 0;
               const unsigned total = __reduce_add_sync(0xffffffffu, (unsigned)bytes);
-              if (lane == 0) bar_arrive_tx(rfull + 8 * st, total);
-              else bar_arrive(rfull + 8 * st);
+              if (go) {
+                if (lane == 0) bar_arrive_tx(rfull + 8 * st, total);
+                else bar_arrive(rfull + 8 * st);
+                sent = no + 1;
+              }
               __syncwarp();
               if (lead)
                 bulk_copy(s_codes + st * P::kRawBytes + 8 * lane * D,
@@ -529,9 +541,12 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
               bar_wait(rfull + 8 * st, no / P::kRaw & 1, up, g.dev_status);
               bar_wait(empty + 8 * sl, (k / P::kSlots & 1) ^ 1, up, g.dev_status);
               const uint32_t slot = s_ring + sl * P::kSlotBytes;
-              if (held > t0)
-                expand_tile<D, kLoaders - 32>(s_codes + st * P::kRawBytes, s_scale[st], held - t0,
-                                              slot, lt - 32);
+              if (held >= t0 + kCols)
+                expand_tile<D, kLoaders - 32, true>(s_codes + st * P::kRawBytes, s_scale[st], kCols,
+                                                    slot, lt - 32);
+              else if (held > t0)
+                expand_tile<D, kLoaders - 32, false>(s_codes + st * P::kRawBytes, s_scale[st],
+                                                     held - t0, slot, lt - 32);
               if (t0 + kCols > held) {                          // bf16 rows, or none, behind it
                 __syncwarp();
                 const int q0 = held > t0 ? (held - t0 + 7) / 8 : 0;
@@ -807,11 +822,22 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
   }
   if (tid == 0) g.ws.desc[b] = desc;
   asm volatile("cp.async.wait_all;" ::: "memory");
-  // after giving up, bulk copies may be under way that nobody waited for: a millisecond's grace
-  if (*up)
-    for (int i = 0; i < 1000; ++i) __nanosleep(1000);
   tc_before();
   __syncthreads();
+  if (*up) {
+    // the last boxes of each ring slot, or bulk copies of each raw stage, and all products
+    constexpr int kDepth = IMAGE ? P::kRaw : P::kSlots;
+    const uint32_t bar = IMAGE ? rfull : full;
+    if (warp == kLoadWarp) {
+      for (int k = max(0, sent - kDepth); k < sent; ++k)
+        bar_drain(bar + 8 * (k % kDepth), k / kDepth & 1);
+    } else if (warp >= kIssueWarp) {
+      if (elected()) commit(drained);
+      __syncwarp();
+      bar_drain(drained, 0);
+    }
+    __syncthreads();
+  }
   if (warp == kIssueWarp) {
     tc_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
