@@ -384,12 +384,10 @@ size_t nexus_attend_workspace_bytes(const nx_cache* cache, const nx_tokens* toke
  * the cache. Slices flagged NX_DEV_BAD_LEN or NX_DEV_BAD_IMAGE count as empty; a row on a
  * page out of range (NX_DEV_BAD_PAGE) is left out of the sums; tokens of a sequence flagged
  * NX_DEV_BAD_TOKENS get no output. Rows at or beyond lens never show in a result, whatever they
- * hold. A row below lens that is not finite shows in its own slice only: a logit of minus
- * infinity drops out, an infinite value may come out as NaN, and a value row that is not finite
- * shows also in the outputs of tokens of this call that do not see it yet (their weight is 0,
- * and 0 times an infinity or NaN is NaN). Sums of weights times values are binary32, the weights up
- * to 2^8 each: values whose size times the slice's rows exceeds 2^119 may overflow. Up to 16 query rows per slice (max_tokens * group;
- * 32 where the layer's slices take up to 128 MB, 80 from an image) go to a kernel that streams
+ * hold. A row below lens that is not finite shows in the outputs that see it only: a logit of
+ * minus infinity drops out, an infinite value may come out as NaN. Sums of weights times values are
+ * binary32, the weights up to 2^8 each: values whose size times the slice's rows exceeds 2^119 may
+ * overflow. Up to 16 query rows per slice (max_tokens * group; 32 where the layer's slices take up to 128 MB, 80 from an image) go to a kernel that streams
  * rows through mma.sync, more to one on tcgen05; fp32 caches always to the first. One launch for
  * few or short slices (capacity up to some hundred rows, some thousand for a few dozen slices) on
  * the first, else two; the same bits every time.

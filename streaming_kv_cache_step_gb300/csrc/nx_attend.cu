@@ -528,14 +528,62 @@ __device__ __forceinline__ void pv_apart(uint32_t stage, int lane, const float x
   }
 }
 
+// A step's value rows [from, to) that some query rows see and others do not: what is not finite in
+// them would reach the latter as 0 times an infinity or NaN. Whether there is any:
+template <int KIND, int D>
+__device__ __forceinline__ bool leaks(uint32_t stage, int lane, int from, int to) {
+  using S = Shape<KIND, D>;
+  uint32_t bad = 0;
+#pragma unroll 1
+  for (int i = max(from, 0) * S::kChunks + lane; i < min(to, S::kSlots) * S::kChunks; i += 32) {
+    const uint4 x = lds16(stage + S::kStage / 2 + i * 16);
+    bad |= not_finite<Shape<KIND, D>::kBytes>(x.x) | not_finite<Shape<KIND, D>::kBytes>(x.y) | not_finite<Shape<KIND, D>::kBytes>(x.z) |
+           not_finite<Shape<KIND, D>::kBytes>(x.w);
+  }
+  return __any_sync(0xffffffffu, bad != 0);
+}
+// and it goes to the outputs of the rows that see it here, and out of the step's values.
+template <int KIND, int D, int ROWS>
+__device__ __forceinline__ void take_leaks(uint32_t stage, int lane, int t, int from, int to,
+                                           const int* lim, State<D, ROWS>& st) {
+  using S = Shape<KIND, D>;
+  const uint32_t v = stage + S::kStage / 2;
+#pragma unroll 1
+  for (int r = max(from, 0); r < min(to, S::kSlots); ++r)
+#pragma unroll
+    for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const int f = S::feature(n, 2 * (lane % 4) + y) * S::kBytes, in = f % 4;
+        uint32_t w;
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(v + S::v_at(r, f / 16) + f % 16 - in));
+        if (!(not_finite<Shape<KIND, D>::kBytes>(w) >> 8 * in & 1u)) continue;
+        const float x = KIND == kF32     ? __uint_as_float(w)
+                        : KIND == kImage ? __uint_as_float(0x7FC00000u)
+                        : in             ? __uint_as_float(w & 0xFFFF0000u)
+                                         : __uint_as_float(w << 16);
+#pragma unroll
+        for (int e = 0; e < ROWS / 8; ++e)
+          if (t + r < lim[e]) st.o[n][2 * e + y] += x;
+      }
+  __syncwarp();
+#pragma unroll 1
+  for (int i = max(from, 0) * S::kChunks * 4 + lane; i < min(to, S::kSlots) * S::kChunks * 4; i += 32) {
+    uint32_t w;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(v + i * 4));
+    asm volatile("st.shared.u32 [%0], %1;" ::"r"(v + i * 4), "r"(w & ~not_finite<Shape<KIND, D>::kBytes>(w)) : "memory");
+  }
+  __syncwarp();
+}
+
 // Slots [base + kSlots * i, ...) for i = from, from + kWarps, ... < to, up to slot `end`. vref: the
-// image's largest value scale so far, which o is in units of. Where a run's scale is far below it,
-// the steps from there on are attend_apart's.
-template <int D, int ROWS, int kDeep, int kStageBytes>
-__device__ __noinline__ void attend_apart(const AttendArgs& g, const AttendUnit& u, int base, int end,
-                                          int from, int to, uint32_t ring, Meta* meta,
-                                          State<D, ROWS>& st, float vref);
-template <int KIND, int D, int ROWS, int kDeep, int kStageBytes, bool APART = false>
+// image's largest value scale so far, which o is in units of. Where a run's scale is far below it, or
+// a value that only some rows see is not finite, the steps from there on are attend_slow's (SLOW).
+template <int KIND, int D, int ROWS, int kDeep, int kStageBytes>
+__device__ __noinline__ void attend_slow(const AttendArgs& g, const AttendUnit& u, int base, int end,
+                                         int from, int to, uint32_t ring, Meta* meta,
+                                         State<D, ROWS>& st, float vref);
+template <int KIND, int D, int ROWS, int kDeep, int kStageBytes, bool SLOW = false>
 __device__ __forceinline__ void attend_part(const AttendArgs& g, const AttendUnit& u, int base,
                                             int end, int from, int to, uint32_t ring, Meta* meta,
                                             State<D, ROWS>& st, float vref = 1.1754944e-38f) {
@@ -627,7 +675,7 @@ __device__ __forceinline__ void attend_part(const AttendArgs& g, const AttendUni
     const auto far_below = [&](float v) {
       return __float_as_uint(meta[n].scale[4 + lane % S::NT]) - 1u < __float_as_uint(v * kApart) - 1u;
     };
-    const bool far = KIND == kImage && !APART && far_below(vref);
+    const bool far = KIND == kImage && !SLOW && far_below(vref);
     n = n == kDeep - 1 ? 0 : n + 1;
     float s[S::NT][4];
     qk<KIND, D, ROWS>(q, stage, lane, s);
@@ -653,6 +701,10 @@ __device__ __forceinline__ void attend_part(const AttendArgs& g, const AttendUni
           z *= KIND == kImage ? q.c1[e] * ks[j] : q.c1[e];
         }
     if (mask) {
+      if (low < end) {                  // (one token: no row sees less than another)
+        if constexpr (SLOW) take_leaks<KIND, D, ROWS>(stage, lane, t, low - t, end - t, lim, st);
+        else if (leaks<KIND, D>(stage, lane, low - t, end - t)) break;
+      }
 #pragma unroll
       for (int j = 0; j < S::NT; ++j)
 #pragma unroll
@@ -682,7 +734,7 @@ __device__ __forceinline__ void attend_part(const AttendArgs& g, const AttendUni
       up |= vnew > vref || far;
     }
     if (__any_sync(0xffffffffu, up)) {
-      if constexpr (KIND == kImage && !APART) {
+      if constexpr (KIND == kImage && !SLOW) {
         n = n == 0 ? kDeep - 1 : n - 1;
         const bool leave = __any_sync(0xffffffffu, far_below(vnew));
         n = n == kDeep - 1 ? 0 : n + 1;
@@ -708,7 +760,7 @@ __device__ __forceinline__ void attend_part(const AttendArgs& g, const AttendUni
         st.o[n][3] *= f[ROWS / 8 - 1];
       }
     }
-    if constexpr (APART) {
+    if constexpr (SLOW && KIND == kImage) {
       pv_apart<D, ROWS>(stage, lane, s, meta[n == 0 ? kDeep - 1 : n - 1].scale + 4, vinv, st);
       continue;
     }
@@ -732,16 +784,17 @@ __device__ __forceinline__ void attend_part(const AttendArgs& g, const AttendUni
     }
     pv<KIND, D, ROWS>(stage, lane, s, st);
   }
+  if constexpr (!SLOW)
+    if (i < to) {
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      State<D, ROWS> copy = st;         // in local memory: st and u stay in registers
+      const AttendUnit unit = u;
+      attend_slow<KIND, D, ROWS, kDeep, kStageBytes>(g, unit, base, end, i, to, ring, meta, copy,
+                                                     vref);
+      st = copy;
+      return;
+    }
   if constexpr (KIND == kImage) {
-    if constexpr (!APART)
-      if (i < to) {
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        State<D, ROWS> copy = st;       // in local memory: st and u stay in registers
-        const AttendUnit unit = u;
-        attend_apart<D, ROWS, kDeep, kStageBytes>(g, unit, base, end, i, to, ring, meta, copy, vref);
-        st = copy;
-        return;
-      }
     constexpr float down = 1.f / (1 << (int)kUp);
 #pragma unroll
     for (int e = 0; e < ROWS / 8; ++e) st.l[e] *= down;
@@ -752,15 +805,15 @@ __device__ __forceinline__ void attend_part(const AttendArgs& g, const AttendUni
   }
 }
 
-// The steps of an image from `from` on by pv_apart: a function of its own, so that the others' loop
+// The steps from `from` on with what only some need: a function of its own, so that the others' loop
 // keeps its registers.
-template <int D, int ROWS, int kDeep, int kStageBytes>
-__device__ __noinline__ void attend_apart(const AttendArgs& g, const AttendUnit& u, int base, int end,
-                                          int from, int to, uint32_t ring, Meta* meta,
-                                          State<D, ROWS>& st, float vref) {
+template <int KIND, int D, int ROWS, int kDeep, int kStageBytes>
+__device__ __noinline__ void attend_slow(const AttendArgs& g, const AttendUnit& u, int base, int end,
+                                         int from, int to, uint32_t ring, Meta* meta,
+                                         State<D, ROWS>& st, float vref) {
   State<D, ROWS> mine = st;
-  attend_part<kImage, D, ROWS, kDeep, kStageBytes, true>(g, u, base, end, from, to, ring, meta, mine,
-                                                         vref);
+  attend_part<KIND, D, ROWS, kDeep, kStageBytes, true>(g, u, base, end, from, to, ring, meta, mine,
+                                                       vref);
   st = mine;
 }
 

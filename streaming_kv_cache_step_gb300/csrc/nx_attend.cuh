@@ -195,6 +195,14 @@ __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
   const __nv_bfloat162 r = __floats2bfloat162_rn(a, b);
   return reinterpret_cast<const uint32_t&>(r);
 }
+// Which of a word's values are not finite: all bits of theirs (4-byte values: fp32, 2: bf16, 1: e4m3
+// codes).
+template <int BYTES>
+__device__ __forceinline__ uint32_t not_finite(uint32_t w) {
+  if constexpr (BYTES == 4) return (w & 0x7F800000u) == 0x7F800000u ? 0xFFFFFFFFu : 0u;
+  else if constexpr (BYTES == 2) return __vcmpeq2(w & 0x7F807F80u, 0x7F807F80u);
+  else return __vcmpeq4(w & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+}
 // Four e4m3 codes as two pairs of fp16.
 __device__ __forceinline__ void e4m3_pairs(uint32_t four, uint32_t& lo, uint32_t& hi) {
   asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"

@@ -242,12 +242,70 @@ __device__ __forceinline__ void copy_group(const char* src, long long row, int t
   }
 }
 
+// The value rows of a tile that some query rows see and others do not, slots [low, end): what is not
+// finite in them would reach the latter as 0 times an infinity or NaN. It goes out of the tile, and
+// the slot is marked in `hot`, for take_hot. Of the 8 bf16 rows that copy_group brought to row r:
+__device__ __forceinline__ void mark_hot(uint32_t* hot, int j) {
+  atomicOr(hot + (j >> 5), 1u << (j & 31));
+}
+template <int D>
+__device__ __forceinline__ void clear_group(int t, int low, int end, uint32_t slot, int r, int lane,
+                                            uint32_t* hot) {
+  constexpr int kChunks = D / 8, kLine = 32 / kChunks;
+  const int chunk = lane % kChunks, sub = lane / kChunks;
+#pragma unroll 1
+  for (int i = sub; i < 8; i += kLine) {
+    const uint32_t at = slot + chunk / 8 * (kCols * 128) + (r + i) * 128 + ((chunk ^ i) & 7) * 16;
+    uint32_t x[4];
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                 : "r"(at)
+                 : "memory");
+    uint32_t bad = 0;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const uint32_t y = not_finite<2>(x[w]);
+      x[w] &= ~y;
+      bad |= y;
+    }
+    if (bad && t + i >= low && t + i < end) {
+      asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(x[0]), "r"(x[1]),
+                   "r"(x[2]), "r"(x[3])
+                   : "memory");
+      mark_hot(hot, t + i - low);
+    }
+  }
+}
+// and what is not finite in the marked slots that a row sees, added to 32 of its outputs.
+__device__ __noinline__ void take_hot(const AttendArgs& g, const AttendUnit& u, const uint32_t* hot,
+                                      int lim, int D, int d0, float* o) {
+  const SlotRows rows(g, u);
+  for (int j = 0; j < 256 && u.low + j < lim; ++j) {
+    if (!(hot[j >> 5] >> (j & 31) & 1u)) continue;
+    const int t = u.low + j;
+    const long long row = rows.row(t, u.end, rows.page(t, u.end));
+    if (row < 0) continue;
+    for (int e = 0; e < 32; ++e) {
+      float x;
+      if (t < u.held) {
+        const unsigned char c = static_cast<const unsigned char*>(g.im.v)[row * D + d0 + e];
+        x = (c & 0x7F) == 0x7F ? __uint_as_float(0x7FC00000u) : 0.f;
+      } else {
+        x = __bfloat162float(static_cast<const __nv_bfloat16*>(g.c.v)[row * D + d0 + e]);
+      }
+      if (!isfinite(x)) o[e] += x;
+    }
+  }
+}
+
 // The codes of a tile's rows below `some`, times the scales of their runs of 8, as bf16 in a ring
 // slot, with zeros behind them up to the next run. Thread `tid` of N takes every N-th 8 codes. WHOLE:
-// all rows, so that every load is on its way before the first one is used.
+// all rows, so that every load is on its way before the first one is used. Otherwise values from row
+// `part` on that are not finite are marked in `hot`, row `part` - `first` first, and left out.
 template <int D, int N, bool WHOLE>
 __device__ __forceinline__ void expand_tile(uint32_t raw, const float* scale, int some,
-                                            uint32_t slot, int tid) {
+                                            uint32_t slot, int tid, int part = kCols,
+                                            int first = 0, uint32_t* hot = nullptr) {
   constexpr int kChunks = D / 8, kAll = kCols * kChunks, kEach = (kAll + N - 1) / N;
   const int rows = WHOLE ? kCols : min(kCols, (some + 7) / 8 * 8);
   uint32_t x[kEach][2];
@@ -263,6 +321,13 @@ __device__ __forceinline__ void expand_tile(uint32_t raw, const float* scale, in
                    : "r"(raw + c * 8)
                    : "memory");
       f[i] = scale[r / 8];
+      if constexpr (!WHOLE)
+        if (r >= part) {
+          const uint32_t y0 = not_finite<1>(x[i][0]), y1 = not_finite<1>(x[i][1]);
+          x[i][0] &= ~y0;
+          x[i][1] &= ~y1;
+          if (y0 | y1) mark_hot(hot, r - first);
+        }
     }
   }
 #pragma unroll
@@ -310,7 +375,8 @@ __device__ __forceinline__ void store_lse(const AttendArgs& g, const AttendUnit&
 template <int D, int NQ, bool IMAGE>
 __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
     attend_tc_kernel(const __grid_constant__ CUtensorMap map_k,
-                     const __grid_constant__ CUtensorMap map_v, bool use_maps, AttendArgs g) {
+                     const __grid_constant__ CUtensorMap map_v, bool use_maps,
+                     const __grid_constant__ AttendArgs g) {
   using P = Plan<D, NQ, IMAGE>;
   constexpr int kLoadWarps = P::kLoadWarps, kLoaders = P::kLoaders, kRuns = P::kRuns;
   constexpr int kIssueWarp = P::kIssueWarp, kThreads = P::kThreads;
@@ -318,6 +384,7 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
   __shared__ __align__(8) uint64_t s_bar[P::kBars];
   __shared__ uint32_t s_tmem;
   __shared__ int s_up, s_bad[16];                   // bad-page marks of tile % 16
+  __shared__ uint32_t s_hot[2][8];                  // marked slots of a piece, by turns, from u.low on
   __shared__ float s_m[kRows], s_l[kRows];
   __shared__ float s_scale[IMAGE ? P::kRaw : 1][kGroups];     // of the runs in a raw stage
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, b = blockIdx.x;
@@ -355,6 +422,7 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     s_up = 0;
   }
+  if (tid < 16) s_hot[tid / 8][tid % 8] = 0;
   grid_dep_wait();
   tc_before();
   const AttendShare sh = attend_share<kThreads>(
@@ -383,6 +451,8 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
         // ---- loader ----
         const int lt = tid - 32 * kLoadWarp, lw = warp - kLoadWarp;
         const SlotRows rows(g, u);
+        uint32_t* hot = s_hot[segment & 1];
+        const auto mixed = [&](int t0) { return u.low < u.end && t0 + kCols > u.low; };
         // K and V tiles in turn, every warp its runs of 8 slots
         const auto announce = [&](int k) {
           fence_async();
@@ -427,7 +497,8 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
         const int box = g.c.page_size ? min(kCols, 1 << rows.shift) : kCols;
         if constexpr (!IMAGE) {
           // whole tiles: one warp issues their boxes
-          const int whole = use_maps && !any_bad ? max(0, min(n, u.end / kCols - a0)) : 0;
+          // (but those that not every row sees whole)
+          const int whole = use_maps && !any_bad ? max(0, min(n, u.low / kCols - a0)) : 0;
           const int boxes = kCols / box * P::kBlocks;
           int y = 0;
           for (int i = 0; i < 2 * whole; ++i) {
@@ -452,6 +523,15 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
             }
           }
           // the others: a slot is announced kLag slots later, when its copies are in
+          const auto settle = [&](int i) {
+            const int t0 = (a0 + i / 2) * kCols, k = slot_no + i;
+            if ((i & 1) && mixed(t0))
+#pragma unroll 1
+              for (int r = 8 * lw; r < kCols; r += 8 * kLoadWarps)
+                clear_group<D>(t0 + r, u.low, u.end, s_ring + k % P::kSlots * P::kSlotBytes, r, lane,
+                               hot);
+            announce(k);
+          };
           constexpr int kLag = 4;
           for (int i = 2 * whole; i < 2 * n; ++i) {
             const int k = slot_no + i, sl = k % P::kSlots;
@@ -461,11 +541,11 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
             copy_tile(i, sl);
             if (i >= 2 * whole + kLag) {
               asm volatile("cp.async.wait_group %0;" ::"n"(kLag) : "memory");
-              announce(k - kLag);
+              settle(i - kLag);
             }
           }
           asm volatile("cp.async.wait_group 0;" ::: "memory");
-          for (int i = max(2 * whole, 2 * n - kLag); i < 2 * n; ++i) announce(slot_no + i);
+          for (int i = max(2 * whole, 2 * n - kLag); i < 2 * n; ++i) settle(i);
         } else {
           const int held = min(u.held, u.end);
           if (lw == 0) {
@@ -541,12 +621,14 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
               bar_wait(rfull + 8 * st, no / P::kRaw & 1, up, g.dev_status);
               bar_wait(empty + 8 * sl, (k / P::kSlots & 1) ^ 1, up, g.dev_status);
               const uint32_t slot = s_ring + sl * P::kSlotBytes;
-              if (held >= t0 + kCols)
+              const bool some = (i & 1) && mixed(t0);            // not every row sees it whole
+              if (held >= t0 + kCols && !some)
                 expand_tile<D, kLoaders - 32, true>(s_codes + st * P::kRawBytes, s_scale[st], kCols,
                                                     slot, lt - 32);
               else if (held > t0)
-                expand_tile<D, kLoaders - 32, false>(s_codes + st * P::kRawBytes, s_scale[st],
-                                                     held - t0, slot, lt - 32);
+                expand_tile<D, kLoaders - 32, false>(
+                    s_codes + st * P::kRawBytes, s_scale[st], min(held - t0, kCols), slot, lt - 32,
+                    some ? max(u.low - t0, 0) : kCols, u.low - t0, hot);
               if (t0 + kCols > held) {                          // bf16 rows, or none, behind it
                 __syncwarp();
                 const int q0 = held > t0 ? (held - t0 + 7) / 8 : 0;
@@ -555,6 +637,10 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
                                 rows.row(t0 + r, u.end, rows.page(t0 + r, u.end)), t0 + r, u.end,
                                 slot, r, lane);
                 asm volatile("cp.async.wait_all;" ::: "memory");
+                if (some)
+#pragma unroll 1
+                  for (int r = 8 * (q0 + lw - 1); r < kCols; r += 8 * (kLoadWarps - 1))
+                    clear_group<D>(t0 + r, u.low, u.end, slot, r, lane, hot);
               }
               announce(k);
               __syncwarp();
@@ -630,6 +716,7 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
       } else if (warp < 8) {
         // ---- softmax ----
         const int x = warp / 4, r = tid % kRows, rr = (NQ == 2 ? x * kRows : 0) + r;
+        if (tid < 8) s_hot[segment & 1 ^ 1][tid] = 0;         // the next piece's
         const uint32_t lanes = (uint32_t)(warp % 4 * 32) << 16;
         const uint32_t to = tmem + lanes + x * 256 + 128;
         const float c1 = fmaxf(fabsf(g.c1), 1.1754944e-38f);   // not 0: -inf c1 is -inf
@@ -772,6 +859,10 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
             m = nm;
           }
           const float f = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+          const uint32_t* hot = s_hot[segment & 1];
+          uint32_t any_hot = 0;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) any_hot |= hot[e];
 #pragma unroll 1
           for (int q = 0; q < D / 32; ++q) {
             float o[32];
@@ -781,6 +872,15 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
 #pragma unroll
               for (int e = 0; e < 32; ++e)
                 o[e] = o[e] * f0 + (count[1] ? s_o[(32 * q + e) * kRows + r] * f1 : 0.f);
+            if (any_hot) {
+              float y[32];
+              const AttendUnit unit = u;
+#pragma unroll
+              for (int e = 0; e < 32; ++e) y[e] = o[e];
+              take_hot(g, unit, hot, lim, D, 32 * q, y);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = y[e];
+            }
             // of a piece all 32 rows of a warp: whole 128-byte lines (with parts of them the join
             // of 19 pieces took 13 us longer)
             if (whole ? rr < u.rows : !idle) {

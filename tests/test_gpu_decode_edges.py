@@ -259,3 +259,76 @@ def test_attend_leaves_bad_pages_out(kind, page, group, tokens):
     if kind == "image":            # some of them among the rows behind the image
         held = [[[256, 480 // c.b * c.b], [32, 0], [128, 128], [480, 64], [0, 64]]]
         _check_bad_pages(c, [tokens, 1, tokens, tokens, tokens], bad, True, held=held, causal=False)
+
+
+# ---------------------------------------------------------------------------
+# values that are not finite in rows that only some tokens see
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("kind", ["bf16", "bf16_64", "image", "image_64", "f32", "f32_64"])
+@pytest.mark.parametrize("page", [0, 8])
+@pytest.mark.parametrize("group,tokens", [(1, 2), (4, 2), (2, 7), (4, 10), (8, 12), (4, 60), (1, 300)])
+def test_attend_values_that_are_not_finite_show_where_they_are_seen(kind, page, group, tokens):
+    # infinities and NaN in single features of the newest rows: in tokens before them the same
+    # features are finite and exact, in tokens that see them not finite
+    d = 64 if kind.endswith("_64") else 128
+    image, dt = kind.startswith("image"), F32 if kind.startswith("f32") else BF
+    c = Case(seqs=3, kv_heads=2, group=group, d=d, dtype=dt, page=page, capacity=720,
+             lens=[[720, 700], [tokens + 5, tokens], [320, 449]], seed=tokens)
+    n = [tokens, max(1, tokens - 1), tokens]
+    marks = (math.nan, math.nan) if image else (math.nan, math.inf, -math.inf)  # (codes hold no infinity)
+    for s in range(c.S):
+        for h in range(c.H):
+            T = int(c.lens[0, s, h])
+            for j, back in enumerate((0, 1, n[s] // 2, n[s] - 1)[:max(1, n[s])]):
+                at = c.at(0, s, h, T - back, T - back - 1)
+                rows = c.v[at]
+                rows[:, (17 * j + 5 * h) % d] = marks[(j + s) % len(marks)]
+                c.v[at] = rows
+    HG, N = c.H * group, sum(n)
+    q = torch.randn(N, HG, d, generator=c.g).to(dt)
+    cache, st = c.device_cache(), _status()
+    im = None
+    if image:
+        im = _image(c, cache)
+        nexus.quantize(cache, im, st)
+        im.rows[0, 2, 1] = 448 if tokens > 1 else im.rows[0, 2, 1]
+    out = torch.zeros(N, HG, d, dtype=dt, device=DEV)
+    lse = torch.zeros(N, HG, device=DEV)
+    ws = nexus.alloc_attend_workspace(cache, tokens=N, max_tokens=max(n))
+    kw = dict(max_tokens=max(n), cu_tokens=c.cu(n).to(DEV), image=im)
+    nexus.attend(cache, 0, q.to(DEV), out, ws, st, lse=lse, **kw)
+    out2 = torch.zeros_like(out)
+    nexus.attend(cache, 0, q.to(DEV), out2, ws, st, **kw)
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0
+    assert torch.equal(out.nan_to_num(), out2.nan_to_num())
+    deq = None if im is None else [x.cpu().float() for x in (im.k, im.v, im.k_scale, im.v_scale)]
+    a, sc, seen = 0, d ** -0.5, 0
+    for s, m in enumerate(n):
+        for h in range(c.H):
+            T = int(c.lens[0, s, h])
+            at = c.at(0, s, h, T)
+            k, v = c.k[at].double(), c.v[at].double()
+            r = int(im.rows[0, s, h]) if image else 0
+            if r:
+                for t, codes, scales in ((k, deq[0], deq[2]), (v, deq[1], deq[3])):
+                    per = [float(scales[_scale_at(c, 0, s, h, j)]) for j in range(0, r, c.b)]
+                    t[:r] = codes[c.at(0, s, h, r)].double() * \
+                        torch.tensor(per, dtype=torch.float64).repeat_interleave(c.b)[:, None]
+            M = [T - (m - 1 - i) for i in range(m) for _ in range(group)]
+            rows = q[a:a + m, h * group:(h + 1) * group].reshape(m * group, d)
+            ro, rl, A, big = attend64(rows, k, v, M, sc)
+            got = out[a:a + m, h * group:(h + 1) * group].reshape(m * group, d).cpu().double()
+            gl = lse[a:a + m, h * group:(h + 1) * group].reshape(-1).cpu().double()
+            fin = torch.isfinite(ro)
+            assert torch.equal(torch.isfinite(got), fin), (s, h)
+            dx = sc * big * (2.0 ** -24 * (d + 8) if dt == BF else 2.0 ** -20)
+            p = 2.0 ** -8 if dt == BF else 2.0 ** -19
+            tol = (2.0 ** -8 if dt == BF else 2.0 ** -24) * ro.abs() + (p + 2 * dx)[:, None] * A + 1e-30
+            assert torch.all((got - ro).abs()[fin] <= tol[fin]), (s, h)
+            some = torch.tensor(M) > 0
+            assert torch.all((gl - rl).abs()[some] <= (dx + 2.0 ** -19 * (1 + rl.abs()))[some]), (s, h)
+            seen += int((~fin).sum())
+        a += m
+    assert seen > 0
