@@ -787,11 +787,16 @@ __device__ __forceinline__ void attend_part(const AttendArgs& g, const AttendUni
   if constexpr (!SLOW)
     if (i < to) {
       asm volatile("cp.async.wait_all;" ::: "memory");
-      State<D, ROWS> copy = st;         // in local memory: st and u stay in registers
-      const AttendUnit unit = u;
-      attend_slow<KIND, D, ROWS, kDeep, kStageBytes>(g, unit, base, end, i, to, ring, meta, copy,
-                                                     vref);
-      st = copy;
+      if constexpr (KIND == kF32) {
+        attend_part<KIND, D, ROWS, kDeep, kStageBytes, true>(g, u, base, end, i, to, ring, meta, st,
+                                                             vref);
+      } else {
+        State<D, ROWS> copy = st;       // in local memory: st and u stay in registers
+        const AttendUnit unit = u;
+        attend_slow<KIND, D, ROWS, kDeep, kStageBytes>(g, unit, base, end, i, to, ring, meta, copy,
+                                                       vref);
+        st = copy;
+      }
       return;
     }
   if constexpr (KIND == kImage) {
@@ -806,7 +811,8 @@ __device__ __forceinline__ void attend_part(const AttendArgs& g, const AttendUni
 }
 
 // The steps from `from` on with what only some need: a function of its own, so that the others' loop
-// keeps its registers.
+// keeps its registers (image, 16 x 32768 rows: 165 us, 166 as a second loop of the caller; fp32, with
+// 255 registers instead of 168, does better with the loop: 64 x 6000 rows 82 us, 84 with the function).
 template <int KIND, int D, int ROWS, int kDeep, int kStageBytes>
 __device__ __noinline__ void attend_slow(const AttendArgs& g, const AttendUnit& u, int base, int end,
                                          int from, int to, uint32_t ring, Meta* meta,
