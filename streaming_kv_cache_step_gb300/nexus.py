@@ -448,6 +448,12 @@ def _int32(t, n: int, name: str):
         raise ValueError(f"{name} must be {n} contiguous int32 values on the GPU")
 
 
+def _status(t):
+    if t is None or t.dtype != torch.int32 or not t.is_cuda:
+        raise ValueError("dev_status must be an int32 tensor on the GPU")
+    return ctypes.c_void_p(t.data_ptr())
+
+
 def _heads(t, tokens: int, heads: int, cache: Cache, name: str):
     """A per-token tensor [tokens, heads, head_dim] whose heads lie behind one another;
     returns the elements between two tokens."""
@@ -489,6 +495,8 @@ def append(cache: Cache, layer: int, q, k, v, token_pos, q_out, dev_status, *, m
         _int32(lens_in, cache.seqs * H, "lens_in")
         a.lens_in = lens_in.data_ptr()
     if rotary is not None:
+        if not rotary.table.is_cuda:
+            raise ValueError("the rotary table must be on the GPU")
         a.rotary, a.rotary_dim = rotary.table.data_ptr(), rotary.rotary_dim
         a.interleaved = rotary.interleaved
     for name, w in (("q_norm", q_norm), ("k_norm", k_norm)):
@@ -500,7 +508,7 @@ def append(cache: Cache, layer: int, q, k, v, token_pos, q_out, dev_status, *, m
     im = None if image is None else ctypes.byref(image.c_struct(cache))
     _check(load().nexus_append_image(ctypes.byref(cache.c_struct()),
                                      ctypes.byref(_tokens(cache, layer, n, max_tokens, cu_tokens)),
-                                     ctypes.byref(a), im, _ptr(dev_status), _stream(stream)),
+                                     ctypes.byref(a), im, _status(dev_status), _stream(stream)),
            "nexus_append")
 
 
@@ -512,7 +520,7 @@ def quantize(cache: Cache, image: Image, dev_status, *, rows_in=None, stream=Non
         _int32(rows_in, cache.n_slices, "rows_in")
     _check(load().nexus_quantize(ctypes.byref(cache.c_struct()),
                                  ctypes.byref(image.c_struct(cache)), _ptr(rows_in),
-                                 _ptr(dev_status), _stream(stream)),
+                                 _status(dev_status), _stream(stream)),
            "nexus_quantize")
 
 
@@ -547,9 +555,11 @@ def attend(cache: Cache, layer: int, q, out, ws, dev_status, *, max_tokens: int,
                 lse.numel() != n * HQ:
             raise ValueError("lse must be [tokens, kv_heads * group] float32 on the GPU")
         a.lse = lse.data_ptr()
+    if not ws.is_cuda:
+        raise ValueError("ws must be on the GPU")
     im = None if image is None else ctypes.byref(image.c_struct(cache))
     _check(load().nexus_attend(ctypes.byref(cache.c_struct()),
                                ctypes.byref(_tokens(cache, layer, n, max_tokens, cu_tokens)), im,
-                               ctypes.byref(a), _ptr(ws), ws.numel(), _ptr(dev_status),
+                               ctypes.byref(a), _ptr(ws), ws.numel(), _status(dev_status),
                                _stream(stream)),
            "nexus_attend")

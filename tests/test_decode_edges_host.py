@@ -3,8 +3,10 @@ for, beside those of test_decode_host.py."""
 import ctypes
 import os
 import subprocess
+from types import SimpleNamespace
 
 import pytest
+import torch
 
 from streaming_kv_cache_step_gb300 import build
 from test_abi_host import _structs
@@ -61,3 +63,45 @@ def test_attend_workspace_goes_by_the_rows_alone(lib, rows, head_dim):  # noqa: 
                   dict(seqs=64, kv_heads=8, capacity=1 << 17)):
         assert size(rows, rows, **cache) == one and size(rows, 1 << 30, **cache) == one
         assert size(1 << 20, rows, **cache) == one
+
+
+class _Gpu:
+    """Stands for a CUDA tensor's properties around a CPU one (no call gets as far as its data)."""
+
+    def __init__(self, t):
+        self.t, self.is_cuda = t, True
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+
+def test_binding_refuses_host_memory(lib, monkeypatch):  # noqa: F811
+    from streaming_kv_cache_step_gb300 import nexus
+    called = lambda *a: pytest.fail("called with host memory")  # noqa: E731
+    monkeypatch.setattr(nexus, "load", lambda: SimpleNamespace(
+        nexus_append_image=called, nexus_quantize=called, nexus_attend=called))
+    monkeypatch.setattr(nexus.Cache, "c_struct", lambda self: nexus.CCache())
+    monkeypatch.setattr(nexus, "_stream", lambda stream: None)
+    monkeypatch.setattr(nexus.Image, "c_struct", lambda self, cache: nexus.CImage())
+    z = lambda *s, dt=torch.bfloat16: _Gpu(torch.zeros(*s, dtype=dt))  # noqa: E731
+    i = lambda *s: z(*s, dt=torch.int32)  # noqa: E731
+    cache = nexus.Cache(k=z(1, 1, 1, 64, 64), v=z(1, 1, 1, 64, 64), pos=i(1, 1, 1, 64), lens=i(1, 1, 1),
+                        layers=1, seqs=1, kv_heads=1, group=1, head_dim=64, capacity=64)
+    q, kv, pos, st, ws = z(1, 1, 64), z(1, 1, 64), i(1), i(1), z(4096, dt=torch.uint8)
+    rot = nexus.Rotary([1.0] * 4, device="cpu")
+    on = nexus.Rotary([1.0] * 4, device="cpu")
+    on.table = _Gpu(on.table)
+
+    def append(status=st, rotary=on):
+        nexus.append(cache, 0, q, kv, kv, pos, q, status, max_tokens=1, rotary=rotary)
+
+    def attend(status=st, ws=ws):
+        nexus.attend(cache, 0, q, q, ws, status, max_tokens=1)
+
+    host, wrong = torch.zeros(1, dtype=torch.int32), z(1, dt=torch.float32)
+    for call in (lambda: append(rotary=rot), lambda: append(status=host), lambda: append(status=None),
+                 lambda: append(status=wrong), lambda: attend(status=host), lambda: attend(status=wrong),
+                 lambda: attend(ws=torch.zeros(4096, dtype=torch.uint8)),
+                 lambda: nexus.quantize(cache, nexus.Image(*[None] * 5), host)):
+        with pytest.raises(ValueError):
+            call()
