@@ -26,6 +26,7 @@
  *   - All buffer pointers are DEVICE pointers owned by the caller. The library
  *     never allocates, frees or synchronises; scratch memory is the caller's
  *     workspace of nexus_workspace_bytes() bytes (256-byte aligned).
+ *     Pointers to 4-byte values are 4-byte aligned.
  *   - Calls are asynchronous on `stream`. The returned nx_status covers argument
  *     checks and launch errors only. Conditions found on the device are OR-ed into
  *     *dev_status (an int32 in device memory, caller-owned, which the caller zeroes

@@ -394,6 +394,8 @@ extern "C" nx_status nexus_append_image(nx_cache* cache, const nx_tokens* tokens
   if (image && cache->dtype != NX_DTYPE_BF16) return NX_ERR_UNSUPPORTED;
   const nx_cache& c = *cache;
   const nx_append& a = *args;
+  if (!aligned4(c.pos, c.lens, c.block_table, a.pos, a.lens_in, dev_status))
+    return NX_ERR_INVALID_ARG;
   const int size = c.dtype == NX_DTYPE_BF16 ? 2 : 4;
   const int D = c.head_dim;
   if (a.reserved != 0 || !(a.eps >= 0.f) || !(a.eps < 3.0e38f)) return NX_ERR_INVALID_ARG;

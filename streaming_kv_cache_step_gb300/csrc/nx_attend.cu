@@ -1207,6 +1207,7 @@ extern "C" nx_status nexus_attend(const nx_cache* cache, const nx_tokens* tokens
   const nx_cache& c = *cache;
   const nx_attend& a = *args;
   if (image && !valid_image(image)) return NX_ERR_INVALID_ARG;
+  if (!aligned4(c.lens, c.block_table, a.lse, dev_status)) return NX_ERR_INVALID_ARG;
   if (image && c.dtype != NX_DTYPE_BF16) return NX_ERR_UNSUPPORTED;
   // tiles (of at least 64 slots, and a partial one) of all units (of at least 8 rows)
   const long long heads = (long long)c.kv_heads * c.group;

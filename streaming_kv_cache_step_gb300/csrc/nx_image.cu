@@ -125,7 +125,8 @@ __global__ void image_rows_kernel(ImageArgs g, int slices) {
 
 bool valid_image(const nx_image* im) {
   return im && im->k && im->v && im->k_scale && im->v_scale && im->rows &&
-         !((uintptr_t)im->k & 15u) && !((uintptr_t)im->v & 15u);
+         !((uintptr_t)im->k & 15u) && !((uintptr_t)im->v & 15u) &&
+         aligned4(im->k_scale, im->v_scale, im->rows);
 }
 
 }  // namespace nx
@@ -136,7 +137,9 @@ extern "C" nx_status nexus_quantize(const nx_cache* cache, const nx_image* image
   using namespace nx;
   int launches = 0;
   begin_call();
-  if (!valid_cache(cache) || !valid_image(image) || !dev_status) return NX_ERR_INVALID_ARG;
+  if (!valid_cache(cache) || !valid_image(image) || !dev_status ||
+      !aligned4(cache->lens, cache->block_table, rows_in, dev_status))
+    return NX_ERR_INVALID_ARG;
   if (cache->dtype != NX_DTYPE_BF16) return NX_ERR_UNSUPPORTED;
   const long long slices = (long long)cache->layers * cache->seqs * cache->kv_heads;
   if (rows_in && rows_in != image->rows && rows_in < image->rows + slices &&

@@ -89,9 +89,16 @@ __device__ __forceinline__ long long row_of(const nx_cache& c, int l, int s, int
          (j % c.page_size);
 }
 
+// Whether pointers to 4-byte values (null too) are aligned.
+template <typename... T>
+inline bool aligned4(const T*... p) {
+  return ((((uintptr_t)p & 3u) == 0) && ...);
+}
+
 // Whether a description of new tokens fits the cache.
 inline bool valid_tokens(const nx_cache& c, const nx_tokens* t) {
   if (!t || t->layer < 0 || t->layer >= c.layers || t->reserved != 0) return false;
+  if (!aligned4(t->cu_tokens)) return false;
   if (t->tokens < 0 || t->max_tokens < 1) return false;
   return t->cu_tokens || (long long)c.seqs * t->max_tokens == t->tokens;
 }

@@ -105,3 +105,39 @@ def test_binding_refuses_host_memory(lib, monkeypatch):  # noqa: F811
                  lambda: nexus.quantize(cache, nexus.Image(*[None] * 5), host)):
         with pytest.raises(ValueError):
             call()
+
+
+def test_misaligned_counts_and_scales_are_refused(lib):  # noqa: F811
+    from streaming_kv_cache_step_gb300 import nexus
+    big = ctypes.c_size_t(1 << 40)
+
+    def append(cache=None, tok=None, status=STATUS, **over):
+        a = dict(k=0x2000000, v=0x3000000, k_stride=1024, v_stride=1024, pos=0x5000000, eps=1e-6)
+        c, _ = _structs(**(cache or {}))
+        return lib.nexus_append(ctypes.byref(c), ctypes.byref(_tok(**(tok or {}))),
+                                ctypes.byref(nexus.CAppend(**{**a, **over})), status, None)
+
+    def attend(cache=None, tok=None, image=None, status=STATUS, **over):
+        a = dict(q=0x100000, out=0x200000, q_stride=4096, out_stride=4096, scale=0.1, causal=1)
+        c, _ = _structs(**(cache or {}))
+        return lib.nexus_attend(ctypes.byref(c), ctypes.byref(_tok(**(tok or {}))),
+                                None if image is None else ctypes.byref(image),
+                                ctypes.byref(nexus.CAttend(**{**a, **over})),
+                                ctypes.c_void_p(0x1000000), big, status, None)
+
+    def quantize(cache=None, rows_in=None, status=STATUS, **im):
+        c, _ = _structs(**(cache or {}))
+        return lib.nexus_quantize(ctypes.byref(c), ctypes.byref(_image(**im)), rows_in, status, None)
+
+    off = ctypes.c_void_p(0x900002)
+    cu = dict(tok=dict(cu_tokens=0x8001))
+    for call in (lambda: append(pos=0x5000002), lambda: append(lens_in=0x7000001),
+                 lambda: append(status=off), lambda: append(**cu),
+                 lambda: append(cache=dict(lens=0x40002)), lambda: append(cache=dict(pos=0x30001)),
+                 lambda: attend(lse=0x300002), lambda: attend(status=off), lambda: attend(**cu),
+                 lambda: attend(cache=dict(lens=0x40001)),
+                 lambda: attend(image=_image(rows=0x500002)),
+                 lambda: attend(image=_image(k_scale=0x300001)),
+                 lambda: quantize(rows_in=ctypes.c_void_p(0x600003)), lambda: quantize(status=off),
+                 lambda: quantize(v_scale=0x400002), lambda: quantize(cache=dict(lens=0x40002))):
+        assert call() == nexus.NX_ERR_INVALID_ARG
