@@ -392,8 +392,9 @@ size_t nexus_attend_workspace_bytes(const nx_cache* cache, const nx_tokens* toke
  * rows through mma.sync, more to one on tcgen05; fp32 caches always to the first. One launch for
  * few or short slices (capacity up to some hundred rows, some thousand for a few dozen slices) on
  * the first, else two; the same bits every time.
- * NX_ERR_UNSUPPORTED for an image of an fp32 cache, for more than 2^20 query heads or 2^24
- * (sequence, KV head) pairs, or more than 2^31 tiles of 8 query rows x 64 slots. The scales of an
+ * NX_ERR_UNSUPPORTED for an image of an fp32 cache, for more than 2^20 query heads, 2^24
+ * (sequence, KV head) pairs, 2^31 - 256 query rows of a slice, or 2^31 tiles of 8 query rows x 64
+ * slots. The scales of an
  * image are non-negative; a slice's blocks may differ in scale by any factor up to 2^120 (values
  * below that part of the slice's largest may be lost).
  */

@@ -1212,6 +1212,7 @@ extern "C" nx_status nexus_attend(const nx_cache* cache, const nx_tokens* tokens
   // tiles (of at least 64 slots, and a partial one) of all units (of at least 8 rows)
   const long long heads = (long long)c.kv_heads * c.group;
   if (heads > (1 << 20) || (long long)c.seqs * c.kv_heads > (1 << 24) ||
+      most_tokens(*tokens) * c.group > 0x7FFFFFFFLL - 256 ||       // rows of a slice, by tiles
       (long long)c.seqs * c.kv_heads * (most_tokens(*tokens) * c.group / 8 + 1) >
           0x7FFFFFFFLL / (c.capacity / 64 + 2))
     return NX_ERR_UNSUPPORTED;

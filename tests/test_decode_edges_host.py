@@ -141,3 +141,16 @@ def test_misaligned_counts_and_scales_are_refused(lib):  # noqa: F811
                  lambda: quantize(rows_in=ctypes.c_void_p(0x600003)), lambda: quantize(status=off),
                  lambda: quantize(v_scale=0x400002), lambda: quantize(cache=dict(lens=0x40002))):
         assert call() == nexus.NX_ERR_INVALID_ARG
+
+
+def test_attend_refuses_more_rows_than_it_counts(lib):  # noqa: F811
+    from streaming_kv_cache_step_gb300 import nexus
+
+    def call(tokens):
+        c, _ = _structs(seqs=1, kv_heads=1, group=1 << 20, head_dim=64, capacity=64)
+        a = nexus.CAttend(q=0x100000, out=0x200000, q_stride=1 << 26, out_stride=1 << 26, scale=0.1, causal=1)
+        return lib.nexus_attend(ctypes.byref(c), ctypes.byref(_tok(tokens=tokens, max_tokens=tokens)), None,
+                                ctypes.byref(a), ctypes.c_void_p(0x1000000), ctypes.c_size_t(0), STATUS, None)
+
+    assert call(2048) == nexus.NX_ERR_UNSUPPORTED
+    assert call(2047) == nexus.NX_ERR_WORKSPACE                      # taken, but for the workspace
