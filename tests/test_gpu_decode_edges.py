@@ -332,3 +332,26 @@ def test_attend_values_that_are_not_finite_show_where_they_are_seen(kind, page, 
             seen += int((~fin).sum())
         a += m
     assert seen > 0
+
+
+# ---------------------------------------------------------------------------
+# whole prompts, and caches that hold far fewer rows than they could
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("kind", ["bf16", "image", "f32"])
+@pytest.mark.parametrize("page", [0, 16])
+def test_attend_whole_prompts(kind, page):
+    # every row of the slices is a token of the call: the causal triangle, and prompts of other lengths
+    c = Case(seqs=3, kv_heads=2, group=2, dtype=F32 if kind == "f32" else BF, page=page, capacity=2112,
+             lens=[[2100, 2100], [1, 1], [777, 777]], seed=page)
+    _check_attend(c, [2100, 1, 777], image=kind == "image")
+
+
+@pytest.mark.parametrize("kind", ["bf16", "image", "f32"])
+@pytest.mark.parametrize("page", [0, 16])
+@pytest.mark.parametrize("tokens", [1, 5, 40])
+def test_attend_few_rows_of_a_large_capacity(kind, page, tokens):
+    # kernels are chosen by capacity: slices of any length give the same whatever it is
+    c = Case(seqs=2, kv_heads=2, group=4, dtype=F32 if kind == "f32" else BF, page=page, capacity=1 << 15,
+             lens=[[40, 1638], [257, 64]], seed=tokens)
+    _check_attend(c, [tokens] * 2, image=kind == "image", uniform=True)
