@@ -355,3 +355,15 @@ def test_attend_few_rows_of_a_large_capacity(kind, page, tokens):
     c = Case(seqs=2, kv_heads=2, group=4, dtype=F32 if kind == "f32" else BF, page=page, capacity=1 << 15,
              lens=[[40, 1638], [257, 64]], seed=tokens)
     _check_attend(c, [tokens] * 2, image=kind == "image", uniform=True)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("page", [0, 8])
+@pytest.mark.parametrize("tokens", [12, 40])
+def test_attend_many_rows_over_scales_that_differ(tokens, page, d):
+    # the kernel for more than 80 rows: zeros, 2^-70 to 2^40, and values near the end of the range
+    for powers in ([None, -30, 20], [-70, 40, -9, -10, 0], [118, 110]):
+        c = Case(seqs=2, kv_heads=2, group=8, d=d, page=page, capacity=256, lens=[[256, 192], [96, 70]],
+                 seed=tokens)
+        _by_block(c, powers)
+        _check_attend(c, [tokens] * 2, image=True, uniform=True)
