@@ -355,7 +355,7 @@ nx_status nexus_append_image(nx_cache* cache, const nx_tokens* tokens, const nx_
  * are all 0; exponents are kept in -100..120), its codes are x / s rounded to nearest even:
  * s is a power of two, so that this is the only rounding and code times scale is exact in
  * bf16. Infinities become the largest code, NaN stays NaN. A block on a page out of range
- * (NX_DEV_BAD_PAGE) is left out. bf16 caches only (NX_ERR_UNSUPPORTED otherwise).
+ * (NX_DEV_BAD_PAGE) is left out, but rows counts it: with the table mended, rows_in takes it up. bf16 caches only (NX_ERR_UNSUPPORTED otherwise).
  */
 nx_status nexus_quantize(const nx_cache* cache, const nx_image* image, const int32_t* rows_in,
                          int32_t* dev_status, nx_stream_t stream);
@@ -392,6 +392,10 @@ size_t nexus_attend_workspace_bytes(const nx_cache* cache, const nx_tokens* toke
  * rows through mma.sync, more to one on tcgen05; fp32 caches always to the first. One launch for
  * few or short slices (capacity up to some hundred rows, some thousand for a few dozen slices) on
  * the first, else two; the same bits every time.
+ * What is rounded before the output: bf16 caches, the weights to two bf16 terms (2^-16 of each)
+ * with up to 128 query rows, to one (2^-8) with more; an image's rows, to fp16 (2^-11) with 9 to 80
+ * rows, to two terms (2^-22 fp16, 2^-16 bf16) otherwise; fp32 caches, all factors to two terms that
+ * hold 23 bits. All sums are binary32. (Rows are min(max_tokens, tokens) * group here.)
  * NX_ERR_UNSUPPORTED for an image of an fp32 cache, for more than 2^20 query heads, 2^24
  * (sequence, KV head) pairs, 2^31 - 256 query rows of a slice, or 2^31 tiles of 8 query rows x 64
  * slots. The scales of an

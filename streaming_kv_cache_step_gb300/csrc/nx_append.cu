@@ -12,9 +12,9 @@
 // by asynchronous copies, which hold no registers and start before the angles are computed.
 //
 // What bounds it: reads and writes of head rows, 2 B a value each way. 25144 tokens of prompts of
-// up to 8192, 40 normed and rotated and 8 plain head rows of 128 each, bf16: 618 MB in 97.3 us,
-// 6.35 TB/s, 93 % of a plain copy's rate (108 us with the next two tokens in registers). A
-// single token of 48 head rows takes 2.6 us, all latency.
+// up to 8192, 40 normed and rotated and 8 plain head rows of 128 each, bf16: 618 MB in 97.1 us,
+// 6.37 TB/s, 94 % of a plain copy's rate (108 us with the next two tokens in registers); fp32, 1.24
+// GB in 183 us, 6.74 TB/s. A single token of 48 head rows takes 2.6 us, all latency.
 #include <type_traits>
 
 #include "nx_internal.cuh"
@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(kMaxThreads) append_kernel(AppendArgs g) {
   const int rows = HQ + 2 * H;                       // head rows per token: q, k, v
   const int groups = blockDim.x / kLanes;
   // a warp's groups take neighbouring head rows; a row that does not exist takes part in the
-  // warp's shuffles, with zeros
+  // warp's shuffles, with whatever its place in the ring holds: groups do not mix
   bool primed = false;
   for (int base = part * groups + (tid & ~31) / kLanes; !primed || base < rows;
        base += g.parts * groups) {

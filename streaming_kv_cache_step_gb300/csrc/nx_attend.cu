@@ -22,10 +22,12 @@
 // more than an even deal: a slice is then a block's own, or a cluster's, whose blocks join their
 // pieces from one another's shared memory.
 //
-// Measured, one new token of 16 x 8 slices of 32768 rows, 4 query heads each: 308 us in bf16
-// (7.0 TB/s of K and V, what a plain copy reaches), 164 us from the image (6.55 TB/s); 64
-// sequences of ragged lengths in 16-row pages 271 us (6.7 TB/s); 8 slices of 1638 rows 9.3 us,
-// latencies; 8 slices of 64 rows 5.7 us.
+// Measured, one new token of 16 x 8 slices of 32768 rows, 4 query heads each: 310 us in bf16
+// (6.9 TB/s of K and V, what a plain copy reaches), 165 us from the image (6.5 TB/s); 64
+// sequences of ragged lengths in 16-row pages 270 to 284 us by the lengths (6.4 to 6.7 TB/s); 8
+// slices of 1638 rows 9.6 us, latencies; 8 slices of 64 rows 5.9 us. fp32: 64 slices of 6000 rows
+// 82 us (4.8 TB/s), 8 slices of 8192 rows 25 us for one token, 105 for 16 and 371 for 64, which take a
+// pass over K and V and their terms for every 8 query rows.
 #include "nx_attend.cuh"
 
 namespace nx {
@@ -46,8 +48,8 @@ constexpr bool kIsBf16 = KIND == kBf16 || KIND == kTail;
 // multiplied by its values' scale, in units of the largest scale so far, before it becomes fp16: that
 // leaves 2^-28 of the largest while scales stay within kApart of one another. From the first step
 // with a run below that on, a warp's steps go to pv_apart, whose operands never hold a scale (behind a
-// block of zeros, whose scale is 1, values of 2^-12 take 116 us over 32 x 8 x 6960 rows, one token, not
-// 83; the check itself 0.6 of 165 us over 16 x 8 x 32768).
+// block of zeros, whose scale is 1, values of 2^-12 take 119 us over 32 x 8 x 6960 rows, one token, not
+// 82; the check itself 0.6 of 165 us over 16 x 8 x 32768).
 constexpr float kUp = 11.f, kSlack = 4.f, kApart = 0.00390625f;
 
 template <int KIND>
@@ -83,7 +85,7 @@ __device__ __forceinline__ uint32_t rest2(float a, float b, uint32_t hi) {
   return pack2<KIND>(a - __low2float(h), b - __high2float(h));
 }
 
-// A binary32 value as the sum of two tf32 operands (11 bits each), to 2^-24 of it: the nearest
+// A binary32 value as the sum of two tf32 operands (11 bits each), to 2^-23 of it: the nearest
 // tf32, and the nearest to what that leaves (of an infinity: NaN, see plain_logits).
 __device__ __forceinline__ uint32_t tf32_near(float x) {
   uint32_t y;
@@ -1041,7 +1043,7 @@ __global__ void __launch_bounds__(kWarps * 32, Ring<KIND, D, ROWS>::kPerSm)
 
 // Joins the pieces of a unit that starts in a block b and ends in a later one. Few units, each of
 // many pieces: `g.splits` blocks a unit, for its rows in turn (8 slices of 32768 rows, 16 query
-// rows: attention takes 38.2 us in bf16, 48.9 with a block for each b; 31.9 and 43.1 us from the
+// rows: attention takes 38.3 us in bf16, 48.9 with a block for each b; 33.3 and 43.1 us from the
 // image); else a block for each b.
 constexpr int kJoinWarps = 16;
 template <int KIND, int D, int ROWS>

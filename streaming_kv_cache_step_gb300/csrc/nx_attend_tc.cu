@@ -21,15 +21,17 @@
 //   the last two    issue the matrix instructions, one warp for each stream
 // Where the tensor cores have time to spare (one row tile: K and V from HBM bound the kernel)
 // and for 8-bit rows, whose values need no rounding, p is kept as two bf16 terms, p = hi + lo,
-// with one product each; else as one (half a step of bf16, 2^-8, in each p).
+// with one product each; else, with more than 128 rows, as one (half a step of bf16, 2^-8, in each p:
+// error of the output against 64 bits 2.1e-3, 1.7e-3 with two terms).
 // Every wait is bounded; when one gives up, the block flags NX_DEV_TIMEOUT, starts no more copies,
 // waits (bounded too) for the copies and products that are under way and ends, its TMEM freed.
 //
-// Measured: two chunks of 512 tokens, 8 x 4 heads, over 8704 rows: 134 us on the GPU, 1.09 PFLOP/s,
-// 59 % of a plain bf16 product's rate; a step of a stream (64 slots) takes about 2000 clocks, of
+// Measured: two chunks of 512 tokens, 8 x 4 heads, over 8704 rows: 134 us per call, 1.09 PFLOP/s,
+// 56 % of a plain bf16 product's rate; a step of a stream (64 slots) takes about 2000 clocks, of
 // which its products need 640 and the other stream's as many: the rest is the latency of issuing
-// and committing them. 20 to 128 rows over 32 x 8 slices of 6960 rows: 181 to 186 us in bf16
-// (5.0 TB/s), 335 to 363 us from the image, where expanding the codes bounds it.
+// and committing them. 20 to 128 rows over 32 x 8 slices of 6960 rows: 180 to 186 us in bf16
+// (5.0 TB/s), 349 to 358 us from the image, where expanding the codes bounds it; the chunks from the
+// image 212 us.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -1032,9 +1034,9 @@ cudaError_t launch_t(AttendArgs& g, cudaStream_t st, int* launches) {
 
 // The row kernel takes 16 rows a pass over K and V, this one 256 but at a higher cost, from 8-bit
 // rows more so. Measured (us, this kernel / the row kernel) on 32 x 8 slices of 6960 rows: bf16, 16
-// rows 181 / 151, 20 rows 180 / 283; 8 bits, 80 rows 363 / 339, 96 rows 366 / 420. A second pass
+// rows 180 / 151, 20 rows 180 / 280; 8 bits, 80 rows 357 / 344, 96 rows 357 / 424. A second pass
 // that finds K and V in L2 costs less: bf16, 32 rows, 4 x 8 slices 45 / 43, one sequence of 8
-// slices of 32768 rows 62 / 45; 36 rows 45 / 53 and 62 / 58.
+// slices of 32768 rows 64 / 46; 36 rows 46 / 53 and 64 / 59.
 bool attend_tc_takes(const nx_cache& c, const nx_tokens& t, bool image) {
   const long long bytes = (long long)c.seqs * c.kv_heads * c.capacity * c.head_dim * 4;
   const int rows = image ? 80 : bytes <= (128LL << 20) ? 32 : kFewRows;

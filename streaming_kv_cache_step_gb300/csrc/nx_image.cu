@@ -6,7 +6,7 @@
 // that the largest magnitude and the codes come from one read. The rows are read once (2 B
 // a value) and the codes written once (1 B); nothing else moves, and HBM bounds it: 256 slices
 // of 6554 rows take 203 us, 6.35 TB/s of those bytes, 94 % of a plain copy's rate. Five blocks of
-// four warps per SM (102 registers) hold 160 KB of rows in flight; two blocks of eight warps took
+// four warps per SM (96 registers) hold 160 KB of rows in flight; two blocks of eight warps took
 // 221 us, seven of four (73 registers, with spills) 223 us.
 #include <cuda_fp8.h>
 
