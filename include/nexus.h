@@ -70,8 +70,12 @@ enum {
   NX_DEV_BAD_TOKENS = 16,   /* cu_tokens of a sequence decreases, leaves [0, tokens] or spans
                                more than max_tokens: the sequence's tokens are not processed */
   NX_DEV_FULL = 32,         /* a slice has no room for its new rows: slice left untouched */
-  NX_DEV_BAD_IMAGE = 64     /* an image holds a row count that is negative, not whole blocks
+  NX_DEV_BAD_IMAGE = 64,    /* an image holds a row count that is negative, not whole blocks
                                or beyond the slice's rows: slice left untouched */
+  NX_DEV_NO_PAGES = 128,    /* nexus_plan: too few free pages for a sequence's tokens; it keeps
+                               its pages and brings no tokens */
+  NX_DEV_BAD_PROBS = 256    /* nexus_verify: a row of probabilities that is 0 everywhere; its
+                               token is 0 */
 };
 
 enum { NX_DTYPE_F32 = 0, NX_DTYPE_BF16 = 1 };
@@ -405,6 +409,144 @@ size_t nexus_attend_workspace_bytes(const nx_cache* cache, const nx_tokens* toke
 nx_status nexus_attend(const nx_cache* cache, const nx_tokens* tokens, const nx_image* image,
                        const nx_attend* args, void* ws, size_t ws_bytes, int32_t* dev_status,
                        nx_stream_t stream);
+
+/*
+ * Attention over a prefix that several sequences share and over their own rows.
+ * prefix: a cache of its own (prefix->seqs prefixes, each a "sequence" with lens of its own, so
+ *   that it can have been evicted like any other), of the same kv_heads, group, head_dim and dtype.
+ *   Both caches may be paged over the same pool. Nothing is written to it.
+ * cu_seqs: prefix i is shared by sequences [cu_seqs[i], cu_seqs[i + 1]) of `cache`; what lies
+ *   before the first or behind the last has no prefix. NULL: one prefix, shared by all.
+ */
+typedef struct nx_shared {
+  const nx_cache* prefix;
+  const nx_image* image;       /* nullable: 8-bit image of the prefix cache */
+  const int32_t* cu_seqs;      /* nullable device int32 [prefix->seqs + 1] */
+  int32_t max_tokens;          /* host bound: no prefix is shared by more new tokens (>= 1) */
+  int32_t reserved;            /* 0 */
+} nx_shared;
+
+/* Bytes of workspace nexus_attend_shared needs for these arguments (0 on invalid arguments). They
+   go by dtype, head_dim, heads, tokens and the two max_tokens, not by capacities or lengths. */
+size_t nexus_attend_shared_workspace_bytes(const nx_cache* cache, const nx_tokens* tokens,
+                                           const nx_shared* shared);
+
+/*
+ * nexus_attend with one softmax over the rows of a token's prefix and the rows of its own slice:
+ * for a token of sequence s that shares prefix i and query head h * group + g, over all slots of
+ * slice (layer, i, h) of shared->prefix, then the slots j < M of slice (layer, s, h) of `cache` as
+ * in nexus_attend (causal says which of its own slice's rows a token sees; the prefix it sees
+ * whole). The rows of a prefix are read once for all tokens that share it, not once per sequence.
+ * Everything else is as in nexus_attend, for either part by itself: images, flagged slices and
+ * pages, rows that are not finite, the kernels taken (the prefix part has the rows of all the
+ * tokens that share it, max_tokens of nx_shared times group, at most) and what they round. The two
+ * parts meet in binary32. Three or more launches.
+ * A prefix whose entries of cu_seqs decrease or leave [0, seqs], or whose tokens are more than
+ * nx_shared.max_tokens (NX_DEV_BAD_TOKENS), counts as empty.
+ */
+nx_status nexus_attend_shared(const nx_cache* cache, const nx_tokens* tokens,
+                              const nx_image* image, const nx_shared* shared,
+                              const nx_attend* args, void* ws, size_t ws_bytes,
+                              int32_t* dev_status, nx_stream_t stream);
+
+/* ------------------------------------------------------------------------------------
+ * Around a step: laying out the next batch, and judging drafted tokens.
+ * ------------------------------------------------------------------------------------ */
+
+/*
+ * The pages of a paged cache. A sequence holds its first held[s] entries of the block table, in
+ * all layers and heads alike; entries behind them mean nothing. Pages that nobody holds are
+ * free_pages[0 .. *free_count - 1], in any order. Pages of a prefix that another cache's table
+ * names are in neither.
+ */
+typedef struct nx_pool {
+  int32_t* block_table;        /* cache->block_table, [seqs][max_pages_per_seq] */
+  int32_t* free_pages;         /* [num_pages] */
+  int32_t* free_count;         /* [1] */
+  int32_t* held;               /* [seqs] */
+  const int32_t* free_count_in;  /* nullable [1]: *free_count before the call, NULL: *free_count */
+  const int32_t* held_in;      /* nullable [seqs]: held before the call, NULL: held */
+} nx_pool;
+
+typedef struct nx_plan {
+  const int32_t* new_tokens;   /* [seqs] tokens that each sequence brings next; < 0: it ends */
+  const int32_t* first_pos;    /* [seqs] position of the first of them; NULL with token_pos */
+  int32_t* cu_tokens;          /* [seqs + 1] */
+  int32_t* token_seq;          /* nullable [tokens] */
+  int32_t* token_pos;          /* nullable [tokens] */
+  int32_t tokens;              /* rows of the per-token arrays */
+  int32_t max_tokens;          /* no sequence brings more (>= 1) */
+} nx_plan;
+
+/*
+ * Lays out the next batch. Sequence s, whose longest slice holds m = max over layers and heads of
+ * lens rows, needs ceil((m + new_tokens[s]) / page_size) pages; one that ends needs none, and its
+ * slices' lens (and the image's rows, with an image) become 0. Pages held beyond need, which an
+ * eviction or drafts taken back leave behind, go back; then missing ones are dealt out:
+ *   released pages are appended to free_pages, by sequence, then by table entry;
+ *   taken ones come from its end, last page first, in the same order;
+ *   held[s] = need, *free_count counts what is left; free_pages beyond it keeps what it held.
+ * cu_tokens[s] = tokens of the sequences before s; token_seq[i] and token_pos[i] of a sequence's
+ * j-th token are s and first_pos[s] + j; entries from cu_tokens[seqs] on are not written. With
+ * cu_tokens, token_pos and the block table nexus_append and nexus_attend can follow on the stream
+ * without the host having seen a length.
+ * A sequence is refused -- it brings no tokens, and its pages and lens stay -- where a slice has a
+ * bad length (NX_DEV_BAD_LEN), new_tokens is above max_tokens or its tokens, with those of the
+ * sequences before, are more than `tokens` (NX_DEV_BAD_TOKENS), m + new_tokens is above capacity
+ * (NX_DEV_FULL), held is out of range (NX_DEV_BAD_PAGE), or the pages that it and the sequences
+ * before take are more than there are (NX_DEV_NO_PAGES: nobody overtakes a sequence that waits).
+ * A *free_count out of range counts as 0, pages that find no room in free_pages are lost
+ * (NX_DEV_BAD_PAGE): neither happens unless the caller's tables are wrong.
+ * pool: NULL for a contiguous cache (no pages), else required. held_in and free_count_in make a
+ * call repeatable, as long as free_pages below *free_count_in and the table's entries stay. One
+ * launch. NX_ERR_UNSUPPORTED for more than 8192 sequences or 2^24 (layer, head) pairs.
+ */
+nx_status nexus_plan(nx_cache* cache, const nx_pool* pool, const nx_plan* plan,
+                     const nx_image* image, int32_t* dev_status, nx_stream_t stream);
+
+/*
+ * What nexus_verify reads and writes. Per-token arrays have the rows of nx_tokens: row i of a
+ * sequence is the i-th token it fed to the model in this step, token 0 the last one known before,
+ * the others drafts. p: row i is the model's distribution behind token i. q: row i is what draft
+ * i + 1 was drawn from (a sequence's last row is not read); NULL: drafts were not drawn, q is 1 at
+ * the draft and 0 elsewhere.
+ */
+typedef struct nx_verify {
+  const int32_t* token;        /* [tokens] */
+  const void* p;               /* [tokens][vocab] */
+  const void* q;               /* nullable [tokens][vocab] */
+  int64_t p_stride, q_stride;  /* elements between rows, any; rows need no alignment */
+  const float* u;              /* [tokens] uniform in [0, 1): row i judges draft i + 1 */
+  const float* u_draw;         /* [seqs] uniform in [0, 1): draws the new token */
+  int32_t* out;                /* [tokens] */
+  int32_t* emitted;            /* [seqs] */
+  const int32_t* lens_in;      /* nullable [layers][seqs][kv_heads]: lens before the call */
+  int32_t vocab;
+  int32_t dtype;               /* NX_DTYPE_F32 or NX_DTYPE_BF16, of p and q */
+  int32_t reserved;            /* 0 */
+} nx_verify;
+
+/*
+ * Verifies the drafts of every sequence (n tokens, n - 1 drafts) so that what comes out is
+ * distributed like p. Draft x = token[i + 1] stays if all before it do and u[i] q_i(x) < p_i(x)
+ * (exactly: the product in binary64). With r drafts kept, the next token is drawn by u_draw from
+ *   max(0, p_r - q_r)  where draft r + 1 went (p_r itself where that is 0 everywhere),
+ *   p_r                where all stayed (r = n - 1).
+ * Drawn from weights w_j means: with whole weights W_j = floor(2^42 w_j) (p - q in binary32) and
+ * t = floor(floor(2^31 u_draw) sum W / 2^31), the least j with W_0 + .. + W_j > t, so any
+ * implementation finds the same token. Probabilities count from 0 to 1: NaN and what is below as 0.
+ *   out: the r kept drafts, the new token, then -1;  emitted[s] = r + 1 (0 for no tokens).
+ * The cache then loses what went: lens = lens_in - (n - 1 - r) in every slice of the sequence in
+ * every layer, and rows of an image (nullable) drop to floor(lens / b) b where they are more. A
+ * slice whose lens_in is out of range or below the rows to take back (NX_DEV_BAD_LEN) stays. K, V
+ * and pos are not touched. lens_in may be cache->lens, but not overlap it otherwise.
+ * A draft outside [0, vocab) goes (NX_DEV_BAD_TOKENS). With n = 1 this is plain drawing.
+ * tokens->layer is not used. One launch, which reads one row of p and q per sequence.
+ * NX_ERR_UNSUPPORTED for vocab above 2^20, an image of an fp32 cache, 2^24 sequences or (layer,
+ * head) pairs.
+ */
+nx_status nexus_verify(nx_cache* cache, const nx_tokens* tokens, const nx_verify* args,
+                       const nx_image* image, int32_t* dev_status, nx_stream_t stream);
 
 /*
  * Testing hook for failure detection (not part of the method): kv_compact, except that

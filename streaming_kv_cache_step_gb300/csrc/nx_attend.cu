@@ -842,9 +842,25 @@ __device__ __forceinline__ void store_out(const AttendArgs& g, const AttendUnit&
                            ((long long)u.h * g.c.group + row % g.c.group) * D + f] = (T)x;
 }
 
-// o / l, and ln l with the reference put back.
+// o / l, and ln l with the reference put back; of the prefixes' pass o, m and l as they are, which
+// the own rows' pass takes in first (`joins`: it has some).
 __device__ __forceinline__ void finish_row(const AttendArgs& g, const AttendUnit& u, int r, int D,
-                                           int f, float m, float l, float o) {
+                                           int f, float m, float l, float o, bool joins) {
+  if (g.part.pass) {
+    const long long at = part_row(g, u, r);
+    if (g.part.pass == 1) {
+      g.part.out[at * D + f] = o;
+      if (f == 0) g.part.stat[at] = make_float2(m, l);
+      return;
+    }
+    if (joins) {
+      const float2 other = g.part.stat[at];
+      const float y = g.part.out[at * D + f];
+      const float2 k = join_by(m, l, other);
+      l = l * k.x + other.y * k.y;
+      o = o * k.x + y * k.y;
+    }
+  }
   const float y = l == 0.f ? 0.f : o / l;
   if (g.c.dtype == NX_DTYPE_BF16) store_out<__nv_bfloat16>(g, u, r, D, f, y);
   else store_out<float>(g, u, r, D, f, y);
@@ -973,7 +989,7 @@ __global__ void __launch_bounds__(kWarps * 32, Ring<KIND, D, ROWS>::kPerSm)
           }
         }
       __syncthreads();
-      const bool whole = a0 == 0 && a1 == tiles;
+      const bool whole = a0 == 0 && a1 == tiles, joins = whole && part_joins(g, u);
       const int slot = 2 * b + (a0 == 0 ? 1 : 0);
       for (int i = tid; i < u.rows * D; i += kWarps * 32) {
         const int r = i / D, f = i % D;
@@ -988,7 +1004,7 @@ __global__ void __launch_bounds__(kWarps * 32, Ring<KIND, D, ROWS>::kPerSm)
           o += k * s_o[w][r][f];
         }
         if (whole) {
-          finish_row(g, u, r, D, f, m, l, o);
+          finish_row(g, u, r, D, f, m, l, o, joins);
         } else if (!EVEN && meets) {
           s_o[0][r][f] = o;                             // read by this thread alone so far
           if (f == 0) {
@@ -1014,6 +1030,7 @@ __global__ void __launch_bounds__(kWarps * 32, Ring<KIND, D, ROWS>::kPerSm)
     // the cluster's pieces, in the order of their slots, from the blocks' shared memory
     cluster_sync();
     const AttendUnit u = attend_unit<ROWS>(g, b / g.ranks);
+    const bool joins = part_joins(g, u);
     for (int i = b % g.ranks * (kWarps * 32) + tid; i < u.rows * D; i += g.ranks * kWarps * 32) {
       const int r = i / D, f = i % D;
       float m[kRanks], z[kRanks], x[kRanks], top = -INFINITY, l = 0.f, o = 0.f;
@@ -1035,7 +1052,7 @@ __global__ void __launch_bounds__(kWarps * 32, Ring<KIND, D, ROWS>::kPerSm)
         l += k * z[p];
         o += k * x[p];
       }
-      finish_row(g, u, r, D, f, top, l, o);
+      finish_row(g, u, r, D, f, top, l, o, joins);
     }
     cluster_sync();                                     // nobody reads this block any more
   }
@@ -1065,6 +1082,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(AttendArgs
   const AttendUnit u = attend_unit<ROWS>(g, unit);
   const int mine = (u.rows - split + splits - 1) / splits;         // rows split, split + splits ..
   if (mine <= 0) return;
+  const bool joins = part_joins(g, u);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   int groups = kJoinWarps;                               // warps of a row
   while (groups > 1 && mine * groups > kJoinWarps) groups /= 2;
@@ -1103,7 +1121,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(AttendArgs
       sum += k * s_l[w];
       x += k * s_o[w][f];
     }
-    finish_row(g, u, split + rr * splits, D, f, top, sum, x);
+    finish_row(g, u, split + rr * splits, D, f, top, sum, x, joins);
   }
 }
 
@@ -1187,15 +1205,102 @@ cudaError_t launch_attend(AttendArgs& g, cudaStream_t st, int* launches) {
 }  // namespace
 }  // namespace nx
 
+namespace nx {
+namespace {
+
+// What nexus_attend and nexus_attend_shared check of a cache and the tokens that look into it.
+nx_status attend_limits(const nx_cache& c, const nx_tokens& t, const nx_image* image) {
+  if (image && !valid_image(image)) return NX_ERR_INVALID_ARG;
+  if (!aligned4(c.lens, c.block_table)) return NX_ERR_INVALID_ARG;
+  if (image && c.dtype != NX_DTYPE_BF16) return NX_ERR_UNSUPPORTED;
+  // tiles (of at least 64 slots, and a partial one) of all units (of at least 8 rows)
+  if ((long long)c.kv_heads * c.group > (1 << 20) || (long long)c.seqs * c.kv_heads > (1 << 24) ||
+      most_tokens(t) * c.group > 0x7FFFFFFFLL - 256 ||             // rows of a slice, by tiles
+      (long long)c.seqs * c.kv_heads * (most_tokens(t) * c.group / 8 + 1) >
+          0x7FFFFFFFLL / (c.capacity / 64 + 2))
+    return NX_ERR_UNSUPPORTED;
+  return NX_OK;
+}
+
+nx_status attend_pointers(const nx_cache& c, const nx_tokens& t, const nx_attend& a,
+                          int32_t* dev_status) {
+  if (!aligned4(a.lse, dev_status)) return NX_ERR_INVALID_ARG;
+  const int size = c.dtype == NX_DTYPE_BF16 ? 2 : 4;
+  if (!isfinite(a.scale)) return NX_ERR_INVALID_ARG;
+  if (a.q_stride < 0 || a.out_stride < 0 || a.q_stride * size % 16 || a.out_stride * size % 16 ||
+      ((uintptr_t)a.q & 15u) || ((uintptr_t)a.out & 15u))
+    return NX_ERR_INVALID_ARG;
+  if (t.tokens > 0 && (!a.q || !a.out)) return NX_ERR_INVALID_ARG;
+  if (t.tokens > 1 && a.out_stride < (long long)c.kv_heads * c.group * c.head_dim)
+    return NX_ERR_INVALID_ARG;           // rows of out would overlap
+  return NX_OK;
+}
+
+size_t attend_bytes(const nx_cache& c, const nx_tokens& t) {
+  AttendWs ws;                            // of any cache of this type, with an image or without
+  const size_t rows = attend_layout(c.head_dim, nullptr, &ws);
+  const size_t tc = attend_tc_may_take(c, t) ? attend_tc_layout(c.head_dim, nullptr, &ws) : 0;
+  return rows > tc ? rows : tc;
+}
+
+// One pass over a cache's slices.
+cudaError_t attend_pass(const nx_cache& c, const nx_tokens& t, const nx_image* image,
+                        const nx_attend& a, const AttendPart& part, char* ws, int32_t* dev_status,
+                        cudaStream_t st, int* launches) {
+  AttendArgs g{};
+  g.c = c;
+  g.t = t;
+  if (image) g.im = *image;
+  g.a = a;
+  g.part = part;
+  g.dev_status = dev_status;
+  if (attend_tc_takes(c, t, image != nullptr)) attend_tc_layout(c.head_dim, ws, &g.ws);
+  else attend_layout(c.head_dim, ws, &g.ws);
+  g.b = image_block(c);
+  while (1 << g.b_shift < g.b) ++g.b_shift;
+  g.c1 = a.scale * 1.4426950408889634f;
+  return c.head_dim == 128 ? launch_attend<128>(g, st, launches)
+                           : launch_attend<64>(g, st, launches);
+}
+
+// The tokens of nexus_attend_shared as the prefixes see them: those of a prefix's sequences are one
+// sequence's. (Which ones go by cu_seqs too: shared_tokens.)
+nx_tokens shared_view(const nx_tokens& t, const nx_shared& x) {
+  nx_tokens y = t;
+  y.max_tokens = x.max_tokens;
+  return y;
+}
+
+bool valid_shared(const nx_cache& c, const nx_tokens& t, const nx_shared* x) {
+  if (!x || x->reserved != 0 || x->max_tokens < 1 || !aligned4(x->cu_seqs)) return false;
+  if (!valid_cache(x->prefix)) return false;
+  const nx_cache& p = *x->prefix;
+  return p.kv_heads == c.kv_heads && p.group == c.group && p.head_dim == c.head_dim &&
+         p.dtype == c.dtype && t.layer < p.layers && (x->cu_seqs || p.seqs == 1);
+}
+
+// Workspaces of the own rows' pass and the prefixes', and where they meet.
+size_t shared_layout(const nx_cache& c, const nx_tokens& t, const nx_shared& x, char* base,
+                     char** own, char** prefix, AttendPart* part) {
+  const size_t rows = (size_t)t.tokens * c.kv_heads * c.group;
+  size_t at = 0;
+  *own = base;
+  at += round256(attend_bytes(c, t));
+  *prefix = base + at;
+  at += round256(attend_bytes(*x.prefix, shared_view(t, x)));
+  part->stat = reinterpret_cast<float2*>(base + at);
+  at += round256(rows * sizeof(float2));
+  part->out = reinterpret_cast<float*>(base + at);
+  return at + rows * c.head_dim * sizeof(float);
+}
+
+}  // namespace
+}  // namespace nx
+
 extern "C" size_t nexus_attend_workspace_bytes(const nx_cache* cache, const nx_tokens* tokens) {
   using namespace nx;
   if (!valid_cache(cache) || !valid_tokens(*cache, tokens)) return 0;
-  AttendWs ws;                            // of any cache of this type, with an image or without
-  const size_t rows = attend_layout(cache->head_dim, nullptr, &ws);
-  const size_t tc = attend_tc_may_take(*cache, *tokens)
-                        ? attend_tc_layout(cache->head_dim, nullptr, &ws)
-                        : 0;
-  return rows > tc ? rows : tc;
+  return attend_bytes(*cache, *tokens);
 }
 
 extern "C" nx_status nexus_attend(const nx_cache* cache, const nx_tokens* tokens,
@@ -1206,43 +1311,64 @@ extern "C" nx_status nexus_attend(const nx_cache* cache, const nx_tokens* tokens
   begin_call();
   if (!valid_cache(cache) || !valid_tokens(*cache, tokens) || !args || !dev_status)
     return NX_ERR_INVALID_ARG;
-  const nx_cache& c = *cache;
-  const nx_attend& a = *args;
-  if (image && !valid_image(image)) return NX_ERR_INVALID_ARG;
-  if (!aligned4(c.lens, c.block_table, a.lse, dev_status)) return NX_ERR_INVALID_ARG;
-  if (image && c.dtype != NX_DTYPE_BF16) return NX_ERR_UNSUPPORTED;
-  // tiles (of at least 64 slots, and a partial one) of all units (of at least 8 rows)
-  const long long heads = (long long)c.kv_heads * c.group;
-  if (heads > (1 << 20) || (long long)c.seqs * c.kv_heads > (1 << 24) ||
-      most_tokens(*tokens) * c.group > 0x7FFFFFFFLL - 256 ||       // rows of a slice, by tiles
-      (long long)c.seqs * c.kv_heads * (most_tokens(*tokens) * c.group / 8 + 1) >
-          0x7FFFFFFFLL / (c.capacity / 64 + 2))
-    return NX_ERR_UNSUPPORTED;
-  const int size = c.dtype == NX_DTYPE_BF16 ? 2 : 4;
-  if (!isfinite(a.scale)) return NX_ERR_INVALID_ARG;
-  if (a.q_stride < 0 || a.out_stride < 0 || a.q_stride * size % 16 || a.out_stride * size % 16 ||
-      ((uintptr_t)a.q & 15u) || ((uintptr_t)a.out & 15u))
-    return NX_ERR_INVALID_ARG;
-  if (tokens->tokens > 0 && (!a.q || !a.out)) return NX_ERR_INVALID_ARG;
-  if (tokens->tokens > 1 && a.out_stride < heads * c.head_dim)
-    return NX_ERR_INVALID_ARG;           // rows of out would overlap
-  if (!ws || ((uintptr_t)ws & 255u) || ws_bytes < nexus_attend_workspace_bytes(cache, tokens))
+  nx_status status = attend_limits(*cache, *tokens, image);
+  if (status == NX_OK) status = attend_pointers(*cache, *tokens, *args, dev_status);
+  if (status != NX_OK) return status;
+  if (!ws || ((uintptr_t)ws & 255u) || ws_bytes < attend_bytes(*cache, *tokens))
     return NX_ERR_WORKSPACE;
   if (tokens->tokens == 0) return finish(cudaSuccess, launches);
-  AttendArgs g{};
-  g.c = c;
-  g.t = *tokens;
-  if (image) g.im = *image;
-  g.a = a;
-  g.dev_status = dev_status;
-  if (attend_tc_takes(c, *tokens, image != nullptr))
-    attend_tc_layout(c.head_dim, static_cast<char*>(ws), &g.ws);
-  else attend_layout(c.head_dim, static_cast<char*>(ws), &g.ws);
-  g.b = image_block(c);
-  while (1 << g.b_shift < g.b) ++g.b_shift;
-  g.c1 = a.scale * 1.4426950408889634f;
+  const cudaError_t e =
+      attend_pass(*cache, *tokens, image, *args, AttendPart{}, static_cast<char*>(ws), dev_status,
+                  reinterpret_cast<cudaStream_t>(stream), &launches);
+  return finish(e, launches);
+}
+
+extern "C" size_t nexus_attend_shared_workspace_bytes(const nx_cache* cache,
+                                                      const nx_tokens* tokens,
+                                                      const nx_shared* shared) {
+  using namespace nx;
+  if (!valid_cache(cache) || !valid_tokens(*cache, tokens) ||
+      !valid_shared(*cache, *tokens, shared))
+    return 0;
+  char *own, *prefix;
+  AttendPart part;
+  return shared_layout(*cache, *tokens, *shared, nullptr, &own, &prefix, &part);
+}
+
+extern "C" nx_status nexus_attend_shared(const nx_cache* cache, const nx_tokens* tokens,
+                                         const nx_image* image, const nx_shared* shared,
+                                         const nx_attend* args, void* ws, size_t ws_bytes,
+                                         int32_t* dev_status, nx_stream_t stream) {
+  using namespace nx;
+  int launches = 0;
+  begin_call();
+  if (!valid_cache(cache) || !valid_tokens(*cache, tokens) || !args || !dev_status ||
+      !valid_shared(*cache, *tokens, shared))
+    return NX_ERR_INVALID_ARG;
+  const nx_tokens view = shared_view(*tokens, *shared);
+  nx_status status = attend_limits(*cache, *tokens, image);
+  if (status == NX_OK) status = attend_limits(*shared->prefix, view, shared->image);
+  if (status == NX_OK) status = attend_pointers(*cache, *tokens, *args, dev_status);
+  if (status != NX_OK) return status;
+  char *own, *prefix;
+  AttendPart part{};
+  const size_t need = shared_layout(*cache, *tokens, *shared, static_cast<char*>(ws), &own,
+                                    &prefix, &part);
+  if (!ws || ((uintptr_t)ws & 255u) || ws_bytes < need) return NX_ERR_WORKSPACE;
+  if (tokens->tokens == 0) return finish(cudaSuccess, launches);
+  part.seqs = cache->seqs;
+  part.max_tokens = tokens->max_tokens;
+  part.prefixes = shared->prefix->seqs;
+  part.max_shared = shared->max_tokens;
+  part.cu_seqs = shared->cu_seqs;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  return finish(c.head_dim == 128 ? launch_attend<128>(g, st, &launches)
-                                  : launch_attend<64>(g, st, &launches),
-                launches);
+  nx_attend whole = *args;                // the prefix comes before all of the new tokens
+  whole.causal = 0;
+  part.pass = 1;
+  cudaError_t e = attend_pass(*shared->prefix, view, shared->image, whole, part, prefix,
+                              dev_status, st, &launches);
+  if (e != cudaSuccess) return finish(e, launches);
+  part.pass = 2;
+  e = attend_pass(*cache, *tokens, image, *args, part, own, dev_status, st, &launches);
+  return finish(e, launches);
 }

@@ -22,8 +22,19 @@ struct AttendWs {
   float* out;          // [2 * blocks][rows x head_dim] unnormalised output
 };
 
+// Where the two passes of nexus_attend_shared meet: for every query row what the prefixes' pass has
+// of it, which the own rows' pass joins with its own when it finishes the row.
+struct AttendPart {
+  int pass;            // 0: a call by itself, 1: the prefixes, 2: the sequences' own rows
+  int seqs, max_tokens, prefixes, max_shared;     // of the cache, its tokens, the prefixes
+  const int32_t* cu_seqs;
+  float2* stat;        // [tokens][query heads] running maximum (log2 units) and sum
+  float* out;          // [tokens][query heads][head_dim] unnormalised output
+};
+
 struct AttendArgs {
-  nx_cache c;
+  nx_cache c;           // pass 1: the prefixes' cache, a "sequence" each
+  AttendPart part;
   nx_tokens t;
   nx_image im;          // im.k null: no image
   nx_attend a;
@@ -51,13 +62,33 @@ __device__ __forceinline__ int row_limit(const AttendArgs& g, const AttendUnit& 
   return m < 0 ? 0 : m;
 }
 
+// The rows of the per-token arrays that share prefix p: [first, first + return value); -1 if the
+// sequences or tokens that it names are out of range.
+__device__ __forceinline__ int shared_tokens(const AttendArgs& g, int p, int& first) {
+  const AttendPart& x = g.part;
+  const int s0 = x.cu_seqs ? x.cu_seqs[p] : 0, s1 = x.cu_seqs ? x.cu_seqs[p + 1] : x.seqs;
+  first = 0;
+  if (s0 < 0 || s1 < s0 || s1 > x.seqs) return -1;
+  long long n;
+  if (g.t.cu_tokens) {
+    first = g.t.cu_tokens[s0];
+    const int end = g.t.cu_tokens[s1];
+    if (first < 0 || end < first || end > g.t.tokens) return -1;
+    n = end - first;
+  } else {
+    first = s0 * x.max_tokens;
+    n = (long long)(s1 - s0) * x.max_tokens;
+  }
+  return n > x.max_shared ? -1 : (int)n;
+}
+
 template <int ROWS>
 __device__ __forceinline__ AttendUnit attend_unit(const AttendArgs& g, int id) {
   AttendUnit u;
   const int mt = id % g.mtiles, sl = id / g.mtiles;
   u.h = sl % g.c.kv_heads;
   u.s = sl / g.c.kv_heads;
-  u.n = tokens_of(g.t, u.s, u.first);
+  u.n = g.part.pass == 1 ? shared_tokens(g, u.s, u.first) : tokens_of(g.t, u.s, u.first);
   if (u.n < 0) {
     atomicOr(g.dev_status, NX_DEV_BAD_TOKENS);
     u.n = 0;
@@ -78,6 +109,33 @@ __device__ __forceinline__ AttendUnit attend_unit(const AttendArgs& g, int id) {
   u.end = u.rows ? row_limit(g, u, u.r0 + u.rows - 1) : 0;
   u.low = u.rows ? row_limit(g, u, u.r0) : 0;
   return u;
+}
+
+// Whether the prefixes' pass has something for the rows of a unit of sequences' own rows: its
+// sequence's prefix is the last that starts at or before it, if that one reaches so far and all of
+// the unit's tokens were among that one's.
+__device__ __forceinline__ bool part_joins(const AttendArgs& g, const AttendUnit& u) {
+  const AttendPart& x = g.part;
+  if (x.pass != 2 || u.n <= 0) return false;
+  int p = 0;
+  if (x.cu_seqs) {
+    for (int hi = x.prefixes; hi - p > 1;) {
+      const int mid = (p + hi) / 2;
+      if (x.cu_seqs[mid] <= u.s) p = mid;
+      else hi = mid;
+    }
+    if (x.cu_seqs[p] > u.s || x.cu_seqs[p + 1] <= u.s) return false;
+  }
+  int first;
+  const int n = shared_tokens(g, p, first);
+  return n >= 0 && u.first >= first && u.first + u.n <= first + n;
+}
+
+// Row r of a unit among all rows of the call.
+__device__ __forceinline__ long long part_row(const AttendArgs& g, const AttendUnit& u, int r) {
+  const int row = u.r0 + r;
+  return (long long)(u.first + row / g.c.group) * (g.c.kv_heads * g.c.group) +
+         u.h * g.c.group + row % g.c.group;
 }
 
 // A thread block's share of all tiles (up to 2^31 - 1): `per` of `total` from `start` to `stop`,
@@ -209,6 +267,16 @@ __device__ __forceinline__ void e4m3_pairs(uint32_t four, uint32_t& lo, uint32_t
       "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
       : "=r"(lo), "=r"(hi)
       : "r"(four));
+}
+
+// Two pieces of a row: what multiplies the sums of either, so that they add up; m becomes the
+// reference of both. Maxima of -infinity come with a sum of 0, or with NaN, which stays.
+__device__ __forceinline__ float2 join_by(float& m, float l, float2 other) {
+  const float top = fmaxf(m, other.x), ref = top == -INFINITY ? 0.f : top;
+  const float a = m == -INFINITY && l != l ? 1.f : ex2(m - ref);
+  const float b = other.x == -INFINITY && other.y != other.y ? 1.f : ex2(other.x - ref);
+  m = top;
+  return make_float2(a, b);
 }
 
 inline size_t round256(size_t x) { return (x + 255) / 256 * 256; }

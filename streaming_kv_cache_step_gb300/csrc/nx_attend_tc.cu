@@ -353,25 +353,48 @@ __device__ __forceinline__ void expand_tile(uint32_t raw, const float* scale, in
   }
 }
 
-// Where row r of a unit's output and its statistics go.
-__device__ __forceinline__ void store_row(const AttendArgs& g, const AttendUnit& u, int r, int D,
-                                          int d0, const float* x, int n, float f) {
+// Ends 32 features of row r: o / l to the output and, with the first of them, ln l; of the prefixes'
+// pass o, m and l as they are, which the own rows' pass takes in first (`joins`: it has some).
+__device__ __forceinline__ void finish_features(const AttendArgs& g, const AttendUnit& u, int r,
+                                                int D, int d0, float* o, float m, float l,
+                                                bool joins) {
+  const long long at = part_row(g, u, r);
+  if (g.part.pass == 1) {
+    float4* to = reinterpret_cast<float4*>(g.part.out + at * D + d0);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      to[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+    if (d0 == 0) g.part.stat[at] = make_float2(m, l);
+    return;
+  }
+  if (joins) {
+    const float2 other = g.part.stat[at], k = join_by(m, l, other);
+    const float4* from = reinterpret_cast<const float4*>(g.part.out + at * D + d0);
+    l = l * k.x + other.y * k.y;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float4 y = from[i];
+      o[4 * i] = o[4 * i] * k.x + y.x * k.y;
+      o[4 * i + 1] = o[4 * i + 1] * k.x + y.y * k.y;
+      o[4 * i + 2] = o[4 * i + 2] * k.x + y.z * k.y;
+      o[4 * i + 3] = o[4 * i + 3] * k.x + y.w * k.y;
+    }
+  }
+  const float f = l == 0.f ? 0.f : 1.f / l;
+  if (l == 0.f)
+#pragma unroll
+    for (int e = 0; e < 32; ++e) o[e] = 0.f;
   const int row = u.r0 + r;
   __nv_bfloat16* p = static_cast<__nv_bfloat16*>(g.a.out) +
                      (long long)(u.first + row / g.c.group) * g.a.out_stride +
                      ((long long)u.h * g.c.group + row % g.c.group) * D + d0;
-  for (int i = 0; i < n; i += 8)
+#pragma unroll
+  for (int i = 0; i < 32; i += 8)
     *reinterpret_cast<uint4*>(p + i) =
-        make_uint4(bf16_pair(x[i] * f, x[i + 1] * f), bf16_pair(x[i + 2] * f, x[i + 3] * f),
-                   bf16_pair(x[i + 4] * f, x[i + 5] * f), bf16_pair(x[i + 6] * f, x[i + 7] * f));
-}
-__device__ __forceinline__ void store_lse(const AttendArgs& g, const AttendUnit& u, int r, float m,
-                                          float l) {
-  if (!g.a.lse) return;
-  const int row = u.r0 + r;
-  g.a.lse[(long long)(u.first + row / g.c.group) * (g.c.kv_heads * g.c.group) +
-          u.h * g.c.group + row % g.c.group] =
-      l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+        make_uint4(bf16_pair(o[i] * f, o[i + 1] * f), bf16_pair(o[i + 2] * f, o[i + 3] * f),
+                   bf16_pair(o[i + 4] * f, o[i + 5] * f), bf16_pair(o[i + 6] * f, o[i + 7] * f));
+  if (d0 == 0 && g.a.lse)
+    g.a.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
 }
 
 template <int D, int NQ, bool IMAGE>
@@ -860,7 +883,7 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
             l = l * f0 + (count[1] ? s_l[r] * f1 : 0.f);
             m = nm;
           }
-          const float f = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+          const bool joins = whole && part_joins(g, u);
           const uint32_t* hot = s_hot[segment & 1];
           uint32_t any_hot = 0;
 #pragma unroll
@@ -887,10 +910,7 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
             // of 19 pieces took 13 us longer)
             if (whole ? rr < u.rows : !idle) {
               if (whole) {
-                if (l == 0.f)
-#pragma unroll
-                  for (int e = 0; e < 32; ++e) o[e] = 0.f;
-                store_row(g, u, rr, D, 32 * q, o, 32, f);
+                finish_features(g, u, rr, D, 32 * q, o, m, l, joins);
               } else {
 #pragma unroll
                 for (int e = 0; e < 32; ++e)
@@ -898,10 +918,7 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
               }
             }
           }
-          if (whole ? rr < u.rows : !idle) {
-            if (whole) store_lse(g, u, rr, m, l);
-            else g.ws.stat[piece * kTcRows + rr] = make_float2(m, l);
-          }
+          if (!whole && !idle) g.ws.stat[piece * kTcRows + rr] = make_float2(m, l);
         }
         // s_o lies over the ring, which the next piece's boxes fill by the other proxy
         if constexpr (NQ == 1 && !IMAGE) fence_async();
@@ -970,11 +987,7 @@ __global__ void __launch_bounds__(kTcRows) attend_tc_join_kernel(AttendArgs g) {
 #pragma unroll
     for (int e = 0; e < 32; ++e) o[e] = o[e] * f0 + p[e * kTcRows] * f1;
   }
-  if (l == 0.f)
-#pragma unroll
-    for (int e = 0; e < 32; ++e) o[e] = 0.f;
-  store_row(g, u, r, D, d0, o, 32, l == 0.f ? 0.f : 1.f / l);
-  if (d0 == 0) store_lse(g, u, r, m, l);
+  finish_features(g, u, r, D, d0, o, m, l, part_joins(g, u));
 }
 
 // Rows of head_dim bf16 values in boxes of 64 features x a page (or a tile); false if the

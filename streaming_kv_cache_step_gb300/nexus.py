@@ -24,6 +24,7 @@ NX_OK, NX_ERR_INVALID_ARG, NX_ERR_UNSUPPORTED, NX_ERR_CUDA = 0, 1, 2, 3
 NX_ERR_TIMEOUT, NX_ERR_WORKSPACE, NX_ERR_DEVICE_FAULT = 4, 5, 6
 NX_DEV_TIMEOUT, NX_DEV_BAD_LEN, NX_DEV_BAD_BUDGET, NX_DEV_BAD_PAGE = 1, 2, 4, 8
 NX_DEV_BAD_TOKENS, NX_DEV_FULL, NX_DEV_BAD_IMAGE = 16, 32, 64
+NX_DEV_NO_PAGES, NX_DEV_BAD_PROBS = 128, 256
 DTYPE_F32, DTYPE_BF16 = 0, 1
 MODE_RESERVOIR, MODE_TOPK = 0, 1
 
@@ -33,7 +34,9 @@ SYMBOLS = ("nexus_workspace_bytes", "nexus_direct_scores", "nexus_walk",
            "nexus_profile_next_call", "nexus_debug_force_simt", "nexus_debug_set_trace",
            "nexus_debug_scorer_config", "nexus_debug_scorer_layout", "kv_compact_noalloc",
            "nexus_last_scorer", "nexus_debug_compact_kernel", "nexus_append",
-           "nexus_append_image", "nexus_quantize", "nexus_attend_workspace_bytes", "nexus_attend")
+           "nexus_append_image", "nexus_quantize", "nexus_attend_workspace_bytes", "nexus_attend",
+           "nexus_attend_shared_workspace_bytes", "nexus_attend_shared", "nexus_plan",
+           "nexus_verify")
 SCORER_NONE, SCORER_TENSOR_CORE, SCORER_CUDA_CORE, SCORER_TENSOR_CORE_TWO_PASS = 0, 1, 2, 3
 
 
@@ -85,6 +88,30 @@ class CAttend(ctypes.Structure):
     _fields_ = [("q", ctypes.c_void_p), ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p),
                 ("q_stride", ctypes.c_int64), ("out_stride", ctypes.c_int64),
                 ("scale", ctypes.c_float), ("causal", ctypes.c_int32)]
+
+
+class CShared(ctypes.Structure):
+    _fields_ = [("prefix", ctypes.c_void_p), ("image", ctypes.c_void_p),
+                ("cu_seqs", ctypes.c_void_p), ("max_tokens", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class CPool(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in
+                ("block_table", "free_pages", "free_count", "held", "free_count_in", "held_in")]
+
+
+class CPlan(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in
+                ("new_tokens", "first_pos", "cu_tokens", "token_seq", "token_pos")] + [
+        ("tokens", ctypes.c_int32), ("max_tokens", ctypes.c_int32)]
+
+
+class CVerify(ctypes.Structure):
+    _fields_ = [("token", ctypes.c_void_p), ("p", ctypes.c_void_p), ("q", ctypes.c_void_p),
+                ("p_stride", ctypes.c_int64), ("q_stride", ctypes.c_int64)] + [
+        (n, ctypes.c_void_p) for n in ("u", "u_draw", "out", "emitted", "lens_in")] + [
+        (n, ctypes.c_int32) for n in ("vocab", "dtype", "reserved")]
 
 
 _lib = None
@@ -142,6 +169,13 @@ def load(path: str = LIB_PATH):
                 getattr(lib, name).restype = ctypes.c_int
             lib.nexus_attend_workspace_bytes.argtypes = [P, P]
             lib.nexus_attend_workspace_bytes.restype = ctypes.c_size_t
+            lib.nexus_attend_shared_workspace_bytes.argtypes = [P, P, P]
+            lib.nexus_attend_shared_workspace_bytes.restype = ctypes.c_size_t
+            lib.nexus_attend_shared.argtypes = [P, P, P, P, P, P, ctypes.c_size_t, P, P]
+            lib.nexus_plan.argtypes = [P, P, P, P, P, P]
+            lib.nexus_verify.argtypes = [P, P, P, P, P, P]
+            for name in ("nexus_attend_shared", "nexus_plan", "nexus_verify"):
+                getattr(lib, name).restype = ctypes.c_int
             _lib = lib
     return _lib
 
@@ -539,13 +573,7 @@ def alloc_attend_workspace(cache: Cache, *, tokens: int, max_tokens: int) -> tor
                        dtype=torch.uint8, device=cache.k.device)
 
 
-def attend(cache: Cache, layer: int, q, out, ws, dev_status, *, max_tokens: int, cu_tokens=None,
-           causal: bool = True, scale: float | None = None, lse=None, image: Image | None = None,
-           stream=None):
-    """nexus_attend: softmax attention of q [tokens, kv_heads * group, d] over the slices of
-    `layer`, into out (like q) and lse float32 [tokens, kv_heads * group] (optional). causal:
-    the tokens are the slices' newest rows, and each sees what came before it and itself.
-    scale: of the logits, 1 / sqrt(d) by default. image: read these 8-bit rows where held."""
+def _attend_args(cache: Cache, q, out, causal, scale, lse, ws) -> CAttend:
     n, HQ = q.shape[0], cache.kv_heads * cache.group
     a = CAttend(q=q.data_ptr(), out=out.data_ptr(), causal=bool(causal),
                 scale=cache.head_dim ** -0.5 if scale is None else scale)
@@ -557,9 +585,189 @@ def attend(cache: Cache, layer: int, q, out, ws, dev_status, *, max_tokens: int,
         a.lse = lse.data_ptr()
     if not ws.is_cuda:
         raise ValueError("ws must be on the GPU")
+    return a
+
+
+def attend(cache: Cache, layer: int, q, out, ws, dev_status, *, max_tokens: int, cu_tokens=None,
+           causal: bool = True, scale: float | None = None, lse=None, image: Image | None = None,
+           stream=None):
+    """nexus_attend: softmax attention of q [tokens, kv_heads * group, d] over the slices of
+    `layer`, into out (like q) and lse float32 [tokens, kv_heads * group] (optional). causal:
+    the tokens are the slices' newest rows, and each sees what came before it and itself.
+    scale: of the logits, 1 / sqrt(d) by default. image: read these 8-bit rows where held."""
+    n = q.shape[0]
+    a = _attend_args(cache, q, out, causal, scale, lse, ws)
     im = None if image is None else ctypes.byref(image.c_struct(cache))
     _check(load().nexus_attend(ctypes.byref(cache.c_struct()),
                                ctypes.byref(_tokens(cache, layer, n, max_tokens, cu_tokens)), im,
                                ctypes.byref(a), _ptr(ws), ws.numel(), _status(dev_status),
                                _stream(stream)),
            "nexus_attend")
+
+
+def _one_device(cache: Cache, **tensors):
+    """Calls go to the current device: everything they name must be there."""
+    here = torch.cuda.current_device()
+    for name, t in (("the cache", cache.k), *tensors.items()):
+        if t is not None and t.device.index != here:
+            raise ValueError(f"{name} must be on the current GPU")
+
+
+def _shared(cache: Cache, prefix: Cache, prefix_image, cu_seqs, max_shared: int):
+    """nx_shared, and what must live as long as it does."""
+    if cu_seqs is not None:
+        _int32(cu_seqs, prefix.seqs + 1, "cu_seqs")
+    c = prefix.c_struct()
+    im = None if prefix_image is None else prefix_image.c_struct(prefix)
+    x = CShared(prefix=ctypes.addressof(c), image=None if im is None else ctypes.addressof(im),
+                cu_seqs=None if cu_seqs is None else cu_seqs.data_ptr(), max_tokens=max_shared)
+    return x, (c, im)
+
+
+def attend_shared_workspace_bytes(cache: Cache, prefix: Cache, *, tokens: int, max_tokens: int,
+                                  max_shared: int) -> int:
+    # as above: any non-null cu_tokens and cu_seqs will do
+    t = CTokens(0, tokens, max_tokens, 0, cache.lens.data_ptr())
+    x, _keep = _shared(cache, prefix, None, None, max_shared)
+    x.cu_seqs = prefix.lens.data_ptr()
+    n = load().nexus_attend_shared_workspace_bytes(ctypes.byref(cache.c_struct()),
+                                                   ctypes.byref(t), ctypes.byref(x))
+    if n == 0:
+        raise NexusError(NX_ERR_INVALID_ARG, "nexus_attend_shared_workspace_bytes")
+    return int(n)
+
+
+def alloc_attend_shared_workspace(cache: Cache, prefix: Cache, *, tokens: int, max_tokens: int,
+                                  max_shared: int) -> torch.Tensor:
+    return torch.empty(attend_shared_workspace_bytes(cache, prefix, tokens=tokens,
+                                                     max_tokens=max_tokens, max_shared=max_shared),
+                       dtype=torch.uint8, device=cache.k.device)
+
+
+def attend_shared(cache: Cache, layer: int, q, out, ws, dev_status, *, prefix: Cache,
+                  max_tokens: int, max_shared: int, cu_seqs=None, cu_tokens=None,
+                  causal: bool = True, scale: float | None = None, lse=None,
+                  image: Image | None = None, prefix_image: Image | None = None, stream=None):
+    """nexus_attend_shared: attend, over the rows of a prefix that several sequences share and the
+    sequence's own rows behind them. prefix: a cache whose "sequences" are the prefixes; prefix i
+    is shared by sequences cu_seqs[i] .. cu_seqs[i + 1] - 1 (int32 [prefix.seqs + 1], or None where
+    all share the only one); max_shared: no prefix is shared by more of the new tokens. The rest is
+    as in attend; prefix_image: an 8-bit image of the prefix cache."""
+    n = q.shape[0]
+    _one_device(cache, q=q, out=out, ws=ws, dev_status=dev_status, lse=lse, cu_seqs=cu_seqs,
+                cu_tokens=cu_tokens, prefix=prefix.k)
+    a = _attend_args(cache, q, out, causal, scale, lse, ws)
+    x, _keep = _shared(cache, prefix, prefix_image, cu_seqs, max_shared)
+    im = None if image is None else ctypes.byref(image.c_struct(cache))
+    _check(load().nexus_attend_shared(ctypes.byref(cache.c_struct()),
+                                      ctypes.byref(_tokens(cache, layer, n, max_tokens, cu_tokens)),
+                                      im, ctypes.byref(x), ctypes.byref(a), _ptr(ws), ws.numel(),
+                                      _status(dev_status), _stream(stream)),
+           "nexus_attend_shared")
+
+
+# ---------------------------------------------------------------------------
+# Around a step: the next batch, and drafted tokens
+# ---------------------------------------------------------------------------
+
+@dataclass
+class Pool:
+    """Pages of a paged cache (nx_pool), int32: the free ones, how many they are [1], and how many
+    each sequence holds [seqs]."""
+    free_pages: torch.Tensor
+    free_count: torch.Tensor
+    held: torch.Tensor
+
+
+def new_pool(cache: Cache) -> Pool:
+    """A pool whose pages are all free (page 0 is dealt out first)."""
+    dev = cache.k.device
+    return Pool(free_pages=torch.arange(cache.num_pages - 1, -1, -1, dtype=torch.int32, device=dev),
+                free_count=torch.full((1,), cache.num_pages, dtype=torch.int32, device=dev),
+                held=torch.zeros(cache.seqs, dtype=torch.int32, device=dev))
+
+
+def plan(cache: Cache, pool: Pool | None, new_tokens, cu_tokens, dev_status, *, max_tokens: int,
+         tokens: int | None = None, token_seq=None, token_pos=None, first_pos=None,
+         image: Image | None = None, held_in=None, free_count_in=None, stream=None):
+    """nexus_plan: gives back pages that sequences no longer need, deals out those that their
+    new_tokens (int32 [seqs]; negative: the sequence ends) take, and lays the tokens out: cu_tokens
+    int32 [seqs + 1], token_seq and token_pos (from first_pos int32 [seqs]) of each token. tokens:
+    rows of the per-token arrays, by default token_seq's or token_pos's. pool: None for a contiguous
+    cache. image: forgets sequences that end. held_in, free_count_in: what the pool held before
+    the call, if not pool.held and pool.free_count."""
+    S = cache.seqs
+    _int32(new_tokens, S, "new_tokens")
+    _int32(cu_tokens, S + 1, "cu_tokens")
+    if tokens is None:
+        if token_seq is None and token_pos is None:
+            raise ValueError("tokens is needed without token_seq and token_pos")
+        tokens = (token_seq if token_pos is None else token_pos).numel()
+    a = CPlan(new_tokens=new_tokens.data_ptr(), cu_tokens=cu_tokens.data_ptr(), tokens=tokens,
+              max_tokens=max_tokens)
+    for name, t, n in (("token_seq", token_seq, tokens), ("token_pos", token_pos, tokens),
+                       ("first_pos", first_pos, S)):
+        if t is not None:
+            _int32(t, n, name)
+            setattr(a, name, t.data_ptr())
+    c = None
+    if pool is not None:
+        _int32(pool.free_pages, cache.num_pages, "free_pages")
+        _int32(pool.free_count, 1, "free_count")
+        _int32(pool.held, S, "held")
+        _int32(cache.block_table, S * cache.max_pages_per_seq, "block_table")
+        c = CPool(block_table=cache.block_table.data_ptr(), free_pages=pool.free_pages.data_ptr(),
+                  free_count=pool.free_count.data_ptr(), held=pool.held.data_ptr())
+        if held_in is not None:
+            _int32(held_in, S, "held_in")
+            c.held_in = held_in.data_ptr()
+        if free_count_in is not None:
+            _int32(free_count_in, 1, "free_count_in")
+            c.free_count_in = free_count_in.data_ptr()
+    elif held_in is not None or free_count_in is not None:
+        raise ValueError("held_in and free_count_in go with a pool")
+    _one_device(cache, new_tokens=new_tokens, cu_tokens=cu_tokens, dev_status=dev_status)
+    im = None if image is None else ctypes.byref(image.c_struct(cache))
+    _check(load().nexus_plan(ctypes.byref(cache.c_struct()),
+                             None if c is None else ctypes.byref(c), ctypes.byref(a), im,
+                             _status(dev_status), _stream(stream)),
+           "nexus_plan")
+
+
+def verify(cache: Cache, token, p, u, u_draw, out, emitted, dev_status, *, max_tokens: int,
+           cu_tokens=None, q=None, lens_in=None, image: Image | None = None, stream=None):
+    """nexus_verify: which drafts stay, the token behind them, and the cache without the others.
+    token int32 [tokens]: of each sequence the last token known, then its drafts; p [tokens, vocab]
+    (float32 or bfloat16, rows any distance apart): the model's distribution behind each; q: row i
+    is what draft i + 1 was drawn from (None: drafts that were not drawn). u float32 [tokens] and
+    u_draw float32 [seqs]: uniform in [0, 1). out int32 [tokens]: the kept drafts, the new token,
+    then -1; emitted int32 [seqs]: how many of them. lens_in int32 [layers, seqs, kv_heads]: rows
+    that the slices held, if not cache.lens. image: forgets the rows taken back."""
+    n, S = token.numel(), cache.seqs
+    _int32(token, n, "token")
+    _int32(out, n, "out")
+    _int32(emitted, S, "emitted")
+    for name, t, m in (("u", u, n), ("u_draw", u_draw, S)):
+        if t.dtype != torch.float32 or not t.is_cuda or not t.is_contiguous() or t.numel() != m:
+            raise ValueError(f"{name} must be {m} contiguous float32 values on the GPU")
+    if p.dim() != 2 or p.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("p must be [tokens, vocab], float32 or bfloat16")
+    for name, t in (("p", p), ("q", q)):
+        if t is not None and (t.shape != (n, p.shape[1]) or t.dtype != p.dtype or not t.is_cuda or
+                              (t.stride(1) != 1 and t.shape[1] > 1)):
+            raise ValueError(f"{name} must be [tokens, vocab] like p on the GPU, rows contiguous")
+    a = CVerify(token=token.data_ptr(), p=p.data_ptr(), p_stride=p.stride(0), u=u.data_ptr(),
+                u_draw=u_draw.data_ptr(), out=out.data_ptr(), emitted=emitted.data_ptr(),
+                vocab=p.shape[1],
+                dtype=DTYPE_BF16 if p.dtype == torch.bfloat16 else DTYPE_F32)
+    if q is not None:
+        a.q, a.q_stride = q.data_ptr(), q.stride(0)
+    if lens_in is not None:
+        _int32(lens_in, cache.n_slices, "lens_in")
+        a.lens_in = lens_in.data_ptr()
+    _one_device(cache, token=token, p=p, q=q, u=u, out=out, emitted=emitted, dev_status=dev_status)
+    im = None if image is None else ctypes.byref(image.c_struct(cache))
+    _check(load().nexus_verify(ctypes.byref(cache.c_struct()),
+                               ctypes.byref(_tokens(cache, 0, n, max_tokens, cu_tokens)),
+                               ctypes.byref(a), im, _status(dev_status), _stream(stream)),
+           "nexus_verify")
