@@ -903,7 +903,7 @@ __global__ void __launch_bounds__(kWarps * 32, Ring<KIND, D, ROWS>::kPerSm)
   __shared__ Meta s_meta[kWarps][R::kDeep];
   __shared__ float s_m[kWarps][ROWS], s_l[kWarps][ROWS];
   __shared__ float s_pm[ROWS], s_pl[ROWS];              // of the block's piece
-  grid_dep_wait();
+  begin_pass(g);
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const int b = blockIdx.x;
   const uint32_t ring = smem_at(s_ring) + warp * kRing;
@@ -925,7 +925,10 @@ __global__ void __launch_bounds__(kWarps * 32, Ring<KIND, D, ROWS>::kPerSm)
         g, [&](int i) { return unit_tiles<KIND>(attend_unit<ROWS>(g, i)); });
     grid_dep_trigger();
     if (tid == 0 && !g.splits) g.ws.desc[b] = make_int2(-1, 0);
-    if (sh.start >= sh.total) return;
+    if (sh.start >= sh.total) {
+      meet_pass(g);
+      return;
+    }
     per = sh.per;
     stop = sh.stop;
     unit = sh.unit;
@@ -990,6 +993,7 @@ __global__ void __launch_bounds__(kWarps * 32, Ring<KIND, D, ROWS>::kPerSm)
         }
       __syncthreads();
       const bool whole = a0 == 0 && a1 == tiles, joins = whole && part_joins(g, u);
+      if (whole) meet_pass(g);
       const int slot = 2 * b + (a0 == 0 ? 1 : 0);
       for (int i = tid; i < u.rows * D; i += kWarps * 32) {
         const int r = i / D, f = i % D;
@@ -1031,6 +1035,7 @@ __global__ void __launch_bounds__(kWarps * 32, Ring<KIND, D, ROWS>::kPerSm)
     cluster_sync();
     const AttendUnit u = attend_unit<ROWS>(g, b / g.ranks);
     const bool joins = part_joins(g, u);
+    meet_pass(g);
     for (int i = b % g.ranks * (kWarps * 32) + tid; i < u.rows * D; i += g.ranks * kWarps * 32) {
       const int r = i / D, f = i % D;
       float m[kRanks], z[kRanks], x[kRanks], top = -INFINITY, l = 0.f, o = 0.f;
@@ -1056,6 +1061,7 @@ __global__ void __launch_bounds__(kWarps * 32, Ring<KIND, D, ROWS>::kPerSm)
     }
     cluster_sync();                                     // nobody reads this block any more
   }
+  meet_pass(g);
 }
 
 // Joins the pieces of a unit that starts in a block b and ends in a later one. Few units, each of
@@ -1067,6 +1073,7 @@ template <int KIND, int D, int ROWS>
 __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(AttendArgs g) {
   constexpr int E = D / 32;
   __shared__ float s_o[kJoinWarps][D], s_m[kJoinWarps], s_l[kJoinWarps];
+  if (g.part.pass == 1) grid_dep_trigger();
   grid_dep_wait();
   const int splits = max(g.splits, 1), split = blockIdx.x % splits;
   int b = blockIdx.x / splits, unit = b;
@@ -1164,6 +1171,9 @@ cudaError_t launch_attend(AttendArgs& g, cudaStream_t st, int* launches) {
   if (g.c.capacity <= (units * kRanks <= 2 * kSms ? few / 2 : few)) ranks = 1;
   const int limit = ranks > 1 ? ranks * most_of : units >= fit ? 2 * few : few;
   g.ranks = g.c.capacity <= limit ? ranks : 0;
+#ifdef OWN_EVEN
+  g.ranks = 0;
+#endif
   g.splits = 0;
   if (units * 2 <= kSms)
     for (g.splits = ROWS; g.splits > 1 && units * g.splits > kSms;) g.splits /= 2;
@@ -1190,10 +1200,18 @@ cudaError_t launch_attend(AttendArgs& g, cudaStream_t st, int* launches) {
   return e;
 }
 
+#ifndef SHROWS
+#define SHROWS 0
+#endif
+bool tc_takes(const AttendArgs& g) {
+  if (SHROWS && g.part.pass == 1) return g.c.dtype == NX_DTYPE_BF16 && most_tokens(g.t) * g.c.group > SHROWS;
+  return attend_tc_takes(g.c, g.t, g.im.k != nullptr);
+}
+
 template <int D>
 cudaError_t launch_attend(AttendArgs& g, cudaStream_t st, int* launches) {
   if (g.c.dtype == NX_DTYPE_F32) return launch_attend<kF32, D, 8>(g, st, launches);
-  if (attend_tc_takes(g.c, g.t, g.im.k != nullptr)) return launch_attend_tc(g, st, launches);
+  if (tc_takes(g)) return launch_attend_tc(g, st, launches);
   const bool few = most_tokens(g.t) * g.c.group <= 8;
   if (g.im.k)
     return few ? launch_attend<kImage, D, 8>(g, st, launches)
@@ -1254,7 +1272,7 @@ cudaError_t attend_pass(const nx_cache& c, const nx_tokens& t, const nx_image* i
   g.a = a;
   g.part = part;
   g.dev_status = dev_status;
-  if (attend_tc_takes(c, t, image != nullptr)) attend_tc_layout(c.head_dim, ws, &g.ws);
+  if (tc_takes(g)) attend_tc_layout(c.head_dim, ws, &g.ws);
   else attend_layout(c.head_dim, ws, &g.ws);
   g.b = image_block(c);
   while (1 << g.b_shift < g.b) ++g.b_shift;

@@ -131,6 +131,18 @@ __device__ __forceinline__ bool part_joins(const AttendArgs& g, const AttendUnit
   return n >= 0 && u.first >= first && u.first + u.n <= first + n;
 }
 
+// The two passes overlap: the kernels of the prefixes' let the next one be scheduled as soon as what
+// came before the call is done, and the own rows' pass needs them only where a row is finished. Every
+// one of its thread blocks waits for them before it ends, so that when it is done they are.
+__device__ __forceinline__ void begin_pass(const AttendArgs& g) {
+  if (g.part.pass == 2) return;
+  grid_dep_wait();
+  if (g.part.pass == 1) grid_dep_trigger();
+}
+__device__ __forceinline__ void meet_pass(const AttendArgs& g) {
+  if (g.part.pass == 2) grid_dep_wait();
+}
+
 // Row r of a unit among all rows of the call.
 __device__ __forceinline__ long long part_row(const AttendArgs& g, const AttendUnit& u, int r) {
   const int row = u.r0 + r;

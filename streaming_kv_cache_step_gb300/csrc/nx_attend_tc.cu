@@ -353,8 +353,9 @@ __device__ __forceinline__ void expand_tile(uint32_t raw, const float* scale, in
   }
 }
 
-// Ends 32 features of row r: o / l to the output and, with the first of them, ln l; of the prefixes'
+// Ends N features of row r: o / l to the output and, with the first of them, ln l; of the prefixes'
 // pass o, m and l as they are, which the own rows' pass takes in first (`joins`: it has some).
+template <int N>
 __device__ __forceinline__ void finish_features(const AttendArgs& g, const AttendUnit& u, int r,
                                                 int D, int d0, float* o, float m, float l,
                                                 bool joins) {
@@ -362,7 +363,7 @@ __device__ __forceinline__ void finish_features(const AttendArgs& g, const Atten
   if (g.part.pass == 1) {
     float4* to = reinterpret_cast<float4*>(g.part.out + at * D + d0);
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < N / 4; ++i)
       to[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
     if (d0 == 0) g.part.stat[at] = make_float2(m, l);
     return;
@@ -372,7 +373,7 @@ __device__ __forceinline__ void finish_features(const AttendArgs& g, const Atten
     const float4* from = reinterpret_cast<const float4*>(g.part.out + at * D + d0);
     l = l * k.x + other.y * k.y;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < N / 4; ++i) {
       const float4 y = from[i];
       o[4 * i] = o[4 * i] * k.x + y.x * k.y;
       o[4 * i + 1] = o[4 * i + 1] * k.x + y.y * k.y;
@@ -383,13 +384,13 @@ __device__ __forceinline__ void finish_features(const AttendArgs& g, const Atten
   const float f = l == 0.f ? 0.f : 1.f / l;
   if (l == 0.f)
 #pragma unroll
-    for (int e = 0; e < 32; ++e) o[e] = 0.f;
+    for (int e = 0; e < N; ++e) o[e] = 0.f;
   const int row = u.r0 + r;
   __nv_bfloat16* p = static_cast<__nv_bfloat16*>(g.a.out) +
                      (long long)(u.first + row / g.c.group) * g.a.out_stride +
                      ((long long)u.h * g.c.group + row % g.c.group) * D + d0;
 #pragma unroll
-  for (int i = 0; i < 32; i += 8)
+  for (int i = 0; i < N; i += 8)
     *reinterpret_cast<uint4*>(p + i) =
         make_uint4(bf16_pair(o[i] * f, o[i + 1] * f), bf16_pair(o[i + 2] * f, o[i + 3] * f),
                    bf16_pair(o[i + 4] * f, o[i + 5] * f), bf16_pair(o[i + 6] * f, o[i + 7] * f));
@@ -448,7 +449,7 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
     s_up = 0;
   }
   if (tid < 16) s_hot[tid / 8][tid % 8] = 0;
-  grid_dep_wait();
+  begin_pass(g);
   tc_before();
   const AttendShare sh = attend_share<kThreads>(
       g, [&](int i) { return tc_tiles<NQ>(attend_unit<kRows * NQ>(g, i)); });
@@ -884,6 +885,7 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
             m = nm;
           }
           const bool joins = whole && part_joins(g, u);
+          if (whole) meet_pass(g);
           const uint32_t* hot = s_hot[segment & 1];
           uint32_t any_hot = 0;
 #pragma unroll
@@ -910,7 +912,7 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
             // of 19 pieces took 13 us longer)
             if (whole ? rr < u.rows : !idle) {
               if (whole) {
-                finish_features(g, u, rr, D, 32 * q, o, m, l, joins);
+                finish_features<32>(g, u, rr, D, 32 * q, o, m, l, joins);
               } else {
 #pragma unroll
                 for (int e = 0; e < 32; ++e)
@@ -940,6 +942,7 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
     ++unit;
   }
   if (tid == 0) g.ws.desc[b] = desc;
+  meet_pass(g);
   asm volatile("cp.async.wait_all;" ::: "memory");
   tc_before();
   __syncthreads();
@@ -964,30 +967,50 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
 }
 
 // Joins the pieces of the unit that starts in block blockIdx.x and ends in a later one:
-// 32 features of it, a thread per row.
+// kJoinCols features of it, a thread per row. Units can be few and of many pieces (64 tokens over 8
+// slices: 8 of 19), so a block has few features, and the loads of kJoinAhead pieces are under way at
+// once (with 32 features a block and a piece at a time 62 us for those, of which now XX).
+constexpr int kJoinCols = 8, kJoinAhead = 4;
 template <int D, int NQ>
 __global__ void __launch_bounds__(kTcRows) attend_tc_join_kernel(AttendArgs g) {
+  if (g.part.pass == 1) grid_dep_trigger();
   grid_dep_wait();
-  const int b = blockIdx.x, d0 = blockIdx.y * 32, r = threadIdx.x;
+  const int b = blockIdx.x, d0 = blockIdx.y * kJoinCols, r = threadIdx.x;
   const int2 desc = g.ws.desc[b];
   if (desc.x < 0) return;
   const AttendUnit u = attend_unit<kRows * NQ>(g, desc.x);
   if (r >= u.rows) return;
-  float m = -INFINITY, l = 0.f, o[32];
+  const bool joins = part_joins(g, u);
+  float m = -INFINITY, l = 0.f, o[kJoinCols];
 #pragma unroll
-  for (int e = 0; e < 32; ++e) o[e] = 0.f;
-  for (int i = b; i <= desc.y; ++i) {
-    const int piece = i == b ? 2 * b + 1 : 2 * i;
-    const float2 x = g.ws.stat[piece * kTcRows + r];
-    const float nm = fmaxf(m, x.x), ref = nm == -INFINITY ? 0.f : nm;
-    const float f0 = ex2(m - ref), f1 = x.x == -INFINITY && x.y != x.y ? 1.f : ex2(x.x - ref);
-    l = l * f0 + x.y * f1;
-    m = nm;
-    const float* p = g.ws.out + ((long long)piece * D + d0) * kTcRows + r;
+  for (int e = 0; e < kJoinCols; ++e) o[e] = 0.f;
+#pragma unroll 1
+  for (int i0 = b; i0 <= desc.y; i0 += kJoinAhead) {
+    float2 x[kJoinAhead];
+    float y[kJoinAhead][kJoinCols];
 #pragma unroll
-    for (int e = 0; e < 32; ++e) o[e] = o[e] * f0 + p[e * kTcRows] * f1;
+    for (int a = 0; a < kJoinAhead; ++a) {
+      const int i = i0 + a;
+      if (i > desc.y) continue;
+      const int piece = i == b ? 2 * b + 1 : 2 * i;
+      x[a] = g.ws.stat[piece * kTcRows + r];
+      const float* p = g.ws.out + ((long long)piece * D + d0) * kTcRows + r;
+#pragma unroll
+      for (int e = 0; e < kJoinCols; ++e) y[a][e] = p[e * kTcRows];
+    }
+#pragma unroll
+    for (int a = 0; a < kJoinAhead; ++a) {
+      if (i0 + a > desc.y) continue;
+      const float nm = fmaxf(m, x[a].x), ref = nm == -INFINITY ? 0.f : nm;
+      const float f0 = ex2(m - ref);
+      const float f1 = x[a].x == -INFINITY && x[a].y != x[a].y ? 1.f : ex2(x[a].x - ref);
+      l = l * f0 + x[a].y * f1;
+      m = nm;
+#pragma unroll
+      for (int e = 0; e < kJoinCols; ++e) o[e] = o[e] * f0 + y[a][e] * f1;
+    }
   }
-  finish_features(g, u, r, D, d0, o, m, l, part_joins(g, u));
+  finish_features<kJoinCols>(g, u, r, D, d0, o, m, l, joins);
 }
 
 // Rows of head_dim bf16 values in boxes of 64 features x a page (or a tile); false if the
@@ -1033,7 +1056,7 @@ cudaError_t launch_t(AttendArgs& g, cudaStream_t st, int* launches) {
                    dim3(Plan<D, NQ, IMAGE>::kThreads), smem, st, map_k, map_v, maps, g);
   if (e != cudaSuccess) return e;
   note_launch(st, launches, "attend_tc");
-  e = launch_after(attend_tc_join_kernel<D, NQ>, dim3(grid, D / 32), dim3(kTcRows), 0, st, g);
+  e = launch_after(attend_tc_join_kernel<D, NQ>, dim3(grid, D / kJoinCols), dim3(kTcRows), 0, st, g);
   if (e == cudaSuccess) note_launch(st, launches, "attend_tc_join");
   return e;
 }

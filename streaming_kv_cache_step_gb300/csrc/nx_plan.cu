@@ -7,17 +7,14 @@
 // search in the sums and moves by itself. One cluster of eight thread blocks does it all in one
 // launch: the lengths of all slices, its largest read, are reduced by a warp per sequence and
 // pushed to all blocks; the sums are then worked out by every block for itself (S values from its
-// shared memory: cheaper than asking another); a cluster barrier stands between the pages given
-// back and those taken, which may be the same.
+// shared memory: cheaper than asking another); where pages are both given back and taken, which may
+// be the same ones, a cluster barrier stands between.
 #include "nx_internal.cuh"
 
 namespace nx {
 namespace {
 
-constexpr int kPlanThreads = 1024;
-constexpr int kPlanWarps = kPlanThreads / 32;
 constexpr int kPlanRanks = 8;         // thread blocks, one cluster (the portable limit)
-constexpr int kPlanStep = kPlanRanks * kPlanThreads;
 
 struct PlanArgs {
   nx_cache c;
@@ -29,26 +26,37 @@ struct PlanArgs {
   int shift;            // log2 page_size
 };
 
-// Sums over all threads' values of what comes before this thread's; total: of all.
-__device__ __forceinline__ long long block_before(long long x, long long* s_sum, long long& total) {
+// The running sums over sequences: tokens, pages given back, pages taken.
+struct Sums {
+  long long v[3];
+};
+// What the threads before this one have, and what all have.
+template <int WARPS>
+__device__ __forceinline__ Sums block_before(const Sums& x, Sums* s_sum, Sums& total) {
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  long long incl = x;
+  Sums incl = x, before;
 #pragma unroll
-  for (int o = 1; o < 32; o *= 2) {
-    const long long y = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += y;
-  }
+  for (int o = 1; o < 32; o *= 2)
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      const long long y = __shfl_up_sync(0xffffffffu, incl.v[i], o);
+      if (lane >= o) incl.v[i] += y;
+    }
   __syncthreads();                       // the sums before are read
   if (lane == 31) s_sum[warp] = incl;
   __syncthreads();
-  long long w = s_sum[lane], before = lane < warp ? w : 0;
 #pragma unroll
-  for (int o = 16; o; o /= 2) {
-    w += __shfl_xor_sync(0xffffffffu, w, o);
-    before += __shfl_xor_sync(0xffffffffu, before, o);
+  for (int i = 0; i < 3; ++i) {
+    long long w = lane < WARPS ? s_sum[lane].v[i] : 0, b = lane < warp ? w : 0;
+#pragma unroll
+    for (int o = 16; o; o /= 2) {
+      w += __shfl_xor_sync(0xffffffffu, w, o);
+      b += __shfl_xor_sync(0xffffffffu, b, o);
+    }
+    total.v[i] = w;
+    before.v[i] = b + incl.v[i] - x.v[i];
   }
-  total = w;
-  return before + incl - x;
+  return before;
 }
 
 // The sequence whose share of a running sum holds place i: the last s with at[s] <= i.
@@ -73,122 +81,128 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive;\n\tbarrier.cluster.wait;" ::: "memory");
 }
 
+template <int kPlanThreads>
 __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const __grid_constant__ PlanArgs g) {
+  constexpr int kPlanWarps = kPlanThreads / 32, kPlanStep = kPlanRanks * kPlanThreads;
   extern __shared__ int s_mem[];
-  __shared__ long long s_sum[kPlanWarps];
+  __shared__ Sums s_sum[kPlanWarps];
   const int S = g.c.seqs, H = g.c.kv_heads, per = g.c.layers * H;
   int* s_rows = s_mem;                   // rows of the longest slice (-1: a bad one), then pages
-  int* s_held = s_rows + S;              // pages held before
-  int* s_cu = s_held + S;                // the running sums: tokens,
-  int* s_give = s_cu + S;                // pages given back,
+  int* s_new = s_rows + S;               // tokens asked for
+  int* s_held = s_new + S;               // pages held before
+  int* s_cu = s_held + S;                // tokens granted (-1: refused); then the running sums:
+  int* s_give = s_cu + S;                // tokens, pages given back,
   int* s_take = s_give + S;              // pages taken
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, rank = blockIdx.x;
   const int all = rank * kPlanThreads + tid;
-  const bool lead = rank == 0;
+  const bool lead = rank == 0, paged = g.p.held != nullptr;
   grid_dep_wait();
-  cluster_sync();                        // every block's shared memory is there
-  // ---- rows ----
+  // pushes must find the other blocks running; the inputs come meanwhile
+  asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
+  for (int s = tid; s < S; s += kPlanThreads) {
+    s_new[s] = g.a.new_tokens[s];
+    s_held[s] = paged ? g.held_in[s] : 0;
+  }
+  int free_before = paged ? *g.free_in : 0;
+  bool pushed = false;
   for (int s = rank * kPlanWarps + warp; s < S; s += kPlanRanks * kPlanWarps) {
     int most = 0, least = 0;
-    if (g.a.new_tokens[s] >= 0) {        // (the lengths of one that ends do not matter)
 #pragma unroll 8
-      for (int i = lane; i < per; i += 32) {
-        const int l = i / H, len = g.c.lens[((long long)l * S + s) * H + (i - l * H)];
-        most = max(most, len);
-        least = min(least, len);
-      }
-      most = __reduce_max_sync(0xffffffffu, most);
-      least = __reduce_min_sync(0xffffffffu, least);
+    for (int i = lane; i < per; i += 32) {
+      const int l = i / H, len = g.c.lens[((long long)l * S + s) * H + (i - l * H)];
+      most = max(most, len);
+      least = min(least, len);
     }
+    most = __reduce_max_sync(0xffffffffu, most);
+    least = __reduce_min_sync(0xffffffffu, least);
+    if (!pushed) asm volatile("barrier.cluster.wait;" ::: "memory");
+    pushed = true;
     if (lane < kPlanRanks) push(&s_rows[s], lane, least < 0 || most > g.c.capacity ? -1 : most);
   }
-  int free_before = g.p.held ? *g.free_in : 0;
-  cluster_sync();
+  if (!pushed) asm volatile("barrier.cluster.wait;" ::: "memory");
+  cluster_sync();                        // all lengths are there, and all inputs are read
   // ---- what each sequence gets: a run of sequences to each thread ----
   const int run = (S + kPlanThreads - 1) / kPlanThreads;
   const int s0 = min(S, tid * run), s1 = min(S, s0 + run);
-  // A refused sequence brings no tokens and keeps its pages: s_cu holds -1 for now.
-  long long total, sum = 0;
+  Sums x = {}, total;
   for (int s = s0; s < s1; ++s) {
-    int n = g.a.new_tokens[s], flag = 0;
-    const int held = g.p.held ? g.held_in[s] : 0, rows = s_rows[s];
-    if (held < 0 || (g.p.held && held > g.c.max_pages_per_seq)) flag = NX_DEV_BAD_PAGE;
+    const int held = s_held[s], asked = s_new[s], n = max(asked, 0);
+    const int rows = asked < 0 ? 0 : s_rows[s];    // (the lengths of one that ends do not matter)
+    int flag = 0;
+    if (held < 0 || (paged && held > g.c.max_pages_per_seq)) flag = NX_DEV_BAD_PAGE;
     else if (rows < 0) flag = NX_DEV_BAD_LEN;
     else if (n > g.a.max_tokens) flag = NX_DEV_BAD_TOKENS;
     else if (n > g.c.capacity - rows) flag = NX_DEV_FULL;
     if (flag && lead) atomicOr(g.dev_status, flag);
-    n = max(n, 0);
-    s_held[s] = held;
     s_cu[s] = flag ? -1 : n;
-    if (!flag) sum += n;
-    if (g.p.held) s_rows[s] = flag ? held : (rows + n + (1 << g.shift) - 1) >> g.shift;
+    const int need = flag ? held : paged ? (rows + n + (1 << g.shift) - 1) >> g.shift : 0;
+    s_rows[s] = need;
+    x.v[0] += flag ? 0 : n;
+    x.v[1] += max(0, held - need);
+    x.v[2] += max(0, need - held);
   }
-  long long before = block_before(sum, s_sum, total);
-  const bool crowded = total > g.a.tokens;
-  long long give = 0, take = 0;
-  for (int s = s0; s < s1; ++s) {
-    if (crowded && s_cu[s] > 0) {
-      before += s_cu[s];
-      if (before > g.a.tokens) {
-        if (lead) atomicOr(g.dev_status, NX_DEV_BAD_TOKENS);
-        s_cu[s] = -1;
-        s_rows[s] = s_held[s];
+  Sums before = block_before<kPlanWarps>(x, s_sum, total);
+  if (paged && (free_before < 0 || free_before > g.c.num_pages)) {
+    if (lead && tid == 0) atomicOr(g.dev_status, NX_DEV_BAD_PAGE);
+    free_before = 0;
+  }
+  // Mostly there is room for all. If not, once more without those that the arrays have no room for,
+  // then without those that the pool has no pages for: in order, so that who would need more than
+  // are left waits, and whoever wants any behind.
+  if (total.v[0] > g.a.tokens) {
+    x = {};
+    for (int s = s0; s < s1; ++s) {
+      if (s_cu[s] > 0) {
+        before.v[0] += s_cu[s];
+        if (before.v[0] > g.a.tokens) {
+          if (lead) atomicOr(g.dev_status, NX_DEV_BAD_TOKENS);
+          s_cu[s] = -1;
+          s_rows[s] = s_held[s];
+        }
       }
+      x.v[0] += max(0, s_cu[s]);
+      x.v[1] += max(0, s_held[s] - s_rows[s]);
+      x.v[2] += max(0, s_rows[s] - s_held[s]);
     }
-    if (g.p.held) {
-      give += max(0, s_held[s] - s_rows[s]);
-      take += max(0, s_rows[s] - s_held[s]);
-    }
+    before = block_before<kPlanWarps>(x, s_sum, total);
   }
-  int given = 0, taken = 0, top = 0;
-  if (g.p.held) {
-    if (free_before < 0 || free_before > g.c.num_pages) {
+  int given = 0, top = 0;
+  if (paged) {
+    if (total.v[1] > g.c.num_pages - free_before) {     // more pages than there are
       if (lead && tid == 0) atomicOr(g.dev_status, NX_DEV_BAD_PAGE);
-      free_before = 0;
+      total.v[1] = g.c.num_pages - free_before;
     }
-    long long gives, takes;
-    give = block_before(give, s_sum, gives);
-    if (gives > g.c.num_pages - free_before) {   // more pages than there are
-      if (lead && tid == 0) atomicOr(g.dev_status, NX_DEV_BAD_PAGE);
-      gives = g.c.num_pages - free_before;
-    }
-    given = (int)gives;
+    given = (int)total.v[1];
     top = free_before + given;
-    take = block_before(take, s_sum, takes);
-    // pages are dealt out in order: who would need more than are left waits, and whoever takes
-    // any behind
-    const bool short_of = takes > top;
-    long long mine = 0;
-    for (int s = s0; s < s1; ++s) {
-      const int more = s_rows[s] - s_held[s];
-      s_give[s] = (int)min(give, (long long)given);
-      give += max(0, -more);
-      if (more <= 0) continue;
-      take += more;
-      if (short_of && take > top) {
-        if (lead) atomicOr(g.dev_status, NX_DEV_NO_PAGES);
-        s_cu[s] = -1;
-        s_rows[s] = s_held[s];
-      } else {
-        mine += more;
+    if (total.v[2] > top) {
+      x = {};
+      for (int s = s0; s < s1; ++s) {
+        const int more = s_rows[s] - s_held[s];
+        if (more > 0) {
+          before.v[2] += more;
+          if (before.v[2] > top) {
+            if (lead) atomicOr(g.dev_status, NX_DEV_NO_PAGES);
+            s_cu[s] = -1;
+            s_rows[s] = s_held[s];
+          }
+        }
+        x.v[0] += max(0, s_cu[s]);
+        x.v[1] += max(0, -more);
+        x.v[2] += max(0, s_rows[s] - s_held[s]);
       }
-    }
-    mine = block_before(mine, s_sum, takes);
-    taken = (int)takes;
-    for (int s = s0; s < s1; ++s) {
-      s_take[s] = (int)mine;
-      mine += max(0, s_rows[s] - s_held[s]);
+      before = block_before<kPlanWarps>(x, s_sum, total);
     }
   }
-  sum = 0;
-  for (int s = s0; s < s1; ++s) sum += max(0, s_cu[s]);
-  before = block_before(sum, s_sum, total);
-  const int N = (int)total;
+  const int taken = (int)total.v[2], N = (int)total.v[0];
   for (int s = s0; s < s1; ++s) {
-    const int n = max(0, s_cu[s]);
-    s_cu[s] = (int)before;
-    if (lead) g.a.cu_tokens[s] = (int)before;
-    before += n;
+    const int n = max(0, s_cu[s]), more = s_rows[s] - s_held[s];
+    s_cu[s] = (int)before.v[0];
+    s_give[s] = (int)min(before.v[1], (long long)given);
+    s_take[s] = (int)before.v[2];
+    if (lead) g.a.cu_tokens[s] = (int)before.v[0];
+    before.v[0] += n;
+    before.v[1] += max(0, -more);
+    before.v[2] += max(0, more);
   }
   if (lead && tid == 0) g.a.cu_tokens[S] = N;
   __syncthreads();
@@ -198,17 +212,18 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const __grid_cons
     const int s = owner_of(s_give, S, i);
     g.p.free_pages[free_before + i] = g.p.block_table[s * columns + s_rows[s] + i - s_give[s]];
   }
+  const bool wait = given > 0 && taken > 0;       // taken ones may be among them
+  if (wait) asm volatile("barrier.cluster.arrive;" ::: "memory");
   // ---- the tokens ----
   if (g.a.token_seq || g.a.token_pos)
     for (unsigned i = all; i < (unsigned)N; i += kPlanStep) {
       const int s = owner_of(s_cu, S, i);
       if (g.a.token_seq) g.a.token_seq[i] = s;
-      if (g.a.token_pos) g.a.token_pos[i] = g.a.first_pos[s] + i - s_cu[s];
+      if (g.a.token_pos) g.a.token_pos[i] = g.a.first_pos[s] + (int)i - s_cu[s];
     }
-  // ---- sequences that end ----
+  // ---- sequences that end (a refused one still holds pages) ----
   for (int s = rank * kPlanWarps + warp; s < S; s += kPlanRanks * kPlanWarps) {
-    if (g.a.new_tokens[s] >= 0) continue;
-    if (g.p.held && (s_rows[s] > 0 || s_held[s] < 0)) continue;     // refused
+    if (s_new[s] >= 0 || s_rows[s] != 0) continue;
     for (int i = lane; i < per; i += 32) {
       const int l = i / H;
       const long long at = ((long long)l * S + s) * H + (i - l * H);
@@ -216,18 +231,29 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const __grid_cons
       if (g.image_rows) g.image_rows[at] = 0;
     }
   }
-  if (!g.p.held) return;
-  cluster_sync();                        // the pages given back are there, all inputs are read
+  if (!paged) return;
+  if (wait) asm volatile("barrier.cluster.wait;" ::: "memory");
   // ---- pages taken, from the top ----
   for (unsigned i = all; i < (unsigned)taken; i += kPlanStep) {
     const int s = owner_of(s_take, S, i);
     g.p.block_table[s * columns + s_held[s] + i - s_take[s]] =
-        __ldcg(g.p.free_pages + (top - 1 - i));
+        __ldcg(g.p.free_pages + (top - 1 - (int)i));
   }
   if (lead) {
     for (int s = tid; s < S; s += kPlanThreads) g.p.held[s] = s_rows[s];
     if (tid == 0) *g.p.free_count = top - taken;
   }
+}
+
+template <int THREADS>
+cudaError_t launch_plan(const PlanArgs& g, cudaStream_t st) {
+  const int smem = 6 * g.c.seqs * (int)sizeof(int);
+  if (smem > 32 * 1024) {
+    const cudaError_t e = allow_smem<plan_kernel<THREADS>>(6 * kMaxPlanSeqs * (int)sizeof(int));
+    if (e != cudaSuccess) return e;
+  }
+  return launch_after_clusters(plan_kernel<THREADS>, dim3(kPlanRanks), dim3(THREADS), smem,
+                               kPlanRanks, st, g);
 }
 
 bool overlap(const int32_t* a, const int32_t* b, long long n) {
@@ -274,12 +300,10 @@ extern "C" nx_status nexus_plan(nx_cache* cache, const nx_pool* pool, const nx_p
   g.dev_status = dev_status;
   g.image_rows = image ? image->rows : nullptr;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const int smem = 5 * cache->seqs * (int)sizeof(int);
-  cudaError_t e = cudaSuccess;
-  if (smem > 32 * 1024) e = allow_smem<plan_kernel>(5 * kMaxPlanSeqs * (int)sizeof(int));
-  if (e != cudaSuccess) return finish(e, launches);
-  e = launch_after_clusters(plan_kernel, dim3(kPlanRanks), dim3(kPlanThreads), smem, kPlanRanks,
-                            st, g);
+  // few sequences and tokens: small blocks, whose barriers are shorter (16 sequences 4.1 us, not 5.0);
+  // many keep larger ones busy (256 sequences 10.0 us, not 12.1)
+  const bool few = cache->seqs <= 64 && a.tokens <= 4096;
+  const cudaError_t e = few ? launch_plan<256>(g, st) : launch_plan<512>(g, st);
   if (e == cudaSuccess) note_launch(st, &launches, "plan");
   return finish(e, launches);
 }

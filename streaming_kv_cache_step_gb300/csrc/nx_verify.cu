@@ -17,12 +17,13 @@
 namespace nx {
 namespace {
 
-constexpr int kVerifyThreads = 512;
+constexpr int kVerifyThreads = 256;
+constexpr int kAhead = 2;                // loads of p and of q under way (without q twice as many)
 constexpr int kVerifyWarps = kVerifyThreads / 32;
-constexpr int kVerifyPerSm = 2;          // thread blocks of an SM
+constexpr int kVerifyPerSm = 4;          // thread blocks of an SM
 constexpr int kVerifyRanks = 8;          // thread blocks of a sequence, at most
-constexpr int kVec = 4;                  // columns of one load
-constexpr float kUnit = 4398046511104.f; // 2^42
+template <typename T>
+constexpr int kVecOf = 16 / (int)sizeof(T);     // columns of one load
 
 struct VerifyArgs {
   nx_cache c;
@@ -36,7 +37,32 @@ struct VerifyArgs {
 };
 
 // A probability as it counts: NaN and what is negative as 0, what is above 1 as 1.
-__device__ __forceinline__ float in_unit(float x) { return fminf(fmaxf(x, 0.f), 1.f); }
+__device__ __forceinline__ float in_unit(float x) { return __saturatef(x); }
+
+// Sums of floor(2^42 w), 0 <= w <= 1, without a conversion to 64 bits (of which an SM makes one or
+// two a clock: 256 rows of 65536 columns 47.8 us): added to 8, whose last place is worth 2^-20, w
+// leaves its nearest multiple of that in the sum's low bits; what remains, at most 2^-21 and exact,
+// leaves its multiple of 2^-42, rounded down, in those of 1.5 2^-19 in the same way. Up to 64
+// weights fit 32 bits (the places' start values, `many` of each, come off modulo 2^32).
+constexpr float kHigh = 8.f, kLow = 1.5f / 524288.f;
+struct Counts {
+  uint32_t hi = 0, lo = 0;
+  __device__ __forceinline__ void add(float w) {
+    const float h = __fadd_rn(w, kHigh), rest = __fsub_rn(w, __fsub_rn(h, kHigh));
+    hi += __float_as_uint(h);
+    lo += __float_as_uint(__fadd_rd(rest, kLow));
+  }
+  __device__ __forceinline__ unsigned long long sum(int many) const {
+    const uint32_t h = hi - many * __float_as_uint(kHigh);
+    const int32_t l = (int32_t)(lo - many * __float_as_uint(kLow));
+    return ((unsigned long long)h << 22) + (unsigned long long)(long long)l;
+  }
+};
+__device__ __forceinline__ unsigned long long units(float w) {
+  Counts c;
+  c.add(w);
+  return c.sum(1);
+}
 
 template <typename T>
 __device__ __forceinline__ float value(const T* p) {
@@ -44,21 +70,23 @@ __device__ __forceinline__ float value(const T* p) {
   else return *p;
 }
 
-// Four neighbouring values of a row, all there and aligned to their size.
-__device__ __forceinline__ void load4(const float* p, float* x) {
-  const float4 y = *reinterpret_cast<const float4*>(p);
-  x[0] = y.x, x[1] = y.y, x[2] = y.z, x[3] = y.w;
+// 16 bytes of neighbouring values, aligned, and what they are.
+template <typename T>
+__device__ __forceinline__ uint4 load16(const T* p) {
+  return *reinterpret_cast<const uint4*>(p);
 }
-__device__ __forceinline__ void load4(const __nv_bfloat16* p, float* x) {
-  const uint2 y = *reinterpret_cast<const uint2*>(p);
-  x[0] = __uint_as_float(y.x << 16), x[1] = __uint_as_float(y.x & 0xFFFF0000u);
-  x[2] = __uint_as_float(y.y << 16), x[3] = __uint_as_float(y.y & 0xFFFF0000u);
+template <typename T>
+__device__ __forceinline__ float part(const uint4& x, int e) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  if constexpr (sizeof(T) == 4) return __uint_as_float(w[e]);
+  else return __uint_as_float(e & 1 ? w[e / 2] & 0xFFFF0000u : w[e / 2] << 16);
 }
 
 // The row that a token is drawn from. Columns are counted from `shift` places before the row, so
-// that every fourth one is aligned.
+// that loads start at multiples of their size.
 template <typename T>
 struct Weights {
+  static constexpr int kVec = kVecOf<T>;
   const T *p, *q;       // the rows, `shift` places before them; q null: none is taken off
   int shift, end;       // columns [shift, end) exist
   int out;              // a column without weight (-1: none)
@@ -69,38 +97,31 @@ struct Weights {
     end = shift + V;
     p = row - shift;
     q = other ? other - shift : nullptr;
-    q_vec = (uintptr_t)q / sizeof(T) % kVec == 0;
+    q_vec = (uintptr_t)q % 16 == 0;
     out = without < 0 ? -1 : without + shift;
   }
-  __device__ __forceinline__ unsigned long long weigh(int col, float x, float y) const {
-    const float w = fmaxf(in_unit(x) - in_unit(y), 0.f);
-    return col == out ? 0ull : (unsigned long long)__float2ll_rz(w * kUnit);
+  template <bool TWO>
+  __device__ __forceinline__ float weigh(float x, float y) const {
+    return TWO ? __saturatef(in_unit(x) - in_unit(y)) : in_unit(x);
   }
-  __device__ __forceinline__ unsigned long long one(int col) const {
-    if (col < shift || col >= end) return 0;
-    return weigh(col, value(p + col), q ? value(q + col) : 0.f);
-  }
-  // columns col .. col + 3, col a multiple of 4
-  __device__ __forceinline__ void fetch(int col, float* x, float* y) const {
-    if (col >= shift && col + kVec <= end) {
-      load4(p + col, x);
-      if (!q) {
+  __device__ __forceinline__ uint4 gather(const T* from, int col) const {
+    uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
-        for (int e = 0; e < kVec; ++e) y[e] = 0.f;
-      } else if (q_vec) {
-        load4(q + col, y);
-      } else {
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) y[e] = value(q + col + e);
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < kVec; ++e) {
-        const bool ok = col + e >= shift && col + e < end;
-        x[e] = ok ? value(p + col + e) : 0.f;
-        y[e] = ok && q ? value(q + col + e) : 0.f;
-      }
+    for (int e = 0; e < kVec; ++e) {
+      if (col + e < shift || col + e >= end) continue;
+      if constexpr (sizeof(T) == 4) w[e] = __float_as_uint(from[col + e]);
+      else
+        w[e / 2] |= (uint32_t)reinterpret_cast<const uint16_t*>(from)[col + e] << 16 * (e & 1);
     }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  // columns col .. col + kVec - 1, col a multiple of kVec; zeros for those that do not exist
+  template <bool TWO>
+  __device__ __forceinline__ void fetch(int col, uint4& x, uint4& y) const {
+    const bool whole = col >= shift && col + kVec <= end;
+    x = whole ? load16(p + col) : gather(p, col);
+    if (TWO) y = whole && q_vec ? load16(q + col) : gather(q, col);
+    else y = make_uint4(0, 0, 0, 0);
   }
 };
 
@@ -126,28 +147,76 @@ __device__ __forceinline__ void push(unsigned long long* p, int rank, unsigned l
       : "memory");
 }
 
-// lens of a sequence's slices without the drafts that went, and the image without their blocks;
-// thread `id` of all of the sequence's.
-__device__ __forceinline__ void take_back(const VerifyArgs& g, int s, int gone, int id) {
-  const int per = g.c.layers * g.c.kv_heads;
-  for (int i = id; i < per; i += g.ranks * kVerifyThreads) {
-    const int l = i / g.c.kv_heads, h = i - l * g.c.kv_heads;
-    const long long at = ((long long)l * g.c.seqs + s) * g.c.kv_heads + h;
-    const int len = g.lens_in[at];
-    if (len < gone || len > g.c.capacity) {
-      atomicOr(g.dev_status, NX_DEV_BAD_LEN);
-      continue;
-    }
-    g.c.lens[at] = len - gone;
-    const int hold = (len - gone) / g.b * g.b;
-    if (g.held && g.held[at] > hold) g.held[at] = hold;
+// The slices of a sequence, thread `id` of all of its blocks' every so many of them: lens without
+// the drafts that went, and an image without their blocks. The first length is fetched early.
+struct TakeBack {
+  int i, len;
+  static __device__ __forceinline__ long long at(const VerifyArgs& g, int s, int i) {
+    const int l = i / g.c.kv_heads;
+    return ((long long)l * g.c.seqs + s) * g.c.kv_heads + (i - l * g.c.kv_heads);
   }
+  __device__ __forceinline__ TakeBack(const VerifyArgs& g, int s, int id) {
+    i = id;
+    len = i < g.c.layers * g.c.kv_heads ? g.lens_in[at(g, s, i)] : 0;
+  }
+  __device__ __forceinline__ void finish(const VerifyArgs& g, int s, int gone) {
+    const int per = g.c.layers * g.c.kv_heads, step = g.ranks * kVerifyThreads;
+    while (i < per) {
+      const long long x = at(g, s, i);
+      if (len < gone || len > g.c.capacity) {
+        atomicOr(g.dev_status, NX_DEV_BAD_LEN);
+      } else {
+        g.c.lens[x] = len - gone;
+        const int hold = (len - gone) / g.b * g.b;
+        if (g.held && g.held[x] > hold) g.held[x] = hold;
+      }
+      i += step;
+      if (i < per) len = g.lens_in[at(g, s, i)];
+    }
+  }
+};
+
+// The sum of the weights of columns [c0, c1), c0 a multiple of a load's, of one warp: a lane's part.
+template <typename T, bool TWO, int AHEAD>
+__device__ __forceinline__ unsigned long long lane_sum(const Weights<T>& w, int c0, int c1,
+                                                       int lane) {
+  constexpr int kVec = kVecOf<T>;
+  unsigned long long sum = 0;
+#pragma unroll 1
+  for (int c = c0 + lane * kVec; c < c1; c += AHEAD * 32 * kVec) {
+    uint4 x[AHEAD], y[AHEAD];
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      const int col = c + i * 32 * kVec;
+      x[i] = y[i] = make_uint4(0, 0, 0, 0);
+      if (col < c1) w.template fetch<TWO>(col, x[i], y[i]);
+    }
+    Counts n;
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i)
+#pragma unroll
+      for (int e = 0; e < kVec; ++e)
+        n.add(w.template weigh<TWO>(part<T>(x[i], e), part<T>(y[i], e)));
+    static_assert(AHEAD * kVec <= 64, "");
+    sum += n.sum(AHEAD * kVec);
+  }
+  // the column without weight comes off again
+  if (!TWO && lane == 0 && w.out >= max(c0, w.shift) && w.out < c1)
+    sum -= units(in_unit(value(w.p + w.out)));
+  return sum;
+}
+template <typename T>
+__device__ __forceinline__ unsigned long long columns_sum(const Weights<T>& w, int c0, int c1,
+                                                          int lane) {
+  return warp_sum(w.q ? lane_sum<T, true, kAhead>(w, c0, c1, lane)
+                      : lane_sum<T, false, 2 * kAhead>(w, c0, c1, lane));
 }
 
 template <typename T>
 __global__ void __launch_bounds__(kVerifyThreads, kVerifyPerSm) verify_kernel(VerifyArgs g) {
   __shared__ int s_first;
-  __shared__ unsigned long long s_warp[kVerifyWarps], s_rank[2][kVerifyRanks];
+  __shared__ unsigned long long s_warp[kVerifyWarps], s_part[kVerifyWarps];
+  __shared__ unsigned long long s_rank[2][kVerifyRanks];
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const int s = blockIdx.x / g.ranks, rank = blockIdx.x % g.ranks;
   const int V = g.a.vocab;
@@ -156,11 +225,6 @@ __global__ void __launch_bounds__(kVerifyThreads, kVerifyPerSm) verify_kernel(Ve
   grid_dep_wait();
   int first;
   const int n = tokens_of(g.t, s, first);
-  if (n == 0) {
-    if (tid == 0 && rank == 0) g.a.emitted[s] = 0;
-    take_back(g, s, 0, rank * kVerifyThreads + tid);
-    return;
-  }
   if (n < 0) {                           // (the whole cluster goes)
     if (tid == 0 && rank == 0) {
       atomicOr(g.dev_status, NX_DEV_BAD_TOKENS);
@@ -168,70 +232,54 @@ __global__ void __launch_bounds__(kVerifyThreads, kVerifyPerSm) verify_kernel(Ve
     }
     return;
   }
+  TakeBack back(g, s, rank * kVerifyThreads + tid);
+  if (n == 0) {
+    if (tid == 0 && rank == 0) g.a.emitted[s] = 0;
+    back.finish(g, s, 0);
+    return;
+  }
+  const float u_draw = g.a.u_draw[s];
   // pushes into another block's shared memory must find it running
   if (g.ranks > 1) asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
   // ---- the first draft that goes ----
   if (tid == 0) s_first = n - 1;
-  __syncthreads();
-  for (int i = tid; i < n - 1; i += kVerifyThreads) {
-    const long long row = first + i;
-    const int x = g.a.token[row + 1];
-    bool stays = false;
-    if (x >= 0 && x < V) {
-      const double want = in_unit(value(p + row * g.a.p_stride + x));
-      const double had = q ? in_unit(value(q + row * g.a.q_stride + x)) : 1.0;
-      stays = (double)g.a.u[row] * had < want;
-    } else if (rank == 0) {
-      atomicOr(g.dev_status, NX_DEV_BAD_TOKENS);
-    }
-    if (!stays) {
-      atomicMin(&s_first, i);
-      break;                             // this thread's later ones do not matter
+  if (n > 1) {
+    __syncthreads();
+    for (int i = tid; i < n - 1; i += kVerifyThreads) {
+      const long long row = first + i;
+      const int x = g.a.token[row + 1];
+      bool stays = false;
+      if (x >= 0 && x < V) {
+        const double want = in_unit(value(p + row * g.a.p_stride + x));
+        const double had = q ? in_unit(value(q + row * g.a.q_stride + x)) : 1.0;
+        stays = (double)g.a.u[row] * had < want;
+      } else if (rank == 0) {
+        atomicOr(g.dev_status, NX_DEV_BAD_TOKENS);
+      }
+      if (!stays) {
+        atomicMin(&s_first, i);
+        break;                           // this thread's later ones do not matter
+      }
     }
   }
   __syncthreads();
   const int r = s_first, gone = n - 1 - r;
-  if (rank == 0) {
-    for (int i = tid; i < n; i += kVerifyThreads)
-      if (i != r) g.a.out[first + i] = i < r ? g.a.token[first + i + 1] : -1;
-    if (tid == 0) g.a.emitted[s] = r + 1;
-  }
-  take_back(g, s, gone, rank * kVerifyThreads + tid);
-  // ---- the draw ----
+  // ---- the draw: block sums ----
   const int next = gone ? g.a.token[first + r + 1] : -1;
   const T* row_p = p + (first + r) * g.a.p_stride;
   const T* row_q = gone && q ? q + (first + r) * g.a.q_stride : nullptr;
   Weights<T> w(row_p, row_q, V, gone && !q ? next : -1);
   // every warp's columns: whole loads of all lanes
+  constexpr int kVec = kVecOf<T>, kLine = 32 * kVec;
   const int warps = g.ranks * kVerifyWarps;
-  const int run = ((w.end + warps - 1) / warps + 32 * kVec - 1) / (32 * kVec) * (32 * kVec);
-  const int c0 = (int)min((long long)w.end, (long long)(rank * kVerifyWarps + warp) * run);
+  const int run = ((w.end + warps - 1) / warps + kLine - 1) / kLine * kLine;
+  const int block0 = (int)min((long long)w.end, (long long)rank * kVerifyWarps * run);
+  const int c0 = (int)min((long long)w.end, (long long)block0 + warp * run);
   const int c1 = (int)min((long long)w.end, (long long)c0 + run);
   unsigned long long total = 0, before = 0;
-  if (g.ranks > 1) asm volatile("barrier.cluster.wait;" ::: "memory");
 #pragma unroll 1
   for (int round = 0; round < 2; ++round) {
-    unsigned long long sum = 0;
-    constexpr int kAhead = 4;            // loads of p, and of q, under way
-#pragma unroll 1
-    for (int c = c0 + lane * kVec; c < c1; c += kAhead * 32 * kVec) {
-      float x[kAhead][kVec], y[kAhead][kVec];
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        const int col = c + i * 32 * kVec;
-        if (col < c1) {
-          w.fetch(col, x[i], y[i]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < kVec; ++e) x[i][e] = y[i][e] = 0.f;
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i)
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) sum += w.weigh(c + i * 32 * kVec + e, x[i][e], y[i][e]);
-    }
-    sum = warp_sum(sum);
+    const unsigned long long sum = columns_sum(w, c0, c1, lane);
     if (lane == 0) s_warp[warp] = sum;
     __syncthreads();
     if (tid < g.ranks) {
@@ -241,9 +289,12 @@ __global__ void __launch_bounds__(kVerifyThreads, kVerifyPerSm) verify_kernel(Ve
       if (g.ranks == 1) s_rank[round][0] = all;
       else push(&s_rank[round][rank], tid, all);
     }
-    if (g.ranks == 1) __syncthreads();
-    else
+    if (g.ranks == 1) {
+      __syncthreads();
+    } else {
+      if (round == 0) asm volatile("barrier.cluster.wait;" ::: "memory");
       asm volatile("barrier.cluster.arrive;\n\tbarrier.cluster.wait;" ::: "memory");
+    }
     total = before = 0;
     for (int i = 0; i < g.ranks; ++i) {
       if (i < rank) before += s_rank[round][i];
@@ -253,56 +304,74 @@ __global__ void __launch_bounds__(kVerifyThreads, kVerifyPerSm) verify_kernel(Ve
     // nothing left of p behind q: the draw goes by p itself
     w = Weights<T>(row_p, nullptr, V, -1);
   }
-  const double u = g.a.u_draw[s];
+  // ---- what does not wait for the draw ----
+  back.finish(g, s, gone);
+  if (rank == 0) {
+    for (int i = tid; i < n; i += kVerifyThreads)
+      if (i != r) g.a.out[first + i] = i < r ? g.a.token[first + i + 1] : -1;
+    if (tid == 0) {
+      g.a.emitted[s] = r + 1;
+      if (total == 0) {
+        atomicOr(g.dev_status, NX_DEV_BAD_PROBS);
+        g.a.out[first + r] = 0;
+      }
+    }
+  }
+  // ---- the column: whose warp's run holds the threshold, which part of it, which line, lane ----
+  const double u = u_draw;
   const unsigned long long U =
       u > 0. ? (unsigned long long)fmin(u * 2147483648., 2147483647.) : 0ull;
   const unsigned long long t = U * (total >> 31) + (U * (total & 0x7FFFFFFFull) >> 31);
-  if (total == 0) {
-    if (rank == 0 && tid == 0) {
-      atomicOr(g.dev_status, NX_DEV_BAD_PROBS);
-      g.a.out[first + r] = 0;
+  int owner = -1;
+  if (t >= before)
+    for (int i = 0; i < kVerifyWarps && owner < 0; ++i) {
+      if (t - before < s_warp[i]) owner = i;
+      else before += s_warp[i];
     }
-    return;
-  }
-  for (int i = 0; i < warp; ++i) before += s_warp[i];
-  if (t < before || t - before >= s_warp[warp]) return;
-  // ---- this warp's columns hold the threshold: which lane's, then which one ----
-  const int each = run / 32;
-  const int l0 = c0 + lane * each;
-  unsigned long long sum = 0;
-#pragma unroll 4
-  for (int c = l0; c < min(l0 + each, c1); c += kVec) {
-    float x[kVec], y[kVec];
-    w.fetch(c, x, y);
+  if (owner < 0) return;                 // another block's, or nobody's
+  const int share = (run / kLine + kVerifyWarps - 1) / kVerifyWarps * kLine;
+  const int r0 = block0 + owner * run, r1 = min(w.end, r0 + run);
+  const int p0 = min(r1, r0 + warp * share), p1 = min(r1, p0 + share);
+  const unsigned long long sum = columns_sum(w, p0, p1, lane);
+  if (lane == 0) s_part[warp] = sum;
+  __syncthreads();
+  for (int i = 0; i < warp; ++i) before += s_part[i];
+  if (t < before || t - before >= sum) return;
+#pragma unroll 1
+  for (int c = p0 + lane * kVec; c - lane * kVec < p1; c += kLine) {
+    uint4 x, y;
+    unsigned long long each[kVec], mine = 0;
+    x = y = make_uint4(0, 0, 0, 0);
+    if (c < p1) {
+      if (w.q) w.template fetch<true>(c, x, y);
+      else w.template fetch<false>(c, x, y);
+    }
 #pragma unroll
-    for (int e = 0; e < kVec; ++e) sum += w.weigh(c + e, x[e], y[e]);
-  }
-  unsigned long long mine = before + warp_before(sum, lane);
-  const unsigned owner = __ballot_sync(0xffffffffu, t >= mine && t - mine < sum);
-  if (!owner) return;                    // (only if somebody writes to the rows meanwhile)
-  const int src = __ffs(owner) - 1;
-  before = __shfl_sync(0xffffffffu, mine, src);
-  for (int c = c0 + src * each, stop = c + each; c < stop; c += 32) {
-    const int col = c + lane;
-    const unsigned long long x = col < stop ? w.one(col) : 0ull;
-    mine = before + warp_before(x, lane);
-    const unsigned hit = __ballot_sync(0xffffffffu, t >= mine && t - mine < x);
-    if (hit) {
-      if (lane == __ffs(hit) - 1) g.a.out[first + r] = col - w.shift;
-      return;
+    for (int e = 0; e < kVec; ++e) {
+      each[e] = c + e == w.out ? 0ull
+                               : units(w.template weigh<true>(part<T>(x, e), part<T>(y, e)));
+      mine += each[e];
     }
-    before = __shfl_sync(0xffffffffu, mine + x, 31);
+    unsigned long long at = before + warp_before(mine, lane);
+    if (t >= at && t - at < mine) {
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) {
+        if (t >= at && t - at < each[e]) g.a.out[first + r] = c + e - w.shift;
+        at += each[e];
+      }
+    }
+    before = __shfl_sync(0xffffffffu, at + mine, 31);
+    if (before > t) return;
   }
 }
 
 // Thread blocks of a sequence: as many as fit the GPU at once for all sequences, but each with
 // work for its warps.
 int verify_ranks(int seqs, int vocab) {
-  int ranks = kVerifyRanks;
-  while (ranks > 1 && ((long long)seqs * ranks > kVerifyPerSm * 152 ||
-                       vocab <= ranks / 2 * kVerifyThreads * kVec))
-    ranks /= 2;
-  return ranks;
+  const int fit = kVerifyPerSm * 152 / seqs;
+  const int feed = (vocab + kVerifyThreads * 4 - 1) / (kVerifyThreads * 4);
+  const int ranks = fit < feed ? fit : feed;
+  return ranks < 1 ? 1 : ranks > kVerifyRanks ? kVerifyRanks : ranks;
 }
 
 }  // namespace

@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 import threading
 from dataclasses import dataclass
 from fractions import Fraction
@@ -113,6 +114,12 @@ class CVerify(ctypes.Structure):
         (n, ctypes.c_void_p) for n in ("u", "u_draw", "out", "emitted", "lens_in")] + [
         (n, ctypes.c_int32) for n in ("vocab", "dtype", "reserved")]
 
+
+# The same structures as bytes, which the entry points around a step pass by value: packing one
+# costs a tenth of a Structure's construction, and these calls take as long on the host as on the GPU.
+_CACHE, _TOKENS, _IMAGE = struct.Struct("10i5P"), struct.Struct("4iP"), struct.Struct("5P")
+_POOL, _PLAN, _VERIFY = struct.Struct("6P"), struct.Struct("5P2i"), struct.Struct("3P2q5P3i4x")
+_ATTEND, _SHARED = struct.Struct("3P2qfi"), struct.Struct("3P2i")
 
 _lib = None
 _lock = threading.Lock()
@@ -605,33 +612,84 @@ def attend(cache: Cache, layer: int, q, out, ws, dev_status, *, max_tokens: int,
            "nexus_attend")
 
 
-def _one_device(cache: Cache, **tensors):
-    """Calls go to the current device: everything they name must be there."""
-    here = torch.cuda.current_device()
-    for name, t in (("the cache", cache.k), *tensors.items()):
-        if t is not None and t.device.index != here:
-            raise ValueError(f"{name} must be on the current GPU")
+def _device(cache: Cache) -> int:
+    """The cache's GPU, which must be the current one: calls go there."""
+    dev = cache.k.get_device()
+    if dev < 0 or dev != torch.cuda.current_device():
+        raise ValueError("the cache must be on the current GPU")
+    return dev
 
 
-def _shared(cache: Cache, prefix: Cache, prefix_image, cu_seqs, max_shared: int):
+def _ints(t, n: int, name: str, dev: int) -> int:
+    """The address of n contiguous int32 values on GPU `dev`."""
+    if t.get_device() != dev or t.dtype is not torch.int32 or t.numel() != n or \
+            not t.is_contiguous():
+        raise ValueError(f"{name} must be {n} contiguous int32 values on the current GPU")
+    return t.data_ptr()
+
+
+def _floats(t, n: int, name: str, dev: int) -> int:
+    if t.get_device() != dev or t.dtype is not torch.float32 or t.numel() != n or \
+            not t.is_contiguous():
+        raise ValueError(f"{name} must be {n} contiguous float32 values on the current GPU")
+    return t.data_ptr()
+
+
+def _packed_cache(c: Cache, dev: int) -> bytes:
+    """nx_cache of a cache on GPU `dev`."""
+    for t in (c.k, c.v, c.pos, c.lens):
+        if t.get_device() != dev or not t.is_contiguous():
+            raise ValueError("cache tensors must be contiguous and on the current GPU")
+    if c.pos.dtype is not torch.int32 or c.lens.dtype is not torch.int32:
+        raise ValueError("pos and lens must be int32")
+    if c.k.dtype is torch.bfloat16:
+        dtype = DTYPE_BF16
+    elif c.k.dtype is torch.float32:
+        dtype = DTYPE_F32
+    else:
+        raise ValueError("k and v must be bfloat16 or float32")
+    table = 0
+    if c.block_table is not None:
+        table = _ints(c.block_table, c.seqs * c.max_pages_per_seq, "block_table", dev)
+    return _CACHE.pack(c.layers, c.seqs, c.kv_heads, c.group, c.head_dim, c.capacity, c.page_size,
+                       c.num_pages, c.max_pages_per_seq, dtype, c.k.data_ptr(), c.v.data_ptr(),
+                       c.pos.data_ptr(), c.lens.data_ptr(), table)
+
+
+def _packed_image(image: Image | None, cache: Cache, dev: int) -> bytes | None:
+    if image is None:
+        return None
+    if image.k.get_device() != dev:
+        raise ValueError("the image must be on the current GPU")
+    return bytes(image.c_struct(cache))
+
+
+def _raw(stream, dev: int) -> int | None:
+    """The handle of a stream, or of the current one."""
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(dev)
+    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+
+
+def _packed_shared(prefix: Cache, prefix_image, cu_seqs, max_shared: int, dev: int):
     """nx_shared, and what must live as long as it does."""
-    if cu_seqs is not None:
-        _int32(cu_seqs, prefix.seqs + 1, "cu_seqs")
-    c = prefix.c_struct()
-    im = None if prefix_image is None else prefix_image.c_struct(prefix)
-    x = CShared(prefix=ctypes.addressof(c), image=None if im is None else ctypes.addressof(im),
-                cu_seqs=None if cu_seqs is None else cu_seqs.data_ptr(), max_tokens=max_shared)
-    return x, (c, im)
+    c = CCache.from_buffer_copy(_packed_cache(prefix, dev))
+    im = None
+    if prefix_image is not None:
+        im = CImage.from_buffer_copy(_packed_image(prefix_image, prefix, dev))
+    return _SHARED.pack(ctypes.addressof(c), 0 if im is None else ctypes.addressof(im),
+                        0 if cu_seqs is None else _ints(cu_seqs, prefix.seqs + 1, "cu_seqs", dev),
+                        max_shared, 0), (c, im)
 
 
 def attend_shared_workspace_bytes(cache: Cache, prefix: Cache, *, tokens: int, max_tokens: int,
                                   max_shared: int) -> int:
     # as above: any non-null cu_tokens and cu_seqs will do
     t = CTokens(0, tokens, max_tokens, 0, cache.lens.data_ptr())
-    x, _keep = _shared(cache, prefix, None, None, max_shared)
-    x.cu_seqs = prefix.lens.data_ptr()
-    n = load().nexus_attend_shared_workspace_bytes(ctypes.byref(cache.c_struct()),
-                                                   ctypes.byref(t), ctypes.byref(x))
+    c, p = cache.c_struct(), prefix.c_struct()
+    x = CShared(prefix=ctypes.addressof(p), cu_seqs=prefix.lens.data_ptr(), max_tokens=max_shared)
+    n = load().nexus_attend_shared_workspace_bytes(ctypes.byref(c), ctypes.byref(t),
+                                                   ctypes.byref(x))
     if n == 0:
         raise NexusError(NX_ERR_INVALID_ARG, "nexus_attend_shared_workspace_bytes")
     return int(n)
@@ -653,17 +711,22 @@ def attend_shared(cache: Cache, layer: int, q, out, ws, dev_status, *, prefix: C
     is shared by sequences cu_seqs[i] .. cu_seqs[i + 1] - 1 (int32 [prefix.seqs + 1], or None where
     all share the only one); max_shared: no prefix is shared by more of the new tokens. The rest is
     as in attend; prefix_image: an 8-bit image of the prefix cache."""
-    n = q.shape[0]
-    _one_device(cache, q=q, out=out, ws=ws, dev_status=dev_status, lse=lse, cu_seqs=cu_seqs,
-                cu_tokens=cu_tokens, prefix=prefix.k)
-    a = _attend_args(cache, q, out, causal, scale, lse, ws)
-    x, _keep = _shared(cache, prefix, prefix_image, cu_seqs, max_shared)
-    im = None if image is None else ctypes.byref(image.c_struct(cache))
-    _check(load().nexus_attend_shared(ctypes.byref(cache.c_struct()),
-                                      ctypes.byref(_tokens(cache, layer, n, max_tokens, cu_tokens)),
-                                      im, ctypes.byref(x), ctypes.byref(a), _ptr(ws), ws.numel(),
-                                      _status(dev_status), _stream(stream)),
-           "nexus_attend_shared")
+    dev = _device(cache)
+    n, HQ = q.shape[0], cache.kv_heads * cache.group
+    c = _packed_cache(cache, dev)
+    if q.get_device() != dev or out.get_device() != dev or ws.get_device() != dev:
+        raise ValueError("q, out and ws must be on the current GPU")
+    a = _ATTEND.pack(q.data_ptr(), out.data_ptr(),
+                     0 if lse is None else _floats(lse, n * HQ, "lse", dev),
+                     _heads(q, n, HQ, cache, "q"), _heads(out, n, HQ, cache, "out"),
+                     cache.head_dim ** -0.5 if scale is None else scale, bool(causal))
+    x, _keep = _packed_shared(prefix, prefix_image, cu_seqs, max_shared, dev)
+    cu = 0 if cu_tokens is None else _ints(cu_tokens, cache.seqs + 1, "cu_tokens", dev)
+    status = load().nexus_attend_shared(
+        c, _TOKENS.pack(layer, n, max_tokens, 0, cu), _packed_image(image, cache, dev), x, a,
+        ws.data_ptr(), ws.numel(), _ints(dev_status, 1, "dev_status", dev), _raw(stream, dev))
+    if status:
+        raise NexusError(status, "nexus_attend_shared")
 
 
 # ---------------------------------------------------------------------------
@@ -696,42 +759,33 @@ def plan(cache: Cache, pool: Pool | None, new_tokens, cu_tokens, dev_status, *, 
     rows of the per-token arrays, by default token_seq's or token_pos's. pool: None for a contiguous
     cache. image: forgets sequences that end. held_in, free_count_in: what the pool held before
     the call, if not pool.held and pool.free_count."""
-    S = cache.seqs
-    _int32(new_tokens, S, "new_tokens")
-    _int32(cu_tokens, S + 1, "cu_tokens")
+    dev, S = _device(cache), cache.seqs
     if tokens is None:
         if token_seq is None and token_pos is None:
             raise ValueError("tokens is needed without token_seq and token_pos")
         tokens = (token_seq if token_pos is None else token_pos).numel()
-    a = CPlan(new_tokens=new_tokens.data_ptr(), cu_tokens=cu_tokens.data_ptr(), tokens=tokens,
-              max_tokens=max_tokens)
-    for name, t, n in (("token_seq", token_seq, tokens), ("token_pos", token_pos, tokens),
-                       ("first_pos", first_pos, S)):
-        if t is not None:
-            _int32(t, n, name)
-            setattr(a, name, t.data_ptr())
-    c = None
+    a = _PLAN.pack(_ints(new_tokens, S, "new_tokens", dev),
+                   0 if first_pos is None else _ints(first_pos, S, "first_pos", dev),
+                   _ints(cu_tokens, S + 1, "cu_tokens", dev),
+                   0 if token_seq is None else _ints(token_seq, tokens, "token_seq", dev),
+                   0 if token_pos is None else _ints(token_pos, tokens, "token_pos", dev),
+                   tokens, max_tokens)
+    x = None
     if pool is not None:
-        _int32(pool.free_pages, cache.num_pages, "free_pages")
-        _int32(pool.free_count, 1, "free_count")
-        _int32(pool.held, S, "held")
-        _int32(cache.block_table, S * cache.max_pages_per_seq, "block_table")
-        c = CPool(block_table=cache.block_table.data_ptr(), free_pages=pool.free_pages.data_ptr(),
-                  free_count=pool.free_count.data_ptr(), held=pool.held.data_ptr())
-        if held_in is not None:
-            _int32(held_in, S, "held_in")
-            c.held_in = held_in.data_ptr()
-        if free_count_in is not None:
-            _int32(free_count_in, 1, "free_count_in")
-            c.free_count_in = free_count_in.data_ptr()
+        if cache.block_table is None:
+            raise ValueError("a pool goes with a paged cache")
+        x = _POOL.pack(cache.block_table.data_ptr(),
+                       _ints(pool.free_pages, cache.num_pages, "free_pages", dev),
+                       _ints(pool.free_count, 1, "free_count", dev),
+                       _ints(pool.held, S, "held", dev),
+                       0 if free_count_in is None else _ints(free_count_in, 1, "free_count_in", dev),
+                       0 if held_in is None else _ints(held_in, S, "held_in", dev))
     elif held_in is not None or free_count_in is not None:
         raise ValueError("held_in and free_count_in go with a pool")
-    _one_device(cache, new_tokens=new_tokens, cu_tokens=cu_tokens, dev_status=dev_status)
-    im = None if image is None else ctypes.byref(image.c_struct(cache))
-    _check(load().nexus_plan(ctypes.byref(cache.c_struct()),
-                             None if c is None else ctypes.byref(c), ctypes.byref(a), im,
-                             _status(dev_status), _stream(stream)),
-           "nexus_plan")
+    status = load().nexus_plan(_packed_cache(cache, dev), x, a, _packed_image(image, cache, dev),
+                               _ints(dev_status, 1, "dev_status", dev), _raw(stream, dev))
+    if status:
+        raise NexusError(status, "nexus_plan")
 
 
 def verify(cache: Cache, token, p, u, u_draw, out, emitted, dev_status, *, max_tokens: int,
@@ -743,31 +797,28 @@ def verify(cache: Cache, token, p, u, u_draw, out, emitted, dev_status, *, max_t
     u_draw float32 [seqs]: uniform in [0, 1). out int32 [tokens]: the kept drafts, the new token,
     then -1; emitted int32 [seqs]: how many of them. lens_in int32 [layers, seqs, kv_heads]: rows
     that the slices held, if not cache.lens. image: forgets the rows taken back."""
-    n, S = token.numel(), cache.seqs
-    _int32(token, n, "token")
-    _int32(out, n, "out")
-    _int32(emitted, S, "emitted")
-    for name, t, m in (("u", u, n), ("u_draw", u_draw, S)):
-        if t.dtype != torch.float32 or not t.is_cuda or not t.is_contiguous() or t.numel() != m:
-            raise ValueError(f"{name} must be {m} contiguous float32 values on the GPU")
-    if p.dim() != 2 or p.dtype not in (torch.float32, torch.bfloat16):
+    dev, S, n = _device(cache), cache.seqs, token.numel()
+    kind = p.dtype
+    if kind is not torch.float32 and kind is not torch.bfloat16 or p.dim() != 2:
         raise ValueError("p must be [tokens, vocab], float32 or bfloat16")
-    for name, t in (("p", p), ("q", q)):
-        if t is not None and (t.shape != (n, p.shape[1]) or t.dtype != p.dtype or not t.is_cuda or
-                              (t.stride(1) != 1 and t.shape[1] > 1)):
-            raise ValueError(f"{name} must be [tokens, vocab] like p on the GPU, rows contiguous")
-    a = CVerify(token=token.data_ptr(), p=p.data_ptr(), p_stride=p.stride(0), u=u.data_ptr(),
-                u_draw=u_draw.data_ptr(), out=out.data_ptr(), emitted=emitted.data_ptr(),
-                vocab=p.shape[1],
-                dtype=DTYPE_BF16 if p.dtype == torch.bfloat16 else DTYPE_F32)
-    if q is not None:
-        a.q, a.q_stride = q.data_ptr(), q.stride(0)
-    if lens_in is not None:
-        _int32(lens_in, cache.n_slices, "lens_in")
-        a.lens_in = lens_in.data_ptr()
-    _one_device(cache, token=token, p=p, q=q, u=u, out=out, emitted=emitted, dev_status=dev_status)
-    im = None if image is None else ctypes.byref(image.c_struct(cache))
-    _check(load().nexus_verify(ctypes.byref(cache.c_struct()),
-                               ctypes.byref(_tokens(cache, 0, n, max_tokens, cu_tokens)),
-                               ctypes.byref(a), im, _status(dev_status), _stream(stream)),
-           "nexus_verify")
+    vocab = p.shape[1]
+    strides = [0, 0]
+    for i, t in enumerate((p, q)):
+        if t is None:
+            continue
+        strides[i], one = t.stride()
+        if t.get_device() != dev or t.shape != (n, vocab) or t.dtype is not kind or \
+                (one != 1 and vocab > 1):
+            raise ValueError("p and q must be [tokens, vocab] on the current GPU, rows contiguous")
+    a = _VERIFY.pack(_ints(token, n, "token", dev), p.data_ptr(), 0 if q is None else q.data_ptr(),
+                     strides[0], strides[1], _floats(u, n, "u", dev),
+                     _floats(u_draw, S, "u_draw", dev), _ints(out, n, "out", dev),
+                     _ints(emitted, S, "emitted", dev),
+                     0 if lens_in is None else _ints(lens_in, cache.n_slices, "lens_in", dev),
+                     vocab, DTYPE_BF16 if kind is torch.bfloat16 else DTYPE_F32, 0)
+    cu = 0 if cu_tokens is None else _ints(cu_tokens, S + 1, "cu_tokens", dev)
+    status = load().nexus_verify(_packed_cache(cache, dev), _TOKENS.pack(0, n, max_tokens, 0, cu),
+                                 a, _packed_image(image, cache, dev),
+                                 _ints(dev_status, 1, "dev_status", dev), _raw(stream, dev))
+    if status:
+        raise NexusError(status, "nexus_verify")

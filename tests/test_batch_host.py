@@ -165,6 +165,18 @@ def test_binding_refuses_shapes_and_types():
         nexus.alloc_attend_shared_workspace(cache, cache, tokens=1, max_tokens=1, max_shared=1)
 
 
+def test_packed_structures_have_the_layout_of_the_header():
+    from streaming_kv_cache_step_gb300 import nexus
+    for packed, c in ((nexus._CACHE, nexus.CCache), (nexus._TOKENS, nexus.CTokens),
+                      (nexus._POOL, nexus.CPool), (nexus._PLAN, nexus.CPlan),
+                      (nexus._VERIFY, nexus.CVerify), (nexus._ATTEND, nexus.CAttend),
+                      (nexus._SHARED, nexus.CShared), (nexus._IMAGE, nexus.CImage)):
+        assert packed.size == ctypes.sizeof(c)
+        values = list(range(1, 1 + len(c._fields_)))
+        x = c.from_buffer_copy(packed.pack(*values))
+        assert [getattr(x, n) for n, _ in c._fields_] == values
+
+
 def test_plain_plan_by_hand():
     # pages of 8: a grows by a page, b gives two back, c ends, d has to wait
     lens = np.zeros((2, 4, 1), np.int64)
