@@ -581,11 +581,13 @@ __device__ __forceinline__ void take_leaks(uint32_t stage, int lane, int t, int 
 // Slots [base + kSlots * i, ...) for i = from, from + kWarps, ... < to, up to slot `end`. vref: the
 // image's largest value scale so far, which o is in units of. Where a run's scale is far below it, or
 // a value that only some rows see is not finite, the steps from there on are attend_slow's (SLOW).
-template <int KIND, int D, int ROWS, int kDeep, int kStageBytes>
+// STEP: warps that share the unit.
+template <int KIND, int D, int ROWS, int kDeep, int kStageBytes, int STEP>
 __device__ __noinline__ void attend_slow(const AttendArgs& g, const AttendUnit& u, int base, int end,
                                          int from, int to, uint32_t ring, Meta* meta,
                                          State<D, ROWS>& st, float vref);
-template <int KIND, int D, int ROWS, int kDeep, int kStageBytes, bool SLOW = false>
+template <int KIND, int D, int ROWS, int kDeep, int kStageBytes, int STEP = kWarps,
+          bool SLOW = false>
 __device__ __forceinline__ void attend_part(const AttendArgs& g, const AttendUnit& u, int base,
                                             int end, int from, int to, uint32_t ring, Meta* meta,
                                             State<D, ROWS>& st, float vref = 1.1754944e-38f) {
@@ -603,7 +605,7 @@ __device__ __forceinline__ void attend_part(const AttendArgs& g, const AttendUni
   const SlotRows at(g, u);
   const long long blocks0 =
       KIND == kImage && !g.c.page_size ? image_scale_at(g.c, g.t.layer, u.s, u.h, 0, g.b) : 0;
-  constexpr int kNext = S::kSlots * kWarps;
+  constexpr int kNext = S::kSlots * STEP;
   static_assert(S::kStage <= kStageBytes, "");
   // whether the rows of a whole step follow one another (base is a multiple of its slots, but
   // behind an image, where a step is one run): one page table entry is enough then
@@ -653,15 +655,15 @@ __device__ __forceinline__ void attend_part(const AttendArgs& g, const AttendUni
   fetch_pages(base + S::kSlots * from);
   __syncwarp();                         // the warp is done with what the ring held before
 #pragma unroll
-  for (int n = 0; n < kDeep - 1; ++n) start(from + n * kWarps, n);
+  for (int n = 0; n < kDeep - 1; ++n) start(from + n * STEP, n);
   Query<KIND, D, ROWS> q;               // while the first rows are on their way
   q.load(g, u, lane);
   int n = 0, i = from;
-  for (; i < to; i += kWarps) {
+  for (; i < to; i += STEP) {
     const int t = base + S::kSlots * i;
     asm volatile("cp.async.wait_group %0;" ::"n"(kDeep - 2) : "memory");
     __syncwarp();                       // everyone's copies are in, and step i - 1 is read
-    start(i + (kDeep - 1) * kWarps, n == 0 ? kDeep - 1 : n - 1);
+    start(i + (kDeep - 1) * STEP, n == 0 ? kDeep - 1 : n - 1);
     const uint32_t stage = ring + n * kStageBytes;
     float ks[S::NT], vs[S::NT];
     bool bad_half[S::NT];
@@ -790,12 +792,12 @@ __device__ __forceinline__ void attend_part(const AttendArgs& g, const AttendUni
     if (i < to) {
       asm volatile("cp.async.wait_all;" ::: "memory");
       if constexpr (KIND == kF32) {
-        attend_part<KIND, D, ROWS, kDeep, kStageBytes, true>(g, u, base, end, i, to, ring, meta, st,
+        attend_part<KIND, D, ROWS, kDeep, kStageBytes, STEP, true>(g, u, base, end, i, to, ring, meta, st,
                                                              vref);
       } else {
         State<D, ROWS> copy = st;       // in local memory: st and u stay in registers
         const AttendUnit unit = u;
-        attend_slow<KIND, D, ROWS, kDeep, kStageBytes>(g, unit, base, end, i, to, ring, meta, copy,
+        attend_slow<KIND, D, ROWS, kDeep, kStageBytes, STEP>(g, unit, base, end, i, to, ring, meta, copy,
                                                        vref);
         st = copy;
       }
@@ -815,12 +817,12 @@ __device__ __forceinline__ void attend_part(const AttendArgs& g, const AttendUni
 // The steps from `from` on with what only some need: a function of its own, so that the others' loop
 // keeps its registers (image, 16 x 32768 rows: 165 us, 166 as a second loop of the caller; fp32, with
 // 255 registers instead of 168, does better with the loop: 64 x 6000 rows 82 us, 84 with the function).
-template <int KIND, int D, int ROWS, int kDeep, int kStageBytes>
+template <int KIND, int D, int ROWS, int kDeep, int kStageBytes, int STEP>
 __device__ __noinline__ void attend_slow(const AttendArgs& g, const AttendUnit& u, int base, int end,
                                          int from, int to, uint32_t ring, Meta* meta,
                                          State<D, ROWS>& st, float vref) {
   State<D, ROWS> mine = st;
-  attend_part<KIND, D, ROWS, kDeep, kStageBytes, true>(g, u, base, end, from, to, ring, meta, mine,
+  attend_part<KIND, D, ROWS, kDeep, kStageBytes, STEP, true>(g, u, base, end, from, to, ring, meta, mine,
                                                        vref);
   st = mine;
 }
@@ -846,11 +848,11 @@ __device__ __forceinline__ void store_out(const AttendArgs& g, const AttendUnit&
 // the own rows' pass takes in first (`joins`: it has some).
 __device__ __forceinline__ void finish_row(const AttendArgs& g, const AttendUnit& u, int r, int D,
                                            int f, float m, float l, float o, bool joins) {
-  if (g.part.pass) {
+  if (g.pass) {
     const long long at = part_row(g, u, r);
-    if (g.part.pass == 1) {
-      g.part.out[at * D + f] = o;
-      if (f == 0) g.part.stat[at] = make_float2(m, l);
+    if (g.pass == 1 || (g.pass == 3 && joins)) {
+      (g.pass == 1 ? g.part.out : g.part.own_out)[at * D + f] = o;
+      if (f == 0) (g.pass == 1 ? g.part.stat : g.part.own_stat)[at] = make_float2(m, l);
       return;
     }
     if (joins) {
@@ -922,11 +924,12 @@ __global__ void __launch_bounds__(kWarps * 32, Ring<KIND, D, ROWS>::kPerSm)
     }
   } else {
     const AttendShare sh = attend_share<kWarps * 32>(
-        g, [&](int i) { return unit_tiles<KIND>(attend_unit<ROWS>(g, i)); });
+        g, [&](int i) { return unit_tiles<KIND>(attend_unit<ROWS>(g, i)); },
+        [](int) { return (int)gridDim.x; });
     grid_dep_trigger();
     if (tid == 0 && !g.splits) g.ws.desc[b] = make_int2(-1, 0);
     if (sh.start >= sh.total) {
-      meet_pass(g);
+      end_pass(g);
       return;
     }
     per = sh.per;
@@ -1061,7 +1064,125 @@ __global__ void __launch_bounds__(kWarps * 32, Ring<KIND, D, ROWS>::kPerSm)
     }
     cluster_sync();                                     // nobody reads this block any more
   }
-  meet_pass(g);
+  end_pass(g);
+}
+
+// finish_row of four neighbouring features.
+__device__ __forceinline__ void finish_four(const AttendArgs& g, const AttendUnit& u, int r, int D,
+                                            int f, float m, float l, float4 o, bool joins) {
+  const long long at = part_row(g, u, r);
+  if (g.pass == 1 || (g.pass == 3 && joins)) {
+    *reinterpret_cast<float4*>((g.pass == 1 ? g.part.out : g.part.own_out) + at * D + f) = o;
+    if (f == 0) (g.pass == 1 ? g.part.stat : g.part.own_stat)[at] = make_float2(m, l);
+    return;
+  }
+  if (joins) {
+    const float2 other = g.part.stat[at];
+    const float4 y = *reinterpret_cast<const float4*>(g.part.out + at * D + f);
+    const float2 k = join_by(m, l, other);
+    l = l * k.x + other.y * k.y;
+    o.x = o.x * k.x + y.x * k.y;
+    o.y = o.y * k.x + y.y * k.y;
+    o.z = o.z * k.x + y.z * k.y;
+    o.w = o.w * k.x + y.w * k.y;
+  }
+  o = l == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
+               : make_float4(o.x / l, o.y / l, o.z / l, o.w / l);
+  const int row = u.r0 + r;
+  const long long to = (long long)(u.first + row / g.c.group) * g.a.out_stride +
+                       ((long long)u.h * g.c.group + row % g.c.group) * D + f;
+  if (g.c.dtype == NX_DTYPE_BF16)
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(g.a.out) + to) =
+        make_uint2(bf16_pair(o.x, o.y), bf16_pair(o.z, o.w));
+  else
+    *reinterpret_cast<float4*>(static_cast<float*>(g.a.out) + to) = o;
+  if (f == 0 && g.a.lse)
+    g.a.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+}
+
+// Short slices: a warp has a unit to itself, from its rows to its outputs, without the other warps'
+// barriers (of whom one step would leave three idle).
+template <int KIND, int D, int ROWS>
+__global__ void __launch_bounds__(kWarps * 32, Ring<KIND, D, ROWS>::kPerSm)
+    attend_short_kernel(const __grid_constant__ AttendArgs g) {
+  using R = Ring<KIND, D, ROWS>;
+  constexpr int kRing = R::kDeep * R::kBytes;
+  extern __shared__ __align__(128) char s_ring[];
+  __shared__ Meta s_meta[kWarps][R::kDeep];
+  static_assert(kRing >= ROWS * D * 4, "");
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  begin_pass(g);
+  const int unit = blockIdx.x * kWarps + warp;
+  if (unit < g.units) {
+    const AttendUnit u = attend_unit<ROWS>(g, unit);
+    if (u.rows > 0) {
+      const uint32_t ring = smem_at(s_ring) + warp * kRing;
+      State<D, ROWS> st;
+#pragma unroll
+      for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) st.o[n][e] = 0.f;
+#pragma unroll
+      for (int e = 0; e < ROWS / 8; ++e) {
+        st.m[e] = -INFINITY;
+        st.l[e] = 0.f;
+      }
+      const int ea = min(u.held, u.end);
+      if constexpr (KIND == kImage) {
+        attend_part<kImage, D, ROWS, R::kDeep, R::kBytes, 1>(g, u, 0, ea, 0, (ea + 31) / 32, ring,
+                                                             s_meta[warp], st);
+        attend_part<kTail, D, ROWS, R::kDeep, R::kBytes, 1>(
+            g, u, ea, u.end, 0, (u.end - ea + 7) / 8, ring, s_meta[warp], st);
+      } else {
+        constexpr int w = Shape<KIND, D>::kSlots;
+        attend_part<KIND, D, ROWS, R::kDeep, R::kBytes, 1>(g, u, 0, u.end, 0, (u.end + w - 1) / w,
+                                                           ring, s_meta[warp], st);
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      __syncwarp();
+      // outputs by row and feature through the ring; rows g and g + 8 of an 8-row tile are the two
+      // terms of the same row
+      float (*s_o)[D] = reinterpret_cast<float (*)[D]>(s_ring + warp * kRing);
+#pragma unroll
+      for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const int f = Shape<KIND, D>::feature(n, 2 * (lane % 4) + y);
+          if constexpr (ROWS == 8) {
+            s_o[lane / 4][f] = st.o[n][y] + st.o[n][2 + y];
+          } else {
+            s_o[lane / 4][f] = st.o[n][y];
+            s_o[lane / 4 + 8][f] = st.o[n][2 + y];
+          }
+        }
+#pragma unroll
+      for (int e = 0; e < ROWS / 8; ++e) {
+        st.l[e] += __shfl_xor_sync(0xffffffffu, st.l[e], 1);
+        st.l[e] += __shfl_xor_sync(0xffffffffu, st.l[e], 2);
+      }
+      const bool joins = part_joins(g, u);
+      meet_pass(g);
+      __syncwarp();
+#pragma unroll 4
+      for (int i = lane; i < ROWS * D / 4; i += 32) {
+        const int r = i / (D / 4), f = i % (D / 4) * 4;
+        // row r's statistics are lane 4 (r % 8)'s
+        float m = __shfl_sync(0xffffffffu, st.m[0], 4 * (r % 8));
+        float l = __shfl_sync(0xffffffffu, st.l[0], 4 * (r % 8));
+        if constexpr (ROWS == 16) {
+          const float m1 = __shfl_sync(0xffffffffu, st.m[1], 4 * (r % 8));
+          const float l1 = __shfl_sync(0xffffffffu, st.l[1], 4 * (r % 8));
+          if (r >= 8) {
+            m = m1;
+            l = l1;
+          }
+        }
+        if (r < u.rows)
+          finish_four(g, u, r, D, f, m, l, *reinterpret_cast<const float4*>(&s_o[r][f]), joins);
+      }
+    }
+  }
+  end_pass(g);
 }
 
 // Joins the pieces of a unit that starts in a block b and ends in a later one. Few units, each of
@@ -1073,7 +1194,7 @@ template <int KIND, int D, int ROWS>
 __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(AttendArgs g) {
   constexpr int E = D / 32;
   __shared__ float s_o[kJoinWarps][D], s_m[kJoinWarps], s_l[kJoinWarps];
-  if (g.part.pass == 1) grid_dep_trigger();
+  if (g.pass == 1) grid_dep_trigger();
   grid_dep_wait();
   const int splits = max(g.splits, 1), split = blockIdx.x % splits;
   int b = blockIdx.x / splits, unit = b;
@@ -1142,14 +1263,13 @@ size_t attend_layout(int D, char* base, AttendWs* ws) {
   return at + (size_t)2 * kAttendGrid * kPieceRows * D * sizeof(float);
 }
 
+// How the row kernel takes a call; returns its thread blocks where they have units of their own, 0
+// where they share all tiles evenly.
 template <int KIND, int D, int ROWS>
-cudaError_t launch_attend(AttendArgs& g, cudaStream_t st, int* launches) {
-  using R = Ring<KIND, D, ROWS>;
+long long plan_rows(AttendArgs& g) {
   const long long mtiles = (most_tokens(g.t) * g.c.group + ROWS - 1) / ROWS;
   const long long units = (long long)g.c.seqs * g.c.kv_heads * mtiles;
-  constexpr int kTileSlots = kTileOf<KIND>;
-  const long long most = units * ((g.c.capacity + kTileSlots - 1) / kTileSlots + 1);
-  const long long fit = kSms * R::kPerSm;
+  const long long fit = kSms * Ring<KIND, D, ROWS>::kPerSm;
   g.mtiles = (int)mtiles;
   g.units = (int)units;
   // A unit is one block's, or a cluster's of 2, 4 or 8 blocks, as many as fit the GPU at once;
@@ -1171,15 +1291,44 @@ cudaError_t launch_attend(AttendArgs& g, cudaStream_t st, int* launches) {
   if (g.c.capacity <= (units * kRanks <= 2 * kSms ? few / 2 : few)) ranks = 1;
   const int limit = ranks > 1 ? ranks * most_of : units >= fit ? 2 * few : few;
   g.ranks = g.c.capacity <= limit ? ranks : 0;
-#ifdef OWN_EVEN
-  g.ranks = 0;
-#endif
   g.splits = 0;
   if (units * 2 <= kSms)
     for (g.splits = ROWS; g.splits > 1 && units * g.splits > kSms;) g.splits /= 2;
-  const int grid = (int)(g.ranks ? units * g.ranks : most < fit ? most : fit);
+  // Short slices, in passes of nexus_attend_shared: a warp per unit. It takes four times a block's
+  // time over the slots, but needs no barrier and four times as many run at once, so that it pays the
+  // longer the more units there are (one warp with a slice of thousands would come last). Both passes,
+  // own slices and the prefix equally long, 4 query heads per group, in us (a warp / a block):
+  //   bf16: 32 units of 32 slots 12 / 13, of 128 16 / 13; 800 units of 32 13 / 31, of 128 18 / 35, of
+  //   512 67 / 78; 2400 units of 16 rows, 32 slots 44 / 117, 128 68 / 113, 512 128 / 167
+  //   fp32: 32 units of 16 slots 11 / 11, of 64 17 / 12; 800 units of 32 16 / 36, of 256 62 / 86, of
+  //   1024 315 / 270; 4000 units of 32 54 / 147, of 256 239 / 340, of 1024 864 / 1007
+  //   image: 32 units of 32 15 / 16, of 64 17 / 16; 2400 units of 16 rows, 32 slots 36 / 109, 512 104 / 152
+  const int waves = (int)((units + fit - 1) / fit);
+  const int brief = waves <= 1   ? (KIND == kF32 ? 16 : 64)
+                    : waves == 2 ? (KIND == kF32 ? 128 : 256)
+                    : waves == 3 ? 512
+                                 : 2048;
+  g.brief = g.pass && g.c.capacity <= brief;
+  return g.brief ? (units + kWarps - 1) / kWarps : units * g.ranks;
+}
+
+template <int KIND, int D, int ROWS>
+cudaError_t launch_attend(AttendArgs& g, cudaStream_t st, int* launches) {
+  using R = Ring<KIND, D, ROWS>;
+  constexpr int kTileSlots = kTileOf<KIND>;
+  const long long blocks = plan_rows<KIND, D, ROWS>(g), units = g.units;
+  const long long most = units * ((g.c.capacity + kTileSlots - 1) / kTileSlots + 1);
+  const long long fit = kSms * R::kPerSm;
+  const int grid = (int)(blocks ? blocks : most < fit ? most : fit);
   constexpr int smem = kWarps * R::kDeep * R::kBytes;
   cudaError_t e;
+  if (g.brief) {
+    e = allow_smem<attend_short_kernel<KIND, D, ROWS>>(smem);
+    if (e != cudaSuccess) return e;
+    e = launch_after(attend_short_kernel<KIND, D, ROWS>, dim3(grid), dim3(kWarps * 32), smem, st, g);
+    if (e == cudaSuccess) note_launch(st, launches, "attend_short");
+    return e;
+  }
   if (g.ranks) {
     e = allow_smem<attend_kernel<KIND, D, ROWS, false>>(smem);
     if (e != cudaSuccess) return e;
@@ -1200,12 +1349,38 @@ cudaError_t launch_attend(AttendArgs& g, cudaStream_t st, int* launches) {
   return e;
 }
 
-#ifndef SHROWS
-#define SHROWS 0
-#endif
+// Which of the two kernels takes a pass. Those of nexus_attend_shared (alone: attend_tc_takes): the
+// row kernel's time goes by its passes of 16 query rows over the slots (from HBM each, where they do
+// not fit L2), that of the tensor cores by the slots behind a dearer start, which pays early where
+// there are few long slices. Both passes on the GPU, own slices of one row, in us (tensor cores / row
+// kernel), prefixes of 8 slices with 20, 48, 96, 192 query rows:
+//   bf16: 512 slots 17 / 15, 18 / 17, 19 / 18, 19 / 19; 2048 18 / 18, 20 / 19, 20 / 23, 22 / 32;
+//   8192 28 / 28, 27 / 29, 28 / 45, 32 / 62; 32768 51 / 49, 51 / 65, 52 / 101, 58 / 174
+//   8 bits: 512 20 / 18, 20 / 20, 20 / 20, 21 / 20; 8192 35 / 29, 36 / 31, 37 / 35, 41 / 59; 32768
+//   63 / 45, 69 / 58, 70 / 84, 81 / 134;
+// of 1 slice, 8192 slots: bf16 19 / 25, 20 / 25, 22 / 25, 23 / 25; 8 bits 21 / 26, 23 / 26, 24 / 27,
+// 26 / 27; four prefixes of 8 slices: bf16, 512 slots 21 / 18, 22 / 18, 26 / 22, 28 / 43; 2048 29 / 23,
+// 29 / 32, 31 / 47, 37 / 78; 32768 116 / 178, 116 / 254, 118 / 481, 144 / 868.
 bool tc_takes(const AttendArgs& g) {
-  if (SHROWS && g.part.pass == 1) return g.c.dtype == NX_DTYPE_BF16 && most_tokens(g.t) * g.c.group > SHROWS;
-  return attend_tc_takes(g.c, g.t, g.im.k != nullptr);
+  const bool image = g.im.k != nullptr;
+  if (!g.pass) return attend_tc_takes(g.c, g.t, image);
+  const long long passes = (most_tokens(g.t) * g.c.group + 15) / 16;
+  if (g.c.dtype != NX_DTYPE_BF16 || passes < 2) return false;
+  const long long slices = (long long)g.c.seqs * g.c.kv_heads, slots = slices * g.c.capacity;
+  if (!image && slots * g.c.head_dim * 4 > 128LL << 20) return true;
+  if (slices <= 8 && g.c.capacity >= 4096 && slots <= (image ? 1 << 15 : 1 << 17)) return true;
+  return slots * (10 * passes - (image ? 50 : 23)) >= (g.c.capacity >= 1024 ? 450000 : 800000);
+}
+
+// Thread blocks of the own rows' pass that can go where there is room: not those of one launch that
+// deals its tiles to as many as fit the GPU at once.
+template <int D>
+long long free_blocks(AttendArgs g) {
+  if (g.c.dtype == NX_DTYPE_F32) return plan_rows<kF32, D, 8>(g);
+  if (tc_takes(g)) return 0;
+  const bool few = most_tokens(g.t) * g.c.group <= 8;
+  if (g.im.k) return few ? plan_rows<kImage, D, 8>(g) : plan_rows<kImage, D, 16>(g);
+  return few ? plan_rows<kBf16, D, 8>(g) : plan_rows<kBf16, D, 16>(g);
 }
 
 template <int D>
@@ -1262,14 +1437,15 @@ size_t attend_bytes(const nx_cache& c, const nx_tokens& t) {
 }
 
 // One pass over a cache's slices.
-cudaError_t attend_pass(const nx_cache& c, const nx_tokens& t, const nx_image* image,
-                        const nx_attend& a, const AttendPart& part, char* ws, int32_t* dev_status,
-                        cudaStream_t st, int* launches) {
+AttendArgs attend_args(const nx_cache& c, const nx_tokens& t, const nx_image* image,
+                       const nx_attend& a, int pass, const AttendPart& part, char* ws,
+                       int32_t* dev_status) {
   AttendArgs g{};
   g.c = c;
   g.t = t;
   if (image) g.im = *image;
   g.a = a;
+  g.pass = pass;
   g.part = part;
   g.dev_status = dev_status;
   if (tc_takes(g)) attend_tc_layout(c.head_dim, ws, &g.ws);
@@ -1277,8 +1453,11 @@ cudaError_t attend_pass(const nx_cache& c, const nx_tokens& t, const nx_image* i
   g.b = image_block(c);
   while (1 << g.b_shift < g.b) ++g.b_shift;
   g.c1 = a.scale * 1.4426950408889634f;
-  return c.head_dim == 128 ? launch_attend<128>(g, st, launches)
-                           : launch_attend<64>(g, st, launches);
+  return g;
+}
+cudaError_t launch_pass(AttendArgs& g, cudaStream_t st, int* launches) {
+  return g.c.head_dim == 128 ? launch_attend<128>(g, st, launches)
+                             : launch_attend<64>(g, st, launches);
 }
 
 // The tokens of nexus_attend_shared as the prefixes see them: those of a prefix's sequences are one
@@ -1299,7 +1478,7 @@ bool valid_shared(const nx_cache& c, const nx_tokens& t, const nx_shared* x) {
 
 // Workspaces of the own rows' pass and the prefixes', and where they meet.
 size_t shared_layout(const nx_cache& c, const nx_tokens& t, const nx_shared& x, char* base,
-                     char** own, char** prefix, AttendPart* part) {
+                     char** own, char** prefix, AttendPart* part, int2** desc) {
   const size_t rows = (size_t)t.tokens * c.kv_heads * c.group;
   size_t at = 0;
   *own = base;
@@ -1309,7 +1488,14 @@ size_t shared_layout(const nx_cache& c, const nx_tokens& t, const nx_shared& x, 
   part->stat = reinterpret_cast<float2*>(base + at);
   at += round256(rows * sizeof(float2));
   part->out = reinterpret_cast<float*>(base + at);
-  return at + rows * c.head_dim * sizeof(float);
+  at += round256(rows * c.head_dim * sizeof(float));
+  if (!attend_tc_may_take(*x.prefix, shared_view(t, x))) return at;
+  part->own_stat = reinterpret_cast<float2*>(base + at);
+  at += round256(rows * sizeof(float2));
+  part->own_out = reinterpret_cast<float*>(base + at);
+  at += round256(rows * c.head_dim * sizeof(float));
+  *desc = reinterpret_cast<int2*>(base + at);
+  return at + round256(attend_tc_units(*x.prefix, shared_view(t, x)) * sizeof(int2));
 }
 
 }  // namespace
@@ -1335,10 +1521,9 @@ extern "C" nx_status nexus_attend(const nx_cache* cache, const nx_tokens* tokens
   if (!ws || ((uintptr_t)ws & 255u) || ws_bytes < attend_bytes(*cache, *tokens))
     return NX_ERR_WORKSPACE;
   if (tokens->tokens == 0) return finish(cudaSuccess, launches);
-  const cudaError_t e =
-      attend_pass(*cache, *tokens, image, *args, AttendPart{}, static_cast<char*>(ws), dev_status,
-                  reinterpret_cast<cudaStream_t>(stream), &launches);
-  return finish(e, launches);
+  AttendArgs g = attend_args(*cache, *tokens, image, *args, 0, AttendPart{},
+                             static_cast<char*>(ws), dev_status);
+  return finish(launch_pass(g, reinterpret_cast<cudaStream_t>(stream), &launches), launches);
 }
 
 extern "C" size_t nexus_attend_shared_workspace_bytes(const nx_cache* cache,
@@ -1349,8 +1534,9 @@ extern "C" size_t nexus_attend_shared_workspace_bytes(const nx_cache* cache,
       !valid_shared(*cache, *tokens, shared))
     return 0;
   char *own, *prefix;
-  AttendPart part;
-  return shared_layout(*cache, *tokens, *shared, nullptr, &own, &prefix, &part);
+  AttendPart part{};
+  int2* desc = nullptr;
+  return shared_layout(*cache, *tokens, *shared, nullptr, &own, &prefix, &part, &desc);
 }
 
 extern "C" nx_status nexus_attend_shared(const nx_cache* cache, const nx_tokens* tokens,
@@ -1370,8 +1556,9 @@ extern "C" nx_status nexus_attend_shared(const nx_cache* cache, const nx_tokens*
   if (status != NX_OK) return status;
   char *own, *prefix;
   AttendPart part{};
+  int2* desc = nullptr;
   const size_t need = shared_layout(*cache, *tokens, *shared, static_cast<char*>(ws), &own,
-                                    &prefix, &part);
+                                    &prefix, &part, &desc);
   if (!ws || ((uintptr_t)ws & 255u) || ws_bytes < need) return NX_ERR_WORKSPACE;
   if (tokens->tokens == 0) return finish(cudaSuccess, launches);
   part.seqs = cache->seqs;
@@ -1382,11 +1569,24 @@ extern "C" nx_status nexus_attend_shared(const nx_cache* cache, const nx_tokens*
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   nx_attend whole = *args;                // the prefix comes before all of the new tokens
   whole.causal = 0;
-  part.pass = 1;
-  cudaError_t e = attend_pass(*shared->prefix, view, shared->image, whole, part, prefix,
-                              dev_status, st, &launches);
-  if (e != cudaSuccess) return finish(e, launches);
-  part.pass = 2;
-  e = attend_pass(*cache, *tokens, image, *args, part, own, dev_status, st, &launches);
+  AttendArgs g = attend_args(*shared->prefix, view, shared->image, whole, 1, part, prefix, dev_status);
+  const bool beside = tc_takes(g);
+  AttendArgs o = attend_args(*cache, *tokens, image, *args, beside ? 3 : 2, part, own, dev_status);
+  if (beside) {
+    g.part.desc = desc;
+    g.part.own_lens = cache->lens + (long long)tokens->layer * cache->seqs * cache->kv_heads;
+    // What the tensor-core kernel deals out the SMs by: a tile of a prefix takes one of them 1.5 us
+    // (3.5 from 8-bit rows), a row of 128 features and 16 query rows of the other pass 10 ns (6). With
+    // fewer blocks than two an SM, or of a launch that counts on all SMs, a part of them is no gain:
+    // 128 slices of 2048 rows next to 16384 slots, 54 us, not 60.
+    const long long rows = most_tokens(*tokens) * cache->group, passes = (rows + 15) / 16;
+    const long long cost = (image ? 6 : 10) * passes * cache->head_dim / 128 + 1;
+    const long long blocks = cache->head_dim == 128 ? free_blocks<128>(o) : free_blocks<64>(o);
+    g.part.tile_cost = shared->image ? 3500 : 1500;
+    g.part.row_cost = blocks < 2 * kSms ? 0 : (int)(cost < 1000 ? cost : 1000);
+  }
+  cudaError_t e = launch_pass(g, st, &launches);
+  if (e == cudaSuccess) e = launch_pass(o, st, &launches);
+  if (e == cudaSuccess && beside) e = launch_attend_meet(g, st, &launches);
   return finish(e, launches);
 }

@@ -22,19 +22,25 @@ struct AttendWs {
   float* out;          // [2 * blocks][rows x head_dim] unnormalised output
 };
 
-// Where the two passes of nexus_attend_shared meet: for every query row what the prefixes' pass has
-// of it, which the own rows' pass joins with its own when it finishes the row.
+// Where the two passes of nexus_attend_shared meet. Either the own rows' pass takes in what the
+// prefixes' has of a query row when it finishes the row (pass 2 after 1), or, with the prefixes on the
+// tensor cores, the two run next to each other and a last kernel joins what both have (pass 3 next
+// to 1).
 struct AttendPart {
-  int pass;            // 0: a call by itself, 1: the prefixes, 2: the sequences' own rows
   int seqs, max_tokens, prefixes, max_shared;     // of the cache, its tokens, the prefixes
   const int32_t* cu_seqs;
   float2* stat;        // [tokens][query heads] running maximum (log2 units) and sum
   float* out;          // [tokens][query heads][head_dim] unnormalised output
+  float2* own_stat;    // the same of the own rows' pass, where it is pass 3
+  float* own_out;
+  // pass 1 next to 3 only (else null):
+  int2* desc;          // by unit: its first and last block, or (-1, 0): one block's
+  const int32_t* own_lens;      // the layer's lengths of the cache, seqs * kv_heads of them
+  int tile_cost, row_cost;      // ns of an SM for a tile of a prefix, for a row of an own slice
 };
 
 struct AttendArgs {
   nx_cache c;           // pass 1: the prefixes' cache, a "sequence" each
-  AttendPart part;
   nx_tokens t;
   nx_image im;          // im.k null: no image
   nx_attend a;
@@ -46,6 +52,9 @@ struct AttendArgs {
   int splits;           // its join: blocks per unit (0: a block for each block's last unit)
   int units;            // seqs * kv_heads * mtiles
   float c1;             // scale * log2(e)
+  int pass;             // 0: a call by itself, 1: the prefixes, 2, 3: the sequences' own rows
+  bool brief;           // row kernel: a warp per unit
+  AttendPart part;      // not of pass 0
 };
 
 // Unit (slice of the layer, row tile): up to `rows` query rows (row r = token r / group, head
@@ -88,7 +97,7 @@ __device__ __forceinline__ AttendUnit attend_unit(const AttendArgs& g, int id) {
   const int mt = id % g.mtiles, sl = id / g.mtiles;
   u.h = sl % g.c.kv_heads;
   u.s = sl / g.c.kv_heads;
-  u.n = g.part.pass == 1 ? shared_tokens(g, u.s, u.first) : tokens_of(g.t, u.s, u.first);
+  u.n = g.pass == 1 ? shared_tokens(g, u.s, u.first) : tokens_of(g.t, u.s, u.first);
   if (u.n < 0) {
     atomicOr(g.dev_status, NX_DEV_BAD_TOKENS);
     u.n = 0;
@@ -116,7 +125,7 @@ __device__ __forceinline__ AttendUnit attend_unit(const AttendArgs& g, int id) {
 // the unit's tokens were among that one's.
 __device__ __forceinline__ bool part_joins(const AttendArgs& g, const AttendUnit& u) {
   const AttendPart& x = g.part;
-  if (x.pass != 2 || u.n <= 0) return false;
+  if (g.pass < 2 || u.n <= 0) return false;
   int p = 0;
   if (x.cu_seqs) {
     for (int hi = x.prefixes; hi - p > 1;) {
@@ -132,15 +141,18 @@ __device__ __forceinline__ bool part_joins(const AttendArgs& g, const AttendUnit
 }
 
 // The two passes overlap: the kernels of the prefixes' let the next one be scheduled as soon as what
-// came before the call is done, and the own rows' pass needs them only where a row is finished. Every
-// one of its thread blocks waits for them before it ends, so that when it is done they are.
+// came before the call is done. As pass 2 the own rows' needs them only where a row is finished, and
+// all of its thread blocks wait there; as pass 3 it does not, and its last block waits alone. When it
+// is done, so are they.
 __device__ __forceinline__ void begin_pass(const AttendArgs& g) {
-  if (g.part.pass == 2) return;
-  grid_dep_wait();
-  if (g.part.pass == 1) grid_dep_trigger();
+  if (g.pass <= 1) grid_dep_wait();
+  if (g.pass & 1) grid_dep_trigger();
 }
 __device__ __forceinline__ void meet_pass(const AttendArgs& g) {
-  if (g.part.pass == 2) grid_dep_wait();
+  if (g.pass == 2) grid_dep_wait();
+}
+__device__ __forceinline__ void end_pass(const AttendArgs& g) {
+  if (g.pass == 2 || (g.pass == 3 && blockIdx.x == gridDim.x - 1)) grid_dep_wait();
 }
 
 // Row r of a unit among all rows of the call.
@@ -164,9 +176,10 @@ __host__ __device__ constexpr int share_start(int total, int per, int b) {
 }
 
 // Every one of THREADS threads adds up a run of units; tiles(i): tiles of unit i. unit and at
-// are undefined if start >= total.
-template <int THREADS, typename Tiles>
-__device__ __forceinline__ AttendShare attend_share(const AttendArgs& g, const Tiles& tiles) {
+// are undefined if start >= total. blocks(total): how many thread blocks share them.
+template <int THREADS, typename Tiles, typename Blocks>
+__device__ __forceinline__ AttendShare attend_share(const AttendArgs& g, const Tiles& tiles,
+                                                    const Blocks& blocks) {
   __shared__ int s_sum[THREADS / 32], s_at[2];
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const int run = (g.units + THREADS - 1) / THREADS;
@@ -189,7 +202,7 @@ __device__ __forceinline__ AttendShare attend_share(const AttendArgs& g, const T
   }
   AttendShare x;
   x.total = total;
-  x.per = share_per(total, gridDim.x);
+  x.per = share_per(total, blocks(total));
   const int start = share_start(total, x.per, blockIdx.x);
   if (start >= before && start - before < sum) {
     int at = before;
@@ -304,6 +317,9 @@ inline long long most_tokens(const nx_tokens& t) {
 bool attend_tc_takes(const nx_cache& c, const nx_tokens& t, bool image);
 bool attend_tc_may_take(const nx_cache& c, const nx_tokens& t);
 size_t attend_tc_layout(int D, char* base, AttendWs* ws);
+size_t attend_tc_units(const nx_cache& c, const nx_tokens& t);
 cudaError_t launch_attend_tc(AttendArgs& g, cudaStream_t st, int* launches);
+// The end of nexus_attend_shared where the passes ran next to each other; g: the prefixes' pass.
+cudaError_t launch_attend_meet(const AttendArgs& g, cudaStream_t st, int* launches);
 
 }  // namespace nx

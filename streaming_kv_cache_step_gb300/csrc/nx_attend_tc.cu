@@ -353,6 +353,27 @@ __device__ __forceinline__ void expand_tile(uint32_t raw, const float* scale, in
   }
 }
 
+// N features of row r of the output, and with the first of them ln l.
+template <int N>
+__device__ __forceinline__ void finish_output(const AttendArgs& g, const AttendUnit& u, int r, int D,
+                                              int d0, float* o, float m, float l) {
+  const float f = l == 0.f ? 0.f : 1.f / l;
+  if (l == 0.f)
+#pragma unroll
+    for (int e = 0; e < N; ++e) o[e] = 0.f;
+  const int row = u.r0 + r;
+  __nv_bfloat16* p = static_cast<__nv_bfloat16*>(g.a.out) +
+                     (long long)(u.first + row / g.c.group) * g.a.out_stride +
+                     ((long long)u.h * g.c.group + row % g.c.group) * D + d0;
+#pragma unroll
+  for (int i = 0; i < N; i += 8)
+    *reinterpret_cast<uint4*>(p + i) =
+        make_uint4(bf16_pair(o[i] * f, o[i + 1] * f), bf16_pair(o[i + 2] * f, o[i + 3] * f),
+                   bf16_pair(o[i + 4] * f, o[i + 5] * f), bf16_pair(o[i + 6] * f, o[i + 7] * f));
+  if (d0 == 0 && g.a.lse)
+    g.a.lse[part_row(g, u, r)] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+}
+
 // Ends N features of row r: o / l to the output and, with the first of them, ln l; of the prefixes'
 // pass o, m and l as they are, which the own rows' pass takes in first (`joins`: it has some).
 template <int N>
@@ -360,12 +381,13 @@ __device__ __forceinline__ void finish_features(const AttendArgs& g, const Atten
                                                 int D, int d0, float* o, float m, float l,
                                                 bool joins) {
   const long long at = part_row(g, u, r);
-  if (g.part.pass == 1) {
-    float4* to = reinterpret_cast<float4*>(g.part.out + at * D + d0);
+  if (g.pass == 1 || (g.pass == 3 && joins)) {
+    float4* to = reinterpret_cast<float4*>((g.pass == 1 ? g.part.out : g.part.own_out) +
+                                           at * D + d0);
 #pragma unroll
     for (int i = 0; i < N / 4; ++i)
       to[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-    if (d0 == 0) g.part.stat[at] = make_float2(m, l);
+    if (d0 == 0) (g.pass == 1 ? g.part.stat : g.part.own_stat)[at] = make_float2(m, l);
     return;
   }
   if (joins) {
@@ -381,21 +403,30 @@ __device__ __forceinline__ void finish_features(const AttendArgs& g, const Atten
       o[4 * i + 3] = o[4 * i + 3] * k.x + y.w * k.y;
     }
   }
-  const float f = l == 0.f ? 0.f : 1.f / l;
-  if (l == 0.f)
+  finish_output<N>(g, u, r, D, d0, o, m, l);
+}
+
+// How many thread blocks share the tiles. With the sequences' own rows next to them: a part of the
+// GPU that goes by what both cost; the other blocks end at once, and their SMs are the other pass's.
+// (64 sequences, 4 heads each of 8 groups, 32768 rows of prefix, 512 to 1024 of their own: XX us one
+// behind the other.)
+template <int THREADS>
+__device__ __forceinline__ int beside_blocks(const AttendArgs& g, int total) {
+  if (g.pass != 1 || !g.part.desc || !g.part.row_cost) return gridDim.x;
+  __shared__ float s_rows[THREADS / 32];
+  const int n = g.part.seqs * g.c.kv_heads;
+  float rows = 0.f;
+  for (int i = threadIdx.x; i < n; i += THREADS) rows += (float)max(0, g.part.own_lens[i]);
 #pragma unroll
-    for (int e = 0; e < N; ++e) o[e] = 0.f;
-  const int row = u.r0 + r;
-  __nv_bfloat16* p = static_cast<__nv_bfloat16*>(g.a.out) +
-                     (long long)(u.first + row / g.c.group) * g.a.out_stride +
-                     ((long long)u.h * g.c.group + row % g.c.group) * D + d0;
+  for (int o = 16; o; o /= 2) rows += __shfl_xor_sync(0xffffffffu, rows, o);
+  if (threadIdx.x % 32 == 0) s_rows[threadIdx.x / 32] = rows;
+  __syncthreads();
+  rows = 0.f;
 #pragma unroll
-  for (int i = 0; i < N; i += 8)
-    *reinterpret_cast<uint4*>(p + i) =
-        make_uint4(bf16_pair(o[i] * f, o[i + 1] * f), bf16_pair(o[i + 2] * f, o[i + 3] * f),
-                   bf16_pair(o[i + 4] * f, o[i + 5] * f), bf16_pair(o[i + 6] * f, o[i + 7] * f));
-  if (d0 == 0 && g.a.lse)
-    g.a.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+  for (int w = 0; w < THREADS / 32; ++w) rows += s_rows[w];
+  const float here = (float)total * g.part.tile_cost, there = rows * g.part.row_cost;
+  const int blocks = (int)(kSms * (here / (here + there + 1.f)) + 0.5f);
+  return min((int)gridDim.x, max(blocks, kSms / 4));
 }
 
 template <int D, int NQ, bool IMAGE>
@@ -452,7 +483,8 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
   begin_pass(g);
   tc_before();
   const AttendShare sh = attend_share<kThreads>(
-      g, [&](int i) { return tc_tiles<NQ>(attend_unit<kRows * NQ>(g, i)); });
+      g, [&](int i) { return tc_tiles<NQ>(attend_unit<kRows * NQ>(g, i)); },
+      [&](int total) { return beside_blocks<kThreads>(g, total); });
   tc_after();
   grid_dep_trigger();
   const uint32_t tmem = s_tmem;
@@ -932,6 +964,8 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
       used[1] += count[1];
       ++segment;
       if (a0 == 0 && a1 < tiles) desc = make_int2(unit, (at + tiles - 1) / sh.per);
+      if (g.pass == 1 && a0 == 0 && tid == 0)
+        g.part.desc[unit] = make_int2(a1 < tiles ? b : -1, (at + tiles - 1) / sh.per);
       // the next piece's loads and products come after this one's results
       __syncwarp();
       __syncthreads();
@@ -942,7 +976,7 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
     ++unit;
   }
   if (tid == 0) g.ws.desc[b] = desc;
-  meet_pass(g);
+  end_pass(g);
   asm volatile("cp.async.wait_all;" ::: "memory");
   tc_before();
   __syncthreads();
@@ -971,35 +1005,35 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
 // slices: 8 of 19), so a block has few features, and the loads of kJoinAhead pieces are under way at
 // once (with 32 features a block and a piece at a time 62 us for those, of which now XX).
 constexpr int kJoinCols = 8, kJoinAhead = 4;
-template <int D, int NQ>
+template <int D, int NQ, int COLS>
 __global__ void __launch_bounds__(kTcRows) attend_tc_join_kernel(AttendArgs g) {
-  if (g.part.pass == 1) grid_dep_trigger();
+  constexpr int kAhead = COLS > kJoinCols ? 1 : kJoinAhead;
   grid_dep_wait();
-  const int b = blockIdx.x, d0 = blockIdx.y * kJoinCols, r = threadIdx.x;
+  const int b = blockIdx.x, d0 = blockIdx.y * COLS, r = threadIdx.x;
   const int2 desc = g.ws.desc[b];
   if (desc.x < 0) return;
   const AttendUnit u = attend_unit<kRows * NQ>(g, desc.x);
   if (r >= u.rows) return;
   const bool joins = part_joins(g, u);
-  float m = -INFINITY, l = 0.f, o[kJoinCols];
+  float m = -INFINITY, l = 0.f, o[COLS];
 #pragma unroll
-  for (int e = 0; e < kJoinCols; ++e) o[e] = 0.f;
+  for (int e = 0; e < COLS; ++e) o[e] = 0.f;
 #pragma unroll 1
-  for (int i0 = b; i0 <= desc.y; i0 += kJoinAhead) {
-    float2 x[kJoinAhead];
-    float y[kJoinAhead][kJoinCols];
+  for (int i0 = b; i0 <= desc.y; i0 += kAhead) {
+    float2 x[kAhead];
+    float y[kAhead][COLS];
 #pragma unroll
-    for (int a = 0; a < kJoinAhead; ++a) {
+    for (int a = 0; a < kAhead; ++a) {
       const int i = i0 + a;
       if (i > desc.y) continue;
       const int piece = i == b ? 2 * b + 1 : 2 * i;
       x[a] = g.ws.stat[piece * kTcRows + r];
       const float* p = g.ws.out + ((long long)piece * D + d0) * kTcRows + r;
 #pragma unroll
-      for (int e = 0; e < kJoinCols; ++e) y[a][e] = p[e * kTcRows];
+      for (int e = 0; e < COLS; ++e) y[a][e] = p[e * kTcRows];
     }
 #pragma unroll
-    for (int a = 0; a < kJoinAhead; ++a) {
+    for (int a = 0; a < kAhead; ++a) {
       if (i0 + a > desc.y) continue;
       const float nm = fmaxf(m, x[a].x), ref = nm == -INFINITY ? 0.f : nm;
       const float f0 = ex2(m - ref);
@@ -1007,10 +1041,130 @@ __global__ void __launch_bounds__(kTcRows) attend_tc_join_kernel(AttendArgs g) {
       l = l * f0 + x[a].y * f1;
       m = nm;
 #pragma unroll
-      for (int e = 0; e < kJoinCols; ++e) o[e] = o[e] * f0 + y[a][e] * f1;
+      for (int e = 0; e < COLS; ++e) o[e] = o[e] * f0 + y[a][e] * f1;
     }
   }
-  finish_features<kJoinCols>(g, u, r, D, d0, o, m, l, joins);
+  finish_features<COLS>(g, u, r, D, d0, o, m, l, joins);
+}
+
+// Whether the own rows' pass left something for a token that shares prefix p: if its sequence's
+// tokens are where they should be and that pass found the same prefix (part_joins).
+__device__ __forceinline__ bool own_part(const AttendArgs& g, int p, int token) {
+  AttendArgs o = g;
+  o.pass = 3;
+  AttendUnit u;
+  if (!g.t.cu_tokens) {
+    u.s = token / g.part.max_tokens;
+    u.first = u.s * g.part.max_tokens;
+    u.n = g.part.max_tokens;
+  } else {
+    int s = g.part.cu_seqs ? g.part.cu_seqs[p] : 0;
+    for (int hi = g.part.cu_seqs ? g.part.cu_seqs[p + 1] : g.part.seqs; hi - s > 1;) {
+      const int mid = (s + hi) / 2;
+      if (g.t.cu_tokens[mid] <= token) s = mid;
+      else hi = mid;
+    }
+    u.s = s;
+    u.first = g.t.cu_tokens[s];
+    const int end = g.t.cu_tokens[s + 1];
+    if (u.first < 0 || token < u.first || token >= end || end > g.t.tokens ||
+        end - u.first > g.part.max_tokens)
+      return false;
+    u.n = end - u.first;
+  }
+  return part_joins(o, u);
+}
+
+// The end where the two passes ran next to each other: the pieces of a unit of the prefixes, or all of
+// it, and what its rows have of their own. A block has kJoinCols features of 256 / GROUPS rows, a thread
+// each, and deals the pieces to GROUPS of those.
+template <int D, int NQ, int GROUPS>
+__global__ void __launch_bounds__(kTcRows) attend_meet_kernel(const __grid_constant__ AttendArgs g) {
+  constexpr int kEach = kTcRows / GROUPS;
+  __shared__ float s_m[GROUPS][kEach], s_l[GROUPS][kEach], s_o[GROUPS][kJoinCols][kEach + 1];
+  const int unit = blockIdx.x, d0 = blockIdx.y * kJoinCols;
+  const int group = threadIdx.x / kEach, mine = threadIdx.x % kEach, r = blockIdx.z * kEach + mine;
+  grid_dep_wait();
+  const AttendUnit u = attend_unit<kRows * NQ>(g, unit);
+  if (blockIdx.z * kEach >= u.rows) return;
+  const int2 desc = g.part.desc[unit];
+  const bool here = r < u.rows;
+  const long long at = part_row(g, u, here ? r : 0);
+  // the own rows' part, while the pieces are on their way
+  float2 own = make_float2(-INFINITY, 0.f);
+  float4 own_o[kJoinCols / 4];
+  bool there = false;
+  if (here && group == 0) {
+    own = g.part.own_stat[at];
+#pragma unroll
+    for (int i = 0; i < kJoinCols / 4; ++i)
+      own_o[i] = reinterpret_cast<const float4*>(g.part.own_out + at * D + d0)[i];
+    there = own_part(g, u.s, u.first + (u.r0 + r) / g.c.group);
+  }
+  float m = -INFINITY, l = 0.f, o[kJoinCols];
+#pragma unroll
+  for (int e = 0; e < kJoinCols; ++e) o[e] = 0.f;
+  if (desc.x < 0) {
+    if (here && group == 0) {
+      const float2 x = g.part.stat[at];
+      m = x.x;
+      l = x.y;
+#pragma unroll
+      for (int e = 0; e < kJoinCols; ++e) o[e] = g.part.out[at * D + d0 + e];
+    }
+  } else {
+#pragma unroll 1
+    for (int i0 = desc.x + group; i0 <= desc.y; i0 += kJoinAhead * GROUPS) {
+      float2 x[kJoinAhead];
+      float y[kJoinAhead][kJoinCols];
+#pragma unroll
+      for (int a = 0; a < kJoinAhead; ++a) {
+        const int i = i0 + a * GROUPS;
+        x[a] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+        for (int e = 0; e < kJoinCols; ++e) y[a][e] = 0.f;
+        if (i > desc.y || !here) continue;
+        const int piece = i == desc.x ? 2 * i + 1 : 2 * i;
+        x[a] = g.ws.stat[piece * kTcRows + r];
+        const float* p = g.ws.out + ((long long)piece * D + d0) * kTcRows + r;
+#pragma unroll
+        for (int e = 0; e < kJoinCols; ++e) y[a][e] = p[e * kTcRows];
+      }
+#pragma unroll
+      for (int a = 0; a < kJoinAhead; ++a) {
+        const float2 k = join_by(m, l, x[a]);
+        l = l * k.x + x[a].y * k.y;
+#pragma unroll
+        for (int e = 0; e < kJoinCols; ++e) o[e] = o[e] * k.x + y[a][e] * k.y;
+      }
+    }
+    if constexpr (GROUPS > 1) {
+      s_m[group][mine] = m;
+      s_l[group][mine] = l;
+#pragma unroll
+      for (int e = 0; e < kJoinCols; ++e) s_o[group][e][mine] = o[e];
+      __syncthreads();
+      if (group == 0)
+#pragma unroll
+        for (int w = 1; w < GROUPS; ++w) {
+          const float2 x = make_float2(s_m[w][mine], s_l[w][mine]), k = join_by(m, l, x);
+          l = l * k.x + x.y * k.y;
+#pragma unroll
+          for (int e = 0; e < kJoinCols; ++e) o[e] = o[e] * k.x + s_o[w][e][mine] * k.y;
+        }
+    }
+  }
+  if (!there) return;                    // no row, no output: its sequence is flagged
+  const float2 k = join_by(m, l, own);
+  l = l * k.x + own.y * k.y;
+#pragma unroll
+  for (int i = 0; i < kJoinCols / 4; ++i) {
+    o[4 * i] = o[4 * i] * k.x + own_o[i].x * k.y;
+    o[4 * i + 1] = o[4 * i + 1] * k.x + own_o[i].y * k.y;
+    o[4 * i + 2] = o[4 * i + 2] * k.x + own_o[i].z * k.y;
+    o[4 * i + 3] = o[4 * i + 3] * k.x + own_o[i].w * k.y;
+  }
+  finish_output<kJoinCols>(g, u, r, D, d0, o, m, l);
 }
 
 // Rows of head_dim bf16 values in boxes of 64 features x a page (or a tile); false if the
@@ -1056,7 +1210,12 @@ cudaError_t launch_t(AttendArgs& g, cudaStream_t st, int* launches) {
                    dim3(Plan<D, NQ, IMAGE>::kThreads), smem, st, map_k, map_v, maps, g);
   if (e != cudaSuccess) return e;
   note_launch(st, launches, "attend_tc");
-  e = launch_after(attend_tc_join_kernel<D, NQ>, dim3(grid, D / kJoinCols), dim3(kTcRows), 0, st, g);
+  if (g.pass == 1) return e;        // launch_attend_meet
+  if (units * 2 <= kSms)
+    e = launch_after(attend_tc_join_kernel<D, NQ, kJoinCols>, dim3(grid, D / kJoinCols),
+                     dim3(kTcRows), 0, st, g);
+  else
+    e = launch_after(attend_tc_join_kernel<D, NQ, 32>, dim3(grid, D / 32), dim3(kTcRows), 0, st, g);
   if (e == cudaSuccess) note_launch(st, launches, "attend_tc_join");
   return e;
 }
@@ -1098,6 +1257,38 @@ cudaError_t launch_attend_tc(AttendArgs& g, cudaStream_t st, int* launches) {
   if (g.c.head_dim == 128)
     return two ? launch_t<128, 2>(g, st, launches) : launch_t<128, 1>(g, st, launches);
   return two ? launch_t<64, 2>(g, st, launches) : launch_t<64, 1>(g, st, launches);
+}
+
+size_t attend_tc_units(const nx_cache& c, const nx_tokens& t) {
+  const long long all = most_tokens(t) * c.group, rows = kRows * (all > kRows ? 2 : 1);
+  return (size_t)c.seqs * c.kv_heads * ((all + rows - 1) / rows);
+}
+
+namespace {
+template <int D, int NQ>
+cudaError_t launch_meet(const AttendArgs& g, cudaStream_t st) {
+  // As many groups as leave about two blocks an SM. Both passes, in us, with 1, 2, 4 and 8 groups: 1
+  // unit of 152 pieces 41, 33, 29, 27; 8 units of 19, 128 rows 54, 54, 53, 55, 256 rows 64, 60, 60, 62;
+  // 32 units, 128 rows 32, 32, 35, 41.
+  int groups = 8;
+  while (groups > (NQ == 1 ? 2 : 1) &&
+         (long long)g.units * (D / kJoinCols) * (kRows * NQ * groups / kTcRows) > 2 * kSms)
+    groups /= 2;
+  const dim3 grid(g.units, D / kJoinCols, kRows * NQ * groups / kTcRows), block(kTcRows);
+  return groups == 8   ? launch_after(attend_meet_kernel<D, NQ, 8>, grid, block, 0, st, g)
+         : groups == 4 ? launch_after(attend_meet_kernel<D, NQ, 4>, grid, block, 0, st, g)
+         : groups == 2 ? launch_after(attend_meet_kernel<D, NQ, 2>, grid, block, 0, st, g)
+                       : launch_after(attend_meet_kernel<D, NQ, 1>, grid, block, 0, st, g);
+}
+}  // namespace
+
+cudaError_t launch_attend_meet(const AttendArgs& g, cudaStream_t st, int* launches) {
+  const bool two = most_tokens(g.t) * g.c.group > kRows;
+  const cudaError_t e = g.c.head_dim == 128
+                            ? (two ? launch_meet<128, 2>(g, st) : launch_meet<128, 1>(g, st))
+                            : (two ? launch_meet<64, 2>(g, st) : launch_meet<64, 1>(g, st));
+  if (e == cudaSuccess) note_launch(st, launches, "attend_meet");
+  return e;
 }
 
 }  // namespace nx

@@ -607,6 +607,19 @@ def test_shared_query_rows(kind, causal, seqs, tokens):
     _check_shared(own, pre, None, [tokens] * seqs, causal=causal)
 
 
+@pytest.mark.parametrize("image", ["none", "own", "both"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("rows", [20, 900])
+def test_shared_chunks_of_long_slices(rows, d, image):
+    # own slices with many query rows, behind a prefix of few rows and of many: both of its parts by
+    # either kernel
+    own, pre = _pair("bf16", 3, 1, [[1400, 1201], [1399, 96], [1100, 1340]], [[rows, rows - 5]], d=d,
+                     page=16)
+    _, _, names = _check_shared(own, pre, None, [96, 95, 60], image=image != "none",
+                                pre_image=image == "both")
+    assert "attend_tc_join" in names and ("attend_meet" in names) == (rows == 900)
+
+
 @pytest.mark.parametrize("kind", ["bf16", "f32"])
 @pytest.mark.parametrize("page,pre_page", [(8, 8), (16, 0), (0, 16), (32, 64), (128, 128)])
 def test_shared_several_prefixes_ragged_and_paged(kind, page, pre_page):
