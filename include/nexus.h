@@ -440,7 +440,7 @@ size_t nexus_attend_shared_workspace_bytes(const nx_cache* cache, const nx_token
  * Everything else is as in nexus_attend, for either part by itself: images, flagged slices and
  * pages, rows that are not finite, the kernels taken (the prefix part has the rows of all the
  * tokens that share it, max_tokens of nx_shared times group, at most) and what they round. The two
- * parts meet in binary32. Three or more launches.
+ * parts meet in binary32. Two launches or more.
  * A prefix whose entries of cu_seqs decrease or leave [0, seqs], or whose tokens are more than
  * nx_shared.max_tokens (NX_DEV_BAD_TOKENS), counts as empty.
  */

@@ -22,6 +22,21 @@ struct AttendWs {
   float* out;          // [2 * blocks][rows x head_dim] unnormalised output
 };
 
+struct AttendArgs {
+  nx_cache c;
+  nx_tokens t;
+  nx_image im;          // im.k null: no image
+  nx_attend a;
+  int32_t* dev_status;
+  AttendWs ws;
+  int b, b_shift;       // rows per image block, a power of two
+  int mtiles;           // row tiles per slice
+  int ranks;            // row kernel: thread blocks per unit, one cluster (0: even shares)
+  int splits;           // its join: blocks per unit (0: a block for each block's last unit)
+  int units;            // seqs * kv_heads * mtiles
+  float c1;             // scale * log2(e)
+};
+
 // Where the two passes of nexus_attend_shared meet. Either the own rows' pass takes in what the
 // prefixes' has of a query row when it finishes the row (pass 2 after 1), or, with the prefixes on the
 // tensor cores, the two run next to each other and a last kernel joins what both have (pass 3 next
@@ -39,22 +54,12 @@ struct AttendPart {
   int tile_cost, row_cost;      // ns of an SM for a tile of a prefix, for a row of an own slice
 };
 
-struct AttendArgs {
-  nx_cache c;           // pass 1: the prefixes' cache, a "sequence" each
-  nx_tokens t;
-  nx_image im;          // im.k null: no image
-  nx_attend a;
-  int32_t* dev_status;
-  AttendWs ws;
-  int b, b_shift;       // rows per image block, a power of two
-  int mtiles;           // row tiles per slice
-  int ranks;            // row kernel: thread blocks per unit, one cluster (0: even shares)
-  int splits;           // its join: blocks per unit (0: a block for each block's last unit)
-  int units;            // seqs * kv_heads * mtiles
-  float c1;             // scale * log2(e)
-  int pass;             // 0: a call by itself, 1: the prefixes, 2, 3: the sequences' own rows
+// A pass of nexus_attend_shared. (Of a type of its own, as are the kernels that take it: nexus_attend's
+// have fewer arguments and branches, and its shortest calls were 0.3 to 0.5 of 6 to 9 us slower with.)
+struct SharedArgs : AttendArgs {       // c of pass 1: the prefixes' cache, a "sequence" each
+  int pass;             // 1: the prefixes, 2, 3: the sequences' own rows
   bool brief;           // row kernel: a warp per unit
-  AttendPart part;      // not of pass 0
+  AttendPart part;
 };
 
 // Unit (slice of the layer, row tile): up to `rows` query rows (row r = token r / group, head
@@ -73,7 +78,7 @@ __device__ __forceinline__ int row_limit(const AttendArgs& g, const AttendUnit& 
 
 // The rows of the per-token arrays that share prefix p: [first, first + return value); -1 if the
 // sequences or tokens that it names are out of range.
-__device__ __forceinline__ int shared_tokens(const AttendArgs& g, int p, int& first) {
+__device__ __forceinline__ int shared_tokens(const SharedArgs& g, int p, int& first) {
   const AttendPart& x = g.part;
   const int s0 = x.cu_seqs ? x.cu_seqs[p] : 0, s1 = x.cu_seqs ? x.cu_seqs[p + 1] : x.seqs;
   first = 0;
@@ -91,13 +96,21 @@ __device__ __forceinline__ int shared_tokens(const AttendArgs& g, int p, int& fi
   return n > x.max_shared ? -1 : (int)n;
 }
 
-template <int ROWS>
-__device__ __forceinline__ AttendUnit attend_unit(const AttendArgs& g, int id) {
+// The tokens of a unit's sequence, or of those that share its prefix.
+__device__ __forceinline__ int unit_tokens(const AttendArgs& g, int s, int& first) {
+  return tokens_of(g.t, s, first);
+}
+__device__ __forceinline__ int unit_tokens(const SharedArgs& g, int s, int& first) {
+  return g.pass == 1 ? shared_tokens(g, s, first) : tokens_of(g.t, s, first);
+}
+
+template <int ROWS, typename Args>
+__device__ __forceinline__ AttendUnit attend_unit(const Args& g, int id) {
   AttendUnit u;
   const int mt = id % g.mtiles, sl = id / g.mtiles;
   u.h = sl % g.c.kv_heads;
   u.s = sl / g.c.kv_heads;
-  u.n = g.pass == 1 ? shared_tokens(g, u.s, u.first) : tokens_of(g.t, u.s, u.first);
+  u.n = unit_tokens(g, u.s, u.first);
   if (u.n < 0) {
     atomicOr(g.dev_status, NX_DEV_BAD_TOKENS);
     u.n = 0;
@@ -123,7 +136,8 @@ __device__ __forceinline__ AttendUnit attend_unit(const AttendArgs& g, int id) {
 // Whether the prefixes' pass has something for the rows of a unit of sequences' own rows: its
 // sequence's prefix is the last that starts at or before it, if that one reaches so far and all of
 // the unit's tokens were among that one's.
-__device__ __forceinline__ bool part_joins(const AttendArgs& g, const AttendUnit& u) {
+__device__ __forceinline__ bool part_joins(const AttendArgs&, const AttendUnit&) { return false; }
+__device__ __forceinline__ bool part_joins(const SharedArgs& g, const AttendUnit& u) {
   const AttendPart& x = g.part;
   if (g.pass < 2 || u.n <= 0) return false;
   int p = 0;
@@ -144,16 +158,29 @@ __device__ __forceinline__ bool part_joins(const AttendArgs& g, const AttendUnit
 // came before the call is done. As pass 2 the own rows' needs them only where a row is finished, and
 // all of its thread blocks wait there; as pass 3 it does not, and its last block waits alone. When it
 // is done, so are they.
-__device__ __forceinline__ void begin_pass(const AttendArgs& g) {
-  if (g.pass <= 1) grid_dep_wait();
+__device__ __forceinline__ void begin_pass(const AttendArgs&) { grid_dep_wait(); }
+__device__ __forceinline__ void begin_pass(const SharedArgs& g) {
+  if (g.pass == 1) grid_dep_wait();
   if (g.pass & 1) grid_dep_trigger();
 }
-__device__ __forceinline__ void meet_pass(const AttendArgs& g) {
+__device__ __forceinline__ void meet_pass(const AttendArgs&) {}
+__device__ __forceinline__ void meet_pass(const SharedArgs& g) {
   if (g.pass == 2) grid_dep_wait();
 }
-__device__ __forceinline__ void end_pass(const AttendArgs& g) {
+__device__ __forceinline__ void end_pass(const AttendArgs&) {}
+__device__ __forceinline__ void end_pass(const SharedArgs& g) {
   if (g.pass == 2 || (g.pass == 3 && blockIdx.x == gridDim.x - 1)) grid_dep_wait();
 }
+// Of their joins: the prefixes' lets the next kernel be scheduled like the rest of its pass.
+__device__ __forceinline__ void begin_join(const AttendArgs&) { grid_dep_wait(); }
+__device__ __forceinline__ void begin_join(const SharedArgs& g) {
+  if (g.pass == 1) grid_dep_trigger();
+  grid_dep_wait();
+}
+template <typename Args>
+constexpr bool kShared = false;
+template <>
+constexpr bool kShared<SharedArgs> = true;
 
 // Row r of a unit among all rows of the call.
 __device__ __forceinline__ long long part_row(const AttendArgs& g, const AttendUnit& u, int r) {
@@ -316,10 +343,22 @@ inline long long most_tokens(const nx_tokens& t) {
 // another capacity or from an image.
 bool attend_tc_takes(const nx_cache& c, const nx_tokens& t, bool image);
 bool attend_tc_may_take(const nx_cache& c, const nx_tokens& t);
+bool shared_tc_takes(const SharedArgs& g);
 size_t attend_tc_layout(int D, char* base, AttendWs* ws);
 size_t attend_tc_units(const nx_cache& c, const nx_tokens& t);
 cudaError_t launch_attend_tc(AttendArgs& g, cudaStream_t st, int* launches);
+cudaError_t launch_attend_tc(SharedArgs& g, cudaStream_t st, int* launches);
 // The end of nexus_attend_shared where the passes ran next to each other; g: the prefixes' pass.
-cudaError_t launch_attend_meet(const AttendArgs& g, cudaStream_t st, int* launches);
+cudaError_t launch_attend_meet(const SharedArgs& g, cudaStream_t st, int* launches);
+
+// nx_attend.cu: what nexus_attend and nexus_attend_shared check of a cache and the tokens that look
+// into it, and of the rest; the workspace of a pass (whichever kernel takes it), and its arguments.
+nx_status attend_limits(const nx_cache& c, const nx_tokens& t, const nx_image* image);
+nx_status attend_pointers(const nx_cache& c, const nx_tokens& t, const nx_attend& a,
+                          int32_t* dev_status);
+size_t attend_bytes(const nx_cache& c, const nx_tokens& t);
+size_t attend_layout(int D, char* base, AttendWs* ws);
+void attend_args(AttendArgs* g, const nx_cache& c, const nx_tokens& t, const nx_image* image,
+                 const nx_attend& a, int32_t* dev_status);
 
 }  // namespace nx
