@@ -425,13 +425,8 @@ __device__ __forceinline__ void finish_features(const Args& g, const AttendUnit&
 // (64 sequences, 4 heads each of 8 groups, 32768 rows of prefix, 512 to 1024 of their own: XX us one
 // behind the other.)
 template <int THREADS>
-__device__ __forceinline__ int beside_blocks(const AttendArgs&, int) {
-  return gridDim.x;
-}
-template <int THREADS>
-__device__ __forceinline__ int beside_blocks(const SharedArgs& g, int total) {
+__device__ __forceinline__ int beside_blocks(const SharedArgs& g, int total, float* s_rows) {
   if (g.pass != 1 || !g.part.desc || !g.part.row_cost) return gridDim.x;
-  __shared__ float s_rows[THREADS / 32];
   const int n = g.part.seqs * g.c.kv_heads;
   float rows = 0.f;
   for (int i = threadIdx.x; i < n; i += THREADS) rows += (float)max(0, g.part.own_lens[i]);
@@ -445,6 +440,39 @@ __device__ __forceinline__ int beside_blocks(const SharedArgs& g, int total) {
   const float here = (float)total * g.part.tile_cost, there = rows * g.part.row_cost;
   const int blocks = (int)(kSms * (here / (here + there + 1.f)) + 0.5f);
   return min((int)gridDim.x, max(blocks, kSms / 4));
+}
+
+// Few units: shares of whole blocks for each of them, where that makes no share longer by more than
+// kAlignMore tiles. A block whose share goes on in a second unit ends one piece and starts another,
+// which costs as much as seven tiles. `last`: of the blocks that have this one's unit; -1: shares stay as
+// they are. tiles: of each unit; *best starts at INT_MAX.
+constexpr int kAlignUnits = 64, kAlignMore = 8;
+__device__ __forceinline__ void align_share(const SharedArgs& g, const int* tiles, int* best,
+                                            int blocks, AttendShare& x, int& last) {
+  if (g.pass != 1 || g.units > kAlignUnits || g.units > blocks) return;
+  if (threadIdx.x < kAlignMore) {
+    const int per = x.per + threadIdx.x;
+    int n = 0;
+    for (int u = 0; u < g.units; ++u) n += (tiles[u] + per - 1) / per;
+    if (n <= blocks) atomicMin(best, per);
+  }
+  __syncthreads();
+  if (*best == 0x7FFFFFFF) return;
+  x.per = *best;
+  x.start = x.stop = x.total;
+  for (int u = 0, first = 0, at = 0; u < g.units; ++u) {
+    const int n = (tiles[u] + x.per - 1) / x.per, b = blockIdx.x - first;
+    if (b < n) {
+      x.unit = u;
+      x.at = at;
+      x.start = at + b * x.per;
+      x.stop = min(at + tiles[u], x.start + x.per);
+      last = first + n - 1;
+      break;
+    }
+    first += n;
+    at += tiles[u];
+  }
 }
 
 template <int D, int NQ, bool IMAGE, typename Args>
@@ -496,13 +524,27 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
     bar_init(drained, 2);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     s_up = 0;
+    if constexpr (kShared<Args>) reinterpret_cast<int*>(s_l)[kRows - 1] = 0x7FFFFFFF;
   }
   if (tid < 16) s_hot[tid / 8][tid % 8] = 0;
   begin_pass(g);
   tc_before();
-  const AttendShare sh = attend_share<kThreads>(
-      g, [&](int i) { return tc_tiles<NQ>(attend_unit<kRows * NQ>(g, i)); },
-      [&](int total) { return beside_blocks<kThreads>(g, total); });
+  int blocks = gridDim.x, last = -1;
+  int* const s_tiles = reinterpret_cast<int*>(s_m);      // (s_m and s_l are the results', later)
+  AttendShare sh = attend_share<kThreads>(
+      g,
+      [&](int i) {
+        const int n = tc_tiles<NQ>(attend_unit<kRows * NQ>(g, i));
+        if constexpr (kShared<Args>)
+          if (i < kAlignUnits) s_tiles[i] = n;
+        return n;
+      },
+      [&](int total) {
+        if constexpr (kShared<Args>) blocks = beside_blocks<kThreads>(g, total, s_l);
+        return blocks;
+      });
+  if constexpr (kShared<Args>)
+    align_share(g, s_tiles, reinterpret_cast<int*>(s_l) + kRows - 1, blocks, sh, last);
   tc_after();
   grid_dep_trigger();
   const uint32_t tmem = s_tmem;
@@ -997,7 +1039,8 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
       if (a0 == 0 && a1 < tiles) desc = make_int2(unit, (at + tiles - 1) / sh.per);
       if constexpr (kShared<Args>)
         if (g.pass == 1 && a0 == 0 && tid == 0)
-          g.part.desc[unit] = make_int2(a1 < tiles ? b : -1, (at + tiles - 1) / sh.per);
+          g.part.desc[unit] = make_int2(a1 < tiles ? b : -1,
+                                        last >= 0 ? last : (at + tiles - 1) / sh.per);
       // the next piece's loads and products come after this one's results
       __syncwarp();
       __syncthreads();

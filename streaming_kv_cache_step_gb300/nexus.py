@@ -657,11 +657,23 @@ def _packed_cache(c: Cache, dev: int) -> bytes:
 
 
 def _packed_image(image: Image | None, cache: Cache, dev: int) -> bytes | None:
+    """nx_image of an image of that cache, or None."""
     if image is None:
         return None
-    if image.k.get_device() != dev:
-        raise ValueError("the image must be on the current GPU")
-    return bytes(image.c_struct(cache))
+    k, v, ks, vs, rows = image.k, image.v, image.k_scale, image.v_scale, image.rows
+    for t in (k, v, ks, vs, rows):
+        if t.get_device() != dev or not t.is_contiguous():
+            raise ValueError("image tensors must be contiguous and on the current GPU")
+    if k.dtype is not torch.float8_e4m3fn or v.dtype is not torch.float8_e4m3fn or \
+            ks.dtype is not torch.float32 or vs.dtype is not torch.float32 or \
+            rows.dtype is not torch.int32:
+        raise ValueError("image k and v must be float8_e4m3fn, scales float32, rows int32")
+    n, b, slices = cache.k.numel(), image_block(cache), cache.n_slices
+    blocks = n // cache.head_dim // b if cache.page_size else slices * (-(-cache.capacity // b))
+    if k.numel() != n or v.numel() != n or rows.numel() != slices or ks.numel() != blocks or \
+            vs.numel() != blocks:
+        raise ValueError("image sizes do not fit the cache")
+    return _IMAGE.pack(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), rows.data_ptr())
 
 
 def _raw(stream, dev: int) -> int | None:
@@ -722,7 +734,7 @@ def attend_shared(cache: Cache, layer: int, q, out, ws, dev_status, *, prefix: C
                      cache.head_dim ** -0.5 if scale is None else scale, bool(causal))
     x, _keep = _packed_shared(prefix, prefix_image, cu_seqs, max_shared, dev)
     cu = 0 if cu_tokens is None else _ints(cu_tokens, cache.seqs + 1, "cu_tokens", dev)
-    status = load().nexus_attend_shared(
+    status = (_lib or load()).nexus_attend_shared(
         c, _TOKENS.pack(layer, n, max_tokens, 0, cu), _packed_image(image, cache, dev), x, a,
         ws.data_ptr(), ws.numel(), _ints(dev_status, 1, "dev_status", dev), _raw(stream, dev))
     if status:
@@ -782,7 +794,7 @@ def plan(cache: Cache, pool: Pool | None, new_tokens, cu_tokens, dev_status, *, 
                        0 if held_in is None else _ints(held_in, S, "held_in", dev))
     elif held_in is not None or free_count_in is not None:
         raise ValueError("held_in and free_count_in go with a pool")
-    status = load().nexus_plan(_packed_cache(cache, dev), x, a, _packed_image(image, cache, dev),
+    status = (_lib or load()).nexus_plan(_packed_cache(cache, dev), x, a, _packed_image(image, cache, dev),
                                _ints(dev_status, 1, "dev_status", dev), _raw(stream, dev))
     if status:
         raise NexusError(status, "nexus_plan")
@@ -817,7 +829,7 @@ def verify(cache: Cache, token, p, u, u_draw, out, emitted, dev_status, *, max_t
                      0 if lens_in is None else _ints(lens_in, cache.n_slices, "lens_in", dev),
                      vocab, DTYPE_BF16 if kind is torch.bfloat16 else DTYPE_F32, 0)
     cu = 0 if cu_tokens is None else _ints(cu_tokens, S + 1, "cu_tokens", dev)
-    status = load().nexus_verify(_packed_cache(cache, dev), _TOKENS.pack(0, n, max_tokens, 0, cu),
+    status = (_lib or load()).nexus_verify(_packed_cache(cache, dev), _TOKENS.pack(0, n, max_tokens, 0, cu),
                                  a, _packed_image(image, cache, dev),
                                  _ints(dev_status, 1, "dev_status", dev), _raw(stream, dev))
     if status:

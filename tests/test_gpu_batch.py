@@ -607,6 +607,20 @@ def test_shared_query_rows(kind, causal, seqs, tokens):
     _check_shared(own, pre, None, [tokens] * seqs, causal=causal)
 
 
+@pytest.mark.parametrize("image", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("each", [5, 20, 40])
+@pytest.mark.parametrize("lens", [[[4200, 4096]], [[4500, 0], [1, 4200], [64, 4097]]], ids=["one", "three"])
+def test_shared_prefixes_on_the_tensor_cores(lens, each, d, image):
+    # 20, 80 and 160 query rows to a prefix, whole shares of blocks for units of any length
+    P = len(lens)
+    rng = np.random.default_rng(each)
+    own, pre = _pair("bf16", P * each, P, rng.integers(1, 40, (P * each, 2)), lens, d=d, page=16)
+    groups = [each * i for i in range(P + 1)]
+    _, _, names = _check_shared(own, pre, groups, [1] * (P * each), pre_image=image)
+    assert names[0] == "attend_tc" and names[-1] == "attend_meet"
+
+
 @pytest.mark.parametrize("image", ["none", "own", "both"])
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("rows", [20, 900])
