@@ -442,7 +442,8 @@ size_t nexus_attend_shared_workspace_bytes(const nx_cache* cache, const nx_token
  * tokens that share it, max_tokens of nx_shared times group, at most) and what they round. The two
  * parts meet in binary32. Two launches or more.
  * A prefix whose entries of cu_seqs decrease or leave [0, seqs], or whose tokens are more than
- * nx_shared.max_tokens (NX_DEV_BAD_TOKENS), counts as empty.
+ * nx_shared.max_tokens (NX_DEV_BAD_TOKENS), counts as empty; where cu_seqs decreases a sequence that
+ * it gives to two prefixes has one of them.
  */
 nx_status nexus_attend_shared(const nx_cache* cache, const nx_tokens* tokens,
                               const nx_image* image, const nx_shared* shared,
@@ -470,7 +471,8 @@ typedef struct nx_pool {
 
 typedef struct nx_plan {
   const int32_t* new_tokens;   /* [seqs] tokens that each sequence brings next; < 0: it ends */
-  const int32_t* first_pos;    /* [seqs] position of the first of them; NULL with token_pos */
+  const int32_t* first_pos;    /* [seqs] position of the first of them (no part of token_pos);
+                                  NULL with token_pos */
   int32_t* cu_tokens;          /* [seqs + 1] */
   int32_t* token_seq;          /* nullable [tokens] */
   int32_t* token_pos;          /* nullable [tokens] */
@@ -512,7 +514,7 @@ nx_status nexus_plan(nx_cache* cache, const nx_pool* pool, const nx_plan* plan,
  * the draft and 0 elsewhere.
  */
 typedef struct nx_verify {
-  const int32_t* token;        /* [tokens] */
+  const int32_t* token;        /* [tokens]; may not overlap out */
   const void* p;               /* [tokens][vocab] */
   const void* q;               /* nullable [tokens][vocab] */
   int64_t p_stride, q_stride;  /* elements between rows, any; rows need no alignment */

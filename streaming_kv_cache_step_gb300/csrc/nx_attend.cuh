@@ -160,7 +160,9 @@ __device__ __forceinline__ bool part_joins(const SharedArgs& g, const AttendUnit
 // is done, so are they.
 __device__ __forceinline__ void begin_pass(const AttendArgs&) { grid_dep_wait(); }
 __device__ __forceinline__ void begin_pass(const SharedArgs& g) {
+  // what came before the call is complete when pass 1 lets the others go: seen from here with a fence
   if (g.pass == 1) grid_dep_wait();
+  else __threadfence();
   if (g.pass & 1) grid_dep_trigger();
 }
 __device__ __forceinline__ void meet_pass(const AttendArgs&) {}

@@ -422,7 +422,7 @@ __device__ __forceinline__ void finish_features(const Args& g, const AttendUnit&
 
 // How many thread blocks share the tiles. With the sequences' own rows next to them: a part of the
 // GPU that goes by what both cost; the other blocks end at once, and their SMs are the other pass's.
-// (64 sequences, 4 heads each of 8 groups, 32768 rows of prefix, 512 to 1024 of their own: XX us one
+// (64 sequences, 4 heads each of 8 groups, 32768 rows of prefix, 512 to 1024 of their own: 81 us, 99 one
 // behind the other.)
 template <int THREADS>
 __device__ __forceinline__ int beside_blocks(const SharedArgs& g, int total, float* s_rows) {
@@ -1078,7 +1078,7 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
 // Joins the pieces of the unit that starts in block blockIdx.x and ends in a later one:
 // kJoinCols features of it, a thread per row. Units can be few and of many pieces (64 tokens over 8
 // slices: 8 of 19), so a block has few features, and the loads of kJoinAhead pieces are under way at
-// once (with 32 features a block and a piece at a time 62 us for those, of which now XX).
+// once (with 32 features a block and a piece at a time those took 62 us in all, now 25).
 constexpr int kJoinCols = 8, kJoinAhead = 4;
 template <int D, int NQ, int COLS, typename Args>
 __global__ void __launch_bounds__(kTcRows) attend_tc_join_kernel(Args g) {

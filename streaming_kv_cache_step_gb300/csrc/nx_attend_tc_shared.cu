@@ -45,7 +45,8 @@ __global__ void __launch_bounds__(kTcRows) attend_meet_kernel(const __grid_const
   grid_dep_wait();
   const AttendUnit u = attend_unit<kRows * NQ>(g, unit);
   if (blockIdx.z * kEach >= u.rows) return;
-  const int2 desc = g.part.desc[unit];
+  int2 desc = g.part.desc[unit];
+  desc.y = min(desc.y, kTcGrid - 1);     // (its pieces exist, whatever gave up)
   const bool here = r < u.rows;
   const long long at = part_row(g, u, here ? r : 0);
   // the own rows' part, while the pieces are on their way

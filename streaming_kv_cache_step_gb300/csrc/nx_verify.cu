@@ -397,6 +397,8 @@ extern "C" nx_status nexus_verify(nx_cache* cache, const nx_tokens* tokens, cons
   if (a.p_stride < 0 || a.q_stride < 0 || !a.emitted) return NX_ERR_INVALID_ARG;
   if (tokens->tokens > 0 && (!a.token || !a.p || !a.u || !a.u_draw || !a.out))
     return NX_ERR_INVALID_ARG;
+  if (a.token && a.token < a.out + tokens->tokens && a.out < a.token + tokens->tokens)
+    return NX_ERR_INVALID_ARG;
   const long long slices = (long long)cache->layers * cache->seqs * cache->kv_heads;
   if (a.lens_in && a.lens_in != cache->lens && a.lens_in < cache->lens + slices &&
       cache->lens < a.lens_in + slices)

@@ -82,7 +82,8 @@ def _verify(lib, cache=None, tok=None, image=None, status=STATUS, **over):
     dict(status=None), dict(dtype=2), dict(reserved=1), dict(vocab=0), dict(p=None),
     dict(p=0x200002), dict(q=0x300001), dict(token=None), dict(u=None), dict(u_draw=None),
     dict(out=None), dict(emitted=None), dict(p_stride=-1), dict(q_stride=-4), dict(u=0x400002),
-    dict(lens_in=0x40004), dict(lens_in=0x40002), dict(image="bad")])
+    dict(lens_in=0x40004), dict(lens_in=0x40002), dict(image="bad"), dict(out=0x100000),
+    dict(out=0x100004), dict(out=0xFFFFC)])
 def test_verify_refuses(lib, bad):
     from streaming_kv_cache_step_gb300 import nexus
     if bad.get("image") == "bad":

@@ -1005,3 +1005,54 @@ def test_calls_on_another_stream():
         nexus.verify(bare, out.clone(), p, u, u, out, em, st, max_tokens=1, cu_tokens=cu)
     other.synchronize()
     assert int(st.item()) == 0 and pos.cpu().tolist() == [4, 5] and em.cpu().tolist() == [1, 1]
+
+
+@pytest.mark.parametrize("prefix_rows,seqs", [(40, 6), (4200, 24), (300, 40)])
+def test_steps_of_many_layers_without_a_pause(prefix_rows, seqs):
+    # append and attend_shared of three layers and five steps in a row, one workspace, against the
+    # same with a pause behind every call; then from a graph. Nothing may run ahead of what it reads
+    # or overwrite what somebody still reads: the bits are the same.
+    def run(how):
+        own, pre = _pair("bf16", seqs, 1, 30, prefix_rows, layers=3, page=16)
+        g = torch.Generator(device=DEV).manual_seed(3)
+        own = Case(seqs=seqs, kv_heads=2, group=4, layers=3, page=16, capacity=64, lens=30, seed=1)
+        cache, prefix, st = own.device_cache(), pre.device_cache(), _status()
+        cache.k.nan_to_num_(), cache.v.nan_to_num_()
+        x = torch.randn(5, 3, seqs, 12, 128, generator=g, device=DEV).to(BF)
+        pos = torch.full((seqs,), 7, dtype=torch.int32, device=DEV)
+        rot = torch.empty(seqs, 8, 128, dtype=BF, device=DEV)
+        out = torch.zeros(5, 3, seqs, 8, 128, dtype=BF, device=DEV)
+        ws = nexus.alloc_attend_shared_workspace(cache, prefix, tokens=seqs, max_tokens=1,
+                                                 max_shared=seqs)
+
+        def steps():
+            for i in range(5):
+                for l in range(3):
+                    p = x[i, l]
+                    nexus.append(cache, l, p[:, :8], p[:, 8:10], p[:, 10:], pos, rot, st, max_tokens=1)
+                    if how == "paused":
+                        torch.cuda.synchronize()
+                    nexus.attend_shared(cache, l, rot, out[i, l], ws, st, prefix=prefix, max_tokens=1,
+                                        max_shared=seqs)
+                    if how == "paused":
+                        torch.cuda.synchronize()
+        if how == "graph":
+            lens = cache.lens.clone()
+            graph = torch.cuda.CUDAGraph()
+            steps()
+            torch.cuda.synchronize()
+            with torch.cuda.graph(graph):
+                steps()
+            for _ in range(3):
+                cache.lens.copy_(lens)
+                out.zero_()
+                graph.replay()
+        else:
+            steps()
+        torch.cuda.synchronize()
+        assert int(st.item()) == 0 and torch.all(cache.lens == 35)
+        return out
+    want = run("paused")
+    assert torch.all(torch.isfinite(want)) and want.abs().max() > 0
+    for how in ("straight", "straight", "graph"):
+        assert torch.equal(run(how), want), how
