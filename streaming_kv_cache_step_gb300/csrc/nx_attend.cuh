@@ -52,6 +52,7 @@ struct AttendPart {
   int2* desc;          // by unit: its first and last block, or (-1, 0): one block's
   const int32_t* own_lens;      // the layer's lengths of the cache, seqs * kv_heads of them
   int tile_cost, row_cost;      // ns of an SM for a tile of a prefix, for a row of an own slice
+  int room;            // or the SMs that hold all blocks of the own rows' pass
 };
 
 // A pass of nexus_attend_shared. (Of a type of its own, as are the kernels that take it: nexus_attend's

@@ -155,14 +155,15 @@ extern "C" nx_status nexus_attend_shared(const nx_cache* cache, const nx_tokens*
     g.part.desc = desc;
     g.part.own_lens = cache->lens + (long long)tokens->layer * cache->seqs * cache->kv_heads;
     // What the tensor-core kernel deals out the SMs by: a tile of a prefix takes one of them 1.5 us
-    // (3.5 from 8-bit rows), a row of 128 features and 16 query rows of the other pass 10 ns (6). With
-    // fewer blocks than two an SM, or of a launch that counts on all SMs, a part of them is no gain:
-    // 128 slices of 2048 rows next to 16384 slots, 54 us, not 60.
+    // (3.5 from 8-bit rows), a row of 128 features and 16 query rows of the other pass 10 ns (6). That
+    // is no gain next to fewer blocks than two an SM (128 slices of 2048 rows next to 16384 slots, 54
+    // us, not 60), which get room for all of them or none, or to a launch that counts on all SMs.
     const long long rows = most_tokens(*tokens) * cache->group, passes = (rows + 15) / 16;
     const long long cost = (image ? 6 : 10) * passes * cache->head_dim / 128 + 1;
     const long long blocks = cache->head_dim == 128 ? free_blocks<128>(o) : free_blocks<64>(o);
     g.part.tile_cost = shared->image ? 3500 : 1500;
-    g.part.row_cost = blocks < 2 * kSms ? 0 : (int)(cost < 1000 ? cost : 1000);
+    if (blocks >= 2 * kSms) g.part.row_cost = (int)(cost < 1000 ? cost : 1000);
+    else g.part.room = (int)(blocks + 1) / 2;
   }
   cudaError_t e = launch_pass(g, st, &launches);
   if (e == cudaSuccess) e = launch_pass(o, st, &launches);

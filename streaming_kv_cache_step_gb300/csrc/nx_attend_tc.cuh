@@ -1,5 +1,6 @@
-// nx_attend_tc.cuh -- nexus_attend and nexus_attend_shared for many query rows per slice (prompt chunks, drafts of
-// several tokens): the same softmax as nx_attend_rows.cuh on the 5th-generation tensor cores.
+// nx_attend_tc.cuh -- nexus_attend and nexus_attend_shared for many query rows per slice (prompt chunks,
+// drafts of several tokens, prefixes that many sequences share): the same softmax as nx_attend_rows.cuh on
+// the 5th-generation tensor cores.
 //
 // A thread block holds two streams of 128 query rows (thread = row): two row tiles that share
 // each tile of 64 slots of K and V, or, for slices with up to 128 rows, one row tile whose
@@ -421,12 +422,25 @@ __device__ __forceinline__ void finish_features(const Args& g, const AttendUnit&
 }
 
 // How many thread blocks share the tiles. With the sequences' own rows next to them: a part of the
-// GPU that goes by what both cost; the other blocks end at once, and their SMs are the other pass's.
+// GPU that goes by what both cost; the other blocks end at once, and their SMs are the other pass's
 // (64 sequences, 4 heads each of 8 groups, 32768 rows of prefix, 512 to 1024 of their own: 81 us, 99 one
 // behind the other.)
+// Where the others are fewer blocks than fit the GPU at once, they get room for all of them if that
+// costs this pass less than 4 us (16 sequences behind 4096 rows, 128 of their own: 19.9 us, not 24.6).
+__device__ __forceinline__ int part_of_sms(const SharedArgs& g, int total, float rows) {
+  if (g.part.room) {
+    const int left = kSms - g.part.room;
+    const float cost = (float)total * g.part.tile_cost;
+    return left >= kSms / 4 && cost / left - cost / kSms < 4000.f ? min((int)gridDim.x, left)
+                                                                  : gridDim.x;
+  }
+  const float here = (float)total * g.part.tile_cost, there = rows * g.part.row_cost;
+  const int blocks = (int)(kSms * (here / (here + there + 1.f)) + 0.5f);
+  return min((int)gridDim.x, max(blocks, kSms / 4));
+}
 template <int THREADS>
 __device__ __forceinline__ int beside_blocks(const SharedArgs& g, int total, float* s_rows) {
-  if (g.pass != 1 || !g.part.desc || !g.part.row_cost) return gridDim.x;
+  if (g.pass != 1 || !(g.part.row_cost || g.part.room)) return gridDim.x;
   const int n = g.part.seqs * g.c.kv_heads;
   float rows = 0.f;
   for (int i = threadIdx.x; i < n; i += THREADS) rows += (float)max(0, g.part.own_lens[i]);
@@ -437,42 +451,87 @@ __device__ __forceinline__ int beside_blocks(const SharedArgs& g, int total, flo
   rows = 0.f;
 #pragma unroll
   for (int w = 0; w < THREADS / 32; ++w) rows += s_rows[w];
-  const float here = (float)total * g.part.tile_cost, there = rows * g.part.row_cost;
-  const int blocks = (int)(kSms * (here / (here + there + 1.f)) + 0.5f);
-  return min((int)gridDim.x, max(blocks, kSms / 4));
+  return part_of_sms(g, total, rows);
 }
 
-// Few units: shares of whole blocks for each of them, where that makes no share longer by more than
-// kAlignMore tiles. A block whose share goes on in a second unit ends one piece and starts another,
-// which costs as much as seven tiles. `last`: of the blocks that have this one's unit; -1: shares stay as
-// they are. tiles: of each unit; *best starts at INT_MAX.
-constexpr int kAlignUnits = 64, kAlignMore = 8;
-__device__ __forceinline__ void align_share(const SharedArgs& g, const int* tiles, int* best,
-                                            int blocks, AttendShare& x, int& last) {
-  if (g.pass != 1 || g.units > kAlignUnits || g.units > blocks) return;
-  if (threadIdx.x < kAlignMore) {
-    const int per = x.per + threadIdx.x;
-    int n = 0;
-    for (int u = 0; u < g.units; ++u) n += (tiles[u] + per - 1) / per;
-    if (n <= blocks) atomicMin(best, per);
+// The same shares for up to kFewUnits units with one barrier instead of five (of 13 us before a block's
+// second tile the shares took 3 to 4): one warp looks after the units, the others after the own rows'
+// lengths, then every warp finds the block's share by itself. Where that makes no share longer by more
+// than kAlignMore tiles, a unit's shares are whole blocks': one whose share goes on in a second unit ends
+// one piece and starts another, which costs as much as seven tiles (8 slices of 8192 rows, 64 query rows
+// 26.8 us, now 25.6). `last`: the last of the blocks that have this one's unit; -1: shares are even.
+constexpr int kFewUnits = 64, kAlignMore = 8;
+__device__ __forceinline__ int warp_scan(int x, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o *= 2) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  return x;
+}
+template <int THREADS, int NQ>
+__device__ __forceinline__ AttendShare few_share(const SharedArgs& g, int* s_tiles, float* s_rows,
+                                                 int& last) {
+  constexpr unsigned kFull = 0xffffffffu;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  if (warp == 0) {
+    for (int i = lane; i < kFewUnits; i += 32)
+      s_tiles[i] = i < g.units ? tc_tiles<NQ>(attend_unit<kRows * NQ>(g, i)) : 0;
+  } else if (g.part.row_cost) {
+    float rows = 0.f;
+    for (int i = threadIdx.x - 32; i < g.part.seqs * g.c.kv_heads; i += THREADS - 32)
+      rows += (float)max(0, g.part.own_lens[i]);
+#pragma unroll
+    for (int o = 16; o; o /= 2) rows += __shfl_xor_sync(kFull, rows, o);
+    if (lane == 0) s_rows[warp] = rows;
   }
   __syncthreads();
-  if (*best == 0x7FFFFFFF) return;
-  x.per = *best;
-  x.start = x.stop = x.total;
-  for (int u = 0, first = 0, at = 0; u < g.units; ++u) {
-    const int n = (tiles[u] + x.per - 1) / x.per, b = blockIdx.x - first;
-    if (b < n) {
-      x.unit = u;
-      x.at = at;
-      x.start = at + b * x.per;
-      x.stop = min(at + tiles[u], x.start + x.per);
-      last = first + n - 1;
+  const int t[2] = {s_tiles[lane], s_tiles[lane + 32]};
+  AttendShare x;
+  x.total = __reduce_add_sync(kFull, t[0] + t[1]);
+  int blocks = gridDim.x;
+  if (g.part.row_cost || g.part.room) {
+    float rows = g.part.row_cost && lane > 0 && lane < THREADS / 32 ? s_rows[lane] : 0.f;
+#pragma unroll
+    for (int o = 16; o; o /= 2) rows += __shfl_xor_sync(kFull, rows, o);
+    blocks = part_of_sms(g, x.total, rows);
+  }
+  x.per = share_per(x.total, blocks);
+  last = -1;
+  int per = 0;
+  if (g.units <= blocks)
+    for (int k = 0; k < kAlignMore && !per; ++k) {
+      const int y = x.per + k;
+      if (__reduce_add_sync(kFull, (t[0] + y - 1) / y + (t[1] + y - 1) / y) <= blocks) per = y;
+    }
+  if (per) x.per = per;
+  const int b = blockIdx.x;
+  x.start = per ? x.total : share_start(x.total, x.per, b);
+  x.stop = per ? x.total : share_start(x.total, x.per, b + 1);
+  x.unit = x.at = 0;
+  int at0 = 0, first0 = 0;               // tiles and blocks of the units before
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int n = (t[h] + x.per - 1) / x.per;
+    const int at = at0 + warp_scan(t[h], lane) - t[h], first = first0 + warp_scan(n, lane) - n;
+    const bool mine = per ? b >= first && b < first + n : x.start >= at && x.start < at + t[h];
+    const unsigned hit = __ballot_sync(kFull, mine);
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      x.unit = 32 * h + src;
+      x.at = __shfl_sync(kFull, at, src);
+      const int f = __shfl_sync(kFull, first, src), tiles = __shfl_sync(kFull, t[h], src);
+      if (per) {
+        x.start = x.at + (b - f) * per;
+        x.stop = min(x.at + tiles, x.start + per);
+        last = f + (tiles + per - 1) / per - 1;
+      }
       break;
     }
-    first += n;
-    at += tiles[u];
+    at0 = __shfl_sync(kFull, at + t[h], 31);
+    first0 = __shfl_sync(kFull, first + n, 31);
   }
+  return x;
 }
 
 template <int D, int NQ, bool IMAGE, typename Args>
@@ -524,27 +583,23 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
     bar_init(drained, 2);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     s_up = 0;
-    if constexpr (kShared<Args>) reinterpret_cast<int*>(s_l)[kRows - 1] = 0x7FFFFFFF;
   }
   if (tid < 16) s_hot[tid / 8][tid % 8] = 0;
   begin_pass(g);
   tc_before();
-  int blocks = gridDim.x, last = -1;
-  int* const s_tiles = reinterpret_cast<int*>(s_m);      // (s_m and s_l are the results', later)
-  AttendShare sh = attend_share<kThreads>(
-      g,
-      [&](int i) {
-        const int n = tc_tiles<NQ>(attend_unit<kRows * NQ>(g, i));
-        if constexpr (kShared<Args>)
-          if (i < kAlignUnits) s_tiles[i] = n;
-        return n;
-      },
-      [&](int total) {
-        if constexpr (kShared<Args>) blocks = beside_blocks<kThreads>(g, total, s_l);
-        return blocks;
-      });
-  if constexpr (kShared<Args>)
-    align_share(g, s_tiles, reinterpret_cast<int*>(s_l) + kRows - 1, blocks, sh, last);
+  int last = -1;
+  const AttendShare sh = [&] {
+    // (s_m and s_l are the results', later)
+    if constexpr (kShared<Args>)
+      if (g.pass == 1 && g.units <= kFewUnits)
+        return few_share<kThreads, NQ>(g, reinterpret_cast<int*>(s_m), s_l, last);
+    return attend_share<kThreads>(
+        g, [&](int i) { return tc_tiles<NQ>(attend_unit<kRows * NQ>(g, i)); },
+        [&](int total) {
+          if constexpr (kShared<Args>) return beside_blocks<kThreads>(g, total, s_l);
+          return (int)gridDim.x;
+        });
+  }();
   tc_after();
   grid_dep_trigger();
   const uint32_t tmem = s_tmem;

@@ -11,7 +11,15 @@
 //
 // Only one row of p (and of q) of each sequence is read, whatever the number of its drafts. A
 // cluster of thread blocks takes a sequence, each warp a run of columns; block sums meet in shared
-// memory, and the one warp whose run holds the threshold goes over it again, from L2.
+// memory, and the block whose warp's run holds the threshold goes over that run again, from L2, with
+// all its warps.
+//
+// What bounds it: latencies (lengths, drafts, their probabilities, the block sums: 5 us for five tokens
+// of one sequence), then the rows: 64 sequences of 131072 binary32 columns, 67 MB in 12.6 us on the GPU
+// (15.7 us a call with rows that are not in L2), 256 draws from 65536 columns 13.6 us, 200 sequences of
+// 50257 bf16 columns, 18 MB, 11.1 us (on the GPU; with whole rows searched by one warp 47.8, 18.2).
+// Blocks of 256 threads, four an SM, took 11.4, 11.2 and 13.7 us, of 512, two an SM, 12.5, 12.7, 12.9, with
+// twice the loads under way 12.1, 12.6, 13.5; three an SM 15.5, 11.5, 15.2.
 #include "nx_internal.cuh"
 
 namespace nx {
