@@ -443,6 +443,7 @@ __device__ __forceinline__ int beside_blocks(const SharedArgs& g, int total, flo
   if (g.pass != 1 || !(g.part.row_cost || g.part.room)) return gridDim.x;
   const int n = g.part.seqs * g.c.kv_heads;
   float rows = 0.f;
+#pragma unroll 4
   for (int i = threadIdx.x; i < n; i += THREADS) rows += (float)max(0, g.part.own_lens[i]);
 #pragma unroll
   for (int o = 16; o; o /= 2) rows += __shfl_xor_sync(0xffffffffu, rows, o);
@@ -479,6 +480,7 @@ __device__ __forceinline__ AttendShare few_share(const SharedArgs& g, int* s_til
       s_tiles[i] = i < g.units ? tc_tiles<NQ>(attend_unit<kRows * NQ>(g, i)) : 0;
   } else if (g.part.row_cost) {
     float rows = 0.f;
+#pragma unroll 4
     for (int i = threadIdx.x - 32; i < g.part.seqs * g.c.kv_heads; i += THREADS - 32)
       rows += (float)max(0, g.part.own_lens[i]);
 #pragma unroll
