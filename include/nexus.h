@@ -427,7 +427,8 @@ typedef struct nx_shared {
 } nx_shared;
 
 /* Bytes of workspace nexus_attend_shared needs for these arguments (0 on invalid arguments). They
-   go by dtype, head_dim, heads, tokens and the two max_tokens, not by capacities or lengths. */
+   go by dtype, head_dim, heads, tokens, the two max_tokens and the number of prefixes, not by
+   capacities or lengths. */
 size_t nexus_attend_shared_workspace_bytes(const nx_cache* cache, const nx_tokens* tokens,
                                            const nx_shared* shared);
 
@@ -437,13 +438,16 @@ size_t nexus_attend_shared_workspace_bytes(const nx_cache* cache, const nx_token
  * slice (layer, i, h) of shared->prefix, then the slots j < M of slice (layer, s, h) of `cache` as
  * in nexus_attend (causal says which of its own slice's rows a token sees; the prefix it sees
  * whole). The rows of a prefix are read once for all tokens that share it, not once per sequence.
- * Everything else is as in nexus_attend, for either part by itself: images, flagged slices and
- * pages, rows that are not finite, the kernels taken (the prefix part has the rows of all the
- * tokens that share it, max_tokens of nx_shared times group, at most) and what they round. The two
- * parts meet in binary32. Two launches or more.
+ * Images, flagged slices and pages, rows that are not finite: as in nexus_attend, for either part by
+ * itself. Which kernel takes a part goes by its query rows (the prefix part has those of all tokens
+ * that share it, up to max_tokens of nx_shared times group) and by its slots. What it rounds before
+ * the parts meet: the row kernel, a bf16 part's weights to two bf16 terms (2^-16), an image part's to
+ * fp16 (2^-11; up to 8 query rows to two terms, 2^-22); the tensor cores, weights to two bf16 terms
+ * with up to 128 query rows or from an image, to one (2^-8) with more; fp32 parts as in nexus_attend.
+ * The parts meet in binary32. Two launches or more; the same bits for the same lengths every time.
  * A prefix whose entries of cu_seqs decrease or leave [0, seqs], or whose tokens are more than
- * nx_shared.max_tokens (NX_DEV_BAD_TOKENS), counts as empty; where cu_seqs decreases a sequence that
- * it gives to two prefixes has one of them.
+ * nx_shared.max_tokens (NX_DEV_BAD_TOKENS), counts as empty; what a sequence gets that decreasing
+ * entries give to two prefixes is not defined.
  */
 nx_status nexus_attend_shared(const nx_cache* cache, const nx_tokens* tokens,
                               const nx_image* image, const nx_shared* shared,

@@ -621,6 +621,36 @@ def test_shared_prefixes_on_the_tensor_cores(lens, each, d, image):
     assert names[0] == "attend_tc" and names[-1] == "attend_meet"
 
 
+@pytest.mark.parametrize("prefixes,rows", [(5, 200), (9, 20)])
+def test_shared_many_prefix_units(prefixes, rows):
+    # 40 and 72 units of the tensor cores, next to so many own rows that the 40 get 38 blocks: shares
+    # that go on from one unit to the next
+    each = 80
+    rng = np.random.default_rng(prefixes)
+    own, pre = _pair("bf16_64", prefixes * each, prefixes,
+                     rng.integers(rows // 2, rows * 3 // 2, (prefixes * each, 4)),
+                     rng.integers(900, 1000, (prefixes, 4)), kv_heads=4)
+    groups = [each * i for i in range(prefixes + 1)]
+    _, _, names = _check_shared(own, pre, groups, [1] * (prefixes * each))
+    assert names[0] == "attend_tc" and names[-1] == "attend_meet"
+
+
+@pytest.mark.parametrize("kind,image", [("bf16", False), ("bf16", True), ("f32", False)])
+@pytest.mark.parametrize("rows", [40, 4200])
+def test_shared_long_own_slices(rows, kind, image):
+    # own slices so long that their tiles are shared evenly and joined, in either order of the passes
+    rng = np.random.default_rng(rows)
+    own, pre = _pair(kind, 20, 1, rng.integers(4000, 9000, (20, 2)), [[rows, rows - 7]])
+    _, _, names = _check_shared(own, pre, None, [1] * 20, image=image)
+    assert "attend_join" in names and ("attend_meet" in names) == (rows == 4200 and kind == "bf16")
+
+
+def test_shared_prefixes_that_nobody_shares():
+    own, pre = _pair("bf16", 6, 2, 30, [[4200, 4000], [4100, 4200]])
+    a, _, names = _check_shared(own, pre, [3, 3, 3], [1] * 6, max_shared=40)
+    assert names[0] == "attend_tc" and names[-1] == "attend_meet"
+
+
 @pytest.mark.parametrize("image", ["none", "own", "both"])
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("rows", [20, 900])
