@@ -27,8 +27,8 @@
 // Every wait is bounded; when one gives up, the block flags NX_DEV_TIMEOUT, starts no more copies,
 // waits (bounded too) for the copies and products that are under way and ends, its TMEM freed.
 //
-// Measured: two chunks of 512 tokens, 8 x 4 heads, over 8704 rows: 134 us per call, 1.09 PFLOP/s,
-// 56 % of a plain bf16 product's rate; a step of a stream (64 slots) takes about 2000 clocks, of
+// Measured: two chunks of 512 tokens, 8 x 4 heads, over 8704 rows: 131 us per call, 1.11 PFLOP/s,
+// 57 % of a plain bf16 product's rate; a step of a stream (64 slots) takes about 2000 clocks, of
 // which its products need 640 and the other stream's as many: the rest is the latency of issuing
 // and committing them. 20 to 128 rows over 32 x 8 slices of 6960 rows: 180 to 186 us in bf16
 // (5.0 TB/s), 349 to 358 us from the image, where expanding the codes bounds it; the chunks from the
@@ -897,19 +897,24 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
         const float c1 = fmaxf(fabsf(g.c1), 1.1754944e-38f);   // not 0: -inf c1 is -inf
         const int lim = rr < u.rows ? min(u.end, row_limit(g, u, u.r0 + rr)) : 0;
         const int low = min(u.end, u.low);
-        if (NQ == 2 || x == 0) {       // this thread's query row, 128 bytes of it to a block
+        if (NQ == 2 || x == 0) {
+          // the warp's query rows, 128 bytes of each to a block: whole rows by neighbouring lanes (a lane
+          // to each row took 3.6 us of a piece's start, its copies 32 lines an instruction)
+          constexpr int kChunks = D / 8, kLine = 32 / kChunks;
           const int row = u.r0 + rr, token = row / g.c.group;
           const bool ok = rr < u.rows;
-          const __nv_bfloat16* src =
-              static_cast<const __nv_bfloat16*>(g.a.q) +
-              (ok ? (u.first + token) * g.a.q_stride +
-                        ((long long)u.h * g.c.group + row - token * g.c.group) * D
-                  : 0);
+          const long long src = ok ? (u.first + token) * g.a.q_stride +
+                                         ((long long)u.h * g.c.group + row - token * g.c.group) * D
+                                   : -1;
 #pragma unroll 4
-          for (int i = 0; i < D / 8; ++i)
-            copy16(s_q + (NQ == 2 ? x : 0) * P::kQBytes + i / 8 * P::kRowBlock + r * 128 +
-                       ((i ^ r) & 7) * 16,
-                   ok ? src + 8 * i : src, ok);
+          for (int i = 0; i < 32; i += kLine) {
+            const long long from = __shfl_sync(0xffffffffu, src, i + lane / kChunks);
+            const int to = (r & ~31) + i + lane / kChunks, chunk = lane % kChunks;
+            copy16(s_q + (NQ == 2 ? x : 0) * P::kQBytes + chunk / 8 * P::kRowBlock + to * 128 +
+                       ((chunk ^ to) & 7) * 16,
+                   static_cast<const __nv_bfloat16*>(g.a.q) + (from < 0 ? 0 : from) + 8 * chunk,
+                   from >= 0);
+          }
           asm volatile("cp.async.wait_all;" ::: "memory");
           fence_async();
           bar_arrive(qfull);
