@@ -1281,7 +1281,11 @@ long long plan_rows(Args& g) {
   int ranks = kRanks;
   while (ranks > 1 && units * ranks > fit) ranks /= 2;
   if (g.c.capacity <= (units * kRanks <= 2 * kSms ? few / 2 : few)) ranks = 1;
-  const int limit = ranks > 1 ? ranks * most_of : units >= fit ? 2 * few : few;
+  int limit = ranks > 1 ? ranks * most_of : units >= fit ? 2 * few : few;
+  // Blocks of their own can go where a prefix on the tensor cores leaves room, even shares cannot: 512
+  // slices of 1024 to 2048 rows next to 8192 slots of 8 slices 87 us, not 108, next to 32768 105, not 121.
+  if constexpr (kShared<Args>)
+    if (g.pass == 3 && ranks == 1 && units >= fit) limit = 4 * few;
   g.ranks = g.c.capacity <= limit ? ranks : 0;
   g.splits = 0;
   if (units * 2 <= kSms)
