@@ -1301,10 +1301,12 @@ long long plan_rows(Args& g) {
     //   1024 315 / 270; 4000 units of 32 54 / 147, of 256 239 / 340, of 1024 864 / 1007
     //   image: 32 units of 32 15 / 16, of 64 17 / 16; 2400 units of 16 rows, 32 slots 36 / 109, 512 104 / 152
     const int waves = (int)((units + fit - 1) / fit);
-    const int brief = waves <= 1   ? (KIND == kF32 ? 16 : 64)
-                      : waves == 2 ? (KIND == kF32 ? 128 : 256)
-                      : waves == 3 ? 512
-                                   : 2048;
+    // Few units: a block each does better for own slices (behind 300 rows of prefix, 128 units of 16 rows
+    // over 32 slots bf16 25.2 / 23.8, image 30.2 / 26.8, fp32 28.3 / 31.0; 240 units bf16 20.2 / 24.7).
+    const int once = g.pass == 1    ? (KIND == kF32 ? 16 : 64)
+                     : KIND == kF32 ? (units >= 64 ? 32 : 0)
+                                    : (units >= 192 ? 64 : 0);
+    const int brief = waves <= 1 ? once : waves == 2 ? (KIND == kF32 ? 128 : 256) : waves == 3 ? 512 : 2048;
     g.brief = g.c.capacity <= brief;
     if (g.brief) return (units + kWarps - 1) / kWarps;
   }
