@@ -106,7 +106,7 @@ struct Weights {
     p = row - shift;
     q = other ? other - shift : nullptr;
     q_vec = (uintptr_t)q % 16 == 0;
-    out = without < 0 ? -1 : without + shift;
+    out = without < 0 || without >= V ? -1 : without + shift;
   }
   template <bool TWO>
   __device__ __forceinline__ float weigh(float x, float y) const {

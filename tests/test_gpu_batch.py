@@ -414,6 +414,15 @@ def test_verify_drafts_outside_the_vocabulary(drafted):
     assert _check_verify([4, 4], 1000, drafted=drafted, mutate=bad) == [2, 1]
 
 
+@pytest.mark.parametrize("drafted", [True, False])
+@pytest.mark.parametrize("far", [1000, 1001, 1003, 2 ** 31 - 1, -2 ** 31])
+def test_verify_first_draft_outside_draws_from_the_whole_row(far, drafted):
+    def bad(p, q, token, u, u_draw):
+        u[:] = 0
+        token[1] = far
+    assert _check_verify([3, 1], 1000, drafted=drafted, mutate=bad) == [1, 1]
+
+
 def test_verify_faults_are_flagged():
     cache = _bare_cache(1, 3, 2, 50, lens=_ints([[[5, 1], [51, 5], [-1, 7]]]))
     token, out = _ints([0, 1, 1] * 3), torch.full((9,), -9, dtype=torch.int32, device=DEV)
