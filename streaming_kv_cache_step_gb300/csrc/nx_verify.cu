@@ -247,7 +247,8 @@ __global__ void __launch_bounds__(kVerifyThreads, kVerifyPerSm) verify_kernel(Ve
     return;
   }
   const float u_draw = g.a.u_draw[s];
-  // pushes into another block's shared memory must find it running
+  // pushes into another block's shared memory must find it running: each thread waits before the
+  // first of them, and its columns' loads come meanwhile
   if (g.ranks > 1) asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
   // ---- the first draft that goes ----
   if (tid == 0) s_first = n - 1;
@@ -289,6 +290,7 @@ __global__ void __launch_bounds__(kVerifyThreads, kVerifyPerSm) verify_kernel(Ve
   for (int round = 0; round < 2; ++round) {
     const unsigned long long sum = columns_sum(w, c0, c1, lane);
     if (lane == 0) s_warp[warp] = sum;
+    if (round == 0 && g.ranks > 1) asm volatile("barrier.cluster.wait;" ::: "memory");
     __syncthreads();
     if (tid < g.ranks) {
       unsigned long long all = 0;
@@ -300,7 +302,6 @@ __global__ void __launch_bounds__(kVerifyThreads, kVerifyPerSm) verify_kernel(Ve
     if (g.ranks == 1) {
       __syncthreads();
     } else {
-      if (round == 0) asm volatile("barrier.cluster.wait;" ::: "memory");
       asm volatile("barrier.cluster.arrive;\n\tbarrier.cluster.wait;" ::: "memory");
     }
     total = before = 0;

@@ -454,6 +454,32 @@ def test_verify_padded_batch_and_none():
     assert em.cpu().tolist() == [0, 0] and cache.lens.cpu().tolist() == [[[5], [6]]]
 
 
+@pytest.mark.parametrize("V", [1025, 2049, 4100, 8193])
+def test_verify_blocks_of_a_sequence_that_start_apart(V):
+    # few columns to each of a sequence's two to eight thread blocks, next to another stream that keeps
+    # the GPU's places taken: a block may be done with its sum long before the others have begun, and
+    # must not send it to them until they have
+    rng = np.random.default_rng(V)
+    S, calls = 40, 60
+    p, _ = _probs(rng, S, V)
+    u_draw = np.minimum(rng.random(S).astype(np.float32), np.float32(1 - 2.0 ** -24))
+    want = B.verify_plain([0] * S, p, None, np.zeros(S), u_draw, list(range(S + 1)))
+    cache = _bare_cache(1, S, 1, 8, lens=torch.full((1, S, 1), 4, dtype=torch.int32, device=DEV))
+    pd, ud, u = torch.as_tensor(p, device=DEV), torch.as_tensor(u_draw, device=DEV), torch.zeros(S, device=DEV)
+    token, st = _ints([0] * S), _status()
+    out, em = torch.full((calls, S), -9, dtype=torch.int32, device=DEV), _ints([-9] * S)
+    busy = torch.zeros(1 << 22, device=DEV)
+    other = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for i in range(calls):
+        with torch.cuda.stream(other):
+            busy.add_(1.0)
+        nexus.verify(cache, token, pd, u, ud, out[i], em, st, max_tokens=1)
+    torch.cuda.synchronize()
+    assert int(st.item()) == want[3] == 0 and em.cpu().tolist() == want[1]
+    assert out.cpu().tolist() == [want[0]] * calls
+
+
 def test_verify_gives_the_models_distribution():
     # 60000 sequences with the same p and q, drafts drawn from q: the first token is distributed
     # like p. Five standard deviations of a count out of n: 5 sqrt(n p (1 - p)), missed by chance
