@@ -455,7 +455,7 @@ __device__ __forceinline__ int beside_blocks(const SharedArgs& g, int total, flo
   return part_of_sms(g, total, rows);
 }
 
-// The same shares for up to kFewUnits units with one barrier instead of five (of 13 us before a block's
+// The same shares for up to kFewUnits units with two barriers instead of five (of 13 us before a block's
 // second tile the shares took 3 to 4): one warp looks after the units, the others after the own rows'
 // lengths, then every warp finds the block's share by itself. Where that makes no share longer by more
 // than kAlignMore tiles, a unit's shares are whole blocks': one whose share goes on in a second unit ends
@@ -491,9 +491,13 @@ __device__ __forceinline__ AttendShare few_share(const SharedArgs& g, int* s_til
   const int t[2] = {s_tiles[lane], s_tiles[lane + 32]};
   AttendShare x;
   x.total = __reduce_add_sync(kFull, t[0] + t[1]);
+  float rows = g.part.row_cost && lane > 0 && lane < THREADS / 32 ? s_rows[lane] : 0.f;
+  // All warps have read: the block's first piece may write its results there. (An issuing warp whose
+  // stream has no tile in that piece waits for nothing else. The image's 128 features and one row tile
+  // leave no room for arrays of their own.)
+  __syncthreads();
   int blocks = gridDim.x;
   if (g.part.row_cost || g.part.room) {
-    float rows = g.part.row_cost && lane > 0 && lane < THREADS / 32 ? s_rows[lane] : 0.f;
 #pragma unroll
     for (int o = 16; o; o /= 2) rows += __shfl_xor_sync(kFull, rows, o);
     blocks = part_of_sms(g, x.total, rows);
@@ -598,6 +602,7 @@ __global__ void __launch_bounds__(Plan<D, NQ, IMAGE>::kThreads, 1)
     return attend_share<kThreads>(
         g, [&](int i) { return tc_tiles<NQ>(attend_unit<kRows * NQ>(g, i)); },
         [&](int total) {
+          // (attend_share ends with a barrier)
           if constexpr (kShared<Args>) return beside_blocks<kThreads>(g, total, s_l);
           return (int)gridDim.x;
         });

@@ -656,6 +656,32 @@ def test_shared_prefixes_on_the_tensor_cores(lens, each, d, image):
     assert names[0] == "attend_tc" and names[-1] == "attend_meet"
 
 
+@pytest.mark.parametrize("image,slots", [(False, 1030), (True, 1930)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_shared_pieces_of_one_tile(d, image, slots):
+    # up to 128 query rows, so that a row tile's slots are dealt to two streams, and 17 or 31 tiles (of 64
+    # slots) to each unit in shares of 2 or 3: in a piece of one the second stream has none, and its warp
+    # nothing to wait for between the block's share and the first piece's results. The same bits again
+    # and again.
+    own, pre = _pair("bf16", 32, 1, 5, [[slots] * 8], d=d, kv_heads=8)
+    first, _, names = _check_shared(own, pre, None, [1] * 32, pre_image=image)
+    assert names[0] == "attend_tc" and names[-1] == "attend_meet"
+    own, pre = _pair("bf16", 32, 1, 5, [[slots] * 8], d=d, kv_heads=8)
+    cache, prefix, st = own.device_cache(), pre.device_cache(), _status()
+    im = None
+    if image:
+        im = _image(prefix)
+        nexus.quantize(prefix, im, st)
+    q = torch.randn(32, 32 + 3, d, generator=own.g).to(own.dtype).to(DEV)[:, 1:33]
+    ws = nexus.alloc_attend_shared_workspace(cache, prefix, tokens=32, max_tokens=1, max_shared=32)
+    out = torch.full((100, 32, 32, d), math.nan, dtype=BF, device=DEV)
+    for i in range(100):
+        nexus.attend_shared(cache, 0, q, out[i], ws, st, prefix=prefix, max_tokens=1, max_shared=32,
+                            prefix_image=im)
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0 and torch.all(out == first[None])
+
+
 @pytest.mark.parametrize("prefixes,rows", [(5, 200), (9, 20)])
 def test_shared_many_prefix_units(prefixes, rows):
     # 40 and 72 units of the tensor cores, next to so many own rows that the 40 get 38 blocks: shares
