@@ -16,19 +16,24 @@ __device__ __forceinline__ bool own_part(const SharedArgs& g, int p, int token) 
     u.first = u.s * g.part.max_tokens;
     u.n = g.part.max_tokens;
   } else {
-    int s = g.part.cu_seqs ? g.part.cu_seqs[p] : 0;
-    for (int hi = g.part.cu_seqs ? g.part.cu_seqs[p + 1] : g.part.seqs; hi - s > 1;) {
-      const int mid = (s + hi) / 2;
-      if (g.t.cu_tokens[mid] <= token) s = mid;
+    const int s0 = g.part.cu_seqs ? g.part.cu_seqs[p] : 0;
+    const int s1 = g.part.cu_seqs ? g.part.cu_seqs[p + 1] : g.part.seqs;
+    u.s = s0;
+    for (int hi = s1; hi - u.s > 1;) {
+      const int mid = (u.s + hi) / 2;
+      if (g.t.cu_tokens[mid] <= token) u.s = mid;
       else hi = mid;
     }
-    u.s = s;
-    u.first = g.t.cu_tokens[s];
-    const int end = g.t.cu_tokens[s + 1];
-    if (u.first < 0 || token < u.first || token >= end || end > g.t.tokens ||
-        end - u.first > g.part.max_tokens)
-      return false;
-    u.n = end - u.first;
+    const auto owns = [&] {
+      u.n = tokens_of(g.t, u.s, u.first, g.part.max_tokens);
+      return u.n > 0 && token >= u.first && token - u.first < u.n;
+    };
+    // Entries that decrease or leave the tokens take away the sequences that they bound and no others, but
+    // lead the search astray: one after the other, then.
+    if (!owns()) {
+      for (u.s = s0; u.s < s1 && !owns();) ++u.s;
+      if (u.s == s1) return false;
+    }
   }
   return part_joins(o, u);
 }

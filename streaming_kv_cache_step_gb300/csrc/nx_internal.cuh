@@ -106,16 +106,19 @@ inline bool valid_tokens(const nx_cache& c, const nx_tokens* t) {
 }
 
 // The rows [first, first + return value) that sequence s owns of the per-token arrays; -1
-// for a bad cu_tokens.
-__device__ __forceinline__ int tokens_of(const nx_tokens& t, int s, int& first) {
+// for a bad cu_tokens. `most`: no sequence owns more.
+__device__ __forceinline__ int tokens_of(const nx_tokens& t, int s, int& first, int most) {
   if (!t.cu_tokens) {
-    first = s * t.max_tokens;
-    return t.max_tokens;
+    first = s * most;
+    return most;
   }
   first = t.cu_tokens[s];
   const int end = t.cu_tokens[s + 1];
-  if (first < 0 || end < first || end > t.tokens || end - first > t.max_tokens) return -1;
+  if (first < 0 || end < first || end > t.tokens || end - first > most) return -1;
   return end - first;
+}
+__device__ __forceinline__ int tokens_of(const nx_tokens& t, int s, int& first) {
+  return tokens_of(t, s, first, t.max_tokens);
 }
 
 // Rows of one block of an 8-bit image.

@@ -894,6 +894,49 @@ def test_shared_sequence_without_its_tokens():
     assert torch.all(out[2:5].isnan())
 
 
+@pytest.mark.parametrize("rows", [60, 5000])
+@pytest.mark.parametrize("cu,groups,most,good", [
+    ([0, 9, 3, 6], None, 3, [2]),                      # 0: beyond the tokens, 1: decreases
+    ([0, 2, 5, 6], None, 2, [0, 2]),                   # 1: three of at most two
+    ([0, 2, 6, 3, 6], None, 3, [0, 3]),                # 1: four of at most three, 2: decreases
+    ([0, 40, -5, 1, 3, 9, 4, 6], [0, 3, 7], 2, [3, 6]),
+])
+def test_shared_tokens_of_sequences_that_are_not_flagged(cu, groups, most, good, rows):
+    # entries of cu_tokens that make no sense leave out the sequences that they bound; the others have
+    # their outputs, whichever kernels take the prefix
+    seqs = len(cu) - 1
+    own, pre = _pair("bf16", seqs, 2 if groups else 1, 40, [[rows, rows - 3]] * (2 if groups else 1))
+    cache, prefix, st = own.device_cache(), pre.device_cache(), _status()
+    q = torch.randn(6, 8, 128, generator=own.g).to(BF)
+    out = torch.full((6, 8, 128), math.nan, dtype=BF, device=DEV)
+    lse = torch.full((6, 8), math.nan, device=DEV)
+    ws = nexus.alloc_attend_shared_workspace(cache, prefix, tokens=6, max_tokens=most, max_shared=6)
+    ws.fill_(0xFF)
+    nexus.attend_shared(cache, 0, q.to(DEV), out, ws, st, prefix=prefix, max_tokens=most, max_shared=6,
+                        cu_tokens=_ints(cu), cu_seqs=_ints(groups) if groups else None, lse=lse)
+    torch.cuda.synchronize()
+    assert ("attend_meet" in nexus.last_launch_names()) == (rows == 5000)
+    assert int(st.item()) == nexus.NX_DEV_BAD_TOKENS
+    bounds = groups or [0, seqs]
+    rest = torch.ones(6, dtype=torch.bool)
+    for s in good:
+        p, a, b = B.prefix_of(bounds, s), cu[s], cu[s + 1]
+        rest[a:b] = False
+        for h in range(own.H):
+            M = [40 - (b - a - 1 - i) for i in range(b - a) for _ in range(own.G)]
+            k, v = _rows(pre, None, 0, p, h)
+            parts = [(k, v, [k.shape[0]] * len(M)), (*_rows(own, None, 0, s, h), M)]
+            x = q[a:b, h * own.G:(h + 1) * own.G].reshape(-1, 128)
+            ro, rl, A, big = B.shared64(x, parts, 128 ** -0.5)
+            got = out[a:b, h * own.G:(h + 1) * own.G].reshape(-1, 128).cpu().double()
+            gl = lse[a:b, h * own.G:(h + 1) * own.G].reshape(-1).cpu().double()
+            dx = 128 ** -0.5 * big * 2.0 ** -24 * 136
+            tol = HALF[BF] * ro.abs() + (2.0 ** -8 + 2.0 ** -20 + 2 * dx)[:, None] * A
+            assert torch.all((got - ro).abs() <= tol), (s, h)
+            assert torch.all((gl - rl).abs() <= dx + 2.0 ** -18 * (1 + rl.abs())), (s, h)
+    assert torch.all(out[rest].isnan()) and torch.all(lse[rest].isnan())
+
+
 # ---------------------------------------------------------------------------
 # streams, graphs, and all of them together
 # ---------------------------------------------------------------------------
