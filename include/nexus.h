@@ -74,7 +74,7 @@ enum {
                                or beyond the slice's rows: slice left untouched */
   NX_DEV_NO_PAGES = 128,    /* nexus_plan: too few free pages for a sequence's tokens; it keeps
                                its pages and brings no tokens */
-  NX_DEV_BAD_PROBS = 256    /* nexus_verify: a row of probabilities that is 0 everywhere; its
+  NX_DEV_BAD_PROBS = 256    /* nexus_verify: a row whose probabilities are all below 2^-42; its
                                token is 0 */
 };
 
@@ -536,11 +536,13 @@ typedef struct nx_verify {
  * Verifies the drafts of every sequence (n tokens, n - 1 drafts) so that what comes out is
  * distributed like p. Draft x = token[i + 1] stays if all before it do and u[i] q_i(x) < p_i(x)
  * (exactly: the product in binary64). With r drafts kept, the next token is drawn by u_draw from
- *   max(0, p_r - q_r)  where draft r + 1 went (p_r itself where that is 0 everywhere),
+ *   max(0, p_r - q_r)  where draft r + 1 went (p_r itself where that is below 2^-42 everywhere),
  *   p_r                where all stayed (r = n - 1).
  * Drawn from weights w_j means: with whole weights W_j = floor(2^42 w_j) (p - q in binary32) and
  * t = floor(floor(2^31 u_draw) sum W / 2^31), the least j with W_0 + .. + W_j > t, so any
- * implementation finds the same token. Probabilities count from 0 to 1: NaN and what is below as 0.
+ * implementation finds the same token. A column below 2^-42 has no weight: it is not drawn, and where
+ * all are, the row counts as 0 everywhere (of p_r: NX_DEV_BAD_PROBS). Probabilities count from 0 to 1:
+ * NaN and what is below as 0.
  *   out: the r kept drafts, the new token, then -1;  emitted[s] = r + 1 (0 for no tokens).
  * The cache then loses what went: lens = lens_in - (n - 1 - r) in every slice of the sequence in
  * every layer, and rows of an image (nullable) drop to floor(lens / b) b where they are more. A

@@ -406,6 +406,30 @@ def test_verify_nothing_left_and_nothing_at_all():
     _check_verify([1, 1], 5000, mutate=one, drafted=False)
 
 
+@pytest.mark.parametrize("V", [7, 700, 9001])
+def test_verify_weights_below_the_smallest_count_as_none(V):
+    # 2^-43 (1 + 2^-23 at most) is no weight, however many columns have it
+    def below(p, q, token, u, u_draw):
+        p[:], q[:] = 2.0 ** -43, 0
+        u[:] = np.float32(1 - 2.0 ** -24)
+        p[0] = np.nextafter(np.float32(2.0 ** -42), np.float32(0))
+    for n in ([1, 1], [3, 2]):
+        kept = _check_verify(n, V, mutate=below)         # NX_DEV_BAD_PROBS, token 0
+        assert kept == n                                 # (the drafts' q is 0: they stay)
+
+    # as what is left of p behind q: p itself is drawn from, columns that q excludes among them
+    def left(p, q, token, u, u_draw):
+        p[:] = 0
+        p[:, 0], p[:, 1] = 0.75, 0.25
+        q[:] = p
+        p[:, 2:] = 2.0 ** -43
+        u[:] = np.float32(1 - 2.0 ** -24)
+        q[:, 0], q[:, 1] = 0.875, 0.5
+        token[:] = 0
+        u_draw[:] = [0.25, 0.875]
+    assert _check_verify([3, 3], V, mutate=left) == [1, 1]
+
+
 @pytest.mark.parametrize("drafted", [True, False])
 def test_verify_drafts_outside_the_vocabulary(drafted):
     def bad(p, q, token, u, u_draw):
