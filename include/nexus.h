@@ -503,6 +503,7 @@ typedef struct nx_plan {
  * before take are more than there are (NX_DEV_NO_PAGES: nobody overtakes a sequence that waits).
  * A *free_count out of range counts as 0, pages that find no room in free_pages are lost
  * (NX_DEV_BAD_PAGE): neither happens unless the caller's tables are wrong.
+ * new_tokens and first_pos are read before anything is written: they may lie in the arrays that are.
  * pool: NULL for a contiguous cache (no pages), else required. held_in and free_count_in make a
  * call repeatable, as long as free_pages below *free_count_in and the table's entries stay. One
  * launch. NX_ERR_UNSUPPORTED for more than 8192 sequences or 2^24 (layer, head) pairs.

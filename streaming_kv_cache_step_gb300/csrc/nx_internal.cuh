@@ -29,7 +29,7 @@ constexpr int kMultiSlices = 256;
 constexpr int kMultiStride = 512;
 constexpr int kMaxAppendHeads = 8192; // KV heads of nexus_append (their lengths sit in shared memory)
 constexpr int kMaxVocab = 1 << 20;    // columns of nexus_verify: 2^20 weights of 2^42 units fit 64 bits
-constexpr int kMaxPlanSeqs = 8192;    // sequences of nexus_plan (six values each in shared memory)
+constexpr int kMaxPlanSeqs = 8192;    // sequences of nexus_plan (seven values each in shared memory)
 constexpr uint32_t kForcedKey = 0xFFFFFFFFu;  // order key of a forced (always kept) slot
 
 // ---------------------------------------------------------------------------

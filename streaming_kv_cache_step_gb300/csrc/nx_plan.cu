@@ -98,6 +98,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const __grid_cons
   int* s_cu = s_held + S;                // tokens granted (-1: refused); then the running sums:
   int* s_give = s_cu + S;                // tokens, pages given back,
   int* s_take = s_give + S;              // pages taken
+  int* s_first = s_take + S;             // position of the first token
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, rank = blockIdx.x;
   const int all = rank * kPlanThreads + tid;
   const bool lead = rank == 0, paged = g.p.held != nullptr;
@@ -107,6 +108,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const __grid_cons
   for (int s = tid; s < S; s += kPlanThreads) {
     s_new[s] = g.a.new_tokens[s];
     s_held[s] = paged ? g.held_in[s] : 0;
+    s_first[s] = g.a.token_pos ? g.a.first_pos[s] : 0;
   }
   int free_before = paged ? *g.free_in : 0;
   bool pushed = false;
@@ -224,7 +226,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const __grid_cons
     for (unsigned i = all; i < (unsigned)N; i += kPlanStep) {
       const int s = owner_of(s_cu, S, i);
       if (g.a.token_seq) g.a.token_seq[i] = s;
-      if (g.a.token_pos) g.a.token_pos[i] = g.a.first_pos[s] + (int)i - s_cu[s];
+      if (g.a.token_pos) g.a.token_pos[i] = s_first[s] + (int)i - s_cu[s];
     }
   // ---- sequences that end (a refused one still holds pages) ----
   for (int s = rank * kPlanWarps + warp; s < S; s += kPlanRanks * kPlanWarps) {
@@ -252,9 +254,9 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const __grid_cons
 
 template <int THREADS>
 cudaError_t launch_plan(const PlanArgs& g, cudaStream_t st) {
-  const int smem = 6 * g.c.seqs * (int)sizeof(int);
+  const int smem = 7 * g.c.seqs * (int)sizeof(int);
   if (smem > 32 * 1024) {
-    const cudaError_t e = allow_smem<plan_kernel<THREADS>>(6 * kMaxPlanSeqs * (int)sizeof(int));
+    const cudaError_t e = allow_smem<plan_kernel<THREADS>>(7 * kMaxPlanSeqs * (int)sizeof(int));
     if (e != cudaSuccess) return e;
   }
   return launch_after_clusters(plan_kernel<THREADS>, dim3(kPlanRanks), dim3(THREADS), smem,

@@ -233,6 +233,32 @@ def test_plan_without_pages(seqs, heads):
     assert np.array_equal(im.rows.cpu().numpy(), want_rows)
 
 
+@pytest.mark.parametrize("seqs", [1, 30, 64, 65, 1000, 8192])
+@pytest.mark.parametrize("where", ["pos", "seq", "cu"])
+def test_plan_first_positions_in_an_array_that_it_writes(seqs, where):
+    # first_pos at the front of token_pos, of token_seq or of cu_tokens: all of it is read before
+    # anything is written there, also where tokens and sequences are not one to one
+    rng = np.random.default_rng([seqs, 2])
+    for most in (2, 40):
+        n = rng.integers(-1, most, seqs)
+        n[0] = 1
+        first = rng.integers(0, 1 << 30, seqs)
+        lens = rng.integers(0, 50, (2, seqs, 1))
+        N = int(np.maximum(n, 0).sum())
+        pos, seq = (torch.full((max(N, seqs),), -9, dtype=torch.int32, device=DEV) for _ in range(2))
+        cu, st = torch.full((seqs + 1,), -9, dtype=torch.int32, device=DEV), _status()
+        at = {"pos": pos, "seq": seq, "cu": cu}[where][:seqs]
+        at.copy_(_ints(first))
+        cache = _bare_cache(2, seqs, 1, 100, lens=_ints(lens))
+        nexus.plan(cache, None, _ints(n), cu, st, max_tokens=most, token_seq=seq, token_pos=pos,
+                   first_pos=at)
+        torch.cuda.synchronize()
+        rcu, rseq, rpos, _, status = B.plan_plain(lens, n, 100, tokens=len(pos), max_tokens=most,
+                                                  first_pos=first)
+        assert int(st.item()) == status == 0 and cu.cpu().tolist() == rcu
+        assert seq[:N].cpu().tolist() == rseq and pos[:N].cpu().tolist() == rpos
+
+
 def test_plan_largest_prompts():
     # pages by the ten thousands, one sequence with most of the tokens
     rng = np.random.default_rng(9)
