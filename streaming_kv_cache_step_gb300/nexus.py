@@ -296,7 +296,7 @@ class Cache:
         return self.layers * self.seqs * self.kv_heads
 
     def c_struct(self) -> CCache:
-        dt = DTYPE_BF16 if self.k.dtype == torch.bfloat16 else DTYPE_F32
+        dt = _kind(self)
         for t in (self.k, self.v, self.pos, self.lens):
             if not t.is_cuda or not t.is_contiguous():
                 raise ValueError("cache tensors must be contiguous CUDA tensors")
@@ -307,6 +307,16 @@ class Cache:
                       self.k.data_ptr(), self.v.data_ptr(), self.pos.data_ptr(),
                       self.lens.data_ptr(),
                       None if self.block_table is None else self.block_table.data_ptr())
+
+
+def _kind(c: Cache) -> int:
+    """NX_DTYPE_* of a cache's keys and values, whose lengths are one for each slice."""
+    kind = c.k.dtype
+    if c.v.dtype is not kind or kind is not torch.bfloat16 and kind is not torch.float32:
+        raise ValueError("k and v must be bfloat16 or float32, both the same")
+    if c.lens.numel() != c.layers * c.seqs * c.kv_heads:
+        raise ValueError("lens must have a value for each slice")
+    return DTYPE_BF16 if kind is torch.bfloat16 else DTYPE_F32
 
 
 @dataclass
@@ -642,12 +652,7 @@ def _packed_cache(c: Cache, dev: int) -> bytes:
             raise ValueError("cache tensors must be contiguous and on the current GPU")
     if c.pos.dtype is not torch.int32 or c.lens.dtype is not torch.int32:
         raise ValueError("pos and lens must be int32")
-    if c.k.dtype is torch.bfloat16:
-        dtype = DTYPE_BF16
-    elif c.k.dtype is torch.float32:
-        dtype = DTYPE_F32
-    else:
-        raise ValueError("k and v must be bfloat16 or float32")
+    dtype = _kind(c)
     table = 0
     if c.block_table is not None:
         table = _ints(c.block_table, c.seqs * c.max_pages_per_seq, "block_table", dev)

@@ -166,6 +166,27 @@ def test_binding_refuses_shapes_and_types():
         nexus.alloc_attend_shared_workspace(cache, cache, tokens=1, max_tokens=1, max_shared=1)
 
 
+def test_binding_refuses_caches_that_do_not_fit_together(monkeypatch):
+    # what would be read or written behind an array: keys and values of two types, or of one that is
+    # taken for another, and too few lengths
+    from streaming_kv_cache_step_gb300 import nexus
+
+    def cache(k=torch.bfloat16, v=torch.bfloat16, lens=(2, 3, 1)):
+        return nexus.Cache(k=torch.zeros(2, 3, 1, 32, 64, dtype=k), v=torch.zeros(2, 3, 1, 32, 64, dtype=v),
+                           pos=torch.zeros(2, 3, 1, 32, dtype=torch.int32),
+                           lens=torch.zeros(lens, dtype=torch.int32), layers=2, seqs=3, kv_heads=1,
+                           group=1, head_dim=64, capacity=32)
+
+    monkeypatch.setattr(torch.Tensor, "is_cuda", True)               # (no call gets as far as the data)
+    for way in (nexus.Cache.c_struct, lambda c: nexus._packed_cache(c, -1)):
+        way(cache())
+        way(cache(k=torch.float32, v=torch.float32))
+        for bad in (dict(v=torch.float32), dict(k=torch.float32), dict(lens=(2, 2, 1)),
+                    dict(lens=(3, 3, 1)), dict(k=torch.float16, v=torch.float16)):
+            with pytest.raises(ValueError):
+                way(cache(**bad))
+
+
 def test_packed_structures_have_the_layout_of_the_header():
     from streaming_kv_cache_step_gb300 import nexus
     for packed, c in ((nexus._CACHE, nexus.CCache), (nexus._TOKENS, nexus.CTokens),
