@@ -437,7 +437,11 @@ size_t nexus_attend_shared_workspace_bytes(const nx_cache* cache, const nx_token
  * for a token of sequence s that shares prefix i and query head h * group + g, over all slots of
  * slice (layer, i, h) of shared->prefix, then the slots j < M of slice (layer, s, h) of `cache` as
  * in nexus_attend (causal says which of its own slice's rows a token sees; the prefix it sees
- * whole). The rows of a prefix are read once for all tokens that share it, not once per sequence.
+ * whole). All tokens that share a prefix are query rows over its slots together: the tensor cores read
+ * those once for every 256 query rows (128 where there are no more), the row kernel once for every 16
+ * (fp32 caches and up to 8: once for every 8), from the second pass on from L2 where it holds the slices.
+ * nexus_evict_step scores either cache by a softmax over that cache alone: behind a prefix, window queries
+ * that look mostly into the prefix count as much for a sequence's own rows as the others.
  * Images, flagged slices and pages, rows that are not finite: as in nexus_attend, for either part by
  * itself. Which kernel takes a part goes by its query rows (the prefix part has those of all tokens
  * that share it, up to max_tokens of nx_shared times group) and by its slots. What it rounds before
@@ -445,9 +449,11 @@ size_t nexus_attend_shared_workspace_bytes(const nx_cache* cache, const nx_token
  * fp16 (2^-11; up to 8 query rows to two terms, 2^-22); the tensor cores, weights to two bf16 terms
  * with up to 128 query rows or from an image, to one (2^-8) with more; fp32 parts as in nexus_attend.
  * The parts meet in binary32. Two launches or more; the same bits for the same lengths every time.
- * A prefix whose entries of cu_seqs decrease or leave [0, seqs], or whose tokens are more than
- * nx_shared.max_tokens (NX_DEV_BAD_TOKENS), counts as empty; what a sequence gets that decreasing
- * entries give to two prefixes is not defined.
+ * A prefix whose entries of cu_seqs decrease or leave [0, seqs], or whose tokens (from the first one's
+ * to behind the last one's of its sequences in cu_tokens) decrease, leave [0, tokens] or are more than
+ * nx_shared.max_tokens (NX_DEV_BAD_TOKENS), counts as empty, as it does for a sequence whose own tokens are
+ * not all among them; where entries of cu_seqs decrease anywhere, which prefix a sequence has, if any, is
+ * not defined. Entries of cu_tokens that make no sense leave out the sequences that they bound only.
  */
 nx_status nexus_attend_shared(const nx_cache* cache, const nx_tokens* tokens,
                               const nx_image* image, const nx_shared* shared,

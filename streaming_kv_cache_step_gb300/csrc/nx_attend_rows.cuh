@@ -1299,7 +1299,8 @@ long long plan_rows(Args& g) {
     //   512 67 / 78; 2400 units of 16 rows, 32 slots 44 / 117, 128 68 / 113, 512 128 / 167
     //   fp32: 32 units of 16 slots 11 / 11, of 64 17 / 12; 800 units of 32 16 / 36, of 256 62 / 86, of
     //   1024 315 / 270; 4000 units of 32 54 / 147, of 256 239 / 340, of 1024 864 / 1007
-    //   image: 32 units of 32 15 / 16, of 64 17 / 16; 2400 units of 16 rows, 32 slots 36 / 109, 512 104 / 152
+    //   image (where a warp's kernel spills some 100 bytes of registers): 32 units of 32 15 / 16, of 64
+    //   17 / 16; 2400 units of 16 rows, 32 slots 36 / 109, 512 104 / 152
     const int waves = (int)((units + fit - 1) / fit);
     // Few units: a block each does better for own slices (behind 300 rows of prefix, 128 units of 16 rows
     // over 32 slots bf16 25.2 / 23.8, image 30.2 / 26.8, fp32 28.3 / 31.0; 240 units bf16 20.2 / 24.7).

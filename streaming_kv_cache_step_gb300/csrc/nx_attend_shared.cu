@@ -1,8 +1,9 @@
 // nx_attend_shared.cu -- nexus_attend_shared: attention over a prefix that several sequences share and
 // over their own rows, with the kernels of nexus_attend.
 //
-// All tokens that share a prefix are query rows of one unit of work, so that its rows are read once for
-// them all: with 64 sequences of 4 query heads per KV head, 256 rows to every 512 B. Softmax sums over
+// All tokens that share a prefix are query rows of the same units of work, so that its rows are read not
+// once per sequence but, by the tensor cores, once for every 256 query rows: 64 sequences of 4 query heads
+// per KV head to every 512 B. (The row kernel makes a pass for every 16, or 8.) Softmax sums over
 // two sets of slots join by their maxima (see nx_attend_rows.cuh), in binary32, so the two sets are two
 // passes, each by the kernel that suits it, which run over one another as far as they can:
 //   - by the row kernel the prefixes' pass leaves (m, l, o) of every query row in the workspace and the
@@ -154,8 +155,10 @@ extern "C" nx_status nexus_attend_shared(const nx_cache* cache, const nx_tokens*
   if (beside) {
     g.part.desc = desc;
     g.part.own_lens = cache->lens + (long long)tokens->layer * cache->seqs * cache->kv_heads;
-    // What the tensor-core kernel deals out the SMs by: a tile of a prefix takes one of them 1.5 us
-    // (3.5 from 8-bit rows), a row of 128 features and 16 query rows of the other pass 10 ns (6). That
+    // What the tensor-core kernel deals out the SMs by: a tile of a prefix counts 1.5 us of one of them
+    // (3.5 from 8-bit rows; with 128 features and 256 query rows a tile takes 1.0 to 1.2, or 2.0, behind a
+    // start of 8 to 11 us, or 17: 1.5 and 2.5 a tile over shares of 40 and 28. Other forms count the same),
+    // a row of 128 features and 16 query rows of the other pass 10 ns (6). That
     // is no gain next to fewer blocks than two an SM (128 slices of 2048 rows next to 16384 slots, 54
     // us, not 60), which get room for all of them or none, or to a launch that counts on all SMs.
     const long long rows = most_tokens(*tokens) * cache->group, passes = (rows + 15) / 16;

@@ -11,8 +11,8 @@
 // be the same ones, a cluster barrier stands between.
 //
 // What bounds it: a chain of latencies (lengths, the barrier, the sums, the pages taken). 16 sequences of
-// 32 x 8 slices that go on by a token 4.1 us on the GPU, 256 of which a third end, arrive or were
-// evicted 9.9, prompts of up to 2048 tokens in 96 places 8.8; three sums one after the other instead of
+// 32 x 8 slices that go on by a token 3.7 us on the GPU, 256 of which a third end, arrive or were
+// evicted 9.3, prompts of up to 2048 tokens in 96 places 8.1; three sums one after the other instead of
 // one, and inputs fetched behind the first barrier: 8.2, 11.5, 11.8.
 #include "nx_internal.cuh"
 

@@ -15,11 +15,12 @@
 // all its warps.
 //
 // What bounds it: latencies (lengths, drafts, their probabilities, the block sums: 5 us for five tokens
-// of one sequence), then the rows: 64 sequences of 131072 binary32 columns, 67 MB in 12.6 us on the GPU
-// (15.7 us a call with rows that are not in L2), 256 draws from 65536 columns 13.6 us, 200 sequences of
-// 50257 bf16 columns, 18 MB, 11.1 us (on the GPU; with whole rows searched by one warp 47.8, 18.2).
-// Blocks of 256 threads, four an SM, took 11.4, 11.2 and 13.7 us, of 512, two an SM, 12.5, 12.7, 12.9, with
-// twice the loads under way 12.1, 12.6, 13.5; three an SM 15.5, 11.5, 15.2.
+// of one sequence), then the rows: 64 sequences of 131072 binary32 columns, 67 MB with the drafts' rows, in
+// 11.2 to 12.6 us on the GPU, by how many drafts stay (16.0 us a call with rows that are not in L2), 256
+// draws from 65536 columns 13.6 us, 200 sequences of 50257 bf16 columns, 18 MB, 10.9 us. With each run
+// searched by one warp those were 17.1, 24.3 and 18.2 where all warps of the block took 12.7, 16.2 and 14.2.
+// Blocks of 256 threads, four an SM, took 11.4, 13.7 and 11.2 us, of 512, two an SM, 12.5, 12.9, 12.7, with
+// twice the loads under way 12.1, 13.5, 12.6; three an SM 15.5, 15.2, 11.5.
 #include "nx_internal.cuh"
 
 namespace nx {
